@@ -42,7 +42,14 @@ typedef enum {
     LLM_TYPE_F32  = 0,
     LLM_TYPE_F16  = 1,
     LLM_TYPE_BF16 = 2,
-    LLM_TYPE_Q8_0 = 8
+    LLM_TYPE_Q8_0 = 8,
+    LLM_TYPE_F8_E4M3 = 100   /* cache rows only (a number GGUF does not use): 8-bit floats of 4 exponent
+                              * and 3 mantissa bits (no infinities, largest 448), value = scale * q with
+                              * one float32 power-of-two scale per row of head_dim values: the least
+                              * 2^e >= 2^-126 with max|x| / 2^e <= 448 over the row's finite values (1 for a
+                              * row of zeros). Scaling by a power of two is exact, so the only rounding
+                              * is x / scale to the nearest E4M3 value, ties to even; infinities become
+                              * +-448 * scale and NaN stays NaN. */
 } llm_type;
 
 /* Model hyper-parameters ([P2] Example 8, print_info). head_dim * n_head is the width of the Q
@@ -271,6 +278,126 @@ typedef struct llm_sampler_params {
 } llm_sampler_params;
 int32_t llm_sample_ith(llm_ctx *ctx, int32_t i, const llm_sampler_params *params, float u);
 
+/* ---- operators on the caller's own device buffers ---------------------------------------------
+ * For programs that keep their own KV cache (pages handed out by their own allocator) or their own
+ * logits and want this library's kernels on them. They are the kernels a context runs for F8_E4M3
+ * caches, attention windows (llm_set_attn_window) and llm_sample_batch. Conventions:
+ *   - every data pointer is device memory of one GPU (a host pointer is refused, -1); the call runs
+ *     on that GPU whichever device is current, and leaves the current device as it was;
+ *   - work is enqueued on `stream` (a cudaStream_t of that GPU, NULL = the legacy default stream)
+ *     and the call returns without waiting; it allocates nothing, so it may be captured in a graph;
+ *   - returns 0, -1 for arguments the call refuses (nothing is enqueued), -3 if CUDA refuses the launch;
+ *   - `err`, where taken, is a device word (or NULL) that kernels OR bits into when an index they
+ *     read on the device is out of range (1: a cell or page, 4: a row); the access is skipped. The
+ *     caller zeroes it.
+ * llm_op_last_error() describes the calling thread's last refused or failed operator call. */
+const char *llm_op_last_error(void);
+
+/* A paged K/V cache: n_pages pages of page_size cells, a cell holds one row of head_dim values per KV
+ * head for K and one for V. Cell number = page * page_size + place in the page (below 2^31). The row of
+ * (page, place, head) starts page * stride_page + place * stride_cell + head * stride_head elements
+ * after k (and v): any order of the dimensions fits. type: F16, BF16 or F8_E4M3; head_dim 32, 64 or
+ * 128; rows start on 16-byte boundaries. F8_E4M3: k_scale / v_scale hold the rows' float32
+ * scales, (page, place, head) at page * sstride_page + place * sstride_cell + head * sstride_head
+ * (NULL for the other types). Strides are not negative and rows must not overlap. */
+typedef struct llm_kv_pages {
+    int32_t type, n_head_kv, head_dim, page_size, n_pages;
+    void   *k, *v;
+    int64_t stride_page, stride_cell, stride_head;
+    float  *k_scale, *v_scale;
+    int64_t sstride_page, sstride_cell, sstride_head;
+} llm_kv_pages;
+
+/* Write n rows of new keys and values into the cells cell[0..n) (device), cast to the cache's type or
+ * quantised as LLM_TYPE_F8_E4M3 says. k / v: F32, F16 or BF16 (`type`), row (i, head) at
+ * i * stride_tok + head * stride_head elements, 16-byte aligned rows. A negative cell skips the row
+ * (padding); a cell past the cache is skipped and sets err bit 1. The cells named by one call must
+ * differ (a cell named twice keeps one of the rows, or for F8_E4M3 a mix of them). n = 0 is a no-op. */
+int llm_kv_store(const llm_kv_pages *kv, int32_t type, const void *k, const void *v,
+                 int64_t stride_tok, int64_t stride_head, const int32_t *cell, int32_t n,
+                 uint32_t *err, void *stream);
+
+/* Read the rows of cells cell[0..n) back into k / v (the same arguments, now outputs): value = scale *
+ * q for F8_E4M3, rounded once to `type`. The row of a negative cell is left as it was, and so is that of
+ * a cell past the cache (err bit 1). A cell may be named any number of times. */
+int llm_kv_load(const llm_kv_pages *kv, int32_t type, void *k, void *v,
+                int64_t stride_tok, int64_t stride_head, const int32_t *cell, int32_t n,
+                uint32_t *err, void *stream);
+
+/* Attention of new tokens over a paged cache:
+ *   out[i][h] = sum_j softmax_j(scale * q[i][h] . k[j][h / G]) v[j][h / G],  G = n_head / n_head_kv,
+ * over the keys j of token i's sequence with j <= p and (window == 0 or j > p - window or j < n_sink),
+ * p = the token's position. A sequence with n_kv cached rows and n_new new tokens has its new tokens
+ * at positions n_kv - n_new .. n_kv - 1 (their rows are in the cache already, see llm_kv_store); key j
+ * is the row at place j % page_size of page table[j / page_size]. A row without a visible key
+ * (n_kv < n_new: negative positions) is zeros. What masked or unwritten cells hold (NaN,
+ * infinities) does not reach the output.
+ *
+ * The plan of a step (which rows attend to which cells, split over the GPU) is made on the host once
+ * and serves every layer: llm_attn_plan_set validates it and uploads it on `stream`; llm_attn_run
+ * launches. A plan owns its workspace, so two runs of one plan must not overlap in time (use one
+ * plan per stream, or order the streams); two graphs that may run at the same time need two plans.
+ * llm_attn_run may be captured: the graph replays with whatever the plan was last set to, provided
+ * it has the same form (llm_attn_plan_form), else it leaves the output alone and sets
+ * bit 16 of the plan's error word. llm_attn_plan_set must not be captured (-1). */
+typedef struct llm_attn_shape {
+    int32_t type;            /* of q and out: F32, F16 or BF16 */
+    int32_t n_head;          /* a multiple of the cache's n_head_kv, at most 1024 */
+    float   scale;           /* 0 = 1 / sqrt(head_dim) */
+    int32_t window, n_sink;  /* 0 = no window (n_sink then has no effect) */
+    int32_t max_tok;         /* most new tokens of a step, all sequences together */
+    int32_t max_seq;         /* most sequences of a step */
+    int32_t max_table;       /* most page-table entries of a step, all sequences together */
+} llm_attn_shape;
+typedef struct llm_attn_plan llm_attn_plan;
+
+/* A plan for caches of kv's type, head count, head_dim, page size and page count (kv's pointers are
+ * not kept; F16 caches take F16 or F32 activations, BF16 caches BF16, F8_E4M3 all three). Device
+ * memory is allocated on the current device here and nowhere else. NULL on invalid parameters or a
+ * failed allocation. */
+llm_attn_plan *llm_attn_plan_init(const llm_attn_shape *shape, const llm_kv_pages *kv);
+void llm_attn_plan_free(llm_attn_plan *plan);
+/* n_new, n_kv [n_seq] and pages [n_seq][ld_pages] are host arrays; sequence s uses the first
+ * ceil(n_kv[s] / page_size) entries of its row. The rows of q and out are the sequences' new tokens
+ * one after the other. -1: a count out of range (n_new < 0, n_kv < 0, sums above the shape's
+ * maxima, a row shorter than n_kv needs), a page outside the cache, or a stream being captured; the
+ * plan then keeps what it held. */
+int llm_attn_plan_set(llm_attn_plan *plan, int32_t n_seq, const int32_t *n_new, const int32_t *n_kv,
+                      const int32_t *pages, int32_t ld_pages, void *stream);
+/* q row (i, h) at i * q_stride_tok + h * q_stride_head elements, out likewise; 16-byte aligned rows.
+ * Rows behind the last sequence's tokens are neither read nor written. out may not overlap q. */
+int llm_attn_run(llm_attn_plan *plan, const void *q, int64_t q_stride_tok, int64_t q_stride_head,
+                 const llm_kv_pages *kv, void *out, int64_t o_stride_tok, int64_t o_stride_head,
+                 void *stream);
+/* 0: nothing to run, 1: 16-row tiles (few rows per KV head), 2: 128-row tensor-core tiles. -1: NULL. */
+int llm_attn_plan_form(const llm_attn_plan *plan);
+/* The plan's error word (0 = none) after waiting for its device; cleared by the call. */
+uint32_t llm_attn_plan_error(llm_attn_plan *plan);
+
+/* The sampler chain of llm_sample_ith for n_rows rows of logits at once, one token per row, without
+ * a host round trip. logits: row r at r * ld elements, F32, F16 or BF16. Per-row device arrays of
+ * n_rows values: top_k (<= 0 or >= n_vocab: off), top_p (>= 1: off; <= 0 or NaN: the first candidate),
+ * min_p (<= 0 or NaN: off, > 1 counts as 1), temperature (<= 0 or NaN: greedy), u in [0, 1)
+ * (clamped to it), repeat_penalty (with
+ * penalty_start [n_rows + 1] and penalty_token [n_penalty_token]: row r's tokens are
+ * penalty_token[start[r] .. start[r + 1]), ids outside the vocabulary are ignored, a token listed twice
+ * counts once). A NULL array switches its step off (temperature NULL: greedy; u may be NULL only then);
+ * n_vocab is at most 360448. The logits are not changed. Candidates
+ * are ordered by logit descending, then id ascending; probabilities are summed in fixed point
+ * (2^-44 of the largest), exactly and in any order, so the pick does not depend on the launch. NaN
+ * and -infinity have no weight; a row of nothing else gives -1. */
+typedef struct llm_sample_rows_args {
+    int32_t type, n_rows, n_vocab;
+    const void *logits;
+    int64_t ld;
+    const int32_t *top_k;
+    const float *top_p, *min_p, *temperature, *u, *repeat_penalty;
+    const int32_t *penalty_start, *penalty_token;
+    int32_t n_penalty_token;
+    int32_t *token;              /* out [n_rows] */
+} llm_sample_rows_args;
+int llm_sample_rows(const llm_sample_rows_args *args, void *stream);
+
 /* ---- test and debugging hooks ---------------------------------------------------------------
  * They expose intermediate state so tests can compare it with an independent implementation
  * (the eval-callback idea of [P2] Example 4). */
@@ -412,6 +539,17 @@ int64_t llm_debug_step_trace(llm_ctx *ctx, uint64_t *out, int64_t cap, int32_t *
  * from the host array row (for tests of llm_sample_ith on chosen rows: ties, NaN, flat rows).
  * llm_get_argmax_ith keeps the argmax that llm_decode computed. Returns 0, or -1 for a row without logits or a failed copy. Synchronises the stream. */
 int llm_debug_set_logits(llm_ctx *ctx, int32_t i, const float *row);
+
+/* The units of work llm_attn_plan_set would make for a step on a GPU of n_sm SMs, without one: 16 int32
+ * values per unit (first token, first row, rows, position of the first token; page-table offset, sink keys,
+ * first windowed key, first virtual key; end key, units of the tile, this unit's index, its first partial
+ * slot; ticket, 3 unused), those of 16-row tiles first (n_rows_units receives their number). tc != 0
+ * allows 128-row tiles. caps, if given, receives the plan's buffer bounds for the shape's maxima:
+ * 16-row and 128-row units, tiles, 16-row and 128-row partial slots. Returns the number of units (writes at
+ * most cap of them), -1 for invalid arguments. */
+int64_t llm_debug_attn_units(const llm_attn_shape *shape, const llm_kv_pages *kv, int32_t n_sm, int32_t tc,
+                             int32_t n_seq, const int32_t *n_new, const int32_t *n_kv, int32_t *out,
+                             int64_t cap, int64_t *n_rows_units, int64_t caps[5]);
 
 /* Fault injection: kind 1 makes ubatch `ub` of the next llm_decode hand the K/V append kernel a
  * cell index past the cache; the kernel's bounds check skips the write and reports the error

@@ -15,7 +15,7 @@ import numpy as np
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libllm.so")
 
-F32, F16, BF16, Q8_0 = 0, 1, 2, 8
+F32, F16, BF16, Q8_0, F8_E4M3 = 0, 1, 2, 8, 100
 CTX_HOST_ONLY = 1
 CTX_FUSED_STEP = 2
 CTX_KV_SPLIT = 4
@@ -44,6 +44,31 @@ class SamplerParams(C.Structure):
     _fields_ = [("top_k", C.c_int32), ("top_p", C.c_float), ("min_p", C.c_float),
                 ("temperature", C.c_float), ("repeat_penalty", C.c_float),
                 ("penalty_tokens", C.POINTER(C.c_int32)), ("n_penalty_tokens", C.c_int32)]
+
+
+class KvPagesDesc(C.Structure):
+    _fields_ = [("type", C.c_int32), ("n_head_kv", C.c_int32), ("head_dim", C.c_int32),
+                ("page_size", C.c_int32), ("n_pages", C.c_int32),
+                ("k", C.c_void_p), ("v", C.c_void_p),
+                ("stride_page", C.c_int64), ("stride_cell", C.c_int64), ("stride_head", C.c_int64),
+                ("k_scale", C.c_void_p), ("v_scale", C.c_void_p),
+                ("sstride_page", C.c_int64), ("sstride_cell", C.c_int64),
+                ("sstride_head", C.c_int64)]
+
+
+class AttnShape(C.Structure):
+    _fields_ = [("type", C.c_int32), ("n_head", C.c_int32), ("scale", C.c_float),
+                ("window", C.c_int32), ("n_sink", C.c_int32), ("max_tok", C.c_int32),
+                ("max_seq", C.c_int32), ("max_table", C.c_int32)]
+
+
+class SampleRowsArgs(C.Structure):
+    _fields_ = [("type", C.c_int32), ("n_rows", C.c_int32), ("n_vocab", C.c_int32),
+                ("logits", C.c_void_p), ("ld", C.c_int64), ("top_k", C.c_void_p),
+                ("top_p", C.c_void_p), ("min_p", C.c_void_p), ("temperature", C.c_void_p),
+                ("u", C.c_void_p), ("repeat_penalty", C.c_void_p), ("penalty_start", C.c_void_p),
+                ("penalty_token", C.c_void_p), ("n_penalty_token", C.c_int32),
+                ("token", C.c_void_p)]
 
 
 class PerfData(C.Structure):
@@ -108,6 +133,26 @@ SIGNATURES = {
                                         C.c_int32, C.c_void_p, C.c_int32, C.c_int32, C.c_int32, C.c_int32]),
     "llm_debug_gemm_bf16": (C.c_int, [C.c_int32, C.c_void_p, C.c_int64, C.c_int64, C.c_void_p,
                                       C.c_int32, C.c_void_p, C.c_int32, C.c_int32]),
+    "llm_op_last_error": (C.c_char_p, []),
+    "llm_kv_store": (C.c_int, [C.POINTER(KvPagesDesc), C.c_int32, C.c_void_p, C.c_void_p, C.c_int64,
+                               C.c_int64, C.c_void_p, C.c_int32, C.c_void_p, C.c_void_p]),
+    "llm_kv_load": (C.c_int, [C.POINTER(KvPagesDesc), C.c_int32, C.c_void_p, C.c_void_p, C.c_int64,
+                              C.c_int64, C.c_void_p, C.c_int32, C.c_void_p, C.c_void_p]),
+    "llm_attn_plan_init": (C.c_void_p, [C.POINTER(AttnShape), C.POINTER(KvPagesDesc)]),
+    "llm_attn_plan_free": (None, [C.c_void_p]),
+    "llm_attn_plan_set": (C.c_int, [C.c_void_p, C.c_int32, C.POINTER(C.c_int32),
+                                    C.POINTER(C.c_int32), C.POINTER(C.c_int32), C.c_int32,
+                                    C.c_void_p]),
+    "llm_attn_run": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int64, C.c_int64,
+                               C.POINTER(KvPagesDesc), C.c_void_p, C.c_int64, C.c_int64,
+                               C.c_void_p]),
+    "llm_attn_plan_form": (C.c_int, [C.c_void_p]),
+    "llm_attn_plan_error": (C.c_uint32, [C.c_void_p]),
+    "llm_sample_rows": (C.c_int, [C.POINTER(SampleRowsArgs), C.c_void_p]),
+    "llm_debug_attn_units": (C.c_int64, [C.POINTER(AttnShape), C.POINTER(KvPagesDesc), C.c_int32,
+                                         C.c_int32, C.c_int32, C.POINTER(C.c_int32),
+                                         C.POINTER(C.c_int32), C.POINTER(C.c_int32), C.c_int64,
+                                         C.POINTER(C.c_int64), C.POINTER(C.c_int64)]),
     "llm_debug_kernel_stats": (C.c_int32, [C.c_void_p, C.c_int32, C.c_char_p, C.c_int32,
                                            C.POINTER(C.c_int64), C.POINTER(C.c_double),
                                            C.POINTER(C.c_double), C.POINTER(C.c_double)]),
@@ -201,6 +246,193 @@ def debug_gemm_tn_f16_trace(epi: int, W, X, Y, F: int = 0, splits: int = 1):
 def debug_noalloc_scratch_poke(value: int) -> int:
     """Plant a value in the allocation-free GEMM's error word on the current device."""
     return lib().llm_debug_noalloc_scratch_poke(value)
+
+
+# ---- operators on the caller's own torch CUDA tensors --------------------------------------------
+def _type_of(t) -> int:
+    """The llm_type of a torch tensor's elements (uint8 holds E4M3 codes)."""
+    import torch
+    types = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16,
+             torch.float8_e4m3fn: F8_E4M3, torch.uint8: F8_E4M3}
+    if t.dtype not in types:
+        raise TypeError(f"unsupported element type {t.dtype}")
+    return types[t.dtype]
+
+
+def _stream_of(t, stream: Optional[int]):
+    """The given cudaStream_t, or torch's current stream of t's device."""
+    if stream is not None:
+        return C.c_void_p(stream)
+    import torch
+    return C.c_void_p(torch.cuda.current_stream(t.device).cuda_stream if t.is_cuda else None)
+
+
+def _need(t, name: str, dtype: str, shape) -> None:
+    """t must be a dense tensor of this type and shape: the library reads it as such."""
+    if str(t.dtype) != "torch." + dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
+                         f"not {t.dtype} {tuple(t.shape)}")
+
+
+def _op(status: int) -> None:
+    if status != 0:
+        raise LlmError(lib().llm_op_last_error().decode() + f" ({status})")
+
+
+def _rows(t, name: str, heads: int, dim: int) -> None:
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or (dim > 1 and t.stride(2) != 1):
+        raise ValueError(f"{name} must be [tokens, {heads}, {dim}] with dense rows, "
+                         f"not {tuple(t.shape)} with strides {t.stride()}")
+
+
+class KvPages:
+    """A paged K/V cache held in torch CUDA tensors: k and v [n_pages, page_size, n_head_kv, head_dim]
+    (float16, bfloat16, or E4M3 codes as float8_e4m3fn or uint8), in any memory order that keeps the
+    rows of head_dim values dense (a [page, head, cell, dim] cache is passed as its transpose).
+    k_scale and v_scale [n_pages, page_size, n_head_kv] float32 belong to an E4M3 cache."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.stride() != v.stride():
+            raise ValueError("k and v must be alike, [n_pages, page_size, n_head_kv, head_dim]")
+        if k.stride(3) != 1:
+            raise ValueError("cache rows must be dense")
+        d = KvPagesDesc()
+        d.type = _type_of(k)
+        d.n_pages, d.page_size, d.n_head_kv, d.head_dim = k.shape
+        d.k, d.v = k.data_ptr(), v.data_ptr()
+        d.stride_page, d.stride_cell, d.stride_head = k.stride()[:3]
+        if (d.type == F8_E4M3) != (k_scale is not None) or (k_scale is None) != (v_scale is None):
+            raise ValueError("an E4M3 cache has scales, other caches have none")
+        if k_scale is not None:
+            for s in (k_scale, v_scale):
+                if str(s.dtype) != "torch.float32" or s.shape != k.shape[:3]:
+                    raise ValueError("scales must be float32 [n_pages, page_size, n_head_kv]")
+            if k_scale.stride() != v_scale.stride():
+                raise ValueError("k_scale and v_scale must be laid out alike")
+            d.k_scale, d.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
+            d.sstride_page, d.sstride_cell, d.sstride_head = k_scale.stride()
+        self.desc = d
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+
+    def _kv_rows(self, fn, k, v, cell, err, stream):
+        for t, name in ((k, "k"), (v, "v")):
+            _rows(t, name, self.desc.n_head_kv, self.desc.head_dim)
+        if k.shape != v.shape or k.dtype != v.dtype or k.stride() != v.stride():
+            raise ValueError("k and v must be alike")
+        _need(cell, "cell", "int32", (k.shape[0],))
+        if err is not None and str(err.dtype) not in ("torch.int32", "torch.uint32"):
+            raise ValueError("err must be a 32-bit word")
+        _op(fn(C.byref(self.desc), _type_of(k), k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1),
+               cell.data_ptr(), k.shape[0], err.data_ptr() if err is not None else None,
+               _stream_of(k, stream)))
+
+
+def kv_store(pages: KvPages, k, v, cell, err=None, stream: Optional[int] = None) -> None:
+    """Write rows k, v [n, n_head_kv, head_dim] into cells cell [n] (int32; negative: skipped) of the
+    cache, cast or quantised to its type. err: an optional device word for bad cells."""
+    pages._kv_rows(lib().llm_kv_store, k, v, cell, err, stream)
+
+
+def kv_load(pages: KvPages, cell, k, v, err=None, stream: Optional[int] = None) -> None:
+    """Read the rows of cells cell [n] back into k, v [n, n_head_kv, head_dim] (rows of negative cells
+    are left as they were)."""
+    pages._kv_rows(lib().llm_kv_load, k, v, cell, err, stream)
+
+
+class AttnPlan:
+    """Attention of new tokens over a paged cache like `pages` (its type and shape, not its memory):
+    made once, set once per step, run once per layer. dtype is the type of q and out."""
+
+    def __init__(self, pages: KvPages, n_head: int, dtype, max_tok: int, max_seq: int, max_table: int,
+                 window: int = 0, n_sink: int = 0, scale: float = 0.0):
+        import torch
+        self.ptr = None
+        types = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
+        if dtype not in types:
+            raise TypeError(f"unsupported activation type {dtype}")
+        self.dtype, self.n_head, self.head_dim = dtype, n_head, pages.desc.head_dim
+        self.device = pages.k.device
+        self.n_tok = 0
+        s = AttnShape(types[dtype], n_head, scale, window, n_sink, max_tok, max_seq, max_table)
+        with torch.cuda.device(self.device if pages.k.is_cuda else -1):
+            self.ptr = lib().llm_attn_plan_init(C.byref(s), C.byref(pages.desc))
+        if not self.ptr:
+            raise LlmError("llm_attn_plan_init failed: " + lib().llm_op_last_error().decode())
+
+    def free(self) -> None:
+        if self.ptr:
+            lib().llm_attn_plan_free(self.ptr)
+            self.ptr = None
+
+    def __del__(self):
+        try:
+            self.free()
+        except Exception:
+            pass
+
+    def set(self, n_new, n_kv, pages, stream: Optional[int] = None) -> None:
+        """The step's sequences: n_new tokens each, n_kv cached rows each (the new ones included), page
+        table [n_seq, at least ceil(n_kv / page_size)]; host integers."""
+        n_new, n_kv = _i32(n_new), _i32(n_kv)
+        t = _i32(pages)
+        if n_new.ndim != 1 or n_new.shape != n_kv.shape or t.ndim != 2 or len(t) != len(n_new):
+            raise ValueError("n_new [n_seq], n_kv [n_seq] and pages [n_seq, n] are needed")
+        if stream is None:
+            import torch
+            stream = torch.cuda.current_stream(self.device).cuda_stream
+        _op(lib().llm_attn_plan_set(self.ptr, len(n_new), _ptr(n_new, C.c_int32),
+                                    _ptr(n_kv, C.c_int32), _ptr(t, C.c_int32), t.shape[1],
+                                    C.c_void_p(stream)))
+        self.n_tok = int(n_new.sum())
+
+    def run(self, q, pages: KvPages, out, stream: Optional[int] = None) -> None:
+        """out[i] = attention of token i of the step; q and out [at least the step's tokens, n_head,
+        head_dim], rows past the tokens are not touched."""
+        for t, name in ((q, "q"), (out, "out")):
+            _rows(t, name, self.n_head, self.head_dim)
+            if t.dtype != self.dtype:
+                raise TypeError(f"{name} must be {self.dtype}")
+            if t.shape[0] < self.n_tok:
+                raise ValueError(f"{name} has fewer rows than the step has tokens ({self.n_tok})")
+        _op(lib().llm_attn_run(self.ptr, q.data_ptr(), q.stride(0), q.stride(1),
+                               C.byref(pages.desc), out.data_ptr(), out.stride(0), out.stride(1),
+                               _stream_of(q, stream)))
+
+    @property
+    def form(self) -> int:
+        return lib().llm_attn_plan_form(self.ptr)
+
+    def error(self) -> int:
+        """The plan's error word after the device has finished (0 = none)."""
+        return lib().llm_attn_plan_error(self.ptr)
+
+
+def sample_rows(logits, token, u=None, top_k=None, top_p=None, min_p=None, temperature=None,
+                repeat_penalty=None, penalty_start=None, penalty_token=None,
+                stream: Optional[int] = None) -> None:
+    """The sampler chain for every row of logits [n, n_vocab]; token [n] int32 receives the picks. The
+    parameters are device arrays of n values (top_k int32, the others float32; None = off; temperature
+    None = greedy); row r's penalty tokens are penalty_token[penalty_start[r]:penalty_start[r + 1]]."""
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be [rows, n_vocab] with dense rows")
+    R, V = logits.shape
+    a = SampleRowsArgs()
+    a.type = _type_of(logits)
+    a.n_rows, a.n_vocab, a.ld, a.logits = R, V, logits.stride(0), logits.data_ptr()
+    _need(token, "token", "int32", (R,))
+    a.token = token.data_ptr()
+    for name, t, dt in (("u", u, "float32"), ("top_k", top_k, "int32"), ("top_p", top_p, "float32"),
+                        ("min_p", min_p, "float32"), ("temperature", temperature, "float32"),
+                        ("repeat_penalty", repeat_penalty, "float32")):
+        if t is not None:
+            _need(t, name, dt, (R,))
+            setattr(a, name, t.data_ptr())
+    if repeat_penalty is not None and penalty_start is not None and penalty_token is not None:
+        _need(penalty_start, "penalty_start", "int32", (R + 1,))
+        _need(penalty_token, "penalty_token", "int32", (penalty_token.numel(),))
+        a.penalty_start, a.penalty_token = penalty_start.data_ptr(), penalty_token.data_ptr()
+        a.n_penalty_token = penalty_token.numel()
+    _op(lib().llm_sample_rows(C.byref(a), _stream_of(logits, stream)))
 
 
 class Context:

@@ -1,0 +1,128 @@
+// Operators over a paged KV cache (kv_paged.cu, attn_paged.cu) and the batched sampler
+// (sample_rows.cu): launch arguments shared by the C entry points (op_api.cu) and the decode loop.
+#pragma once
+
+#include <cstdint>
+#include <string>
+#include <vector>
+
+#include <cuda_runtime.h>
+
+#include "kernels.h"
+
+namespace llm {
+
+constexpr int32_t W_F8 = 100;                    // LLM_TYPE_F8_E4M3
+enum : uint32_t { ERR_PLAN_FORM = 16u };         // beside the bits of kernels.h
+
+// A paged cache as the kernels see it; strides in bytes (scales: elements).
+struct PagedKv {
+    int32_t type = W_F16, Hkv = 0, hd = 0, page_size = 1, n_pages = 0;
+    uint8_t *k = nullptr, *v = nullptr;
+    int64_t sb_page = 0, sb_cell = 0, sb_head = 0;
+    float *ks = nullptr, *vs = nullptr;
+    int64_t ss_page = 0, ss_cell = 0, ss_head = 0;
+};
+
+// Rows between dense token-major buffers and cache cells (kv_paged.cu); strides in elements.
+struct KvRowsArgs {
+    PagedKv kv;
+    int32_t type = W_F32;                        // of the dense rows
+    void *k = nullptr, *v = nullptr;
+    int64_t s_tok = 0, s_head = 0;
+    const int32_t* cell = nullptr;
+    int32_t n = 0;
+    uint32_t* err = nullptr;
+};
+bool launch_kv_rows_store(const KvRowsArgs& a, cudaStream_t st);
+bool launch_kv_rows_load(const KvRowsArgs& a, cudaStream_t st);
+
+// One unit of attention work (per KV head): rows of one tile of a sequence against a range of the keys
+// those rows may see. A tile's rows are (token, query head) pairs of the KV head's group, row
+// token * G + head. Its keys are numbered by a virtual index: sink keys 0 .. n_sink_keys - 1, then the
+// keys from key_lo on (the sequence's keys between the sinks and the tile's windows are left out).
+struct AttnUnit {
+    int32_t tok0, row0, n_row, p0;               // first token of the sequence; the tile's rows; position of tok0
+    int32_t table, n_sink_keys, key_lo, v0;      // page-table offset; the virtual key range [v0, v1)
+    int32_t v1, n_chunk, chunk, part;            // units of this tile; this one; the first's partial slot
+    int32_t tile, pad[3];                        // ticket index
+};
+static_assert(sizeof(AttnUnit) == 64, "read as four int4");
+
+constexpr int kUnitRows1 = 16, kUnitRows2 = 128; // rows per tile of the two forms
+enum : int32_t { ATTN_FORM_ROWS = 1, ATTN_FORM_TC = 2 };
+enum AttnOut : int32_t { AO_F16 = 0, AO_BF16 = 1, AO_F32 = 2, AO_BF16_PAIR = 3 };
+
+// Header words of a plan's device buffer.
+enum : int32_t { PH_UNITS1 = 0, PH_UNITS2 = 1, PH_FORM = 2, PH_WORDS = 8 };
+
+struct AttnPagedArgs {
+    PagedKv kv;
+    int32_t q_type = W_F16, G = 1;
+    const void* q = nullptr;
+    int64_t q_tok = 0, q_head = 0;               // elements
+    void* out = nullptr;
+    void* out_lo = nullptr;                      // AO_BF16_PAIR: the low terms
+    int32_t out_kind = AO_F16;
+    int64_t o_tok = 0, o_head = 0;
+    float scale_log2 = 0.f;                      // scale * log2(e)
+    int32_t window = 0, n_sink = 0;
+    const int32_t* hdr = nullptr;
+    const AttnUnit* units1 = nullptr;
+    const AttnUnit* units2 = nullptr;
+    const int32_t* table = nullptr;
+    const int32_t* perm = nullptr;               // token order (null: identity)
+    const int32_t* tok_pos = nullptr;            // positions of tokens (null: p0 + token)
+    const int32_t* key_pos = nullptr;            // positions of the page-table's keys, pages of one cell
+    float* part_o = nullptr;                     // [part * Hkv + head][rows][hd] unnormalised
+    float2* part_ml = nullptr;                   // [part * Hkv + head][rows] (running max, sum)
+    int32_t* tickets = nullptr;                  // [tile * Hkv + head], zero between launches
+    uint32_t* err = nullptr;
+    int32_t form = 0;                            // forms the caller launches
+    int32_t n_sm = 148;
+    bool pdl = false;
+};
+// Both forms' kernels as the plan's form says; false if a launch failed.
+bool launch_attn_paged(const AttnPagedArgs& a, cudaStream_t st);
+bool attn_paged_types_ok(int32_t q_type, int32_t kv_type);
+// 128-row tiles serve this shape (attn_paged_tc.cu).
+bool attn_paged_tc_ok(int32_t hd, int32_t kv_type, int32_t q_type);
+bool launch_attn_paged_tc(const AttnPagedArgs& a, cudaStream_t st);
+
+// ---- host plan (attn_paged_plan.cpp)
+struct PlanSeq {
+    int32_t tok0, n_new, p0;                     // its tokens; position of the first
+    int32_t table, n_keys;                       // its keys (in position order)
+    // positions where they are not the indices: of its tokens (through perm) and of its keys
+    const int32_t *tok_pos = nullptr, *key_pos = nullptr;
+};
+struct PlanShape {
+    int32_t G = 1, Hkv = 1, window = 0, n_sink = 0, n_sm = 148;
+    bool tc = false;                             // 128-row tiles allowed
+};
+struct PagedPlan {
+    std::vector<AttnUnit> units1, units2;
+    int32_t n_tiles = 0, n_parts1 = 0, n_parts2 = 0;
+    int32_t form() const { return (units1.empty() ? 0 : ATTN_FORM_ROWS) | (units2.empty() ? 0 : ATTN_FORM_TC); }
+};
+void build_paged_plan(const PlanShape& s, const std::vector<PlanSeq>& seqs, PagedPlan& plan);
+// Upper bounds for buffers over every plan of at most max_tok tokens in max_seq sequences.
+struct PagedPlanCaps { int64_t units1, units2, tiles, parts1, parts2; };
+PagedPlanCaps paged_plan_caps(const PlanShape& s, int32_t max_tok, int32_t max_seq);
+
+// ---- the sampler chain per row (sample_rows.cu)
+struct SampleRowsArgs {
+    int32_t type = W_F32, n_rows = 0, V = 0;
+    const void* logits = nullptr;
+    int64_t ld = 0;
+    const int32_t* row = nullptr;                // logits row of each entry (null: identity)
+    const int32_t* top_k = nullptr;
+    const float *top_p = nullptr, *min_p = nullptr, *temperature = nullptr, *u = nullptr, *penalty = nullptr;
+    const int32_t *pen_start = nullptr, *pen_tok = nullptr;
+    int32_t n_pen = 0;                           // entries of pen_tok
+    int32_t* token = nullptr;
+};
+int32_t sample_rows_max_vocab();
+bool launch_sample_rows(const SampleRowsArgs& a, cudaStream_t st);
+
+}  // namespace llm
