@@ -369,7 +369,7 @@ int llm_attn_plan_set(llm_attn_plan *plan, int32_t n_seq, const int32_t *n_new, 
 int llm_attn_run(llm_attn_plan *plan, const void *q, int64_t q_stride_tok, int64_t q_stride_head,
                  const llm_kv_pages *kv, void *out, int64_t o_stride_tok, int64_t o_stride_head,
                  void *stream);
-/* 0: nothing to run, 1: 16-row tiles (few rows per KV head), 2: 128-row tensor-core tiles. -1: NULL. */
+/* 0: nothing to run, 1: 16-row tiles (few rows per KV head), 2: 256-row tensor-core tiles. -1: NULL. */
 int llm_attn_plan_form(const llm_attn_plan *plan);
 /* The plan's error word (0 = none) after waiting for its device; cleared by the call. */
 uint32_t llm_attn_plan_error(llm_attn_plan *plan);
@@ -544,8 +544,8 @@ int llm_debug_set_logits(llm_ctx *ctx, int32_t i, const float *row);
  * values per unit (first token, first row, rows, position of the first token; page-table offset, sink keys,
  * first windowed key, first virtual key; end key, units of the tile, this unit's index, its first partial
  * slot; ticket, 3 unused), those of 16-row tiles first (n_rows_units receives their number). tc != 0
- * allows 128-row tiles. caps, if given, receives the plan's buffer bounds for the shape's maxima:
- * 16-row and 128-row units, tiles, 16-row and 128-row partial slots. Returns the number of units (writes at
+ * allows 256-row tiles. caps, if given, receives the plan's buffer bounds for the shape's maxima:
+ * 16-row and 256-row units, tiles, 16-row and 256-row partial slots. Returns the number of units (writes at
  * most cap of them), -1 for invalid arguments. */
 int64_t llm_debug_attn_units(const llm_attn_shape *shape, const llm_kv_pages *kv, int32_t n_sm, int32_t tc,
                              int32_t n_seq, const int32_t *n_new, const int32_t *n_kv, int32_t *out,

@@ -106,7 +106,7 @@ def attention_tol(out, mag, smag, dtype, n, hd, vmax):
       - a score is a float32 sum of hd products and three more roundings: an error of (hd + 4) 2^-24
         of sum |q k| scale (smag), the same again for a float32 q held in two 11-bit terms (2^-22 of each
         product); it changes a weight by as much, relatively, and 2^x costs 2^-22 more;
-      - p is rounded to 11 bits (half a step 2^-11) for f16 activations and in 128-row bf16 tiles to 8
+      - p is rounded to 11 bits (half a step 2^-11) for f16 activations and in 256-row bf16 tiles to 8
         bits (2^-9 is half a step of bf16: 2^-8 of the value at most), otherwise held to 2^-17;
       - p below f16's normal range (a second term's too): an absolute error of 2^-25 each, over n keys,
         against a weight sum of at least 2^6 (a row's largest p is 2^6 or more);

@@ -153,7 +153,7 @@ def test_plan_covers_every_visible_key_once(B, seed):
         tok0, row0, n_row, p0, tab, ns, lo, v0, v1, n_chunk, chunk, part, tile = u[:13]
         s = [j for j in range(n_seq) if starts[j] == tok0 and n_new[j] > 0][0]
         assert tab == tabs[s] and p0 == n_kv[s] - n_new[s]
-        assert 1 <= n_row <= (16 if i < n1 else 128) and 0 <= v0 <= v1 and 0 <= chunk < n_chunk
+        assert 1 <= n_row <= (16 if i < n1 else 256) and 0 <= v0 <= v1 and 0 <= chunk < n_chunk
         tiles.setdefault(tile, []).append((chunk, n_chunk))
         if n_chunk > 1:
             slot = part + chunk

@@ -11,9 +11,9 @@ namespace {
 // CTAs of each form that run at once (attn_paged.cu: two per SM; attn_paged_tc.cu: one).
 int64_t slots(const PlanShape& s, bool tc) { return (int64_t)s.n_sm * (tc ? 1 : 2); }
 // Shortest key range worth a unit of its own: a unit of the 16-row form gives each of its four warps one
-// block of 16 keys, one of the 128-row form one step of 128 keys.
+// block of 16 keys, one of the 256-row form one step of 128 keys.
 constexpr int64_t kMinKeys1 = 64, kMinKeys2 = 128;
-// Sequences with at least this many rows per KV head take 128-row tiles.
+// Sequences with at least this many rows per KV head take 256-row tiles.
 constexpr int64_t kTcRows = 64;
 
 int64_t up_to(int64_t x, int64_t m) { return (x + m - 1) / m * m; }

@@ -1,10 +1,719 @@
-// The 128-row tensor-core tiles of the attention over a paged cache: no shape takes them yet, the
-// 16-row tiles (attn_paged.cu) serve every call.
-#include "paged.h"
+// Attention of new tokens over a paged cache, 256-row tiles on the fifth-generation tensor cores
+// (tcgen05, accumulators in TMEM): chunks of new tokens, where the products are the bound. F16, BF16 and
+// E4M3 caches, head_dim 64 and 128, F16 or BF16 activations.
+//
+// A CTA takes a unit: up to 256 rows of (token, query head) pairs of one KV head, as two halves of 128
+// MMA rows, against a range of keys in blocks of 128. Per block and half:
+//   S = Q K^T     tcgen05.mma M 128 x N 128, into the half's TMEM columns
+//   softmax       a thread per row: p = 2^(s - m) in float32, written back to TMEM as f16 (bf16) over the
+//                 second half of S's columns
+//   O += P V      tcgen05.mma M 128 x N head_dim, P the A operand from TMEM, V as stored ([keys][dims], an
+//                 MN-major B operand)
+// While one half's rows are in the softmax, the tensor cores work on the other half. K and V tiles are
+// shared by both halves, so each byte from L2 feeds 256 rows. The MMAs of a CTA are issued by one
+// thread and run in issue order, so O += P V of block j may be followed at once by S of block j + 1 over
+// the same columns, and a completed S means that every product before it is complete too.
+//
+// Roles (12 warps, so that a thread may have 168 registers): warps 0-1 bring K and V rows cell by cell into a ring of 128-byte-swizzled tiles
+// (16-byte asynchronous copies; E4M3 rows through registers, converted to f16), with the keys' positions;
+// warp 2 issues the MMAs; warps 4-7 and 8-11 are the two halves' softmax and epilogue (a thread owns a
+// TMEM lane: warp w reads lanes 32 (w % 4) on). m is 6 below a row maximum and raised lazily, when p would
+// pass 2^14: O, in TMEM, is rarely rescaled, and never more than it must. P is rounded to f16 (half a step 2^-11)
+// or, for bf16 products, to bf16 (2^-8 of p: the sums run over the rounded values' float32 originals, and
+// the output is rounded to bf16 itself).
+//
+// E4M3 rows enter as f16 numbers q * s / s0 with s0 the largest scale of the unit's first block (a power
+// of two like s): exact from s0 2^-15 to s0 2^7. A row of a larger scale sends the unit to the careful path,
+// as do values that are not finite.
+//
+// Every wait is bounded by a wall-clock limit; a timeout sets ERR_TIMEOUT, ends every role's loop, and
+// the CTA leaves after its copies and with its TMEM freed.
+#include "attn_paged_common.cuh"
+
+#include <algorithm>
 
 namespace llm {
 
-bool attn_paged_tc_ok(int32_t, int32_t, int32_t) { return false; }
-bool launch_attn_paged_tc(const AttnPagedArgs&, cudaStream_t) { return false; }
+namespace {
+
+using namespace pattn;
+
+constexpr int kProdWarps = 2;
+constexpr int kMmaWarp = 2;
+constexpr int kSoft0 = 4;                                  // first softmax warp
+constexpr int kThr = 12 * 32;
+constexpr int kGroups = 4 / kProdWarps;                    // groups of 32 keys a producing warp brings
+constexpr int kKeys = 128;                                 // keys per block
+constexpr int kStages = 5;                                 // K or V tiles in flight
+constexpr int kMeta = 3;                                   // blocks whose positions are kept (see meta_full)
+constexpr uint32_t kBlk = 128 * 128;                       // [128 rows][64 16-bit values], swizzled
+constexpr uint64_t kWaitNs = 2000000000ull;
+static_assert(kUnitRows2 == 256, "two halves of 128 MMA rows");
+
+template <int HD>
+struct Smem {
+    static constexpr uint32_t tile = HD / 64 * kBlk;
+    static constexpr uint32_t q = 0;                        // [2] tiles
+    static constexpr uint32_t kv = q + 2 * tile;            // [kStages] tiles
+    static constexpr uint32_t kpos = kv + kStages * tile;   // int [kMeta][kKeys]
+    static constexpr uint32_t full = kpos + kMeta * kKeys * 4;   // uint8 [kMeta][4]
+    static constexpr uint32_t rs = full + 16;               // float [256]: scale of a row's scores
+    static constexpr uint32_t bars = rs + 256 * 4;
+    static constexpr uint32_t misc = bars + 24 * 8;
+    static constexpr uint32_t bytes = misc + 64;
+};
+static_assert(Smem<128>::bytes <= 227 * 1024, "shared memory of one CTA");
+
+__device__ __forceinline__ uint32_t sa(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+__device__ __forceinline__ uint64_t now_ns() {
+    uint64_t t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+__device__ __forceinline__ void bar_init(uint64_t* b, uint32_t n) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(sa(b)), "r"(n));
+}
+__device__ __forceinline__ void bar_arrive(uint64_t* b) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(sa(b)) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint64_t* b, uint32_t par) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok) : "r"(sa(b)), "r"(par) : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void to_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// K-major 128-row tile, 128-byte swizzle (8-row groups 1024 bytes apart)
+__device__ __forceinline__ uint64_t desc_k(uint32_t s) {
+    return (uint64_t)((s & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
+           (uint64_t)2 << 61;
+}
+// the same memory as an MN-major operand: rows are the contracted dimension, blocks of 64 columns kBlk apart
+__device__ __forceinline__ uint64_t desc_mn(uint32_t s) {
+    return (uint64_t)((s & 0x3FFFFu) >> 4) | (uint64_t)(kBlk >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+           (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// kind::f16 with f16 or bf16 A and B, float32 D
+__host__ __device__ constexpr uint32_t idesc(bool bf, int m, int n, bool b_mn) {
+    return (1u << 4) | (bf ? (1u << 7) | (1u << 10) : 0u) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
+           ((uint32_t)(m >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(id), "r"(acc));
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(id), "r"(acc));
+}
+__device__ __forceinline__ void commit(uint64_t* b) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(sa(b)) : "memory");
+}
+
+#define R8(r, o) "=r"(r[o]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), "=r"(r[o + 4]), "=r"(r[o + 5]), "=r"(r[o + 6]), "=r"(r[o + 7])
+#define W8(r, o) "r"(r[o]), "r"(r[o + 1]), "r"(r[o + 2]), "r"(r[o + 3]), "r"(r[o + 4]), "r"(r[o + 5]), "r"(r[o + 6]), "r"(r[o + 7])
+// this thread's lane, 32 columns from taddr; warp-wide, and waited for by ld_wait
+__device__ __forceinline__ void tld32(uint32_t taddr, uint32_t* r) {
+    __syncwarp();
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : R8(r, 0), R8(r, 8), R8(r, 16), R8(r, 24) : "r"(taddr));
+}
+__device__ __forceinline__ void ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tst32(uint32_t taddr, const uint32_t* r) {
+    __syncwarp();
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr), W8(r, 0), W8(r, 8), W8(r, 16), W8(r, 24)
+        : "memory");
+}
+__device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+#undef R8
+#undef W8
+
+// (a0, a1) = (x0, x1) * s + b and (a0, a1) += (x0, x1), two float32 operations per instruction
+__device__ __forceinline__ void fma_pair(float& a0, float& a1, float x0, float x1, float s, float b) {
+    asm("{\n .reg .b64 x, s, b, d;\n mov.b64 x, {%2, %3};\n mov.b64 s, {%4, %4};\n mov.b64 b, {%5, %5};\n"
+        " fma.rn.f32x2 d, x, s, b;\n mov.b64 {%0, %1}, d;\n}\n"
+        : "=f"(a0), "=f"(a1) : "f"(x0), "f"(x1), "f"(s), "f"(b));
+}
+__device__ __forceinline__ void add_pair(float& a0, float& a1, float x0, float x1) {
+    asm("{\n .reg .b64 x, a;\n mov.b64 x, {%2, %3};\n mov.b64 a, {%0, %1};\n add.rn.f32x2 a, a, x;\n mov.b64 {%0, %1}, a;\n}\n"
+        : "+f"(a0), "+f"(a1) : "f"(x0), "f"(x1));
+}
+
+template <bool BF>
+__device__ __forceinline__ uint32_t pack(float x, float y) {
+    if constexpr (BF) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+        const __half2 h = __floats2half2_rn(x, y);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+}
+
+// byte offset of 16-byte chunk ch of row r in a swizzled tile
+__device__ __forceinline__ uint32_t swz(int r, int ch) {
+    return (uint32_t)((ch >> 3) * kBlk + r * 128 + ((((uint32_t)ch & 7u) ^ ((uint32_t)r & 7u)) << 4));
+}
+
+struct Ring {                                              // position in the ring of K and V tiles
+    uint32_t s = 0, ph = 0;
+    __device__ __forceinline__ void next() { if (++s == kStages) { s = 0; ph ^= 1u; } }
+};
+struct MetaAt {
+    uint32_t s = 0, ph = 0;
+    __device__ __forceinline__ void next() { if (++s == kMeta) { s = 0; ph ^= 1u; } }
+};
+
+template <int HD, int CT, int QT>
+__global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a) {
+    using M = Smem<HD>;
+    constexpr bool F8 = CT == W_F8, BF = CT == W_BF16;
+    constexpr int CH = HD / 8;                              // 16-byte chunks of a 16-bit row
+    extern __shared__ __align__(1024) uint8_t sm[];
+    int* kpos = reinterpret_cast<int*>(sm + M::kpos);
+    uint8_t* full = sm + M::full;
+    float* rs_s = reinterpret_cast<float*>(sm + M::rs);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + M::bars);
+    uint64_t* kv_full = bars;                               // [kStages] 4: the producing warps
+    uint64_t* kv_empty = bars + kStages;                    // [kStages] 1: MMA commit
+    uint64_t* s_full = bars + 2 * kStages;                  // [2] 1: MMA commit
+    uint64_t* p_full = s_full + 2;                          // [2] 128: the softmax threads
+    uint64_t* o_done = p_full + 2;                          // [2] 1: MMA commit after the unit's last product
+    uint64_t* q_full = o_done + 2;                          // 256
+    // [kMeta] 4: a block's positions. Slot j % 3 is written again for block j + 3, whose K tile needs the
+    // ring place of V tile j (five stages), freed after both halves' softmax of block j.
+    uint64_t* meta_full = q_full + 1;
+    int* misc = reinterpret_cast<int*>(sm + M::misc);
+    volatile int* abort_f = misc;
+    int* flag = misc + 1;
+    volatile int* redo_f = misc + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 3);
+    float* s0 = reinterpret_cast<float*>(misc + 4);         // [2] E4M3: scale of the K and V tiles
+    float* wmax = reinterpret_cast<float*>(misc + 6);       // [kProdWarps][2]
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (a.pdl) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (form_missing(a)) return;
+    if (sa(sm) & 1023u) {                                   // the swizzle patterns repeat every 1024 bytes
+        if (tid == 0 && a.err) atomicOr(a.err, ERR_TIMEOUT);
+        return;
+    }
+    const int n_units = a.hdr[PH_UNITS2] * a.kv.Hkv;
+    if ((int)blockIdx.x >= n_units) return;
+
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) { bar_init(&kv_full[i], kProdWarps); bar_init(&kv_empty[i], 1); }
+        for (int i = 0; i < 2; ++i) { bar_init(&s_full[i], 1); bar_init(&p_full[i], 128); bar_init(&o_done[i], 1); }
+        bar_init(q_full, 256);
+        for (int i = 0; i < kMeta; ++i) bar_init(&meta_full[i], kProdWarps);
+        *abort_f = 0;
+        *redo_f = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sa(tmem_slot)), "r"(512u));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const uint32_t tmem = *tmem_slot;
+
+    auto wait = [&](uint64_t* b, uint32_t par) -> bool {
+        if (bar_try(b, par)) return true;
+        const uint64_t t0 = now_ns();
+        while (!bar_try(b, par)) {
+            if (*abort_f) return false;
+            if (now_ns() - t0 > kWaitNs) {
+                if (a.err) atomicOr(a.err, ERR_TIMEOUT);
+                *abort_f = 1;
+                return false;
+            }
+        }
+        return true;
+    };
+
+    Ring ring;
+    MetaAt meta;
+    uint32_t q_ph = 0, o_ph = 0, sp_ph[2] = {0u, 0u};
+    int produced = 0;                                       // ring places filled (up to all of them)
+
+    for (int ui = blockIdx.x; ui < n_units; ui += gridDim.x) {
+        const AttnUnit u = load_unit(a.units2 + ui / a.kv.Hkv);
+        const int kvh = ui % a.kv.Hkv;
+        const int nt = (u.v1 - u.v0 + kKeys - 1) / kKeys;
+        const int halves = u.n_row > 128 ? 2 : 1;
+
+        if (warp < kProdWarps) {
+            // ---- K and V tiles
+            const uint8_t* kb = a.kv.k + (int64_t)kvh * a.kv.sb_head;
+            const uint8_t* vb = a.kv.v + (int64_t)kvh * a.kv.sb_head;
+            int pmin, pmax;
+            {
+                const int r1 = u.row0 + u.n_row - 1;
+                pmin = row_pos(a, u, u.row0, row_token(a, u, u.row0));
+                pmax = row_pos(a, u, r1, row_token(a, u, r1));
+                if (a.tok_pos) {                            // any order: over all of the unit's tokens
+                    for (int r = u.row0; r <= r1; r += a.G) {
+                        const int p = row_pos(a, u, r, row_token(a, u, r));
+                        pmin = min(pmin, p);
+                        pmax = max(pmax, p);
+                    }
+                }
+            }
+            const int hid_all = hidden_below(a, pmin);
+            struct Key { int64_t off; int pos; float ks, vs; };
+            const Key none{-1, INT_MAX, 0.f, 0.f};
+            Key cur[kGroups], nxt[kGroups];                  // key 32 (kGroups warp + i) + lane of a block
+            auto lookup = [&](Key* k, int j) {
+#pragma unroll
+                for (int i = 0; i < kGroups; ++i) {
+                    k[i] = none;
+                    const int v = u.v0 + j * kKeys + 32 * (kGroups * warp + i) + lane;
+                    if (v >= u.v1) continue;
+                    const KeyAt at = key_at(a, u, v);
+                    if (at.off >= 0 && sees(at.pos, pmax, hid_all, a.n_sink)) {
+                        k[i].off = at.off;
+                        k[i].pos = at.pos;
+                        if constexpr (F8) {
+                            k[i].ks = a.kv.ks[at.soff + (int64_t)kvh * a.kv.ss_head];
+                            k[i].vs = a.kv.vs[at.soff + (int64_t)kvh * a.kv.ss_head];
+                        }
+                    }
+                }
+            };
+            auto claim = [&]() { return produced < kStages || wait(&kv_empty[ring.s], ring.ph ^ 1u); };
+            if (nt > 0) lookup(cur, 0);
+            float ik = 1.f, iv = 1.f;
+            if (F8 && nt > 0) {
+                // s0 of this unit: the largest scales of its first block
+                float mk = 0.f, mv = 0.f;
+#pragma unroll
+                for (int i = 0; i < kGroups; ++i) { mk = fmaxf(mk, cur[i].ks); mv = fmaxf(mv, cur[i].vs); }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) {
+                    mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, o));
+                    mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
+                }
+                if (lane == 0) { wmax[2 * warp] = mk; wmax[2 * warp + 1] = mv; }
+                asm volatile("bar.sync 1, %0;" ::"n"(32 * kProdWarps) : "memory");
+#pragma unroll
+                for (int i = 0; i < kProdWarps; ++i) { mk = fmaxf(mk, wmax[2 * i]); mv = fmaxf(mv, wmax[2 * i + 1]); }
+                if (!(mk > 0.f)) mk = 1.f;
+                if (!(mv > 0.f)) mv = 1.f;
+                if (tid == 0) { s0[0] = mk; s0[1] = mv; }
+                ik = 1.f / mk;
+                iv = 1.f / mv;
+            }
+            // 16-bit tiles: asynchronous copies, announced two tiles later, when they have landed
+            uint32_t pend[2];
+            int n_pend = 0;
+            auto announce = [&](uint32_t s) {
+                to_async_proxy();
+                __syncwarp();
+                if (lane == 0) bar_arrive(&kv_full[s]);
+            };
+            bool ok = true;
+            for (int j = 0; j < nt && ok; ++j) {
+                for (int kvi = 0; kvi < 2; ++kvi) {
+                    const uint8_t* base = kvi ? vb : kb;
+                    uint8_t* dst = sm + M::kv + ring.s * M::tile;
+                    if constexpr (F8) {
+                        // the rows' bytes first: they travel while the stage is waited for
+                        constexpr int LR = HD / 16;         // lanes per row, 16 values each
+                        uint4 raw[kGroups * LR];
+#pragma unroll
+                        for (int x = 0; x < kGroups * LR; ++x) {
+                            const int64_t off = __shfl_sync(0xffffffffu, cur[x / LR].off, x % LR * (32 / LR) + lane / LR);
+                            raw[x] = off >= 0 ? *reinterpret_cast<const uint4*>(base + off + 16 * (lane % LR))
+                                              : make_uint4(0u, 0u, 0u, 0u);
+                        }
+                        float f[kGroups];
+#pragma unroll
+                        for (int i = 0; i < kGroups; ++i) {
+                            f[i] = kvi ? cur[i].vs * iv : cur[i].ks * ik;
+                            if (cur[i].off >= 0 && !(f[i] <= 128.f)) *redo_f = 1;
+                        }
+                        if (kvi == 1 && j + 1 < nt) lookup(nxt, j + 1);
+                        if (!__all_sync(0xffffffffu, claim())) { ok = false; break; }
+#pragma unroll
+                        for (int x = 0; x < kGroups * LR; ++x) {
+                            const int r = x % LR * (32 / LR) + lane / LR, c = lane % LR;
+                            const __half2 fh = __float2half2_rn(__shfl_sync(0xffffffffu, f[x / LR], r));
+                            const uint32_t w[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
+                            uint32_t h[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const uint32_t e = e4m3x2_to_h2((w[i / 2] >> (16 * (i & 1))) & 0xffffu);
+                                const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&e), fh);
+                                h[i] = *reinterpret_cast<const uint32_t*>(&y);
+                            }
+                            const int rr = 32 * (kGroups * warp + x / LR) + r;
+                            *reinterpret_cast<uint4*>(dst + swz(rr, 2 * c)) = make_uint4(h[0], h[1], h[2], h[3]);
+                            *reinterpret_cast<uint4*>(dst + swz(rr, 2 * c + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
+                        }
+                    } else {
+                        if (!__all_sync(0xffffffffu, claim())) { ok = false; break; }
+                        constexpr int RI = 32 / CH;         // rows per instruction
+                        const int ch = lane % CH;
+#pragma unroll
+                        for (int x = 0; x < kGroups * 32 / RI; ++x) {
+                            const int r = x * RI % 32 + lane / CH;
+                            const int64_t off = __shfl_sync(0xffffffffu, cur[x * RI / 32].off, r);
+                            const uint8_t* src = base + (off >= 0 ? off : 0) + 16 * ch;
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                             sa(dst) + swz(32 * (kGroups * warp + x * RI / 32) + r, ch)),
+                                         "l"(src), "r"(off >= 0 ? 16 : 0) : "memory");
+                        }
+                        asm volatile("cp.async.commit_group;" ::: "memory");
+                    }
+                    if (kvi == 0) {
+#pragma unroll
+                        for (int i = 0; i < kGroups; ++i) {
+                            const int gr = kGroups * warp + i;
+                            kpos[meta.s * kKeys + 32 * gr + lane] = cur[i].pos;
+                            const bool all = __all_sync(0xffffffffu, cur[i].off >= 0);
+                            if (lane == 0) full[meta.s * 4 + gr] = all;
+                        }
+                        __syncwarp();
+                        if (lane == 0) bar_arrive(&meta_full[meta.s]);
+                        meta.next();
+                    }
+                    if constexpr (F8) {
+                        announce(ring.s);
+                    } else {
+                        if (kvi == 1 && j + 1 < nt) lookup(nxt, j + 1);
+                        if (n_pend == 2) {
+                            asm volatile("cp.async.wait_group 2;" ::: "memory");
+                            announce(pend[0]);
+                            pend[0] = pend[1];
+                            pend[1] = ring.s;
+                        } else {
+                            pend[n_pend++] = ring.s;
+                        }
+                    }
+                    ring.next();
+                    if (produced < kStages) ++produced;
+                }
+#pragma unroll
+                for (int i = 0; i < kGroups; ++i) cur[i] = nxt[i];
+            }
+            if constexpr (!F8) {
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
+                for (int i = 0; i < n_pend; ++i) announce(pend[i]);
+            }
+        } else if (warp == kMmaWarp) {
+            // ---- MMA issuer
+            if (lane == 0) {
+                constexpr uint32_t ids = idesc(BF, 128, kKeys, false), ido = idesc(BF, 128, HD, true);
+                bool ok = wait(q_full, q_ph);
+                auto scores = [&](int t, uint32_t stage) {
+                    const uint32_t qa = sa(sm + M::q + t * M::tile), ka = sa(sm + M::kv + stage * M::tile);
+#pragma unroll
+                    for (int kk = 0; kk < HD / 16; ++kk)
+                        mma_ss(tmem + 128 * t, desc_k(qa + (kk >> 2) * kBlk) + (uint64_t)(2 * (kk & 3)),
+                               desc_k(ka + (kk >> 2) * kBlk) + (uint64_t)(2 * (kk & 3)), ids, kk > 0);
+                    commit(&s_full[t]);
+                };
+                if (ok && nt > 0) {
+                    ok = wait(&kv_full[ring.s], ring.ph);
+                    if (ok) {
+                        tc_after();
+                        for (int t = 0; t < halves; ++t) scores(t, ring.s);
+                        commit(&kv_empty[ring.s]);
+                        ring.next();
+                    }
+                }
+                for (int j = 0; j < nt && ok; ++j) {
+                    const Ring rv = ring;
+                    ring.next();
+                    const Ring rk = ring;
+                    const bool more = j + 1 < nt;
+                    if (!(ok = wait(&kv_full[rv.s], rv.ph))) break;
+                    const uint32_t va = sa(sm + M::kv + rv.s * M::tile);
+                    for (int t = 0; t < halves; ++t) {
+                        if (!(ok = wait(&p_full[t], sp_ph[t]))) break;
+                        sp_ph[t] ^= 1u;
+                        tc_after();
+#pragma unroll
+                        for (int kk = 0; kk < kKeys / 16; ++kk)
+                            mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 64 + 8 * kk, desc_mn(va + kk * 2048), ido,
+                                   j > 0 || kk > 0);
+                        if (more) {
+                            if (t == 0 && !(ok = wait(&kv_full[rk.s], rk.ph))) break;
+                            tc_after();
+                            scores(t, rk.s);
+                        } else {
+                            commit(&o_done[t]);
+                        }
+                    }
+                    if (!ok) break;
+                    commit(&kv_empty[rv.s]);
+                    if (more) {
+                        commit(&kv_empty[rk.s]);
+                        ring.next();
+                    }
+                }
+            }
+            __syncwarp();
+        } else if (warp >= kSoft0) {
+            // ---- the two halves: Q tile, softmax, epilogue
+            const int t = warp >= kSoft0 + 4 ? 1 : 0;
+            const int ht = tid - 32 * (kSoft0 + 4 * t);     // thread of the half
+            {
+                // neighbouring threads hold a row: 8 values each
+                uint8_t* qs = sm + M::q + t * M::tile;
+                for (int x = ht; x < 128 * CH; x += 128) {
+                    const int r = x / CH, ch = x % CH, row = u.row0 + 128 * t + r;
+                    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                    if (128 * t + r < u.n_row) {
+                        const int tok = row_token(a, u, row);
+                        const int64_t i = (int64_t)tok * a.q_tok + (int64_t)(kvh * a.G + row % a.G) * a.q_head + ch * 8;
+                        w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + i);
+                    }
+                    uint32_t v[4] = {w.x, w.y, w.z, w.w};
+                    float rs = fabsf(a.scale_log2);
+                    if constexpr (!BF && QT == W_BF16) {
+                        // f16 products: the row times a power of two that brings its largest value to [1, 2)
+                        float mx = 0.f;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(v[i] << 16)), fabsf(__uint_as_float(v[i] & 0xffff0000u))));
+#pragma unroll
+                        for (int o = CH / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                        const uint32_t ex = __float_as_uint(mx) >> 23;
+                        float dn = 1.f;
+                        if (ex > 0u && ex < 254u) {
+                            dn = __uint_as_float((254u - ex) << 23);
+                            rs *= __uint_as_float(ex << 23);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            v[i] = pack<false>(__uint_as_float(v[i] << 16) * dn, __uint_as_float(v[i] & 0xffff0000u) * dn);
+                    }
+                    if (a.scale_log2 < 0.f)                 // the scores' scale is positive, the sign is in Q
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) v[i] ^= 0x80008000u;
+                    *reinterpret_cast<uint4*>(qs + swz(r, ch)) = make_uint4(v[0], v[1], v[2], v[3]);
+                    if (ch == 0) rs_s[128 * t + r] = rs;
+                }
+                to_async_proxy();
+                // the rows' scales are read by other threads of the half
+                asm volatile("bar.sync %0, 128;" ::"r"(2 + t) : "memory");
+                bar_arrive(q_full);
+            }
+            const int r = 32 * (warp & 3) + lane;           // this thread's row of the half, its TMEM lane
+            const uint32_t lane_at = (uint32_t)(32 * (warp & 3)) << 16;
+            const uint32_t sb = tmem + 128 * t + lane_at, ob = tmem + 256 + 128 * t + lane_at;
+            const bool mine = 128 * t + r < u.n_row;
+            const int row = u.row0 + min(128 * t + r, u.n_row - 1);
+            const int tok = row_token(a, u, row);
+            const int rp = row_pos(a, u, row, tok), rh = hidden_below(a, rp);
+            const int wp_min = __reduce_min_sync(0xffffffffu, rp), wh_max = __reduce_max_sync(0xffffffffu, rh);
+            float rs = rs_s[128 * t + r];
+            float m = -INFINITY, l = 0.f;
+            bool live = t < halves;
+            for (int j = 0; j < nt && live; ++j) {
+                const bool got = wait(&meta_full[meta.s], meta.ph) && wait(&s_full[t], sp_ph[t]);
+                if (!__all_sync(0xffffffffu, got)) { live = false; break; }
+                tc_after();
+                sp_ph[t] ^= 1u;
+                if (F8 && j == 0) rs *= s0[0];
+                const int* kp = kpos + meta.s * kKeys;
+                const int4* kp4 = reinterpret_cast<const int4*>(kp);
+                const bool open = *reinterpret_cast<const uint32_t*>(full + meta.s * 4) == 0x01010101u &&
+                                  kp[kKeys - 1] <= wp_min && (kp[0] > wh_max || kp[kKeys - 1] < a.n_sink);
+                auto mask = [&](uint32_t* v, int c0, int n) {
+                    if (open) return;
+#pragma unroll
+                    for (int c = 0; c < n; c += 4) {
+                        const int4 k = kp4[(c0 + c) / 4];
+                        if (!sees(k.x, rp, rh, a.n_sink)) v[c] = __float_as_uint(-INFINITY);
+                        if (!sees(k.y, rp, rh, a.n_sink)) v[c + 1] = __float_as_uint(-INFINITY);
+                        if (!sees(k.z, rp, rh, a.n_sink)) v[c + 2] = __float_as_uint(-INFINITY);
+                        if (!sees(k.w, rp, rh, a.n_sink)) v[c + 3] = __float_as_uint(-INFINITY);
+                    }
+                };
+                auto top = [&](const uint32_t* v, int n, float mx) {
+#pragma unroll
+                    for (int c = 0; c < n; c += 4)
+                        mx = fmaxf(fmaxf(fmaxf(mx, __uint_as_float(v[c])), __uint_as_float(v[c + 1])),
+                                   fmaxf(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3])));
+                    return mx;
+                };
+                // the row's largest score: columns 0-63 are read again below (P overwrites 64-127 only)
+                uint32_t v[64];
+                tld32(sb, v);
+                tld32(sb + 32, v + 32);
+                ld_wait();
+                mask(v, 0, 64);
+                float mx = top(v, 64, -INFINITY);
+                tld32(sb + 64, v);
+                tld32(sb + 96, v + 32);
+                ld_wait();
+                mask(v, 64, 64);
+                mx = top(v, 64, mx) * rs;
+                float f = 1.f;
+                bool up = false;
+                if (mx > m + 14.f) {
+                    f = ex2(m - (mx - 6.f));                // 0 from nothing
+                    m = mx - 6.f;
+                    l *= f;
+                    up = true;
+                }
+                const float bias = m == -INFINITY ? 0.f : -m;   // nothing seen: every score is -inf
+                float l0 = 0.f, l1 = 0.f;
+                auto powers = [&](uint32_t* x, uint32_t* p) {   // 64 scores to 32 words of P
+#pragma unroll
+                    for (int c = 0; c < 64; c += 2) {
+                        float p0, p1;
+                        fma_pair(p0, p1, __uint_as_float(x[c]), __uint_as_float(x[c + 1]), rs, bias);
+                        p0 = ex2(p0);
+                        p1 = ex2(p1);
+                        add_pair(l0, l1, p0, p1);
+                        p[c / 2] = pack<BF>(p0, p1);
+                    }
+                };
+                powers(v, v);
+                tst32(sb + 96, v);
+                uint32_t w[64];
+                tld32(sb, w);
+                tld32(sb + 32, w + 32);
+                ld_wait();
+                mask(w, 0, 64);
+                powers(w, w);
+                tst32(sb + 64, w);
+                l += l0 + l1;
+                // O is complete up to the block before (its products precede these scores)
+                if (j > 0 && __any_sync(0xffffffffu, up)) {
+#pragma unroll 1
+                    for (int c = 0; c < HD; c += 32) {
+                        uint32_t o[32];
+                        tld32(ob + c, o);
+                        ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                        tst32(ob + c, o);
+                    }
+                }
+                st_wait();
+                tc_before();
+                bar_arrive(&p_full[t]);
+                meta.next();
+            }
+            if (t >= halves)
+                for (int j = 0; j < nt; ++j) meta.next();   // the other half's blocks
+            if (live && nt > 0) {
+                if (!__all_sync(0xffffffffu, wait(&o_done[t], o_ph))) live = false;
+                o_ph ^= 1u;
+                tc_after();
+            }
+            // ---- epilogue: a unit alone writes its rows, one of several its partial result
+            if (live) {
+                bool finite = l <= 3.0e38f && m <= 3.0e38f;
+                const float inv = l == 0.f ? 0.f : 1.f / l, sv = F8 && nt > 0 ? s0[1] : 1.f;
+                const int64_t at = ((int64_t)(u.part + u.chunk) * a.kv.Hkv + kvh) * kUnitRows2 + 128 * t + r;
+                const int64_t oi = (int64_t)tok * a.o_tok + (int64_t)(kvh * a.G + row % a.G) * a.o_head;
+                if (u.n_chunk > 1 && mine) a.part_ml[at] = make_float2(m, l);
+#pragma unroll 1
+                for (int c = 0; c < HD; c += 32) {
+                    uint32_t o[32];
+                    if (nt > 0) {
+                        tld32(ob + c, o);
+                        ld_wait();
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        float x[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            x[e] = nt > 0 ? __uint_as_float(o[i + e]) * sv : 0.f;
+                            finite = finite && fabsf(x[e]) <= 3.0e38f;
+                            if (u.n_chunk == 1) x[e] = l == 0.f ? 0.f : x[e] * inv;
+                        }
+                        if (!mine) continue;
+                        if (u.n_chunk == 1) store_out4(a, oi + c + i, x);
+                        else *reinterpret_cast<float4*>(a.part_o + at * HD + c + i) = make_float4(x[0], x[1], x[2], x[3]);
+                    }
+                }
+                if (!finite && mine) *redo_f = 1;
+            }
+            tc_before();
+        }
+        q_ph ^= 1u;
+        __syncthreads();
+        tc_after();
+        if (*abort_f) break;
+        if (*redo_f) {
+            // not every operand was finite (or an E4M3 row outgrew s0): the rows again, key by key
+            for (int r = warp; r < u.n_row; r += kThr / 32) {
+                float o[HD / 32], rm, rl;
+                const int row = u.row0 + r, tok = row_token(a, u, row);
+                careful_row<HD>(a, u, kvh, row, o, rm, rl);
+                const int64_t at = ((int64_t)(u.part + u.chunk) * a.kv.Hkv + kvh) * kUnitRows2 + r;
+                const int64_t oi = (int64_t)tok * a.o_tok + (int64_t)(kvh * a.G + row % a.G) * a.o_head;
+                const float inv = rl == 0.f ? 0.f : 1.f / rl;
+#pragma unroll
+                for (int d = 0; d < HD / 32; ++d) {
+                    if (u.n_chunk == 1) store_out1(a, oi + lane * (HD / 32) + d, rl == 0.f ? 0.f : o[d] * inv);
+                    else a.part_o[at * HD + lane * (HD / 32) + d] = o[d];
+                }
+                if (u.n_chunk > 1 && lane == 0) a.part_ml[at] = make_float2(rm, rl);
+            }
+            __syncthreads();
+            if (tid == 0) *redo_f = 0;
+        }
+        if (u.n_chunk > 1 && last_of_tile(a, u, kvh, flag)) merge_parts<HD>(a, u, kvh, kUnitRows2);
+        __syncthreads();
+    }
+    __syncthreads();
+    if (warp == kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
+}
+
+template <int HD, int CT, int QT>
+bool go(const AttnPagedArgs& a, cudaStream_t st) {
+    if (cudaFuncSetAttribute(attn_tc_rows_kernel<HD, CT, QT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)Smem<HD>::bytes) != cudaSuccess)
+        return false;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.n_sm);                             // one CTA per SM, each walking its units
+    cfg.blockDim = dim3(kThr);
+    cfg.dynamicSmemBytes = Smem<HD>::bytes;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = a.pdl ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, attn_tc_rows_kernel<HD, CT, QT>, a) == cudaSuccess;
+}
+template <int HD>
+bool go_hd(const AttnPagedArgs& a, cudaStream_t st) {
+    if (a.kv.type == W_F16) return go<HD, W_F16, W_F16>(a, st);
+    if (a.kv.type == W_BF16) return go<HD, W_BF16, W_BF16>(a, st);
+    return a.q_type == W_F16 ? go<HD, W_F8, W_F16>(a, st) : go<HD, W_F8, W_BF16>(a, st);
+}
+
+}  // namespace
+
+// F32 activations stay with the 16-row tiles, which carry Q and P as two terms each.
+bool attn_paged_tc_ok(int32_t hd, int32_t kv_type, int32_t q_type) {
+    return (hd == 64 || hd == 128) && q_type != W_F32 && attn_paged_types_ok(q_type, kv_type);
+}
+
+bool launch_attn_paged_tc(const AttnPagedArgs& a, cudaStream_t st) {
+    if (!attn_paged_tc_ok(a.kv.hd, a.kv.type, a.q_type)) return false;
+    return a.kv.hd == 64 ? go_hd<64>(a, st) : go_hd<128>(a, st);
+}
 
 }  // namespace llm

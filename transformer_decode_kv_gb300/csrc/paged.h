@@ -49,7 +49,7 @@ struct AttnUnit {
 };
 static_assert(sizeof(AttnUnit) == 64, "read as four int4");
 
-constexpr int kUnitRows1 = 16, kUnitRows2 = 128; // rows per tile of the two forms
+constexpr int kUnitRows1 = 16, kUnitRows2 = 256; // rows per tile of the two forms
 enum : int32_t { ATTN_FORM_ROWS = 1, ATTN_FORM_TC = 2 };
 enum AttnOut : int32_t { AO_F16 = 0, AO_BF16 = 1, AO_F32 = 2, AO_BF16_PAIR = 3 };
 
@@ -85,7 +85,7 @@ struct AttnPagedArgs {
 // Both forms' kernels as the plan's form says; false if a launch failed.
 bool launch_attn_paged(const AttnPagedArgs& a, cudaStream_t st);
 bool attn_paged_types_ok(int32_t q_type, int32_t kv_type);
-// 128-row tiles serve this shape (attn_paged_tc.cu).
+// 256-row tiles serve this shape (attn_paged_tc.cu).
 bool attn_paged_tc_ok(int32_t hd, int32_t kv_type, int32_t q_type);
 bool launch_attn_paged_tc(const AttnPagedArgs& a, cudaStream_t st);
 
@@ -98,7 +98,7 @@ struct PlanSeq {
 };
 struct PlanShape {
     int32_t G = 1, Hkv = 1, window = 0, n_sink = 0, n_sm = 148;
-    bool tc = false;                             // 128-row tiles allowed
+    bool tc = false;                             // 256-row tiles allowed
 };
 struct PagedPlan {
     std::vector<AttnUnit> units1, units2;
