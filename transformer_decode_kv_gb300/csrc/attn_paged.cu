@@ -9,13 +9,13 @@
 //                below a row maximum and raised lazily, when p would pass 2^14: O is rarely rescaled, the
 //                largest p is between 2^6 and 2^14, and f16's subnormal steps start 2^20 below it
 //   O += P V     mma.sync, the score fragments are the A operand as they stand
-// This form is for few rows per KV head (single tokens, short chunks), where reading K and V once
-// is the bound. Keys and values therefore go from global memory straight into the MMA's B
-// fragments, 16 bytes per load, without shared memory: a contraction may be taken in any order, so a
-// thread's 16 bytes of a key row simply are the dims its fragments hold (Q is loaded in the same
-// order), and a thread's values of four keys become fragments by byte permutes (f16/bf16: pairs of
-// keys; E4M3: 4 x 4 bytes, then the conversion to f16, which is exact). The next block's keys load
-// during this block's softmax and its values during the next block's scores.
+// This form is for few rows per KV head (single tokens, short chunks), where reading K and V once is the
+// bound. A contraction may be taken in any order, so a thread's 16 bytes of a key row simply are the dims its
+// B fragments hold (Q is loaded in the same order), and a thread's values of four keys become fragments
+// by byte permutes (f16/bf16: pairs of keys; E4M3: 4 x 4 bytes, then the conversion to f16, which is
+// exact). Every thread copies just the bytes it will use, asynchronously, into its own places of a ring in shared
+// memory (no bank conflicts, no barrier), as many blocks ahead as two CTAs per SM have room for: 3 blocks
+// of 8 KB per warp of an f16 cache with head_dim 128, 6 of an E4M3 one.
 //
 // Precision: products of f16 (bf16) terms with float32 sums. F16 activations and caches enter as they
 // are. BF16 or F32 activations over an f16-typed product are scaled per row by a power of two (taken out of the
@@ -73,29 +73,32 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
     lo = pack2<BF>(x - f.x, y - f.y);
 }
 
-// N words from global memory in 16-, 8- or 4-byte loads; cached lines are not kept in L1 (each row is
-// read once per tile)
+// N words (N = 1, 2, 4) from global memory to this thread's place in shared memory, asynchronously; zeros
+// where the key is not read
 template <int N>
-__device__ __forceinline__ void ldw(uint32_t* d, const uint8_t* p, bool ok) {
-    if (!ok) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) d[i] = 0u;
-        return;
-    }
-    if constexpr (N % 4 == 0) {
-#pragma unroll
-        for (int i = 0; i < N; i += 4)
-            asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(d[i]), "=r"(d[i + 1]), "=r"(d[i + 2]), "=r"(d[i + 3]) : "l"(p + 4 * i));
+__device__ __forceinline__ void fetch(uint32_t dst, const uint8_t* src, bool ok) {
+    if constexpr (N == 4)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+    else if constexpr (N == 2)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(ok ? 8 : 0) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(ok ? 4 : 0) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void take(uint32_t* d, const uint8_t* p) {
+    if constexpr (N == 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
+        d[0] = v.x; d[1] = v.y; d[2] = v.z; d[3] = v.w;
     } else if constexpr (N == 2) {
-        asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(d[0]), "=r"(d[1]) : "l"(p));
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
+        d[0] = v.x; d[1] = v.y;
     } else {
-        asm volatile("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(d[0]) : "l"(p));
+        d[0] = *reinterpret_cast<const uint32_t*>(p);
     }
 }
 
-// What lane L knows of key L % 16 of a block.
-struct Info { int64_t off; int pos; float ks, vs; };
+// Where lane L finds key L % 16 of a block (off < 0: not read) and its position.
+struct Info { int64_t off, soff; int pos; };
 
 template <int HD, int CT, int QT>
 struct Cfg {
@@ -110,15 +113,27 @@ struct Cfg {
     static constexpr int VP = F8 ? HD / 8 : (HD / 8 < 8 ? HD / 8 : 8);   // contiguous dims of a value per thread
     static constexpr int VH = HD / 8 / VP;                      // ... in VH places 8 * VP dims apart
     static constexpr int VWP = F8 ? VP / 4 : VP / 2;            // words of one place
+    // a stage: 16 keys of K and V as the lanes will read them (piece by piece, a lane's words side by
+    // side), then the keys' positions and, for E4M3, scales
+    static constexpr int KB = 2 * KW * 128, VB = 4 * VH * VWP * 128;
+    static constexpr int STAGE = KB + VB + 64 + (F8 ? 128 : 0);
+    static constexpr int OUT = kWarps * 16 * (HD + 4) * 4;       // the warps' results, over the stages
+    static constexpr int FIT = (112 * 1024 - 1024) / (kWarps * STAGE);
+    static constexpr int S = FIT < 8 ? FIT : 8;                 // two CTAs per SM
+    static constexpr int RING = kWarps * S * STAGE;
+    static constexpr int BYTES = (RING > OUT ? RING : OUT) + 2 * kWarps * 16 * 4 + 16;
 };
 
 template <int HD, int CT, int QT>
 __global__ void __launch_bounds__(kThr, 2) attn_rows_kernel(AttnPagedArgs a) {
     using C = Cfg<HD, CT, QT>;
     constexpr bool F8 = C::F8, BF = C::BF;
-    __shared__ __align__(16) float s_o[kWarps][16][HD + 4];
-    __shared__ float s_m[kWarps][16], s_l[kWarps][16];
-    __shared__ int s_flag;
+    extern __shared__ __align__(16) uint8_t sm[];
+    float (*s_o)[16][HD + 4] = reinterpret_cast<float (*)[16][HD + 4]>(sm);
+    constexpr int kEnd = C::RING > C::OUT ? C::RING : C::OUT;
+    float (*s_m)[16] = reinterpret_cast<float (*)[16]>(sm + kEnd);
+    float (*s_l)[16] = s_m + kWarps;
+    int& s_flag = *reinterpret_cast<int*>(sm + kEnd + 2 * kWarps * 16 * 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     if (a.pdl) asm volatile("griddepcontrol.wait;" ::: "memory");
     if (form_missing(a)) return;
@@ -207,40 +222,51 @@ __global__ void __launch_bounds__(kThr, 2) attn_rows_kernel(AttnPagedArgs a) {
         // a key no row sees is not read: its cell may hold anything
         const int hid_all = hidden_below(a, pmin);
 
+        const int nb = (u.v1 - u.v0 + 15) / 16;
         auto lookup = [&](int b) {
-            Info f;
-            f.off = -1;
-            f.pos = INT_MAX;
-            f.ks = f.vs = 0.f;
+            Info f{-1, 0, INT_MAX};
             const int v = u.v0 + 16 * b + (lane & 15);
-            if (v < u.v1) {
+            if (b < nb && v < u.v1) {
                 const KeyAt k = key_at(a, u, v);
                 if (k.off >= 0 && sees(k.pos, pmax, hid_all, a.n_sink)) {
                     f.off = k.off;
+                    f.soff = k.soff;
                     f.pos = k.pos;
-                    if constexpr (F8) { f.ks = ksb[k.soff]; f.vs = vsb[k.soff]; }
                 }
             }
             return f;
         };
-        uint32_t kr[2][C::KW], vr[4][C::VH * C::VWP];
-        auto load_k = [&](const Info& f) {
+        uint8_t* const ring = sm + warp * C::S * C::STAGE;
+        // the copies of block b into stage s; a group of copies is counted even where there is no block
+        auto issue = [&](int b, int s, const Info& f) {
+            uint8_t* const st = ring + s * C::STAGE;
+            if (b < nb) {
+                const uint32_t ka = static_cast<uint32_t>(__cvta_generic_to_shared(st));
+                const uint32_t va = ka + C::KB;
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const int64_t off = __shfl_sync(0xffffffffu, f.off, 8 * t + g);
+                for (int t = 0; t < 2; ++t) {
+                    const int64_t off = __shfl_sync(0xffffffffu, f.off, 8 * t + g);
+                    const uint8_t* src = kbase + (off >= 0 ? off : 0) + 4 * C::KC * c;
 #pragma unroll
-                for (int i = 0; i < C::KW / C::KC; ++i)
-                    ldw<C::KC>(&kr[t][C::KC * i], kbase + off + 4 * C::KC * (4 * i + c), off >= 0);
+                    for (int i = 0; i < C::KW / C::KC; ++i)
+                        fetch<C::KC>(ka + (t * C::KW / C::KC + i) * 128 * C::KC + lane * 4 * C::KC, src + 16 * C::KC * i,
+                                     off >= 0);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int64_t off = __shfl_sync(0xffffffffu, f.off, 2 * c + (e & 1) + 8 * (e >> 1));
+                    const uint8_t* src = vbase + (off >= 0 ? off : 0) + 4 * C::VWP * g;
+#pragma unroll
+                    for (int i = 0; i < C::VH; ++i)
+                        fetch<C::VWP>(va + (e * C::VH + i) * 128 * C::VWP + lane * 4 * C::VWP, src + 32 * C::VWP * i, off >= 0);
+                }
+                const uint32_t ma = va + C::VB;
+                if (lane < 16) *reinterpret_cast<int*>(st + C::KB + C::VB + 4 * lane) = f.pos;
+                if constexpr (F8)
+                    fetch<1>(ma + 64 + 4 * lane,
+                             reinterpret_cast<const uint8_t*>((lane < 16 ? ksb : vsb) + (f.off >= 0 ? f.soff : 0)), f.off >= 0);
             }
-        };
-        auto load_v = [&](const Info& f) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int64_t off = __shfl_sync(0xffffffffu, f.off, 2 * c + (e & 1) + 8 * (e >> 1));
-#pragma unroll
-                for (int i = 0; i < C::VH; ++i)
-                    ldw<C::VWP>(&vr[e][C::VWP * i], vbase + off + 4 * C::VWP * (8 * i + g), off >= 0);
-            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
         };
 
         float O[C::NT][4];
@@ -251,46 +277,64 @@ __global__ void __launch_bounds__(kThr, 2) attn_rows_kernel(AttnPagedArgs a) {
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
         float E = 0.f;                                      // O is in units of E (E4M3 values only)
 
-        const int nb = (u.v1 - u.v0 + 15) / 16;
-        Info cur, nxt;
-        if (warp < nb) {
-            cur = lookup(warp);
-            load_k(cur);
-            load_v(cur);
-            nxt = lookup(warp + kWarps);
+        Info nxt;
+        {
+            Info f[C::S - 1];
+#pragma unroll
+            for (int s = 0; s < C::S - 1; ++s) f[s] = lookup(warp + s * kWarps);
+#pragma unroll
+            for (int s = 0; s < C::S - 1; ++s) issue(warp + s * kWarps, s, f[s]);
+            nxt = lookup(warp + (C::S - 1) * kWarps);
         }
+        int stage = 0, free_stage = C::S - 1;
         for (int b = warp; b < nb; b += kWarps) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(C::S - 2) : "memory");
+            __syncwarp();
+            // the stage read in the last round takes the block S - 1 rounds ahead
+            issue(b + (C::S - 1) * kWarps, free_stage, nxt);
+            nxt = lookup(b + C::S * kWarps);
+            const uint8_t* const st = ring + stage * C::STAGE;
+            free_stage = stage;
+            if (++stage == C::S) stage = 0;
             float S[2][4] = {};
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int t = 0; t < 2; ++t) {
+                uint32_t kr[C::KW];
+#pragma unroll
+                for (int i = 0; i < C::KW / C::KC; ++i)
+                    take<C::KC>(&kr[C::KC * i], st + (t * C::KW / C::KC + i) * 128 * C::KC + lane * 4 * C::KC);
 #pragma unroll
                 for (int s = 0; s < C::KS; ++s) {
                     uint32_t b0, b1;
                     if constexpr (F8) {
-                        b0 = e4m3x2_to_h2(kr[t][s] & 0xffffu);
-                        b1 = e4m3x2_to_h2(kr[t][s] >> 16);
+                        b0 = e4m3x2_to_h2(kr[s] & 0xffffu);
+                        b1 = e4m3x2_to_h2(kr[s] >> 16);
                     } else {
-                        b0 = kr[t][2 * s];
-                        b1 = kr[t][2 * s + 1];
+                        b0 = kr[2 * s];
+                        b1 = kr[2 * s + 1];
                     }
                     mma<BF>(S[t], qf[s], b0, b1);
                     if constexpr (C::SPLIT_Q) mma<BF>(S[t], ql[s], b0, b1);
                 }
-            if (b + kWarps < nb) load_k(nxt);
+            }
+            const uint8_t* const meta = st + C::KB + C::VB;
             // scores in the log2 domain, masked; the rows' maxima
             float mx[2] = {-INFINITY, -INFINITY};
             float kvs[2][2];
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int t = 0; t < 2; ++t) {
+                const int2 kp2 = *reinterpret_cast<const int2*>(meta + 4 * (8 * t + 2 * c));
+                float2 ks2 = make_float2(1.f, 1.f);
+                if constexpr (F8) {
+                    ks2 = *reinterpret_cast<const float2*>(meta + 64 + 4 * (8 * t + 2 * c));
+                    const float2 v2 = *reinterpret_cast<const float2*>(meta + 128 + 4 * (8 * t + 2 * c));
+                    kvs[t][0] = v2.x;
+                    kvs[t][1] = v2.y;
+                }
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int src = 8 * t + 2 * c + e;
-                    const int kp = __shfl_sync(0xffffffffu, cur.pos, src);
-                    float ksc = 1.f;
-                    if constexpr (F8) {
-                        ksc = __shfl_sync(0xffffffffu, cur.ks, src);
-                        kvs[t][e] = __shfl_sync(0xffffffffu, cur.vs, src);
-                    }
+                    const int kp = e ? kp2.y : kp2.x;
+                    const float ksc = e ? ks2.y : ks2.x;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         float& s = S[t][2 * h + e];
@@ -298,6 +342,7 @@ __global__ void __launch_bounds__(kThr, 2) attn_rows_kernel(AttnPagedArgs a) {
                         mx[h] = fmaxf(mx[h], s);
                     }
                 }
+            }
             bool up = false;
             float f[2] = {1.f, 1.f};
 #pragma unroll
@@ -313,9 +358,9 @@ __global__ void __launch_bounds__(kThr, 2) attn_rows_kernel(AttnPagedArgs a) {
             }
             if constexpr (F8) {
                 // the values' scales relative to the largest seen
-                float e = cur.vs;
-#pragma unroll
-                for (int o = 8; o > 0; o >>= 1) e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, o));
+                float e = fmaxf(fmaxf(kvs[0][0], kvs[0][1]), fmaxf(kvs[1][0], kvs[1][1]));
+                e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, 1));
+                e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, 2));
                 if (e > E) {
                     f[0] *= E / e;
                     f[1] *= E / e;
@@ -348,26 +393,31 @@ __global__ void __launch_bounds__(kThr, 2) attn_rows_kernel(AttnPagedArgs a) {
                 if constexpr (C::SPLIT_P) mma<BF>(O[n], pl, b0, b1);
             };
 #pragma unroll
-            for (int i = 0; i < C::VH * C::VWP; ++i) {
-                const uint32_t w0 = vr[0][i], w1 = vr[1][i], w2 = vr[2][i], w3 = vr[3][i];
-                if constexpr (F8) {
-                    const uint32_t x0 = __byte_perm(w0, w1, 0x5140), x1 = __byte_perm(w0, w1, 0x7362);
-                    const uint32_t y0 = __byte_perm(w2, w3, 0x5140), y1 = __byte_perm(w2, w3, 0x7362);
-                    pv(4 * i, e4m3x2_to_h2(x0 & 0xffffu), e4m3x2_to_h2(y0 & 0xffffu));
-                    pv(4 * i + 1, e4m3x2_to_h2(x0 >> 16), e4m3x2_to_h2(y0 >> 16));
-                    pv(4 * i + 2, e4m3x2_to_h2(x1 & 0xffffu), e4m3x2_to_h2(y1 & 0xffffu));
-                    pv(4 * i + 3, e4m3x2_to_h2(x1 >> 16), e4m3x2_to_h2(y1 >> 16));
-                } else {
-                    pv(2 * i, __byte_perm(w0, w1, 0x5410), __byte_perm(w2, w3, 0x5410));
-                    pv(2 * i + 1, __byte_perm(w0, w1, 0x7632), __byte_perm(w2, w3, 0x7632));
+            for (int p = 0; p < C::VH; ++p) {
+                uint32_t vr[4][C::VWP];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    take<C::VWP>(vr[e], st + C::KB + (e * C::VH + p) * 128 * C::VWP + lane * 4 * C::VWP);
+#pragma unroll
+                for (int w = 0; w < C::VWP; ++w) {
+                    const int i = p * C::VWP + w;
+                    const uint32_t w0 = vr[0][w], w1 = vr[1][w], w2 = vr[2][w], w3 = vr[3][w];
+                    if constexpr (F8) {
+                        const uint32_t x0 = __byte_perm(w0, w1, 0x5140), x1 = __byte_perm(w0, w1, 0x7362);
+                        const uint32_t y0 = __byte_perm(w2, w3, 0x5140), y1 = __byte_perm(w2, w3, 0x7362);
+                        pv(4 * i, e4m3x2_to_h2(x0 & 0xffffu), e4m3x2_to_h2(y0 & 0xffffu));
+                        pv(4 * i + 1, e4m3x2_to_h2(x0 >> 16), e4m3x2_to_h2(y0 >> 16));
+                        pv(4 * i + 2, e4m3x2_to_h2(x1 & 0xffffu), e4m3x2_to_h2(y1 & 0xffffu));
+                        pv(4 * i + 3, e4m3x2_to_h2(x1 >> 16), e4m3x2_to_h2(y1 >> 16));
+                    } else {
+                        pv(2 * i, __byte_perm(w0, w1, 0x5410), __byte_perm(w2, w3, 0x5410));
+                        pv(2 * i + 1, __byte_perm(w0, w1, 0x7632), __byte_perm(w2, w3, 0x7632));
+                    }
                 }
             }
-            if (b + kWarps < nb) {
-                load_v(nxt);
-                cur = nxt;
-                nxt = lookup(b + 2 * kWarps);
-            }
         }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();                                    // the results go where the stages were
         // this warp's state to shared memory: row sums over the four threads of a row
         bool finite = true;
 #pragma unroll
@@ -434,9 +484,14 @@ __global__ void __launch_bounds__(kThr, 2) attn_rows_kernel(AttnPagedArgs a) {
 
 template <int HD, int CT, int QT>
 bool go(const AttnPagedArgs& a, cudaStream_t st) {
+    using C = Cfg<HD, CT, QT>;
+    if (cudaFuncSetAttribute(attn_rows_kernel<HD, CT, QT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES) !=
+        cudaSuccess)
+        return false;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * a.n_sm);                         // two CTAs per SM, each walking its units
     cfg.blockDim = dim3(kThr);
+    cfg.dynamicSmemBytes = C::BYTES;
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
