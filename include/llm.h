@@ -369,7 +369,8 @@ int llm_attn_plan_set(llm_attn_plan *plan, int32_t n_seq, const int32_t *n_new, 
 int llm_attn_run(llm_attn_plan *plan, const void *q, int64_t q_stride_tok, int64_t q_stride_head,
                  const llm_kv_pages *kv, void *out, int64_t o_stride_tok, int64_t o_stride_head,
                  void *stream);
-/* 0: nothing to run, 1: 16-row tiles (few rows per KV head), 2: 256-row tensor-core tiles. -1: NULL. */
+/* The kernels the plan needs: 0 nothing to run, else the sum of 1 (8-row tiles: a token or two per
+ * sequence), 2 (16-row tiles: a few) and 4 (256-row tensor-core tiles: chunks). -1: NULL. */
 int llm_attn_plan_form(const llm_attn_plan *plan);
 /* The plan's error word (0 = none) after waiting for its device; cleared by the call. */
 uint32_t llm_attn_plan_error(llm_attn_plan *plan);
@@ -543,13 +544,14 @@ int llm_debug_set_logits(llm_ctx *ctx, int32_t i, const float *row);
 /* The units of work llm_attn_plan_set would make for a step on a GPU of n_sm SMs, without one: 16 int32
  * values per unit (first token, first row, rows, position of the first token; page-table offset, sink keys,
  * first windowed key, first virtual key; end key, units of the tile, this unit's index, its first partial
- * slot; ticket, 3 unused), those of 16-row tiles first (n_rows_units receives their number). tc != 0
- * allows 256-row tiles. caps, if given, receives the plan's buffer bounds for the shape's maxima:
- * 16-row and 256-row units, tiles, 16-row and 256-row partial slots. Returns the number of units (writes at
- * most cap of them), -1 for invalid arguments. */
+ * slot; ticket, KV head, 2 unused), those of the 8- or 16-row tiles first (n_rows_units receives their
+ * number). tc != 0 allows 256-row tiles. first, if given, receives two arrays of 3 n_sm + 1: where the
+ * units of each CTA begin, for the small and the 256-row tiles. caps, if given, receives the plan's
+ * buffer bounds for the shape's maxima: units of both, CTAs of both, tickets, partial slots of both. Returns the
+ * number of units (writes at most cap of them), -1 for invalid arguments. */
 int64_t llm_debug_attn_units(const llm_attn_shape *shape, const llm_kv_pages *kv, int32_t n_sm, int32_t tc,
                              int32_t n_seq, const int32_t *n_new, const int32_t *n_kv, int32_t *out,
-                             int64_t cap, int64_t *n_rows_units, int64_t caps[5]);
+                             int64_t cap, int64_t *n_rows_units, int32_t *first, int64_t caps[7]);
 
 /* Fault injection: kind 1 makes ubatch `ub` of the next llm_decode hand the K/V append kernel a
  * cell index past the cache; the kernel's bounds check skips the write and reports the error

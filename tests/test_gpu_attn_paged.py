@@ -148,6 +148,20 @@ def test_non_finite_rows_reach_only_the_tokens_that_see_them(L, act, cdt, n_new)
         check(L, act, cdt, 64, 2, 4, 16, [n_new], n_kv, window=5, n_sink=1, seed=21, mutate=mutate)
 
 
+@pytest.mark.parametrize("n_new", [1, 3, 40])
+@pytest.mark.parametrize("act,cdt", [PAIRS[0], PAIRS[1], PAIRS[4]])
+def test_a_token_that_sees_only_nan_gives_nan(L, act, cdt, n_new):
+    n_kv = [n_new + 20]
+
+    def mutate(k, v, kv_, vv, tables):
+        cell = int(tables[0][(n_kv[0] - 1) // 16]) * 16 + (n_kv[0] - 1) % 16
+        k[cell // 16, cell % 16] = 0x7f if k.dtype == torch.uint8 else float("nan")
+        kv_[cell] = np.nan
+
+    with np.errstate(all="ignore"):
+        check(L, act, cdt, 64, 2, 4, 16, [n_new], n_kv, window=1, seed=22, mutate=mutate)
+
+
 @pytest.mark.parametrize("act,cdt", [PAIRS[0], PAIRS[2], PAIRS[4]])
 def test_large_and_small_activations(L, act, cdt):
     """Rows of q far from 1 (their products stay finite) and a scale of its own."""

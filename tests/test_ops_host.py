@@ -86,7 +86,7 @@ def test_bad_attention_shapes_are_refused(B, bad):
     s = B.AttnShape(**{**GOOD_SHAPE, **bad})
     d = desc(B)
     assert not B.lib().llm_attn_plan_init(C.byref(s), C.byref(d))
-    assert B.lib().llm_debug_attn_units(C.byref(s), C.byref(d), 152, 0, 0, None, None, None, 0, None, None) == -1
+    assert B.lib().llm_debug_attn_units(C.byref(s), C.byref(d), 152, 0, 0, None, None, None, 0, None, None, None) == -1
 
 
 def test_null_arguments_are_refused(B):
@@ -119,74 +119,86 @@ def test_bad_sampler_arguments_are_refused(B, bad):
 def units_of(B, shape, kv, n_new, n_kv, n_sm=152, tc=0):
     n_new, n_kv = np.asarray(n_new, np.int32), np.asarray(n_kv, np.int32)
     p = lambda a: a.ctypes.data_as(C.POINTER(C.c_int32))
-    n1, caps = C.c_int64(), (C.c_int64 * 5)()
+    n1, caps = C.c_int64(), (C.c_int64 * 7)()
     args = (C.byref(shape), C.byref(kv), n_sm, tc, len(n_new), p(n_new), p(n_kv))
-    n = B.lib().llm_debug_attn_units(*args, None, 0, C.byref(n1), caps)
+    first = np.zeros((2, 3 * n_sm + 1), np.int32)
+    n = B.lib().llm_debug_attn_units(*args, None, 0, C.byref(n1), None, caps)
     assert n >= 0, B.lib().llm_op_last_error()
     out = np.zeros((max(n, 1), 16), np.int32)
-    assert B.lib().llm_debug_attn_units(*args, p(out), n, C.byref(n1), caps) == n
-    return out[:n], n1.value, list(caps)
+    assert B.lib().llm_debug_attn_units(*args, p(out), n, C.byref(n1), p(first), caps) == n
+    return out[:n], n1.value, first, list(caps)
 
 
-@pytest.mark.parametrize("seed", range(40))
+@pytest.mark.parametrize("seed", range(60))
 def test_plan_covers_every_visible_key_once(B, seed):
     rng = np.random.default_rng(seed)
     Hkv, G = int(rng.choice([1, 2, 8])), int(rng.choice([1, 3, 4, 8]))
     window = int(rng.choice([0, 0, 1, 7, 64, 300]))
     n_sink = int(rng.choice([0, 1, 4, 40]))
     n_seq = int(rng.integers(0, 7))
-    n_new = rng.integers(0, 90, n_seq)
+    n_new = rng.integers(0, 90, n_seq) if seed % 5 else rng.integers(0, 2, n_seq)
     n_kv = np.maximum(0, n_new + rng.integers(-20, 700, n_seq))
     if n_seq and seed % 3 == 0:
         n_kv[0] += 20000                                   # one long sequence
     tok, page = max(1, int(n_new.sum())), 16
+    n_sm = [152, 3, 1][seed % 3]
     shape = B.AttnShape(type=1, n_head=Hkv * G, scale=0.0, window=window, n_sink=n_sink, max_tok=tok,
                         max_seq=max(1, n_seq), max_table=max(1, int((n_kv // page + 1).sum())))
     kv = desc(B, n_head_kv=Hkv, n_pages=4096, page_size=page)
-    tc = seed % 2
-    units, n1, caps = units_of(B, shape, kv, n_new, n_kv, n_sm=[152, 8][seed % 4 == 0], tc=tc)
-    seen = {}                                              # (token, head of the group) -> keys
+    units, n1, first, caps = units_of(B, shape, kv, n_new, n_kv, n_sm=n_sm, tc=seed % 2)
+    seen = {}                                              # (sequence, token, query head) -> keys
     starts = np.concatenate([[0], np.cumsum(n_new)])
     tabs = np.concatenate([[0], np.cumsum(-(-n_kv // page))])
-    parts, tiles = [set(), set()], {}
+    parts, tickets, chunks = [set(), set()], {}, {}
+    max_row = max([int(u[2]) for u in units[:n1]], default=0)
     for i, u in enumerate(units):
-        tok0, row0, n_row, p0, tab, ns, lo, v0, v1, n_chunk, chunk, part, tile = u[:13]
+        tok0, row0, n_row, p0, tab, ns, lo, v0, v1, n_chunk, chunk, part, ticket, head = u[:14]
         s = [j for j in range(n_seq) if starts[j] == tok0 and n_new[j] > 0][0]
-        assert tab == tabs[s] and p0 == n_kv[s] - n_new[s]
+        assert tab == tabs[s] and p0 == n_kv[s] - n_new[s] and 0 <= head < Hkv
         assert 1 <= n_row <= (16 if i < n1 else 256) and 0 <= v0 <= v1 and 0 <= chunk < n_chunk
-        tiles.setdefault(tile, []).append((chunk, n_chunk))
+        tile = (i >= n1, tok0, row0, head)
+        chunks.setdefault(tile, []).append((chunk, n_chunk))
         if n_chunk > 1:
-            slot = part + chunk
-            assert slot not in parts[i >= n1]
-            parts[i >= n1].add(slot)
+            assert part + chunk not in parts[i >= n1]
+            parts[i >= n1].add(part + chunk)
+            assert tickets.setdefault(ticket, tile) == tile
         keys = [v if v < ns else v - ns + lo for v in range(v0, v1)]
         assert all(0 <= k < n_kv[s] for k in keys)
         for r in range(row0, row0 + n_row):
             t, h = divmod(r, G)
             p = p0 + t
-            vis = [k for k in keys if k <= p and (window == 0 or k > p - window or k < n_sink)]
-            got = seen.setdefault((s, t, h), [])
-            got += vis
+            got = seen.setdefault((s, t, head * G + h), [])
+            got += [k for k in keys if k <= p and (window == 0 or k > p - window or k < n_sink)]
     for s in range(n_seq):
         for t in range(n_new[s]):
             p = n_kv[s] - n_new[s] + t
             want = [k for k in range(p + 1) if window == 0 or k > p - window or k < n_sink]
-            for h in range(G):
+            for h in range(Hkv * G):
                 assert sorted(seen[(s, t, h)]) == want
-    for c in tiles.values():
+    for c in chunks.values():
         assert sorted(x[0] for x in c) == list(range(c[0][1]))
-    assert n1 <= caps[0] and len(units) - n1 <= caps[1] and len(tiles) <= caps[2]
-    assert all(t < caps[2] for t in tiles)
-    assert max(parts[0], default=-1) < caps[3] and max(parts[1], default=-1) < max(caps[4], 1)
+    # the CTAs' ranges are the units, each once and in order
+    ctas = [n_sm * (3 if max_row <= 8 else 2), n_sm]
+    for f, n in ((0, n1), (1, len(units) - n1)):
+        if n:
+            r = first[f][:ctas[f] + 1]
+            assert r[0] == 0 and r[-1] == n and (np.diff(r) >= 0).all()
+    # and everything fits the plan's buffers
+    assert n1 <= caps[0] and len(units) - n1 <= caps[1]
+    assert ctas[0] <= caps[2] and (len(units) == n1 or ctas[1] <= caps[3])
+    assert all(0 <= t < caps[4] for t in tickets)
+    assert max(parts[0], default=-1) < caps[5] and max(parts[1], default=-1) < max(caps[6], 1)
 
 
-def test_plan_splits_a_long_sequence_over_the_gpu(B):
-    shape = B.AttnShape(**{**GOOD_SHAPE, "max_table": 1 << 20})
+@pytest.mark.parametrize("n_kv", [[300000], [32768 - 1571 * i for i in range(16)], [9, 70000, 5, 2000]])
+def test_plan_gives_every_cta_an_even_share(B, n_kv):
+    shape = B.AttnShape(**{**GOOD_SHAPE, "max_table": 1 << 20, "max_seq": 64})
     kv = desc(B, n_pages=1 << 16)
-    units, _, _ = units_of(B, shape, kv, [1], [300000])
-    # 2 KV heads on 304 resident CTAs: at least 140 units per head, none much longer than another
-    assert len(units) >= 140
-    assert (units[:, 8] - units[:, 7]).max() <= 300000 * 2 / 304 + 64
+    units, _, first, _ = units_of(B, shape, kv, [1] * len(n_kv), n_kv)
+    load = [(units[a:b, 8] - units[a:b, 7]).sum() for a, b in zip(first[0][:-1], first[0][1:])]
+    fair = sum(n_kv) * 2 / len(load)
+    # a share is even up to two blocks of 128 keys for the units' own costs and one for rounding
+    assert max(load) <= fair + 3 * 128
 
 
 @pytest.mark.parametrize("n_new,n_kv", [([1] * 9, [1] * 9), ([65], [65]), ([-1], [4]), ([1], [-1]),
@@ -196,4 +208,4 @@ def test_steps_past_the_shape_are_refused(B, n_new, n_kv):
     a, b = np.asarray(n_new, np.int32), np.asarray(n_kv, np.int32)
     p = lambda x: x.ctypes.data_as(C.POINTER(C.c_int32))
     assert B.lib().llm_debug_attn_units(C.byref(shape), C.byref(kv), 152, 0, len(a), p(a), p(b), None, 0,
-                                        None, None) == -1
+                                        None, None, None) == -1

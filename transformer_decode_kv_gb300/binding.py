@@ -152,7 +152,7 @@ SIGNATURES = {
     "llm_debug_attn_units": (C.c_int64, [C.POINTER(AttnShape), C.POINTER(KvPagesDesc), C.c_int32,
                                          C.c_int32, C.c_int32, C.POINTER(C.c_int32),
                                          C.POINTER(C.c_int32), C.POINTER(C.c_int32), C.c_int64,
-                                         C.POINTER(C.c_int64), C.POINTER(C.c_int64)]),
+                                         C.POINTER(C.c_int64), C.POINTER(C.c_int32), C.POINTER(C.c_int64)]),
     "llm_debug_kernel_stats": (C.c_int32, [C.c_void_p, C.c_int32, C.c_char_p, C.c_int32,
                                            C.POINTER(C.c_int64), C.POINTER(C.c_double),
                                            C.POINTER(C.c_double), C.POINTER(C.c_double)]),

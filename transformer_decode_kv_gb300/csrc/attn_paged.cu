@@ -1,27 +1,28 @@
-// Attention of new tokens over a paged cache, 16-row tiles: out = softmax(scale q K^T, masked) V for the
-// (token, query head) pairs that share a KV head, an optional sliding window and sink keys.
+// Attention of new tokens over a paged cache, 8- and 16-row tiles: out = softmax(scale q K^T, masked) V for
+// the (token, query head) pairs that share a KV head, an optional sliding window and sink keys.
 //
-// A warp owns 16 rows and walks blocks of 16 keys; the four warps of a CTA take every fourth block
-// of the unit's keys and merge their (maximum, sum, output) at the end, the units of a tile
-// through partial results in global memory (the last to finish merges). Per block and warp:
-//   S = Q K^T    mma.sync m16n8k16, two 8-key column tiles, float32 sums
-//   softmax      p = 2^(s - m) with a reference m and the sum l per row in float32, in the log2 domain. m is 6
-//                below a row maximum and raised lazily, when p would pass 2^14: O is rarely rescaled, the
-//                largest p is between 2^6 and 2^14, and f16's subnormal steps start 2^20 below it
-//   O += P V     mma.sync, the score fragments are the A operand as they stand
+// A CTA walks its share of the plan's units. Its four warps take 32 keys of every 128 of a unit's and
+// merge their (reference, sum, output) at the end; the units of a cut tile merge through partial results in
+// global memory (the last to finish does it). Per 16 keys and warp, with the keys and dims as the rows of the MMA
+// and the tile's 8 (or 2 x 8) rows as its columns, so that few rows waste little:
+//   S^T = K Q^T      mma.sync m16n8k16, 16 keys x 8 rows, float32 sums
+//   softmax          p = 2^(s - m) with a reference m per row in float32, in the log2 domain. m is 6 below a
+//                    row maximum and raised lazily, when some p would pass 2^14: no maximum is reduced
+//                    otherwise, O is rarely rescaled, the largest p is between 2^6 and 2^14, and f16's
+//                    subnormal steps start 2^20 below it
+//   O^T += V^T P^T   mma.sync, 16 dims x 8 rows; P^T from S^T by an 8x8 transpose between the lanes
 // This form is for few rows per KV head (single tokens, short chunks), where reading K and V once is the
-// bound. A contraction may be taken in any order, so a thread's 16 bytes of a key row simply are the dims its
-// B fragments hold (Q is loaded in the same order), and a thread's values of four keys become fragments
+// bound. A contraction may be taken in any order, so a lane's 16 bytes of a key row simply are the dims its
+// A fragments hold (Q is loaded in the same order), and a lane's values of four keys become fragments
 // by byte permutes (f16/bf16: pairs of keys; E4M3: 4 x 4 bytes, then the conversion to f16, which is
-// exact). Every thread copies just the bytes it will use, asynchronously, into its own places of a ring in shared
-// memory (no bank conflicts, no barrier), as many blocks ahead as two CTAs per SM have room for: 3 blocks
-// of 8 KB per warp of an f16 cache with head_dim 128, 6 of an E4M3 one.
+// exact). Every lane copies just the bytes it will use, asynchronously, into its own places of a ring in shared
+// memory (no bank conflicts, no barrier), as many blocks of 16 keys ahead as the CTAs of an SM have room for.
 //
 // Precision: products of f16 (bf16) terms with float32 sums. F16 activations and caches enter as they
 // are. BF16 or F32 activations over an f16-typed product are scaled per row by a power of two (taken out of the
 // scores again), so that no value leaves f16's range; F32 ones enter as two f16 terms (22 bits). P is
-// rounded to f16 (relative 2^-11 / 2) where activations are f16; for F32 activations and for bf16 products
-// it enters as two terms, so its rounding (2^-9 / 2 for bf16) does not show. An E4M3 row's scale multiplies
+// rounded to f16 (half a step: 2^-11) where activations are f16; for F32 activations and for bf16 products
+// it enters as two terms, so its rounding (2^-8 for bf16) does not show. An E4M3 row's scale multiplies
 // the score (K) or p (V, relative to the largest scale seen so far by the warp, a power of two, so exact
 // down to f16's subnormals).
 #include "attn_paged_common.cuh"
@@ -40,17 +41,20 @@ constexpr int kThr = 32 * kWarps;
 template <bool BF>
 __device__ __forceinline__ void mma(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
     if constexpr (BF)
-        asm(
-            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
     else
-        asm(
-            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// (lo, hi) as two f16 or bf16; with `rest` the rounding errors as a second pair
+// the 8x8 matrix of 16-bit values whose row lane / 4 this lane holds two of, transposed
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
 template <bool BF>
 __device__ __forceinline__ uint32_t pack2(float x, float y) {
     if constexpr (BF) {
@@ -66,6 +70,7 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
     if constexpr (BF) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
     else return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
+// (x, y) as two terms: rounded, and the rounding errors
 template <bool BF>
 __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
     hi = pack2<BF>(x, y);
@@ -73,7 +78,7 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
     lo = pack2<BF>(x - f.x, y - f.y);
 }
 
-// N words (N = 1, 2, 4) from global memory to this thread's place in shared memory, asynchronously; zeros
+// N words (N = 1, 2, 4) from global memory to this lane's place in shared memory, asynchronously; zeros
 // where the key is not read
 template <int N>
 __device__ __forceinline__ void fetch(uint32_t dst, const uint8_t* src, bool ok) {
@@ -97,81 +102,151 @@ __device__ __forceinline__ void take(uint32_t* d, const uint8_t* p) {
     }
 }
 
-// Where lane L finds key L % 16 of a block (off < 0: not read) and its position.
+// Where this lane's key of a group of 32 lies (off < 0: not read) and its position.
 struct Info { int64_t off, soff; int pos; };
 
-template <int HD, int CT, int QT>
+template <int HD, int CT, int QT, int ROWS>
 struct Cfg {
     static constexpr bool F8 = CT == W_F8, BF = CT == W_BF16;
     static constexpr bool SPLIT_Q = QT == W_F32;
     static constexpr bool SPLIT_P = QT == W_F32 || BF;
     static constexpr bool ROW_SCALE = !BF && QT != W_F16;
-    static constexpr int KS = HD / 16;                          // k-steps of Q K^T
-    static constexpr int KW = F8 ? HD / 16 : HD / 8;            // words of a key a thread holds
-    static constexpr int KC = KW < 4 ? KW : 4;                  // ... loaded KC at a time
-    static constexpr int NT = HD / 8;                           // 8-dim column tiles of O
-    static constexpr int VP = F8 ? HD / 8 : (HD / 8 < 8 ? HD / 8 : 8);   // contiguous dims of a value per thread
+    static constexpr int R = ROWS / 8;                          // 8-row column tiles
+    static constexpr int KS = HD / 16;                          // k-steps of K Q^T
+    static constexpr int KW = F8 ? HD / 16 : HD / 8;            // words of a key a lane holds
+    static constexpr int KC = KW < 4 ? KW : 4;                  // ... copied KC at a time
+    static constexpr int KP = KW / KC;
+    static constexpr int MT = HD / 16;                          // 16-dim row tiles of O^T
+    static constexpr int VP = F8 ? HD / 8 : (HD / 8 < 8 ? HD / 8 : 8);   // contiguous dims of a value per lane
     static constexpr int VH = HD / 8 / VP;                      // ... in VH places 8 * VP dims apart
-    static constexpr int VWP = F8 ? VP / 4 : VP / 2;            // words of one place
+    static constexpr int VW = F8 ? VP / 4 : VP / 2;             // words of one place
     // a stage: 16 keys of K and V as the lanes will read them (piece by piece, a lane's words side by
-    // side), then the keys' positions and, for E4M3, scales
-    static constexpr int KB = 2 * KW * 128, VB = 4 * VH * VWP * 128;
-    static constexpr int STAGE = KB + VB + 64 + (F8 ? 128 : 0);
-    static constexpr int OUT = kWarps * 16 * (HD + 4) * 4;       // the warps' results, over the stages
-    static constexpr int FIT = (112 * 1024 - 1024) / (kWarps * STAGE);
-    static constexpr int S = FIT < 8 ? FIT : 8;                 // two CTAs per SM
+    // side), then the keys' positions, whether all or none are read, and, for E4M3, scales
+    static constexpr int KB = 2 * KW * 128, VB = 4 * VH * VW * 128;
+    static constexpr int STAGE = KB + VB + 64 + 16 + (F8 ? 128 : 0);
+    static constexpr int OUT = kWarps * ROWS * (HD + 4) * 4;     // the warps' results, over the stages
+    static constexpr int CTAS = attn_rows_ctas(ROWS);
+    static constexpr int FIT = (227 * 1024 / CTAS - 2048) / (kWarps * STAGE);
+    static constexpr int S = FIT < 8 ? FIT : 8;
     static constexpr int RING = kWarps * S * STAGE;
-    static constexpr int BYTES = (RING > OUT ? RING : OUT) + 2 * kWarps * 16 * 4 + 16;
+    static constexpr int END = RING > OUT ? RING : OUT;
+    static constexpr int BYTES = END + 2 * kWarps * ROWS * 4 + 16;
+    static_assert(S >= 2, "a stage to read and one to fill");
 };
 
-template <int HD, int CT, int QT>
-__global__ void __launch_bounds__(kThr, 2) attn_rows_kernel(AttnPagedArgs a) {
-    using C = Cfg<HD, CT, QT>;
+template <int HD, int CT, int QT, int ROWS>
+__global__ void __launch_bounds__(kThr, attn_rows_ctas(ROWS)) attn_rows_kernel(AttnPagedArgs a) {
+    using C = Cfg<HD, CT, QT, ROWS>;
     constexpr bool F8 = C::F8, BF = C::BF;
+    constexpr int R = C::R;
     extern __shared__ __align__(16) uint8_t sm[];
-    float (*s_o)[16][HD + 4] = reinterpret_cast<float (*)[16][HD + 4]>(sm);
-    constexpr int kEnd = C::RING > C::OUT ? C::RING : C::OUT;
-    float (*s_m)[16] = reinterpret_cast<float (*)[16]>(sm + kEnd);
-    float (*s_l)[16] = s_m + kWarps;
-    int& s_flag = *reinterpret_cast<int*>(sm + kEnd + 2 * kWarps * 16 * 4);
+    float (*s_o)[ROWS][HD + 4] = reinterpret_cast<float (*)[ROWS][HD + 4]>(sm);
+    float (*s_m)[ROWS] = reinterpret_cast<float (*)[ROWS]>(sm + C::END);
+    float (*s_l)[ROWS] = s_m + kWarps;
+    int& s_flag = *reinterpret_cast<int*>(sm + C::END + 2 * kWarps * ROWS * 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     if (a.pdl) asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (form_missing(a)) return;
-    const int n_units = a.hdr[PH_UNITS1] * a.kv.Hkv;
+    if (form_missing(a) || (a.hdr[PH_FORM] & (ROWS == 8 ? ATTN_FORM_ROWS8 : ATTN_FORM_ROWS16)) == 0) return;
+    const int ui1 = a.first1[blockIdx.x + 1];
 
-    for (int ui = blockIdx.x; ui < n_units; ui += gridDim.x) {
-        const AttnUnit u = load_unit(a.units1 + ui / a.kv.Hkv);
-        const int kvh = ui % a.kv.Hkv;
+    for (int ui = a.first1[blockIdx.x]; ui < ui1; ++ui) {
+        const AttnUnit u = load_unit(a.units1 + ui);
+        const int kvh = u.head;
         const uint8_t* kbase = a.kv.k + (int64_t)kvh * a.kv.sb_head;
         const uint8_t* vbase = a.kv.v + (int64_t)kvh * a.kv.sb_head;
         const float* ksb = F8 ? a.kv.ks + (int64_t)kvh * a.kv.ss_head : nullptr;
         const float* vsb = F8 ? a.kv.vs + (int64_t)kvh * a.kv.ss_head : nullptr;
 
-        // rows g and g + 8 of the tile: position, first hidden position, Q fragments
-        int rp[2], rh[2];
-        float rs[2] = {a.scale_log2, a.scale_log2};
-        uint32_t qf[C::KS][4], ql[C::SPLIT_Q ? C::KS : 1][4];
-        int pmin = INT_MAX, pmax = INT_MIN;
+        // positions of the tile's rows: a row per lane, then what every lane needs of them
+        int rpos = INT_MIN, pmin = INT_MAX, pmax = INT_MIN, rtok = 0;
+        if (lane < u.n_row) {
+            rtok = row_token(a, u, u.row0 + lane);
+            rpos = row_pos(a, u, u.row0 + lane, rtok);
+            pmin = pmax = rpos;
+        }
+        pmin = __reduce_min_sync(0xffffffffu, pmin);
+        pmax = __reduce_max_sync(0xffffffffu, pmax);
+        const int hid_min = hidden_below(a, pmin), hid_max = hidden_below(a, pmax);
+
+        const int n_keys = u.v1 - u.v0;
+        // this warp's groups of 32 keys: 32 (warp + 4 i); two stages of 16 keys each
+        const int n_st = 2 * max(0, (n_keys - 32 * warp + 127) / 128);
+        auto lookup = [&](int i) {
+            Info f{-1, 0, INT_MAX};
+            const int v = 32 * (warp + kWarps * i) + lane;
+            if (v < n_keys) {
+                const KeyAt k = key_at(a, u, u.v0 + v);
+                // a key no row sees is not read: its cell may hold anything
+                if (k.off >= 0 && sees(k.pos, pmax, hid_min, a.n_sink)) {
+                    f.off = k.off;
+                    f.soff = k.soff;
+                    f.pos = k.pos;
+                }
+            }
+            return f;
+        };
+        uint8_t* const ring = sm + warp * C::S * C::STAGE;
+        Info fcur{-1, 0, INT_MAX}, fnext = lookup(0);
+        int in = 0, in_stage = 0;
+        // the copies of the next 16 keys; a group of copies is counted even where there are none
+        auto issue = [&]() {
+            if (in < n_st) {
+                if ((in & 1) == 0) {
+                    fcur = fnext;
+                    fnext = lookup((in >> 1) + 1);
+                }
+                const int l0 = 16 * (in & 1);
+                uint8_t* const st = ring + in_stage * C::STAGE;
+                const uint32_t ka = static_cast<uint32_t>(__cvta_generic_to_shared(st)), va = ka + C::KB;
+                const unsigned read = (__ballot_sync(0xffffffffu, fcur.off >= 0) >> l0) & 0xffffu;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int r = g + 8 * h;
-            rp[h] = INT_MIN;
-            rh[h] = INT_MIN;
+                for (int t = 0; t < 2; ++t) {
+                    const int64_t off = __shfl_sync(0xffffffffu, fcur.off, l0 + 8 * t + g);
+                    const uint8_t* src = kbase + (off >= 0 ? off : 0) + 4 * C::KC * c;
+#pragma unroll
+                    for (int i = 0; i < C::KP; ++i)
+                        fetch<C::KC>(ka + (t * C::KP + i) * 128 * C::KC + lane * 4 * C::KC, src + 16 * C::KC * i, off >= 0);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int64_t off = __shfl_sync(0xffffffffu, fcur.off, l0 + 2 * c + (e & 1) + 8 * (e >> 1));
+                    const uint8_t* src = vbase + (off >= 0 ? off : 0) + 4 * C::VW * g;
+#pragma unroll
+                    for (int i = 0; i < C::VH; ++i)
+                        fetch<C::VW>(va + (e * C::VH + i) * 128 * C::VW + lane * 4 * C::VW, src + 32 * C::VW * i, off >= 0);
+                }
+                if ((lane & 16) == l0) reinterpret_cast<int*>(st + C::KB + C::VB)[lane & 15] = fcur.pos;
+                if (lane == 0) *reinterpret_cast<int*>(st + C::KB + C::VB + 64) = read == 0xffffu ? 2 : read ? 1 : 0;
+                if constexpr (F8) {
+                    // lanes 0-15 the keys' scales, 16-31 the values'
+                    const int64_t so = __shfl_sync(0xffffffffu, fcur.off >= 0 ? fcur.soff : (int64_t)-1, l0 + (lane & 15));
+                    fetch<1>(va + C::VB + 80 + 4 * lane,
+                             reinterpret_cast<const uint8_t*>((lane < 16 ? ksb : vsb) + (so >= 0 ? so : 0)), so >= 0);
+                }
+                ++in;
+                if (++in_stage == C::S) in_stage = 0;
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+#pragma unroll
+        for (int s = 0; s < C::S - 1; ++s) issue();
+
+        // Q fragments: column g of column tile r is row 8 r + g; a lane's dims as its key words hold them
+        uint32_t qf[R][C::KS][2], ql[C::SPLIT_Q ? R : 1][C::KS][2];
+        float rsc[R];                                       // scale of row 8 r + g
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
             float x[C::KS][4];
 #pragma unroll
             for (int s = 0; s < C::KS; ++s)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[s][e] = 0.f;
-            if (r < u.n_row) {
-                const int row = u.row0 + r, tok = row_token(a, u, row);
-                rp[h] = row_pos(a, u, row, tok);
-                rh[h] = hidden_below(a, rp[h]);
-                pmin = min(pmin, rp[h]);
-                pmax = max(pmax, rp[h]);
+            const int tok = __shfl_sync(0xffffffffu, rtok, 8 * r + g);
+            if (8 * r + g < u.n_row) {
+                const int row = u.row0 + 8 * r + g;
                 const int64_t qo = (int64_t)tok * a.q_tok + (int64_t)(kvh * a.G + row % a.G) * a.q_head;
 #pragma unroll
                 for (int s = 0; s < C::KS; ++s) {
-                    // the four dims of k-step s this thread's key words hold
                     const int d = !F8 ? 32 * (s / 2) + 8 * c + 4 * (s % 2)
                                 : HD >= 64 ? 64 * (s / 4) + 16 * c + 4 * (s % 4) : 8 * c + 4 * s;
                     if constexpr (QT == W_F32) {
@@ -184,6 +259,7 @@ __global__ void __launch_bounds__(kThr, 2) attn_rows_kernel(AttnPagedArgs a) {
                     }
                 }
             }
+            rsc[r] = a.scale_log2;
             if constexpr (C::ROW_SCALE) {
                 // bring the row's largest value to [1, 2) (exactly; not finite or zero: as it is)
                 float mx = 0.f;
@@ -195,246 +271,229 @@ __global__ void __launch_bounds__(kThr, 2) attn_rows_kernel(AttnPagedArgs a) {
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                 const uint32_t ex = __float_as_uint(mx) >> 23;
                 if (ex > 0u && ex < 254u) {
-                    const float dn = __uint_as_float((254u - ex) << 23), up = __uint_as_float(ex << 23);
+                    const float dn = __uint_as_float((254u - ex) << 23);
 #pragma unroll
                     for (int s = 0; s < C::KS; ++s)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) x[s][e] *= dn;
-                    rs[h] *= up;
+                    rsc[r] *= __uint_as_float(ex << 23);
                 }
             }
 #pragma unroll
             for (int s = 0; s < C::KS; ++s) {
                 if constexpr (C::SPLIT_Q) {
-                    split2<BF>(x[s][0], x[s][1], qf[s][h], ql[s][h]);
-                    split2<BF>(x[s][2], x[s][3], qf[s][h + 2], ql[s][h + 2]);
+                    split2<BF>(x[s][0], x[s][1], qf[r][s][0], ql[r][s][0]);
+                    split2<BF>(x[s][2], x[s][3], qf[r][s][1], ql[r][s][1]);
                 } else {
-                    qf[s][h] = pack2<BF>(x[s][0], x[s][1]);
-                    qf[s][h + 2] = pack2<BF>(x[s][2], x[s][3]);
+                    qf[r][s][0] = pack2<BF>(x[s][0], x[s][1]);
+                    qf[r][s][1] = pack2<BF>(x[s][2], x[s][3]);
                 }
             }
         }
+        // the score fragment's columns are rows 8 r + 2 c + e: their positions and scales
+        int rp[R][2], rh[R][2];
+        float rs[R][2];
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) {
-            pmin = min(pmin, __shfl_xor_sync(0xffffffffu, pmin, o));
-            pmax = max(pmax, __shfl_xor_sync(0xffffffffu, pmax, o));
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                rp[r][e] = __shfl_sync(0xffffffffu, rpos, 8 * r + 2 * c + e);
+                rh[r][e] = hidden_below(a, rp[r][e]);
+                rs[r][e] = __shfl_sync(0xffffffffu, rsc[r], 4 * (2 * c + e));
+            }
+
+        float O[R][C::MT][4];
+        float m[R][2], l[R][2];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+#pragma unroll
+            for (int t = 0; t < C::MT; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) O[r][t][e] = 0.f;
+            m[r][0] = m[r][1] = -INFINITY;
+            l[r][0] = l[r][1] = 0.f;
         }
-        // a key no row sees is not read: its cell may hold anything
-        const int hid_all = hidden_below(a, pmin);
-
-        const int nb = (u.v1 - u.v0 + 15) / 16;
-        auto lookup = [&](int b) {
-            Info f{-1, 0, INT_MAX};
-            const int v = u.v0 + 16 * b + (lane & 15);
-            if (b < nb && v < u.v1) {
-                const KeyAt k = key_at(a, u, v);
-                if (k.off >= 0 && sees(k.pos, pmax, hid_all, a.n_sink)) {
-                    f.off = k.off;
-                    f.soff = k.soff;
-                    f.pos = k.pos;
-                }
-            }
-            return f;
-        };
-        uint8_t* const ring = sm + warp * C::S * C::STAGE;
-        // the copies of block b into stage s; a group of copies is counted even where there is no block
-        auto issue = [&](int b, int s, const Info& f) {
-            uint8_t* const st = ring + s * C::STAGE;
-            if (b < nb) {
-                const uint32_t ka = static_cast<uint32_t>(__cvta_generic_to_shared(st));
-                const uint32_t va = ka + C::KB;
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const int64_t off = __shfl_sync(0xffffffffu, f.off, 8 * t + g);
-                    const uint8_t* src = kbase + (off >= 0 ? off : 0) + 4 * C::KC * c;
-#pragma unroll
-                    for (int i = 0; i < C::KW / C::KC; ++i)
-                        fetch<C::KC>(ka + (t * C::KW / C::KC + i) * 128 * C::KC + lane * 4 * C::KC, src + 16 * C::KC * i,
-                                     off >= 0);
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int64_t off = __shfl_sync(0xffffffffu, f.off, 2 * c + (e & 1) + 8 * (e >> 1));
-                    const uint8_t* src = vbase + (off >= 0 ? off : 0) + 4 * C::VWP * g;
-#pragma unroll
-                    for (int i = 0; i < C::VH; ++i)
-                        fetch<C::VWP>(va + (e * C::VH + i) * 128 * C::VWP + lane * 4 * C::VWP, src + 32 * C::VWP * i, off >= 0);
-                }
-                const uint32_t ma = va + C::VB;
-                if (lane < 16) *reinterpret_cast<int*>(st + C::KB + C::VB + 4 * lane) = f.pos;
-                if constexpr (F8)
-                    fetch<1>(ma + 64 + 4 * lane,
-                             reinterpret_cast<const uint8_t*>((lane < 16 ? ksb : vsb) + (f.off >= 0 ? f.soff : 0)), f.off >= 0);
-            }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-        };
-
-        float O[C::NT][4];
-#pragma unroll
-        for (int n = 0; n < C::NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) O[n][e] = 0.f;
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
         float E = 0.f;                                      // O is in units of E (E4M3 values only)
 
-        Info nxt;
-        {
-            Info f[C::S - 1];
-#pragma unroll
-            for (int s = 0; s < C::S - 1; ++s) f[s] = lookup(warp + s * kWarps);
-#pragma unroll
-            for (int s = 0; s < C::S - 1; ++s) issue(warp + s * kWarps, s, f[s]);
-            nxt = lookup(warp + (C::S - 1) * kWarps);
-        }
-        int stage = 0, free_stage = C::S - 1;
-        for (int b = warp; b < nb; b += kWarps) {
+        int stage = 0;
+        for (int n = 0; n < n_st; ++n) {
             asm volatile("cp.async.wait_group %0;" ::"n"(C::S - 2) : "memory");
-            __syncwarp();
-            // the stage read in the last round takes the block S - 1 rounds ahead
-            issue(b + (C::S - 1) * kWarps, free_stage, nxt);
-            nxt = lookup(b + C::S * kWarps);
+            __syncwarp();                                   // every lane's part of the stage, and of the last is done with
+            issue();
             const uint8_t* const st = ring + stage * C::STAGE;
-            free_stage = stage;
             if (++stage == C::S) stage = 0;
-            float S[2][4] = {};
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                uint32_t kr[C::KW];
-#pragma unroll
-                for (int i = 0; i < C::KW / C::KC; ++i)
-                    take<C::KC>(&kr[C::KC * i], st + (t * C::KW / C::KC + i) * 128 * C::KC + lane * 4 * C::KC);
-#pragma unroll
-                for (int s = 0; s < C::KS; ++s) {
-                    uint32_t b0, b1;
-                    if constexpr (F8) {
-                        b0 = e4m3x2_to_h2(kr[s] & 0xffffu);
-                        b1 = e4m3x2_to_h2(kr[s] >> 16);
-                    } else {
-                        b0 = kr[2 * s];
-                        b1 = kr[2 * s + 1];
-                    }
-                    mma<BF>(S[t], qf[s], b0, b1);
-                    if constexpr (C::SPLIT_Q) mma<BF>(S[t], ql[s], b0, b1);
-                }
-            }
             const uint8_t* const meta = st + C::KB + C::VB;
-            // scores in the log2 domain, masked; the rows' maxima
-            float mx[2] = {-INFINITY, -INFINITY};
-            float kvs[2][2];
+            const int read = *reinterpret_cast<const int*>(meta + 64);
+            if (read == 0) continue;
+            float S[R][4];
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const int2 kp2 = *reinterpret_cast<const int2*>(meta + 4 * (8 * t + 2 * c));
-                float2 ks2 = make_float2(1.f, 1.f);
-                if constexpr (F8) {
-                    ks2 = *reinterpret_cast<const float2*>(meta + 64 + 4 * (8 * t + 2 * c));
-                    const float2 v2 = *reinterpret_cast<const float2*>(meta + 128 + 4 * (8 * t + 2 * c));
-                    kvs[t][0] = v2.x;
-                    kvs[t][1] = v2.y;
-                }
+            for (int r = 0; r < R; ++r) S[r][0] = S[r][1] = S[r][2] = S[r][3] = 0.f;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int kp = e ? kp2.y : kp2.x;
-                    const float ksc = e ? ks2.y : ks2.x;
+            for (int i = 0; i < C::KP; ++i) {
+                uint32_t k0[C::KC], k1[C::KC];              // keys g and g + 8
+                take<C::KC>(k0, st + i * 128 * C::KC + lane * 4 * C::KC);
+                take<C::KC>(k1, st + (C::KP + i) * 128 * C::KC + lane * 4 * C::KC);
+                constexpr int PER = F8 ? C::KC : C::KC / 2;  // k-steps of a piece
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float& s = S[t][2 * h + e];
-                        s = sees(kp, rp[h], rh[h], a.n_sink) ? s * (F8 ? rs[h] * ksc : rs[h]) : -INFINITY;
-                        mx[h] = fmaxf(mx[h], s);
+                for (int j = 0; j < PER; ++j) {
+                    uint32_t ka[4];
+                    if constexpr (F8) {
+                        ka[0] = e4m3x2_to_h2(k0[j] & 0xffffu);
+                        ka[1] = e4m3x2_to_h2(k1[j] & 0xffffu);
+                        ka[2] = e4m3x2_to_h2(k0[j] >> 16);
+                        ka[3] = e4m3x2_to_h2(k1[j] >> 16);
+                    } else {
+                        ka[0] = k0[2 * j]; ka[1] = k1[2 * j]; ka[2] = k0[2 * j + 1]; ka[3] = k1[2 * j + 1];
+                    }
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        mma<BF>(S[r], ka, qf[r][i * PER + j][0], qf[r][i * PER + j][1]);
+                        if constexpr (C::SPLIT_Q) mma<BF>(S[r], ka, ql[r][i * PER + j][0], ql[r][i * PER + j][1]);
                     }
                 }
             }
-            bool up = false;
-            float f[2] = {1.f, 1.f};
+            // scores in the log2 domain: S[r][2 h + e] is key g + 8 h, row 8 r + 2 c + e
+            const int* kpos = reinterpret_cast<const int*>(meta);
+            float ks[2] = {1.f, 1.f}, vs[2] = {1.f, 1.f};
+            if constexpr (F8) {
+                const float* sc = reinterpret_cast<const float*>(meta + 80);
+                ks[0] = sc[g]; ks[1] = sc[g + 8];
+                vs[0] = sc[16 + g]; vs[1] = sc[24 + g];
+            }
+            const int k_lo = kpos[0], k_hi = kpos[15];
+            // every row sees every key (positions ascend)
+            const bool open = read == 2 && k_hi <= pmin && (k_lo > hid_max || k_hi < a.n_sink);
+            bool raise = false;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
-                mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
-                if (mx[h] > m[h] + 14.f) {                  // true from nothing too
-                    f[h] = ex2(m[h] - (mx[h] - 6.f));       // 0 from nothing
-                    m[h] = mx[h] - 6.f;
-                    l[h] *= f[h];
-                    up = true;
-                }
+                const int kp = kpos[g + 8 * h];
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float& s = S[r][2 * h + e];
+                        s *= F8 ? rs[r][e] * ks[h] : rs[r][e];
+                        if (!open && !sees(kp, rp[r][e], rh[r][e], a.n_sink)) s = -INFINITY;
+                        raise = raise || s > m[r][e] + 14.f;
+                    }
             }
+            float em = 0.f;
             if constexpr (F8) {
-                // the values' scales relative to the largest seen
-                float e = fmaxf(fmaxf(kvs[0][0], kvs[0][1]), fmaxf(kvs[1][0], kvs[1][1]));
-                e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, 1));
-                e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, 2));
-                if (e > E) {
-                    f[0] *= E / e;
-                    f[1] *= E / e;
-                    E = e;
-                    up = true;
+                em = fmaxf(vs[0], vs[1]);
+                raise = raise || em > E;
+            }
+            if (__any_sync(0xffffffffu, raise)) {
+                float fe = 1.f;
+                if constexpr (F8) {
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) em = fmaxf(em, __shfl_xor_sync(0xffffffffu, em, o));
+                    if (em > E) {
+                        fe = E / em;
+                        E = em;
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    float f[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float mx = fmaxf(S[r][e], S[r][2 + e]);
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                        f[e] = 1.f;
+                        if (mx > m[r][e] + 14.f) {          // true from nothing too
+                            f[e] = ex2(m[r][e] - (mx - 6.f));   // 0 from nothing
+                            m[r][e] = mx - 6.f;
+                            l[r][e] *= f[e];
+                        }
+                        f[e] *= fe;
+                    }
+#pragma unroll
+                    for (int t = 0; t < C::MT; ++t) {
+                        O[r][t][0] *= f[0]; O[r][t][1] *= f[1];
+                        O[r][t][2] *= f[0]; O[r][t][3] *= f[1];
+                    }
                 }
             }
-            if (__any_sync(0xffffffffu, up)) {
+            // P^T fragments: pf[r][h] holds keys 8 h + 2 c, + 1 of row 8 r + g
+            uint32_t pf[R][2], pl[C::SPLIT_P ? R : 1][2];
+            const float inv = F8 && E > 0.f ? 1.f / E : 0.f;
 #pragma unroll
-                for (int n = 0; n < C::NT; ++n) {
-                    O[n][0] *= f[0]; O[n][1] *= f[0];
-                    O[n][2] *= f[1]; O[n][3] *= f[1];
-                }
-            }
-            uint32_t pf[4], pl[C::SPLIT_P ? 4 : 1];
-            const float inv = E > 0.f ? 1.f / E : 0.f;
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int r = 0; r < R; ++r)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    float p0 = m[h] == -INFINITY ? 0.f : ex2(S[t][2 * h] - m[h]);
-                    float p1 = m[h] == -INFINITY ? 0.f : ex2(S[t][2 * h + 1] - m[h]);
-                    l[h] += p0 + p1;
-                    if constexpr (F8) { p0 *= kvs[t][0] * inv; p1 *= kvs[t][1] * inv; }
-                    if constexpr (C::SPLIT_P) split2<BF>(p0, p1, pf[2 * t + h], pl[2 * t + h]);
-                    else pf[2 * t + h] = pack2<BF>(p0, p1);
+                    // (nothing seen yet: scores of -inf, or NaN, which has to show)
+                    float p0 = ex2(S[r][2 * h] - (m[r][0] == -INFINITY ? 0.f : m[r][0]));
+                    float p1 = ex2(S[r][2 * h + 1] - (m[r][1] == -INFINITY ? 0.f : m[r][1]));
+                    l[r][0] += p0;
+                    l[r][1] += p1;
+                    if constexpr (F8) { p0 *= vs[h] * inv; p1 *= vs[h] * inv; }
+                    if constexpr (C::SPLIT_P) {
+                        uint32_t hi, lo;
+                        split2<BF>(p0, p1, hi, lo);
+                        pf[r][h] = transpose8(hi);
+                        pl[r][h] = transpose8(lo);
+                    } else {
+                        pf[r][h] = transpose8(pack2<BF>(p0, p1));
+                    }
                 }
-            auto pv = [&](int n, uint32_t b0, uint32_t b1) {
-                mma<BF>(O[n], pf, b0, b1);
-                if constexpr (C::SPLIT_P) mma<BF>(O[n], pl, b0, b1);
+            auto pv = [&](int t, const uint32_t* va) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    mma<BF>(O[r][t], va, pf[r][0], pf[r][1]);
+                    if constexpr (C::SPLIT_P) mma<BF>(O[r][t], va, pl[r][0], pl[r][1]);
+                }
             };
+            // V^T fragments: rows g and g + 8 of a 16-dim tile are two neighbouring dims of the lane's
 #pragma unroll
             for (int p = 0; p < C::VH; ++p) {
-                uint32_t vr[4][C::VWP];
+                uint32_t vr[4][C::VW];                      // keys 2c, 2c + 1, 2c + 8, 2c + 9
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    take<C::VWP>(vr[e], st + C::KB + (e * C::VH + p) * 128 * C::VWP + lane * 4 * C::VWP);
+                    take<C::VW>(vr[e], st + C::KB + (e * C::VH + p) * 128 * C::VW + lane * 4 * C::VW);
 #pragma unroll
-                for (int w = 0; w < C::VWP; ++w) {
-                    const int i = p * C::VWP + w;
+                for (int w = 0; w < C::VW; ++w) {
                     const uint32_t w0 = vr[0][w], w1 = vr[1][w], w2 = vr[2][w], w3 = vr[3][w];
                     if constexpr (F8) {
                         const uint32_t x0 = __byte_perm(w0, w1, 0x5140), x1 = __byte_perm(w0, w1, 0x7362);
                         const uint32_t y0 = __byte_perm(w2, w3, 0x5140), y1 = __byte_perm(w2, w3, 0x7362);
-                        pv(4 * i, e4m3x2_to_h2(x0 & 0xffffu), e4m3x2_to_h2(y0 & 0xffffu));
-                        pv(4 * i + 1, e4m3x2_to_h2(x0 >> 16), e4m3x2_to_h2(y0 >> 16));
-                        pv(4 * i + 2, e4m3x2_to_h2(x1 & 0xffffu), e4m3x2_to_h2(y1 & 0xffffu));
-                        pv(4 * i + 3, e4m3x2_to_h2(x1 >> 16), e4m3x2_to_h2(y1 >> 16));
+                        const uint32_t a0[4] = {e4m3x2_to_h2(x0 & 0xffffu), e4m3x2_to_h2(x0 >> 16),
+                                                e4m3x2_to_h2(y0 & 0xffffu), e4m3x2_to_h2(y0 >> 16)};
+                        pv(2 * (p * C::VW + w), a0);
+                        const uint32_t a1[4] = {e4m3x2_to_h2(x1 & 0xffffu), e4m3x2_to_h2(x1 >> 16),
+                                                e4m3x2_to_h2(y1 & 0xffffu), e4m3x2_to_h2(y1 >> 16)};
+                        pv(2 * (p * C::VW + w) + 1, a1);
                     } else {
-                        pv(2 * i, __byte_perm(w0, w1, 0x5410), __byte_perm(w2, w3, 0x5410));
-                        pv(2 * i + 1, __byte_perm(w0, w1, 0x7632), __byte_perm(w2, w3, 0x7632));
+                        const uint32_t a0[4] = {__byte_perm(w0, w1, 0x5410), __byte_perm(w0, w1, 0x7632),
+                                                __byte_perm(w2, w3, 0x5410), __byte_perm(w2, w3, 0x7632)};
+                        pv(p * C::VW + w, a0);
                     }
                 }
             }
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();                                    // the results go where the stages were
-        // this warp's state to shared memory: row sums over the four threads of a row
+        // this warp's state to shared memory: row sums over the lanes that share a row
         bool finite = true;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-            if (c == 0) { s_m[warp][g + 8 * h] = m[h]; s_l[warp][g + 8 * h] = l[h]; }
-            finite = finite && l[h] <= 3.0e38f && m[h] <= 3.0e38f;
+        for (int r = 0; r < R; ++r)
 #pragma unroll
-            for (int n = 0; n < C::NT; ++n)
+            for (int e = 0; e < 2; ++e) {
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float o = F8 ? O[n][2 * h + e] * E : O[n][2 * h + e];
-                    finite = finite && fabsf(o) <= 3.0e38f;
-                    s_o[warp][g + 8 * h][(n / C::VP) * 8 * C::VP + C::VP * (2 * c + e) + n % C::VP] = o;
-                }
-        }
+                for (int o = 4; o < 32; o <<= 1) l[r][e] += __shfl_xor_sync(0xffffffffu, l[r][e], o);
+                const int row = 8 * r + 2 * c + e;
+                if (g == 0) { s_m[warp][row] = m[r][e]; s_l[warp][row] = l[r][e]; }
+                finite = finite && l[r][e] <= 3.0e38f && m[r][e] <= 3.0e38f;
+#pragma unroll
+                for (int t = 0; t < C::MT; ++t)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float o = F8 ? O[r][t][2 * h + e] * E : O[r][t][2 * h + e];
+                        finite = finite && fabsf(o) <= 3.0e38f;
+                        const int i = 2 * t + h;            // the lane's i-th dim
+                        s_o[warp][row][(i / C::VP) * 8 * C::VP + C::VP * g + i % C::VP] = o;
+                    }
+            }
         const bool redo = __syncthreads_or(!finite);
         if (redo) {
             // not every operand was finite: the rows again, key by key; warp 0's state takes the result
@@ -472,24 +531,24 @@ __global__ void __launch_bounds__(kThr, 2) attn_rows_kernel(AttnPagedArgs a) {
                 const int row = u.row0 + r, tok = row_token(a, u, row);
                 store_out4(a, (int64_t)tok * a.o_tok + (int64_t)(kvh * a.G + row % a.G) * a.o_head + d, v);
             } else {
-                const int64_t at = ((int64_t)(u.part + u.chunk) * a.kv.Hkv + kvh) * kUnitRows1 + r;
+                const int64_t at = (int64_t)(u.part + u.chunk) * ROWS + r;
                 *reinterpret_cast<float4*>(a.part_o + at * HD + d) = make_float4(v[0], v[1], v[2], v[3]);
                 if (d == 0) a.part_ml[at] = make_float2(M, L);
             }
         }
-        if (u.n_chunk > 1 && last_of_tile(a, u, kvh, &s_flag)) merge_parts<HD>(a, u, kvh, kUnitRows1);
+        if (u.n_chunk > 1 && last_of_tile(a, u, &s_flag)) merge_parts<HD>(a, u, ROWS);
         __syncthreads();                                    // shared memory is free for the next unit
     }
 }
 
-template <int HD, int CT, int QT>
+template <int HD, int CT, int QT, int ROWS>
 bool go(const AttnPagedArgs& a, cudaStream_t st) {
-    using C = Cfg<HD, CT, QT>;
-    if (cudaFuncSetAttribute(attn_rows_kernel<HD, CT, QT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES) !=
+    using C = Cfg<HD, CT, QT, ROWS>;
+    if (cudaFuncSetAttribute(attn_rows_kernel<HD, CT, QT, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES) !=
         cudaSuccess)
         return false;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * a.n_sm);                         // two CTAs per SM, each walking its units
+    cfg.gridDim = dim3(C::CTAS * a.n_sm);                   // the plan's CTAs
     cfg.blockDim = dim3(kThr);
     cfg.dynamicSmemBytes = C::BYTES;
     cfg.stream = st;
@@ -498,14 +557,24 @@ bool go(const AttnPagedArgs& a, cudaStream_t st) {
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = a.pdl ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, attn_rows_kernel<HD, CT, QT>, a) == cudaSuccess;
+    return cudaLaunchKernelEx(&cfg, attn_rows_kernel<HD, CT, QT, ROWS>, a) == cudaSuccess;
 }
-template <int HD>
-bool go_hd(const AttnPagedArgs& a, cudaStream_t st) {
-    if (a.kv.type == W_F16) return a.q_type == W_F16 ? go<HD, W_F16, W_F16>(a, st) : go<HD, W_F16, W_F32>(a, st);
-    if (a.kv.type == W_BF16) return go<HD, W_BF16, W_BF16>(a, st);
-    if (a.q_type == W_F16) return go<HD, W_F8, W_F16>(a, st);
-    return a.q_type == W_BF16 ? go<HD, W_F8, W_BF16>(a, st) : go<HD, W_F8, W_F32>(a, st);
+template <int HD, int ROWS>
+bool go_types(const AttnPagedArgs& a, cudaStream_t st) {
+    if (a.kv.type == W_F16)
+        return a.q_type == W_F16 ? go<HD, W_F16, W_F16, ROWS>(a, st) : go<HD, W_F16, W_F32, ROWS>(a, st);
+    if (a.kv.type == W_BF16) return go<HD, W_BF16, W_BF16, ROWS>(a, st);
+    if (a.q_type == W_F16) return go<HD, W_F8, W_F16, ROWS>(a, st);
+    return a.q_type == W_BF16 ? go<HD, W_F8, W_BF16, ROWS>(a, st) : go<HD, W_F8, W_F32, ROWS>(a, st);
+}
+template <int ROWS>
+bool go_rows(const AttnPagedArgs& a, cudaStream_t st) {
+    switch (a.kv.hd) {
+        case 32: return go_types<32, ROWS>(a, st);
+        case 64: return go_types<64, ROWS>(a, st);
+        case 128: return go_types<128, ROWS>(a, st);
+    }
+    return false;
 }
 
 }  // namespace
@@ -518,16 +587,9 @@ bool attn_paged_types_ok(int32_t q, int32_t kv) {
 
 bool launch_attn_paged(const AttnPagedArgs& a, cudaStream_t st) {
     if (!attn_paged_types_ok(a.q_type, a.kv.type)) return false;
-    if (a.form & ATTN_FORM_TC) {
-        if (!launch_attn_paged_tc(a, st)) return false;
-    }
-    if (!(a.form & ATTN_FORM_ROWS)) return true;
-    switch (a.kv.hd) {
-        case 32: return go_hd<32>(a, st);
-        case 64: return go_hd<64>(a, st);
-        case 128: return go_hd<128>(a, st);
-    }
-    return false;
+    if ((a.form & ATTN_FORM_TC) && !launch_attn_paged_tc(a, st)) return false;
+    if ((a.form & ATTN_FORM_ROWS8) && !go_rows<8>(a, st)) return false;
+    return (a.form & ATTN_FORM_ROWS16) == 0 || go_rows<16>(a, st);
 }
 
 }  // namespace llm

@@ -169,15 +169,15 @@ __device__ __noinline__ void careful_row(const AttnPagedArgs& a, const AttnUnit&
 // The last unit of a tile to finish merges the partial results of all of them (in their order, so
 // the result does not depend on which unit was last). rows: the tile form's rows.
 template <int HD>
-__device__ void merge_parts(const AttnPagedArgs& a, const AttnUnit& u, int kvh, int rows) {
+__device__ void merge_parts(const AttnPagedArgs& a, const AttnUnit& u, int rows) {
     constexpr int Q = HD / 4;                                  // four dims per thread
     for (int x = threadIdx.x; x < u.n_row * Q; x += blockDim.x) {
         const int r = x / Q, d = (x % Q) * 4;
         float M = -INFINITY, L = 0.f, O[4] = {};
         for (int c = 0; c < u.n_chunk; ++c)
-            M = fmaxf(M, __ldcg(&a.part_ml[((int64_t)(u.part + c) * a.kv.Hkv + kvh) * rows + r]).x);
+            M = fmaxf(M, __ldcg(&a.part_ml[(int64_t)(u.part + c) * rows + r]).x);
         for (int c = 0; c < u.n_chunk; ++c) {
-            const int64_t at = ((int64_t)(u.part + c) * a.kv.Hkv + kvh) * rows + r;
+            const int64_t at = (int64_t)(u.part + c) * rows + r;
             const float2 ml = __ldcg(&a.part_ml[at]);
             // a chunk without a visible key has nothing to add (its maximum is -inf); NaN sums pass
             if (ml.x == -INFINITY && ml.y == 0.f) continue;
@@ -190,16 +190,16 @@ __device__ void merge_parts(const AttnPagedArgs& a, const AttnUnit& u, int kvh, 
 #pragma unroll
         for (int j = 0; j < 4; ++j) O[j] = L == 0.f ? 0.f : O[j] * inv;
         const int row = u.row0 + r, tok = row_token(a, u, row);
-        store_out4(a, (int64_t)tok * a.o_tok + (int64_t)(kvh * a.G + row % a.G) * a.o_head + d, O);
+        store_out4(a, (int64_t)tok * a.o_tok + (int64_t)(u.head * a.G + row % a.G) * a.o_head + d, O);
     }
 }
 
 // Count this unit as finished (its partial results are written); true in every thread of the last one.
-__device__ __forceinline__ bool last_of_tile(const AttnPagedArgs& a, const AttnUnit& u, int kvh, int* flag) {
+__device__ __forceinline__ bool last_of_tile(const AttnPagedArgs& a, const AttnUnit& u, int* flag) {
     __threadfence();
     __syncthreads();
     if (threadIdx.x == 0) {
-        int* t = a.tickets + (int64_t)u.tile * a.kv.Hkv + kvh;
+        int* t = a.tickets + u.ticket;
         const bool last = atomicAdd(t, 1) + 1 == u.n_chunk;
         if (last) *t = 0;
         *flag = last;

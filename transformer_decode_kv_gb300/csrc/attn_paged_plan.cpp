@@ -1,5 +1,5 @@
 // Host plan of the attention over a paged cache: tiles of (token, query head) rows per sequence, the
-// keys each tile may see, and the split of long key ranges into units so that every SM gets a share.
+// keys each tile may see, and an even share of all of that for every CTA that runs at once.
 #include "paged.h"
 
 #include <algorithm>
@@ -8,15 +8,16 @@ namespace llm {
 
 namespace {
 
-// CTAs of each form that run at once (attn_paged.cu: two per SM; attn_paged_tc.cu: one).
-int64_t slots(const PlanShape& s, bool tc) { return (int64_t)s.n_sm * (tc ? 1 : 2); }
-// Shortest key range worth a unit of its own: a unit of the 16-row form gives each of its four warps one
-// block of 16 keys, one of the 256-row form one step of 128 keys.
-constexpr int64_t kMinKeys1 = 64, kMinKeys2 = 128;
+// Keys are dealt out in blocks of 128: a 16-row form's CTA has four warps of 32 keys each, the 256-row form
+// multiplies 128 keys at a time.
+constexpr int64_t kBlockKeys = 128;
+// What a unit costs beyond its keys, in blocks: Q in, the warps' (halves') results out and merged.
+// 16-row forms: about 2 us against 3 us a block and CTA; 256-row form: about 3 us against 1 us a block.
+constexpr int64_t kUnitCost[2] = {1, 3};
 // Sequences with at least this many rows per KV head take 256-row tiles.
 constexpr int64_t kTcRows = 64;
 
-int64_t up_to(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+int64_t ctas(const PlanShape& s, int f, int rows) { return (int64_t)s.n_sm * (f ? 1 : attn_rows_ctas(rows)); }
 
 // The virtual key range of the rows [row0, row0 + n) of a sequence: sink keys, then [lo, hi).
 struct Keys { int32_t n_sink, lo, n; };
@@ -54,70 +55,99 @@ Keys tile_keys(const PlanShape& s, const PlanSeq& q, int64_t row0, int64_t n) {
 
 void build_paged_plan(const PlanShape& s, const std::vector<PlanSeq>& seqs, PagedPlan& plan) {
     plan = PagedPlan();
+    auto tc = [&](const PlanSeq& q) { return s.tc && (int64_t)q.n_new * s.G >= kTcRows; };
+    // rows of the small tiles: 8 where every sequence that takes them fits (half the products of 16)
+    plan.rows1 = 8;
+    for (const PlanSeq& q : seqs)
+        if (!tc(q) && (int64_t)q.n_new * s.G > 8) plan.rows1 = 16;
     struct Tile { int32_t seq, row0, n_row; Keys keys; };
     std::vector<Tile> tiles[2];
     int64_t total[2] = {0, 0};
     for (size_t i = 0; i < seqs.size(); ++i) {
         const int64_t rows = (int64_t)seqs[i].n_new * s.G;
-        const int f = s.tc && rows >= kTcRows ? 1 : 0;
-        const int64_t step = f ? kUnitRows2 : kUnitRows1;
+        const int f = tc(seqs[i]);
+        const int64_t step = f ? kUnitRows2 : plan.rows1;
         for (int64_t r = 0; r < rows; r += step) {
             Tile t{(int32_t)i, (int32_t)r, (int32_t)std::min(step, rows - r), {}};
             t.keys = tile_keys(s, seqs[i], t.row0, t.n_row);
-            total[f] += t.keys.n;
+            total[f] += (t.keys.n + kBlockKeys - 1) / kBlockKeys + kUnitCost[f];
             tiles[f].push_back(t);
         }
     }
     for (int f = 0; f < 2; ++f) {
-        std::vector<AttnUnit>& units = f ? plan.units2 : plan.units1;
-        int32_t& parts = f ? plan.n_parts2 : plan.n_parts1;
-        // an even share of all keys per running CTA is the longest unit
-        const int64_t min_keys = f ? kMinKeys2 : kMinKeys1;
-        const int64_t share = (total[f] * s.Hkv + slots(s, f) - 1) / slots(s, f);
-        const int64_t chunk = std::max(min_keys, up_to(share, min_keys));
-        for (const Tile& t : tiles[f]) {
-            const PlanSeq& q = seqs[t.seq];
-            AttnUnit u{};
-            u.tok0 = q.tok0;
-            u.row0 = t.row0;
-            u.n_row = t.n_row;
-            u.p0 = q.p0;
-            u.table = q.table;
-            u.n_sink_keys = t.keys.n_sink;
-            u.key_lo = t.keys.lo;
-            u.tile = plan.n_tiles++;
-            u.n_chunk = (int32_t)std::max<int64_t>(1, (t.keys.n + chunk - 1) / chunk);
-            u.part = u.n_chunk > 1 ? parts : 0;
-            if (u.n_chunk > 1) parts += u.n_chunk;
-            // equal pieces in whole blocks
-            const int64_t piece = up_to((t.keys.n + u.n_chunk - 1) / u.n_chunk, f ? 128 : 16);
-            for (int32_t i = 0; i < u.n_chunk; ++i) {
-                u.chunk = i;
-                u.v0 = (int32_t)std::min<int64_t>(t.keys.n, i * piece);
-                u.v1 = (int32_t)std::min<int64_t>(t.keys.n, (i + 1) * piece);
-                units.push_back(u);
-            }
+        PlanForm& pf = plan.form_[f];
+        if (tiles[f].empty()) continue;
+        const int64_t n_cta = ctas(s, f, plan.rows1), cost = kUnitCost[f];
+        // a CTA's share: what is there divided evenly, and one more unit for the cut at its end
+        const int64_t share = (total[f] * s.Hkv + n_cta - 1) / n_cta + cost;
+        int64_t left = share;                           // of the current CTA's share
+        pf.first.assign(1, 0);
+        auto next_cta = [&]() { pf.first.push_back((int32_t)pf.units.size()); left = share; };
+        size_t i0 = 0;
+        while (i0 < tiles[f].size()) {
+            // the tiles of a sequence head by head, so that neighbouring CTAs read the same keys
+            size_t i1 = i0;
+            while (i1 < tiles[f].size() && tiles[f][i1].seq == tiles[f][i0].seq) ++i1;
+            for (int32_t h = 0; h < s.Hkv; ++h)
+                for (size_t i = i0; i < i1; ++i) {
+                    const Tile& t = tiles[f][i];
+                    const PlanSeq& q = seqs[t.seq];
+                    const int64_t blocks = (t.keys.n + kBlockKeys - 1) / kBlockKeys;
+                    const size_t u0 = pf.units.size();
+                    int64_t at = 0;
+                    do {
+                        const bool last_cta = (int64_t)pf.first.size() >= n_cta;
+                        if (left <= cost && !last_cta) next_cta();
+                        int64_t take = blocks - at;
+                        // past the share: cut (a remainder shorter than a unit's cost is not left over)
+                        if ((int64_t)pf.first.size() < n_cta && take > left) take = left - cost;
+                        AttnUnit u{};
+                        u.tok0 = q.tok0;
+                        u.row0 = t.row0;
+                        u.n_row = t.n_row;
+                        u.p0 = q.p0;
+                        u.table = q.table;
+                        u.n_sink_keys = t.keys.n_sink;
+                        u.key_lo = t.keys.lo;
+                        u.v0 = (int32_t)(at * kBlockKeys);
+                        u.v1 = (int32_t)std::min<int64_t>(t.keys.n, (at + take) * kBlockKeys);
+                        u.chunk = (int32_t)(pf.units.size() - u0);
+                        u.head = h;
+                        pf.units.push_back(u);
+                        at += take;
+                        left -= take + cost;
+                    } while (at < blocks);
+                    const int32_t n = (int32_t)(pf.units.size() - u0);
+                    for (size_t j = u0; j < pf.units.size(); ++j) {
+                        pf.units[j].n_chunk = n;
+                        pf.units[j].part = n > 1 ? pf.n_parts : 0;
+                        pf.units[j].ticket = n > 1 ? plan.n_tickets : 0;
+                    }
+                    if (n > 1) {
+                        pf.n_parts += n;
+                        ++plan.n_tickets;
+                    }
+                }
+            i0 = i1;
         }
-        // longest first, so that the CTAs' last units are short ones
-        std::stable_sort(units.begin(), units.end(),
-                         [](const AttnUnit& a, const AttnUnit& b) { return a.v1 - a.v0 > b.v1 - b.v0; });
+        while ((int64_t)pf.first.size() <= n_cta) pf.first.push_back((int32_t)pf.units.size());
     }
 }
 
 PagedPlanCaps paged_plan_caps(const PlanShape& s, int32_t max_tok, int32_t max_seq) {
-    // A tile is cut into ceil(n / chunk) units with chunk >= total * Hkv / slots: the cuts of all tiles
-    // add at most slots / Hkv units to one per tile, and the units of the tiles that are cut are at most
-    // twice that (such a tile is longer than a chunk).
+    // Every (tile, head) is one unit, plus one for each cut, and a CTA's share ends in one cut at most. So a
+    // CTA has at most two partial units (its first and its last), and fewer tiles than CTAs are cut.
     PagedPlanCaps c{};
     const int64_t rows = (int64_t)max_tok * s.G;
-    const int64_t t1 = rows / kUnitRows1 + std::min<int64_t>(max_seq, max_tok);
+    const int64_t t1 = rows / 8 + std::min<int64_t>(max_seq, max_tok);
     const int64_t t2 = s.tc ? rows / kUnitRows2 + std::min<int64_t>(max_seq, rows / kTcRows) : 0;
-    const int64_t x1 = slots(s, false) / s.Hkv + 1, x2 = s.tc ? slots(s, true) / s.Hkv + 1 : 0;
-    c.units1 = t1 + x1;
-    c.units2 = t2 + x2;
-    c.tiles = t1 + t2;
-    c.parts1 = 2 * x1;
-    c.parts2 = 2 * x2;
+    c.ctas1 = std::max(ctas(s, 0, 8), ctas(s, 0, 16));
+    c.ctas2 = s.tc ? ctas(s, 1, 0) : 0;
+    c.units1 = t1 * s.Hkv + c.ctas1;
+    c.units2 = t2 * s.Hkv + c.ctas2;
+    c.tickets = c.ctas1 + c.ctas2;
+    c.parts1 = 2 * c.ctas1;
+    c.parts2 = 2 * c.ctas2;
     return c;
 }
 

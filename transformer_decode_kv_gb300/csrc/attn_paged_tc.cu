@@ -208,8 +208,8 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a) 
         if (tid == 0 && a.err) atomicOr(a.err, ERR_TIMEOUT);
         return;
     }
-    const int n_units = a.hdr[PH_UNITS2] * a.kv.Hkv;
-    if ((int)blockIdx.x >= n_units) return;
+    const int ui0 = a.first2[blockIdx.x], ui1 = a.first2[blockIdx.x + 1];
+    if ((a.hdr[PH_FORM] & ATTN_FORM_TC) == 0 || ui0 >= ui1) return;
 
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) { bar_init(&kv_full[i], kProdWarps); bar_init(&kv_empty[i], 1); }
@@ -248,9 +248,9 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a) 
     uint32_t q_ph = 0, o_ph = 0, sp_ph[2] = {0u, 0u};
     int produced = 0;                                       // ring places filled (up to all of them)
 
-    for (int ui = blockIdx.x; ui < n_units; ui += gridDim.x) {
-        const AttnUnit u = load_unit(a.units2 + ui / a.kv.Hkv);
-        const int kvh = ui % a.kv.Hkv;
+    for (int ui = ui0; ui < ui1; ++ui) {
+        const AttnUnit u = load_unit(a.units2 + ui);
+        const int kvh = u.head;
         const int nt = (u.v1 - u.v0 + kKeys - 1) / kKeys;
         const int halves = u.n_row > 128 ? 2 : 1;
 
@@ -622,7 +622,7 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a) 
             if (live) {
                 bool finite = l <= 3.0e38f && m <= 3.0e38f;
                 const float inv = l == 0.f ? 0.f : 1.f / l, sv = F8 && nt > 0 ? s0[1] : 1.f;
-                const int64_t at = ((int64_t)(u.part + u.chunk) * a.kv.Hkv + kvh) * kUnitRows2 + 128 * t + r;
+                const int64_t at = (int64_t)(u.part + u.chunk) * kUnitRows2 + 128 * t + r;
                 const int64_t oi = (int64_t)tok * a.o_tok + (int64_t)(kvh * a.G + row % a.G) * a.o_head;
                 if (u.n_chunk > 1 && mine) a.part_ml[at] = make_float2(m, l);
 #pragma unroll 1
@@ -660,7 +660,7 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a) 
                 float o[HD / 32], rm, rl;
                 const int row = u.row0 + r, tok = row_token(a, u, row);
                 careful_row<HD>(a, u, kvh, row, o, rm, rl);
-                const int64_t at = ((int64_t)(u.part + u.chunk) * a.kv.Hkv + kvh) * kUnitRows2 + r;
+                const int64_t at = (int64_t)(u.part + u.chunk) * kUnitRows2 + r;
                 const int64_t oi = (int64_t)tok * a.o_tok + (int64_t)(kvh * a.G + row % a.G) * a.o_head;
                 const float inv = rl == 0.f ? 0.f : 1.f / rl;
 #pragma unroll
@@ -673,7 +673,7 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a) 
             __syncthreads();
             if (tid == 0) *redo_f = 0;
         }
-        if (u.n_chunk > 1 && last_of_tile(a, u, kvh, flag)) merge_parts<HD>(a, u, kvh, kUnitRows2);
+        if (u.n_chunk > 1 && last_of_tile(a, u, flag)) merge_parts<HD>(a, u, kUnitRows2);
         __syncthreads();
     }
     __syncthreads();

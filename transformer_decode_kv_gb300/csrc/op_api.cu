@@ -243,8 +243,8 @@ struct llm_attn_plan {
     int device = 0;
     float scale_log2 = 0.f;
     PagedPlan plan;
-    // device buffer: header, units of both forms, page table; the pinned copy it is uploaded from
-    size_t off_units1 = 0, off_units2 = 0, off_table = 0, bytes = 0;
+    // device buffer: header, both forms' CTA starts, their units, page table; the pinned copy it is uploaded from
+    size_t off_first[2] = {0, 0}, off_units[2] = {0, 0}, off_table = 0, bytes = 0;
     uint8_t *d_buf = nullptr, *h_buf = nullptr;
     float* part_o = nullptr;
     float2* part_ml = nullptr;
@@ -291,12 +291,13 @@ llm_attn_plan* llm_attn_plan_init(const llm_attn_shape* s, const llm_kv_pages* k
     p->ps = plan_shape(s, kv, n_sm, attn_paged_tc_ok(kv->head_dim, kv->type, s->type));
     p->caps = paged_plan_caps(p->ps, s->max_tok, s->max_seq);
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-    p->off_units1 = up(PH_WORDS * sizeof(int32_t));
-    p->off_units2 = p->off_units1 + up(p->caps.units1 * sizeof(AttnUnit));
-    p->off_table = p->off_units2 + up(p->caps.units2 * sizeof(AttnUnit));
+    p->off_first[0] = up(PH_WORDS * sizeof(int32_t));
+    p->off_first[1] = p->off_first[0] + up((p->caps.ctas1 + 1) * sizeof(int32_t));
+    p->off_units[0] = p->off_first[1] + up((p->caps.ctas2 + 1) * sizeof(int32_t));
+    p->off_units[1] = p->off_units[0] + up(p->caps.units1 * sizeof(AttnUnit));
+    p->off_table = p->off_units[1] + up(p->caps.units2 * sizeof(AttnUnit));
     p->bytes = p->off_table + up((size_t)s->max_table * sizeof(int32_t));
-    const int64_t H = kv->n_head_kv;
-    const int64_t rows = H * std::max(p->caps.parts1 * kUnitRows1, p->caps.parts2 * kUnitRows2);
+    const int64_t rows = plan_part_rows(p->caps);
     // the two forms run one after the other on a stream: they share the partial results' memory
     auto get = [&](auto** q, size_t n) {
         void* v = nullptr;
@@ -306,16 +307,16 @@ llm_attn_plan* llm_attn_plan_init(const llm_attn_shape* s, const llm_kv_pages* k
     get(&p->d_buf, p->bytes);
     get(&p->part_o, (size_t)rows * kv->head_dim * sizeof(float));
     get(&p->part_ml, (size_t)rows * sizeof(float2));
-    get(&p->tickets, (size_t)(p->caps.tiles * H) * sizeof(int32_t));
+    get(&p->tickets, (size_t)p->caps.tickets * sizeof(int32_t));
     get(&p->err, sizeof(uint32_t));
     if (e == cudaSuccess) {
         void* h = nullptr;
         e = cudaMallocHost(&h, p->bytes);
         p->h_buf = static_cast<uint8_t*>(h);
     }
-    if (e == cudaSuccess) e = cudaMemset(p->tickets, 0, (size_t)(p->caps.tiles * H) * sizeof(int32_t));
+    if (e == cudaSuccess) e = cudaMemset(p->tickets, 0, (size_t)p->caps.tickets * sizeof(int32_t));
     if (e == cudaSuccess) e = cudaMemset(p->err, 0, sizeof(uint32_t));
-    if (e == cudaSuccess) e = cudaMemset(p->d_buf, 0, p->off_units1);
+    if (e == cudaSuccess) e = cudaMemset(p->d_buf, 0, p->off_units[0]);
     if (e == cudaSuccess) e = cudaEventCreateWithFlags(&p->uploaded, cudaEventDisableTiming);
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return die("llm_attn_plan_init", e);
@@ -368,19 +369,24 @@ int llm_attn_plan_set(llm_attn_plan* p, int32_t n_seq, const int32_t* n_new, con
     } catch (const std::exception&) {
         return refuse("out of memory");
     }
-    if ((int64_t)plan.units1.size() > p->caps.units1 || (int64_t)plan.units2.size() > p->caps.units2 ||
-        plan.n_parts1 > p->caps.parts1 || plan.n_parts2 > p->caps.parts2 || plan.n_tiles > p->caps.tiles)
-        return refuse("plan exceeds its buffers");
+    const int64_t max_units[2] = {p->caps.units1, p->caps.units2}, max_cta[2] = {p->caps.ctas1, p->caps.ctas2},
+                  max_parts[2] = {p->caps.parts1, p->caps.parts2};
+    for (int f = 0; f < 2; ++f)
+        if ((int64_t)plan.form_[f].units.size() > max_units[f] || (int64_t)plan.form_[f].first.size() > max_cta[f] + 1 ||
+            plan.form_[f].n_parts > max_parts[f] || plan.n_tickets > p->caps.tickets)
+            return refuse("plan exceeds its buffers");
     // the previous upload has read the pinned buffer
     if (p->pending && (e = cudaEventSynchronize(p->uploaded)) != cudaSuccess) return failed("upload", e);
     p->pending = false;
     int32_t* hdr = reinterpret_cast<int32_t*>(p->h_buf);
     std::memset(hdr, 0, PH_WORDS * sizeof(int32_t));
-    hdr[PH_UNITS1] = (int32_t)plan.units1.size();
-    hdr[PH_UNITS2] = (int32_t)plan.units2.size();
     hdr[PH_FORM] = plan.form();
-    if (!plan.units1.empty()) std::memcpy(p->h_buf + p->off_units1, plan.units1.data(), plan.units1.size() * sizeof(AttnUnit));
-    if (!plan.units2.empty()) std::memcpy(p->h_buf + p->off_units2, plan.units2.data(), plan.units2.size() * sizeof(AttnUnit));
+    for (int f = 0; f < 2; ++f) {
+        const PlanForm& pf = plan.form_[f];
+        if (pf.units.empty()) continue;
+        std::memcpy(p->h_buf + p->off_first[f], pf.first.data(), pf.first.size() * sizeof(int32_t));
+        std::memcpy(p->h_buf + p->off_units[f], pf.units.data(), pf.units.size() * sizeof(AttnUnit));
+    }
     int32_t* table = reinterpret_cast<int32_t*>(p->h_buf + p->off_table);
     for (int32_t i = 0; i < n_seq; ++i) {
         const int64_t need = pages_of(p->kv, n_kv[i]);
@@ -391,8 +397,8 @@ int llm_attn_plan_set(llm_attn_plan* p, int32_t n_seq, const int32_t* n_new, con
         if (e == cudaSuccess && n)
             e = cudaMemcpyAsync(p->d_buf + off, p->h_buf + off, n, cudaMemcpyHostToDevice, st);
     };
-    copy(0, p->off_units1 + plan.units1.size() * sizeof(AttnUnit));
-    copy(p->off_units2, plan.units2.size() * sizeof(AttnUnit));
+    copy(0, p->off_units[0] + plan.form_[0].units.size() * sizeof(AttnUnit));
+    copy(p->off_units[1], plan.form_[1].units.size() * sizeof(AttnUnit));
     copy(p->off_table, (size_t)tab * sizeof(int32_t));
     if (e == cudaSuccess) e = cudaEventRecord(p->uploaded, st);
     if (e != cudaSuccess) { cudaGetLastError(); return failed("plan upload", e); }
@@ -435,8 +441,10 @@ int llm_attn_run(llm_attn_plan* p, const void* q, int64_t q_stride_tok, int64_t 
     a.window = p->shape.window;
     a.n_sink = p->shape.n_sink;
     a.hdr = reinterpret_cast<const int32_t*>(p->d_buf);
-    a.units1 = reinterpret_cast<const AttnUnit*>(p->d_buf + p->off_units1);
-    a.units2 = reinterpret_cast<const AttnUnit*>(p->d_buf + p->off_units2);
+    a.first1 = reinterpret_cast<const int32_t*>(p->d_buf + p->off_first[0]);
+    a.first2 = reinterpret_cast<const int32_t*>(p->d_buf + p->off_first[1]);
+    a.units1 = reinterpret_cast<const AttnUnit*>(p->d_buf + p->off_units[0]);
+    a.units2 = reinterpret_cast<const AttnUnit*>(p->d_buf + p->off_units[1]);
     a.table = reinterpret_cast<const int32_t*>(p->d_buf + p->off_table);
     a.part_o = p->part_o; a.part_ml = p->part_ml; a.tickets = p->tickets; a.err = p->err;
     a.form = p->plan.form();
@@ -461,7 +469,7 @@ uint32_t llm_attn_plan_error(llm_attn_plan* p) {
 
 int64_t llm_debug_attn_units(const llm_attn_shape* s, const llm_kv_pages* kv, int32_t n_sm, int32_t tc, int32_t n_seq,
                              const int32_t* n_new, const int32_t* n_kv, int32_t* out, int64_t cap,
-                             int64_t* n_rows_units, int64_t caps[5]) {
+                             int64_t* n_rows_units, int32_t* first, int64_t caps[7]) {
     if (const char* w = attn_shape_fault(s, kv)) return refuse(w);
     if (n_sm < 1) return refuse("n_sm < 1");
     if (const char* w = step_fault(s, *kv, n_seq, n_new, n_kv)) return refuse(w);
@@ -472,13 +480,20 @@ int64_t llm_debug_attn_units(const llm_attn_shape* s, const llm_kv_pages* kv, in
     } catch (const std::exception&) {
         return refuse("out of memory");
     }
-    const int64_t n1 = (int64_t)plan.units1.size(), n2 = (int64_t)plan.units2.size();
+    const std::vector<AttnUnit>&u1 = plan.form_[0].units, &u2 = plan.form_[1].units;
+    const int64_t n1 = (int64_t)u1.size(), n2 = (int64_t)u2.size();
     for (int64_t i = 0; out && i < n1 + n2 && i < cap; ++i)
-        std::memcpy(out + 16 * i, i < n1 ? &plan.units1[i] : &plan.units2[i - n1], sizeof(AttnUnit));
+        std::memcpy(out + 16 * i, i < n1 ? &u1[i] : &u2[i - n1], sizeof(AttnUnit));
+    if (first) {
+        std::memset(first, 0, sizeof(int32_t) * 2 * (3 * (size_t)n_sm + 1));
+        for (int f = 0; f < 2; ++f)
+            std::copy(plan.form_[f].first.begin(), plan.form_[f].first.end(), first + f * (3 * n_sm + 1));
+    }
     if (n_rows_units) *n_rows_units = n1;
     if (caps) {
         const PagedPlanCaps c = paged_plan_caps(ps, s->max_tok, s->max_seq);
-        caps[0] = c.units1; caps[1] = c.units2; caps[2] = c.tiles; caps[3] = c.parts1; caps[4] = c.parts2;
+        caps[0] = c.units1; caps[1] = c.units2; caps[2] = c.ctas1; caps[3] = c.ctas2;
+        caps[4] = c.tickets; caps[5] = c.parts1; caps[6] = c.parts2;
     }
     return n1 + n2;
 }

@@ -37,7 +37,7 @@ struct KvRowsArgs {
 bool launch_kv_rows_store(const KvRowsArgs& a, cudaStream_t st);
 bool launch_kv_rows_load(const KvRowsArgs& a, cudaStream_t st);
 
-// One unit of attention work (per KV head): rows of one tile of a sequence against a range of the keys
+// One unit of attention work: rows of one tile of a sequence for one KV head against a range of the keys
 // those rows may see. A tile's rows are (token, query head) pairs of the KV head's group, row
 // token * G + head. Its keys are numbered by a virtual index: sink keys 0 .. n_sink_keys - 1, then the
 // keys from key_lo on (the sequence's keys between the sinks and the tile's windows are left out).
@@ -45,16 +45,19 @@ struct AttnUnit {
     int32_t tok0, row0, n_row, p0;               // first token of the sequence; the tile's rows; position of tok0
     int32_t table, n_sink_keys, key_lo, v0;      // page-table offset; the virtual key range [v0, v1)
     int32_t v1, n_chunk, chunk, part;            // units of this tile; this one; the first's partial slot
-    int32_t tile, pad[3];                        // ticket index
+    int32_t ticket, head, pad[2];                // counter of the tile's finished units; KV head
 };
 static_assert(sizeof(AttnUnit) == 64, "read as four int4");
 
-constexpr int kUnitRows1 = 16, kUnitRows2 = 256; // rows per tile of the two forms
-enum : int32_t { ATTN_FORM_ROWS = 1, ATTN_FORM_TC = 2 };
+// Forms of the kernels: 8- and 16-row tiles on mma.sync, 256-row tiles on tcgen05.
+enum : int32_t { ATTN_FORM_ROWS8 = 1, ATTN_FORM_ROWS16 = 2, ATTN_FORM_TC = 4 };
+constexpr int kUnitRows2 = 256;
+// CTAs of a small-tile form per SM (its shared memory and registers allow as many).
+constexpr int attn_rows_ctas(int rows) { return rows == 8 ? 3 : 2; }
 enum AttnOut : int32_t { AO_F16 = 0, AO_BF16 = 1, AO_F32 = 2, AO_BF16_PAIR = 3 };
 
 // Header words of a plan's device buffer.
-enum : int32_t { PH_UNITS1 = 0, PH_UNITS2 = 1, PH_FORM = 2, PH_WORDS = 8 };
+enum : int32_t { PH_FORM = 0, PH_WORDS = 8 };
 
 struct AttnPagedArgs {
     PagedKv kv;
@@ -68,15 +71,16 @@ struct AttnPagedArgs {
     float scale_log2 = 0.f;                      // scale * log2(e)
     int32_t window = 0, n_sink = 0;
     const int32_t* hdr = nullptr;
-    const AttnUnit* units1 = nullptr;
-    const AttnUnit* units2 = nullptr;
+    // units of the small-tile and the 256-row form, and where each CTA's begin [CTAs + 1]
+    const AttnUnit *units1 = nullptr, *units2 = nullptr;
+    const int32_t *first1 = nullptr, *first2 = nullptr;
     const int32_t* table = nullptr;
     const int32_t* perm = nullptr;               // token order (null: identity)
     const int32_t* tok_pos = nullptr;            // positions of tokens (null: p0 + token)
     const int32_t* key_pos = nullptr;            // positions of the page-table's keys, pages of one cell
-    float* part_o = nullptr;                     // [part * Hkv + head][rows][hd] unnormalised
-    float2* part_ml = nullptr;                   // [part * Hkv + head][rows] (running max, sum)
-    int32_t* tickets = nullptr;                  // [tile * Hkv + head], zero between launches
+    float* part_o = nullptr;                     // [part][rows][hd] unnormalised
+    float2* part_ml = nullptr;                   // [part][rows] (running max, sum)
+    int32_t* tickets = nullptr;                  // zero between launches
     uint32_t* err = nullptr;
     int32_t form = 0;                            // forms the caller launches
     int32_t n_sm = 148;
@@ -100,15 +104,28 @@ struct PlanShape {
     int32_t G = 1, Hkv = 1, window = 0, n_sink = 0, n_sm = 148;
     bool tc = false;                             // 256-row tiles allowed
 };
+struct PlanForm {
+    std::vector<AttnUnit> units;
+    std::vector<int32_t> first;                  // where each CTA's units begin [CTAs + 1]
+    int32_t n_parts = 0;
+};
 struct PagedPlan {
-    std::vector<AttnUnit> units1, units2;
-    int32_t n_tiles = 0, n_parts1 = 0, n_parts2 = 0;
-    int32_t form() const { return (units1.empty() ? 0 : ATTN_FORM_ROWS) | (units2.empty() ? 0 : ATTN_FORM_TC); }
+    PlanForm form_[2];                           // small tiles, 256-row tiles
+    int32_t rows1 = 8;                           // rows of the small tiles
+    int32_t n_tickets = 0;
+    int32_t form() const {
+        return (form_[0].units.empty() ? 0 : rows1 == 8 ? ATTN_FORM_ROWS8 : ATTN_FORM_ROWS16) |
+               (form_[1].units.empty() ? 0 : ATTN_FORM_TC);
+    }
 };
 void build_paged_plan(const PlanShape& s, const std::vector<PlanSeq>& seqs, PagedPlan& plan);
 // Upper bounds for buffers over every plan of at most max_tok tokens in max_seq sequences.
-struct PagedPlanCaps { int64_t units1, units2, tiles, parts1, parts2; };
+struct PagedPlanCaps { int64_t units1, units2, ctas1, ctas2, tickets, parts1, parts2; };
 PagedPlanCaps paged_plan_caps(const PlanShape& s, int32_t max_tok, int32_t max_seq);
+// Partial results of the larger form: rows of head_dim values.
+inline int64_t plan_part_rows(const PagedPlanCaps& c) {
+    return c.parts1 * 16 > c.parts2 * kUnitRows2 ? c.parts1 * 16 : c.parts2 * kUnitRows2;
+}
 
 // ---- the sampler chain per row (sample_rows.cu)
 struct SampleRowsArgs {
