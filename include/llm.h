@@ -545,7 +545,7 @@ int llm_debug_set_logits(llm_ctx *ctx, int32_t i, const float *row);
  * values per unit (first token, first row, rows, position of the first token; page-table offset, sink keys,
  * first windowed key, first virtual key; end key, units of the tile, this unit's index, its first partial
  * slot; ticket, KV head, 2 unused), those of the 8- or 16-row tiles first (n_rows_units receives their
- * number). tc != 0 allows 256-row tiles. first, if given, receives two arrays of 3 n_sm + 1: where the
+ * number). tc != 0 allows 256-row tiles. first, if given, receives two arrays of 2 n_sm + 1: where the
  * units of each CTA begin, for the small and the 256-row tiles. caps, if given, receives the plan's
  * buffer bounds for the shape's maxima: units of both, CTAs of both, tickets, partial slots of both. Returns the
  * number of units (writes at most cap of them), -1 for invalid arguments. */

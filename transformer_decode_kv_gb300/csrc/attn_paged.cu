@@ -1,9 +1,9 @@
 // Attention of new tokens over a paged cache, 8- and 16-row tiles: out = softmax(scale q K^T, masked) V for
 // the (token, query head) pairs that share a KV head, an optional sliding window and sink keys.
 //
-// A CTA walks its share of the plan's units. Its four warps take 32 keys of every 128 of a unit's and
+// A CTA walks its share of the plan's units. Its warps take every so many'th 32 keys of a unit and
 // merge their (reference, sum, output) at the end; the units of a cut tile merge through partial results in
-// global memory (the last to finish does it). Per 16 keys and warp, with the keys and dims as the rows of the MMA
+// global memory (the last to finish does it). Per 32 keys and warp, with the keys and dims as the rows of the MMA
 // and the tile's 8 (or 2 x 8) rows as its columns, so that few rows waste little:
 //   S^T = K Q^T      mma.sync m16n8k16, 16 keys x 8 rows, float32 sums
 //   softmax          p = 2^(s - m) with a reference m per row in float32, in the log2 domain. m is 6 below a
@@ -15,8 +15,11 @@
 // bound. A contraction may be taken in any order, so a lane's 16 bytes of a key row simply are the dims its
 // A fragments hold (Q is loaded in the same order), and a lane's values of four keys become fragments
 // by byte permutes (f16/bf16: pairs of keys; E4M3: 4 x 4 bytes, then the conversion to f16, which is
-// exact). Every lane copies just the bytes it will use, asynchronously, into its own places of a ring in shared
-// memory (no bank conflicts, no barrier), as many blocks of 16 keys ahead as the CTAs of an SM have room for.
+// exact). Rows come by asynchronous 16-byte copies, a row by neighbouring lanes, into a warp's own ring in
+// shared memory: 32 keys are used while the next are under way, and a ring's 16-byte chunks are permuted so that
+// both ways of reading them are free of bank conflicts. (Lanes copying just the bytes they use would need no
+// permutation, but touch K rows in 64-byte pieces: 5.3 TB/s at most for E4M3 rows of 128 bytes, against
+// 7.0 TB/s for whole rows.)
 //
 // Precision: products of f16 (bf16) terms with float32 sums. F16 activations and caches enter as they
 // are. BF16 or F32 activations over an f16-typed product are scaled per row by a power of two (taken out of the
@@ -28,6 +31,7 @@
 #include "attn_paged_common.cuh"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace llm {
 
@@ -35,8 +39,6 @@ namespace {
 
 using namespace pattn;
 
-constexpr int kWarps = 4;
-constexpr int kThr = 32 * kWarps;
 
 template <bool BF>
 __device__ __forceinline__ void mma(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -78,16 +80,25 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
     lo = pack2<BF>(x - f.x, y - f.y);
 }
 
-// N words (N = 1, 2, 4) from global memory to this lane's place in shared memory, asynchronously; zeros
-// where the key is not read
-template <int N>
-__device__ __forceinline__ void fetch(uint32_t dst, const uint8_t* src, bool ok) {
-    if constexpr (N == 4)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
-    else if constexpr (N == 2)
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(ok ? 8 : 0) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(ok ? 4 : 0) : "memory");
+// 16 or 4 bytes from global to shared memory, asynchronously; zeros where the key is not read
+__device__ __forceinline__ void fetch16(uint32_t dst, const uint8_t* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void fetch16z(uint32_t dst, const uint8_t* src, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void fetch4z(uint32_t dst, const float* src, bool ok) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(ok ? 4 : 0) : "memory");
+}
+// Byte offset of 16-byte chunk `ch` of row `row` in a tile of rows of ROWB bytes. The chunks of a 128-byte line are
+// permuted so that neither a K fragment's read (rows g, 16-byte chunks c) nor a V fragment's (rows 2 c, chunks g or
+// parts of them) meets a bank twice.
+template <int ROWB>
+__device__ __forceinline__ uint32_t at16(int row, int ch) {
+    if constexpr (ROWB >= 128) return (uint32_t)(row * ROWB + ((ch ^ (((row >> 1) & 3) << 1) ^ ((row & 1) << 2)) << 4));
+    else if constexpr (ROWB == 64)
+        return (uint32_t)((row >> 1) * 128 + (((((row & 1) << 2) | ch) ^ (((row >> 1) & 3) << 1)) << 4));
+    else return (uint32_t)((row >> 2) * 128 + (((((row & 3) << 1) | ch) ^ (((row >> 2) & 1) << 1)) << 4));
 }
 template <int N>
 __device__ __forceinline__ void take(uint32_t* d, const uint8_t* p) {
@@ -102,7 +113,7 @@ __device__ __forceinline__ void take(uint32_t* d, const uint8_t* p) {
     }
 }
 
-// Where this lane's key of a group of 32 lies (off < 0: not read) and its position.
+// Where this lane's key of 32 lies (off < 0: not read) and its position.
 struct Info { int64_t off, soff; int pos; };
 
 template <int HD, int CT, int QT, int ROWS>
@@ -111,6 +122,7 @@ struct Cfg {
     static constexpr bool SPLIT_Q = QT == W_F32;
     static constexpr bool SPLIT_P = QT == W_F32 || BF;
     static constexpr bool ROW_SCALE = !BF && QT != W_F16;
+    static constexpr int W = attn_rows_warps(HD, CT, ROWS);     // warps
     static constexpr int R = ROWS / 8;                          // 8-row column tiles
     static constexpr int KS = HD / 16;                          // k-steps of K Q^T
     static constexpr int KW = F8 ? HD / 16 : HD / 8;            // words of a key a lane holds
@@ -120,30 +132,32 @@ struct Cfg {
     static constexpr int VP = F8 ? HD / 8 : (HD / 8 < 8 ? HD / 8 : 8);   // contiguous dims of a value per lane
     static constexpr int VH = HD / 8 / VP;                      // ... in VH places 8 * VP dims apart
     static constexpr int VW = F8 ? VP / 4 : VP / 2;             // words of one place
-    // a stage: 16 keys of K and V as the lanes will read them (piece by piece, a lane's words side by
-    // side), then the keys' positions, whether all or none are read, and, for E4M3, scales
-    static constexpr int KB = 2 * KW * 128, VB = 4 * VH * VW * 128;
-    static constexpr int STAGE = KB + VB + 64 + 16 + (F8 ? 128 : 0);
-    static constexpr int OUT = kWarps * ROWS * (HD + 4) * 4;     // the warps' results, over the stages
-    static constexpr int CTAS = attn_rows_ctas(ROWS);
-    static constexpr int FIT = (227 * 1024 / CTAS - 2048) / (kWarps * STAGE);
-    static constexpr int S = FIT < 8 ? FIT : 8;
-    static constexpr int RING = kWarps * S * STAGE;
+    // a stage: 32 rows of K and of V, then the keys' positions, which of them are read, and, for E4M3, scales
+    static constexpr int ROWB = F8 ? HD : 2 * HD;
+    static constexpr int META = 64 * ROWB;
+    static constexpr int STAGE = META + 128 + 16 + (F8 ? 256 : 0);
+    static constexpr int OUT = W * ROWS * (HD + 4) * 4;          // the warps' results, over the stages
+    static constexpr int FIT = (227 * 1024 / kAttnRowsCtas - 4096) / (W * STAGE);
+    static constexpr int S = FIT < 6 ? FIT : 6;
+    static constexpr int RING = W * S * STAGE;
     static constexpr int END = RING > OUT ? RING : OUT;
-    static constexpr int BYTES = END + 2 * kWarps * ROWS * 4 + 16;
+    static constexpr int BYTES = END + W * 256 + 2 * W * ROWS * 4 + 16;
     static_assert(S >= 2, "a stage to read and one to fill");
 };
 
 template <int HD, int CT, int QT, int ROWS>
-__global__ void __launch_bounds__(kThr, attn_rows_ctas(ROWS)) attn_rows_kernel(AttnPagedArgs a) {
+__global__ void __launch_bounds__(32 * attn_rows_warps(HD, CT, ROWS), kAttnRowsCtas)
+attn_rows_kernel(AttnPagedArgs a) {
     using C = Cfg<HD, CT, QT, ROWS>;
+    constexpr int kWarps = C::W, kThr = 32 * kWarps;
     constexpr bool F8 = C::F8, BF = C::BF;
     constexpr int R = C::R;
     extern __shared__ __align__(16) uint8_t sm[];
     float (*s_o)[ROWS][HD + 4] = reinterpret_cast<float (*)[ROWS][HD + 4]>(sm);
-    float (*s_m)[ROWS] = reinterpret_cast<float (*)[ROWS]>(sm + C::END);
+    int64_t (*s_off)[32] = reinterpret_cast<int64_t (*)[32]>(sm + C::END);
+    float (*s_m)[ROWS] = reinterpret_cast<float (*)[ROWS]>(sm + C::END + kWarps * 256);
     float (*s_l)[ROWS] = s_m + kWarps;
-    int& s_flag = *reinterpret_cast<int*>(sm + C::END + 2 * kWarps * ROWS * 4);
+    int& s_flag = *reinterpret_cast<int*>(s_l + kWarps);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     if (a.pdl) asm volatile("griddepcontrol.wait;" ::: "memory");
     if (form_missing(a) || (a.hdr[PH_FORM] & (ROWS == 8 ? ATTN_FORM_ROWS8 : ATTN_FORM_ROWS16)) == 0) return;
@@ -169,8 +183,8 @@ __global__ void __launch_bounds__(kThr, attn_rows_ctas(ROWS)) attn_rows_kernel(A
         const int hid_min = hidden_below(a, pmin), hid_max = hidden_below(a, pmax);
 
         const int n_keys = u.v1 - u.v0;
-        // this warp's groups of 32 keys: 32 (warp + 4 i); two stages of 16 keys each
-        const int n_st = 2 * max(0, (n_keys - 32 * warp + 127) / 128);
+        // this warp's groups of 32 keys: 32 (warp + kWarps i)
+        const int n_st = max(0, (n_keys - 32 * warp + 32 * kWarps - 1) / (32 * kWarps));
         auto lookup = [&](int i) {
             Info f{-1, 0, INT_MAX};
             const int v = 32 * (warp + kWarps * i) + lane;
@@ -186,44 +200,47 @@ __global__ void __launch_bounds__(kThr, attn_rows_ctas(ROWS)) attn_rows_kernel(A
             return f;
         };
         uint8_t* const ring = sm + warp * C::S * C::STAGE;
-        Info fcur{-1, 0, INT_MAX}, fnext = lookup(0);
+        Info fnext = lookup(0);
         int in = 0, in_stage = 0;
-        // the copies of the next 16 keys; a group of copies is counted even where there are none
+        // the copies of the next 32 keys; a group of copies is counted even where there are none
         auto issue = [&]() {
             if (in < n_st) {
-                if ((in & 1) == 0) {
-                    fcur = fnext;
-                    fnext = lookup((in >> 1) + 1);
-                }
-                const int l0 = 16 * (in & 1);
+                const Info f = fnext;
                 uint8_t* const st = ring + in_stage * C::STAGE;
-                const uint32_t ka = static_cast<uint32_t>(__cvta_generic_to_shared(st)), va = ka + C::KB;
-                const unsigned read = (__ballot_sync(0xffffffffu, fcur.off >= 0) >> l0) & 0xffffu;
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const int64_t off = __shfl_sync(0xffffffffu, fcur.off, l0 + 8 * t + g);
-                    const uint8_t* src = kbase + (off >= 0 ? off : 0) + 4 * C::KC * c;
-#pragma unroll
-                    for (int i = 0; i < C::KP; ++i)
-                        fetch<C::KC>(ka + (t * C::KP + i) * 128 * C::KC + lane * 4 * C::KC, src + 16 * C::KC * i, off >= 0);
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int64_t off = __shfl_sync(0xffffffffu, fcur.off, l0 + 2 * c + (e & 1) + 8 * (e >> 1));
-                    const uint8_t* src = vbase + (off >= 0 ? off : 0) + 4 * C::VW * g;
-#pragma unroll
-                    for (int i = 0; i < C::VH; ++i)
-                        fetch<C::VW>(va + (e * C::VH + i) * 128 * C::VW + lane * 4 * C::VW, src + 32 * C::VW * i, off >= 0);
-                }
-                if ((lane & 16) == l0) reinterpret_cast<int*>(st + C::KB + C::VB)[lane & 15] = fcur.pos;
-                if (lane == 0) *reinterpret_cast<int*>(st + C::KB + C::VB + 64) = read == 0xffffu ? 2 : read ? 1 : 0;
+                const uint32_t sa = static_cast<uint32_t>(__cvta_generic_to_shared(st));
+                const unsigned read = __ballot_sync(0xffffffffu, f.off >= 0);
+                __syncwarp();                               // the last offsets have been read
+                s_off[warp][lane] = f.off >= 0 ? f.off : 0;
+                reinterpret_cast<int*>(st + C::META)[lane] = f.pos;
+                if (lane == 0) *reinterpret_cast<unsigned*>(st + C::META + 128) = read;
                 if constexpr (F8) {
-                    // lanes 0-15 the keys' scales, 16-31 the values'
-                    const int64_t so = __shfl_sync(0xffffffffu, fcur.off >= 0 ? fcur.soff : (int64_t)-1, l0 + (lane & 15));
-                    fetch<1>(va + C::VB + 80 + 4 * lane,
-                             reinterpret_cast<const uint8_t*>((lane < 16 ? ksb : vsb) + (so >= 0 ? so : 0)), so >= 0);
+                    const int64_t so = f.off >= 0 ? f.soff : 0;
+                    fetch4z(sa + C::META + 144 + 4 * lane, ksb + so, f.off >= 0);
+                    fetch4z(sa + C::META + 272 + 4 * lane, vsb + so, f.off >= 0);
                 }
-                ++in;
+                __syncwarp();
+                constexpr int LPR = C::ROWB / 16, RPI = 32 / LPR;   // lanes per row, rows per copy
+                // (all offsets before the first copy: the copies do not wait for one another's)
+                int64_t off[LPR];
+#pragma unroll
+                for (int x = 0; x < LPR; ++x) off[x] = s_off[warp][x * RPI + lane / LPR] + 16 * (lane % LPR);
+                if (read == 0xffffffffu) {
+#pragma unroll
+                    for (int x = 0; x < LPR; ++x) {
+                        const uint32_t d = sa + at16<C::ROWB>(x * RPI + lane / LPR, lane % LPR);
+                        fetch16(d, kbase + off[x]);
+                        fetch16(d + 32 * C::ROWB, vbase + off[x]);
+                    }
+                } else {
+#pragma unroll
+                    for (int x = 0; x < LPR; ++x) {
+                        const int k = x * RPI + lane / LPR;
+                        const uint32_t d = sa + at16<C::ROWB>(k, lane % LPR);
+                        fetch16z(d, kbase + off[x], read >> k & 1u);
+                        fetch16z(d + 32 * C::ROWB, vbase + off[x], read >> k & 1u);
+                    }
+                }
+                fnext = lookup(++in);
                 if (++in_stage == C::S) in_stage = 0;
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
@@ -319,67 +336,89 @@ __global__ void __launch_bounds__(kThr, attn_rows_ctas(ROWS)) attn_rows_kernel(A
         for (int n = 0; n < n_st; ++n) {
             asm volatile("cp.async.wait_group %0;" ::"n"(C::S - 2) : "memory");
             __syncwarp();                                   // every lane's part of the stage, and of the last is done with
-            issue();
             const uint8_t* const st = ring + stage * C::STAGE;
             if (++stage == C::S) stage = 0;
-            const uint8_t* const meta = st + C::KB + C::VB;
-            const int read = *reinterpret_cast<const int*>(meta + 64);
-            if (read == 0) continue;
-            float S[R][4];
+            const uint8_t* const meta = st + C::META;
+            const unsigned read = *reinterpret_cast<const unsigned*>(meta + 128);
+            // keys 16 b + g and 16 b + g + 8, read ahead of the next copies in the memory pipe's queue
+            uint32_t k[2][2][C::KW];
 #pragma unroll
-            for (int r = 0; r < R; ++r) S[r][0] = S[r][1] = S[r][2] = S[r][3] = 0.f;
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int i = 0; i < C::KP; ++i) {
+                        const int at = 4 * C::KC * (4 * i + c);   // byte of the row
+                        take<C::KC>(&k[b][t][C::KC * i], st + at16<C::ROWB>(16 * b + 8 * t + g, at >> 4) + (at & 15));
+                    }
+            issue();
+            if (read == 0u) continue;
+            // S[b][r][2 h + e] is key 16 b + 8 h + g, row 8 r + 2 c + e
+            float S[2][R][4];
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int r = 0; r < R; ++r) S[b][r][0] = S[b][r][1] = S[b][r][2] = S[b][r][3] = 0.f;
 #pragma unroll
             for (int i = 0; i < C::KP; ++i) {
-                uint32_t k0[C::KC], k1[C::KC];              // keys g and g + 8
-                take<C::KC>(k0, st + i * 128 * C::KC + lane * 4 * C::KC);
-                take<C::KC>(k1, st + (C::KP + i) * 128 * C::KC + lane * 4 * C::KC);
                 constexpr int PER = F8 ? C::KC : C::KC / 2;  // k-steps of a piece
 #pragma unroll
-                for (int j = 0; j < PER; ++j) {
-                    uint32_t ka[4];
-                    if constexpr (F8) {
-                        ka[0] = e4m3x2_to_h2(k0[j] & 0xffffu);
-                        ka[1] = e4m3x2_to_h2(k1[j] & 0xffffu);
-                        ka[2] = e4m3x2_to_h2(k0[j] >> 16);
-                        ka[3] = e4m3x2_to_h2(k1[j] >> 16);
-                    } else {
-                        ka[0] = k0[2 * j]; ka[1] = k1[2 * j]; ka[2] = k0[2 * j + 1]; ka[3] = k1[2 * j + 1];
-                    }
+                for (int j = 0; j < PER; ++j)
 #pragma unroll
-                    for (int r = 0; r < R; ++r) {
-                        mma<BF>(S[r], ka, qf[r][i * PER + j][0], qf[r][i * PER + j][1]);
-                        if constexpr (C::SPLIT_Q) mma<BF>(S[r], ka, ql[r][i * PER + j][0], ql[r][i * PER + j][1]);
+                    for (int b = 0; b < 2; ++b) {
+                        uint32_t ka[4];
+                        if constexpr (F8) {
+                            e4m3x4_to_h2(k[b][0][C::KC * i + j], ka[0], ka[2]);
+                            e4m3x4_to_h2(k[b][1][C::KC * i + j], ka[1], ka[3]);
+                        } else {
+                            ka[0] = k[b][0][C::KC * i + 2 * j]; ka[1] = k[b][1][C::KC * i + 2 * j];
+                            ka[2] = k[b][0][C::KC * i + 2 * j + 1]; ka[3] = k[b][1][C::KC * i + 2 * j + 1];
+                        }
+#pragma unroll
+                        for (int r = 0; r < R; ++r) {
+                            mma<BF>(S[b][r], ka, qf[r][i * PER + j][0], qf[r][i * PER + j][1]);
+                            if constexpr (C::SPLIT_Q) mma<BF>(S[b][r], ka, ql[r][i * PER + j][0], ql[r][i * PER + j][1]);
+                        }
                     }
-                }
             }
-            // scores in the log2 domain: S[r][2 h + e] is key g + 8 h, row 8 r + 2 c + e
+            // scores in the log2 domain
             const int* kpos = reinterpret_cast<const int*>(meta);
-            float ks[2] = {1.f, 1.f}, vs[2] = {1.f, 1.f};
-            if constexpr (F8) {
-                const float* sc = reinterpret_cast<const float*>(meta + 80);
-                ks[0] = sc[g]; ks[1] = sc[g + 8];
-                vs[0] = sc[16 + g]; vs[1] = sc[24 + g];
-            }
-            const int k_lo = kpos[0], k_hi = kpos[15];
+            const float* sc = reinterpret_cast<const float*>(meta + 144);
+            float vs[2][2];
+            const int k_lo = kpos[0], k_hi = kpos[31];
             // every row sees every key (positions ascend)
-            const bool open = read == 2 && k_hi <= pmin && (k_lo > hid_max || k_hi < a.n_sink);
+            const bool open = read == 0xffffffffu && k_hi <= pmin && (k_lo > hid_max || k_hi < a.n_sink);
             bool raise = false;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int kp = kpos[g + 8 * h];
+            for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int r = 0; r < R; ++r)
+                for (int h = 0; h < 2; ++h) {
+                    const float ks = F8 ? sc[16 * b + 8 * h + g] : 1.f;
+                    vs[b][h] = F8 ? sc[32 + 16 * b + 8 * h + g] : 1.f;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float& s = S[r][2 * h + e];
-                        s *= F8 ? rs[r][e] * ks[h] : rs[r][e];
-                        if (!open && !sees(kp, rp[r][e], rh[r][e], a.n_sink)) s = -INFINITY;
-                        raise = raise || s > m[r][e] + 14.f;
+                    for (int r = 0; r < R; ++r)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) S[b][r][2 * h + e] *= F8 ? rs[r][e] * ks : rs[r][e];
+                    if (!open) {
+                        const int kp = kpos[16 * b + 8 * h + g];
+#pragma unroll
+                        for (int r = 0; r < R; ++r)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                if (!sees(kp, rp[r][e], rh[r][e], a.n_sink)) S[b][r][2 * h + e] = -INFINITY;
                     }
-            }
+                }
+            float mx[R][2];
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    mx[r][e] = fmaxf(fmaxf(S[0][r][e], S[0][r][2 + e]), fmaxf(S[1][r][e], S[1][r][2 + e]));
+                    raise = raise || mx[r][e] > m[r][e] + 14.f;
+                }
             float em = 0.f;
             if constexpr (F8) {
-                em = fmaxf(vs[0], vs[1]);
+                em = fmaxf(fmaxf(vs[0][0], vs[0][1]), fmaxf(vs[1][0], vs[1][1]));
                 raise = raise || em > E;
             }
             if (__any_sync(0xffffffffu, raise)) {
@@ -397,13 +436,13 @@ __global__ void __launch_bounds__(kThr, attn_rows_ctas(ROWS)) attn_rows_kernel(A
                     float f[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float mx = fmaxf(S[r][e], S[r][2 + e]);
 #pragma unroll
-                        for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                        for (int o = 4; o < 32; o <<= 1)
+                            mx[r][e] = fmaxf(mx[r][e], __shfl_xor_sync(0xffffffffu, mx[r][e], o));
                         f[e] = 1.f;
-                        if (mx > m[r][e] + 14.f) {          // true from nothing too
-                            f[e] = ex2(m[r][e] - (mx - 6.f));   // 0 from nothing
-                            m[r][e] = mx - 6.f;
+                        if (mx[r][e] > m[r][e] + 14.f) {    // true from nothing too
+                            f[e] = ex2(m[r][e] - (mx[r][e] - 6.f));   // 0 from nothing
+                            m[r][e] = mx[r][e] - 6.f;
                             l[r][e] *= f[e];
                         }
                         f[e] *= fe;
@@ -415,58 +454,65 @@ __global__ void __launch_bounds__(kThr, attn_rows_ctas(ROWS)) attn_rows_kernel(A
                     }
                 }
             }
-            // P^T fragments: pf[r][h] holds keys 8 h + 2 c, + 1 of row 8 r + g
-            uint32_t pf[R][2], pl[C::SPLIT_P ? R : 1][2];
             const float inv = F8 && E > 0.f ? 1.f / E : 0.f;
+            // P^T fragments: pf[b][r][h] holds keys 16 b + 8 h + 2 c, + 1 of row 8 r + g
+            uint32_t pf[2][R][2], pl[2][C::SPLIT_P ? R : 1][2];
 #pragma unroll
-            for (int r = 0; r < R; ++r)
+            for (int r = 0; r < R; ++r) {
+                // (nothing seen yet: scores of -inf, or NaN, which has to show)
+                const float m0 = m[r][0] == -INFINITY ? 0.f : m[r][0], m1 = m[r][1] == -INFINITY ? 0.f : m[r][1];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    // (nothing seen yet: scores of -inf, or NaN, which has to show)
-                    float p0 = ex2(S[r][2 * h] - (m[r][0] == -INFINITY ? 0.f : m[r][0]));
-                    float p1 = ex2(S[r][2 * h + 1] - (m[r][1] == -INFINITY ? 0.f : m[r][1]));
-                    l[r][0] += p0;
-                    l[r][1] += p1;
-                    if constexpr (F8) { p0 *= vs[h] * inv; p1 *= vs[h] * inv; }
-                    if constexpr (C::SPLIT_P) {
-                        uint32_t hi, lo;
-                        split2<BF>(p0, p1, hi, lo);
-                        pf[r][h] = transpose8(hi);
-                        pl[r][h] = transpose8(lo);
-                    } else {
-                        pf[r][h] = transpose8(pack2<BF>(p0, p1));
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float p0 = ex2(S[b][r][2 * h] - m0), p1 = ex2(S[b][r][2 * h + 1] - m1);
+                        l[r][0] += p0;
+                        l[r][1] += p1;
+                        if constexpr (F8) { p0 *= vs[b][h] * inv; p1 *= vs[b][h] * inv; }
+                        if constexpr (C::SPLIT_P) {
+                            uint32_t hi, lo;
+                            split2<BF>(p0, p1, hi, lo);
+                            pf[b][r][h] = transpose8(hi);
+                            pl[b][r][h] = transpose8(lo);
+                        } else {
+                            pf[b][r][h] = transpose8(pack2<BF>(p0, p1));
+                        }
                     }
-                }
-            auto pv = [&](int t, const uint32_t* va) {
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    mma<BF>(O[r][t], va, pf[r][0], pf[r][1]);
-                    if constexpr (C::SPLIT_P) mma<BF>(O[r][t], va, pl[r][0], pl[r][1]);
-                }
-            };
+            }
             // V^T fragments: rows g and g + 8 of a 16-dim tile are two neighbouring dims of the lane's
 #pragma unroll
-            for (int p = 0; p < C::VH; ++p) {
-                uint32_t vr[4][C::VW];                      // keys 2c, 2c + 1, 2c + 8, 2c + 9
+            for (int b = 0; b < 2; ++b) {
+                auto pv = [&](int t, const uint32_t* va) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    take<C::VW>(vr[e], st + C::KB + (e * C::VH + p) * 128 * C::VW + lane * 4 * C::VW);
+                    for (int r = 0; r < R; ++r) {
+                        mma<BF>(O[r][t], va, pf[b][r][0], pf[b][r][1]);
+                        if constexpr (C::SPLIT_P) mma<BF>(O[r][t], va, pl[b][r][0], pl[b][r][1]);
+                    }
+                };
 #pragma unroll
-                for (int w = 0; w < C::VW; ++w) {
-                    const uint32_t w0 = vr[0][w], w1 = vr[1][w], w2 = vr[2][w], w3 = vr[3][w];
-                    if constexpr (F8) {
-                        const uint32_t x0 = __byte_perm(w0, w1, 0x5140), x1 = __byte_perm(w0, w1, 0x7362);
-                        const uint32_t y0 = __byte_perm(w2, w3, 0x5140), y1 = __byte_perm(w2, w3, 0x7362);
-                        const uint32_t a0[4] = {e4m3x2_to_h2(x0 & 0xffffu), e4m3x2_to_h2(x0 >> 16),
-                                                e4m3x2_to_h2(y0 & 0xffffu), e4m3x2_to_h2(y0 >> 16)};
-                        pv(2 * (p * C::VW + w), a0);
-                        const uint32_t a1[4] = {e4m3x2_to_h2(x1 & 0xffffu), e4m3x2_to_h2(x1 >> 16),
-                                                e4m3x2_to_h2(y1 & 0xffffu), e4m3x2_to_h2(y1 >> 16)};
-                        pv(2 * (p * C::VW + w) + 1, a1);
-                    } else {
-                        const uint32_t a0[4] = {__byte_perm(w0, w1, 0x5410), __byte_perm(w0, w1, 0x7632),
-                                                __byte_perm(w2, w3, 0x5410), __byte_perm(w2, w3, 0x7632)};
-                        pv(p * C::VW + w, a0);
+                for (int p = 0; p < C::VH; ++p) {
+                    uint32_t vr[4][C::VW];                  // keys 16 b + 2c, 2c + 1, 2c + 8, 2c + 9
+                    const int at = 4 * C::VW * (8 * p + g);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        take<C::VW>(vr[e], st + 32 * C::ROWB + (at & 15) +
+                                               at16<C::ROWB>(16 * b + 2 * c + (e & 1) + 8 * (e >> 1), at >> 4));
+#pragma unroll
+                    for (int w = 0; w < C::VW; ++w) {
+                        const uint32_t w0 = vr[0][w], w1 = vr[1][w], w2 = vr[2][w], w3 = vr[3][w];
+                        if constexpr (F8) {
+                            uint32_t a0[4], a1[4];
+                            e4m3x4_to_h2(__byte_perm(w0, w1, 0x5140), a0[0], a0[1]);
+                            e4m3x4_to_h2(__byte_perm(w2, w3, 0x5140), a0[2], a0[3]);
+                            e4m3x4_to_h2(__byte_perm(w0, w1, 0x7362), a1[0], a1[1]);
+                            e4m3x4_to_h2(__byte_perm(w2, w3, 0x7362), a1[2], a1[3]);
+                            pv(2 * (p * C::VW + w), a0);
+                            pv(2 * (p * C::VW + w) + 1, a1);
+                        } else {
+                            const uint32_t a0[4] = {__byte_perm(w0, w1, 0x5410), __byte_perm(w0, w1, 0x7632),
+                                                    __byte_perm(w2, w3, 0x5410), __byte_perm(w2, w3, 0x7632)};
+                            pv(p * C::VW + w, a0);
+                        }
                     }
                 }
             }
@@ -548,8 +594,8 @@ bool go(const AttnPagedArgs& a, cudaStream_t st) {
         cudaSuccess)
         return false;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(C::CTAS * a.n_sm);                   // the plan's CTAs
-    cfg.blockDim = dim3(kThr);
+    cfg.gridDim = dim3(kAttnRowsCtas * a.n_sm);             // the plan's CTAs
+    cfg.blockDim = dim3(32 * C::W);
     cfg.dynamicSmemBytes = C::BYTES;
     cfg.stream = st;
     cudaLaunchAttribute at[1];

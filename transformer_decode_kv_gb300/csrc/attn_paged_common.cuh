@@ -35,6 +35,12 @@ __device__ __forceinline__ AttnUnit load_unit(const AttnUnit* u) {
     return r;
 }
 
+// four E4M3 codes to two f16 pairs (exact)
+__device__ __forceinline__ void e4m3x4_to_h2(uint32_t four, uint32_t& lo, uint32_t& hi) {
+    asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}\n"
+        : "=r"(lo), "=r"(hi) : "r"(four));
+}
+
 // A key of a unit: its cell as byte and scale offsets (without the head), its position. off < 0: a cell
 // outside the cache.
 struct KeyAt { int64_t off, soff; int pos; };

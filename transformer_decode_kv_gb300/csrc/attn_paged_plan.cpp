@@ -8,16 +8,15 @@ namespace llm {
 
 namespace {
 
-// Keys are dealt out in blocks of 128: a 16-row form's CTA has four warps of 32 keys each, the 256-row form
-// multiplies 128 keys at a time.
-constexpr int64_t kBlockKeys = 128;
+// Keys are dealt out in blocks: what the warps of a small-tile CTA take at once (32 keys each), or the 128 keys
+// that the 256-row form multiplies at a time.
+int64_t block_keys(const PlanShape& s, int f, int rows) { return f ? 128 : 32 * attn_rows_warps(s.hd, s.kv_type, rows); }
 // What a unit costs beyond its keys, in blocks: Q in, the warps' (halves') results out and merged.
-// 16-row forms: about 2 us against 3 us a block and CTA; 256-row form: about 3 us against 1 us a block.
 constexpr int64_t kUnitCost[2] = {1, 3};
 // Sequences with at least this many rows per KV head take 256-row tiles.
 constexpr int64_t kTcRows = 64;
 
-int64_t ctas(const PlanShape& s, int f, int rows) { return (int64_t)s.n_sm * (f ? 1 : attn_rows_ctas(rows)); }
+int64_t ctas(const PlanShape& s, int f) { return (int64_t)s.n_sm * (f ? 1 : kAttnRowsCtas); }
 
 // The virtual key range of the rows [row0, row0 + n) of a sequence: sink keys, then [lo, hi).
 struct Keys { int32_t n_sink, lo, n; };
@@ -70,14 +69,15 @@ void build_paged_plan(const PlanShape& s, const std::vector<PlanSeq>& seqs, Page
         for (int64_t r = 0; r < rows; r += step) {
             Tile t{(int32_t)i, (int32_t)r, (int32_t)std::min(step, rows - r), {}};
             t.keys = tile_keys(s, seqs[i], t.row0, t.n_row);
-            total[f] += (t.keys.n + kBlockKeys - 1) / kBlockKeys + kUnitCost[f];
+            const int64_t bk = block_keys(s, f, plan.rows1);
+            total[f] += (t.keys.n + bk - 1) / bk + kUnitCost[f];
             tiles[f].push_back(t);
         }
     }
     for (int f = 0; f < 2; ++f) {
         PlanForm& pf = plan.form_[f];
         if (tiles[f].empty()) continue;
-        const int64_t n_cta = ctas(s, f, plan.rows1), cost = kUnitCost[f];
+        const int64_t n_cta = ctas(s, f), cost = kUnitCost[f], bk = block_keys(s, f, plan.rows1);
         // a CTA's share: what is there divided evenly, and one more unit for the cut at its end
         const int64_t share = (total[f] * s.Hkv + n_cta - 1) / n_cta + cost;
         int64_t left = share;                           // of the current CTA's share
@@ -92,7 +92,7 @@ void build_paged_plan(const PlanShape& s, const std::vector<PlanSeq>& seqs, Page
                 for (size_t i = i0; i < i1; ++i) {
                     const Tile& t = tiles[f][i];
                     const PlanSeq& q = seqs[t.seq];
-                    const int64_t blocks = (t.keys.n + kBlockKeys - 1) / kBlockKeys;
+                    const int64_t blocks = (t.keys.n + bk - 1) / bk;
                     const size_t u0 = pf.units.size();
                     int64_t at = 0;
                     do {
@@ -109,8 +109,8 @@ void build_paged_plan(const PlanShape& s, const std::vector<PlanSeq>& seqs, Page
                         u.table = q.table;
                         u.n_sink_keys = t.keys.n_sink;
                         u.key_lo = t.keys.lo;
-                        u.v0 = (int32_t)(at * kBlockKeys);
-                        u.v1 = (int32_t)std::min<int64_t>(t.keys.n, (at + take) * kBlockKeys);
+                        u.v0 = (int32_t)(at * bk);
+                        u.v1 = (int32_t)std::min<int64_t>(t.keys.n, (at + take) * bk);
                         u.chunk = (int32_t)(pf.units.size() - u0);
                         u.head = h;
                         pf.units.push_back(u);
@@ -141,8 +141,8 @@ PagedPlanCaps paged_plan_caps(const PlanShape& s, int32_t max_tok, int32_t max_s
     const int64_t rows = (int64_t)max_tok * s.G;
     const int64_t t1 = rows / 8 + std::min<int64_t>(max_seq, max_tok);
     const int64_t t2 = s.tc ? rows / kUnitRows2 + std::min<int64_t>(max_seq, rows / kTcRows) : 0;
-    c.ctas1 = std::max(ctas(s, 0, 8), ctas(s, 0, 16));
-    c.ctas2 = s.tc ? ctas(s, 1, 0) : 0;
+    c.ctas1 = ctas(s, 0);
+    c.ctas2 = s.tc ? ctas(s, 1) : 0;
     c.units1 = t1 * s.Hkv + c.ctas1;
     c.units2 = t2 * s.Hkv + c.ctas2;
     c.tickets = c.ctas1 + c.ctas2;

@@ -166,6 +166,8 @@ PlanShape plan_shape(const llm_attn_shape* s, const llm_kv_pages* kv, int32_t n_
     p.window = s->window;
     p.n_sink = s->n_sink;
     p.n_sm = n_sm;
+    p.hd = kv->head_dim;
+    p.kv_type = kv->type;
     p.tc = tc;
     return p;
 }
@@ -485,9 +487,9 @@ int64_t llm_debug_attn_units(const llm_attn_shape* s, const llm_kv_pages* kv, in
     for (int64_t i = 0; out && i < n1 + n2 && i < cap; ++i)
         std::memcpy(out + 16 * i, i < n1 ? &u1[i] : &u2[i - n1], sizeof(AttnUnit));
     if (first) {
-        std::memset(first, 0, sizeof(int32_t) * 2 * (3 * (size_t)n_sm + 1));
+        std::memset(first, 0, sizeof(int32_t) * 2 * (2 * (size_t)n_sm + 1));
         for (int f = 0; f < 2; ++f)
-            std::copy(plan.form_[f].first.begin(), plan.form_[f].first.end(), first + f * (3 * n_sm + 1));
+            std::copy(plan.form_[f].first.begin(), plan.form_[f].first.end(), first + f * (2 * n_sm + 1));
     }
     if (n_rows_units) *n_rows_units = n1;
     if (caps) {

@@ -52,8 +52,13 @@ static_assert(sizeof(AttnUnit) == 64, "read as four int4");
 // Forms of the kernels: 8- and 16-row tiles on mma.sync, 256-row tiles on tcgen05.
 enum : int32_t { ATTN_FORM_ROWS8 = 1, ATTN_FORM_ROWS16 = 2, ATTN_FORM_TC = 4 };
 constexpr int kUnitRows2 = 256;
-// CTAs of a small-tile form per SM (its shared memory and registers allow as many).
-constexpr int attn_rows_ctas(int rows) { return rows == 8 ? 3 : 2; }
+// The small-tile forms run two CTAs per SM. A warp keeps 32 keys in use and 32 under way, so a 16-bit cache with
+// head_dim 128 (33 KB a warp) leaves room for three warps per CTA; the others take six, or four where the
+// 16-row form needs the registers.
+constexpr int kAttnRowsCtas = 2;
+constexpr int attn_rows_warps(int hd, int kv_type, int rows) {
+    return hd == 128 && kv_type != W_F8 ? 3 : rows == 8 ? 6 : 4;
+}
 enum AttnOut : int32_t { AO_F16 = 0, AO_BF16 = 1, AO_F32 = 2, AO_BF16_PAIR = 3 };
 
 // Header words of a plan's device buffer.
@@ -102,6 +107,7 @@ struct PlanSeq {
 };
 struct PlanShape {
     int32_t G = 1, Hkv = 1, window = 0, n_sink = 0, n_sm = 148;
+    int32_t hd = 128, kv_type = W_F16;
     bool tc = false;                             // 256-row tiles allowed
 };
 struct PlanForm {
