@@ -249,29 +249,42 @@ def debug_noalloc_scratch_poke(value: int) -> int:
 
 
 # ---- operators on the caller's own torch CUDA tensors --------------------------------------------
+# These calls are made many times a step, so their checks read each tensor property once.
+_types = {}
+
+
+def _type(t):
+    """The llm_type of a torch tensor's elements (uint8 holds E4M3 codes), "int32", or None."""
+    if not _types:
+        import torch
+        _types.update({torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16,
+                       torch.float8_e4m3fn: F8_E4M3, torch.uint8: F8_E4M3, torch.int32: "int32"})
+    return _types.get(t.dtype)
+
+
 def _type_of(t) -> int:
-    """The llm_type of a torch tensor's elements (uint8 holds E4M3 codes)."""
-    import torch
-    types = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16,
-             torch.float8_e4m3fn: F8_E4M3, torch.uint8: F8_E4M3}
-    if t.dtype not in types:
+    """The llm_type of a tensor of values."""
+    r = _type(t)
+    if not isinstance(r, int):
         raise TypeError(f"unsupported element type {t.dtype}")
-    return types[t.dtype]
+    return r
 
 
-def _stream_of(t, stream: Optional[int]):
+def _stream_of(t, stream: Optional[int]) -> Optional[int]:
     """The given cudaStream_t, or torch's current stream of t's device."""
-    if stream is not None:
-        return C.c_void_p(stream)
+    if stream is not None or not t.is_cuda:
+        return stream
     import torch
-    return C.c_void_p(torch.cuda.current_stream(t.device).cuda_stream if t.is_cuda else None)
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
-def _need(t, name: str, dtype: str, shape) -> None:
-    """t must be a dense tensor of this type and shape: the library reads it as such."""
-    if str(t.dtype) != "torch." + dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
-                         f"not {t.dtype} {tuple(t.shape)}")
+def _need(t, name: str, dtype, shape) -> int:
+    """The address of t, which must be a dense tensor of this type and shape: the library reads it
+    as such."""
+    if _type(t) != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)} (int32 or "
+                         f"float32 as documented), not {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
 
 
 def _op(status: int) -> None:
@@ -279,10 +292,13 @@ def _op(status: int) -> None:
         raise LlmError(lib().llm_op_last_error().decode() + f" ({status})")
 
 
-def _rows(t, name: str, heads: int, dim: int) -> None:
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or (dim > 1 and t.stride(2) != 1):
+def _rows(t, name: str, heads: int, dim: int):
+    """The strides of a [tokens, heads, dim] tensor with dense rows."""
+    sh, st = t.shape, t.stride()
+    if len(sh) != 3 or sh[1] != heads or sh[2] != dim or st[2] != 1:
         raise ValueError(f"{name} must be [tokens, {heads}, {dim}] with dense rows, "
-                         f"not {tuple(t.shape)} with strides {t.stride()}")
+                         f"not {tuple(sh)} with strides {st}")
+    return st
 
 
 class KvPages:
@@ -305,31 +321,32 @@ class KvPages:
             raise ValueError("an E4M3 cache has scales, other caches have none")
         if k_scale is not None:
             for s in (k_scale, v_scale):
-                if str(s.dtype) != "torch.float32" or s.shape != k.shape[:3]:
+                if _type(s) != F32 or s.shape != k.shape[:3]:
                     raise ValueError("scales must be float32 [n_pages, page_size, n_head_kv]")
             if k_scale.stride() != v_scale.stride():
                 raise ValueError("k_scale and v_scale must be laid out alike")
             d.k_scale, d.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
             d.sstride_page, d.sstride_cell, d.sstride_head = k_scale.stride()
         self.desc = d
+        self.ref = C.byref(d)
+        self.heads, self.dim = d.n_head_kv, d.head_dim
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
 
     def _kv_rows(self, fn, k, v, cell, err, stream):
-        for t, name in ((k, "k"), (v, "v")):
-            _rows(t, name, self.desc.n_head_kv, self.desc.head_dim)
-        if k.shape != v.shape or k.dtype != v.dtype or k.stride() != v.stride():
+        st = _rows(k, "k", self.heads, self.dim)
+        n = k.shape[0]
+        if v.shape != k.shape or v.dtype is not k.dtype or v.stride() != st:
             raise ValueError("k and v must be alike")
-        _need(cell, "cell", "int32", (k.shape[0],))
-        if err is not None and str(err.dtype) not in ("torch.int32", "torch.uint32"):
-            raise ValueError("err must be a 32-bit word")
-        _op(fn(C.byref(self.desc), _type_of(k), k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1),
-               cell.data_ptr(), k.shape[0], err.data_ptr() if err is not None else None,
-               _stream_of(k, stream)))
+        cells = _need(cell, "cell", "int32", (n,))
+        r = fn(self.ref, _type_of(k), k.data_ptr(), v.data_ptr(), st[0], st[1], cells, n,
+               None if err is None else _need(err, "err", "int32", (1,)), _stream_of(k, stream))
+        if r != 0:
+            _op(r)
 
 
 def kv_store(pages: KvPages, k, v, cell, err=None, stream: Optional[int] = None) -> None:
     """Write rows k, v [n, n_head_kv, head_dim] into cells cell [n] (int32; negative: skipped) of the
-    cache, cast or quantised to its type. err: an optional device word for bad cells."""
+    cache, cast or quantised to its type. err: an optional device word (int32 [1]) for bad cells."""
     pages._kv_rows(lib().llm_kv_store, k, v, cell, err, stream)
 
 
@@ -350,12 +367,13 @@ class AttnPlan:
         types = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
         if dtype not in types:
             raise TypeError(f"unsupported activation type {dtype}")
-        self.dtype, self.n_head, self.head_dim = dtype, n_head, pages.desc.head_dim
+        self.dtype, self.n_head, self.head_dim = dtype, n_head, pages.dim
         self.device = pages.k.device
         self.n_tok = 0
+        self._run = lib().llm_attn_run
         s = AttnShape(types[dtype], n_head, scale, window, n_sink, max_tok, max_seq, max_table)
         with torch.cuda.device(self.device if pages.k.is_cuda else -1):
-            self.ptr = lib().llm_attn_plan_init(C.byref(s), C.byref(pages.desc))
+            self.ptr = lib().llm_attn_plan_init(C.byref(s), pages.ref)
         if not self.ptr:
             raise LlmError("llm_attn_plan_init failed: " + lib().llm_op_last_error().decode())
 
@@ -381,22 +399,22 @@ class AttnPlan:
             import torch
             stream = torch.cuda.current_stream(self.device).cuda_stream
         _op(lib().llm_attn_plan_set(self.ptr, len(n_new), _ptr(n_new, C.c_int32),
-                                    _ptr(n_kv, C.c_int32), _ptr(t, C.c_int32), t.shape[1],
-                                    C.c_void_p(stream)))
+                                    _ptr(n_kv, C.c_int32), _ptr(t, C.c_int32), t.shape[1], stream))
         self.n_tok = int(n_new.sum())
 
     def run(self, q, pages: KvPages, out, stream: Optional[int] = None) -> None:
         """out[i] = attention of token i of the step; q and out [at least the step's tokens, n_head,
         head_dim], rows past the tokens are not touched."""
-        for t, name in ((q, "q"), (out, "out")):
-            _rows(t, name, self.n_head, self.head_dim)
-            if t.dtype != self.dtype:
-                raise TypeError(f"{name} must be {self.dtype}")
-            if t.shape[0] < self.n_tok:
-                raise ValueError(f"{name} has fewer rows than the step has tokens ({self.n_tok})")
-        _op(lib().llm_attn_run(self.ptr, q.data_ptr(), q.stride(0), q.stride(1),
-                               C.byref(pages.desc), out.data_ptr(), out.stride(0), out.stride(1),
-                               _stream_of(q, stream)))
+        sq = _rows(q, "q", self.n_head, self.head_dim)
+        so = _rows(out, "out", self.n_head, self.head_dim)
+        if q.dtype is not self.dtype or out.dtype is not self.dtype:
+            raise TypeError(f"q and out must be {self.dtype}")
+        if q.shape[0] < self.n_tok or out.shape[0] < self.n_tok:
+            raise ValueError(f"q or out has fewer rows than the step has tokens ({self.n_tok})")
+        r = self._run(self.ptr, q.data_ptr(), sq[0], sq[1], pages.ref, out.data_ptr(), so[0], so[1],
+                      _stream_of(q, stream))
+        if r != 0:
+            _op(r)
 
     @property
     def form(self) -> int:
@@ -413,26 +431,35 @@ def sample_rows(logits, token, u=None, top_k=None, top_p=None, min_p=None, tempe
     """The sampler chain for every row of logits [n, n_vocab]; token [n] int32 receives the picks. The
     parameters are device arrays of n values (top_k int32, the others float32; None = off; temperature
     None = greedy); row r's penalty tokens are penalty_token[penalty_start[r]:penalty_start[r + 1]]."""
-    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+    sh = logits.shape
+    if len(sh) != 2 or (sh[1] > 1 and logits.stride(1) != 1):
         raise ValueError("logits must be [rows, n_vocab] with dense rows")
-    R, V = logits.shape
+    R = sh[0]
+    row = (R,)
     a = SampleRowsArgs()
     a.type = _type_of(logits)
-    a.n_rows, a.n_vocab, a.ld, a.logits = R, V, logits.stride(0), logits.data_ptr()
-    _need(token, "token", "int32", (R,))
-    a.token = token.data_ptr()
-    for name, t, dt in (("u", u, "float32"), ("top_k", top_k, "int32"), ("top_p", top_p, "float32"),
-                        ("min_p", min_p, "float32"), ("temperature", temperature, "float32"),
-                        ("repeat_penalty", repeat_penalty, "float32")):
-        if t is not None:
-            _need(t, name, dt, (R,))
-            setattr(a, name, t.data_ptr())
-    if repeat_penalty is not None and penalty_start is not None and penalty_token is not None:
-        _need(penalty_start, "penalty_start", "int32", (R + 1,))
-        _need(penalty_token, "penalty_token", "int32", (penalty_token.numel(),))
-        a.penalty_start, a.penalty_token = penalty_start.data_ptr(), penalty_token.data_ptr()
-        a.n_penalty_token = penalty_token.numel()
-    _op(lib().llm_sample_rows(C.byref(a), _stream_of(logits, stream)))
+    a.n_rows, a.n_vocab, a.ld, a.logits = R, sh[1], logits.stride(0), logits.data_ptr()
+    a.token = _need(token, "token", "int32", row)
+    if u is not None:
+        a.u = _need(u, "u", F32, row)
+    if top_k is not None:
+        a.top_k = _need(top_k, "top_k", "int32", row)
+    if top_p is not None:
+        a.top_p = _need(top_p, "top_p", F32, row)
+    if min_p is not None:
+        a.min_p = _need(min_p, "min_p", F32, row)
+    if temperature is not None:
+        a.temperature = _need(temperature, "temperature", F32, row)
+    if repeat_penalty is not None:
+        a.repeat_penalty = _need(repeat_penalty, "repeat_penalty", F32, row)
+        if penalty_start is not None and penalty_token is not None:
+            n = penalty_token.numel()
+            a.penalty_start = _need(penalty_start, "penalty_start", "int32", (R + 1,))
+            a.penalty_token = _need(penalty_token, "penalty_token", "int32", (n,))
+            a.n_penalty_token = n
+    r = lib().llm_sample_rows(C.byref(a), _stream_of(logits, stream))
+    if r != 0:
+        _op(r)
 
 
 class Context:

@@ -590,9 +590,8 @@ attn_rows_kernel(AttnPagedArgs a) {
 template <int HD, int CT, int QT, int ROWS>
 bool go(const AttnPagedArgs& a, cudaStream_t st) {
     using C = Cfg<HD, CT, QT, ROWS>;
-    if (cudaFuncSetAttribute(attn_rows_kernel<HD, CT, QT, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES) !=
-        cudaSuccess)
-        return false;
+    static std::atomic<uint64_t> done{0};
+    if (!allow_smem(reinterpret_cast<const void*>(attn_rows_kernel<HD, CT, QT, ROWS>), C::BYTES, done)) return false;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(kAttnRowsCtas * a.n_sm);             // the plan's CTAs
     cfg.blockDim = dim3(32 * C::W);

@@ -682,9 +682,8 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a) 
 
 template <int HD, int CT, int QT>
 bool go(const AttnPagedArgs& a, cudaStream_t st) {
-    if (cudaFuncSetAttribute(attn_tc_rows_kernel<HD, CT, QT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)Smem<HD>::bytes) != cudaSuccess)
-        return false;
+    static std::atomic<uint64_t> done{0};
+    if (!allow_smem(reinterpret_cast<const void*>(attn_tc_rows_kernel<HD, CT, QT>), Smem<HD>::bytes, done)) return false;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.n_sm);                             // one CTA per SM, each walking its units
     cfg.blockDim = dim3(kThr);

@@ -2,6 +2,7 @@
 // (sample_rows.cu): launch arguments shared by the C entry points (op_api.cu) and the decode loop.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <string>
 #include <vector>
@@ -14,6 +15,18 @@ namespace llm {
 
 constexpr int32_t W_F8 = 100;                    // LLM_TYPE_F8_E4M3
 enum : uint32_t { ERR_PLAN_FORM = 16u };         // beside the bits of kernels.h
+
+// Allow a kernel its dynamic shared memory, once per device (`done`: a bit per device; the call costs about as much
+// as a launch).
+inline bool allow_smem(const void* kernel, size_t bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+    if (bit && (done.load(std::memory_order_acquire) & bit)) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess) return false;
+    done.fetch_or(bit, std::memory_order_release);
+    return true;
+}
 
 // A paged cache as the kernels see it; strides in bytes (scales: elements).
 struct PagedKv {

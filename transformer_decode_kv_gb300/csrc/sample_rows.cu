@@ -424,8 +424,8 @@ bool go(const SampleRowsArgs& a, cudaStream_t st) {
     const int slice = ((a.V + cl - 1) / cl + 31) / 32 * 32;
     if (slice > kSliceMax) return false;
     const size_t bytes = smem_bytes(slice);
-    if (cudaFuncSetAttribute(sample_rows_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess)
-        return false;
+    static std::atomic<uint64_t> done{0};
+    if (!allow_smem(reinterpret_cast<const void*>(sample_rows_kernel<T>), smem_bytes(kSliceMax), done)) return false;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.n_rows * cl));
     cfg.blockDim = dim3(kThr);
