@@ -582,7 +582,13 @@ attn_rows_kernel(AttnPagedArgs a) {
                 if (d == 0) a.part_ml[at] = make_float2(M, L);
             }
         }
-        if (u.n_chunk > 1 && last_of_tile(a, u, &s_flag)) merge_parts<HD>(a, u, ROWS);
+        if (u.n_chunk > 1) {
+            __threadfence();
+            __syncthreads();
+            if (threadIdx.x == 0) s_flag = count_unit(a, u);
+            __syncthreads();
+            if (s_flag) merge_parts<HD>(a, u, ROWS, threadIdx.x, kThr);
+        }
         __syncthreads();                                    // shared memory is free for the next unit
     }
 }

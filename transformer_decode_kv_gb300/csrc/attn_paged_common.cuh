@@ -175,9 +175,9 @@ __device__ __noinline__ void careful_row(const AttnPagedArgs& a, const AttnUnit&
 // The last unit of a tile to finish merges the partial results of all of them (in their order, so
 // the result does not depend on which unit was last). rows: the tile form's rows.
 template <int HD>
-__device__ void merge_parts(const AttnPagedArgs& a, const AttnUnit& u, int rows) {
+__device__ void merge_parts(const AttnPagedArgs& a, const AttnUnit& u, int rows, int tid, int n_threads) {
     constexpr int Q = HD / 4;                                  // four dims per thread
-    for (int x = threadIdx.x; x < u.n_row * Q; x += blockDim.x) {
+    for (int x = tid; x < u.n_row * Q; x += n_threads) {
         const int r = x / Q, d = (x % Q) * 4;
         float M = -INFINITY, L = 0.f, O[4] = {};
         for (int c = 0; c < u.n_chunk; ++c)
@@ -200,19 +200,16 @@ __device__ void merge_parts(const AttnPagedArgs& a, const AttnUnit& u, int rows)
     }
 }
 
-// Count this unit as finished (its partial results are written); true in every thread of the last one.
-__device__ __forceinline__ bool last_of_tile(const AttnPagedArgs& a, const AttnUnit& u, int* flag) {
+// Count a unit of a cut tile as finished, by one thread after a barrier behind the writes of its partial results
+// (each writer's followed by a __threadfence); true for the last one, whose threads may read all of them after
+// another barrier.
+__device__ __forceinline__ bool count_unit(const AttnPagedArgs& a, const AttnUnit& u) {
     __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        int* t = a.tickets + u.ticket;
-        const bool last = atomicAdd(t, 1) + 1 == u.n_chunk;
-        if (last) *t = 0;
-        *flag = last;
-        __threadfence();
-    }
-    __syncthreads();
-    return *flag != 0;
+    int* t = a.tickets + u.ticket;
+    const bool last = atomicAdd(t, 1) + 1 == u.n_chunk;
+    if (last) *t = 0;
+    __threadfence();
+    return last;
 }
 
 // The plan was made for other forms than this launch runs: nothing is computed, the caller learns of it.

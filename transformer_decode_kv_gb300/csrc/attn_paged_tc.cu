@@ -14,7 +14,8 @@
 // thread and run in issue order, so O += P V of block j may be followed at once by S of block j + 1 over
 // the same columns, and a completed S means that every product before it is complete too.
 //
-// Roles (12 warps, so that a thread may have 168 registers): warps 0-1 bring K and V rows cell by cell into a ring of 128-byte-swizzled tiles
+// Roles (12 warps; warps 0-3 give registers to warps 4-11, whose threads hold a row of scores each): warps
+// 0-1 bring K and V rows cell by cell into a ring of 128-byte-swizzled tiles
 // (16-byte asynchronous copies; E4M3 rows through registers, converted to f16), with the keys' positions;
 // warp 2 issues the MMAs; warps 4-7 and 8-11 are the two halves' softmax and epilogue (a thread owns a
 // TMEM lane: warp w reads lanes 32 (w % 4) on). m is 6 below a row maximum and raised lazily, when p would
@@ -60,7 +61,7 @@ struct Smem {
     static constexpr uint32_t rs = full + 16;               // float [256]: scale of a row's scores
     static constexpr uint32_t bars = rs + 256 * 4;
     static constexpr uint32_t misc = bars + 24 * 8;
-    static constexpr uint32_t bytes = misc + 64;
+    static constexpr uint32_t bytes = misc + 96;
 };
 static_assert(Smem<128>::bytes <= 227 * 1024, "shared memory of one CTA");
 
@@ -86,6 +87,14 @@ __device__ __forceinline__ bool bar_try(uint64_t* b, uint32_t par) {
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void to_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// a barrier of n threads that tells each of them whether any passed true
+__device__ __forceinline__ bool any_of(int id, int n, bool x) {
+    uint32_t r;
+    asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %3, 0;\n bar.red.or.pred q, %1, %2, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+                 : "=r"(r) : "r"(id), "r"(n), "r"((uint32_t)x) : "memory");
+    return r != 0;
+}
 
 // K-major 128-row tile, 128-byte swizzle (8-row groups 1024 bytes apart)
 __device__ __forceinline__ uint64_t desc_k(uint32_t s) {
@@ -138,15 +147,22 @@ __device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.
 #undef R8
 #undef W8
 
-// (a0, a1) = (x0, x1) * s + b and (a0, a1) += (x0, x1), two float32 operations per instruction
-__device__ __forceinline__ void fma_pair(float& a0, float& a1, float x0, float x1, float s, float b) {
-    asm("{\n .reg .b64 x, s, b, d;\n mov.b64 x, {%2, %3};\n mov.b64 s, {%4, %4};\n mov.b64 b, {%5, %5};\n"
-        " fma.rn.f32x2 d, x, s, b;\n mov.b64 {%0, %1}, d;\n}\n"
-        : "=f"(a0), "=f"(a1) : "f"(x0), "f"(x1), "f"(s), "f"(b));
+// two float32 numbers in a register pair, for the instructions that work on both
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
+    return d;
 }
-__device__ __forceinline__ void add_pair(float& a0, float& a1, float x0, float x1) {
-    asm("{\n .reg .b64 x, a;\n mov.b64 x, {%2, %3};\n mov.b64 a, {%0, %1};\n add.rn.f32x2 a, a, x;\n mov.b64 {%0, %1}, a;\n}\n"
-        : "+f"(a0), "+f"(a1) : "f"(x0), "f"(x1));
+__device__ __forceinline__ void unpair(uint64_t d, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(d)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t s, uint64_t b) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(x), "l"(s), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+    return d;
 }
 
 template <bool BF>
@@ -190,16 +206,17 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a) 
     uint64_t* p_full = s_full + 2;                          // [2] 128: the softmax threads
     uint64_t* o_done = p_full + 2;                          // [2] 1: MMA commit after the unit's last product
     uint64_t* q_full = o_done + 2;                          // 256
-    // [kMeta] 4: a block's positions. Slot j % 3 is written again for block j + 3, whose K tile needs the
+    // [kMeta] a block's positions. Slot j % 3 is written again for block j + 3, whose K tile needs the
     // ring place of V tile j (five stages), freed after both halves' softmax of block j.
     uint64_t* meta_full = q_full + 1;
     int* misc = reinterpret_cast<int*>(sm + M::misc);
     volatile int* abort_f = misc;
     int* flag = misc + 1;
-    volatile int* redo_f = misc + 2;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 3);
-    float* s0 = reinterpret_cast<float*>(misc + 4);         // [2] E4M3: scale of the K and V tiles
-    float* wmax = reinterpret_cast<float*>(misc + 6);       // [kProdWarps][2]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 2);
+    // of the units with keys the producers may be ahead by three (a unit has two tiles at least): by unit % 4
+    volatile int* redo_f = misc + 4;                        // [4] the unit has to be redone
+    float* s0 = reinterpret_cast<float*>(misc + 8);         // [4][2] E4M3: scale of the K and V tiles
+    float* wmax = reinterpret_cast<float*>(misc + 16);      // [kProdWarps][2]
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (a.pdl) asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -217,7 +234,7 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a) 
         bar_init(q_full, 256);
         for (int i = 0; i < kMeta; ++i) bar_init(&meta_full[i], kProdWarps);
         *abort_f = 0;
-        *redo_f = 0;
+        for (int i = 0; i < 4; ++i) redo_f[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kMmaWarp) {
@@ -243,18 +260,23 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a) 
         return true;
     };
 
+    // Each role walks the CTA's units by itself; the barriers above keep them in step. Registers: three warpgroups
+    // of 168 a thread at launch, 504 = kRegsLow + 2 kRegsHigh.
+    constexpr int kRegsLow = F8 ? 120 : 88, kRegsHigh = F8 ? 192 : 208;
+    static_assert(kRegsLow + 2 * kRegsHigh <= 3 * 168, "registers of the launch");
     Ring ring;
     MetaAt meta;
-    uint32_t q_ph = 0, o_ph = 0, sp_ph[2] = {0u, 0u};
-    int produced = 0;                                       // ring places filled (up to all of them)
-
-    for (int ui = ui0; ui < ui1; ++ui) {
-        const AttnUnit u = load_unit(a.units2 + ui);
-        const int kvh = u.head;
-        const int nt = (u.v1 - u.v0 + kKeys - 1) / kKeys;
-        const int halves = u.n_row > 128 ? 2 : 1;
-
+    if (warp < kSoft0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
         if (warp < kProdWarps) {
+        int produced = 0, with_keys = 0;                    // ring places filled (up to all of them); units with keys
+        bool ok = true;
+        for (int ui = ui0; ui < ui1 && ok; ++ui) {
+            const AttnUnit u = load_unit(a.units2 + ui);
+            const int kvh = u.head;
+            const int nt = (u.v1 - u.v0 + kKeys - 1) / kKeys;
+            if (nt == 0) continue;
+            const int slot = with_keys++ & 3;
             // ---- K and V tiles
             const uint8_t* kb = a.kv.k + (int64_t)kvh * a.kv.sb_head;
             const uint8_t* vb = a.kv.v + (int64_t)kvh * a.kv.sb_head;
@@ -293,9 +315,9 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a) 
                 }
             };
             auto claim = [&]() { return produced < kStages || wait(&kv_empty[ring.s], ring.ph ^ 1u); };
-            if (nt > 0) lookup(cur, 0);
+            lookup(cur, 0);
             float ik = 1.f, iv = 1.f;
-            if (F8 && nt > 0) {
+            if constexpr (F8) {
                 // s0 of this unit: the largest scales of its first block
                 float mk = 0.f, mv = 0.f;
 #pragma unroll
@@ -306,12 +328,12 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a) 
                     mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
                 }
                 if (lane == 0) { wmax[2 * warp] = mk; wmax[2 * warp + 1] = mv; }
-                asm volatile("bar.sync 1, %0;" ::"n"(32 * kProdWarps) : "memory");
+                asm volatile("bar.sync 4, %0;" ::"n"(32 * kProdWarps) : "memory");
 #pragma unroll
                 for (int i = 0; i < kProdWarps; ++i) { mk = fmaxf(mk, wmax[2 * i]); mv = fmaxf(mv, wmax[2 * i + 1]); }
                 if (!(mk > 0.f)) mk = 1.f;
                 if (!(mv > 0.f)) mv = 1.f;
-                if (tid == 0) { s0[0] = mk; s0[1] = mv; }
+                if (tid == 0) { s0[2 * slot] = mk; s0[2 * slot + 1] = mv; }
                 ik = 1.f / mk;
                 iv = 1.f / mv;
             }
@@ -323,7 +345,6 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a) 
                 __syncwarp();
                 if (lane == 0) bar_arrive(&kv_full[s]);
             };
-            bool ok = true;
             for (int j = 0; j < nt && ok; ++j) {
                 for (int kvi = 0; kvi < 2; ++kvi) {
                     const uint8_t* base = kvi ? vb : kb;
@@ -342,7 +363,7 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a) 
 #pragma unroll
                         for (int i = 0; i < kGroups; ++i) {
                             f[i] = kvi ? cur[i].vs * iv : cur[i].ks * ik;
-                            if (cur[i].off >= 0 && !(f[i] <= 128.f)) *redo_f = 1;
+                            if (cur[i].off >= 0 && !(f[i] <= 128.f)) redo_f[slot] = 1;
                         }
                         if (kvi == 1 && j + 1 < nt) lookup(nxt, j + 1);
                         if (!__all_sync(0xffffffffu, claim())) { ok = false; break; }
@@ -412,11 +433,19 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a) 
                 asm volatile("cp.async.wait_group 0;" ::: "memory");
                 for (int i = 0; i < n_pend; ++i) announce(pend[i]);
             }
-        } else if (warp == kMmaWarp) {
+            ok = !any_of(4, 32 * kProdWarps, !ok);          // both warps go on, or neither; wmax is free again
+        }
+        } else if (warp == kMmaWarp && lane == 0) {
             // ---- MMA issuer
-            if (lane == 0) {
-                constexpr uint32_t ids = idesc(BF, 128, kKeys, false), ido = idesc(BF, 128, HD, true);
-                bool ok = wait(q_full, q_ph);
+            constexpr uint32_t ids = idesc(BF, 128, kKeys, false), ido = idesc(BF, 128, HD, true);
+            uint32_t q_ph = 0, p_ph[2] = {0u, 0u};
+            bool ok = true;
+            for (int ui = ui0; ui < ui1 && ok; ++ui) {
+                const AttnUnit u = load_unit(a.units2 + ui);
+                const int nt = (u.v1 - u.v0 + kKeys - 1) / kKeys, halves = u.n_row > 128 ? 2 : 1;
+                if (nt == 0) continue;
+                ok = wait(q_full, q_ph);
+                q_ph ^= 1u;
                 auto scores = [&](int t, uint32_t stage) {
                     const uint32_t qa = sa(sm + M::q + t * M::tile), ka = sa(sm + M::kv + stage * M::tile);
 #pragma unroll
@@ -425,14 +454,12 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a) 
                                desc_k(ka + (kk >> 2) * kBlk) + (uint64_t)(2 * (kk & 3)), ids, kk > 0);
                     commit(&s_full[t]);
                 };
-                if (ok && nt > 0) {
-                    ok = wait(&kv_full[ring.s], ring.ph);
-                    if (ok) {
-                        tc_after();
-                        for (int t = 0; t < halves; ++t) scores(t, ring.s);
-                        commit(&kv_empty[ring.s]);
-                        ring.next();
-                    }
+                ok = ok && wait(&kv_full[ring.s], ring.ph);
+                if (ok) {
+                    tc_after();
+                    for (int t = 0; t < halves; ++t) scores(t, ring.s);
+                    commit(&kv_empty[ring.s]);
+                    ring.next();
                 }
                 for (int j = 0; j < nt && ok; ++j) {
                     const Ring rv = ring;
@@ -442,8 +469,8 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a) 
                     if (!(ok = wait(&kv_full[rv.s], rv.ph))) break;
                     const uint32_t va = sa(sm + M::kv + rv.s * M::tile);
                     for (int t = 0; t < halves; ++t) {
-                        if (!(ok = wait(&p_full[t], sp_ph[t]))) break;
-                        sp_ph[t] ^= 1u;
+                        if (!(ok = wait(&p_full[t], p_ph[t]))) break;
+                        p_ph[t] ^= 1u;
                         tc_after();
 #pragma unroll
                         for (int kk = 0; kk < kKeys / 16; ++kk)
@@ -465,12 +492,22 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a) 
                     }
                 }
             }
-            __syncwarp();
-        } else if (warp >= kSoft0) {
-            // ---- the two halves: Q tile, softmax, epilogue
-            const int t = warp >= kSoft0 + 4 ? 1 : 0;
-            const int ht = tid - 32 * (kSoft0 + 4 * t);     // thread of the half
-            {
+        }
+        __syncwarp();
+    } else {
+        // ---- the two halves: Q tile, softmax, epilogue
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsHigh));
+        const int t = warp >= kSoft0 + 4 ? 1 : 0;
+        const int ht = tid - 32 * (kSoft0 + 4 * t);         // thread of the half
+        uint32_t s_ph = 0, o_ph = 0;
+        int with_keys = 0;
+        for (int ui = ui0; ui < ui1; ++ui) {
+            const AttnUnit u = load_unit(a.units2 + ui);
+            const int kvh = u.head;
+            const int nt = (u.v1 - u.v0 + kKeys - 1) / kKeys, halves = u.n_row > 128 ? 2 : 1;
+            const int slot = with_keys & 3;
+            if (nt > 0) ++with_keys;
+            if (nt > 0) {
                 // neighbouring threads hold a row: 8 values each
                 uint8_t* qs = sm + M::q + t * M::tile;
                 for (int x = ht; x < 128 * CH; x += 128) {
@@ -520,49 +557,52 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a) 
             const int tok = row_token(a, u, row);
             const int rp = row_pos(a, u, row, tok), rh = hidden_below(a, rp);
             const int wp_min = __reduce_min_sync(0xffffffffu, rp), wh_max = __reduce_max_sync(0xffffffffu, rh);
-            float rs = rs_s[128 * t + r];
+            float rs = nt > 0 ? rs_s[128 * t + r] : 0.f;
             float m = -INFINITY, l = 0.f;
             bool live = t < halves;
             for (int j = 0; j < nt && live; ++j) {
-                const bool got = wait(&meta_full[meta.s], meta.ph) && wait(&s_full[t], sp_ph[t]);
+                const bool got = wait(&meta_full[meta.s], meta.ph) && wait(&s_full[t], s_ph);
                 if (!__all_sync(0xffffffffu, got)) { live = false; break; }
                 tc_after();
-                sp_ph[t] ^= 1u;
-                if (F8 && j == 0) rs *= s0[0];
+                s_ph ^= 1u;
+                if (F8 && j == 0) rs *= s0[2 * slot];
                 const int* kp = kpos + meta.s * kKeys;
                 const int4* kp4 = reinterpret_cast<const int4*>(kp);
                 const bool open = *reinterpret_cast<const uint32_t*>(full + meta.s * 4) == 0x01010101u &&
                                   kp[kKeys - 1] <= wp_min && (kp[0] > wh_max || kp[kKeys - 1] < a.n_sink);
-                auto mask = [&](uint32_t* v, int c0, int n) {
-                    if (open) return;
+                if (!open) {
+                    // some row does not see some key: -inf over those scores, in TMEM (few blocks do this; the code
+                    // of the others stays short enough for the instruction cache)
+#pragma unroll 1
+                    for (int c = 0; c < kKeys; c += 32) {
+                        uint32_t x[32];
+                        tld32(sb + c, x);
+                        ld_wait();
 #pragma unroll
-                    for (int c = 0; c < n; c += 4) {
-                        const int4 k = kp4[(c0 + c) / 4];
-                        if (!sees(k.x, rp, rh, a.n_sink)) v[c] = __float_as_uint(-INFINITY);
-                        if (!sees(k.y, rp, rh, a.n_sink)) v[c + 1] = __float_as_uint(-INFINITY);
-                        if (!sees(k.z, rp, rh, a.n_sink)) v[c + 2] = __float_as_uint(-INFINITY);
-                        if (!sees(k.w, rp, rh, a.n_sink)) v[c + 3] = __float_as_uint(-INFINITY);
+                        for (int i = 0; i < 32; i += 4) {
+                            const int4 k = kp4[(c + i) / 4];
+                            if (!sees(k.x, rp, rh, a.n_sink)) x[i] = __float_as_uint(-INFINITY);
+                            if (!sees(k.y, rp, rh, a.n_sink)) x[i + 1] = __float_as_uint(-INFINITY);
+                            if (!sees(k.z, rp, rh, a.n_sink)) x[i + 2] = __float_as_uint(-INFINITY);
+                            if (!sees(k.w, rp, rh, a.n_sink)) x[i + 3] = __float_as_uint(-INFINITY);
+                        }
+                        tst32(sb + c, x);
                     }
-                };
-                auto top = [&](const uint32_t* v, int n, float mx) {
-#pragma unroll
-                    for (int c = 0; c < n; c += 4)
-                        mx = fmaxf(fmaxf(fmaxf(mx, __uint_as_float(v[c])), __uint_as_float(v[c + 1])),
-                                   fmaxf(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3])));
-                    return mx;
-                };
-                // the row's largest score: columns 0-63 are read again below (P overwrites 64-127 only)
-                uint32_t v[64];
+                    st_wait();
+                }
+                uint32_t v[64], w[64];                      // the row's scores
                 tld32(sb, v);
                 tld32(sb + 32, v + 32);
+                tld32(sb + 64, w);
+                tld32(sb + 96, w + 32);
                 ld_wait();
-                mask(v, 0, 64);
-                float mx = top(v, 64, -INFINITY);
-                tld32(sb + 64, v);
-                tld32(sb + 96, v + 32);
-                ld_wait();
-                mask(v, 64, 64);
-                mx = top(v, 64, mx) * rs;
+                float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < 64; c += 2) {
+                    t0 = fmaxf(fmaxf(t0, __uint_as_float(v[c])), __uint_as_float(v[c + 1]));
+                    t1 = fmaxf(fmaxf(t1, __uint_as_float(w[c])), __uint_as_float(w[c + 1]));
+                }
+                const float mx = fmaxf(t0, t1) * rs;
                 float f = 1.f;
                 bool up = false;
                 if (mx > m + 14.f) {
@@ -571,29 +611,28 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a) 
                     l *= f;
                     up = true;
                 }
-                const float bias = m == -INFINITY ? 0.f : -m;   // nothing seen: every score is -inf
-                float l0 = 0.f, l1 = 0.f;
-                auto powers = [&](uint32_t* x, uint32_t* p) {   // 64 scores to 32 words of P
+                // nothing seen: every score is -inf
+                const uint64_t rs2 = pair(rs, rs), bias2 = m == -INFINITY ? 0ull : pair(-m, -m);
+                uint64_t sum = 0ull;
+                auto powers = [&](uint32_t* x) {            // 64 scores to 32 words of P
 #pragma unroll
                     for (int c = 0; c < 64; c += 2) {
                         float p0, p1;
-                        fma_pair(p0, p1, __uint_as_float(x[c]), __uint_as_float(x[c + 1]), rs, bias);
+                        unpair(fma2(pair(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), rs2, bias2), p0, p1);
                         p0 = ex2(p0);
                         p1 = ex2(p1);
-                        add_pair(l0, l1, p0, p1);
-                        p[c / 2] = pack<BF>(p0, p1);
+                        sum = add2(sum, pair(p0, p1));
+                        x[c / 2] = pack<BF>(p0, p1);
                     }
                 };
-                powers(v, v);
-                tst32(sb + 96, v);
-                uint32_t w[64];
-                tld32(sb, w);
-                tld32(sb + 32, w + 32);
-                ld_wait();
-                mask(w, 0, 64);
-                powers(w, w);
-                tst32(sb + 64, w);
-                l += l0 + l1;
+                // P over S's second half, which has been read
+                powers(v);
+                tst32(sb + 64, v);
+                powers(w);
+                tst32(sb + 96, w);
+                float s0f, s1f;
+                unpair(sum, s0f, s1f);
+                l += s0f + s1f;
                 // O is complete up to the block before (its products precede these scores)
                 if (j > 0 && __any_sync(0xffffffffu, up)) {
 #pragma unroll 1
@@ -621,7 +660,7 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a) 
             // ---- epilogue: a unit alone writes its rows, one of several its partial result
             if (live) {
                 bool finite = l <= 3.0e38f && m <= 3.0e38f;
-                const float inv = l == 0.f ? 0.f : 1.f / l, sv = F8 && nt > 0 ? s0[1] : 1.f;
+                const float inv = l == 0.f ? 0.f : 1.f / l, sv = F8 && nt > 0 ? s0[2 * slot + 1] : 1.f;
                 const int64_t at = (int64_t)(u.part + u.chunk) * kUnitRows2 + 128 * t + r;
                 const int64_t oi = (int64_t)tok * a.o_tok + (int64_t)(kvh * a.G + row % a.G) * a.o_head;
                 if (u.n_chunk > 1 && mine) a.part_ml[at] = make_float2(m, l);
@@ -646,35 +685,39 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a) 
                         else *reinterpret_cast<float4*>(a.part_o + at * HD + c + i) = make_float4(x[0], x[1], x[2], x[3]);
                     }
                 }
-                if (!finite && mine) *redo_f = 1;
+                if (!finite && mine) redo_f[slot] = 1;
             }
             tc_before();
-        }
-        q_ph ^= 1u;
-        __syncthreads();
-        tc_after();
-        if (*abort_f) break;
-        if (*redo_f) {
-            // not every operand was finite (or an E4M3 row outgrew s0): the rows again, key by key
-            for (int r = warp; r < u.n_row; r += kThr / 32) {
-                float o[HD / 32], rm, rl;
-                const int row = u.row0 + r, tok = row_token(a, u, row);
-                careful_row<HD>(a, u, kvh, row, o, rm, rl);
-                const int64_t at = (int64_t)(u.part + u.chunk) * kUnitRows2 + r;
-                const int64_t oi = (int64_t)tok * a.o_tok + (int64_t)(kvh * a.G + row % a.G) * a.o_head;
-                const float inv = rl == 0.f ? 0.f : 1.f / rl;
+            // the unit is written (all softmax warps agree on whether to go on: a wait that gave up ends every role)
+            if (any_of(1, 256, *abort_f != 0)) break;
+            if (nt > 0 && redo_f[slot]) {
+                // not every operand was finite (or an E4M3 row outgrew s0): the rows again, key by key
+                for (int x = warp - kSoft0; x < u.n_row; x += 8) {
+                    float o[HD / 32], rm, rl;
+                    const int xrow = u.row0 + x, xtok = row_token(a, u, xrow);
+                    careful_row<HD>(a, u, kvh, xrow, o, rm, rl);
+                    const int64_t at = (int64_t)(u.part + u.chunk) * kUnitRows2 + x;
+                    const int64_t oi = (int64_t)xtok * a.o_tok + (int64_t)(kvh * a.G + xrow % a.G) * a.o_head;
+                    const float inv = rl == 0.f ? 0.f : 1.f / rl;
 #pragma unroll
-                for (int d = 0; d < HD / 32; ++d) {
-                    if (u.n_chunk == 1) store_out1(a, oi + lane * (HD / 32) + d, rl == 0.f ? 0.f : o[d] * inv);
-                    else a.part_o[at * HD + lane * (HD / 32) + d] = o[d];
+                    for (int d = 0; d < HD / 32; ++d) {
+                        if (u.n_chunk == 1) store_out1(a, oi + lane * (HD / 32) + d, rl == 0.f ? 0.f : o[d] * inv);
+                        else a.part_o[at * HD + lane * (HD / 32) + d] = o[d];
+                    }
+                    if (u.n_chunk > 1 && lane == 0) a.part_ml[at] = make_float2(rm, rl);
                 }
-                if (u.n_chunk > 1 && lane == 0) a.part_ml[at] = make_float2(rm, rl);
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                if (ht == 0 && t == 0) redo_f[slot] = 0;
             }
-            __syncthreads();
-            if (tid == 0) *redo_f = 0;
+            if (u.n_chunk > 1) {
+                __threadfence();
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                if (tid == 32 * kSoft0) *flag = count_unit(a, u);
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                if (*flag) merge_parts<HD>(a, u, kUnitRows2, tid - 32 * kSoft0, 256);
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+            }
         }
-        if (u.n_chunk > 1 && last_of_tile(a, u, flag)) merge_parts<HD>(a, u, kUnitRows2);
-        __syncthreads();
     }
     __syncthreads();
     if (warp == kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
