@@ -131,6 +131,32 @@ def test_chunks(L, act, cdt, hd, n_new, n_kv, window, n_sink):
     check(L, act, cdt, hd, 2, 4, 16, n_new, n_kv, window, n_sink, seed=hd + 1)
 
 
+@pytest.mark.parametrize("page", [1, 8, 16, 24, 64, 128, 200])
+@pytest.mark.parametrize("order", ["pchd", "phcd", "hpcd"])
+@pytest.mark.parametrize("hd,Hkv", [(64, 2), (128, 1)])
+def test_chunks_over_runs_of_cells(L, page, order, hd, Hkv):
+    """Chunks whose key blocks are whole runs of cells, partly so, and not at all."""
+    check(L, torch.float16, torch.float16, hd, Hkv, 4, page, [40, 70], [40, 900], order=order, seed=page)
+    check(L, torch.bfloat16, torch.bfloat16, hd, Hkv, 4, page, [150], [1300], 500, 5, order=order, seed=page + 1)
+
+
+def test_chunks_over_pages_in_order(L):
+    """A cache whose pages follow each other: runs go on from page to page, as in a cache of single cells."""
+    for page in (1, 16):
+        n = 700
+        (k, _, kv_), (v, _, vv) = O.cache(-(-n // page) + 9, page, 2, 128, torch.float16, 3)
+        pages = L.KvPages(k, v)
+        q = torch.randn(60, 8, 128, device="cuda", dtype=torch.float16)
+        out = torch.zeros_like(q)
+        table = (np.arange(-(-n // page)) + 4)[None]
+        plan = L.AttnPlan(pages, 8, torch.float16, 60, 1, table.size)
+        plan.set([60], [n], table)
+        plan.run(q, pages, out)
+        ref, mag, smag = O.attention(q.double().cpu().numpy(), kv_, vv, table, [60], [n], page)
+        tol = O.attention_tol(ref, mag, smag, torch.float16, n, 128, np.abs(vv).max())
+        assert (np.abs(out.double().cpu().numpy() - ref) <= tol).all()
+
+
 @pytest.mark.parametrize("n_new", [1, 100])
 @pytest.mark.parametrize("act,cdt", [PAIRS[0], PAIRS[1], PAIRS[4]])
 def test_non_finite_rows_reach_only_the_tokens_that_see_them(L, act, cdt, n_new):

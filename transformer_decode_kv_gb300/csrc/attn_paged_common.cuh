@@ -41,9 +41,9 @@ __device__ __forceinline__ void e4m3x4_to_h2(uint32_t four, uint32_t& lo, uint32
         : "=r"(lo), "=r"(hi) : "r"(four));
 }
 
-// A key of a unit: its cell as byte and scale offsets (without the head), its position. off < 0: a cell
+// A key of a unit: its cell as byte and scale offsets (without the head) and number, its position. off < 0: a cell
 // outside the cache.
-struct KeyAt { int64_t off, soff; int pos; };
+struct KeyAt { int64_t off, soff; int pos, cell; };
 
 __device__ __forceinline__ KeyAt key_at(const AttnPagedArgs& a, const AttnUnit& u, int v) {
     const int j = v < u.n_sink_keys ? v : v - u.n_sink_keys + u.key_lo;
@@ -56,6 +56,7 @@ __device__ __forceinline__ KeyAt key_at(const AttnPagedArgs& a, const AttnUnit& 
     const int page = a.table[u.table + pg];
     KeyAt k;
     k.pos = a.key_pos ? a.key_pos[u.table + j] : j;
+    k.cell = page * ps + at;
     if ((unsigned)page >= (unsigned)a.kv.n_pages) {
         if (a.err) atomicOr(a.err, ERR_SLOT_RANGE);
         k.off = k.soff = -1;

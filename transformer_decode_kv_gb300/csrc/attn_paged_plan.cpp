@@ -18,10 +18,14 @@ constexpr int64_t kTcRows = 64;
 
 int64_t ctas(const PlanShape& s, int f) { return (int64_t)s.n_sm * (f ? 1 : kAttnRowsCtas); }
 
+int64_t up_to(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+
 // The virtual key range of the rows [row0, row0 + n) of a sequence: sink keys, then [lo, hi).
 struct Keys { int32_t n_sink, lo, n; };
 
-Keys tile_keys(const PlanShape& s, const PlanSeq& q, int64_t row0, int64_t n) {
+// align > 1: both parts begin and end (the sinks) at multiples of it, so that blocks of keys are whole runs of a
+// page's cells; the keys that come in by this are hidden from every row.
+Keys tile_keys(const PlanShape& s, const PlanSeq& q, int64_t row0, int64_t n, int64_t align) {
     const int64_t t0 = row0 / s.G, t1 = (row0 + n - 1) / s.G;
     int64_t pmin = (int64_t)q.p0 + t0, pmax = (int64_t)q.p0 + t1;
     if (q.tok_pos) {
@@ -43,8 +47,8 @@ Keys tile_keys(const PlanShape& s, const PlanSeq& q, int64_t row0, int64_t n) {
         k.n = (int32_t)hi;
         return k;
     }
-    const int64_t lo = std::min(hi, first(pmin - s.window + 1));
-    k.n_sink = (int32_t)std::min(lo, first(s.n_sink));
+    const int64_t lo = std::min(hi, first(pmin - s.window + 1)) / align * align;
+    k.n_sink = (int32_t)std::min(lo, up_to(first(s.n_sink), align));
     k.lo = (int32_t)lo;
     k.n = (int32_t)(k.n_sink + hi - lo);
     return k;
@@ -59,6 +63,8 @@ void build_paged_plan(const PlanShape& s, const std::vector<PlanSeq>& seqs, Page
     plan.rows1 = 8;
     for (const PlanSeq& q : seqs)
         if (!tc(q) && (int64_t)q.n_new * s.G > 8) plan.rows1 = 16;
+    int64_t align = 64;
+    while (align > 1 && s.page_size % align) align /= 2;
     struct Tile { int32_t seq, row0, n_row; Keys keys; };
     std::vector<Tile> tiles[2];
     int64_t total[2] = {0, 0};
@@ -68,7 +74,7 @@ void build_paged_plan(const PlanShape& s, const std::vector<PlanSeq>& seqs, Page
         const int64_t step = f ? kUnitRows2 : plan.rows1;
         for (int64_t r = 0; r < rows; r += step) {
             Tile t{(int32_t)i, (int32_t)r, (int32_t)std::min(step, rows - r), {}};
-            t.keys = tile_keys(s, seqs[i], t.row0, t.n_row);
+            t.keys = tile_keys(s, seqs[i], t.row0, t.n_row, f && !seqs[i].key_pos ? align : 1);
             const int64_t bk = block_keys(s, f, plan.rows1);
             total[f] += (t.keys.n + bk - 1) / bk + kUnitCost[f];
             tiles[f].push_back(t);

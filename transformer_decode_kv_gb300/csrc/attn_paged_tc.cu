@@ -15,8 +15,9 @@
 // the same columns, and a completed S means that every product before it is complete too.
 //
 // Roles (12 warps; warps 0-3 give registers to warps 4-11, whose threads hold a row of scores each): warps
-// 0-1 bring K and V rows cell by cell into a ring of 128-byte-swizzled tiles
-// (16-byte asynchronous copies; E4M3 rows through registers, converted to f16), with the keys' positions;
+// 0-1 bring K and V rows into a ring of 128-byte-swizzled tiles, with the keys' positions: bulk tensor copies of
+// the runs of neighbouring cells that pages are (64 keys of a warp at a time, when all of them are read),
+// otherwise 16-byte asynchronous copies row by row, and E4M3 rows through registers, converted to f16;
 // warp 2 issues the MMAs; warps 4-7 and 8-11 are the two halves' softmax and epilogue (a thread owns a
 // TMEM lane: warp w reads lanes 32 (w % 4) on). m is 6 below a row maximum and raised lazily, when p would
 // pass 2^14: O, in TMEM, is rarely rescaled, and never more than it must. P is rounded to f16 (half a step 2^-11)
@@ -30,6 +31,9 @@
 // Every wait is bounded by a wall-clock limit; a timeout sets ERR_TIMEOUT, ends every role's loop, and
 // the CTA leaves after its copies and with its TMEM freed.
 #include "attn_paged_common.cuh"
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
 
 #include <algorithm>
 
@@ -58,7 +62,8 @@ struct Smem {
     static constexpr uint32_t kv = q + 2 * tile;            // [kStages] tiles
     static constexpr uint32_t kpos = kv + kStages * tile;   // int [kMeta][kKeys]
     static constexpr uint32_t full = kpos + kMeta * kKeys * 4;   // uint8 [kMeta][4]
-    static constexpr uint32_t rs = full + 16;               // float [256]: scale of a row's scores
+    static constexpr uint32_t rs = full + 16;               // E4M3: float [256], scale of a row's scores; 16-bit
+                                                            // caches: int64 [128], offsets of a block's rows
     static constexpr uint32_t bars = rs + 256 * 4;
     static constexpr uint32_t misc = bars + 24 * 8;
     static constexpr uint32_t bytes = misc + 96;
@@ -181,6 +186,10 @@ __device__ __forceinline__ uint32_t swz(int r, int ch) {
     return (uint32_t)((ch >> 3) * kBlk + r * 128 + ((((uint32_t)ch & 7u) ^ ((uint32_t)r & 7u)) << 4));
 }
 
+// How bulk tensor copies find a cell: maps of K and V as [page][head][cell][dim] (one page of all cells where
+// the pages follow each other evenly), in boxes of `rows` cells x 64 dims (rows = 0: none).
+struct TmaRuns { int rows, page_cells; };
+
 struct Ring {                                              // position in the ring of K and V tiles
     uint32_t s = 0, ph = 0;
     __device__ __forceinline__ void next() { if (++s == kStages) { s = 0; ph ^= 1u; } }
@@ -191,7 +200,9 @@ struct MetaAt {
 };
 
 template <int HD, int CT, int QT>
-__global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a) {
+__global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, TmaRuns runs,
+                                                               const __grid_constant__ CUtensorMap map_k,
+                                                               const __grid_constant__ CUtensorMap map_v) {
     using M = Smem<HD>;
     constexpr bool F8 = CT == W_F8, BF = CT == W_BF16;
     constexpr int CH = HD / 8;                              // 16-byte chunks of a 16-bit row
@@ -271,6 +282,9 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a) 
         if (warp < kProdWarps) {
         int produced = 0, with_keys = 0;                    // ring places filled (up to all of them); units with keys
         bool ok = true;
+        int bulk_at[kStages];                               // phase of a stage's last bulk copies, -1: none
+#pragma unroll
+        for (int i = 0; i < kStages; ++i) bulk_at[i] = -1;
         for (int ui = ui0; ui < ui1 && ok; ++ui) {
             const AttnUnit u = load_unit(a.units2 + ui);
             const int kvh = u.head;
@@ -294,8 +308,8 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a) 
                 }
             }
             const int hid_all = hidden_below(a, pmin);
-            struct Key { int64_t off; int pos; float ks, vs; };
-            const Key none{-1, INT_MAX, 0.f, 0.f};
+            struct Key { int64_t off; int pos, cell; float ks, vs; };
+            const Key none{-1, INT_MAX, 0, 0.f, 0.f};
             Key cur[kGroups], nxt[kGroups];                  // key 32 (kGroups warp + i) + lane of a block
             auto lookup = [&](Key* k, int j) {
 #pragma unroll
@@ -307,6 +321,7 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a) 
                     if (at.off >= 0 && sees(at.pos, pmax, hid_all, a.n_sink)) {
                         k[i].off = at.off;
                         k[i].pos = at.pos;
+                        k[i].cell = at.cell;
                         if constexpr (F8) {
                             k[i].ks = a.kv.ks[at.soff + (int64_t)kvh * a.kv.ss_head];
                             k[i].vs = a.kv.vs[at.soff + (int64_t)kvh * a.kv.ss_head];
@@ -337,6 +352,9 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a) 
                 ik = 1.f / mk;
                 iv = 1.f / mv;
             }
+            uint32_t read[kGroups];                         // which of a group's keys are read
+            bool bulk = false;                              // this warp's keys of the block come by bulk copies
+            constexpr int kOwn = 32 * kGroups;              // keys of a block this warp brings
             // 16-bit tiles: asynchronous copies, announced two tiles later, when they have landed
             uint32_t pend[2];
             int n_pend = 0;
@@ -386,17 +404,77 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a) 
                     } else {
                         if (!__all_sync(0xffffffffu, claim())) { ok = false; break; }
                         constexpr int RI = 32 / CH;         // rows per instruction
-                        const int ch = lane % CH;
+                        const int ch = lane % CH, r0 = lane / CH, own = kOwn * warp;
+                        // this warp's part: the rows' offsets, or their cells' numbers
+                        int64_t* offs = reinterpret_cast<int64_t*>(sm + M::rs) + kOwn * warp;
+                        int* cells = reinterpret_cast<int*>(offs);
+                        if (kvi == 0) {
+                            bool run = runs.rows > 0;
 #pragma unroll
-                        for (int x = 0; x < kGroups * 32 / RI; ++x) {
-                            const int r = x * RI % 32 + lane / CH;
-                            const int64_t off = __shfl_sync(0xffffffffu, cur[x * RI / 32].off, r);
-                            const uint8_t* src = base + (off >= 0 ? off : 0) + 16 * ch;
-                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                                             sa(dst) + swz(32 * (kGroups * warp + x * RI / 32) + r, ch)),
-                                         "l"(src), "r"(off >= 0 ? 16 : 0) : "memory");
+                            for (int i = 0; i < kGroups; ++i) {
+                                read[i] = __ballot_sync(0xffffffffu, cur[i].off >= 0);
+                                // a run of runs.rows keys lies in neighbouring cells of a page
+                                const int prev = __shfl_up_sync(0xffffffffu, cur[i].cell, 1);
+                                const int last = __shfl_sync(0xffffffffu, cur[i > 0 ? i - 1 : 0].cell, 31);
+                                const bool starts = ((32 * i + lane) & (runs.rows - 1)) == 0;
+                                run = run && read[i] == 0xffffffffu &&
+                                      (starts ? cur[i].cell % runs.page_cells + runs.rows <= runs.page_cells
+                                              : cur[i].cell == (lane > 0 ? prev : last) + 1);
+                            }
+                            bulk = __all_sync(0xffffffffu, run);
+                            __syncwarp();                   // the last block's have been read
+#pragma unroll
+                            for (int i = 0; i < kGroups; ++i) {
+                                if (bulk) cells[32 * i + lane] = cur[i].cell;
+                                else offs[32 * i + lane] = cur[i].off >= 0 ? cur[i].off : 0;
+                            }
+                            __syncwarp();
+                        }
+                        if (bulk) {
+                            if (n_pend > 0) {               // row copies of earlier blocks are announced first
+                                asm volatile("cp.async.wait_group 0;" ::: "memory");
+                                for (int i = 0; i < n_pend; ++i) announce(pend[i]);
+                                n_pend = 0;
+                            }
+                            const uint32_t fb = sa(&kv_full[ring.s]);
+                            if (lane == 0)
+                                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(fb),
+                                             "r"(kOwn * HD * 2) : "memory");
+                            __syncwarp();
+                            constexpr int HB = HD / 64;     // boxes of 64 dims
+#pragma unroll 1
+                            for (int x = lane; x < kOwn / runs.rows * HB; x += 32) {
+                                const int k = x / HB * runs.rows, h = x % HB, cell = cells[k];
+                                const int page = cell / runs.page_cells, at = cell - page * runs.page_cells;
+                                asm volatile(
+                                    "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+                                    " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(sa(dst) + h * kBlk + (kOwn * warp + k) * 128),
+                                    "l"(reinterpret_cast<uint64_t>(kvi ? &map_v : &map_k)), "r"(fb), "r"(64 * h), "r"(at),
+                                    "r"(kvh), "r"(page) : "memory");
+                            }
+                            bulk_at[ring.s] = (int)ring.ph;
+                        } else {
+                        const uint8_t* src = base + 16 * ch;
+                        bool all = true;
+#pragma unroll
+                        for (int i = 0; i < kGroups; ++i) all = all && read[i] == 0xffffffffu;
+                        if (all) {
+#pragma unroll 8
+                            for (int x = 0; x < 32 * kGroups / RI; ++x)
+                                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sa(dst) + swz(own + r0 + x * RI, ch)),
+                                             "l"(src + offs[r0 + x * RI]) : "memory");
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < kGroups; ++i)
+#pragma unroll 2
+                                for (int x = 0; x < 32 / RI; ++x) {
+                                    const int r = r0 + 32 * i + x * RI;
+                                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sa(dst) + swz(own + r, ch)),
+                                                 "l"(src + offs[r]), "r"(read[i] >> (r & 31) & 1u ? 16 : 0) : "memory");
+                                }
                         }
                         asm volatile("cp.async.commit_group;" ::: "memory");
+                        }
                     }
                     if (kvi == 0) {
 #pragma unroll
@@ -414,7 +492,9 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a) 
                         announce(ring.s);
                     } else {
                         if (kvi == 1 && j + 1 < nt) lookup(nxt, j + 1);
-                        if (n_pend == 2) {
+                        if (bulk) {
+                            // announced by the copies themselves
+                        } else if (n_pend == 2) {
                             asm volatile("cp.async.wait_group 2;" ::: "memory");
                             announce(pend[0]);
                             pend[0] = pend[1];
@@ -435,6 +515,12 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a) 
             }
             ok = !any_of(4, 32 * kProdWarps, !ok);          // both warps go on, or neither; wmax is free again
         }
+        // after a wait that gave up nobody may wait for the copies under way: they land before the CTA leaves
+        if (!ok)
+            for (int i = 0; i < kStages; ++i) {
+                const uint64_t t0 = now_ns();
+                while (bulk_at[i] >= 0 && !bar_try(&kv_full[i], (uint32_t)bulk_at[i]) && now_ns() - t0 < kWaitNs) {}
+            }
         } else if (warp == kMmaWarp && lane == 0) {
             // ---- MMA issuer
             constexpr uint32_t ids = idesc(BF, 128, kKeys, false), ido = idesc(BF, 128, HD, true);
@@ -542,7 +628,7 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a) 
 #pragma unroll
                         for (int i = 0; i < 4; ++i) v[i] ^= 0x80008000u;
                     *reinterpret_cast<uint4*>(qs + swz(r, ch)) = make_uint4(v[0], v[1], v[2], v[3]);
-                    if (ch == 0) rs_s[128 * t + r] = rs;
+                    if (F8 && ch == 0) rs_s[128 * t + r] = rs;
                 }
                 to_async_proxy();
                 // the rows' scales are read by other threads of the half
@@ -557,7 +643,7 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a) 
             const int tok = row_token(a, u, row);
             const int rp = row_pos(a, u, row, tok), rh = hidden_below(a, rp);
             const int wp_min = __reduce_min_sync(0xffffffffu, rp), wh_max = __reduce_max_sync(0xffffffffu, rh);
-            float rs = nt > 0 ? rs_s[128 * t + r] : 0.f;
+            float rs = F8 && nt > 0 ? rs_s[128 * t + r] : fabsf(a.scale_log2);
             float m = -INFINITY, l = 0.f;
             bool live = t < halves;
             for (int j = 0; j < nt && live; ++j) {
@@ -723,6 +809,45 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a) 
     if (warp == kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
 }
 
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        cudaDriverEntryPointQueryResult q;
+        void* p = nullptr;
+        const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+                        q == cudaDriverEntryPointSuccess;
+        return ok ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p) : nullptr;
+    }();
+    return fn;
+}
+
+// The maps of a 16-bit cache and the runs of cells they copy: up to 64 neighbouring cells of a page (a power of two
+// from 8 on that divides the page), any 64 where the pages follow each other evenly. No runs: row copies only.
+TmaRuns cell_runs(const PagedKv& kv, CUtensorMap* mk, CUtensorMap* mv) {
+    TmaRuns r{0, kv.page_size};
+    const bool even = kv.n_pages == 1 || kv.page_size == 1 || kv.sb_page == kv.page_size * kv.sb_cell;
+    const int64_t sb_cell = kv.page_size > 1 ? kv.sb_cell : kv.sb_page;
+    const int64_t cells = (int64_t)kv.page_size * kv.n_pages;
+    int rows = 64;
+    if (kv.page_size > 1)                                   // (pages of one cell: whatever neighbours there are)
+        while (rows >= 8 && kv.page_size % rows) rows /= 2;
+    if (rows < 8 || cells < rows) return r;
+    const uint64_t one = 2 * kv.hd;                         // a stride no copy uses
+    const cuuint64_t dims[4] = {(cuuint64_t)kv.hd, (cuuint64_t)(even ? cells : kv.page_size), (cuuint64_t)kv.Hkv,
+                                (cuuint64_t)(even ? 1 : kv.n_pages)};
+    const cuuint64_t strides[3] = {(cuuint64_t)sb_cell, kv.Hkv > 1 ? (cuuint64_t)kv.sb_head : one,
+                                   even ? one : (cuuint64_t)kv.sb_page};
+    const cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1}, es[4] = {1, 1, 1, 1};
+    const auto fn = encode_fn();
+    for (int i = 0; i < 2; ++i)
+        if (!fn || fn(i ? mv : mk, kv.type == W_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                      i ? kv.v : kv.k, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return r;
+    r.rows = rows;
+    if (even) r.page_cells = (int)cells;
+    return r;
+}
+
 template <int HD, int CT, int QT>
 bool go(const AttnPagedArgs& a, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
@@ -737,7 +862,10 @@ bool go(const AttnPagedArgs& a, cudaStream_t st) {
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = a.pdl ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, attn_tc_rows_kernel<HD, CT, QT>, a) == cudaSuccess;
+    CUtensorMap mk{}, mv{};
+    TmaRuns runs{0, 1};
+    if (CT != W_F8) runs = cell_runs(a.kv, &mk, &mv);
+    return cudaLaunchKernelEx(&cfg, attn_tc_rows_kernel<HD, CT, QT>, a, runs, mk, mv) == cudaSuccess;
 }
 template <int HD>
 bool go_hd(const AttnPagedArgs& a, cudaStream_t st) {

@@ -168,6 +168,7 @@ PlanShape plan_shape(const llm_attn_shape* s, const llm_kv_pages* kv, int32_t n_
     p.n_sm = n_sm;
     p.hd = kv->head_dim;
     p.kv_type = kv->type;
+    p.page_size = kv->page_size;
     p.tc = tc;
     return p;
 }

@@ -120,7 +120,7 @@ struct PlanSeq {
 };
 struct PlanShape {
     int32_t G = 1, Hkv = 1, window = 0, n_sink = 0, n_sm = 148;
-    int32_t hd = 128, kv_type = W_F16;
+    int32_t hd = 128, kv_type = W_F16, page_size = 1;
     bool tc = false;                             // 256-row tiles allowed
 };
 struct PlanForm {
