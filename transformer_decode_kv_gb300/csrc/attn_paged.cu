@@ -587,7 +587,8 @@ attn_rows_kernel(AttnPagedArgs a) {
             __syncthreads();
             if (threadIdx.x == 0) s_flag = count_unit(a, u);
             __syncthreads();
-            if (s_flag) merge_parts<HD>(a, u, ROWS, threadIdx.x, kThr);
+            if (s_flag)
+                for (int r = warp; r < u.n_row; r += kWarps) merge_row<HD>(a, u, ROWS, r);
         }
         __syncthreads();                                    // shared memory is free for the next unit
     }

@@ -173,32 +173,62 @@ __device__ __noinline__ void careful_row(const AttnPagedArgs& a, const AttnUnit&
     }
 }
 
-// The last unit of a tile to finish merges the partial results of all of them (in their order, so
-// the result does not depend on which unit was last). rows: the tile form's rows.
+// Merge the partial results of row r of a cut tile into the output, a warp per row; in the units' order, so the
+// result does not depend on which of them was last. rows: the tile form's rows. A lane weighs up to one unit in
+// 32 at a time (weight exp2(m - M) against the largest reference M), then the warp adds the units' rows, HD / 32
+// neighbouring values per lane.
 template <int HD>
-__device__ void merge_parts(const AttnPagedArgs& a, const AttnUnit& u, int rows, int tid, int n_threads) {
-    constexpr int Q = HD / 4;                                  // four dims per thread
-    for (int x = tid; x < u.n_row * Q; x += n_threads) {
-        const int r = x / Q, d = (x % Q) * 4;
-        float M = -INFINITY, L = 0.f, O[4] = {};
-        for (int c = 0; c < u.n_chunk; ++c)
-            M = fmaxf(M, __ldcg(&a.part_ml[(int64_t)(u.part + c) * rows + r]).x);
-        for (int c = 0; c < u.n_chunk; ++c) {
-            const int64_t at = (int64_t)(u.part + c) * rows + r;
-            const float2 ml = __ldcg(&a.part_ml[at]);
-            // a chunk without a visible key has nothing to add (its maximum is -inf); NaN sums pass
-            if (ml.x == -INFINITY && ml.y == 0.f) continue;
-            const float f = ml.x == M ? 1.f : exp2f(ml.x - M);
-            const float4 o = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * HD + d));
-            L += f * ml.y;
-            O[0] += f * o.x; O[1] += f * o.y; O[2] += f * o.z; O[3] += f * o.w;
-        }
-        const float inv = L == 0.f ? 0.f : 1.f / L;
+__device__ void merge_row(const AttnPagedArgs& a, const AttnUnit& u, int rows, int r) {
+    constexpr int D = HD / 32;
+    const int lane = threadIdx.x & 31;
+    float M = -INFINITY, L = 0.f, o[D];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) O[j] = L == 0.f ? 0.f : O[j] * inv;
-        const int row = u.row0 + r, tok = row_token(a, u, row);
-        store_out4(a, (int64_t)tok * a.o_tok + (int64_t)(u.head * a.G + row % a.G) * a.o_head + d, O);
+    for (int d = 0; d < D; ++d) o[d] = 0.f;
+    const float2* ml = a.part_ml + (int64_t)u.part * rows + r;
+    for (int c = lane; c < u.n_chunk; c += 32) M = fmaxf(M, __ldcg(&ml[(int64_t)c * rows]).x);
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
+    for (int c0 = 0; c0 < u.n_chunk; c0 += 32) {
+        float f = 0.f;
+        if (c0 + lane < u.n_chunk) {
+            const float2 x = __ldcg(&ml[(int64_t)(c0 + lane) * rows]);
+            // a unit without a visible key has nothing to add (its reference is -inf); NaN sums pass
+            if (x.x != -INFINITY || x.y != 0.f) {
+                f = x.x == M ? 1.f : exp2f(x.x - M);
+                L += f * x.y;
+            }
+        }
+        const int n = min(32, u.n_chunk - c0);
+        const float* p = a.part_o + ((int64_t)(u.part + c0) * rows + r) * HD + lane * D;
+#pragma unroll 4
+        for (int c = 0; c < n; ++c) {
+            const float fc = __shfl_sync(0xffffffffu, f, c);
+            const float* q = p + (int64_t)c * rows * HD;
+            float v[D];
+            if constexpr (D == 4) {
+                const float4 w = __ldcg(reinterpret_cast<const float4*>(q));
+                v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
+            } else if constexpr (D == 2) {
+                const float2 w = __ldcg(reinterpret_cast<const float2*>(q));
+                v[0] = w.x; v[1] = w.y;
+            } else {
+                v[0] = __ldcg(q);
+            }
+#pragma unroll
+            for (int d = 0; d < D; ++d) o[d] += fc != 0.f ? fc * v[d] : 0.f;
+        }
     }
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) L += __shfl_xor_sync(0xffffffffu, L, s);
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const int row = u.row0 + r, tok = row_token(a, u, row);
+    const int64_t at = (int64_t)tok * a.o_tok + (int64_t)(u.head * a.G + row % a.G) * a.o_head + lane * D;
+#pragma unroll
+    for (int d = 0; d < D; ++d) o[d] = L == 0.f ? 0.f : o[d] * inv;
+    if constexpr (D == 4) store_out4(a, at, o);
+    else
+#pragma unroll
+        for (int d = 0; d < D; ++d) store_out1(a, at + d, o[d]);
 }
 
 // Count a unit of a cut tile as finished, by one thread after a barrier behind the writes of its partial results

@@ -127,11 +127,11 @@ void build_paged_plan(const PlanShape& s, const std::vector<PlanSeq>& seqs, Page
                     for (size_t j = u0; j < pf.units.size(); ++j) {
                         pf.units[j].n_chunk = n;
                         pf.units[j].part = n > 1 ? pf.n_parts : 0;
-                        pf.units[j].ticket = n > 1 ? plan.n_tickets : 0;
+                        pf.units[j].ticket = n > 1 ? (int32_t)pf.cuts.size() : 0;
                     }
                     if (n > 1) {
                         pf.n_parts += n;
-                        ++plan.n_tickets;
+                        pf.cuts.push_back((int32_t)u0);
                     }
                 }
             i0 = i1;
@@ -151,7 +151,7 @@ PagedPlanCaps paged_plan_caps(const PlanShape& s, int32_t max_tok, int32_t max_s
     c.ctas2 = s.tc ? ctas(s, 1) : 0;
     c.units1 = t1 * s.Hkv + c.ctas1;
     c.units2 = t2 * s.Hkv + c.ctas2;
-    c.tickets = c.ctas1 + c.ctas2;
+    c.tickets = c.ctas1;
     c.parts1 = 2 * c.ctas1;
     c.parts2 = 2 * c.ctas2;
     return c;

@@ -247,7 +247,7 @@ struct llm_attn_plan {
     float scale_log2 = 0.f;
     PagedPlan plan;
     // device buffer: header, both forms' CTA starts, their units, page table; the pinned copy it is uploaded from
-    size_t off_first[2] = {0, 0}, off_units[2] = {0, 0}, off_table = 0, bytes = 0;
+    size_t off_first[2] = {0, 0}, off_cuts = 0, off_units[2] = {0, 0}, off_table = 0, bytes = 0;
     uint8_t *d_buf = nullptr, *h_buf = nullptr;
     float* part_o = nullptr;
     float2* part_ml = nullptr;
@@ -296,7 +296,8 @@ llm_attn_plan* llm_attn_plan_init(const llm_attn_shape* s, const llm_kv_pages* k
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     p->off_first[0] = up(PH_WORDS * sizeof(int32_t));
     p->off_first[1] = p->off_first[0] + up((p->caps.ctas1 + 1) * sizeof(int32_t));
-    p->off_units[0] = p->off_first[1] + up((p->caps.ctas2 + 1) * sizeof(int32_t));
+    p->off_cuts = p->off_first[1] + up((p->caps.ctas2 + 1) * sizeof(int32_t));
+    p->off_units[0] = p->off_cuts + up(p->caps.ctas2 * sizeof(int32_t));
     p->off_units[1] = p->off_units[0] + up(p->caps.units1 * sizeof(AttnUnit));
     p->off_table = p->off_units[1] + up(p->caps.units2 * sizeof(AttnUnit));
     p->bytes = p->off_table + up((size_t)s->max_table * sizeof(int32_t));
@@ -376,7 +377,7 @@ int llm_attn_plan_set(llm_attn_plan* p, int32_t n_seq, const int32_t* n_new, con
                   max_parts[2] = {p->caps.parts1, p->caps.parts2};
     for (int f = 0; f < 2; ++f)
         if ((int64_t)plan.form_[f].units.size() > max_units[f] || (int64_t)plan.form_[f].first.size() > max_cta[f] + 1 ||
-            plan.form_[f].n_parts > max_parts[f] || plan.n_tickets > p->caps.tickets)
+            plan.form_[f].n_parts > max_parts[f] || (int64_t)plan.form_[f].cuts.size() > max_cta[f])
             return refuse("plan exceeds its buffers");
     // the previous upload has read the pinned buffer
     if (p->pending && (e = cudaEventSynchronize(p->uploaded)) != cudaSuccess) return failed("upload", e);
@@ -390,6 +391,9 @@ int llm_attn_plan_set(llm_attn_plan* p, int32_t n_seq, const int32_t* n_new, con
         std::memcpy(p->h_buf + p->off_first[f], pf.first.data(), pf.first.size() * sizeof(int32_t));
         std::memcpy(p->h_buf + p->off_units[f], pf.units.data(), pf.units.size() * sizeof(AttnUnit));
     }
+    const std::vector<int32_t>& cuts = plan.form_[1].cuts;
+    hdr[PH_CUTS2] = (int32_t)cuts.size();
+    if (!cuts.empty()) std::memcpy(p->h_buf + p->off_cuts, cuts.data(), cuts.size() * sizeof(int32_t));
     int32_t* table = reinterpret_cast<int32_t*>(p->h_buf + p->off_table);
     for (int32_t i = 0; i < n_seq; ++i) {
         const int64_t need = pages_of(p->kv, n_kv[i]);
@@ -446,6 +450,7 @@ int llm_attn_run(llm_attn_plan* p, const void* q, int64_t q_stride_tok, int64_t 
     a.hdr = reinterpret_cast<const int32_t*>(p->d_buf);
     a.first1 = reinterpret_cast<const int32_t*>(p->d_buf + p->off_first[0]);
     a.first2 = reinterpret_cast<const int32_t*>(p->d_buf + p->off_first[1]);
+    a.cuts2 = reinterpret_cast<const int32_t*>(p->d_buf + p->off_cuts);
     a.units1 = reinterpret_cast<const AttnUnit*>(p->d_buf + p->off_units[0]);
     a.units2 = reinterpret_cast<const AttnUnit*>(p->d_buf + p->off_units[1]);
     a.table = reinterpret_cast<const int32_t*>(p->d_buf + p->off_table);

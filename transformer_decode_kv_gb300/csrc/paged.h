@@ -58,7 +58,7 @@ struct AttnUnit {
     int32_t tok0, row0, n_row, p0;               // first token of the sequence; the tile's rows; position of tok0
     int32_t table, n_sink_keys, key_lo, v0;      // page-table offset; the virtual key range [v0, v1)
     int32_t v1, n_chunk, chunk, part;            // units of this tile; this one; the first's partial slot
-    int32_t ticket, head, pad[2];                // counter of the tile's finished units; KV head
+    int32_t ticket, head, pad[2];                // counter of the tile's finished units (small tiles); KV head
 };
 static_assert(sizeof(AttnUnit) == 64, "read as four int4");
 
@@ -75,7 +75,7 @@ constexpr int attn_rows_warps(int hd, int kv_type, int rows) {
 enum AttnOut : int32_t { AO_F16 = 0, AO_BF16 = 1, AO_F32 = 2, AO_BF16_PAIR = 3 };
 
 // Header words of a plan's device buffer.
-enum : int32_t { PH_FORM = 0, PH_WORDS = 8 };
+enum : int32_t { PH_FORM = 0, PH_CUTS2 = 1, PH_WORDS = 8 };
 
 struct AttnPagedArgs {
     PagedKv kv;
@@ -92,6 +92,7 @@ struct AttnPagedArgs {
     // units of the small-tile and the 256-row form, and where each CTA's begin [CTAs + 1]
     const AttnUnit *units1 = nullptr, *units2 = nullptr;
     const int32_t *first1 = nullptr, *first2 = nullptr;
+    const int32_t* cuts2 = nullptr;              // first unit of each cut 256-row tile
     const int32_t* table = nullptr;
     const int32_t* perm = nullptr;               // token order (null: identity)
     const int32_t* tok_pos = nullptr;            // positions of tokens (null: p0 + token)
@@ -126,12 +127,12 @@ struct PlanShape {
 struct PlanForm {
     std::vector<AttnUnit> units;
     std::vector<int32_t> first;                  // where each CTA's units begin [CTAs + 1]
+    std::vector<int32_t> cuts;                   // the first unit of each tile that is cut
     int32_t n_parts = 0;
 };
 struct PagedPlan {
     PlanForm form_[2];                           // small tiles, 256-row tiles
     int32_t rows1 = 8;                           // rows of the small tiles
-    int32_t n_tickets = 0;
     int32_t form() const {
         return (form_[0].units.empty() ? 0 : rows1 == 8 ? ATTN_FORM_ROWS8 : ATTN_FORM_ROWS16) |
                (form_[1].units.empty() ? 0 : ATTN_FORM_TC);
