@@ -101,30 +101,63 @@ __device__ __forceinline__ bool any_of(int id, int n, bool x) {
     return r != 0;
 }
 
-// K-major 128-row tile, 128-byte swizzle (8-row groups 1024 bytes apart)
-__device__ __forceinline__ uint64_t desc_k(uint32_t s) {
-    return (uint64_t)((s & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
-           (uint64_t)2 << 61;
-}
-// the same memory as an MN-major operand: rows are the contracted dimension, blocks of 64 columns kBlk apart
-__device__ __forceinline__ uint64_t desc_mn(uint32_t s) {
-    return (uint64_t)((s & 0x3FFFFu) >> 4) | (uint64_t)(kBlk >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
-           (uint64_t)1 << 46 | (uint64_t)2 << 61;
-}
+// Shared-memory matrix descriptors of a swizzled tile (8-row groups 1024 bytes apart), low words; the high word is
+// the same for all. K-major: rows are M or N. MN-major: rows are the contracted dimension, blocks of 64
+// columns kBlk apart.
+constexpr uint32_t kDescHi = (1024 >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_k(uint32_t s) { return ((s & 0x3FFFFu) >> 4) | 1u << 16; }
+__device__ __forceinline__ uint32_t desc_mn(uint32_t s) { return ((s & 0x3FFFFu) >> 4) | (kBlk >> 4) << 16; }
 // kind::f16 with f16 or bf16 A and B, float32 D
 __host__ __device__ constexpr uint32_t idesc(bool bf, int m, int n, bool b_mn) {
     return (1u << 4) | (bf ? (1u << 7) | (1u << 10) : 0u) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
            ((uint32_t)(m >> 4) << 24);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+// One k-step of 16 (ACC 0: the product replaces D; 1: it is added; 2: as `acc` says). The whole warp computes the
+// operands, so that they stay in uniform registers, and one thread issues.
+template <int AO, int BO, int ACC>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(id), "r"(acc));
+        "{\n .reg .pred p;\n .reg .b32 x, y;\n .reg .b64 da, db;\n add.u32 x, %1, %4;\n add.u32 y, %2, %5;\n"
+        " mov.b64 da, {x, %6};\n mov.b64 db, {y, %6};\n setp.ne.b32 p, %7, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}\n" ::"r"(d), "r"(a), "r"(b), "r"(id), "n"(AO),
+        "n"(BO), "r"(kDescHi), "n"(ACC));
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-        "r"(a), "l"(b), "r"(id), "r"(acc));
+template <int AO, int BO, int ACC>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc) {
+    if constexpr (ACC == 2)
+        asm volatile(
+            "{\n .reg .pred p;\n .reg .b32 x, y;\n .reg .b64 db;\n add.u32 x, %1, %4;\n add.u32 y, %2, %5;\n"
+            " mov.b64 db, {y, %6};\n setp.ne.b32 p, %7, 0;\n"
+            " tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %3, p;\n}\n" ::"r"(d), "r"(a), "r"(b), "r"(id), "n"(AO),
+            "n"(BO), "r"(kDescHi), "r"(acc));
+    else
+        asm volatile(
+            "{\n .reg .pred p;\n .reg .b32 x, y;\n .reg .b64 db;\n add.u32 x, %1, %4;\n add.u32 y, %2, %5;\n"
+            " mov.b64 db, {y, %6};\n setp.ne.b32 p, %7, 0;\n"
+            " tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %3, p;\n}\n" ::"r"(d), "r"(a), "r"(b), "r"(id), "n"(AO),
+            "n"(BO), "r"(kDescHi), "n"(ACC));
+}
+// S = Q K^T: HD / 16 k-steps, four to a 64-column block
+template <int HD, int KK = 0>
+__device__ __forceinline__ void mma_scores(uint32_t d, uint32_t q, uint32_t k, uint32_t id) {
+    if constexpr (KK < HD / 16) {
+        constexpr int o = (KK >> 2) * (kBlk >> 4) + 2 * (KK & 3);
+        mma_ss<o, o, (KK > 0)>(d, q, k, id);
+        mma_scores<HD, KK + 1>(d, q, k, id);
+    }
+}
+// O (+)= P V: 8 k-steps of 16 keys, P's words 8 TMEM columns apart, V's rows 2048 bytes
+template <int KK = 0>
+__device__ __forceinline__ void mma_outputs(uint32_t d, uint32_t p, uint32_t v, uint32_t id, uint32_t acc) {
+    if constexpr (KK < kKeys / 16) {
+        mma_ts<8 * KK, KK * (2048 >> 4), (KK > 0) ? 1 : 2>(d, p, v, id, acc);
+        mma_outputs<KK + 1>(d, p, v, id, acc);
+    }
+}
+__device__ __forceinline__ bool elect_one() {
+    uint32_t x;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(x));
+    return x != 0;
 }
 __device__ __forceinline__ void commit(uint64_t* b) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(sa(b)) : "memory");
@@ -520,10 +553,12 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
                 const uint64_t t0 = now_ns();
                 while (bulk_at[i] >= 0 && !bar_try(&kv_full[i], (uint32_t)bulk_at[i]) && now_ns() - t0 < kWaitNs) {}
             }
-        } else if (warp == kMmaWarp && lane == 0) {
+        } else if (warp == kMmaWarp) {
             // ---- MMA issuer
             constexpr uint32_t ids = idesc(BF, 128, kKeys, false), ido = idesc(BF, 128, HD, true);
             uint32_t q_ph = 0, p_ph[2] = {0u, 0u};
+            const bool leader = elect_one();
+            const uint32_t qd = desc_k(sa(sm + M::q)), kd = desc_k(sa(sm + M::kv)), vd = desc_mn(sa(sm + M::kv));
             bool ok = true;
             for (int ui = ui0; ui < ui1 && ok; ++ui) {
                 const AttnUnit u = load_unit(a.units2 + ui);
@@ -532,18 +567,17 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
                 ok = wait(q_full, q_ph);
                 q_ph ^= 1u;
                 auto scores = [&](int t, uint32_t stage) {
-                    const uint32_t qa = sa(sm + M::q + t * M::tile), ka = sa(sm + M::kv + stage * M::tile);
-#pragma unroll
-                    for (int kk = 0; kk < HD / 16; ++kk)
-                        mma_ss(tmem + 128 * t, desc_k(qa + (kk >> 2) * kBlk) + (uint64_t)(2 * (kk & 3)),
-                               desc_k(ka + (kk >> 2) * kBlk) + (uint64_t)(2 * (kk & 3)), ids, kk > 0);
-                    commit(&s_full[t]);
+                    const uint32_t q = qd + t * (M::tile >> 4), k = kd + stage * (M::tile >> 4), d = tmem + 128 * t;
+                    if (leader) {
+                        mma_scores<HD>(d, q, k, ids);
+                        commit(&s_full[t]);
+                    }
                 };
                 ok = ok && wait(&kv_full[ring.s], ring.ph);
                 if (ok) {
                     tc_after();
                     for (int t = 0; t < halves; ++t) scores(t, ring.s);
-                    commit(&kv_empty[ring.s]);
+                    if (leader) commit(&kv_empty[ring.s]);
                     ring.next();
                 }
                 for (int j = 0; j < nt && ok; ++j) {
@@ -552,30 +586,30 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
                     const Ring rk = ring;
                     const bool more = j + 1 < nt;
                     if (!(ok = wait(&kv_full[rv.s], rv.ph))) break;
-                    const uint32_t va = sa(sm + M::kv + rv.s * M::tile);
-                    for (int t = 0; t < halves; ++t) {
+                    const uint32_t v = vd + rv.s * (M::tile >> 4);
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        if (t >= halves) break;
                         if (!(ok = wait(&p_full[t], p_ph[t]))) break;
                         p_ph[t] ^= 1u;
                         tc_after();
-#pragma unroll
-                        for (int kk = 0; kk < kKeys / 16; ++kk)
-                            mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 64 + 8 * kk, desc_mn(va + kk * 2048), ido,
-                                   j > 0 || kk > 0);
+                        if (leader) mma_outputs(tmem + 256 + 128 * t, tmem + 128 * t + 64, v, ido, j > 0);
                         if (more) {
                             if (t == 0 && !(ok = wait(&kv_full[rk.s], rk.ph))) break;
                             tc_after();
                             scores(t, rk.s);
-                        } else {
+                        } else if (leader) {
                             commit(&o_done[t]);
                         }
                     }
                     if (!ok) break;
-                    commit(&kv_empty[rv.s]);
+                    if (leader) commit(&kv_empty[rv.s]);
                     if (more) {
-                        commit(&kv_empty[rk.s]);
+                        if (leader) commit(&kv_empty[rk.s]);
                         ring.next();
                     }
                 }
+                ok = __all_sync(0xffffffffu, ok);           // the warp goes on, or stops, as one
             }
         }
         __syncwarp();
@@ -595,22 +629,33 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
             if (nt > 0) {
                 // neighbouring threads hold a row: 8 values each
                 uint8_t* qs = sm + M::q + t * M::tile;
-                for (int x = ht; x < 128 * CH; x += 128) {
-                    const int r = x / CH, ch = x % CH, row = u.row0 + 128 * t + r;
-                    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                constexpr int RQ = 128 / CH;                // rows the half loads at once
+                const int ch = ht % CH;
+#pragma unroll 1
+                for (int r0 = ht / CH; r0 < 128; r0 += 8 * RQ) {
+                uint4 qv[8];                                // eight loads under way
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int r = r0 + i * RQ, row = u.row0 + 128 * t + r;
+                    qv[i] = make_uint4(0u, 0u, 0u, 0u);
                     if (128 * t + r < u.n_row) {
                         const int tok = row_token(a, u, row);
-                        const int64_t i = (int64_t)tok * a.q_tok + (int64_t)(kvh * a.G + row % a.G) * a.q_head + ch * 8;
-                        w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + i);
+                        const int64_t at = (int64_t)tok * a.q_tok + (int64_t)(kvh * a.G + row % a.G) * a.q_head + ch * 8;
+                        qv[i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at);
                     }
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int r = r0 + i * RQ;
+                    const uint4 w = qv[i];
                     uint32_t v[4] = {w.x, w.y, w.z, w.w};
                     float rs = fabsf(a.scale_log2);
                     if constexpr (!BF && QT == W_BF16) {
                         // f16 products: the row times a power of two that brings its largest value to [1, 2)
                         float mx = 0.f;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(v[i] << 16)), fabsf(__uint_as_float(v[i] & 0xffff0000u))));
+                        for (int e = 0; e < 4; ++e)
+                            mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(v[e] << 16)), fabsf(__uint_as_float(v[e] & 0xffff0000u))));
 #pragma unroll
                         for (int o = CH / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
                         const uint32_t ex = __float_as_uint(mx) >> 23;
@@ -620,14 +665,15 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
                             rs *= __uint_as_float(ex << 23);
                         }
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            v[i] = pack<false>(__uint_as_float(v[i] << 16) * dn, __uint_as_float(v[i] & 0xffff0000u) * dn);
+                        for (int e = 0; e < 4; ++e)
+                            v[e] = pack<false>(__uint_as_float(v[e] << 16) * dn, __uint_as_float(v[e] & 0xffff0000u) * dn);
                     }
                     if (a.scale_log2 < 0.f)                 // the scores' scale is positive, the sign is in Q
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) v[i] ^= 0x80008000u;
+                        for (int e = 0; e < 4; ++e) v[e] ^= 0x80008000u;
                     *reinterpret_cast<uint4*>(qs + swz(r, ch)) = make_uint4(v[0], v[1], v[2], v[3]);
                     if (F8 && ch == 0) rs_s[128 * t + r] = rs;
+                }
                 }
                 to_async_proxy();
                 // the rows' scales are read by other threads of the half
