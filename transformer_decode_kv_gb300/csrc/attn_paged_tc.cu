@@ -572,12 +572,14 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
                         mma_scores<HD>(d, q, k, ids);
                         commit(&s_full[t]);
                     }
+                    __syncwarp();                           // (the others do not spin on a barrier before it has issued)
                 };
                 ok = ok && wait(&kv_full[ring.s], ring.ph);
                 if (ok) {
                     tc_after();
                     for (int t = 0; t < halves; ++t) scores(t, ring.s);
                     if (leader) commit(&kv_empty[ring.s]);
+                    __syncwarp();
                     ring.next();
                 }
                 for (int j = 0; j < nt && ok; ++j) {
@@ -593,7 +595,11 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
                         if (!(ok = wait(&p_full[t], p_ph[t]))) break;
                         p_ph[t] ^= 1u;
                         tc_after();
-                        if (leader) mma_outputs(tmem + 256 + 128 * t, tmem + 128 * t + 64, v, ido, j > 0);
+                        if (leader) {
+                            mma_outputs(tmem + 256 + 128 * t, tmem + 128 * t + 64, v, ido, j > 0);
+                            if (t == halves - 1) commit(&kv_empty[rv.s]);
+                        }
+                        __syncwarp();
                         if (more) {
                             if (t == 0 && !(ok = wait(&kv_full[rk.s], rk.ph))) break;
                             tc_after();
@@ -601,11 +607,12 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
                         } else if (leader) {
                             commit(&o_done[t]);
                         }
+                        __syncwarp();
                     }
                     if (!ok) break;
-                    if (leader) commit(&kv_empty[rv.s]);
                     if (more) {
                         if (leader) commit(&kv_empty[rk.s]);
+                        __syncwarp();
                         ring.next();
                     }
                 }
