@@ -15,9 +15,9 @@
 // the same columns, and a completed S means that every product before it is complete too.
 //
 // Roles (12 warps; warps 0-3 give registers to warps 4-11, whose threads hold a row of scores each): warps
-// 0-1 bring K and V rows into a ring of 128-byte-swizzled tiles, with the keys' positions: bulk tensor copies of
-// the runs of neighbouring cells that pages are (64 keys of a warp at a time, when all of them are read),
-// otherwise 16-byte asynchronous copies row by row, and E4M3 rows through registers, converted to f16;
+// 0 and 1 bring K and V rows into a ring of 128-byte-swizzled tiles, with the keys' positions: a block whose keys are
+// all read in bulk tensor copies of the runs of neighbouring cells that pages are, others in 16-byte
+// asynchronous copies row by row, and E4M3 rows through registers, converted to f16;
 // warp 2 issues the MMAs; warps 4-7 and 8-11 are the two halves' softmax and epilogue (a thread owns a
 // TMEM lane: warp w reads lanes 32 (w % 4) on). m is 6 below a row maximum and raised lazily, when p would
 // pass 2^14: O, in TMEM, is rarely rescaled, and never more than it must. P is rounded to f16 (half a step 2^-11)
@@ -47,7 +47,6 @@ constexpr int kProdWarps = 2;
 constexpr int kMmaWarp = 2;
 constexpr int kSoft0 = 4;                                  // first softmax warp
 constexpr int kThr = 12 * 32;
-constexpr int kGroups = 4 / kProdWarps;                    // groups of 32 keys a producing warp brings
 constexpr int kKeys = 128;                                 // keys per block
 constexpr int kStages = 5;                                 // K or V tiles in flight
 constexpr int kMeta = 3;                                   // blocks whose positions are kept (see meta_full)
@@ -61,12 +60,11 @@ struct Smem {
     static constexpr uint32_t q = 0;                        // [2] tiles
     static constexpr uint32_t kv = q + 2 * tile;            // [kStages] tiles
     static constexpr uint32_t kpos = kv + kStages * tile;   // int [kMeta][kKeys]
-    static constexpr uint32_t full = kpos + kMeta * kKeys * 4;   // uint8 [kMeta][4]
-    static constexpr uint32_t rs = full + 16;               // E4M3: float [256], scale of a row's scores; 16-bit
-                                                            // caches: int64 [128], offsets of a block's rows
+    static constexpr uint32_t full = kpos + kMeta * kKeys * 4;   // uint32 [kMeta]: every key is read
+    static constexpr uint32_t rs = full + 16;               // E4M3: float [256], scale of a row's scores
     static constexpr uint32_t bars = rs + 256 * 4;
     static constexpr uint32_t misc = bars + 24 * 8;
-    static constexpr uint32_t bytes = misc + 96;
+    static constexpr uint32_t bytes = misc + 28 * 4;
 };
 static_assert(Smem<128>::bytes <= 227 * 1024, "shared memory of one CTA");
 
@@ -221,7 +219,8 @@ __device__ __forceinline__ uint32_t swz(int r, int ch) {
 
 // How bulk tensor copies find a cell: maps of K and V as [page][head][cell][dim] (one page of all cells where
 // the pages follow each other evenly), in boxes of `rows` cells x 64 dims (rows = 0: none).
-struct TmaRuns { int rows, page_cells; };
+// even: the maps have one page. aligned: the plan's blocks of keys are whole runs.
+struct TmaRuns { int rows; bool even, aligned; };
 
 struct Ring {                                              // position in the ring of K and V tiles
     uint32_t s = 0, ph = 0;
@@ -241,10 +240,10 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
     constexpr int CH = HD / 8;                              // 16-byte chunks of a 16-bit row
     extern __shared__ __align__(1024) uint8_t sm[];
     int* kpos = reinterpret_cast<int*>(sm + M::kpos);
-    uint8_t* full = sm + M::full;
+    volatile uint32_t* full = reinterpret_cast<volatile uint32_t*>(sm + M::full);
     float* rs_s = reinterpret_cast<float*>(sm + M::rs);
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + M::bars);
-    uint64_t* kv_full = bars;                               // [kStages] 4: the producing warps
+    uint64_t* kv_full = bars;                               // [kStages] 1: the producing warp (and its bulk copies' bytes)
     uint64_t* kv_empty = bars + kStages;                    // [kStages] 1: MMA commit
     uint64_t* s_full = bars + 2 * kStages;                  // [2] 1: MMA commit
     uint64_t* p_full = s_full + 2;                          // [2] 128: the softmax threads
@@ -256,10 +255,9 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
     int* misc = reinterpret_cast<int*>(sm + M::misc);
     volatile int* abort_f = misc;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 2);
-    // of the units with keys the producers may be ahead by three (a unit has two tiles at least): by unit % 4
-    volatile int* redo_f = misc + 4;                        // [4] the unit has to be redone
-    float* s0 = reinterpret_cast<float*>(misc + 8);         // [4][2] E4M3: scale of the K and V tiles
-    float* wmax = reinterpret_cast<float*>(misc + 16);      // [kProdWarps][2]
+    // of the units with keys a producer may look at the fourth ahead (a unit has two tiles at least): by unit % 8
+    volatile int* redo_f = misc + 4;                        // [8] the unit has to be redone
+    float* s0 = reinterpret_cast<float*>(misc + 12);        // [8][2] E4M3: scale of the K and V tiles
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (a.pdl) asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -272,12 +270,12 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
     if ((a.hdr[PH_FORM] & ATTN_FORM_TC) == 0 || ui0 >= ui1) return;
 
     if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) { bar_init(&kv_full[i], kProdWarps); bar_init(&kv_empty[i], 1); }
+        for (int i = 0; i < kStages; ++i) { bar_init(&kv_full[i], 1); bar_init(&kv_empty[i], 1); }
         for (int i = 0; i < 2; ++i) { bar_init(&s_full[i], 1); bar_init(&p_full[i], 128); bar_init(&o_done[i], 1); }
         bar_init(q_full, 256);
-        for (int i = 0; i < kMeta; ++i) bar_init(&meta_full[i], kProdWarps);
+        for (int i = 0; i < kMeta; ++i) bar_init(&meta_full[i], 1);
         *abort_f = 0;
-        for (int i = 0; i < 4; ++i) redo_f[i] = 0;
+        for (int i = 0; i < 8; ++i) redo_f[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kMmaWarp) {
@@ -312,246 +310,258 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
     if (warp < kSoft0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
         if (warp < kProdWarps) {
-        int produced = 0, with_keys = 0;                    // ring places filled (up to all of them); units with keys
-        bool ok = true;
-        int bulk_at[kStages];                               // phase of a stage's last bulk copies, -1: none
+            // ---- K (warp 0) and V (warp 1) tiles, the even and odd ones of the ring
+            const bool is_v = warp == 1;
+            uint32_t it = is_v ? 1 : 0;                     // tile number, over all units
+            int with_keys = 0;                              // units with keys
+            bool ok = true;
+            int bulk_at[kStages];                           // phase of a stage's last bulk copies, -1: none
 #pragma unroll
-        for (int i = 0; i < kStages; ++i) bulk_at[i] = -1;
-        for (int ui = ui0; ui < ui1 && ok; ++ui) {
-            const AttnUnit u = load_unit(a.units2 + ui);
-            const int kvh = u.head;
-            const int nt = (u.v1 - u.v0 + kKeys - 1) / kKeys;
-            if (nt == 0) continue;
-            const int slot = with_keys++ & 3;
-            // ---- K and V tiles
-            const uint8_t* kb = a.kv.k + (int64_t)kvh * a.kv.sb_head;
-            const uint8_t* vb = a.kv.v + (int64_t)kvh * a.kv.sb_head;
-            int pmin, pmax;
-            {
-                const int r1 = u.row0 + u.n_row - 1;
-                pmin = row_pos(a, u, u.row0, row_token(a, u, u.row0));
-                pmax = row_pos(a, u, r1, row_token(a, u, r1));
-                if (a.tok_pos) {                            // any order: over all of the unit's tokens
-                    for (int r = u.row0; r <= r1; r += a.G) {
-                        const int p = row_pos(a, u, r, row_token(a, u, r));
-                        pmin = min(pmin, p);
-                        pmax = max(pmax, p);
-                    }
-                }
-            }
-            const int hid_all = hidden_below(a, pmin);
-            struct Key { int64_t off; int pos, cell; float ks, vs; };
-            const Key none{-1, INT_MAX, 0, 0.f, 0.f};
-            Key cur[kGroups], nxt[kGroups];                  // key 32 (kGroups warp + i) + lane of a block
-            auto lookup = [&](Key* k, int j) {
-#pragma unroll
-                for (int i = 0; i < kGroups; ++i) {
-                    k[i] = none;
-                    const int v = u.v0 + j * kKeys + 32 * (kGroups * warp + i) + lane;
-                    if (v >= u.v1) continue;
-                    const KeyAt at = key_at(a, u, v);
-                    if (at.off >= 0 && sees(at.pos, pmax, hid_all, a.n_sink)) {
-                        k[i].off = at.off;
-                        k[i].pos = at.pos;
-                        k[i].cell = at.cell;
-                        if constexpr (F8) {
-                            k[i].ks = a.kv.ks[at.soff + (int64_t)kvh * a.kv.ss_head];
-                            k[i].vs = a.kv.vs[at.soff + (int64_t)kvh * a.kv.ss_head];
+            for (int i = 0; i < kStages; ++i) bulk_at[i] = -1;
+            const uint64_t map = reinterpret_cast<uint64_t>(is_v ? &map_v : &map_k);
+            for (int ui = ui0; ui < ui1 && ok; ++ui) {
+                const AttnUnit u = load_unit(a.units2 + ui);
+                const int kvh = u.head;
+                const int nt = (u.v1 - u.v0 + kKeys - 1) / kKeys;
+                if (nt == 0) continue;
+                const int slot = with_keys++ & 7;
+                const uint8_t* base = (is_v ? a.kv.v : a.kv.k) + (int64_t)kvh * a.kv.sb_head;
+                const float* scales = F8 ? (is_v ? a.kv.vs : a.kv.ks) + (int64_t)kvh * a.kv.ss_head : nullptr;
+                int pmin, pmax;
+                {
+                    const int r1 = u.row0 + u.n_row - 1;
+                    pmin = row_pos(a, u, u.row0, row_token(a, u, u.row0));
+                    pmax = row_pos(a, u, r1, row_token(a, u, r1));
+                    if (a.tok_pos) {                        // any order: over all of the unit's tokens
+                        for (int r = u.row0; r <= r1; r += a.G) {
+                            const int p = row_pos(a, u, r, row_token(a, u, r));
+                            pmin = min(pmin, p);
+                            pmax = max(pmax, p);
                         }
                     }
                 }
-            };
-            auto claim = [&]() { return produced < kStages || wait(&kv_empty[ring.s], ring.ph ^ 1u); };
-            lookup(cur, 0);
-            float ik = 1.f, iv = 1.f;
-            if constexpr (F8) {
-                // s0 of this unit: the largest scales of its first block
-                float mk = 0.f, mv = 0.f;
+                const int hid_all = hidden_below(a, pmin);
+                struct Key { int64_t off; int pos, cell; float s; };
+                auto lookup = [&](Key* k, int j) {          // keys 32 i + lane of block j
 #pragma unroll
-                for (int i = 0; i < kGroups; ++i) { mk = fmaxf(mk, cur[i].ks); mv = fmaxf(mv, cur[i].vs); }
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) {
-                    mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, o));
-                    mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
-                }
-                if (lane == 0) { wmax[2 * warp] = mk; wmax[2 * warp + 1] = mv; }
-                asm volatile("bar.sync 4, %0;" ::"n"(32 * kProdWarps) : "memory");
-#pragma unroll
-                for (int i = 0; i < kProdWarps; ++i) { mk = fmaxf(mk, wmax[2 * i]); mv = fmaxf(mv, wmax[2 * i + 1]); }
-                if (!(mk > 0.f)) mk = 1.f;
-                if (!(mv > 0.f)) mv = 1.f;
-                if (tid == 0) { s0[2 * slot] = mk; s0[2 * slot + 1] = mv; }
-                ik = 1.f / mk;
-                iv = 1.f / mv;
-            }
-            uint32_t read[kGroups];                         // which of a group's keys are read
-            bool bulk = false;                              // this warp's keys of the block come by bulk copies
-            constexpr int kOwn = 32 * kGroups;              // keys of a block this warp brings
-            // 16-bit tiles: asynchronous copies, announced two tiles later, when they have landed
-            uint32_t pend[2];
-            int n_pend = 0;
-            auto announce = [&](uint32_t s) {
-                to_async_proxy();
-                __syncwarp();
-                if (lane == 0) bar_arrive(&kv_full[s]);
-            };
-            for (int j = 0; j < nt && ok; ++j) {
-                for (int kvi = 0; kvi < 2; ++kvi) {
-                    const uint8_t* base = kvi ? vb : kb;
-                    uint8_t* dst = sm + M::kv + ring.s * M::tile;
-                    if constexpr (F8) {
-                        // the rows' bytes first: they travel while the stage is waited for
-                        constexpr int LR = HD / 16;         // lanes per row, 16 values each
-                        uint4 raw[kGroups * LR];
-#pragma unroll
-                        for (int x = 0; x < kGroups * LR; ++x) {
-                            const int64_t off = __shfl_sync(0xffffffffu, cur[x / LR].off, x % LR * (32 / LR) + lane / LR);
-                            raw[x] = off >= 0 ? *reinterpret_cast<const uint4*>(base + off + 16 * (lane % LR))
-                                              : make_uint4(0u, 0u, 0u, 0u);
+                    for (int i = 0; i < 4; ++i) {
+                        k[i] = Key{-1, INT_MAX, 0, 0.f};
+                        const int v = u.v0 + j * kKeys + 32 * i + lane;
+                        if (v >= u.v1) continue;
+                        const KeyAt at = key_at(a, u, v);
+                        if (at.off >= 0 && sees(at.pos, pmax, hid_all, a.n_sink)) {
+                            k[i].off = at.off;
+                            k[i].pos = at.pos;
+                            k[i].cell = at.cell;
+                            if constexpr (F8) k[i].s = scales[at.soff];
                         }
-                        float f[kGroups];
-#pragma unroll
-                        for (int i = 0; i < kGroups; ++i) {
-                            f[i] = kvi ? cur[i].vs * iv : cur[i].ks * ik;
-                            if (cur[i].off >= 0 && !(f[i] <= 128.f)) redo_f[slot] = 1;
+                    }
+                };
+                // Blocks that need no look at single keys: positions are indices, the block's pages hold whole runs, and
+                // some row sees each key. A lane brings one box of 64 dims x runs.rows cells.
+                constexpr int HB = HD / 64;
+                const int n_box = runs.rows > 0 ? kKeys / runs.rows * HB : 0;
+                const bool paged = runs.rows > 0 && runs.aligned && !a.key_pos;
+                auto plain = [&](int j) {
+                    const int v = u.v0 + j * kKeys;
+                    if (!paged || v + kKeys > u.v1) return false;
+                    if (v < u.n_sink_keys) return v + kKeys <= u.n_sink_keys && v + kKeys <= min(a.n_sink, pmax + 1);
+                    const int k = v - u.n_sink_keys + u.key_lo;
+                    return k + kKeys - 1 <= pmax && (k > hid_all || k + kKeys <= a.n_sink);
+                };
+                auto box_page = [&](int j, int& at) {       // this lane's page, its first cell there
+                    const int v = u.v0 + j * kKeys + (lane < n_box ? lane / HB : 0) * runs.rows;
+                    const int k = v < u.n_sink_keys ? v : v - u.n_sink_keys + u.key_lo;
+                    const int ps = a.kv.page_size, pg = (ps & (ps - 1)) == 0 ? k >> (__ffs(ps) - 1) : k / ps;
+                    at = k - pg * ps;
+                    return a.table[u.table + pg];
+                };
+                int page_nxt = 0, at_nxt = 0;
+                bool plain_nxt = plain(0);
+                if (plain_nxt) page_nxt = box_page(0, at_nxt);
+                float inv = 1.f;
+                // row copies are announced one tile of this warp's later, when they have landed (not two: K tile
+                // j + 2 needs the place of V tile j - 1, which is not free before the scores of block j)
+                int pend = -1;                              // stage
+                auto announce = [&](uint32_t s) {
+                    to_async_proxy();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(&kv_full[s]);
+                };
+                auto flush = [&]() {
+                    if (pend < 0) return;
+                    asm volatile("cp.async.wait_group 0;" ::: "memory");
+                    announce(pend);
+                    pend = -1;
+                };
+                for (int j = 0; j < nt; ++j, it += 2) {
+                    const uint32_t stage = it % kStages, ph = (it / kStages) & 1u;
+                    uint8_t* const dst = sm + M::kv + stage * M::tile;
+                    const uint32_t fb = sa(&kv_full[stage]);
+                    auto claim = [&]() {
+                        ok = it < kStages || wait(&kv_empty[stage], ph ^ 1u);
+                        ok = __all_sync(0xffffffffu, ok);
+                        return ok;
+                    };
+                    auto box = [&](uint32_t d, int h, int cell, int page) {
+                        asm volatile(
+                            "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+                            " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(d), "l"(map), "r"(fb), "r"(64 * h), "r"(cell),
+                            "r"(kvh), "r"(page) : "memory");
+                    };
+                    auto expect = [&]() {
+                        if (lane == 0)
+                            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(fb),
+                                         "r"(kKeys * HD * 2) : "memory");
+                        __syncwarp();
+                        bulk_at[stage] = (int)ph;
+                    };
+                    const int page = page_nxt, at = at_nxt;
+                    bool now = plain_nxt;
+                    plain_nxt = j + 1 < nt && plain(j + 1);
+                    if (plain_nxt) page_nxt = box_page(j + 1, at_nxt);
+                    if (now && __any_sync(0xffffffffu, (unsigned)page >= (unsigned)a.kv.n_pages)) now = false;
+                    if (now) {
+                        flush();
+                        if (!claim()) break;
+                        expect();
+                        if (lane < n_box) {
+                            const int k = lane / HB * runs.rows, h = lane % HB;
+                            box(sa(dst) + h * kBlk + k * 128, h, runs.even ? page * a.kv.page_size + at : at, runs.even ? 0 : page);
                         }
-                        if (kvi == 1 && j + 1 < nt) lookup(nxt, j + 1);
-                        if (!__all_sync(0xffffffffu, claim())) { ok = false; break; }
-#pragma unroll
-                        for (int x = 0; x < kGroups * LR; ++x) {
-                            const int r = x % LR * (32 / LR) + lane / LR, c = lane % LR;
-                            const __half2 fh = __float2half2_rn(__shfl_sync(0xffffffffu, f[x / LR], r));
-                            const uint32_t w[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
-                            uint32_t h[8];
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const uint32_t e = e4m3x2_to_h2((w[i / 2] >> (16 * (i & 1))) & 0xffffu);
-                                const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&e), fh);
-                                h[i] = *reinterpret_cast<const uint32_t*>(&y);
-                            }
-                            const int rr = 32 * (kGroups * warp + x / LR) + r;
-                            *reinterpret_cast<uint4*>(dst + swz(rr, 2 * c)) = make_uint4(h[0], h[1], h[2], h[3]);
-                            *reinterpret_cast<uint4*>(dst + swz(rr, 2 * c + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
+                        if (!is_v) {
+                            const int v = u.v0 + j * kKeys, p0 = v < u.n_sink_keys ? v : v - u.n_sink_keys + u.key_lo;
+                            reinterpret_cast<int4*>(kpos + meta.s * kKeys)[lane] =
+                                make_int4(p0 + 4 * lane, p0 + 4 * lane + 1, p0 + 4 * lane + 2, p0 + 4 * lane + 3);
+                            if (lane == 0) full[meta.s] = 1u;
                         }
                     } else {
-                        if (!__all_sync(0xffffffffu, claim())) { ok = false; break; }
-                        constexpr int RI = 32 / CH;         // rows per instruction
-                        const int ch = lane % CH, r0 = lane / CH, own = kOwn * warp;
-                        // this warp's part: the rows' offsets, or their cells' numbers
-                        int64_t* offs = reinterpret_cast<int64_t*>(sm + M::rs) + kOwn * warp;
-                        int* cells = reinterpret_cast<int*>(offs);
-                        if (kvi == 0) {
-                            bool run = runs.rows > 0;
+                        Key cur[4];
+                        lookup(cur, j);
+                        bool all = true;
 #pragma unroll
-                            for (int i = 0; i < kGroups; ++i) {
-                                read[i] = __ballot_sync(0xffffffffu, cur[i].off >= 0);
-                                // a run of runs.rows keys lies in neighbouring cells of a page
+                        for (int i = 0; i < 4; ++i) all = all && cur[i].off >= 0;
+                        all = __all_sync(0xffffffffu, all);
+                        if constexpr (F8) {
+                            if (j == 0) {                   // s0 of this unit: the largest scale of its first block
+                                float mx = fmaxf(fmaxf(cur[0].s, cur[1].s), fmaxf(cur[2].s, cur[3].s));
+#pragma unroll
+                                for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                                if (!(mx > 0.f)) mx = 1.f;
+                                if (lane == 0) s0[2 * slot + (is_v ? 1 : 0)] = mx;
+                                inv = 1.f / mx;
+                            }
+                            constexpr int LR = HD / 16;     // lanes per row, 16 values each
+                            float f[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                f[i] = cur[i].s * inv;
+                                if (cur[i].off >= 0 && !(f[i] <= 128.f)) redo_f[slot] = 1;
+                            }
+                            // the first half's bytes travel while the stage is waited for
+                            uint4 raw[2 * LR];
+                            auto bring = [&](int g0) {
+#pragma unroll
+                                for (int x = 0; x < 2 * LR; ++x) {
+                                    const int64_t off = __shfl_sync(0xffffffffu, g0 ? cur[2 + x / LR].off : cur[x / LR].off,
+                                                                    x % LR * (32 / LR) + lane / LR);
+                                    raw[x] = off >= 0 ? *reinterpret_cast<const uint4*>(base + off + 16 * (lane % LR))
+                                                      : make_uint4(0u, 0u, 0u, 0u);
+                                }
+                            };
+                            auto put = [&](int g0) {
+#pragma unroll
+                                for (int x = 0; x < 2 * LR; ++x) {
+                                    const int r = x % LR * (32 / LR) + lane / LR, c = lane % LR;
+                                    const __half2 fh = __float2half2_rn(__shfl_sync(0xffffffffu, g0 ? f[2 + x / LR] : f[x / LR], r));
+                                    const uint32_t w[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
+                                    uint32_t h[8];
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) e4m3x4_to_h2(w[i], h[2 * i], h[2 * i + 1]);
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i) {
+                                        const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&h[i]), fh);
+                                        h[i] = *reinterpret_cast<const uint32_t*>(&y);
+                                    }
+                                    const int rr = 32 * (g0 + x / LR) + r;
+                                    *reinterpret_cast<uint4*>(dst + swz(rr, 2 * c)) = make_uint4(h[0], h[1], h[2], h[3]);
+                                    *reinterpret_cast<uint4*>(dst + swz(rr, 2 * c + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
+                                }
+                            };
+                            bring(0);
+                            if (!claim()) break;
+                            put(0);
+                            bring(2);
+                            put(2);
+                        } else {
+                            // runs of neighbouring cells among single cells
+                            bool run = runs.rows > 0 && all;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
                                 const int prev = __shfl_up_sync(0xffffffffu, cur[i].cell, 1);
                                 const int last = __shfl_sync(0xffffffffu, cur[i > 0 ? i - 1 : 0].cell, 31);
                                 const bool starts = ((32 * i + lane) & (runs.rows - 1)) == 0;
-                                run = run && read[i] == 0xffffffffu &&
-                                      (starts ? cur[i].cell % runs.page_cells + runs.rows <= runs.page_cells
-                                              : cur[i].cell == (lane > 0 ? prev : last) + 1);
+                                run = run && (starts ? runs.even || cur[i].cell % a.kv.page_size + runs.rows <= a.kv.page_size
+                                                     : cur[i].cell == (lane > 0 ? prev : last) + 1);
                             }
-                            bulk = __all_sync(0xffffffffu, run);
-                            __syncwarp();                   // the last block's have been read
+                            run = __all_sync(0xffffffffu, run);
+                            if (run) flush();
+                            if (!claim()) break;
+                            if (run) {
+                                expect();
+                                const int k = lane < n_box ? lane / HB * runs.rows : 0, h = lane % HB;
+                                int c = 0;
 #pragma unroll
-                            for (int i = 0; i < kGroups; ++i) {
-                                if (bulk) cells[32 * i + lane] = cur[i].cell;
-                                else offs[32 * i + lane] = cur[i].off >= 0 ? cur[i].off : 0;
-                            }
-                            __syncwarp();
-                        }
-                        if (bulk) {
-                            if (n_pend > 0) {               // row copies of earlier blocks are announced first
-                                asm volatile("cp.async.wait_group 0;" ::: "memory");
-                                for (int i = 0; i < n_pend; ++i) announce(pend[i]);
-                                n_pend = 0;
-                            }
-                            const uint32_t fb = sa(&kv_full[ring.s]);
-                            if (lane == 0)
-                                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(fb),
-                                             "r"(kOwn * HD * 2) : "memory");
-                            __syncwarp();
-                            constexpr int HB = HD / 64;     // boxes of 64 dims
-#pragma unroll 1
-                            for (int x = lane; x < kOwn / runs.rows * HB; x += 32) {
-                                const int k = x / HB * runs.rows, h = x % HB, cell = cells[k];
-                                const int page = cell / runs.page_cells, at = cell - page * runs.page_cells;
-                                asm volatile(
-                                    "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-                                    " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(sa(dst) + h * kBlk + (kOwn * warp + k) * 128),
-                                    "l"(reinterpret_cast<uint64_t>(kvi ? &map_v : &map_k)), "r"(fb), "r"(64 * h), "r"(at),
-                                    "r"(kvh), "r"(page) : "memory");
-                            }
-                            bulk_at[ring.s] = (int)ring.ph;
-                        } else {
-                        const uint8_t* src = base + 16 * ch;
-                        bool all = true;
-#pragma unroll
-                        for (int i = 0; i < kGroups; ++i) all = all && read[i] == 0xffffffffu;
-                        if (all) {
-#pragma unroll 8
-                            for (int x = 0; x < 32 * kGroups / RI; ++x)
-                                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sa(dst) + swz(own + r0 + x * RI, ch)),
-                                             "l"(src + offs[r0 + x * RI]) : "memory");
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < kGroups; ++i)
-#pragma unroll 2
-                                for (int x = 0; x < 32 / RI; ++x) {
-                                    const int r = r0 + 32 * i + x * RI;
-                                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sa(dst) + swz(own + r, ch)),
-                                                 "l"(src + offs[r]), "r"(read[i] >> (r & 31) & 1u ? 16 : 0) : "memory");
+                                for (int i = 0; i < 4; ++i) {
+                                    const int ci = __shfl_sync(0xffffffffu, cur[i].cell, k & 31);
+                                    if (k >> 5 == i) c = ci;
                                 }
-                        }
-                        asm volatile("cp.async.commit_group;" ::: "memory");
-                        }
-                    }
-                    if (kvi == 0) {
+                                if (lane < n_box) {
+                                    const int pg = runs.even ? 0 : c / a.kv.page_size;
+                                    box(sa(dst) + h * kBlk + k * 128, h, c - pg * a.kv.page_size, pg);
+                                }
+                            } else {
+                                constexpr int RI = 32 / CH; // rows per instruction
+                                const int ch = lane % CH, r0 = lane / CH;
 #pragma unroll
-                        for (int i = 0; i < kGroups; ++i) {
-                            const int gr = kGroups * warp + i;
-                            kpos[meta.s * kKeys + 32 * gr + lane] = cur[i].pos;
-                            const bool all = __all_sync(0xffffffffu, cur[i].off >= 0);
-                            if (lane == 0) full[meta.s * 4 + gr] = all;
+                                for (int i = 0; i < 4; ++i)
+#pragma unroll 4
+                                    for (int x = 0; x < 32 / RI; ++x) {
+                                        const int r = r0 + x * RI;
+                                        const int64_t off = __shfl_sync(0xffffffffu, cur[i].off, r);
+                                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sa(dst) + swz(32 * i + r, ch)),
+                                                     "l"(base + (off >= 0 ? off : 0) + 16 * ch), "r"(off >= 0 ? 16 : 0) : "memory");
+                                    }
+                                asm volatile("cp.async.commit_group;" ::: "memory");
+                                if (pend >= 0) {
+                                    asm volatile("cp.async.wait_group 1;" ::: "memory");
+                                    announce(pend);
+                                }
+                                pend = (int)stage;
+                            }
                         }
+                        if (!is_v) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) kpos[meta.s * kKeys + 32 * i + lane] = cur[i].pos;
+                            if (lane == 0) full[meta.s] = all;
+                        }
+                        if constexpr (F8) announce(stage);
+                    }
+                    if (!is_v) {
                         __syncwarp();
                         if (lane == 0) bar_arrive(&meta_full[meta.s]);
                         meta.next();
                     }
-                    if constexpr (F8) {
-                        announce(ring.s);
-                    } else {
-                        if (kvi == 1 && j + 1 < nt) lookup(nxt, j + 1);
-                        if (bulk) {
-                            // announced by the copies themselves
-                        } else if (n_pend == 2) {
-                            asm volatile("cp.async.wait_group 2;" ::: "memory");
-                            announce(pend[0]);
-                            pend[0] = pend[1];
-                            pend[1] = ring.s;
-                        } else {
-                            pend[n_pend++] = ring.s;
-                        }
-                    }
-                    ring.next();
-                    if (produced < kStages) ++produced;
                 }
-#pragma unroll
-                for (int i = 0; i < kGroups; ++i) cur[i] = nxt[i];
+                if constexpr (!F8) flush();
             }
-            if constexpr (!F8) {
+            // after a wait that gave up nobody may wait for the copies under way: they land before the CTA leaves
+            if (!ok) {
                 asm volatile("cp.async.wait_group 0;" ::: "memory");
-                for (int i = 0; i < n_pend; ++i) announce(pend[i]);
-            }
-            ok = !any_of(4, 32 * kProdWarps, !ok);          // both warps go on, or neither; wmax is free again
-        }
-        // after a wait that gave up nobody may wait for the copies under way: they land before the CTA leaves
-        if (!ok)
-            for (int i = 0; i < kStages; ++i) {
-                const uint64_t t0 = now_ns();
-                while (bulk_at[i] >= 0 && !bar_try(&kv_full[i], (uint32_t)bulk_at[i]) && now_ns() - t0 < kWaitNs) {}
+                for (int i = 0; i < kStages; ++i) {
+                    const uint64_t t0 = now_ns();
+                    while (bulk_at[i] >= 0 && !bar_try(&kv_full[i], (uint32_t)bulk_at[i]) && now_ns() - t0 < kWaitNs) {}
+                }
             }
         } else if (warp == kMmaWarp) {
             // ---- MMA issuer
@@ -631,7 +641,7 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
             const AttnUnit u = load_unit(a.units2 + ui);
             const int kvh = u.head;
             const int nt = (u.v1 - u.v0 + kKeys - 1) / kKeys, halves = u.n_row > 128 ? 2 : 1;
-            const int slot = with_keys & 3;
+            const int slot = with_keys & 7;
             if (nt > 0) ++with_keys;
             if (nt > 0) {
                 // neighbouring threads hold a row: 8 values each
@@ -706,7 +716,7 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
                 if (F8 && j == 0) rs *= s0[2 * slot];
                 const int* kp = kpos + meta.s * kKeys;
                 const int4* kp4 = reinterpret_cast<const int4*>(kp);
-                const bool open = *reinterpret_cast<const uint32_t*>(full + meta.s * 4) == 0x01010101u &&
+                const bool open = full[meta.s] != 0u &&
                                   kp[kKeys - 1] <= wp_min && (kp[0] > wh_max || kp[kKeys - 1] < a.n_sink);
                 if (!open) {
                     // some row does not see some key: -inf over those scores, in TMEM (few blocks do this; the code
@@ -883,7 +893,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 // The maps of a 16-bit cache and the runs of cells they copy: up to 64 neighbouring cells of a page (a power of two
 // from 8 on that divides the page), any 64 where the pages follow each other evenly. No runs: row copies only.
 TmaRuns cell_runs(const PagedKv& kv, CUtensorMap* mk, CUtensorMap* mv) {
-    TmaRuns r{0, kv.page_size};
+    TmaRuns r{0, false, false};
     const bool even = kv.n_pages == 1 || kv.page_size == 1 || kv.sb_page == kv.page_size * kv.sb_cell;
     const int64_t sb_cell = kv.page_size > 1 ? kv.sb_cell : kv.sb_page;
     const int64_t cells = (int64_t)kv.page_size * kv.n_pages;
@@ -904,7 +914,8 @@ TmaRuns cell_runs(const PagedKv& kv, CUtensorMap* mk, CUtensorMap* mv) {
                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return r;
     r.rows = rows;
-    if (even) r.page_cells = (int)cells;
+    r.even = even;
+    r.aligned = kv.page_size % rows == 0;
     return r;
 }
 
@@ -923,7 +934,7 @@ bool go(const AttnPagedArgs& a, cudaStream_t st) {
     cfg.attrs = at;
     cfg.numAttrs = a.pdl ? 1 : 0;
     CUtensorMap mk{}, mv{};
-    TmaRuns runs{0, 1};
+    TmaRuns runs{0, false, false};
     if (CT != W_F8) runs = cell_runs(a.kv, &mk, &mv);
     if (cudaLaunchKernelEx(&cfg, attn_tc_rows_kernel<HD, CT, QT>, a, runs, mk, mv) != cudaSuccess) return false;
     // (launched early, it waits for the kernel above)
