@@ -122,6 +122,33 @@ __device__ __forceinline__ void store_out4(const AttnPagedArgs& a, int64_t i, co
     }
 }
 
+// 32 bytes at once (a whole sector per lane), 32-byte aligned
+__device__ __forceinline__ void store32b(void* p, const uint32_t* w) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
+}
+// 32 consecutive values; whole sectors where the output's rows allow it (a.out32)
+__device__ __forceinline__ void store_out32(const AttnPagedArgs& a, int64_t i, const float* v) {
+    if (a.out32 && (a.out_kind == AO_F16 || a.out_kind == AO_BF16)) {
+        uint32_t w[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            if (a.out_kind == AO_F16) {
+                const __half2 h = __floats2half2_rn(v[2 * j], v[2 * j + 1]);
+                w[j] = *reinterpret_cast<const uint32_t*>(&h);
+            } else {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+                w[j] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+        }
+        store32b(static_cast<uint16_t*>(a.out) + i, w);
+        store32b(static_cast<uint16_t*>(a.out) + i + 16, w + 8);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) store_out4(a, i + j, v + j);
+    }
+}
+
 // One value of a cached row as float32.
 __device__ __forceinline__ float kv_value(const AttnPagedArgs& a, const uint8_t* row, float s, int d) {
     if (a.kv.type == W_F16) return __half2float(reinterpret_cast<const __half*>(row)[d]);

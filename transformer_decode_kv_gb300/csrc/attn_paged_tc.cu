@@ -248,10 +248,11 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
     uint64_t* s_full = bars + 2 * kStages;                  // [2] 1: MMA commit
     uint64_t* p_full = s_full + 2;                          // [2] 128: the softmax threads
     uint64_t* o_done = p_full + 2;                          // [2] 1: MMA commit after the unit's last product
-    uint64_t* q_full = o_done + 2;                          // 256
+    uint64_t* q_full = o_done + 2;                          // 1: the loading warp, or 256: the softmax threads
     // [kMeta] a block's positions. Slot j % 3 is written again for block j + 3, whose K tile needs the
     // ring place of V tile j (five stages), freed after both halves' softmax of block j.
     uint64_t* meta_full = q_full + 1;
+    uint64_t* q_empty = meta_full + kMeta;                  // 1: MMA commit after the unit's last scores
     int* misc = reinterpret_cast<int*>(sm + M::misc);
     volatile int* abort_f = misc;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 2);
@@ -269,10 +270,14 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
     const int ui0 = a.first2[blockIdx.x], ui1 = a.first2[blockIdx.x + 1];
     if ((a.hdr[PH_FORM] & ATTN_FORM_TC) == 0 || ui0 >= ui1) return;
 
+    // Q rows that are changed on their way (scaled to f16's range, negated for a negative scale) are loaded by the
+    // softmax threads; others by warp 3, while the unit before is still in its last block and its epilogue
+    const bool own_q = (!BF && QT == W_BF16) || a.scale_log2 < 0.f;
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) { bar_init(&kv_full[i], 1); bar_init(&kv_empty[i], 1); }
         for (int i = 0; i < 2; ++i) { bar_init(&s_full[i], 1); bar_init(&p_full[i], 128); bar_init(&o_done[i], 1); }
-        bar_init(q_full, 256);
+        bar_init(q_full, own_q ? 256 : 1);
+        bar_init(q_empty, 1);
         for (int i = 0; i < kMeta; ++i) bar_init(&meta_full[i], 1);
         *abort_f = 0;
         for (int i = 0; i < 8; ++i) redo_f[i] = 0;
@@ -589,6 +594,7 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
                     tc_after();
                     for (int t = 0; t < halves; ++t) scores(t, ring.s);
                     if (leader) commit(&kv_empty[ring.s]);
+                    if (leader && nt == 1) commit(q_empty);
                     __syncwarp();
                     ring.next();
                 }
@@ -622,11 +628,50 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
                     if (!ok) break;
                     if (more) {
                         if (leader) commit(&kv_empty[rk.s]);
+                        if (leader && j + 2 == nt) commit(q_empty);
                         __syncwarp();
                         ring.next();
                     }
                 }
                 ok = __all_sync(0xffffffffu, ok);           // the warp goes on, or stops, as one
+            }
+        } else if (warp == 3 && !own_q) {
+            // ---- Q tiles: a lane copies 16 bytes, CH lanes a row
+            constexpr int RI = 32 / CH;                     // rows per copy
+            uint32_t e_ph = 1;                              // (the first unit waits for nothing)
+            bool ok = true;
+            for (int ui = ui0; ui < ui1 && ok; ++ui) {
+                const AttnUnit u = load_unit(a.units2 + ui);
+                if (u.v1 <= u.v0) continue;
+                int64_t at[8];                              // where rows 8 lane .. 8 lane + 7 lie, -1: past the unit
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int r = 8 * lane + i, row = u.row0 + r;
+                    at[i] = -1;
+                    if (r < u.n_row) {
+                        const int tok = row_token(a, u, row);
+                        at[i] = ((int64_t)tok * a.q_tok + (int64_t)(u.head * a.G + row % a.G) * a.q_head) * 2;
+                    }
+                }
+                ok = __all_sync(0xffffffffu, wait(q_empty, e_ph));
+                if (!ok) break;
+                e_ph ^= 1u;
+#pragma unroll 1
+                for (int l = 0; l < 32 / RI; ++l)           // rows 8 (l RI + lane / CH) + i
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int from = l * RI + lane / CH, r = 8 * from + i, ch = lane % CH;
+                        const int64_t o = __shfl_sync(0xffffffffu, at[i], from);
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                         sa(sm + M::q + (r >> 7) * M::tile) + swz(r & 127, ch)),
+                                     "l"(static_cast<const uint8_t*>(a.q) + (o >= 0 ? o : 0) + 16 * ch), "r"(o >= 0 ? 16 : 0)
+                                     : "memory");
+                    }
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
+                to_async_proxy();
+                __syncwarp();
+                if (lane == 0) bar_arrive(q_full);
             }
         }
         __syncwarp();
@@ -637,13 +682,13 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
         const int ht = tid - 32 * (kSoft0 + 4 * t);         // thread of the half
         uint32_t s_ph = 0, o_ph = 0;
         int with_keys = 0;
+        AttnUnit u = load_unit(a.units2 + ui0);
         for (int ui = ui0; ui < ui1; ++ui) {
-            const AttnUnit u = load_unit(a.units2 + ui);
             const int kvh = u.head;
             const int nt = (u.v1 - u.v0 + kKeys - 1) / kKeys, halves = u.n_row > 128 ? 2 : 1;
             const int slot = with_keys & 7;
             if (nt > 0) ++with_keys;
-            if (nt > 0) {
+            if (nt > 0 && own_q) {
                 // neighbouring threads hold a row: 8 values each
                 uint8_t* qs = sm + M::q + t * M::tile;
                 constexpr int RQ = 128 / CH;                // rows the half loads at once
@@ -805,6 +850,7 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
                 o_ph ^= 1u;
                 tc_after();
             }
+            const AttnUnit u_nxt = load_unit(a.units2 + min(ui + 1, ui1 - 1));   // (on its way meanwhile)
             // ---- epilogue: a unit alone writes its rows, one of several its partial result
             if (live) {
                 bool finite = l <= 3.0e38f && m <= 3.0e38f;
@@ -819,18 +865,19 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
                         tld32(ob + c, o);
                         ld_wait();
                     }
+                    float x[32];
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        float x[4];
+                    for (int i = 0; i < 32; ++i) {
+                        x[i] = nt > 0 ? __uint_as_float(o[i]) * sv : 0.f;
+                        finite = finite && fabsf(x[i]) <= 3.0e38f;
+                        if (u.n_chunk == 1) x[i] = l == 0.f ? 0.f : x[i] * inv;
+                    }
+                    if (!mine) continue;
+                    if (u.n_chunk == 1) {
+                        store_out32(a, oi + c, x);
+                    } else {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            x[e] = nt > 0 ? __uint_as_float(o[i + e]) * sv : 0.f;
-                            finite = finite && fabsf(x[e]) <= 3.0e38f;
-                            if (u.n_chunk == 1) x[e] = l == 0.f ? 0.f : x[e] * inv;
-                        }
-                        if (!mine) continue;
-                        if (u.n_chunk == 1) store_out4(a, oi + c + i, x);
-                        else *reinterpret_cast<float4*>(a.part_o + at * HD + c + i) = make_float4(x[0], x[1], x[2], x[3]);
+                        for (int i = 0; i < 32; i += 8) store32b(a.part_o + at * HD + c + i, reinterpret_cast<const uint32_t*>(x) + i);
                     }
                 }
                 if (!finite && mine) redo_f[slot] = 1;
@@ -857,6 +904,7 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
                 asm volatile("bar.sync 1, 256;" ::: "memory");
                 if (ht == 0 && t == 0) redo_f[slot] = 0;
             }
+            u = u_nxt;
         }
     }
     __syncthreads();

@@ -444,6 +444,8 @@ int llm_attn_run(llm_attn_plan* p, const void* q, int64_t q_stride_tok, int64_t 
     a.q = q; a.q_tok = p->shape.max_tok > 1 ? q_stride_tok : 0; a.q_head = p->shape.n_head > 1 ? q_stride_head : 0;
     a.out = out; a.o_tok = p->shape.max_tok > 1 ? o_stride_tok : 0; a.o_head = p->shape.n_head > 1 ? o_stride_head : 0;
     a.out_kind = p->shape.type == LLM_TYPE_F32 ? AO_F32 : p->shape.type == LLM_TYPE_F16 ? AO_F16 : AO_BF16;
+    const int64_t oes = esize(p->shape.type);
+    a.out32 = (reinterpret_cast<uintptr_t>(out) & 31) == 0 && a.o_tok * oes % 32 == 0 && a.o_head * oes % 32 == 0;
     a.scale_log2 = p->scale_log2;
     a.window = p->shape.window;
     a.n_sink = p->shape.n_sink;

@@ -86,6 +86,7 @@ struct AttnPagedArgs {
     void* out_lo = nullptr;                      // AO_BF16_PAIR: the low terms
     int32_t out_kind = AO_F16;
     int64_t o_tok = 0, o_head = 0;
+    bool out32 = false;                          // the rows of out start on 32-byte boundaries
     float scale_log2 = 0.f;                      // scale * log2(e)
     int32_t window = 0, n_sink = 0;
     const int32_t* hdr = nullptr;
