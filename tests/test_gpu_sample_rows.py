@@ -100,6 +100,21 @@ def test_16_bit_logits_have_many_ties(L, dt):
     check(L, logits, ps, rng.random(40))
 
 
+def test_distributions(L):
+    """Rows whose top lies in a few bins, or spread over many: offsets and scales of every size, one outlier, long
+    tails, log probabilities, masked vocabularies."""
+    rng = np.random.default_rng(2)
+    V = 60000
+    g = rng.normal(size=V)
+    rows = [g * 1e-4, g * 1e4, g + 1000, g - 1e6, np.where(np.arange(V) == 77, 1e4, g), rng.standard_cauchy(V),
+            np.log(rng.dirichlet(np.full(V, 0.05)) + 1e-30), np.where(rng.random(V) < 0.999, -np.inf, g), np.exp(3 * g), -np.exp(3 * g),
+            np.round(g * 3), np.where(np.arange(V) < 30000, 5.0, g)]
+    logits = torch.from_numpy(np.stack(rows)).float().cuda()
+    for kw in (dict(top_k=40), dict(top_k=4096, top_p=0.9), dict(top_k=1000, min_p=0.01, temperature=1.3), dict(top_k=59999),
+               dict(top_k=513, temperature=0.5)):
+        check(L, logits, [SamplerParams(**kw)] * len(rows), rng.random(len(rows)))
+
+
 def test_flat_and_two_valued_rows(L):
     V = 20000
     x = torch.zeros(6, V, device="cuda")

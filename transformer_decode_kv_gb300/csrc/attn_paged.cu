@@ -160,10 +160,11 @@ attn_rows_kernel(AttnPagedArgs a) {
     int& s_flag = *reinterpret_cast<int*>(s_l + kWarps);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     if (a.pdl) asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");      // the 256-row tiles of a mixed plan may start
+    const int ui0 = a.first1[blockIdx.x], ui1 = a.first1[blockIdx.x + 1];   // (on their way with the header)
     if (form_missing(a) || (a.hdr[PH_FORM] & (ROWS == 8 ? ATTN_FORM_ROWS8 : ATTN_FORM_ROWS16)) == 0) return;
-    const int ui1 = a.first1[blockIdx.x + 1];
 
-    for (int ui = a.first1[blockIdx.x]; ui < ui1; ++ui) {
+    for (int ui = ui0; ui < ui1; ++ui) {
         const AttnUnit u = load_unit(a.units1 + ui);
         const int kvh = u.head;
         const uint8_t* kbase = a.kv.k + (int64_t)kvh * a.kv.sb_head;
@@ -588,7 +589,7 @@ attn_rows_kernel(AttnPagedArgs a) {
             if (threadIdx.x == 0) s_flag = count_unit(a, u);
             __syncthreads();
             if (s_flag)
-                for (int r = warp; r < u.n_row; r += kWarps) merge_row<HD>(a, u, ROWS, r);
+                for (int r = 2 * warp; r < u.n_row; r += 2 * kWarps) merge_rows<HD, 2>(a, a.part_o, a.part_ml, u, ROWS, r);
         }
         __syncthreads();                                    // shared memory is free for the next unit
     }
@@ -639,9 +640,9 @@ bool attn_paged_types_ok(int32_t q, int32_t kv) {
 
 bool launch_attn_paged(const AttnPagedArgs& a, cudaStream_t st) {
     if (!attn_paged_types_ok(a.q_type, a.kv.type)) return false;
-    if ((a.form & ATTN_FORM_TC) && !launch_attn_paged_tc(a, st)) return false;
     if ((a.form & ATTN_FORM_ROWS8) && !go_rows<8>(a, st)) return false;
-    return (a.form & ATTN_FORM_ROWS16) == 0 || go_rows<16>(a, st);
+    if ((a.form & ATTN_FORM_ROWS16) && !go_rows<16>(a, st)) return false;
+    return (a.form & ATTN_FORM_TC) == 0 || launch_attn_paged_tc(a, st);
 }
 
 }  // namespace llm

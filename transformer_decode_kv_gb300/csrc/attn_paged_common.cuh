@@ -200,62 +200,79 @@ __device__ __noinline__ void careful_row(const AttnPagedArgs& a, const AttnUnit&
     }
 }
 
-// Merge the partial results of row r of a cut tile into the output, a warp per row; in the units' order, so the
-// result does not depend on which of them was last. rows: the tile form's rows. A lane weighs up to one unit in
-// 32 at a time (weight exp2(m - M) against the largest reference M), then the warp adds the units' rows, HD / 32
-// neighbouring values per lane.
-template <int HD>
-__device__ void merge_row(const AttnPagedArgs& a, const AttnUnit& u, int rows, int r) {
+// Merge the partial results of rows r0 .. r0 + NR - 1 (those below u.n_row) of a cut tile into the output, by one warp;
+// in the units' order, so the result does not depend on which of them was last. rows: the tile form's rows. A
+// lane weighs up to one unit in 32 at a time (weight exp2(m - M) against the largest reference M), then the warp
+// adds the units' rows, HD / 32 neighbouring values per lane; NR rows keep NR times as many loads under way.
+template <int HD, int NR>
+__device__ void merge_rows(const AttnPagedArgs& a, const float* part_o, const float2* part_ml, const AttnUnit& u, int rows,
+                           int r0) {
     constexpr int D = HD / 32;
     const int lane = threadIdx.x & 31;
-    float M = -INFINITY, L = 0.f, o[D];
+    float M[NR], L[NR], o[NR][D];
+    const float2* ml = part_ml + (int64_t)u.part * rows + r0;
 #pragma unroll
-    for (int d = 0; d < D; ++d) o[d] = 0.f;
-    const float2* ml = a.part_ml + (int64_t)u.part * rows + r;
-    for (int c = lane; c < u.n_chunk; c += 32) M = fmaxf(M, __ldcg(&ml[(int64_t)c * rows]).x);
+    for (int k = 0; k < NR; ++k) {
+        M[k] = -INFINITY;
+        L[k] = 0.f;
 #pragma unroll
-    for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
+        for (int d = 0; d < D; ++d) o[k][d] = 0.f;
+        for (int c = lane; c < u.n_chunk; c += 32)
+            if (r0 + k < u.n_row) M[k] = fmaxf(M[k], __ldcg(&ml[(int64_t)c * rows + k]).x);
+    }
+#pragma unroll
+    for (int k = 0; k < NR; ++k)
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) M[k] = fmaxf(M[k], __shfl_xor_sync(0xffffffffu, M[k], s));
     for (int c0 = 0; c0 < u.n_chunk; c0 += 32) {
-        float f = 0.f;
-        if (c0 + lane < u.n_chunk) {
-            const float2 x = __ldcg(&ml[(int64_t)(c0 + lane) * rows]);
-            // a unit without a visible key has nothing to add (its reference is -inf); NaN sums pass
-            if (x.x != -INFINITY || x.y != 0.f) {
-                f = x.x == M ? 1.f : exp2f(x.x - M);
-                L += f * x.y;
+        float f[NR];
+#pragma unroll
+        for (int k = 0; k < NR; ++k) {
+            f[k] = 0.f;
+            if (c0 + lane < u.n_chunk && r0 + k < u.n_row) {
+                const float2 x = __ldcg(&ml[(int64_t)(c0 + lane) * rows + k]);
+                // a unit without a visible key has nothing to add (its reference is -inf); NaN sums pass
+                if (x.x != -INFINITY || x.y != 0.f) {
+                    f[k] = x.x == M[k] ? 1.f : exp2f(x.x - M[k]);
+                    L[k] += f[k] * x.y;
+                }
             }
         }
         const int n = min(32, u.n_chunk - c0);
-        const float* p = a.part_o + ((int64_t)(u.part + c0) * rows + r) * HD + lane * D;
-#pragma unroll 4
-        for (int c = 0; c < n; ++c) {
-            const float fc = __shfl_sync(0xffffffffu, f, c);
-            const float* q = p + (int64_t)c * rows * HD;
-            float v[D];
-            if constexpr (D == 4) {
-                const float4 w = __ldcg(reinterpret_cast<const float4*>(q));
-                v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
-            } else if constexpr (D == 2) {
-                const float2 w = __ldcg(reinterpret_cast<const float2*>(q));
-                v[0] = w.x; v[1] = w.y;
-            } else {
-                v[0] = __ldcg(q);
-            }
+        const float* p = part_o + ((int64_t)(u.part + c0) * rows + r0) * HD + lane * D;
+#pragma unroll 2
+        for (int c = 0; c < n; ++c)
 #pragma unroll
-            for (int d = 0; d < D; ++d) o[d] += fc != 0.f ? fc * v[d] : 0.f;
-        }
+            for (int k = 0; k < NR; ++k) {
+                const float fc = __shfl_sync(0xffffffffu, f[k], c);
+                const float* q = p + ((int64_t)c * rows + k) * HD;
+                if (fc == 0.f) continue;                    // (also rows that are not the tile's)
+                if constexpr (D == 4) {
+                    const float4 w = __ldcg(reinterpret_cast<const float4*>(q));
+                    o[k][0] += fc * w.x; o[k][1] += fc * w.y; o[k][2] += fc * w.z; o[k][3] += fc * w.w;
+                } else if constexpr (D == 2) {
+                    const float2 w = __ldcg(reinterpret_cast<const float2*>(q));
+                    o[k][0] += fc * w.x; o[k][1] += fc * w.y;
+                } else {
+                    o[k][0] += fc * __ldcg(q);
+                }
+            }
     }
 #pragma unroll
-    for (int s = 16; s > 0; s >>= 1) L += __shfl_xor_sync(0xffffffffu, L, s);
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    const int row = u.row0 + r, tok = row_token(a, u, row);
-    const int64_t at = (int64_t)tok * a.o_tok + (int64_t)(u.head * a.G + row % a.G) * a.o_head + lane * D;
+    for (int k = 0; k < NR; ++k) {
 #pragma unroll
-    for (int d = 0; d < D; ++d) o[d] = L == 0.f ? 0.f : o[d] * inv;
-    if constexpr (D == 4) store_out4(a, at, o);
-    else
+        for (int s = 16; s > 0; s >>= 1) L[k] += __shfl_xor_sync(0xffffffffu, L[k], s);
+        if (r0 + k >= u.n_row) continue;
+        const float inv = L[k] == 0.f ? 0.f : 1.f / L[k];
+        const int row = u.row0 + r0 + k, tok = row_token(a, u, row);
+        const int64_t at = (int64_t)tok * a.o_tok + (int64_t)(u.head * a.G + row % a.G) * a.o_head + lane * D;
 #pragma unroll
-        for (int d = 0; d < D; ++d) store_out1(a, at + d, o[d]);
+        for (int d = 0; d < D; ++d) o[k][d] = L[k] == 0.f ? 0.f : o[k][d] * inv;
+        if constexpr (D == 4) store_out4(a, at, o[k]);
+        else
+#pragma unroll
+            for (int d = 0; d < D; ++d) store_out1(a, at + d, o[k][d]);
+    }
 }
 
 // Count a unit of a cut tile as finished, by one thread after a barrier behind the writes of its partial results

@@ -232,7 +232,7 @@ struct MetaAt {
 };
 
 template <int HD, int CT, int QT>
-__global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, TmaRuns runs,
+__global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, TmaRuns runs, int beside,
                                                                const __grid_constant__ CUtensorMap map_k,
                                                                const __grid_constant__ CUtensorMap map_v) {
     using M = Smem<HD>;
@@ -261,14 +261,20 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
     float* s0 = reinterpret_cast<float*>(misc + 12);        // [8][2] E4M3: scale of the K and V tiles
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (a.pdl) asm volatile("griddepcontrol.wait;" ::: "memory");
+    // beside: the small tiles of the same plan run just before; nothing here depends on them, so this kernel
+    // starts where they leave SMs free, and waits for them at its end
+    if (a.pdl && !beside) asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
     if (form_missing(a)) return;
     if (sa(sm) & 1023u) {                                   // the swizzle patterns repeat every 1024 bytes
         if (tid == 0 && a.err) atomicOr(a.err, ERR_TIMEOUT);
         return;
     }
     const int ui0 = a.first2[blockIdx.x], ui1 = a.first2[blockIdx.x + 1];
-    if ((a.hdr[PH_FORM] & ATTN_FORM_TC) == 0 || ui0 >= ui1) return;
+    if ((a.hdr[PH_FORM] & ATTN_FORM_TC) == 0 || ui0 >= ui1) {
+        if (beside) asm volatile("griddepcontrol.wait;" ::: "memory");
+        return;
+    }
 
     // Q rows that are changed on their way (scaled to f16's range, negated for a negative scale) are loaded by the
     // softmax threads; others by warp 3, while the unit before is still in its last block and its epilogue
@@ -857,7 +863,7 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
                 const float inv = l == 0.f ? 0.f : 1.f / l, sv = F8 && nt > 0 ? s0[2 * slot + 1] : 1.f;
                 const int64_t at = (int64_t)(u.part + u.chunk) * kUnitRows2 + 128 * t + r;
                 const int64_t oi = (int64_t)tok * a.o_tok + (int64_t)(kvh * a.G + row % a.G) * a.o_head;
-                if (u.n_chunk > 1 && mine) a.part_ml[at] = make_float2(m, l);
+                if (u.n_chunk > 1 && mine) a.part_ml2[at] = make_float2(m, l);
 #pragma unroll 1
                 for (int c = 0; c < HD; c += 32) {
                     uint32_t o[32];
@@ -877,7 +883,7 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
                         store_out32(a, oi + c, x);
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8) store32b(a.part_o + at * HD + c + i, reinterpret_cast<const uint32_t*>(x) + i);
+                        for (int i = 0; i < 32; i += 8) store32b(a.part_o2 + at * HD + c + i, reinterpret_cast<const uint32_t*>(x) + i);
                     }
                 }
                 if (!finite && mine) redo_f[slot] = 1;
@@ -897,9 +903,9 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
 #pragma unroll
                     for (int d = 0; d < HD / 32; ++d) {
                         if (u.n_chunk == 1) store_out1(a, oi + lane * (HD / 32) + d, rl == 0.f ? 0.f : o[d] * inv);
-                        else a.part_o[at * HD + lane * (HD / 32) + d] = o[d];
+                        else a.part_o2[at * HD + lane * (HD / 32) + d] = o[d];
                     }
-                    if (u.n_chunk > 1 && lane == 0) a.part_ml[at] = make_float2(rm, rl);
+                    if (u.n_chunk > 1 && lane == 0) a.part_ml2[at] = make_float2(rm, rl);
                 }
                 asm volatile("bar.sync 1, 256;" ::: "memory");
                 if (ht == 0 && t == 0) redo_f[slot] = 0;
@@ -907,11 +913,12 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
             u = u_nxt;
         }
     }
+    if (beside) asm volatile("griddepcontrol.wait;" ::: "memory");
     __syncthreads();
     if (warp == kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
 }
 
-// The rows of the cut tiles from their units' partial results, a warp per row. A kernel of its own: the last unit of a
+// The rows of the cut tiles from their units' partial results, four rows a warp. A kernel of its own: the last unit of a
 // tile to finish would do 256 rows alone while the other SMs are idle (512 tokens over 8192 keys: 170 us so, against
 // 114 us in all with this kernel).
 constexpr int kMergeThr = 256;
@@ -920,10 +927,12 @@ template <int HD>
 __global__ void __launch_bounds__(kMergeThr) attn_tc_merge_kernel(AttnPagedArgs a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if ((a.hdr[PH_FORM] & ~a.form) != 0 || (a.hdr[PH_FORM] & ATTN_FORM_TC) == 0) return;
-    const int n = a.hdr[PH_CUTS2] * kUnitRows2;
+    constexpr int NR = 4;                                   // rows per warp
+    const int n = a.hdr[PH_CUTS2] * (kUnitRows2 / NR);
     for (int x = blockIdx.x * (kMergeThr / 32) + (threadIdx.x >> 5); x < n; x += gridDim.x * (kMergeThr / 32)) {
-        const AttnUnit u = load_unit(a.units2 + a.cuts2[x / kUnitRows2]);
-        if (x % kUnitRows2 < u.n_row) merge_row<HD>(a, u, kUnitRows2, x % kUnitRows2);
+        const AttnUnit u = load_unit(a.units2 + a.cuts2[x / (kUnitRows2 / NR)]);
+        const int r = x % (kUnitRows2 / NR) * NR;
+        if (r < u.n_row) merge_rows<HD, NR>(a, a.part_o2, a.part_ml2, u, kUnitRows2, r);
     }
 }
 
@@ -980,11 +989,12 @@ bool go(const AttnPagedArgs& a, cudaStream_t st) {
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = a.pdl ? 1 : 0;
+    const int beside = (a.form & ~ATTN_FORM_TC) != 0;
+    cfg.numAttrs = a.pdl || beside ? 1 : 0;
     CUtensorMap mk{}, mv{};
     TmaRuns runs{0, false, false};
     if (CT != W_F8) runs = cell_runs(a.kv, &mk, &mv);
-    if (cudaLaunchKernelEx(&cfg, attn_tc_rows_kernel<HD, CT, QT>, a, runs, mk, mv) != cudaSuccess) return false;
+    if (cudaLaunchKernelEx(&cfg, attn_tc_rows_kernel<HD, CT, QT>, a, runs, beside, mk, mv) != cudaSuccess) return false;
     // (launched early, it waits for the kernel above)
     cfg.gridDim = dim3(4 * a.n_sm);
     cfg.blockDim = dim3(kMergeThr);

@@ -301,8 +301,7 @@ llm_attn_plan* llm_attn_plan_init(const llm_attn_shape* s, const llm_kv_pages* k
     p->off_units[1] = p->off_units[0] + up(p->caps.units1 * sizeof(AttnUnit));
     p->off_table = p->off_units[1] + up(p->caps.units2 * sizeof(AttnUnit));
     p->bytes = p->off_table + up((size_t)s->max_table * sizeof(int32_t));
-    const int64_t rows = plan_part_rows(p->caps);
-    // the two forms run one after the other on a stream: they share the partial results' memory
+    const int64_t rows = plan_part_rows(p->caps, true);
     auto get = [&](auto** q, size_t n) {
         void* v = nullptr;
         if (e == cudaSuccess) e = cudaMalloc(&v, n);
@@ -456,7 +455,10 @@ int llm_attn_run(llm_attn_plan* p, const void* q, int64_t q_stride_tok, int64_t 
     a.units1 = reinterpret_cast<const AttnUnit*>(p->d_buf + p->off_units[0]);
     a.units2 = reinterpret_cast<const AttnUnit*>(p->d_buf + p->off_units[1]);
     a.table = reinterpret_cast<const int32_t*>(p->d_buf + p->off_table);
-    a.part_o = p->part_o; a.part_ml = p->part_ml; a.tickets = p->tickets; a.err = p->err;
+    a.part_o = p->part_o; a.part_ml = p->part_ml;
+    a.part_o2 = p->part_o + plan_part_rows(p->caps, false) * kv->head_dim;
+    a.part_ml2 = p->part_ml + plan_part_rows(p->caps, false);
+    a.tickets = p->tickets; a.err = p->err;
     a.form = p->plan.form();
     a.n_sm = p->ps.n_sm;
     if (!launch_attn_paged(a, static_cast<cudaStream_t>(stream))) return failed("attention launch", cudaGetLastError());

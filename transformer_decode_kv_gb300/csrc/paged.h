@@ -100,6 +100,8 @@ struct AttnPagedArgs {
     const int32_t* key_pos = nullptr;            // positions of the page-table's keys, pages of one cell
     float* part_o = nullptr;                     // [part][rows][hd] unnormalised
     float2* part_ml = nullptr;                   // [part][rows] (running max, sum)
+    float* part_o2 = nullptr;                    // the same of the 256-row tiles
+    float2* part_ml2 = nullptr;
     int32_t* tickets = nullptr;                  // zero between launches
     uint32_t* err = nullptr;
     int32_t form = 0;                            // forms the caller launches
@@ -143,10 +145,8 @@ void build_paged_plan(const PlanShape& s, const std::vector<PlanSeq>& seqs, Page
 // Upper bounds for buffers over every plan of at most max_tok tokens in max_seq sequences.
 struct PagedPlanCaps { int64_t units1, units2, ctas1, ctas2, tickets, parts1, parts2; };
 PagedPlanCaps paged_plan_caps(const PlanShape& s, int32_t max_tok, int32_t max_seq);
-// Partial results of the larger form: rows of head_dim values.
-inline int64_t plan_part_rows(const PagedPlanCaps& c) {
-    return c.parts1 * 16 > c.parts2 * kUnitRows2 ? c.parts1 * 16 : c.parts2 * kUnitRows2;
-}
+// Partial results of both forms: rows of head_dim values, the small tiles' first.
+inline int64_t plan_part_rows(const PagedPlanCaps& c, bool both) { return c.parts1 * 16 + (both ? c.parts2 * kUnitRows2 : 0); }
 
 // ---- the sampler chain per row (sample_rows.cu)
 struct SampleRowsArgs {

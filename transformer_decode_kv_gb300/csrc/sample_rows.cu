@@ -5,11 +5,15 @@
 // A row is read once: each CTA of its cluster keeps a contiguous slice in shared memory as
 // order-preserving 32-bit keys. The candidates' order is (logit descending, id ascending), so an element is
 // the 64-bit number key << 32 | ~id, and every cut-off (top-k, top-p, min-p, and the pick itself) is "the
-// elements down to the first one where a running sum reaches a target". Such an element is found without
-// sorting, by a radix select over the 64-bit numbers: per digit a histogram of the sum (a count, or
-// weights), summed over the cluster through distributed shared memory, and a scan from the top; it
-// stops as soon as the bin found is needed whole, or holds one element. When at most kListMax candidates
-// are left after top-k they move into the first CTA, which goes on alone.
+// elements down to the first one where a running sum reaches a target".
+//
+// Up to kListMax candidates (top_k): one histogram of 512 bins between the row's largest value and its mean finds an
+// upper set of at least k elements that hardly exceeds k (a second histogram of the last bin where the first
+// leaves too many); they move into the first CTA, which sorts them and goes on with prefix sums.
+// More candidates, or rows where that set stays too large (ties, infinities): every cut-off is found where the
+// elements lie, by a radix select over the 64-bit numbers: per digit a histogram of the running sum (a
+// count, or weights), summed over the cluster through distributed shared memory, and a scan from the top; it
+// stops as soon as the bin found is needed whole, or holds one element.
 //
 // Sums of probabilities are integers: a weight exp((l - l_max) / t) is rounded to a multiple of 2^-44, so
 // sums of up to 2^18 of them are exact in 64 bits whatever their order, and the pick depends on neither
@@ -37,6 +41,7 @@ constexpr int kThr = 512;
 constexpr int kWarps = kThr / 32;
 constexpr int kListMax = 4096;
 constexpr int kBins = 256;
+constexpr int kNear = 512;                                   // bins from the largest value to the mean; kThr of them
 constexpr int kClusterMax = 8;
 constexpr int kSliceMax = 45056;                             // keys of a slice: 176 KB
 constexpr int kWeightBits = 44;
@@ -115,37 +120,45 @@ __device__ __forceinline__ uint64_t weight_of(uint32_t key, float top, const Slo
 
 struct Shared {
     uint64_t sum[2][kBins];                                  // histograms, alternating
-    uint32_t cnt[2][kBins];
+    union {
+        uint32_t cnt[2][kBins];
+        uint32_t near[kNear];                                // elements by distance from the largest
+    };
+    uint64_t best;                                           // the slice's first element
+    float total_v[kClusterMax];                              // the slices' sums of finite values, and how many
+    uint32_t n_finite[kClusterMax];
+    uint64_t bests[kClusterMax];
+    float wsumf[kWarps];
+    uint32_t near_bin, near_before, near_count;
     uint64_t wsum[kWarps];
     uint32_t wcnt[kWarps];
     uint64_t found_before, total;
-    uint32_t found_bin, found_count, n_list, tops[kClusterMax];
+    uint32_t found_bin, found_count, n_list;
     int found;
 };
 
+constexpr size_t kSharedBytes = (sizeof(Shared) + 15) / 16 * 16;
+constexpr int kPer = kListMax / kThr;                        // listed elements per thread
+static_assert(kListMax >= 2 * kThr, "places for both orders");
+static_assert(kNear == kThr, "a thread per bin");
+
 enum Measure : int { M_COUNT = 0, M_WEIGHT = 1 };
 
-// One CTA's elements: its slice of the row, or the list.
+// A CTA's slice of the row.
 struct Elems {
-    const uint32_t* keys;                                    // slice (null: the list)
-    const uint64_t* list;
+    const uint32_t* keys;
     int n, base;
-    __device__ __forceinline__ uint64_t at(int i) const {
-        return list ? list[i] : ((uint64_t)keys[i] << 32) | (uint32_t)~(uint32_t)(base + i);
-    }
+    __device__ __forceinline__ uint64_t at(int i) const { return ((uint64_t)keys[i] << 32) | (uint32_t)~(uint32_t)(base + i); }
 };
 
-// Everything a select needs to know about its group: the whole cluster, or the first CTA alone.
+// The CTAs of a row.
 struct Group {
     Shared* sh;
     int size;                                                // CTAs
     int phase;                                               // histogram in use
 };
 
-__device__ __forceinline__ void group_sync(const Group& g) {
-    if (g.size > 1) cg::this_cluster().sync();
-    else __syncthreads();
-}
+__device__ __forceinline__ void group_sync(const Group&) { cg::this_cluster().sync(); }
 
 // The bin histogram of the elements x >= cut whose digits above `shift` equal prefix's.
 __device__ void histogram(const Elems& el, Group& g, Measure what, uint64_t cut, uint64_t prefix, int shift, int bits,
@@ -194,7 +207,7 @@ __device__ void scan_bins(Group& g, Measure what, uint64_t before, uint64_t targ
     if (t < kBins) {
         const int b = kBins - 1 - t;
         for (int r = 0; r < g.size; ++r) {
-            const Shared* o = g.size > 1 ? cg::this_cluster().map_shared_rank(&sh, r) : &sh;
+            const Shared* o = cg::this_cluster().map_shared_rank(&sh, r);
             n += o->cnt[g.phase][b];
             if (what == M_WEIGHT) s += o->sum[g.phase][b];
         }
@@ -263,23 +276,167 @@ __device__ uint64_t total_weight(const Elems& el, Group& g, uint64_t cut, float 
     group_sync(g);
     uint64_t z = 0ull;
     for (int r = 0; r < g.size; ++r)
-        z += (g.size > 1 ? cg::this_cluster().map_shared_rank(&sh, r) : &sh)->sum[g.phase][0];
+        z += cg::this_cluster().map_shared_rank(&sh, r)->sum[g.phase][0];
     g.phase ^= 1;
     __syncthreads();
     return z;
 }
 
+// The key of the least float l with l - top >= ln(min_p) in double (the top's own key at most).
+__device__ __forceinline__ uint32_t min_p_key(float top, float min_p) {
+    const double lim = (double)top + log((double)fminf(min_p, 1.f));
+    float f = (float)lim;
+    if ((double)f < lim) f = nextafterf(f, INFINITY);
+    return min(key_of(f), key_of(top));
+}
+// The pick is the first candidate whose running weight exceeds u z.
+__device__ __forceinline__ uint64_t pick_target(uint64_t z, float u) {
+    u = fminf(fmaxf(u, 0.f), 0.99999994f);                   // (NaN: 0)
+    return min(z, (uint64_t)floor((double)u * (double)z) + (uint64_t)1);
+}
 // x * f rounded as a double, up to a whole number, within [1, x] (f in (0, 1))
 __device__ __forceinline__ uint64_t share_up(uint64_t x, float f) {
     const double t = ceil((double)f * (double)x);
     return t < 1.0 ? 1ull : min(x, (uint64_t)t);
 }
 
+// Inclusive prefix sum over the block; *total the sum of all (kThr threads, sh.wsum free before and after).
+__device__ uint64_t block_scan(Shared& sh, uint64_t v, uint64_t* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint64_t x = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += x;
+    }
+    if (lane == 31) sh.wsum[warp] = v;
+    __syncthreads();
+    uint64_t add = 0ull, all = 0ull;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        const uint64_t x = sh.wsum[w];
+        if (w < warp) add += x;
+        all += x;
+    }
+    *total = all;
+    __syncthreads();
+    return v + add;
+}
+
+// The first of the m sorted elements (thread t holds w[] of kPer t ..) where the running weight reaches target;
+// m - 1 if none does. `before`: the thread's exclusive prefix.
+__device__ int first_reaching(Shared& sh, const uint64_t* w, uint64_t before, int m, uint64_t target) {
+    if (threadIdx.x == 0) sh.found = m - 1;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const int i = threadIdx.x * kPer + j;
+        if (i < m && before < target && before + w[j] >= target) sh.found = i;   // one thread's, once
+        before += w[j];
+    }
+    __syncthreads();
+    const int f = sh.found;
+    __syncthreads();
+    return f;
+}
+
+// The chain over n listed elements, an upper set of the row with at least min(k, candidates) of them: sorted, then
+// cut to k, by top-p and min-p, then the pick. One CTA; list has kListMax places.
+__device__ int32_t list_chain(Shared& sh, uint64_t* list, int n, int k, float top_p, float min_p, float temp,
+                              float u) {
+    const int tid = threadIdx.x;
+    if (n <= kThr) {
+        // few: a thread per element counts those before it; sorted into the list's next places
+        uint64_t* spare = list + kThr;
+        const uint64_t x = tid < n ? list[tid] : 0ull;
+        int r = 0;
+        for (int i = 0; i < n; ++i) r += list[i] > x;
+        if (tid < n) spare[r] = x;
+        __syncthreads();
+        list = spare;
+    } else {
+        int P = 2 * kThr;
+        while (P < n) P <<= 1;
+        for (int i = n + tid; i < P; i += kThr) list[i] = 0ull;
+        __syncthreads();
+        for (int size = 2; size <= P; size <<= 1)
+            for (int stride = size >> 1; stride > 0; stride >>= 1) {
+                for (int p = tid; p < P / 2; p += kThr) {
+                    const int i = 2 * p - (p & (stride - 1)), j = i + stride;
+                    const uint64_t x = list[i], y = list[j];
+                    if ((x < y) == ((i & size) == 0)) { list[i] = y; list[j] = x; }   // descending
+                }
+                __syncthreads();
+            }
+    }
+    uint64_t x[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) x[j] = tid * kPer + j < n ? list[tid * kPer + j] : 0ull;
+    const float top = value_of((uint32_t)(list[0] >> 32));
+    int m = min(n, k);
+    uint64_t w[kPer], z, loc;
+    auto weigh = [&](const Slope c) {
+        loc = 0ull;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            w[j] = tid * kPer + j < m ? weight_of((uint32_t)(x[j] >> 32), top, c) : 0ull;
+            loc += w[j];
+        }
+        return block_scan(sh, loc, &z) - loc;
+    };
+    if (top_p < 1.f) {
+        const uint64_t before = weigh(slope_of(1.0));
+        m = first_reaching(sh, w, before, m, share_up(z, top_p)) + 1;
+    }
+    if (min_p > 0.f) {
+        const uint32_t least = min_p_key(top, min_p);
+        int c = 0;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) c += tid * kPer + j < m && (uint32_t)(x[j] >> 32) >= least;
+        uint64_t all;
+        block_scan(sh, (uint64_t)c, &all);
+        m = max(1, (int)all);
+    }
+    const uint64_t before = weigh(slope_of((double)temp));
+    const int f = first_reaching(sh, w, before, m, pick_target(z, u));
+    return (int32_t)~(uint32_t)list[f];
+}
+
+// Bin of value v by its distance from the largest, 0 the nearest; kNear or more: farther than the mean.
+__device__ __forceinline__ uint32_t near_bin(float v, float top, float scale) {
+    const float d = (top - v) * scale;                       // (monotone: the elements up to a bin are an upper set)
+    return d < (float)kNear ? (uint32_t)d : (uint32_t)kNear; // NaN and -infinity are far
+}
+
+// sh.near summed over the cluster, and the bin where the count from the top reaches k: sh.near_*; near_count = 0 if
+// none does.
+__device__ void near_scan(Shared& sh, int CL, uint32_t k) {
+    cg::cluster_group cluster = cg::this_cluster();
+    if (threadIdx.x == 0) sh.near_count = 0u;
+    cluster.sync();
+    uint32_t n = 0u;
+    for (int r = 0; r < CL; ++r) n += cluster.map_shared_rank(&sh, r)->near[threadIdx.x];
+    uint64_t all;
+    const uint32_t inc = (uint32_t)block_scan(sh, n, &all);
+    if (inc >= k && inc - n < k) {
+        sh.near_bin = threadIdx.x;
+        sh.near_before = inc - n;
+        sh.near_count = n;
+    }
+    cluster.sync();                                          // (near may be written again)
+}
+
 template <int T>
-__global__ void __launch_bounds__(kThr) sample_rows_kernel(SampleRowsArgs a, int slice) {
+__device__ __forceinline__ float logit(const void* p, int64_t i) {
+    if constexpr (T == W_F32) return static_cast<const float*>(p)[i];
+    else if constexpr (T == W_F16) return __half2float(static_cast<const __half*>(p)[i]);
+    else return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+
+template <int T>
+__global__ void __launch_bounds__(kThr) sample_rows_kernel(SampleRowsArgs a, int slice, int aligned) {
     extern __shared__ __align__(16) uint8_t raw[];
     Shared& sh = *reinterpret_cast<Shared*>(raw);
-    uint64_t* list = reinterpret_cast<uint64_t*>(raw + sizeof(Shared));                // [kListMax], first CTA
+    uint64_t* list = reinterpret_cast<uint64_t*>(raw + kSharedBytes);                  // [kListMax], first CTA
     uint32_t* keys = reinterpret_cast<uint32_t*>(list + kListMax);                     // [slice]
     uint32_t* marked = keys + slice;                                                  // a bit per key
     cg::cluster_group cluster = cg::this_cluster();
@@ -288,18 +445,39 @@ __global__ void __launch_bounds__(kThr) sample_rows_kernel(SampleRowsArgs a, int
     const int64_t row = a.row ? a.row[e] : e;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int b0 = rank * slice, n = max(0, min(slice, a.V - b0));
+    const float temp = a.temperature ? a.temperature[e] : 0.f;
+    const float top_p = a.top_p ? a.top_p[e] : 1.f;
+    const float min_p = a.min_p ? a.min_p[e] : 0.f;
+    const float u = a.u ? a.u[e] : 0.f;
+    const int k = a.top_k ? a.top_k[e] : 0;
+    const float pen = a.penalty ? a.penalty[e] : 1.f;
 
     if (tid == 0) sh.n_list = 0u;
     auto started = cluster.barrier_arrive();
-#pragma unroll 4
-    for (int i = tid; i < n; i += kThr) {
-        float v;
-        if constexpr (T == W_F32) v = static_cast<const float*>(a.logits)[row * a.ld + b0 + i];
-        else if constexpr (T == W_F16) v = __half2float(static_cast<const __half*>(a.logits)[row * a.ld + b0 + i]);
-        else v = __bfloat162float(static_cast<const __nv_bfloat16*>(a.logits)[row * a.ld + b0 + i]);
-        keys[i] = key_of(v);
+    // the slice: 16 bytes a load, eight under way
+    constexpr int ES = T == W_F32 ? 4 : 2, PV = 16 / ES;
+    const uint8_t* src = static_cast<const uint8_t*>(a.logits) + (row * a.ld + b0) * ES;
+    const int nv = aligned ? n / PV : 0;
+    for (int i0 = 0; i0 < nv; i0 += 8 * kThr) {
+        uint4 q[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int i = i0 + j * kThr + tid;
+            if (i < nv) q[j] = __ldcs(reinterpret_cast<const uint4*>(src) + i);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int i = i0 + j * kThr + tid;
+            if (i >= nv) continue;
+            uint32_t x[PV];
+#pragma unroll
+            for (int c = 0; c < PV; ++c) x[c] = key_of(logit<T>(&q[j], c));
+#pragma unroll
+            for (int c = 0; c < PV; c += 4)
+                *reinterpret_cast<uint4*>(keys + i * PV + c) = make_uint4(x[c], x[c + 1], x[c + 2], x[c + 3]);
+        }
     }
-    const float pen = a.penalty ? a.penalty[e] : 1.f;
+    for (int i = nv * PV + tid; i < n; i += kThr) keys[i] = key_of(logit<T>(src, i));
     if (pen != 1.f && a.pen_start && a.pen_tok) {
         for (int i = tid; i < (n + 31) / 32; i += kThr) marked[i] = 0u;
         __syncthreads();
@@ -313,107 +491,150 @@ __global__ void __launch_bounds__(kThr) sample_rows_kernel(SampleRowsArgs a, int
         }
     }
     __syncthreads();
-    // the row's largest key
-    uint32_t top = 0u;
-    for (int i = tid; i < n; i += kThr) top = max(top, keys[i]);
-    top = __reduce_max_sync(0xffffffffu, top);
-    if (lane == 0) sh.wcnt[warp] = top;
+    // the slice's first element, and the sum and number of its finite values
+    uint32_t top = 0u, top_i = 0u, fin = 0u;
+    float sum = 0.f;
+#pragma unroll 4
+    for (int i = tid; i < n; i += kThr) {
+        const uint32_t x = keys[i];
+        if (x > top) { top = x; top_i = (uint32_t)i; }
+        const float v = value_of(x);
+        if (fabsf(v) <= 3.0e38f && x != kKeyNan) { sum += v; ++fin; }
+    }
+    uint64_t best = ((uint64_t)top << 32) | (uint32_t)~(uint32_t)(b0 + top_i);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    }
+    fin = __reduce_add_sync(0xffffffffu, fin);
+    if (lane == 0) { sh.wsum[warp] = best; sh.wsumf[warp] = sum; sh.wcnt[warp] = fin; }
     __syncthreads();
     cluster.barrier_wait(std::move(started));               // every CTA of the row is running
-    if (tid == 0) {
-        for (int i = 1; i < kWarps; ++i) top = max(top, sh.wcnt[i]);
-        for (int r = 0; r < CL; ++r) cluster.map_shared_rank(&sh, r)->tops[rank] = max(top, sh.wcnt[0]);
+    if (tid < CL) {                                         // to every CTA
+        float s = 0.f;
+        uint32_t c = 0u;
+        uint64_t x = 0ull;
+        for (int i = 0; i < kWarps; ++i) { x = max(x, sh.wsum[i]); s += sh.wsumf[i]; c += sh.wcnt[i]; }
+        Shared* o = cluster.map_shared_rank(&sh, tid);
+        o->bests[rank] = x;
+        o->total_v[rank] = s;
+        o->n_finite[rank] = c;
     }
     cluster.sync();
-    top = 0u;
-    for (int r = 0; r < CL; ++r) top = max(top, sh.tops[r]);
+    best = 0ull;
+    sum = 0.f;
+    fin = 0u;
+    for (int r = 0; r < CL; ++r) { best = max(best, sh.bests[r]); sum += sh.total_v[r]; fin += sh.n_finite[r]; }
+    top = (uint32_t)(best >> 32);
     const float top_v = value_of(top);
-
-    Group g{&sh, CL, 0};
-    Elems el{keys, nullptr, n, b0};
-    const float temp = a.temperature ? a.temperature[e] : 0.f;
-    const float top_p = a.top_p ? a.top_p[e] : 1.f;
-    const bool greedy = !(temp > 0.f) || !(top_p > 0.f);
-    uint64_t cut = (uint64_t)top << 32;                     // greedy: the largest, the lowest id of them
-    uint64_t target = 1ull;
-    Measure what = M_COUNT;
-    Slope slope{0.f, 0.f};
-    bool alone = false;
-    if (!greedy) {
-        const int k = a.top_k ? a.top_k[e] : 0;
-        cut = (uint64_t)(kKeyNan + 1u) << 32;               // NaN is no candidate
-        if (k > 0 && k < a.V) {
-            cut = select_cut(el, g, M_COUNT, cut, (uint64_t)k, false, top_v, slope);
-            if (k <= kListMax && CL > 1) {
-                // at most k candidates: they move to the first CTA
-                Shared* s0 = cluster.map_shared_rank(&sh, 0);
-                uint64_t* l0 = cluster.map_shared_rank(list, 0);
-                for (int i0 = 0; i0 < n; i0 += kThr) {
-                    const int i = i0 + tid;
-                    const uint64_t x = i < n ? el.at(i) : 0ull;
-                    const bool take = i < n && x >= cut;
-                    const unsigned ball = __ballot_sync(0xffffffffu, take);
-                    if (!ball) continue;
-                    uint32_t at = 0u;
-                    if (lane == 0) at = atomicAdd(&s0->n_list, (uint32_t)__popc(ball));
-                    at = __shfl_sync(0xffffffffu, at, 0) + __popc(ball & ((1u << lane) - 1u));
-                    if (take && at < (uint32_t)kListMax) l0[at] = x;
+    if (!(temp > 0.f) || !(top_p > 0.f) || top <= kKeyNegInf) {   // the first candidate, or none
+        if (rank == 0 && tid == 0) a.token[e] = top <= kKeyNegInf ? -1 : (int32_t)~(uint32_t)best;
+        return;                                              // (no CTA reads another's memory after the barrier)
+    }
+    if (k > 0 && k <= kListMax && k < a.V) {
+        // an upper set of k elements or slightly more
+        const float scale = (float)kNear / (top_v - sum / (float)max(fin, 1u));
+        uint32_t bin1 = kNear, bin2 = kNear, count = 0xffffffffu;
+        float lo = 0.f, fine = 0.f;
+        if (scale > 0.f && scale < 3.0e38f) {
+            sh.near[tid] = 0u;
+            __syncthreads();
+#pragma unroll 4
+            for (int i = tid; i < n; i += kThr) {
+                const uint32_t b = near_bin(value_of(keys[i]), top_v, scale);
+                if (b < kNear) atomicAdd(&sh.near[b], 1u);
+            }
+            near_scan(sh, CL, (uint32_t)k);
+            if (sh.near_count > 0u) {
+                bin1 = sh.near_bin;
+                count = sh.near_before + sh.near_count;
+                if (count > kListMax) {
+                    // the last bin again, 512 times as fine
+                    const uint32_t before = sh.near_before;
+                    lo = (float)bin1;
+                    fine = (float)kNear;
+                    __syncthreads();
+                    sh.near[tid] = 0u;
+                    __syncthreads();
+                    for (int i = tid; i < n; i += kThr) {
+                        const float v = value_of(keys[i]);
+                        if (near_bin(v, top_v, scale) == bin1) {
+                            const uint32_t b = min((uint32_t)(((top_v - v) * scale - lo) * fine), (uint32_t)kNear - 1u);
+                            atomicAdd(&sh.near[b], 1u);
+                        }
+                    }
+                    near_scan(sh, CL, (uint32_t)k - before);
+                    bin2 = sh.near_bin;                      // (found: the bin's elements reach k)
+                    count = before + sh.near_before + sh.near_count;
                 }
-                cluster.sync();
-                if (rank != 0) return;                      // nobody reads or writes this CTA any more
-                alone = true;
-                g = Group{&sh, 1, 0};
-                el = Elems{nullptr, list, (int)min(sh.n_list, (uint32_t)kListMax), 0};
             }
         }
-        if (top_p < 1.f) {
-            const Slope one = slope_of(1.0);
-            const uint64_t z = total_weight(el, g, cut, top_v, one);
-            cut = select_cut(el, g, M_WEIGHT, cut, share_up(z, top_p), false, top_v, one);
+        if (count <= kListMax) {
+            Shared* s0 = cluster.map_shared_rank(&sh, 0);
+            uint64_t* l0 = cluster.map_shared_rank(list, 0);
+            for (int i0 = 0; i0 < n; i0 += kThr) {
+                const int i = i0 + tid;
+                bool take = false;
+                if (i < n) {
+                    const float v = value_of(keys[i]);
+                    const uint32_t b = near_bin(v, top_v, scale);
+                    take = b < bin1 || (b == bin1 && (bin2 == kNear ||
+                                                      min((uint32_t)(((top_v - v) * scale - lo) * fine), (uint32_t)kNear - 1u) <= bin2));
+                }
+                const unsigned ball = __ballot_sync(0xffffffffu, take);
+                if (!ball) continue;
+                uint32_t at = 0u;
+                if (lane == 0) at = atomicAdd(&s0->n_list, (uint32_t)__popc(ball));
+                at = __shfl_sync(0xffffffffu, at, 0) + __popc(ball & ((1u << lane) - 1u));
+                if (take && at < (uint32_t)kListMax) l0[at] = ((uint64_t)keys[i] << 32) | (uint32_t)~(uint32_t)(b0 + i);
+            }
+            cluster.sync();
+            if (rank != 0) return;                           // nobody reads or writes this CTA any more
+            const int32_t tok = list_chain(sh, list, (int)min(sh.n_list, (uint32_t)kListMax), k,
+                                           top_p, min_p, temp, u);
+            if (tid == 0) a.token[e] = tok;
+            return;
         }
-        const float min_p = a.min_p ? a.min_p[e] : 0.f;
-        if (min_p > 0.f) {
-            // l - top >= ln(min_p): the least float l for which it holds in double
-            const double lim = (double)top_v + log((double)fminf(min_p, 1.f));
-            float f = (float)lim;
-            if ((double)f < lim) f = nextafterf(f, INFINITY);
-            cut = max(cut, min((uint64_t)key_of(f) << 32, (uint64_t)top << 32));
-        }
-        slope = slope_of((double)temp);
-        const uint64_t z = total_weight(el, g, cut, top_v, slope);
-        const float u = fminf(fmaxf(a.u ? a.u[e] : 0.f, 0.f), 0.99999994f);
-        // the first candidate whose running weight exceeds u z
-        target = min(z, (uint64_t)floor((double)u * (double)z) + (uint64_t)1);
-        what = M_WEIGHT;
     }
-    int32_t tok = -1;
-    if (top > kKeyNegInf) {                                  // the same in every CTA of the row
-        cut = select_cut(el, g, what, cut, target, true, top_v, slope);
-        // the boundary element is the least one >= its prefix: follow it down to the whole number
-        uint64_t best = ~0ull;
-        for (int i = tid; i < el.n; i += kThr) {
-            const uint64_t x = el.at(i);
-            if (x >= cut) best = min(best, x);
-        }
+    // every candidate where it lies
+    Group g{&sh, CL, 0};
+    const Elems el{keys, n, b0};
+    uint64_t cut = (uint64_t)(kKeyNan + 1u) << 32;           // NaN is no candidate
+    if (k > 0 && k < a.V) cut = select_cut(el, g, M_COUNT, cut, (uint64_t)k, false, top_v, Slope{0.f, 0.f});
+    if (top_p < 1.f) {
+        const Slope one = slope_of(1.0);
+        const uint64_t z = total_weight(el, g, cut, top_v, one);
+        cut = select_cut(el, g, M_WEIGHT, cut, share_up(z, top_p), false, top_v, one);
+    }
+    if (min_p > 0.f) cut = max(cut, (uint64_t)min_p_key(top_v, min_p) << 32);
+    const Slope slope = slope_of((double)temp);
+    const uint64_t z = total_weight(el, g, cut, top_v, slope);
+    cut = select_cut(el, g, M_WEIGHT, cut, pick_target(z, u), true, top_v, slope);
+    // the boundary element is the least one >= its prefix
+    best = ~0ull;
+    for (int i = tid; i < el.n; i += kThr) {
+        const uint64_t x = el.at(i);
+        if (x >= cut) best = min(best, x);
+    }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) best = min(best, __shfl_xor_sync(0xffffffffu, best, o));
-        if (lane == 0) sh.wsum[warp] = best;
-        __syncthreads();
-        if (tid == 0) {
-            for (int i = 0; i < kWarps; ++i) best = min(best, sh.wsum[i]);
-            sh.found_before = best;
-        }
-        group_sync(g);
-        for (int r = 0; r < g.size; ++r)
-            best = min(best, (g.size > 1 ? cluster.map_shared_rank(&sh, r) : &sh)->found_before);
-        tok = (int32_t)~(uint32_t)best;
+    for (int o = 16; o > 0; o >>= 1) best = min(best, __shfl_xor_sync(0xffffffffu, best, o));
+    if (lane == 0) sh.wsum[warp] = best;
+    __syncthreads();
+    if (tid == 0) {
+        for (int i = 0; i < kWarps; ++i) best = min(best, sh.wsum[i]);
+        sh.best = best;
     }
-    if (rank == 0 && tid == 0) a.token[e] = tok;
-    if (!alone && CL > 1) cluster.sync();                   // no CTA leaves while another reads it
+    cluster.sync();
+    if (rank == 0 && tid == 0) {
+        for (int r = 0; r < CL; ++r) best = min(best, cluster.map_shared_rank(&sh, r)->best);
+        a.token[e] = (int32_t)~(uint32_t)best;
+    }
+    cluster.sync();                                          // no CTA leaves while another reads it
 }
 
 size_t smem_bytes(int slice) {
-    return sizeof(Shared) + sizeof(uint64_t) * kListMax + sizeof(uint32_t) * ((size_t)slice + (slice + 31) / 32);
+    return kSharedBytes + sizeof(uint64_t) * kListMax + sizeof(uint32_t) * ((size_t)slice + (slice + 31) / 32);
 }
 
 template <int T>
@@ -437,7 +658,9 @@ bool go(const SampleRowsArgs& a, cudaStream_t st) {
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, sample_rows_kernel<T>, a, slice) == cudaSuccess;
+    const int es = T == W_F32 ? 4 : 2;
+    const int aligned = (reinterpret_cast<uintptr_t>(a.logits) % 16 == 0) && a.ld * es % 16 == 0;
+    return cudaLaunchKernelEx(&cfg, sample_rows_kernel<T>, a, slice, aligned) == cudaSuccess;
 }
 
 }  // namespace
