@@ -78,8 +78,10 @@ constexpr uint32_t kKeyNan = 0u, kKeyNegInf = 0x007fffffu;
 
 // The factor log2(e) / t as two floats.
 struct Slope { float hi, lo; };
+constexpr double kLog2E = 1.4426950408889634074;
+constexpr Slope kSlopeOne{(float)kLog2E, (float)(kLog2E - (double)(float)kLog2E)};
 __device__ __forceinline__ Slope slope_of(double t) {
-    const double c = 1.4426950408889634074 / t;
+    const double c = kLog2E / t;
     Slope s;
     s.hi = (float)c;
     s.lo = isinf(s.hi) ? 0.f : (float)(c - (double)s.hi);
@@ -130,6 +132,10 @@ struct Shared {
     uint64_t bests[kClusterMax];
     float wsumf[kWarps];
     uint32_t near_bin, near_before, near_count;
+    // FP64 is slow here: one thread computes what needs it, early
+    Slope slope;                                             // of the row's temperature
+    double log_min_p;
+    uint64_t target;
     uint64_t wsum[kWarps];
     uint32_t wcnt[kWarps];
     uint64_t found_before, total;
@@ -283,8 +289,8 @@ __device__ uint64_t total_weight(const Elems& el, Group& g, uint64_t cut, float 
 }
 
 // The key of the least float l with l - top >= ln(min_p) in double (the top's own key at most).
-__device__ __forceinline__ uint32_t min_p_key(float top, float min_p) {
-    const double lim = (double)top + log((double)fminf(min_p, 1.f));
+__device__ __forceinline__ uint32_t min_p_key(float top, double log_min_p) {
+    const double lim = (double)top + log_min_p;
     float f = (float)lim;
     if ((double)f < lim) f = nextafterf(f, INFINITY);
     return min(key_of(f), key_of(top));
@@ -322,11 +328,16 @@ __device__ uint64_t block_scan(Shared& sh, uint64_t v, uint64_t* total) {
     return v + add;
 }
 
-// The first of the m sorted elements (thread t holds w[] of kPer t ..) where the running weight reaches target;
-// m - 1 if none does. `before`: the thread's exclusive prefix.
-__device__ int first_reaching(Shared& sh, const uint64_t* w, uint64_t before, int m, uint64_t target) {
-    if (threadIdx.x == 0) sh.found = m - 1;
+// The first of the m sorted elements (thread t holds w[] of kPer t ..) where the running weight reaches the target
+// that thread 0 has from make(); m - 1 if none does. `before`: the thread's exclusive prefix.
+template <typename F>
+__device__ int first_reaching(Shared& sh, const uint64_t* w, uint64_t before, int m, F make) {
+    if (threadIdx.x == 0) {
+        sh.found = m - 1;
+        sh.target = make();
+    }
     __syncthreads();
+    const uint64_t target = sh.target;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
         const int i = threadIdx.x * kPer + j;
@@ -341,8 +352,7 @@ __device__ int first_reaching(Shared& sh, const uint64_t* w, uint64_t before, in
 
 // The chain over n listed elements, an upper set of the row with at least min(k, candidates) of them: sorted, then
 // cut to k, by top-p and min-p, then the pick. One CTA; list has kListMax places.
-__device__ int32_t list_chain(Shared& sh, uint64_t* list, int n, int k, float top_p, float min_p, float temp,
-                              float u) {
+__device__ int32_t list_chain(Shared& sh, uint64_t* list, int n, int k, float top_p, float min_p, float u) {
     const int tid = threadIdx.x;
     if (n <= kThr) {
         // few: a thread per element counts those before it; sorted into the list's next places
@@ -384,11 +394,13 @@ __device__ int32_t list_chain(Shared& sh, uint64_t* list, int n, int k, float to
         return block_scan(sh, loc, &z) - loc;
     };
     if (top_p < 1.f) {
-        const uint64_t before = weigh(slope_of(1.0));
-        m = first_reaching(sh, w, before, m, share_up(z, top_p)) + 1;
+        const uint64_t before = weigh(kSlopeOne);
+        m = first_reaching(sh, w, before, m, [&] { return share_up(z, top_p); }) + 1;
     }
     if (min_p > 0.f) {
-        const uint32_t least = min_p_key(top, min_p);
+        if (tid == 0) sh.target = min_p_key(top, sh.log_min_p);
+        __syncthreads();
+        const uint32_t least = (uint32_t)sh.target;
         int c = 0;
 #pragma unroll
         for (int j = 0; j < kPer; ++j) c += tid * kPer + j < m && (uint32_t)(x[j] >> 32) >= least;
@@ -396,8 +408,8 @@ __device__ int32_t list_chain(Shared& sh, uint64_t* list, int n, int k, float to
         block_scan(sh, (uint64_t)c, &all);
         m = max(1, (int)all);
     }
-    const uint64_t before = weigh(slope_of((double)temp));
-    const int f = first_reaching(sh, w, before, m, pick_target(z, u));
+    const uint64_t before = weigh(sh.slope);
+    const int f = first_reaching(sh, w, before, m, [&] { return pick_target(z, u); });
     return (int32_t)~(uint32_t)list[f];
 }
 
@@ -408,13 +420,15 @@ __device__ __forceinline__ uint32_t near_bin(float v, float top, float scale) {
 }
 
 // sh.near summed over the cluster, and the bin where the count from the top reaches k: sh.near_*; near_count = 0 if
-// none does.
+// none does. The others may still be reading near afterwards: a cluster barrier before it is written again.
 __device__ void near_scan(Shared& sh, int CL, uint32_t k) {
     cg::cluster_group cluster = cg::this_cluster();
     if (threadIdx.x == 0) sh.near_count = 0u;
     cluster.sync();
     uint32_t n = 0u;
-    for (int r = 0; r < CL; ++r) n += cluster.map_shared_rank(&sh, r)->near[threadIdx.x];
+#pragma unroll
+    for (int r = 0; r < kClusterMax; ++r)
+        if (r < CL) n += cluster.map_shared_rank(&sh, r)->near[threadIdx.x];
     uint64_t all;
     const uint32_t inc = (uint32_t)block_scan(sh, n, &all);
     if (inc >= k && inc - n < k) {
@@ -422,7 +436,7 @@ __device__ void near_scan(Shared& sh, int CL, uint32_t k) {
         sh.near_before = inc - n;
         sh.near_count = n;
     }
-    cluster.sync();                                          // (near may be written again)
+    __syncthreads();
 }
 
 template <int T>
@@ -453,7 +467,19 @@ __global__ void __launch_bounds__(kThr) sample_rows_kernel(SampleRowsArgs a, int
     const float pen = a.penalty ? a.penalty[e] : 1.f;
 
     if (tid == 0) sh.n_list = 0u;
+    if (tid == kThr - 1) {
+        if (temp > 0.f) sh.slope = slope_of((double)temp);
+        if (min_p > 0.f) sh.log_min_p = log((double)fminf(min_p, 1.f));
+    }
     auto started = cluster.barrier_arrive();
+    // the slice's first element, and the sum and number of its finite values
+    uint32_t top = 0u, top_i = 0u, fin = 0u;
+    float sum = 0.f;
+    auto note = [&](uint32_t x, int i) {
+        if (x > top) { top = x; top_i = (uint32_t)i; }
+        const float v = value_of(x);
+        if (fabsf(v) <= 3.0e38f && x != kKeyNan) { sum += v; ++fin; }
+    };
     // the slice: 16 bytes a load, eight under way
     constexpr int ES = T == W_F32 ? 4 : 2, PV = 16 / ES;
     const uint8_t* src = static_cast<const uint8_t*>(a.logits) + (row * a.ld + b0) * ES;
@@ -471,13 +497,19 @@ __global__ void __launch_bounds__(kThr) sample_rows_kernel(SampleRowsArgs a, int
             if (i >= nv) continue;
             uint32_t x[PV];
 #pragma unroll
-            for (int c = 0; c < PV; ++c) x[c] = key_of(logit<T>(&q[j], c));
+            for (int c = 0; c < PV; ++c) {
+                x[c] = key_of(logit<T>(&q[j], c));
+                note(x[c], i * PV + c);
+            }
 #pragma unroll
             for (int c = 0; c < PV; c += 4)
                 *reinterpret_cast<uint4*>(keys + i * PV + c) = make_uint4(x[c], x[c + 1], x[c + 2], x[c + 3]);
         }
     }
-    for (int i = nv * PV + tid; i < n; i += kThr) keys[i] = key_of(logit<T>(src, i));
+    for (int i = nv * PV + tid; i < n; i += kThr) {
+        keys[i] = key_of(logit<T>(src, i));
+        note(keys[i], i);
+    }
     if (pen != 1.f && a.pen_start && a.pen_tok) {
         for (int i = tid; i < (n + 31) / 32; i += kThr) marked[i] = 0u;
         __syncthreads();
@@ -489,17 +521,10 @@ __global__ void __launch_bounds__(kThr) sample_rows_kernel(SampleRowsArgs a, int
             const float v = value_of(keys[t]);
             if (keys[t] != kKeyNan) keys[t] = key_of(v > 0.f ? __fdiv_rn(v, pen) : __fmul_rn(v, pen));
         }
-    }
-    __syncthreads();
-    // the slice's first element, and the sum and number of its finite values
-    uint32_t top = 0u, top_i = 0u, fin = 0u;
-    float sum = 0.f;
-#pragma unroll 4
-    for (int i = tid; i < n; i += kThr) {
-        const uint32_t x = keys[i];
-        if (x > top) { top = x; top_i = (uint32_t)i; }
-        const float v = value_of(x);
-        if (fabsf(v) <= 3.0e38f && x != kKeyNan) { sum += v; ++fin; }
+        __syncthreads();
+        top = top_i = fin = 0u;
+        sum = 0.f;
+        for (int i = tid; i < n; i += kThr) note(keys[i], i);
     }
     uint64_t best = ((uint64_t)top << 32) | (uint32_t)~(uint32_t)(b0 + top_i);
 #pragma unroll
@@ -533,50 +558,60 @@ __global__ void __launch_bounds__(kThr) sample_rows_kernel(SampleRowsArgs a, int
         return;                                              // (no CTA reads another's memory after the barrier)
     }
     if (k > 0 && k <= kListMax && k < a.V) {
-        // an upper set of k elements or slightly more
-        const float scale = (float)kNear / (top_v - sum / (float)max(fin, 1u));
-        uint32_t bin1 = kNear, bin2 = kNear, count = 0xffffffffu;
-        float lo = 0.f, fine = 0.f;
-        if (scale > 0.f && scale < 3.0e38f) {
+        // an upper set of k elements or slightly more. Most rows have their k first nearer to the largest than two thirds
+        // of the way to the mean; the others look as far as the mean
+        const float gap = top_v - sum / (float)max(fin, 1u);
+        uint32_t bin1 = kNear, bin2 = kNear, count = 0xffffffffu, floor_key = 0u;
+        float scale = 0.f, lo = 0.f, fine = 0.f;
+        // no element below it is within `bins` bins (rounding errors of top - v and of this included)
+        auto key_below = [&](float bins) { return key_of(top_v - bins / scale - fabsf(top_v) * 1e-6f); };
+        for (int far = 0; far < 2 && count == 0xffffffffu; ++far) {
+            scale = (float)kNear / (far ? gap : gap * 0.667f);
+            if (!(scale > 0.f && scale < 3.0e38f)) break;
+            if (far) cluster.sync();
             sh.near[tid] = 0u;
             __syncthreads();
+            floor_key = key_below((float)kNear + 1.f);
 #pragma unroll 4
             for (int i = tid; i < n; i += kThr) {
-                const uint32_t b = near_bin(value_of(keys[i]), top_v, scale);
+                const uint32_t x = keys[i];
+                if (x < floor_key) continue;
+                const uint32_t b = near_bin(value_of(x), top_v, scale);
                 if (b < kNear) atomicAdd(&sh.near[b], 1u);
             }
             near_scan(sh, CL, (uint32_t)k);
             if (sh.near_count > 0u) {
                 bin1 = sh.near_bin;
                 count = sh.near_before + sh.near_count;
-                if (count > kListMax) {
-                    // the last bin again, 512 times as fine
-                    const uint32_t before = sh.near_before;
-                    lo = (float)bin1;
-                    fine = (float)kNear;
-                    __syncthreads();
-                    sh.near[tid] = 0u;
-                    __syncthreads();
-                    for (int i = tid; i < n; i += kThr) {
-                        const float v = value_of(keys[i]);
-                        if (near_bin(v, top_v, scale) == bin1) {
-                            const uint32_t b = min((uint32_t)(((top_v - v) * scale - lo) * fine), (uint32_t)kNear - 1u);
-                            atomicAdd(&sh.near[b], 1u);
-                        }
-                    }
-                    near_scan(sh, CL, (uint32_t)k - before);
-                    bin2 = sh.near_bin;                      // (found: the bin's elements reach k)
-                    count = before + sh.near_before + sh.near_count;
-                }
             }
         }
+        if (bin1 < kNear && count > kListMax) {
+            // the last bin again, 512 times as fine
+            const uint32_t before = sh.near_before;
+            lo = (float)bin1;
+            fine = (float)kNear;
+            cluster.sync();
+            sh.near[tid] = 0u;
+            __syncthreads();
+            for (int i = tid; i < n; i += kThr) {
+                const float v = value_of(keys[i]);
+                if (near_bin(v, top_v, scale) == bin1) {
+                    const uint32_t b = min((uint32_t)(((top_v - v) * scale - lo) * fine), (uint32_t)kNear - 1u);
+                    atomicAdd(&sh.near[b], 1u);
+                }
+            }
+            near_scan(sh, CL, (uint32_t)k - before);
+            bin2 = sh.near_bin;                              // (found: the bin's elements reach k)
+            count = before + sh.near_before + sh.near_count;
+        }
+        if (bin1 < kNear) floor_key = key_below((float)bin1 + 2.f);
         if (count <= kListMax) {
             Shared* s0 = cluster.map_shared_rank(&sh, 0);
             uint64_t* l0 = cluster.map_shared_rank(list, 0);
             for (int i0 = 0; i0 < n; i0 += kThr) {
                 const int i = i0 + tid;
                 bool take = false;
-                if (i < n) {
+                if (i < n && keys[i] >= floor_key) {
                     const float v = value_of(keys[i]);
                     const uint32_t b = near_bin(v, top_v, scale);
                     take = b < bin1 || (b == bin1 && (bin2 == kNear ||
@@ -592,23 +627,23 @@ __global__ void __launch_bounds__(kThr) sample_rows_kernel(SampleRowsArgs a, int
             cluster.sync();
             if (rank != 0) return;                           // nobody reads or writes this CTA any more
             const int32_t tok = list_chain(sh, list, (int)min(sh.n_list, (uint32_t)kListMax), k,
-                                           top_p, min_p, temp, u);
+                                           top_p, min_p, u);
             if (tid == 0) a.token[e] = tok;
             return;
         }
     }
     // every candidate where it lies
+    cluster.sync();                                          // (the histograms share their memory with the one above)
     Group g{&sh, CL, 0};
     const Elems el{keys, n, b0};
     uint64_t cut = (uint64_t)(kKeyNan + 1u) << 32;           // NaN is no candidate
     if (k > 0 && k < a.V) cut = select_cut(el, g, M_COUNT, cut, (uint64_t)k, false, top_v, Slope{0.f, 0.f});
     if (top_p < 1.f) {
-        const Slope one = slope_of(1.0);
-        const uint64_t z = total_weight(el, g, cut, top_v, one);
-        cut = select_cut(el, g, M_WEIGHT, cut, share_up(z, top_p), false, top_v, one);
+        const uint64_t z = total_weight(el, g, cut, top_v, kSlopeOne);
+        cut = select_cut(el, g, M_WEIGHT, cut, share_up(z, top_p), false, top_v, kSlopeOne);
     }
-    if (min_p > 0.f) cut = max(cut, (uint64_t)min_p_key(top_v, min_p) << 32);
-    const Slope slope = slope_of((double)temp);
+    if (min_p > 0.f) cut = max(cut, (uint64_t)min_p_key(top_v, sh.log_min_p) << 32);
+    const Slope slope = sh.slope;
     const uint64_t z = total_weight(el, g, cut, top_v, slope);
     cut = select_cut(el, g, M_WEIGHT, cut, pick_target(z, u), true, top_v, slope);
     // the boundary element is the least one >= its prefix
