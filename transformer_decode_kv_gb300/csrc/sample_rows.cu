@@ -328,10 +328,10 @@ __device__ uint64_t block_scan(Shared& sh, uint64_t v, uint64_t* total) {
     return v + add;
 }
 
-// The first of the m sorted elements (thread t holds w[] of kPer t ..) where the running weight reaches the target
+// The first of the m sorted elements (thread t holds w[] of per t ..) where the running weight reaches the target
 // that thread 0 has from make(); m - 1 if none does. `before`: the thread's exclusive prefix.
 template <typename F>
-__device__ int first_reaching(Shared& sh, const uint64_t* w, uint64_t before, int m, F make) {
+__device__ int first_reaching(Shared& sh, const uint64_t* w, uint64_t before, int per, int m, F make) {
     if (threadIdx.x == 0) {
         sh.found = m - 1;
         sh.target = make();
@@ -340,7 +340,8 @@ __device__ int first_reaching(Shared& sh, const uint64_t* w, uint64_t before, in
     const uint64_t target = sh.target;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-        const int i = threadIdx.x * kPer + j;
+        if (j >= per) break;
+        const int i = threadIdx.x * per + j;
         if (i < m && before < target && before + w[j] >= target) sh.found = i;   // one thread's, once
         before += w[j];
     }
@@ -378,9 +379,11 @@ __device__ int32_t list_chain(Shared& sh, uint64_t* list, int n, int k, float to
                 __syncthreads();
             }
     }
+    // the sorted elements per t .. per t + per - 1 are thread t's
+    const int per = (n + kThr - 1) / kThr;
     uint64_t x[kPer];
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) x[j] = tid * kPer + j < n ? list[tid * kPer + j] : 0ull;
+    for (int j = 0; j < kPer; ++j) x[j] = j < per && tid * per + j < n ? list[tid * per + j] : 0ull;
     const float top = value_of((uint32_t)(list[0] >> 32));
     int m = min(n, k);
     uint64_t w[kPer], z, loc;
@@ -388,14 +391,15 @@ __device__ int32_t list_chain(Shared& sh, uint64_t* list, int n, int k, float to
         loc = 0ull;
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
-            w[j] = tid * kPer + j < m ? weight_of((uint32_t)(x[j] >> 32), top, c) : 0ull;
+            w[j] = 0ull;
+            if (j < per && tid * per + j < m) w[j] = weight_of((uint32_t)(x[j] >> 32), top, c);
             loc += w[j];
         }
         return block_scan(sh, loc, &z) - loc;
     };
     if (top_p < 1.f) {
         const uint64_t before = weigh(kSlopeOne);
-        m = first_reaching(sh, w, before, m, [&] { return share_up(z, top_p); }) + 1;
+        m = first_reaching(sh, w, before, per, m, [&] { return share_up(z, top_p); }) + 1;
     }
     if (min_p > 0.f) {
         if (tid == 0) sh.target = min_p_key(top, sh.log_min_p);
@@ -403,13 +407,13 @@ __device__ int32_t list_chain(Shared& sh, uint64_t* list, int n, int k, float to
         const uint32_t least = (uint32_t)sh.target;
         int c = 0;
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) c += tid * kPer + j < m && (uint32_t)(x[j] >> 32) >= least;
+        for (int j = 0; j < kPer; ++j) c += j < per && tid * per + j < m && (uint32_t)(x[j] >> 32) >= least;
         uint64_t all;
         block_scan(sh, (uint64_t)c, &all);
         m = max(1, (int)all);
     }
     const uint64_t before = weigh(sh.slope);
-    const int f = first_reaching(sh, w, before, m, [&] { return pick_target(z, u); });
+    const int f = first_reaching(sh, w, before, per, m, [&] { return pick_target(z, u); });
     return (int32_t)~(uint32_t)list[f];
 }
 
@@ -444,6 +448,19 @@ __device__ __forceinline__ float logit(const void* p, int64_t i) {
     if constexpr (T == W_F32) return static_cast<const float*>(p)[i];
     else if constexpr (T == W_F16) return __half2float(static_cast<const __half*>(p)[i]);
     else return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+
+// f(key, index) for every key of a slice (16-byte aligned, its length rounded up to 32 keys).
+template <typename F>
+__device__ __forceinline__ void each_key(const uint32_t* keys, int n, F f) {
+#pragma unroll 2
+    for (int i = 4 * threadIdx.x; i < n; i += 4 * kThr) {
+        const uint4 x = *reinterpret_cast<const uint4*>(keys + i);
+        f(x.x, i);
+        if (i + 1 < n) f(x.y, i + 1);
+        if (i + 2 < n) f(x.z, i + 2);
+        if (i + 3 < n) f(x.w, i + 3);
+    }
 }
 
 template <int T>
@@ -524,7 +541,7 @@ __global__ void __launch_bounds__(kThr) sample_rows_kernel(SampleRowsArgs a, int
         __syncthreads();
         top = top_i = fin = 0u;
         sum = 0.f;
-        for (int i = tid; i < n; i += kThr) note(keys[i], i);
+        each_key(keys, n, note);
     }
     uint64_t best = ((uint64_t)top << 32) | (uint32_t)~(uint32_t)(b0 + top_i);
 #pragma unroll
@@ -572,13 +589,11 @@ __global__ void __launch_bounds__(kThr) sample_rows_kernel(SampleRowsArgs a, int
             sh.near[tid] = 0u;
             __syncthreads();
             floor_key = key_below((float)kNear + 1.f);
-#pragma unroll 4
-            for (int i = tid; i < n; i += kThr) {
-                const uint32_t x = keys[i];
-                if (x < floor_key) continue;
+            each_key(keys, n, [&](uint32_t x, int) {
+                if (x < floor_key) return;
                 const uint32_t b = near_bin(value_of(x), top_v, scale);
                 if (b < kNear) atomicAdd(&sh.near[b], 1u);
-            }
+            });
             near_scan(sh, CL, (uint32_t)k);
             if (sh.near_count > 0u) {
                 bin1 = sh.near_bin;
@@ -593,13 +608,11 @@ __global__ void __launch_bounds__(kThr) sample_rows_kernel(SampleRowsArgs a, int
             cluster.sync();
             sh.near[tid] = 0u;
             __syncthreads();
-            for (int i = tid; i < n; i += kThr) {
-                const float v = value_of(keys[i]);
-                if (near_bin(v, top_v, scale) == bin1) {
-                    const uint32_t b = min((uint32_t)(((top_v - v) * scale - lo) * fine), (uint32_t)kNear - 1u);
-                    atomicAdd(&sh.near[b], 1u);
-                }
-            }
+            each_key(keys, n, [&](uint32_t x, int) {
+                const float v = value_of(x);
+                if (near_bin(v, top_v, scale) != bin1) return;
+                atomicAdd(&sh.near[min((uint32_t)(((top_v - v) * scale - lo) * fine), (uint32_t)kNear - 1u)], 1u);
+            });
             near_scan(sh, CL, (uint32_t)k - before);
             bin2 = sh.near_bin;                              // (found: the bin's elements reach k)
             count = before + sh.near_before + sh.near_count;
@@ -608,21 +621,27 @@ __global__ void __launch_bounds__(kThr) sample_rows_kernel(SampleRowsArgs a, int
         if (count <= kListMax) {
             Shared* s0 = cluster.map_shared_rank(&sh, 0);
             uint64_t* l0 = cluster.map_shared_rank(list, 0);
-            for (int i0 = 0; i0 < n; i0 += kThr) {
-                const int i = i0 + tid;
-                bool take = false;
-                if (i < n && keys[i] >= floor_key) {
-                    const float v = value_of(keys[i]);
+            auto give = [&](uint32_t x, int i) {            // the whole warp
+                bool take = x >= floor_key && i < n;
+                if (take) {
+                    const float v = value_of(x);
                     const uint32_t b = near_bin(v, top_v, scale);
                     take = b < bin1 || (b == bin1 && (bin2 == kNear ||
                                                       min((uint32_t)(((top_v - v) * scale - lo) * fine), (uint32_t)kNear - 1u) <= bin2));
                 }
                 const unsigned ball = __ballot_sync(0xffffffffu, take);
-                if (!ball) continue;
+                if (!ball) return;
                 uint32_t at = 0u;
                 if (lane == 0) at = atomicAdd(&s0->n_list, (uint32_t)__popc(ball));
                 at = __shfl_sync(0xffffffffu, at, 0) + __popc(ball & ((1u << lane) - 1u));
-                if (take && at < (uint32_t)kListMax) l0[at] = ((uint64_t)keys[i] << 32) | (uint32_t)~(uint32_t)(b0 + i);
+                if (take && at < (uint32_t)kListMax) l0[at] = ((uint64_t)x << 32) | (uint32_t)~(uint32_t)(b0 + i);
+            };
+            for (int i0 = 0; i0 < n; i0 += 4 * kThr) {      // (the slice's places past n hold no key: i < n above)
+                const int i = i0 + 4 * tid;
+                uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                if (i < n) x = *reinterpret_cast<const uint4*>(keys + i);
+                if (!__any_sync(0xffffffffu, max(max(x.x, x.y), max(x.z, x.w)) >= floor_key)) continue;
+                give(x.x, i); give(x.y, i + 1); give(x.z, i + 2); give(x.w, i + 3);
             }
             cluster.sync();
             if (rank != 0) return;                           // nobody reads or writes this CTA any more
