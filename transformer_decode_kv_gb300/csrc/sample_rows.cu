@@ -483,6 +483,12 @@ __global__ void __launch_bounds__(kThr) sample_rows_kernel(SampleRowsArgs a, int
     const int k = a.top_k ? a.top_k[e] : 0;
     const float pen = a.penalty ? a.penalty[e] : 1.f;
 
+    // the row's penalty list starts its way before the logits do
+    const bool penal = pen != 1.f && a.pen_start && a.pen_tok;
+    const int pen0 = penal ? max(a.pen_start[e], 0) : 0, pen1 = penal ? min(a.pen_start[e + 1], a.n_pen) : 0;
+    const int pen_first = pen0 + tid < pen1 ? a.pen_tok[pen0 + tid] : -1;
+    if (penal)
+        for (int i = tid; i < (n + 31) / 32; i += kThr) marked[i] = 0u;
     if (tid == 0) sh.n_list = 0u;
     if (tid == kThr - 1) {
         if (temp > 0.f) sh.slope = slope_of((double)temp);
@@ -527,12 +533,10 @@ __global__ void __launch_bounds__(kThr) sample_rows_kernel(SampleRowsArgs a, int
         keys[i] = key_of(logit<T>(src, i));
         note(keys[i], i);
     }
-    if (pen != 1.f && a.pen_start && a.pen_tok) {
-        for (int i = tid; i < (n + 31) / 32; i += kThr) marked[i] = 0u;
+    if (penal) {
         __syncthreads();
-        const int j0 = max(a.pen_start[e], 0), j1 = min(a.pen_start[e + 1], a.n_pen);
-        for (int j = j0 + tid; j < j1; j += kThr) {
-            const int t = a.pen_tok[j] - b0;
+        for (int j = pen0 + tid; j < pen1; j += kThr) {
+            const int t = (j < pen0 + kThr ? pen_first : a.pen_tok[j]) - b0;
             if (t < 0 || t >= n) continue;
             if (atomicOr(&marked[t >> 5], 1u << (t & 31)) >> (t & 31) & 1u) continue;   // listed before
             const float v = value_of(keys[t]);
@@ -575,15 +579,16 @@ __global__ void __launch_bounds__(kThr) sample_rows_kernel(SampleRowsArgs a, int
         return;                                              // (no CTA reads another's memory after the barrier)
     }
     if (k > 0 && k <= kListMax && k < a.V) {
-        // an upper set of k elements or slightly more. Most rows have their k first nearer to the largest than two thirds
-        // of the way to the mean; the others look as far as the mean
+        // an upper set of k elements or slightly more. Of logits spread like a normal distribution the k first are within
+        // 0.4 of the way to the mean where they are few (0.2% of the vocabulary), and within two thirds up to
+        // some 7%; other rows look as far as the mean
         const float gap = top_v - sum / (float)max(fin, 1u);
         uint32_t bin1 = kNear, bin2 = kNear, count = 0xffffffffu, floor_key = 0u;
         float scale = 0.f, lo = 0.f, fine = 0.f;
         // no element below it is within `bins` bins (rounding errors of top - v and of this included)
         auto key_below = [&](float bins) { return key_of(top_v - bins / scale - fabsf(top_v) * 1e-6f); };
         for (int far = 0; far < 2 && count == 0xffffffffu; ++far) {
-            scale = (float)kNear / (far ? gap : gap * 0.667f);
+            scale = (float)kNear / (far ? gap : gap * (k <= a.V / 512 ? 0.4f : 0.667f));
             if (!(scale > 0.f && scale < 3.0e38f)) break;
             if (far) cluster.sync();
             sh.near[tid] = 0u;
