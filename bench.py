@@ -157,8 +157,8 @@ def linear_weight_bytes(w) -> float:
     return tot
 
 
-def kv_value_bytes(type_kv: int) -> float:
-    return {0: 4.0, 1: 2.0, 8: 34.0 / 32.0}[type_kv]
+def kv_value_bytes(type_kv: int, head_dim: int = 128) -> float:
+    return {0: 4.0, 1: 2.0, 8: 34.0 / 32.0, 100: 1.0 + 4.0 / head_dim}[type_kv]
 
 
 def decode_step_bytes(w, visible, n_out: int) -> float:
@@ -168,7 +168,7 @@ def decode_step_bytes(w, visible, n_out: int) -> float:
     import synthetic as S
     hp = w.hp
     T = len(visible)
-    kv_row = 2.0 * hp.n_head_kv * hp.head_dim * kv_value_bytes(w.type_kv) * hp.n_layer
+    kv_row = 2.0 * hp.n_head_kv * hp.head_dim * kv_value_bytes(w.type_kv, hp.head_dim) * hp.n_layer
     emb = _row_bytes(S.types_for("token_embd.weight", w.types), hp.n_embd)
     return (linear_weight_bytes(w) + (2 * hp.n_layer + 1) * hp.n_embd * 4.0 + T * emb
             + float(sum(visible)) * kv_row + T * kv_row + n_out * hp.n_vocab * 4.0)
@@ -552,7 +552,7 @@ def main():
     ap.add_argument("--fused-step", action="store_true",
                     help="one-token steps as the single persistent step kernel instead of the "
                          "per-op kernel sequence (for comparison)")
-    ap.add_argument("--type-kv", default="", choices=["", "f32", "f16", "q8_0"],
+    ap.add_argument("--type-kv", default="", choices=["", "f32", "f16", "q8_0", "f8_e4m3"],
                     help="KV cache type instead of the workload's own (f16 unless it says otherwise)")
     ap.add_argument("--layers", type=int, default=0,
                     help="profiling aid: run the workload's shape with only this many layers "
@@ -567,14 +567,14 @@ def main():
         w = dataclasses.replace(w, hp=dataclasses.replace(w.hp, n_layer=args.layers))
         S.WORKLOADS[args.workload] = w
     if args.type_kv:
-        w = dataclasses.replace(w, type_kv={"f32": 0, "f16": 1, "q8_0": 8}[args.type_kv])
+        w = dataclasses.replace(w, type_kv={"f32": 0, "f16": 1, "q8_0": 8, "f8_e4m3": 100}[args.type_kv])
         S.WORKLOADS[args.workload] = w
     args.w = w
     hp = w.hp
     peaks = measured_peaks()
     config = {"workload": args.workload, "description": w.description, "sequences": w.n_seq,
               "prompt_tokens": w.n_prompt, "decode_steps_timed": args.steps,
-              "n_ctx": w.n_ctx, "kv_cache": {0: "f32", 1: "f16", 8: "q8_0"}[w.type_kv],
+              "n_ctx": w.n_ctx, "kv_cache": {0: "f32", 1: "f16", 8: "q8_0", 100: "f8_e4m3"}[w.type_kv],
               "l2": "inputs larger than L2: every decode step streams all weights (no flush)",
               "parallelism": "replicas" if args.gpus > 1 else "single",
               "decode_path": "persistent step kernel" if args.fused_step else "per-op kernels (graph)"}

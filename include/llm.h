@@ -94,8 +94,8 @@ enum {
 
 /* Context parameters ([P1] Крок 9-10 context constructor; [P2] Example 9; [P4] コンテキストの構築).
  * n_ctx is rounded up to a multiple of 256; n_batch becomes min(n_ctx, n_batch) and n_ubatch
- * min(n_batch, n_ubatch). type_k / type_v: both LLM_TYPE_F32, both LLM_TYPE_F16, or both
- * LLM_TYPE_Q8_0 ([P2] Memory Math: a q8_0 cache of 34 bytes per 32 values; [P4] type_k/type_v; each
+ * min(n_batch, n_ubatch). type_k / type_v: both LLM_TYPE_F32, both LLM_TYPE_F16, both
+ * LLM_TYPE_F8_E4M3 (the row written is the float32 row after RoPE), or both LLM_TYPE_Q8_0 ([P2] Memory Math: a q8_0 cache of 34 bytes per 32 values; [P4] type_k/type_v; each
  * written row is quantised per 32-value block with d = max|x| / 127 and q = round(x / d), the
  * decisions taken in float32; the fused persistent decode step takes F32/F16 only). stream: a cudaStream_t
  * the library launches all its work on (NULL = the library creates its own non-blocking stream).
@@ -211,6 +211,14 @@ int llm_seq_rm(llm_ctx *ctx, int32_t seq, int32_t p0, int32_t p1);
  * Returns 1 if cells moved, 0 if nothing to do (or optimize == 0), -1 on a device error. */
 int llm_memory_update(llm_ctx *ctx, int optimize);
 
+/* Sliding window: from the next llm_decode on, a token at position p sees of its sequence's cells those at
+ * positions > p - window (itself included: window tokens) and the first n_sink positions (< n_sink), which
+ * stay visible. window 0 (the default): every earlier position. F16 and F8_E4M3 caches. Cells out of sight are
+ * kept until llm_seq_rm removes them (positions keep counting; a caller that keeps the first n_sink of
+ * them can so run on without end). The fused persistent step is not used with a window. Returns 0, -1 for
+ * a negative argument, another cache type, or a failed allocation (the window is then unchanged). */
+int llm_set_attn_window(llm_ctx *ctx, int32_t window, int32_t n_sink);
+
 /* Largest / smallest position held for a sequence, -1 if it holds none ([P1] KV-cache section). */
 int32_t llm_seq_pos_max(llm_ctx *ctx, int32_t seq);
 int32_t llm_seq_pos_min(llm_ctx *ctx, int32_t seq);
@@ -277,6 +285,15 @@ typedef struct llm_sampler_params {
     int32_t n_penalty_tokens;
 } llm_sampler_params;
 int32_t llm_sample_ith(llm_ctx *ctx, int32_t i, const llm_sampler_params *params, float u);
+
+/* The same chain for n rows of the last llm_decode in one launch: row rows[j] (as i above) with params[j] and u[j]
+ * into tokens[j] (all host arrays). top_k may be any number >= 1 (n_vocab or more: off) and the penalty
+ * lists of any length. Probabilities are summed exactly (see llm_sample_rows), so a pick may differ from
+ * llm_sample_ith's, which sums in float32, where u falls on a boundary. A row without a logit above -infinity
+ * gives -1. Returns 0, or -1 for an invalid argument, a row without logits or a device error (tokens is
+ * then not written). Synchronises the context's stream. */
+int32_t llm_sample_batch(llm_ctx *ctx, int32_t n, const int32_t *rows, const llm_sampler_params *params,
+                         const float *u, int32_t *tokens);
 
 /* ---- operators on the caller's own device buffers ---------------------------------------------
  * For programs that keep their own KV cache (pages handed out by their own allocator) or their own
@@ -420,7 +437,7 @@ int llm_debug_capture(llm_ctx *ctx, int enable);
 /* Copy a captured intermediate of the last ubatch to host memory as float32, row-major
  * [n_tokens][width]. name: "embd" (layer ignored), "l_out" (residual stream after layer `layer`),
  * "attn_out" (attention output of layer `layer`, before the output projection), "kq_in" (the Q
- * rows after RoPE of layer `layer`), "k_in" / "v_in" (Q8_0 caches only: the float32 K rows after
+ * rows after RoPE of layer `layer`), "k_in" / "v_in" (Q8_0 and F8_E4M3 caches only: the float32 K rows after
  * RoPE and the V rows, [n_tokens][n_head_kv * head_dim], that layer `layer` quantised into the
  * cache), "result_norm" (final-normed output rows; present only when the
  * output matrix ran unfused, not in the one-token GEMV that normalises in its prologue). Returns the number
@@ -431,7 +448,8 @@ int64_t llm_debug_get_tensor(llm_ctx *ctx, const char *name, int32_t layer, floa
 /* Copy layer `layer`'s K cache (which = 0) or V cache (which = 1) to host memory as stored: type_k
  * / type_v elements laid out [n_head_kv][n_ctx][head_dim] (cell c of KV head g at (g * n_ctx + c)
  * * head_dim). A Q8_0 cache holds the int8 quants in that layout, followed by the fp16 scales
- * [n_head_kv][n_ctx][head_dim / 32] (one per 32-value block; value = scale * quant). which = 2 / 3
+ * [n_head_kv][n_ctx][head_dim / 32] (one per 32-value block; value = scale * quant); an F8_E4M3 cache its
+ * codes, followed by the float32 scales [n_head_kv][n_ctx]. which = 2 / 3
  * (Q8_0 caches only; layer ignored beyond its range check): the f16 copy of the K / V quants, same
  * layout, that the last attention over query tiles of several tokens read (the last layer of the
  * last such ubatch), valid for the cells below that ubatch's n_kv. out may be NULL to query the size.

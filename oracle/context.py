@@ -133,6 +133,7 @@ class OracleContext:
         self.abort_callback: Optional[Callable[[], bool]] = None
         self.fail_at_ubatch: Optional[int] = None      # test hook: ubatch whose compute fails
         self.output_all = False
+        self.window, self.n_sink = 0, 0     # sliding window (0: none) and first positions kept in sight
         self._reset_outputs(0)
         self.last_ubatches: List[dict] = []
 
@@ -271,10 +272,19 @@ class OracleContext:
         for s, p in pos_min.items():
             self.cells.seq_rm(s, p, -1)
 
+    def mask(self, pos, seq_ids, n_kv):
+        """The cells' mask, narrowed to the window: the last `window` positions up to the token's own,
+        and the first n_sink positions."""
+        m = self.cells.mask(pos, seq_ids, n_kv)
+        if self.window:
+            kp = self.cells.pos[:n_kv][None, :]
+            m &= (kp > np.asarray(pos)[:, None] - self.window) | (kp < self.n_sink)
+        return m
+
     def _process_ubatch(self, tokens, upos, useq, slots, out_rows):
         hp = self.hp
         n_kv = self.cells.n_kv()
-        visible = self.cells.mask(upos, useq, n_kv)
+        visible = self.mask(upos, useq, n_kv)
         self.last_ubatches.append({"slots": list(slots), "n_kv": n_kv, "mask": visible,
                                    "out_rows": list(out_rows), "pos": list(upos)})
         if not self.compute:

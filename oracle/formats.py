@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import numpy as np
 
-F32, F16, BF16, Q8_0 = 0, 1, 2, 8
+F32, F16, BF16, Q8_0, F8_E4M3 = 0, 1, 2, 8, 100
 QK8_0 = 32
 Q8_0_BYTES = 34
 
@@ -69,9 +69,33 @@ def quantize_q8_0(x: np.ndarray) -> np.ndarray:
     return out.reshape(lead + (x32.shape[-1] // QK8_0 * Q8_0_BYTES,))
 
 
+E4M3_MAX = 448.0
+
+
+def round_e4m3(y: np.ndarray) -> np.ndarray:
+    """Nearest E4M3 value (4 exponent bits of bias 7, 3 mantissa bits), ties to even, saturating."""
+    a = np.minimum(np.abs(y), E4M3_MAX)
+    e = np.maximum(np.floor(np.log2(np.maximum(a, 2.0 ** -20))), -6)     # below 2^-6: subnormals
+    step = 2.0 ** (e - 3)
+    return np.copysign(np.minimum(np.rint(a / step) * step, E4M3_MAX), y)
+
+
+def f8_e4m3_rows(x: np.ndarray):
+    """(E4M3 values, scales) of rows over the last axis: a row's scale is the least power of two
+    s >= 2^-126 with max|x| / s <= 448; 1 for a row of zeros."""
+    x = np.asarray(x, dtype=np.float64)
+    amax = np.max(np.abs(x), axis=-1, keepdims=True)
+    s = np.exp2(np.maximum(np.ceil(np.log2(np.where(amax > 0, amax, E4M3_MAX) / E4M3_MAX)), -126))
+    return round_e4m3(x / s), s
+
+
 def round_to_type(x: np.ndarray, t: int) -> np.ndarray:
     """Value a cache row holds after a write of x in type t, as float64: F32/F16 round to nearest
-    even; Q8_0 quantises each 32-value block (quantize_q8_0) and reads back d * q."""
+    even; Q8_0 quantises each 32-value block (quantize_q8_0) and reads back d * q; F8_E4M3 rows of
+    float32 values are E4M3 values times one power of two per row (last axis)."""
+    if t == F8_E4M3:
+        v, s = f8_e4m3_rows(np.asarray(x).astype(np.float32))
+        return v * s
     if t == F32:
         return x.astype(np.float32).astype(np.float64)
     if t == F16:

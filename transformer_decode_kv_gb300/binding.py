@@ -133,6 +133,10 @@ SIGNATURES = {
                                         C.c_int32, C.c_void_p, C.c_int32, C.c_int32, C.c_int32, C.c_int32]),
     "llm_debug_gemm_bf16": (C.c_int, [C.c_int32, C.c_void_p, C.c_int64, C.c_int64, C.c_void_p,
                                       C.c_int32, C.c_void_p, C.c_int32, C.c_int32]),
+    "llm_set_attn_window": (C.c_int, [C.c_void_p, C.c_int32, C.c_int32]),
+    "llm_sample_batch": (C.c_int32, [C.c_void_p, C.c_int32, C.POINTER(C.c_int32),
+                                     C.POINTER(SamplerParams), C.POINTER(C.c_float),
+                                     C.POINTER(C.c_int32)]),
     "llm_op_last_error": (C.c_char_p, []),
     "llm_kv_store": (C.c_int, [C.POINTER(KvPagesDesc), C.c_int32, C.c_void_p, C.c_void_p, C.c_int64,
                                C.c_int64, C.c_void_p, C.c_int32, C.c_void_p, C.c_void_p]),
@@ -570,6 +574,33 @@ class Context:
                           pen.ctypes.data_as(C.POINTER(C.c_int32)) if len(pen) else None, len(pen))
         return lib().llm_sample_ith(self.ptr, i, C.byref(p), u)
 
+    def sample_batch(self, rows, u, top_k=40, top_p=1.0, min_p=0.0, temperature=1.0,
+                     repeat_penalty=1.0, penalty_tokens=None) -> np.ndarray:
+        """The sampler chain for several rows in one launch: row rows[j] with the draw u[j]. The
+        parameters are numbers, or one per row; penalty_tokens one list per row. Returns the tokens."""
+        rows, u = _i32(rows), np.ascontiguousarray(u, dtype=np.float32)
+        n = len(rows)
+        if u.shape != (n,):
+            raise ValueError("u needs one draw per row")
+        col = lambda v: np.broadcast_to(np.asarray(v), (n,))
+        cols = [col(x) for x in (top_k, top_p, min_p, temperature, repeat_penalty)]
+        pens = [_i32(list(p)) for p in penalty_tokens] if penalty_tokens is not None else [_i32([])] * n
+        if len(pens) != n:
+            raise ValueError("penalty_tokens needs one list per row")
+        ps = (SamplerParams * max(n, 1))()
+        for j in range(n):
+            ps[j] = SamplerParams(int(cols[0][j]), float(cols[1][j]), float(cols[2][j]), float(cols[3][j]),
+                                  float(cols[4][j]), _ptr(pens[j], C.c_int32) if len(pens[j]) else None,
+                                  len(pens[j]))
+        out = np.zeros(n, dtype=np.int32)
+        if lib().llm_sample_batch(self.ptr, n, _ptr(rows, C.c_int32), ps, _ptr(u, C.c_float),
+                                  _ptr(out, C.c_int32)) != 0:
+            raise LlmError(self.last_error())
+        return out
+
+    def set_attn_window(self, window: int, n_sink: int = 0) -> int:
+        return lib().llm_set_attn_window(self.ptr, window, n_sink)
+
     def debug_set_logits(self, i: int, row) -> int:
         r = np.ascontiguousarray(row, dtype=np.float32)
         assert r.shape == (self.n_vocab,)
@@ -658,7 +689,8 @@ class Context:
     def kv_cache(self, layer: int, which: int) -> Optional[np.ndarray]:
         """Layer `layer`'s K (which 0) or V (which 1) cache as stored, [n_head_kv][n_ctx][head_dim]
         (float32 or float16 elements). A Q8_0 cache comes back as its 34-byte blocks (fp16 scale,
-        then 32 int8 quants), uint8 [n_head_kv][n_ctx][head_dim / 32 * 34]."""
+        then 32 int8 quants), uint8 [n_head_kv][n_ctx][head_dim / 32 * 34]; an E4M3 cache as rows of a
+        float32 scale, then the codes, uint8 [n_head_kv][n_ctx][4 + head_dim]."""
         n = lib().llm_debug_kv_raw(self.ptr, layer, which, None, 0)
         if n <= 0:
             return None
@@ -670,6 +702,9 @@ class Context:
             q = out[:nq].reshape(Hkv, -1, hd // 32, 32)
             s = out[nq:].reshape(Hkv, -1, hd // 32, 2)
             return np.concatenate([s, q], axis=3).reshape(Hkv, -1, hd // 32 * 34)
+        if self.type_k == F8_E4M3:
+            nq = Hkv * self.n_ctx * hd
+            return np.concatenate([out[nq:].reshape(Hkv, -1, 4), out[:nq].reshape(Hkv, -1, hd)], axis=2)
         es = 4 if n // (self._hp.n_head_kv * self._hp.head_dim) == 4 * self.n_ctx else 2
         v = out.view(np.float32 if es == 4 else np.float16)
         return v.reshape(self._hp.n_head_kv, -1, self._hp.head_dim)

@@ -61,7 +61,7 @@ struct Smem {
     static constexpr uint32_t kv = q + 2 * tile;            // [kStages] tiles
     static constexpr uint32_t kpos = kv + kStages * tile;   // int [kMeta][kKeys]
     static constexpr uint32_t full = kpos + kMeta * kKeys * 4;   // uint32 [kMeta]: every key is read
-    static constexpr uint32_t rs = full + 16;               // E4M3: float [256], scale of a row's scores
+    static constexpr uint32_t rs = full + 16;               // float [256]: scale of a row's scores, where they differ
     static constexpr uint32_t bars = rs + 256 * 4;
     static constexpr uint32_t misc = bars + 24 * 8;
     static constexpr uint32_t bytes = misc + 28 * 4;
@@ -276,9 +276,10 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
         return;
     }
 
-    // Q rows that are changed on their way (scaled to f16's range, negated for a negative scale) are loaded by the
-    // softmax threads; others by warp 3, while the unit before is still in its last block and its epilogue
-    const bool own_q = (!BF && QT == W_BF16) || a.scale_log2 < 0.f;
+    // Q rows that are changed on their way (scaled to f16's range, rounded to f16, negated for a negative scale) are
+    // loaded by the softmax threads; others by warp 3, while the unit before is still in its last block and its epilogue
+    constexpr bool SCALED = !BF && QT != W_F16;
+    const bool own_q = SCALED || a.scale_log2 < 0.f;
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) { bar_init(&kv_full[i], 1); bar_init(&kv_empty[i], 1); }
         for (int i = 0; i < 2; ++i) { bar_init(&s_full[i], 1); bar_init(&p_full[i], 128); bar_init(&o_done[i], 1); }
@@ -701,15 +702,57 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
                 const int ch = ht % CH;
 #pragma unroll 1
                 for (int r0 = ht / CH; r0 < 128; r0 += 8 * RQ) {
-                uint4 qv[8];                                // eight loads under way
+                uint4 qv[8];                                // eight loads under way (float32: rounded below)
+                float rq[8];                                // scale of the row's scores
+                float4 fq[QT == W_F32 ? 16 : 1];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int r = r0 + i * RQ, row = u.row0 + 128 * t + r;
                     qv[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if constexpr (QT == W_F32) fq[2 * i] = fq[2 * i + 1] = make_float4(0.f, 0.f, 0.f, 0.f);
                     if (128 * t + r < u.n_row) {
                         const int tok = row_token(a, u, row);
                         const int64_t at = (int64_t)tok * a.q_tok + (int64_t)(kvh * a.G + row % a.G) * a.q_head + ch * 8;
-                        qv[i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at);
+                        if constexpr (QT == W_F32) {
+                            const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at);
+                            const float4 x = p[0], y = p[1];
+                            fq[2 * i] = x;
+                            fq[2 * i + 1] = y;
+                        } else {
+                            qv[i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    rq[i] = fabsf(a.scale_log2);
+                    if constexpr (SCALED) {
+                        // f16 products: the row times a power of two that brings its largest value to [1, 2)
+                        float x[8];
+                        if constexpr (QT == W_F32) {
+                            x[0] = fq[2 * i].x; x[1] = fq[2 * i].y; x[2] = fq[2 * i].z; x[3] = fq[2 * i].w;
+                            x[4] = fq[2 * i + 1].x; x[5] = fq[2 * i + 1].y; x[6] = fq[2 * i + 1].z; x[7] = fq[2 * i + 1].w;
+                        } else {
+                            const uint32_t w[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                x[2 * e] = __uint_as_float(w[e] << 16);
+                                x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+                            }
+                        }
+                        float mx = 0.f;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(x[e]));
+#pragma unroll
+                        for (int o = CH / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                        const uint32_t ex = __float_as_uint(mx) >> 23;
+                        float dn = 1.f;
+                        if (ex > 0u && ex < 254u) {
+                            dn = __uint_as_float((254u - ex) << 23);
+                            rq[i] *= __uint_as_float(ex << 23);
+                        }
+                        qv[i] = make_uint4(pack<false>(x[0] * dn, x[1] * dn), pack<false>(x[2] * dn, x[3] * dn),
+                                           pack<false>(x[4] * dn, x[5] * dn), pack<false>(x[6] * dn, x[7] * dn));
                     }
                 }
 #pragma unroll
@@ -717,30 +760,11 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
                     const int r = r0 + i * RQ;
                     const uint4 w = qv[i];
                     uint32_t v[4] = {w.x, w.y, w.z, w.w};
-                    float rs = fabsf(a.scale_log2);
-                    if constexpr (!BF && QT == W_BF16) {
-                        // f16 products: the row times a power of two that brings its largest value to [1, 2)
-                        float mx = 0.f;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(v[e] << 16)), fabsf(__uint_as_float(v[e] & 0xffff0000u))));
-#pragma unroll
-                        for (int o = CH / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                        const uint32_t ex = __float_as_uint(mx) >> 23;
-                        float dn = 1.f;
-                        if (ex > 0u && ex < 254u) {
-                            dn = __uint_as_float((254u - ex) << 23);
-                            rs *= __uint_as_float(ex << 23);
-                        }
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            v[e] = pack<false>(__uint_as_float(v[e] << 16) * dn, __uint_as_float(v[e] & 0xffff0000u) * dn);
-                    }
                     if (a.scale_log2 < 0.f)                 // the scores' scale is positive, the sign is in Q
 #pragma unroll
                         for (int e = 0; e < 4; ++e) v[e] ^= 0x80008000u;
                     *reinterpret_cast<uint4*>(qs + swz(r, ch)) = make_uint4(v[0], v[1], v[2], v[3]);
-                    if (F8 && ch == 0) rs_s[128 * t + r] = rs;
+                    if (SCALED && ch == 0) rs_s[128 * t + r] = rq[i];
                 }
                 }
                 to_async_proxy();
@@ -756,7 +780,7 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
             const int tok = row_token(a, u, row);
             const int rp = row_pos(a, u, row, tok), rh = hidden_below(a, rp);
             const int wp_min = __reduce_min_sync(0xffffffffu, rp), wh_max = __reduce_max_sync(0xffffffffu, rh);
-            float rs = F8 && nt > 0 ? rs_s[128 * t + r] : fabsf(a.scale_log2);
+            float rs = SCALED && nt > 0 ? rs_s[128 * t + r] : fabsf(a.scale_log2);
             float m = -INFINITY, l = 0.f;
             bool live = t < halves;
             for (int j = 0; j < nt && live; ++j) {
@@ -1004,20 +1028,22 @@ bool go(const AttnPagedArgs& a, cudaStream_t st) {
 }
 template <int HD>
 bool go_hd(const AttnPagedArgs& a, cudaStream_t st) {
-    if (a.kv.type == W_F16) return go<HD, W_F16, W_F16>(a, st);
+    if (a.kv.type == W_F16) return a.q_type == W_F16 ? go<HD, W_F16, W_F16>(a, st) : go<HD, W_F16, W_F32>(a, st);
     if (a.kv.type == W_BF16) return go<HD, W_BF16, W_BF16>(a, st);
-    return a.q_type == W_F16 ? go<HD, W_F8, W_F16>(a, st) : go<HD, W_F8, W_BF16>(a, st);
+    if (a.q_type == W_F16) return go<HD, W_F8, W_F16>(a, st);
+    return a.q_type == W_BF16 ? go<HD, W_F8, W_BF16>(a, st) : go<HD, W_F8, W_F32>(a, st);
 }
 
 }  // namespace
 
-// F32 activations stay with the 16-row tiles, which carry Q and P as two terms each.
-bool attn_paged_tc_ok(int32_t hd, int32_t kv_type, int32_t q_type) {
-    return (hd == 64 || hd == 128) && q_type != W_F32 && attn_paged_types_ok(q_type, kv_type);
+// F32 activations stay with the 16-row tiles, which carry Q and P as two terms each, unless the caller's precision is
+// that of f16 activations (round_q: the context's f16 forward passes).
+bool attn_paged_tc_ok(int32_t hd, int32_t kv_type, int32_t q_type, bool round_q) {
+    return (hd == 64 || hd == 128) && (q_type != W_F32 || round_q) && attn_paged_types_ok(q_type, kv_type);
 }
 
 bool launch_attn_paged_tc(const AttnPagedArgs& a, cudaStream_t st) {
-    if (!attn_paged_tc_ok(a.kv.hd, a.kv.type, a.q_type)) return false;
+    if (!attn_paged_tc_ok(a.kv.hd, a.kv.type, a.q_type, true)) return false;
     return a.kv.hd == 64 ? go_hd<64>(a, st) : go_hd<128>(a, st);
 }
 

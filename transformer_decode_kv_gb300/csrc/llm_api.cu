@@ -23,6 +23,7 @@
 #include "gemv_bulk.h"
 #include "host_plan.h"
 #include "kernels.h"
+#include "paged.h"
 
 using namespace llm;
 
@@ -123,6 +124,17 @@ struct llm_ctx {
     int32_t* d_order = nullptr;                // defrag: old cell of each new cell
     KvCells cells;
 
+    // attention over single cells as pages (paged.h): F8_E4M3 caches, and a window (llm_set_attn_window)
+    int32_t window = 0, n_sink = 0;
+    PlanShape pg_shape;
+    PagedPlanCaps pg_caps{};
+    PagedPlan pg_plan;
+    uint8_t *pg_dev = nullptr, *pg_host = nullptr;   // the plan's upload: header, CTA starts, cuts, units
+    size_t pg_first[2] = {0, 0}, pg_cuts = 0, pg_units[2] = {0, 0}, pg_bytes = 0;
+    float* pg_part_o = nullptr;
+    float2* pg_part_ml = nullptr;
+    int32_t* pg_tickets = nullptr;
+
     // scratch for one ubatch
     float *x = nullptr, *h = nullptr, *qkv = nullptr, *attn = nullptr, *u = nullptr, *tmp = nullptr;
     float *hout = nullptr;
@@ -195,6 +207,9 @@ struct llm_ctx {
     int32_t* d_abort = nullptr;
     uint32_t step_gen = 0;              // launches since the counters were last zeroed
     bool step_trace = false;
+    uint8_t* d_samples = nullptr;       // llm_sample_batch: parameters, penalty tokens and picks
+    uint8_t* h_samples = nullptr;       // pinned: the same layout
+    size_t samples_cap = 0;
     uint8_t* d_sample_state = nullptr;  // sampler barrier, histograms and candidates
     int32_t* d_sample_tok = nullptr;    // [kMaxPenalty] penalty tokens, the picked token, status
     int32_t* h_sample_tok = nullptr;    // pinned: the same layout
@@ -211,11 +226,21 @@ struct llm_ctx {
     int32_t q_width() const { return hp.n_head * hp.head_dim; }
     size_t kv_layer_elems() const { return (size_t)hp.n_head_kv * n_ctx * hp.head_dim; }
     bool kv_q8() const { return type_k == LLM_TYPE_Q8_0; }
-    // bytes of one layer's K (or V) cache: Q8_0 keeps int8 quants, then one fp16 scale per 32 values
+    bool kv_f8() const { return type_k == LLM_TYPE_F8_E4M3; }
+    bool paged() const { return kv_f8() || window > 0; }
+    // bytes of one layer's K (or V) cache: Q8_0 keeps int8 quants, then one fp16 scale per 32 values; F8_E4M3
+    // codes, then one float32 scale per row
     size_t kv_layer_bytes() const {
+        if (kv_f8()) return kv_layer_elems() + sizeof(float) * (size_t)hp.n_head_kv * n_ctx;
         return kv_q8() ? kv_layer_elems() / 32 * 34 : kv_layer_elems() * type_size(type_k);
     }
-    double kv_value_bytes() const { return kv_q8() ? 34.0 / 32.0 : (double)type_size(type_k); }
+    double kv_value_bytes() const {
+        return kv_f8() ? 1.0 + 4.0 / hp.head_dim : kv_q8() ? 34.0 / 32.0 : (double)type_size(type_k);
+    }
+    // whether token position p sees a cell at position kp (causal, window, sinks)
+    bool sees(int32_t p, int32_t kp) const {
+        return kp <= p && (window == 0 || (int64_t)kp > (int64_t)p - window || kp < n_sink);
+    }
 };
 
 namespace {
@@ -427,11 +452,24 @@ void attention_work(llm_ctx* c, const int32_t* pos) {
         by += (double)(p.list_off[l + 1] - p.list_off[l]) * 2.0 * hp.n_head_kv * hp.head_dim * kv_es;
     }
     const int32_t T = (int32_t)p.tok_list.size();
+    if (c->paged()) {                                // each list's cells in sight of any of its tokens, once
+        by = 0;
+        std::vector<int32_t> lo(p.n_lists(), INT32_MAX), hi(p.n_lists(), -1);
+        for (int32_t t = 0; t < T; ++t) {
+            lo[p.tok_list[t]] = std::min(lo[p.tok_list[t]], pos[t]);
+            hi[p.tok_list[t]] = std::max(hi[p.tok_list[t]], pos[t]);
+        }
+        int64_t n = 0;
+        for (int32_t l = 0; l < p.n_lists(); ++l)
+            for (int32_t k = p.list_off[l]; k < p.list_off[l + 1]; ++k)
+                n += p.list_pos[k] <= hi[l] && c->sees(std::max(lo[l], p.list_pos[k]), p.list_pos[k]);
+        by = (double)n * 2.0 * hp.n_head_kv * hp.head_dim * kv_es;
+    }
     by += (double)T * hp.n_head * hp.head_dim * 8.0;
     for (int32_t t = 0; t < T; ++t) {
         const int32_t l = p.tok_list[t];
         int64_t vis = 0;
-        for (int32_t k = p.list_off[l]; k < p.list_off[l + 1]; ++k) vis += p.list_pos[k] <= pos[t];
+        for (int32_t k = p.list_off[l]; k < p.list_off[l + 1]; ++k) vis += c->sees(pos[t], p.list_pos[k]);
         fl += 4.0 * (double)vis * hp.n_head * hp.head_dim;
     }
     c->att_bytes_now = by;
@@ -441,6 +479,159 @@ void attention_work(llm_ctx* c, const int32_t* pos) {
 // Attention work items a decode-shaped ubatch of T tokens may use (the captured grid size).
 int32_t attn_cap(llm_ctx* c, int32_t T) {
     return std::min(c->max_work, std::max(T, 4 * c->n_sm / c->hp.n_head_kv));
+}
+
+// One layer's cache as pages of one cell.
+PagedKv layer_pages(llm_ctx* c, void* kc, void* vc) {
+    PagedKv p;
+    p.type = c->type_k; p.Hkv = c->hp.n_head_kv; p.hd = c->hp.head_dim;
+    p.page_size = 1; p.n_pages = c->n_ctx;
+    p.k = static_cast<uint8_t*>(kc); p.v = static_cast<uint8_t*>(vc);
+    p.sb_page = (int64_t)p.hd * (c->kv_f8() ? 1 : 2);
+    p.sb_head = p.sb_page * c->n_ctx;
+    if (c->kv_f8()) {
+        p.ks = reinterpret_cast<float*>(p.k + c->kv_layer_elems());
+        p.vs = reinterpret_cast<float*>(p.v + c->kv_layer_elems());
+        p.ss_page = 1;
+        p.ss_head = c->n_ctx;
+    }
+    return p;
+}
+
+// Buffers of the paged attention's plans (allocated once; every ubatch's plan fits).
+bool paged_setup(llm_ctx* c) {
+    c->pg_shape.G = c->hp.n_head / c->hp.n_head_kv;
+    c->pg_shape.Hkv = c->hp.n_head_kv;
+    c->pg_shape.n_sm = c->n_sm;
+    c->pg_shape.hd = c->hp.head_dim;
+    c->pg_shape.kv_type = c->type_k;
+    c->pg_shape.tc = true;                           // (bounds for either kind of forward pass)
+    if (c->host_only || c->pg_dev) return true;
+    c->pg_caps = paged_plan_caps(c->pg_shape, c->n_ubatch, c->n_ubatch);
+    const PagedPlanCaps& k = c->pg_caps;
+    size_t at = 0;
+    auto take = [&](size_t n) { const size_t r = at; at += (n + 255) / 256 * 256; return r; };
+    take(PH_WORDS * sizeof(int32_t));
+    c->pg_first[0] = take((k.ctas1 + 1) * sizeof(int32_t));
+    c->pg_first[1] = take((k.ctas2 + 1) * sizeof(int32_t));
+    c->pg_cuts = take(k.ctas2 * sizeof(int32_t));
+    c->pg_units[0] = take(k.units1 * sizeof(AttnUnit));
+    c->pg_units[1] = take(k.units2 * sizeof(AttnUnit));
+    c->pg_bytes = at;
+    const size_t rows = (size_t)plan_part_rows(k, true);
+    uint8_t* host = nullptr;
+    if (!cuda_ok(c, cudaMallocHost(&host, at), "cudaMallocHost")) return false;
+    const bool ok = dalloc(c, &c->pg_part_o, rows * c->hp.head_dim) && dalloc(c, &c->pg_part_ml, rows) &&
+                    dalloc(c, &c->pg_tickets, (size_t)k.tickets) &&
+                    cuda_ok(c, cudaMemsetAsync(c->pg_tickets, 0, sizeof(int32_t) * k.tickets, c->st), "memset") &&
+                    dalloc(c, &c->pg_dev, at);
+    if (!ok) {
+        dfree(c, c->pg_part_o); dfree(c, c->pg_part_ml); dfree(c, c->pg_tickets);
+        cudaFreeHost(host);
+        c->pg_dev = nullptr;
+        return false;
+    }
+    c->pg_host = host;
+    return true;
+}
+
+// The plan of a ubatch from its cell lists (which are put in position order here), into the pinned upload buffer.
+bool paged_plan(llm_ctx* c, const SanBatch& b, int32_t i0, int32_t T, bool f16_pass) {
+    AttnPlan& p = c->plan;
+    std::vector<PlanSeq> seqs(p.n_lists());
+    std::vector<int32_t> tok_pos(T);
+    std::vector<std::pair<int32_t, int32_t>> order;
+    for (int32_t t = 0; t < T; ++t) tok_pos[t] = b.pos[i0 + p.perm[t]];
+    int32_t at = 0;
+    for (int32_t l = 0; l < p.n_lists(); ++l) {
+        const int32_t k0 = p.list_off[l], n = p.list_off[l + 1] - k0;
+        if (!std::is_sorted(p.list_pos.begin() + k0, p.list_pos.begin() + k0 + n)) {
+            order.clear();
+            for (int32_t j = 0; j < n; ++j) order.emplace_back(p.list_pos[k0 + j], p.list_cells[k0 + j]);
+            std::sort(order.begin(), order.end());
+            for (int32_t j = 0; j < n; ++j) { p.list_pos[k0 + j] = order[j].first; p.list_cells[k0 + j] = order[j].second; }
+        }
+        PlanSeq& q = seqs[l];
+        q.tok0 = at;
+        while (at < T && p.tok_list[p.perm[at]] == l) ++at;
+        q.n_new = at - q.tok0;
+        q.p0 = 0;
+        q.table = k0;
+        q.n_keys = n;
+        q.tok_pos = tok_pos.data() + q.tok0;
+        q.key_pos = p.list_pos.data() + k0;
+    }
+    PlanShape s = c->pg_shape;
+    s.window = c->window;
+    s.n_sink = c->n_sink;
+    // float32 queries take the 256-row tiles where the pass has f16 precision anyway
+    s.tc = f16_pass && attn_paged_tc_ok(s.hd, s.kv_type, W_F32, true);
+    build_paged_plan(s, seqs, c->pg_plan);
+    const PagedPlan& g = c->pg_plan;
+    const int64_t max_units[2] = {c->pg_caps.units1, c->pg_caps.units2}, max_cta[2] = {c->pg_caps.ctas1, c->pg_caps.ctas2},
+                  max_parts[2] = {c->pg_caps.parts1, c->pg_caps.parts2};
+    int32_t* hdr = reinterpret_cast<int32_t*>(c->pg_host);
+    std::memset(hdr, 0, PH_WORDS * sizeof(int32_t));
+    hdr[PH_FORM] = g.form();
+    hdr[PH_CUTS2] = (int32_t)g.form_[1].cuts.size();
+    for (int f = 0; f < 2; ++f) {
+        const PlanForm& pf = g.form_[f];
+        if (pf.units.empty()) continue;
+        if ((int64_t)pf.units.size() > max_units[f] || (int64_t)pf.first.size() > max_cta[f] + 1 ||
+            pf.n_parts > max_parts[f] || (int64_t)pf.cuts.size() > max_cta[f]) {
+            c->err = "attention plan exceeds its buffers";
+            return false;
+        }
+        std::memcpy(c->pg_host + c->pg_first[f], pf.first.data(), pf.first.size() * sizeof(int32_t));
+        std::memcpy(c->pg_host + c->pg_units[f], pf.units.data(), pf.units.size() * sizeof(AttnUnit));
+    }
+    const std::vector<int32_t>& cuts = g.form_[1].cuts;
+    if (!cuts.empty()) std::memcpy(c->pg_host + c->pg_cuts, cuts.data(), cuts.size() * sizeof(int32_t));
+    return true;
+}
+
+bool paged_upload(llm_ctx* c) {
+    auto copy = [&](size_t off, size_t n) {
+        return n == 0 || cuda_ok(c, cudaMemcpyAsync(c->pg_dev + off, c->pg_host + off, n, cudaMemcpyHostToDevice, c->st), "plan upload");
+    };
+    return copy(0, c->pg_units[0] + c->pg_plan.form_[0].units.size() * sizeof(AttnUnit)) &&
+           copy(c->pg_units[1], c->pg_plan.form_[1].units.size() * sizeof(AttnUnit));
+}
+
+// The attention of one layer over the plan (a: where the queries are and the outputs go).
+bool paged_attention(llm_ctx* c, const AttnArgs& a, void* kc, void* vc) {
+    AttnPagedArgs g;
+    g.kv = layer_pages(c, kc, vc);
+    g.q_type = W_F32;
+    g.G = c->pg_shape.G;
+    g.q = a.q; g.q_tok = a.ldq; g.q_head = a.hd;
+    g.out = a.out_b ? a.out_b : a.out;
+    g.out_lo = a.out_b_lo;
+    g.out_kind = !a.out_b ? AO_F32 : a.out_f16 ? AO_F16 : AO_BF16_PAIR;
+    g.o_tok = a.ldo; g.o_head = a.hd;
+    g.out32 = g.out_kind == AO_F16 && a.ldo % 16 == 0 && a.hd % 16 == 0;
+    g.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)a.hd));
+    g.window = c->window;
+    g.n_sink = c->n_sink;
+    g.hdr = reinterpret_cast<const int32_t*>(c->pg_dev);
+    g.first1 = reinterpret_cast<const int32_t*>(c->pg_dev + c->pg_first[0]);
+    g.first2 = reinterpret_cast<const int32_t*>(c->pg_dev + c->pg_first[1]);
+    g.cuts2 = reinterpret_cast<const int32_t*>(c->pg_dev + c->pg_cuts);
+    g.units1 = reinterpret_cast<const AttnUnit*>(c->pg_dev + c->pg_units[0]);
+    g.units2 = reinterpret_cast<const AttnUnit*>(c->pg_dev + c->pg_units[1]);
+    g.table = a.list_cells;
+    g.key_pos = a.list_pos;
+    g.perm = a.perm;
+    g.tok_pos = a.tok_pos;
+    g.part_o = c->pg_part_o;
+    g.part_ml = c->pg_part_ml;
+    g.part_o2 = c->pg_part_o + plan_part_rows(c->pg_caps, false) * a.hd;
+    g.part_ml2 = c->pg_part_ml + plan_part_rows(c->pg_caps, false);
+    g.tickets = c->pg_tickets;
+    g.err = c->d_err;
+    g.form = c->pg_plan.form();
+    g.n_sm = c->n_sm;
+    return launch_attn_paged(g, c->st);
 }
 
 // Which decode-GEMV variant serves each op of a T-token ubatch.
@@ -483,10 +674,26 @@ bool forward_ubatch(llm_ctx* c, int32_t T, int32_t O, int32_t out_row0, int32_t 
     const int32_t* din = c->d_in;
     const int32_t *tok = din + io.tok, *pos = din + io.pos, *slot = din + io.slot;
     const double kv_es = c->kv_value_bytes();
-    const bool q8 = c->kv_q8();
+    const bool q8 = c->kv_q8(), staged = q8 || c->kv_f8();
     const int32_t U = c->n_ubatch;
     float* stage_k = c->kv_stage;
-    float* stage_v = q8 ? c->kv_stage + (size_t)Hkv * U * hd : nullptr;
+    float* stage_v = staged ? c->kv_stage + (size_t)Hkv * U * hd : nullptr;
+    // the staged rows of this ubatch, quantised into one layer's cache
+    auto quantise = [&](void* kc, void* vc, bool after) {
+        if (q8) {
+            launch_kv_quant_q8(stage_k, stage_v, U, T, Hkv, hd, slot, kc, vc, c->n_ctx, c->d_err, st, after);
+            return true;
+        }
+        KvRowsArgs r;
+        r.kv = layer_pages(c, kc, vc);
+        r.type = W_F32;
+        r.k = stage_k; r.v = stage_v;
+        r.s_tok = hd; r.s_head = (int64_t)U * hd;
+        r.cell = slot; r.n = T; r.err = c->d_err;
+        if (launch_kv_rows_store(r, st)) return true;
+        c->err = "KV store launch failed";
+        return false;
+    };
     const bool gemv = T <= gemv_max_tokens();
     const int32_t lin_cls = gemv ? KC_LINEAR_GEMV : (c->tc_ok ? KC_LINEAR_TC : KC_LINEAR_GEMM);
     const double Td = T, Od = O;
@@ -583,15 +790,15 @@ bool forward_ubatch(llm_ctx* c, int32_t T, int32_t O, int32_t out_row0, int32_t 
             g.y = c->qkv; g.ldy = qkvw;
             g.H = H; g.Hkv = Hkv; g.hd = hd; g.n_ctx = c->n_ctx; g.kv_type = c->type_k;
             g.cs = c->rope_cs; g.slot = slot; g.kc = kc; g.vc = vc;
-            if (q8) {                               // float32 rows to the staging area, cell = token
+            if (staged) {                           // float32 rows to the staging area, cell = token
                 g.kv_type = W_F32; g.n_ctx = U; g.slot = nullptr; g.kc = stage_k; g.vc = stage_v;
             }
             if (!launch_gemv_bulk(L.qkv.type, g, GEPI_QKV, true, c->n_sm, st, pdl)) return bulk_fail();
-            kt_end(c, k, lin_cls, wbytes(L.qkv, qkvw) + Td * (d * 4.0 + qw * 4.0 + 2.0 * Hkv * hd * (q8 ? 4.0 : kv_es)),
+            kt_end(c, k, lin_cls, wbytes(L.qkv, qkvw) + Td * (d * 4.0 + qw * 4.0 + 2.0 * Hkv * hd * (staged ? 4.0 : kv_es)),
                    2.0 * Td * qkvw * d);
-            if (q8) {
+            if (staged) {
                 k = kt_begin(c);
-                launch_kv_quant_q8(stage_k, stage_v, U, T, Hkv, hd, slot, kc, vc, c->n_ctx, c->d_err, st, pdl);
+                if (!quantise(kc, vc, pdl)) return false;
                 kt_end(c, k, KC_ROPE_KV, Td * 2.0 * Hkv * hd * (4.0 + kv_es), 0);
             }
         } else {
@@ -601,7 +808,7 @@ bool forward_ubatch(llm_ctx* c, int32_t T, int32_t O, int32_t out_row0, int32_t 
             else launch_rmsnorm(c->x, nullptr, T, d, L.attn_norm, hp.rms_eps, c->h, st);
             kt_end(c, k, KC_RMSNORM, norm_bytes, 0);
             // F16 cache, f16 GEMM operands: RoPE and the K/V append run in the GEMM's epilogue
-            const bool fused_qkv = f16 && !q8 && c->type_k == LLM_TYPE_F16 && c->type_v == LLM_TYPE_F16 &&
+            const bool fused_qkv = f16 && !staged && c->type_k == LLM_TYPE_F16 && c->type_v == LLM_TYPE_F16 &&
                                    tc_tn_qkv_ok(H, Hkv, hd) && tc_tn_ok(qkvw, d);
             k = kt_begin(c);
             if (fused_qkv) {
@@ -622,10 +829,10 @@ bool forward_ubatch(llm_ctx* c, int32_t T, int32_t O, int32_t out_row0, int32_t 
             kt_end(c, k, lin_cls, wbytes(L.qkv, qkvw) + Td * (d + qkvw) * 4.0, 2.0 * Td * qkvw * d);
             if (!fused_qkv) {
                 k = kt_begin(c);
-                if (q8) {
+                if (staged) {
                     launch_rope_kv_append(c->qkv, T, H, Hkv, hd, c->rope_cs, nullptr, stage_k, stage_v, U,
                                           W_F32, c->d_err, st);
-                    launch_kv_quant_q8(stage_k, stage_v, U, T, Hkv, hd, slot, kc, vc, c->n_ctx, c->d_err, st, false);
+                    if (!quantise(kc, vc, false)) return false;
                 } else {
                     launch_rope_kv_append(c->qkv, T, H, Hkv, hd, c->rope_cs, slot, kc, vc, c->n_ctx,
                                           c->type_k, c->d_err, st);
@@ -633,7 +840,7 @@ bool forward_ubatch(llm_ctx* c, int32_t T, int32_t O, int32_t out_row0, int32_t 
                 kt_end(c, k, KC_ROPE_KV, Td * ((double)qkvw * 4.0 + qw * 4.0 + 2.0 * Hkv * hd * kv_es), 0);
             }
         }
-        if (c->debug && q8) {                       // staging [Hkv][U][hd] -> [T][Hkv * hd]
+        if (c->debug && staged) {                   // staging [Hkv][U][hd] -> [T][Hkv * hd]
             const size_t kw = (size_t)Hkv * hd;
             for (int32_t g2 = 0; g2 < Hkv; ++g2) {
                 cudaMemcpy2DAsync(c->dbg_kin + (size_t)il * T * kw + (size_t)g2 * hd, sizeof(float) * kw,
@@ -664,7 +871,10 @@ bool forward_ubatch(llm_ctx* c, int32_t T, int32_t O, int32_t out_row0, int32_t 
             a.v_scale = static_cast<const uint8_t*>(vc) + kv_q8_scale_offset(Hkv, c->n_ctx, hd);
         }
         k = kt_begin(c);
-        if (!launch_attention(a, st)) { c->err = "attention shape not supported"; return false; }
+        if (c->paged() ? !paged_attention(c, a, kc, vc) : !launch_attention(a, st)) {
+            c->err = c->paged() ? "attention launch failed" : "attention shape not supported";
+            return false;
+        }
         kt_end(c, k, KC_ATTENTION, -1.0, 0);
         if (c->debug) {
             cudaMemcpy2DAsync(c->dbg_q + (size_t)il * T * qw, sizeof(float) * qw, c->qkv,
@@ -825,9 +1035,10 @@ llm_ctx* llm_ctx_init(const llm_hparams* hp, const llm_cparams* cp) {
     if (!(h.rms_eps >= 0.f) || !(h.rope_freq_base > 0.f)) return fail("bad rms_eps / rope_freq_base");
     if (cp->n_ctx == 0 || cp->n_batch == 0 || cp->n_ubatch == 0) return fail("zero context size");
     if (cp->n_seq_max < 1 || cp->n_seq_max > (uint32_t)kMaxSeq) return fail("n_seq_max out of range");
-    if ((cp->type_k != LLM_TYPE_F32 && cp->type_k != LLM_TYPE_F16 && cp->type_k != LLM_TYPE_Q8_0) ||
+    if ((cp->type_k != LLM_TYPE_F32 && cp->type_k != LLM_TYPE_F16 && cp->type_k != LLM_TYPE_Q8_0 &&
+         cp->type_k != LLM_TYPE_F8_E4M3) ||
         cp->type_v != cp->type_k)
-        return fail("type_k/type_v must both be F32, both F16 or both Q8_0");
+        return fail("type_k/type_v must both be F32, both F16, both Q8_0 or both F8_E4M3");
     if (cp->n_ctx > (1u << 24)) return fail("n_ctx too large");
 
     auto* c = new llm_ctx();
@@ -863,7 +1074,8 @@ llm_ctx* llm_ctx_init(const llm_hparams* hp, const llm_cparams* cp) {
     const size_t kv_bytes = (size_t)h.n_layer * c->kv_layer_bytes();
     bool ok = dalloc(c, reinterpret_cast<uint8_t**>(&c->kv_k), kv_bytes) &&
               dalloc(c, reinterpret_cast<uint8_t**>(&c->kv_v), kv_bytes) &&
-              (!c->kv_q8() || dalloc(c, &c->kv_stage, 2 * (size_t)h.n_head_kv * U * h.head_dim)) &&
+              (!(c->kv_q8() || c->kv_f8()) || dalloc(c, &c->kv_stage, 2 * (size_t)h.n_head_kv * U * h.head_dim)) &&
+              (!c->kv_f8() || paged_setup(c)) &&
               (!c->kv_q8() || dalloc(c, &c->kv_f16, 2 * (size_t)h.n_head_kv * c->n_ctx * h.head_dim)) &&
               dalloc(c, &c->x, U * d) && dalloc(c, &c->h, U * d) &&
               dalloc(c, &c->qkv, U * c->qkv_width()) && dalloc(c, &c->attn, U * c->q_width()) &&
@@ -924,6 +1136,8 @@ void llm_ctx_free(llm_ctx* c) {
     c->allocs.clear();
     if (c->h_in) cudaFreeHost(c->h_in);
     if (c->h_err) cudaFreeHost(c->h_err);
+    if (c->pg_host) cudaFreeHost(c->pg_host);
+    if (c->h_samples) cudaFreeHost(c->h_samples);
     for (cudaEvent_t e : c->ev_pool) cudaEventDestroy(e);
     if (c->own_stream && c->st) cudaStreamDestroy(c->st);
     delete c;
@@ -1296,7 +1510,7 @@ int32_t llm_decode(llm_ctx* c, llm_batch bt) {
         const bool small = T <= gemv_max_tokens();
         const int32_t cap = small ? attn_cap(c, T) : c->max_work;
         // the one-token kernel stages one pass of decode_step_cells() cells per work item
-        const bool fused = T == 1 && c->step_ok && !c->debug;
+        const bool fused = T == 1 && c->step_ok && !c->debug && !c->paged();
         // prefill tiles: a work item per (tile, KV head) unless that leaves SMs idle; splitting a
         // tile's list costs a merge (measured at 512 tokens: 48 us per layer unsplit, 101 us in
         // 256-cell items, 126 us in 128-cell items)
@@ -1307,6 +1521,10 @@ int32_t llm_decode(llm_ctx* c, llm_batch bt) {
         const int32_t tile_q = tc_attn ? attention_tc_tile_q() : kAttnTileQ;
         build_attn_plan(c->cells, b, i0, T, tile_q, c->hp.n_head_kv, G, (small ? 4 : 1) * c->n_sm,
                         c->max_rows, cap, c->plan, fused ? decode_step_cells() : small ? 64 : tc_attn ? 128 : 32);
+        if (c->paged() && !c->host_only && !paged_plan(c, b, i0, T, !small && c->tc_ok && c->tc_f16)) {
+            rollback(c, i0, T);
+            return -2;
+        }
         if (c->debug) {
             UbDebug u;
             u.n_kv = c->cells.n_kv();
@@ -1359,14 +1577,15 @@ int32_t llm_decode(llm_ctx* c, llm_batch bt) {
                                cuda_ok(c, cudaMemcpyAsync(c->d_in + io.list_pos, hi + io.list_pos,
                                                           nl * sizeof(int32_t), cudaMemcpyHostToDevice,
                                                           c->st), "inputs upload"))) &&
-                  cuda_ok(c, cudaMemsetAsync(c->d_err, 0, sizeof(uint32_t), c->st), "memset");
+                  cuda_ok(c, cudaMemsetAsync(c->d_err, 0, sizeof(uint32_t), c->st), "memset") &&
+                  (!c->paged() || paged_upload(c));
         if (c->ktime) attention_work(c, b.pos.data() + i0);
         const int32_t max_nq = p.max_nq <= 1 ? 1 : tile_q;
         int32_t max_len = 0;
         for (size_t l = 0; l + 1 < p.list_off.size(); ++l) max_len = std::max(max_len, p.list_off[l + 1] - p.list_off[l]);
         c->dec_long = max_len >= kDecLongList;
         const StepGraph* sg = nullptr;
-        const bool one_kernel = ok && T == 1 && c->step_ok && !c->debug;
+        const bool one_kernel = ok && T == 1 && c->step_ok && !c->debug && !c->paged();
         if (one_kernel) ok = run_step(c, O, n_out);
         // decode ubatches (one token per attention tile: the cluster kernels, whose grid follows T)
         // replay a captured graph per key; prefill ubatches size their attention grids from the
@@ -1374,7 +1593,8 @@ int32_t llm_decode(llm_ctx* c, llm_batch bt) {
         if (ok && !one_kernel && (small || max_nq <= 1) && c->use_graphs && !c->debug) {
             const uint64_t key = (uint64_t)T | ((uint64_t)O << 10) | ((uint64_t)n_out << 20) |
                                  ((uint64_t)(max_nq > 1) << 52) | ((uint64_t)c->ktime << 53) |
-                                 ((uint64_t)c->dec_long << 54);
+                                 ((uint64_t)c->dec_long << 54) |
+                                 ((uint64_t)(c->paged() ? c->pg_plan.form() : 0) << 55);
             auto it = c->graphs.find(key);
             if (it == c->graphs.end()) {
                 StepGraph ng;
@@ -1492,6 +1712,9 @@ static int defrag(llm_ctx* c) {
         if (c->kv_q8()) {
             regions.push_back({0, hd});
             regions.push_back({kv_q8_scale_offset(Hkv, c->n_ctx, hd), hd / 32 * 2});
+        } else if (c->kv_f8()) {
+            regions.push_back({0, hd});
+            regions.push_back({c->kv_layer_elems(), (int32_t)sizeof(float)});
         } else {
             regions.push_back({0, hd * (int32_t)type_size(c->type_k)});
         }
@@ -1566,7 +1789,7 @@ int64_t llm_debug_ubatch_mask(llm_ctx* c, int32_t ub, uint8_t* out, int64_t cap,
     for (int64_t t = 0; t < T; ++t) {
         const int32_t l = u.tok_list[t];
         for (int32_t k = u.list_off[l]; k < u.list_off[l + 1]; ++k)
-            if (u.list_pos[k] <= u.pos[t] && u.list_cells[k] < nkv) m[t * nkv + u.list_cells[k]] = 1;
+            if (c->sees(u.pos[t], u.list_pos[k]) && u.list_cells[k] < nkv) m[t * nkv + u.list_cells[k]] = 1;
     }
     std::memcpy(out, m.data(), (size_t)std::min(n, cap));
     return n;
@@ -1580,7 +1803,7 @@ int llm_debug_capture(llm_ctx* c, int enable) {
     const bool ok = dalloc(c, &c->dbg_embd, U * d) && dalloc(c, &c->dbg_lout, L * U * d) &&
                     dalloc(c, &c->dbg_attn, L * U * qw) && dalloc(c, &c->dbg_q, L * U * qw) &&
                     dalloc(c, &c->dbg_rnorm, U * d) &&
-                    (!c->kv_q8() || (dalloc(c, &c->dbg_kin, L * U * c->hp.n_head_kv * c->hp.head_dim) &&
+                    (!(c->kv_q8() || c->kv_f8()) || (dalloc(c, &c->dbg_kin, L * U * c->hp.n_head_kv * c->hp.head_dim) &&
                                      dalloc(c, &c->dbg_vin, L * U * c->hp.n_head_kv * c->hp.head_dim)));
     return ok ? 0 : -2;
 }
@@ -1835,6 +2058,102 @@ int32_t llm_sample_ith(llm_ctx* c, int32_t i, const llm_sampler_params* p, float
     }
     if (st != 0) { c->err = "sampler found no candidate"; return -1; }
     return c->h_sample_tok[kMaxPenalty];
+}
+
+int32_t llm_sample_batch(llm_ctx* c, int32_t n, const int32_t* rows, const llm_sampler_params* params, const float* u,
+                         int32_t* tokens) {
+    if (!c || c->host_only || n < 0) return -1;
+    if (n == 0) return 0;
+    if (!rows || !params || !u || !tokens) { c->err = "NULL sampler arguments"; return -1; }
+    if (c->hp.n_vocab > sample_rows_max_vocab()) { c->err = "vocabulary too large for the batched sampler"; return -1; }
+    size_t n_pen = 0;
+    bool any_pen = false;
+    for (int32_t i = 0; i < n; ++i) {
+        const llm_sampler_params& p = params[i];
+        if (p.top_k < 1 || !(p.top_p > 0.f && p.top_p <= 1.f) || !(p.min_p >= 0.f && p.min_p < 1.f) ||
+            !(u[i] >= 0.f && u[i] < 1.f) || p.n_penalty_tokens < 0 || (p.n_penalty_tokens > 0 && !p.penalty_tokens) ||
+            !(p.repeat_penalty > 0.f)) {
+            c->err = "invalid sampler parameters";
+            return -1;
+        }
+        if (resolve_row(c, rows[i]) < 0) { c->err = "no logits for this output"; return -1; }
+        if (p.repeat_penalty != 1.f && p.n_penalty_tokens > 0) {
+            any_pen = true;
+            n_pen += (size_t)p.n_penalty_tokens;
+        }
+    }
+    if (n_pen > (size_t)INT32_MAX) { c->err = "too many penalty tokens"; return -1; }
+    cudaSetDevice(c->device);
+    // one buffer: per entry row, top_k, top_p, min_p, temperature, u, penalty; list starts [n + 1]; lists; the picks
+    const size_t N = (size_t)n, words = 7 * N + (N + 1) + n_pen + N;
+    if (words * 4 > c->samples_cap) {
+        const size_t cap = std::max(words * 4, 2 * c->samples_cap);
+        if (c->h_samples) cudaFreeHost(c->h_samples);
+        dfree(c, c->d_samples);
+        c->h_samples = nullptr;
+        c->d_samples = nullptr;
+        c->samples_cap = 0;
+        if (!cuda_ok(c, cudaMallocHost(&c->h_samples, cap), "cudaMallocHost") || !dalloc(c, &c->d_samples, cap)) return -1;
+        c->samples_cap = cap;
+    }
+    int32_t* hi = reinterpret_cast<int32_t*>(c->h_samples);
+    float* hf = reinterpret_cast<float*>(c->h_samples);
+    int32_t at = 0;
+    for (int32_t i = 0; i < n; ++i) {
+        const llm_sampler_params& p = params[i];
+        hi[i] = resolve_row(c, rows[i]);
+        hi[N + i] = p.top_k;
+        hf[2 * N + i] = p.top_p;
+        hf[3 * N + i] = p.min_p;
+        hf[4 * N + i] = p.temperature;
+        hf[5 * N + i] = u[i];
+        hf[6 * N + i] = p.repeat_penalty;
+        hi[7 * N + i] = at;
+        if (p.repeat_penalty != 1.f && p.n_penalty_tokens > 0) {
+            std::memcpy(hi + 8 * N + 1 + at, p.penalty_tokens, sizeof(int32_t) * (size_t)p.n_penalty_tokens);
+            at += p.n_penalty_tokens;
+        }
+    }
+    hi[8 * N] = at;
+    SampleRowsArgs a;
+    const int32_t* di = reinterpret_cast<const int32_t*>(c->d_samples);
+    const float* df = reinterpret_cast<const float*>(c->d_samples);
+    a.type = W_F32; a.n_rows = n; a.V = c->hp.n_vocab;
+    a.logits = c->d_logits; a.ld = c->hp.n_vocab;
+    a.row = di;
+    a.top_k = di + N; a.top_p = df + 2 * N; a.min_p = df + 3 * N; a.temperature = df + 4 * N; a.u = df + 5 * N;
+    if (any_pen) {
+        a.penalty = df + 6 * N;
+        a.pen_start = di + 7 * N;
+        a.pen_tok = di + 8 * N + 1;
+        a.n_pen = (int32_t)n_pen;
+    }
+    const size_t out = 8 * N + 1 + n_pen;
+    a.token = reinterpret_cast<int32_t*>(c->d_samples) + out;
+    const bool ok = cuda_ok(c, cudaMemcpyAsync(c->d_samples, c->h_samples, out * 4, cudaMemcpyHostToDevice, c->st), "copy") &&
+                    (launch_sample_rows(a, c->st) || (c->err = "sampler launch failed", false)) &&
+                    cuda_ok(c, cudaMemcpyAsync(hi + out, a.token, N * 4, cudaMemcpyDeviceToHost, c->st), "copy") &&
+                    cuda_ok(c, cudaStreamSynchronize(c->st), "sampler");
+    if (!ok) { cudaGetLastError(); return -1; }
+    std::memcpy(tokens, hi + out, N * 4);
+    return 0;
+}
+
+int llm_set_attn_window(llm_ctx* c, int32_t window, int32_t n_sink) {
+    if (!c) return -1;
+    if (window < 0 || n_sink < 0) { c->err = "window and n_sink must not be negative"; return -1; }
+    if (window > 0 && c->type_k != LLM_TYPE_F16 && c->type_k != LLM_TYPE_F8_E4M3) {
+        c->err = "an attention window needs an F16 or F8_E4M3 cache";
+        return -1;
+    }
+    if (window > 0 && !c->host_only) {
+        cudaSetDevice(c->device);
+        if (!paged_setup(c)) return -1;
+    }
+    drop_graphs(c);                              // (they were captured for the window before)
+    c->window = window;
+    c->n_sink = window > 0 ? n_sink : 0;
+    return 0;
 }
 
 int llm_debug_set_logits(llm_ctx* c, int32_t i, const float* row) {

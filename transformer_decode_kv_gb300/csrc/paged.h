@@ -112,7 +112,7 @@ struct AttnPagedArgs {
 bool launch_attn_paged(const AttnPagedArgs& a, cudaStream_t st);
 bool attn_paged_types_ok(int32_t q_type, int32_t kv_type);
 // 256-row tiles serve this shape (attn_paged_tc.cu).
-bool attn_paged_tc_ok(int32_t hd, int32_t kv_type, int32_t q_type);
+bool attn_paged_tc_ok(int32_t hd, int32_t kv_type, int32_t q_type, bool round_q = false);
 bool launch_attn_paged_tc(const AttnPagedArgs& a, cudaStream_t st);
 
 // ---- host plan (attn_paged_plan.cpp)
