@@ -17,7 +17,7 @@
 // Roles (12 warps; warps 0-3 give registers to warps 4-11, whose threads hold a row of scores each): warps
 // 0 and 1 bring K and V rows into a ring of 128-byte-swizzled tiles, with the keys' positions: a block whose keys are
 // all read in bulk tensor copies of the runs of neighbouring cells that pages are, others in 16-byte
-// asynchronous copies row by row, and E4M3 rows through registers, converted to f16;
+// asynchronous copies row by row, and E4M3 rows as raw bytes, converted to f16 from there;
 // warp 2 issues the MMAs; warps 4-7 and 8-11 are the two halves' softmax and epilogue (a thread owns a
 // TMEM lane: warp w reads lanes 32 (w % 4) on). m is 6 below a row maximum and raised lazily, when p would
 // pass 2^14: O, in TMEM, is rarely rescaled, and never more than it must. P is rounded to f16 (half a step 2^-11)
@@ -48,7 +48,7 @@ constexpr int kMmaWarp = 2;
 constexpr int kSoft0 = 4;                                  // first softmax warp
 constexpr int kThr = 12 * 32;
 constexpr int kKeys = 128;                                 // keys per block
-constexpr int kStages = 5;                                 // K or V tiles in flight
+constexpr int kStages = 5;                                 // K or V tiles in flight (E4M3: one less, its place holds raw rows)
 constexpr int kMeta = 3;                                   // blocks whose positions are kept (see meta_full)
 constexpr uint32_t kBlk = 128 * 128;                       // [128 rows][64 16-bit values], swizzled
 constexpr uint64_t kWaitNs = 2000000000ull;
@@ -222,9 +222,10 @@ __device__ __forceinline__ uint32_t swz(int r, int ch) {
 // even: the maps have one page. aligned: the plan's blocks of keys are whole runs.
 struct TmaRuns { int rows; bool even, aligned; };
 
+template <int N>
 struct Ring {                                              // position in the ring of K and V tiles
     uint32_t s = 0, ph = 0;
-    __device__ __forceinline__ void next() { if (++s == kStages) { s = 0; ph ^= 1u; } }
+    __device__ __forceinline__ void next() { if (++s == N) { s = 0; ph ^= 1u; } }
 };
 struct MetaAt {
     uint32_t s = 0, ph = 0;
@@ -238,6 +239,7 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
     using M = Smem<HD>;
     constexpr bool F8 = CT == W_F8, BF = CT == W_BF16;
     constexpr int CH = HD / 8;                              // 16-byte chunks of a 16-bit row
+    constexpr int NS = F8 ? kStages - 1 : kStages;
     extern __shared__ __align__(1024) uint8_t sm[];
     int* kpos = reinterpret_cast<int*>(sm + M::kpos);
     volatile uint32_t* full = reinterpret_cast<volatile uint32_t*>(sm + M::full);
@@ -250,7 +252,7 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
     uint64_t* o_done = p_full + 2;                          // [2] 1: MMA commit after the unit's last product
     uint64_t* q_full = o_done + 2;                          // 1: the loading warp, or 256: the softmax threads
     // [kMeta] a block's positions. Slot j % 3 is written again for block j + 3, whose K tile needs the
-    // ring place of V tile j (five stages), freed after both halves' softmax of block j.
+    // ring place of V tile j (five stages) or K tile j + 1 (four), freed after both halves' softmax of block j.
     uint64_t* meta_full = q_full + 1;
     uint64_t* q_empty = meta_full + kMeta;                  // 1: MMA commit after the unit's last scores
     int* misc = reinterpret_cast<int*>(sm + M::misc);
@@ -314,10 +316,12 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
     };
 
     // Each role walks the CTA's units by itself; the barriers above keep them in step. Registers: three warpgroups
-    // of 168 a thread at launch, 504 = kRegsLow + 2 kRegsHigh.
-    constexpr int kRegsLow = F8 ? 120 : 88, kRegsHigh = F8 ? 192 : 208;
+    // of 168 a thread at launch, 504 >= kRegsLow + 2 kRegsHigh. What is spilled comes back from L2 (shared memory
+    // leaves L1 little), so both parts count: 2048 new tokens at the end of 32768 E4M3 keys (32 / 8 heads of 128) took
+    // 5360 us with 120 + 192 and 3720 us with 152 + 176 while producers held raw rows in registers, 1350 us as here.
+    constexpr int kRegsLow = F8 ? 104 : 88, kRegsHigh = F8 ? 200 : 208;
     static_assert(kRegsLow + 2 * kRegsHigh <= 3 * 168, "registers of the launch");
-    Ring ring;
+    Ring<NS> ring;
     MetaAt meta;
     if (warp < kSoft0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
@@ -369,6 +373,116 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
                         }
                     }
                 };
+                if constexpr (F8) {
+                    // Raw rows travel by asynchronous copies into this warp's part of the ring's last place, a tile in
+                    // four quarters of 32 rows, each loaded for the next tile as soon as it is converted: three or
+                    // four quarters are under way all the time, and none in registers. A lane converts the bytes
+                    // that it copied. Lanes of a quarter warp hold two rows' chunks of one 64-column block, so that
+                    // their stores' banks differ (eight chunks of one row, all even, would meet in pairs); the raw
+                    // rows' halves are swapped in odd rows for the same reason.
+                    constexpr int LR = HD / 16;             // lanes per row, 16 values each
+                    constexpr int RI = 32 / LR;             // rows at a time
+                    constexpr int BX = 4;                   // 16-byte pieces converted together
+                    const int lr = LR == 8 ? ((lane >> 2) & 1) | ((lane >> 4) << 1) : lane / LR;
+                    const int lc = LR == 8 ? (lane & 3) | ((lane >> 1) & 4) : lane % LR;
+                    const uint8_t* const raw = sm + M::kv + NS * M::tile + (is_v ? kKeys * HD : 0) + lr * HD +
+                                               16 * (LR == 8 ? lc ^ ((lr & 1) << 2) : lc);
+                    const uint32_t raw_s = sa(raw);
+                    Key cur[4], nxt[4];
+                    auto bring = [&](const Key& k, int q) { // quarter q of a tile, its keys' rows in the lanes of k
+#pragma unroll
+                        for (int x = 0; x < LR; ++x) {
+                            const int64_t off = __shfl_sync(0xffffffffu, k.off, x * RI + lr);
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(raw_s + (32 * q + x * RI) * HD),
+                                         "l"(base + (off >= 0 ? off : 0) + 16 * lc), "r"(off >= 0 ? 16 : 0) : "memory");
+                        }
+                    };
+                    lookup(cur, 0);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        bring(cur[q], q);
+                        asm volatile("cp.async.commit_group;" ::: "memory");
+                    }
+                    float inv;
+                    {                                       // s0 of this unit: the largest scale of its first block
+                        float mx = fmaxf(fmaxf(cur[0].s, cur[1].s), fmaxf(cur[2].s, cur[3].s));
+#pragma unroll
+                        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                        if (!(mx > 0.f)) mx = 1.f;
+                        if (lane == 0) s0[2 * slot + (is_v ? 1 : 0)] = mx;
+                        inv = 1.f / mx;
+                    }
+                    for (int j = 0; j < nt; ++j, it += 2) {
+                        const uint32_t stage = it % NS, ph = (it / NS) & 1u;
+                        uint8_t* const dst = sm + M::kv + stage * M::tile;
+                        const bool more = j + 1 < nt;
+                        if (more) lookup(nxt, j + 1);
+                        bool all = true;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            cur[i].s *= inv;
+                            all = all && cur[i].off >= 0;
+                            if (cur[i].off >= 0 && !(cur[i].s <= 128.f)) redo_f[slot] = 1;
+                        }
+                        all = __all_sync(0xffffffffu, all);
+                        ok = it < NS || wait(&kv_empty[stage], ph ^ 1u);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+#pragma unroll 1
+                        for (int q = 0; q < 4; ++q) {
+                            asm volatile("cp.async.wait_group 3;" ::: "memory");
+                            float sq = cur[0].s;
+#pragma unroll
+                            for (int i = 1; i < 4; ++i) if (q == i) sq = cur[i].s;
+#pragma unroll
+                            for (int x0 = 0; x0 < LR; x0 += BX) {
+                                uint4 in[BX];               // (all read before the first store: the two might alias)
+                                __half2 fh[BX];
+#pragma unroll
+                                for (int x = 0; x < BX; ++x) {
+                                    in[x] = *reinterpret_cast<const uint4*>(raw + (32 * q + (x0 + x) * RI) * HD);
+                                    fh[x] = __float2half2_rn(__shfl_sync(0xffffffffu, sq, (x0 + x) * RI + lr));
+                                }
+#pragma unroll
+                                for (int x = 0; x < BX; ++x) {
+                                    const uint32_t w[4] = {in[x].x, in[x].y, in[x].z, in[x].w};
+                                    uint32_t h[8];
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) e4m3x4_to_h2(w[i], h[2 * i], h[2 * i + 1]);
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i) {
+                                        const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&h[i]), fh[x]);
+                                        h[i] = *reinterpret_cast<const uint32_t*>(&y);
+                                    }
+                                    const int r = 32 * q + (x0 + x) * RI + lr;
+                                    *reinterpret_cast<uint4*>(dst + swz(r, 2 * lc)) = make_uint4(h[0], h[1], h[2], h[3]);
+                                    *reinterpret_cast<uint4*>(dst + swz(r, 2 * lc + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
+                                }
+                            }
+                            if (more) {
+                                Key kq = nxt[0];
+#pragma unroll
+                                for (int i = 1; i < 4; ++i) if (q == i) kq.off = nxt[i].off;
+                                bring(kq, q);
+                            }
+                            asm volatile("cp.async.commit_group;" ::: "memory");
+                        }
+                        if (!is_v) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) kpos[meta.s * kKeys + 32 * i + lane] = cur[i].pos;
+                            if (lane == 0) full[meta.s] = all;
+                        }
+                        to_async_proxy();
+                        __syncwarp();
+                        if (lane == 0) {
+                            bar_arrive(&kv_full[stage]);
+                            if (!is_v) bar_arrive(&meta_full[meta.s]);
+                        }
+                        if (!is_v) meta.next();
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) cur[i] = nxt[i];
+                    }
+                } else {
                 // Blocks that need no look at single keys: positions are indices, the block's pages hold whole runs, and
                 // some row sees each key. A lane brings one box of 64 dims x runs.rows cells.
                 constexpr int HB = HD / 64;
@@ -391,7 +505,6 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
                 int page_nxt = 0, at_nxt = 0;
                 bool plain_nxt = plain(0);
                 if (plain_nxt) page_nxt = box_page(0, at_nxt);
-                float inv = 1.f;
                 // row copies are announced one tile of this warp's later, when they have landed (not two: K tile
                 // j + 2 needs the place of V tile j - 1, which is not free before the scores of block j)
                 int pend = -1;                              // stage
@@ -407,11 +520,11 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
                     pend = -1;
                 };
                 for (int j = 0; j < nt; ++j, it += 2) {
-                    const uint32_t stage = it % kStages, ph = (it / kStages) & 1u;
+                    const uint32_t stage = it % NS, ph = (it / NS) & 1u;
                     uint8_t* const dst = sm + M::kv + stage * M::tile;
                     const uint32_t fb = sa(&kv_full[stage]);
                     auto claim = [&]() {
-                        ok = it < kStages || wait(&kv_empty[stage], ph ^ 1u);
+                        ok = it < NS || wait(&kv_empty[stage], ph ^ 1u);
                         ok = __all_sync(0xffffffffu, ok);
                         return ok;
                     };
@@ -454,58 +567,7 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
 #pragma unroll
                         for (int i = 0; i < 4; ++i) all = all && cur[i].off >= 0;
                         all = __all_sync(0xffffffffu, all);
-                        if constexpr (F8) {
-                            if (j == 0) {                   // s0 of this unit: the largest scale of its first block
-                                float mx = fmaxf(fmaxf(cur[0].s, cur[1].s), fmaxf(cur[2].s, cur[3].s));
-#pragma unroll
-                                for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                                if (!(mx > 0.f)) mx = 1.f;
-                                if (lane == 0) s0[2 * slot + (is_v ? 1 : 0)] = mx;
-                                inv = 1.f / mx;
-                            }
-                            constexpr int LR = HD / 16;     // lanes per row, 16 values each
-                            float f[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                f[i] = cur[i].s * inv;
-                                if (cur[i].off >= 0 && !(f[i] <= 128.f)) redo_f[slot] = 1;
-                            }
-                            // the first half's bytes travel while the stage is waited for
-                            uint4 raw[2 * LR];
-                            auto bring = [&](int g0) {
-#pragma unroll
-                                for (int x = 0; x < 2 * LR; ++x) {
-                                    const int64_t off = __shfl_sync(0xffffffffu, g0 ? cur[2 + x / LR].off : cur[x / LR].off,
-                                                                    x % LR * (32 / LR) + lane / LR);
-                                    raw[x] = off >= 0 ? *reinterpret_cast<const uint4*>(base + off + 16 * (lane % LR))
-                                                      : make_uint4(0u, 0u, 0u, 0u);
-                                }
-                            };
-                            auto put = [&](int g0) {
-#pragma unroll
-                                for (int x = 0; x < 2 * LR; ++x) {
-                                    const int r = x % LR * (32 / LR) + lane / LR, c = lane % LR;
-                                    const __half2 fh = __float2half2_rn(__shfl_sync(0xffffffffu, g0 ? f[2 + x / LR] : f[x / LR], r));
-                                    const uint32_t w[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
-                                    uint32_t h[8];
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i) e4m3x4_to_h2(w[i], h[2 * i], h[2 * i + 1]);
-#pragma unroll
-                                    for (int i = 0; i < 8; ++i) {
-                                        const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&h[i]), fh);
-                                        h[i] = *reinterpret_cast<const uint32_t*>(&y);
-                                    }
-                                    const int rr = 32 * (g0 + x / LR) + r;
-                                    *reinterpret_cast<uint4*>(dst + swz(rr, 2 * c)) = make_uint4(h[0], h[1], h[2], h[3]);
-                                    *reinterpret_cast<uint4*>(dst + swz(rr, 2 * c + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
-                                }
-                            };
-                            bring(0);
-                            if (!claim()) break;
-                            put(0);
-                            bring(2);
-                            put(2);
-                        } else {
+                        {
                             // runs of neighbouring cells among single cells
                             bool run = runs.rows > 0 && all;
 #pragma unroll
@@ -557,7 +619,6 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
                             for (int i = 0; i < 4; ++i) kpos[meta.s * kKeys + 32 * i + lane] = cur[i].pos;
                             if (lane == 0) full[meta.s] = all;
                         }
-                        if constexpr (F8) announce(stage);
                     }
                     if (!is_v) {
                         __syncwarp();
@@ -565,7 +626,8 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
                         meta.next();
                     }
                 }
-                if constexpr (!F8) flush();
+                flush();
+                }
             }
             // after a wait that gave up nobody may wait for the copies under way: they land before the CTA leaves
             if (!ok) {
@@ -606,9 +668,9 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
                     ring.next();
                 }
                 for (int j = 0; j < nt && ok; ++j) {
-                    const Ring rv = ring;
+                    const Ring<NS> rv = ring;
                     ring.next();
-                    const Ring rk = ring;
+                    const Ring<NS> rk = ring;
                     const bool more = j + 1 < nt;
                     if (!(ok = wait(&kv_full[rv.s], rv.ph))) break;
                     const uint32_t v = vd + rv.s * (M::tile >> 4);

@@ -24,6 +24,7 @@ namespace llm {
 namespace {
 
 constexpr int kThr = 256;
+constexpr int kRows = 4;                                    // rows a thread has in flight
 
 template <int T>
 __device__ __forceinline__ void load8(const void* base, int64_t elem, float* x) {
@@ -81,95 +82,133 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t two) {
     return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-// One row's place: the thread's 8 values of row `which` (0 K, 1 V), token i, head g.
-struct RowAt { int64_t i, g; int which, part; bool in; };
+// Rows in the order token, K or V, head: a block's threads take kRows times kThr * 8 / HD consecutive ones. A row's
+// place, found once per row; cell -1 where there is nothing to do.
+struct RowAt {
+    int64_t dense;                                          // first value of the row in the buffers
+    int64_t page;
+    int32_t at, g, cell;
+    bool v;
+};
 
 template <int HD>
-__device__ __forceinline__ RowAt row_at(const KvRowsArgs& a, int64_t t) {
-    constexpr int P = HD / 8;
-    RowAt r;
-    r.part = (int)(t % P);
-    const int64_t row = t / P;
-    r.in = row < (int64_t)a.n * a.kv.Hkv * 2;
-    r.g = row % a.kv.Hkv;
-    const int64_t q = row / a.kv.Hkv;
-    r.which = (int)(q & 1);
-    r.i = q >> 1;
-    return r;
+__device__ __forceinline__ void rows_at(const KvRowsArgs& a, RowAt* r) {
+    constexpr int N = kThr * 8 / HD;                        // rows of a block at a time
+    const uint32_t cols = 2u * (uint32_t)a.kv.Hkv, part = threadIdx.x % (HD / 8);
+    const uint64_t first = (uint64_t)blockIdx.x * (N * kRows);
+    const uint64_t i0 = first / cols;
+    const uint32_t c0 = (uint32_t)(first - i0 * cols) + threadIdx.x / (HD / 8);
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+        const uint32_t c = c0 + j * N, di = c / cols, col = c - di * cols;
+        const int64_t i = (int64_t)i0 + di;
+        r[j].v = col >= (uint32_t)a.kv.Hkv;
+        r[j].g = (int32_t)(r[j].v ? col - a.kv.Hkv : col);
+        r[j].cell = i < a.n ? a.cell[i] : -1;
+        r[j].dense = i * a.s_tok + r[j].g * a.s_head + part * 8;
+    }
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+        const uint32_t page = (uint32_t)max(r[j].cell, 0) / (uint32_t)a.kv.page_size;
+        r[j].page = page;
+        r[j].at = (int32_t)((uint32_t)max(r[j].cell, 0) - page * (uint32_t)a.kv.page_size);
+        if (page >= (uint32_t)a.kv.n_pages) {
+            if (part == 0 && r[j].cell >= 0 && a.err) atomicOr(a.err, ERR_SLOT_RANGE);
+            r[j].cell = -1;
+        }
+    }
+}
+__device__ __forceinline__ uint8_t* row_ptr(const PagedKv& kv, const RowAt& r) {
+    return (r.v ? kv.v : kv.k) + r.page * kv.sb_page + r.at * kv.sb_cell + r.g * kv.sb_head;
+}
+__device__ __forceinline__ float* scale_ptr(const PagedKv& kv, const RowAt& r) {
+    return (r.v ? kv.vs : kv.ks) + r.page * kv.ss_page + r.at * kv.ss_cell + r.g * kv.ss_head;
 }
 
 template <int HD, int CT, int T>
 __global__ void __launch_bounds__(kThr) kv_store_kernel(KvRowsArgs a) {
     constexpr int P = HD / 8;
-    const RowAt r = row_at<HD>(a, (int64_t)blockIdx.x * kThr + threadIdx.x);
-    const int32_t cell = r.in ? a.cell[r.i] : -1;
-    const bool past = cell >= 0 && cell / a.kv.page_size >= a.kv.n_pages;
-    if (past && r.part == 0 && a.err) atomicOr(a.err, ERR_SLOT_RANGE);
-    const bool live = cell >= 0 && !past;
-    float x[8] = {};
-    if (live) load8<T>(r.which ? a.v : a.k, r.i * a.s_tok + r.g * a.s_head + r.part * 8, x);
-    const int64_t page = live ? cell / a.kv.page_size : 0, at = live ? cell % a.kv.page_size : 0;
-    uint8_t* dst = (r.which ? a.kv.v : a.kv.k) + page * a.kv.sb_page + at * a.kv.sb_cell + r.g * a.kv.sb_head;
-    if constexpr (CT == W_F8) {
-        float amax = 0.f;
+    const int part = threadIdx.x % P;
+    RowAt r[kRows];
+    rows_at<HD>(a, r);
+    float x[kRows][8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float f = fabsf(x[j]);
-            if (f <= FLT_MAX) amax = fmaxf(amax, f);
+    for (int j = 0; j < kRows; ++j) {
+        if (r[j].cell >= 0) {
+            load8<T>(r[j].v ? a.v : a.k, r[j].dense, x[j]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[j][e] = 0.f;
         }
+    }
 #pragma unroll
-        for (int o = P / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        if (!live) return;
-        // 448 = 1.75 * 2^8: e = exponent(amax) - 8, one more above a mantissa of 1.75
-        const uint32_t b = __float_as_uint(amax);
-        int e = (int)(b >> 23) - 127 - 8 + ((b & 0x7fffffu) > 0x600000u);
-        e = amax == 0.f ? 0 : max(e, -126);
-        const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-        uint32_t w[4];
+    for (int j = 0; j < kRows; ++j) {
+        if constexpr (CT == W_F8) {
+            float amax = 0.f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = to_e4m3x2(x[2 * j] * inv, x[2 * j + 1] * inv);
-        *reinterpret_cast<uint2*>(dst + r.part * 8) = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
-        if (r.part == 0)
-            (r.which ? a.kv.vs : a.kv.ks)[page * a.kv.ss_page + at * a.kv.ss_cell + r.g * a.kv.ss_head] =
-                __uint_as_float((uint32_t)(e + 127) << 23);
-    } else {
-        if (live) store8<CT>(dst, r.part * 8, x);
+            for (int e = 0; e < 8; ++e) {
+                const float f = fabsf(x[j][e]);
+                if (f <= FLT_MAX) amax = fmaxf(amax, f);
+            }
+#pragma unroll
+            for (int o = P / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            if (r[j].cell < 0) continue;
+            // 448 = 1.75 * 2^8: e = exponent(amax) - 8, one more above a mantissa of 1.75
+            const uint32_t b = __float_as_uint(amax);
+            int e = (int)(b >> 23) - 127 - 8 + ((b & 0x7fffffu) > 0x600000u);
+            e = amax == 0.f ? 0 : max(e, -126);
+            const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = to_e4m3x2(x[j][2 * i] * inv, x[j][2 * i + 1] * inv);
+            *reinterpret_cast<uint2*>(row_ptr(a.kv, r[j]) + part * 8) = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+            if (part == 0) *scale_ptr(a.kv, r[j]) = __uint_as_float((uint32_t)(e + 127) << 23);
+        } else {
+            if (r[j].cell >= 0) store8<CT>(row_ptr(a.kv, r[j]), part * 8, x[j]);
+        }
     }
 }
 
 template <int HD, int CT, int T>
 __global__ void __launch_bounds__(kThr) kv_load_kernel(KvRowsArgs a) {
-    const RowAt r = row_at<HD>(a, (int64_t)blockIdx.x * kThr + threadIdx.x);
-    if (!r.in) return;
-    const int32_t cell = a.cell[r.i];
-    if (cell < 0) return;
-    if (cell / a.kv.page_size >= a.kv.n_pages) {
-        if (r.part == 0 && a.err) atomicOr(a.err, ERR_SLOT_RANGE);
-        return;
-    }
-    const int64_t page = cell / a.kv.page_size, at = cell % a.kv.page_size;
-    const uint8_t* src = (r.which ? a.kv.v : a.kv.k) + page * a.kv.sb_page + at * a.kv.sb_cell + r.g * a.kv.sb_head;
-    float x[8];
+    const int part = threadIdx.x % (HD / 8);
+    RowAt r[kRows];
+    rows_at<HD>(a, r);
+    float x[kRows][8];
     if constexpr (CT == W_F8) {
-        const uint2 u = *reinterpret_cast<const uint2*>(src + r.part * 8);
-        const float s = (r.which ? a.kv.vs : a.kv.ks)[page * a.kv.ss_page + at * a.kv.ss_cell + r.g * a.kv.ss_head];
-        const uint32_t w[4] = {u.x & 0xffffu, u.x >> 16, u.y & 0xffffu, u.y >> 16};
+        uint2 u[kRows];
+        float s[kRows];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 f = from_e4m3x2(w[j]);
-            x[2 * j] = f.x * s;
-            x[2 * j + 1] = f.y * s;
+        for (int j = 0; j < kRows; ++j) {
+            if (r[j].cell < 0) continue;
+            u[j] = *reinterpret_cast<const uint2*>(row_ptr(a.kv, r[j]) + part * 8);
+            s[j] = *scale_ptr(a.kv, r[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < kRows; ++j) {
+            if (r[j].cell < 0) continue;
+            const uint32_t w[4] = {u[j].x & 0xffffu, u[j].x >> 16, u[j].y & 0xffffu, u[j].y >> 16};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = from_e4m3x2(w[i]);
+                x[j][2 * i] = f.x * s[j];
+                x[j][2 * i + 1] = f.y * s[j];
+            }
         }
     } else {
-        load8<CT>(src, r.part * 8, x);
+#pragma unroll
+        for (int j = 0; j < kRows; ++j)
+            if (r[j].cell >= 0) load8<CT>(row_ptr(a.kv, r[j]), part * 8, x[j]);
     }
-    store8<T>(r.which ? a.v : a.k, r.i * a.s_tok + r.g * a.s_head + r.part * 8, x);
+#pragma unroll
+    for (int j = 0; j < kRows; ++j)
+        if (r[j].cell >= 0) store8<T>(r[j].v ? a.v : a.k, r[j].dense, x[j]);
 }
 
 template <int HD, int CT, int T>
 bool go(const KvRowsArgs& a, bool store, cudaStream_t st) {
-    const int64_t threads = (int64_t)a.n * a.kv.Hkv * 2 * (HD / 8);
-    const int64_t blocks = (threads + kThr - 1) / kThr;
+    constexpr int64_t per = kThr * 8 / HD * kRows;
+    const int64_t blocks = ((int64_t)a.n * a.kv.Hkv * 2 + per - 1) / per;
     if (blocks > 0x7fffffff) return false;
     if (store) kv_store_kernel<HD, CT, T><<<(unsigned)blocks, kThr, 0, st>>>(a);
     else kv_load_kernel<HD, CT, T><<<(unsigned)blocks, kThr, 0, st>>>(a);
