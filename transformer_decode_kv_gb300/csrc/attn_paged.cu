@@ -113,6 +113,8 @@ __device__ __forceinline__ void take(uint32_t* d, const uint8_t* p) {
     }
 }
 
+constexpr int kMaxSm = 160;
+
 // Where this lane's key of 32 lies (off < 0: not read) and its position.
 struct Info { int64_t off, soff; int pos; };
 
@@ -143,6 +145,8 @@ struct Cfg {
     static constexpr int END = RING > OUT ? RING : OUT;
     static constexpr int BYTES = END + W * 256 + 2 * W * ROWS * 4 + 16;
     static_assert(S >= 2, "a stage to read and one to fill");
+    // the join of a cut tile: (reference, sum) of its rows from every CTA, and a part at least
+    static_assert(END >= 8 * ROWS * kAttnRowsCtas * kMaxSm + ROWS * HD * 4, "parts of a cut tile");
 };
 
 template <int HD, int CT, int QT, int ROWS>
@@ -588,8 +592,82 @@ attn_rows_kernel(AttnPagedArgs a) {
             __syncthreads();
             if (threadIdx.x == 0) s_flag = count_unit(a, u);
             __syncthreads();
-            if (s_flag)
-                for (int r = 2 * warp; r < u.n_row; r += 2 * kWarps) merge_rows<HD, 2>(a, a.part_o, a.part_ml, u, ROWS, r);
+            if (s_flag) {
+                // The last unit of a cut tile joins the partial results, as many at a time as the stages' place
+                // holds: asynchronous copies keep them all under way. (Row by row through registers, four tokens
+                // after 8192 keys took 47 us, 32 / 8 heads of 128, f16; so they take 29 us.)
+                constexpr int NP = (ROWS * (HD / 4) + kThr - 1) / kThr;   // 4 dims of a row: a thread has so many
+                const int n_ml = u.n_chunk * u.n_row, row_n = u.n_row * (HD / 4);
+                const int fit = (C::END - 8 * n_ml) / (u.n_row * HD * 4);
+                float2* s_ml = reinterpret_cast<float2*>(sm + C::END - 8 * n_ml);
+                auto bring = [&](int i0) {
+                    const float* src = a.part_o + (int64_t)(u.part + i0) * ROWS * HD;
+                    const int n = min(fit, u.n_chunk - i0);
+                    for (int i = warp; i < n; i += kWarps) {
+                        const float* from = src + (int64_t)i * ROWS * HD + 4 * lane;
+                        const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(sm)) + 16 * (i * row_n + lane);
+#pragma unroll 4
+                        for (int y = 0; y < row_n - lane; y += 32)
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 16 * y), "l"(from + 4 * y) : "memory");
+                    }
+                    asm volatile("cp.async.commit_group;" ::: "memory");
+                };
+                bring(0);
+                const float2* ml = a.part_ml + (int64_t)u.part * ROWS;
+                const int r_ml = threadIdx.x % ROWS;
+                if (r_ml < u.n_row)
+#pragma unroll 8
+                    for (int i = threadIdx.x / ROWS; i < u.n_chunk; i += kThr / ROWS)
+                        s_ml[i * u.n_row + r_ml] = __ldcg(&ml[i * ROWS + r_ml]);
+                __syncthreads();
+                for (int r = warp; r < u.n_row; r += kWarps) {   // a part's reference becomes its factor
+                    float M = -INFINITY, L = 0.f;
+                    for (int i = lane; i < u.n_chunk; i += 32) M = fmaxf(M, s_ml[i * u.n_row + r].x);
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+                    for (int i = lane; i < u.n_chunk; i += 32) {
+                        const float2 x = s_ml[i * u.n_row + r];
+                        const float f = part_factor(x, M);
+                        s_ml[i * u.n_row + r].x = f;
+                        L += f * x.y;
+                    }
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+                    if (lane == 0) s_l[0][r] = L;
+                }
+                float v[NP][4] = {};
+                for (int i0 = 0; i0 < u.n_chunk; i0 += fit) {
+                    if (i0) bring(i0);
+                    const int n = min(fit, u.n_chunk - i0);
+                    asm volatile("cp.async.wait_group 0;" ::: "memory");
+                    __syncthreads();
+#pragma unroll
+                    for (int y = 0; y < NP; ++y) {
+                        const int x = threadIdx.x + y * kThr;
+                        if (x >= row_n) break;
+                        const float2* fr = s_ml + i0 * u.n_row + x / (HD / 4);
+#pragma unroll 4
+                        for (int i = 0; i < n; ++i) {
+                            const float f = fr[i * u.n_row].x;
+                            const float4 o = *reinterpret_cast<const float4*>(sm + 16 * (i * row_n + x));
+                            if (f != 0.f) {                  // (a part without a visible key may hold anything)
+                                v[y][0] += f * o.x; v[y][1] += f * o.y; v[y][2] += f * o.z; v[y][3] += f * o.w;
+                            }
+                        }
+                    }
+                    __syncthreads();
+                }
+#pragma unroll
+                for (int y = 0; y < NP; ++y) {
+                    const int x = threadIdx.x + y * kThr, r = x / (HD / 4);
+                    if (x >= row_n) break;
+                    const float L = s_l[0][r], inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[y][e] = L == 0.f ? 0.f : v[y][e] * inv;
+                    const int row = u.row0 + r, tok = row_token(a, u, row);
+                    store_out4(a, (int64_t)tok * a.o_tok + (int64_t)(kvh * a.G + row % a.G) * a.o_head + x % (HD / 4) * 4, v[y]);
+                }
+            }
         }
         __syncthreads();                                    // shared memory is free for the next unit
     }
@@ -598,6 +676,7 @@ attn_rows_kernel(AttnPagedArgs a) {
 template <int HD, int CT, int QT, int ROWS>
 bool go(const AttnPagedArgs& a, cudaStream_t st) {
     using C = Cfg<HD, CT, QT, ROWS>;
+    if (a.n_sm > kMaxSm) return false;
     static std::atomic<uint64_t> done{0};
     if (!allow_smem(reinterpret_cast<const void*>(attn_rows_kernel<HD, CT, QT, ROWS>), C::BYTES, done)) return false;
     cudaLaunchConfig_t cfg = {};

@@ -200,6 +200,13 @@ __device__ __noinline__ void careful_row(const AttnPagedArgs& a, const AttnUnit&
     }
 }
 
+// What a part with (reference, sum) x counts under the reference M. A part without a visible key has nothing to add
+// (its reference is -inf); NaN sums pass.
+__device__ __forceinline__ float part_factor(float2 x, float M) {
+    if (x.x == -INFINITY && x.y == 0.f) return 0.f;
+    return x.x == M ? 1.f : exp2f(x.x - M);
+}
+
 // Merge the partial results of rows r0 .. r0 + NR - 1 (those below u.n_row) of a cut tile into the output, by one warp;
 // in the units' order, so the result does not depend on which of them was last. rows: the tile form's rows. A
 // lane weighs up to one unit in 32 at a time (weight exp2(m - M) against the largest reference M), then the warp
@@ -231,11 +238,8 @@ __device__ void merge_rows(const AttnPagedArgs& a, const float* part_o, const fl
             f[k] = 0.f;
             if (c0 + lane < u.n_chunk && r0 + k < u.n_row) {
                 const float2 x = __ldcg(&ml[(int64_t)(c0 + lane) * rows + k]);
-                // a unit without a visible key has nothing to add (its reference is -inf); NaN sums pass
-                if (x.x != -INFINITY || x.y != 0.f) {
-                    f[k] = x.x == M[k] ? 1.f : exp2f(x.x - M[k]);
-                    L[k] += f[k] * x.y;
-                }
+                f[k] = part_factor(x, M[k]);
+                L[k] += f[k] * x.y;
             }
         }
         const int n = min(32, u.n_chunk - c0);
