@@ -355,8 +355,10 @@ int llm_kv_load(const llm_kv_pages *kv, int32_t type, void *k, void *v,
  * launches. A plan owns its workspace, so two runs of one plan must not overlap in time (use one
  * plan per stream, or order the streams); two graphs that may run at the same time need two plans.
  * llm_attn_run may be captured: the graph replays with whatever the plan was last set to, provided
- * it has the same form (llm_attn_plan_form), else it leaves the output alone and sets
- * bit 16 of the plan's error word. llm_attn_plan_set must not be captured (-1). */
+ * that needs no other kernels (the bits of its llm_attn_plan_form are among those of the captured form),
+ * else it leaves the output alone and sets bit 16 of the plan's error word. q and out of a captured run
+ * need the rows of every step it is replayed with. A run of an empty step (form 0) cannot be captured (-1),
+ * nor can llm_attn_plan_set (-1). */
 typedef struct llm_attn_shape {
     int32_t type;            /* of q and out: F32, F16 or BF16 */
     int32_t n_head;          /* a multiple of the cache's n_head_kv, at most 1024 */

@@ -268,6 +268,40 @@ def test_graph_replays_the_plan_as_last_set(L):
         assert plan.error() == 0
 
 
+def test_a_graph_refuses_steps_it_was_not_captured_for(L):
+    (k, _, kv_), (v, _, vv) = O.cache(64, 16, 2, 64, torch.float16, 15)
+    pages = L.KvPages(k, v)
+    plan = L.AttnPlan(pages, 8, torch.float16, 64, 4, 256)
+    q = torch.randn(40, 8, 64, device="cuda", dtype=torch.float16)
+    out = torch.zeros_like(q)
+    table = np.arange(64).reshape(1, 64)
+    st = torch.cuda.Stream()
+    plan.set([0], [30], table)
+    assert plan.form == 0
+    plan.run(q, pages, out)                                  # nothing to do
+    with torch.cuda.graph(torch.cuda.CUDAGraph(), stream=st):
+        with pytest.raises(L.LlmError, match="empty step"):
+            plan.run(q, pages, out)
+    plan.set([1], [300], table)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=st):
+        plan.run(q, pages, out)
+    with pytest.raises(ValueError, match="captured run"):
+        plan.set([41], [300], table)
+    plan.set([40], [300], table)                             # needs kernels that the graph has not
+    out.fill_(3)
+    g.replay()
+    assert plan.error() == 16 and plan.error() == 0
+    assert (out == 3).all()
+    plan.set([1], [299], table)
+    g.replay()
+    assert plan.error() == 0
+    ref, mag, smag = O.attention(q.double().cpu().numpy()[:1], kv_, vv, table, [1], [299], 16)
+    tol = O.attention_tol(ref, mag, smag, torch.float16, 299, 64, np.abs(vv).max())
+    assert (np.abs(out.double().cpu().numpy()[:1] - ref) <= tol).all()
+    assert (out[1:] == 3).all()
+
+
 def test_two_plans_on_two_streams(L):
     (k, _, kv_), (v, _, vv) = O.cache(300, 16, 1, 128, torch.float16, 6)
     pages = L.KvPages(k, v)

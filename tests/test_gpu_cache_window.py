@@ -165,6 +165,30 @@ def test_window_switched_between_steps():
     ctx.free()
 
 
+def test_sequences_interleaved_at_random():
+    w = S.WORKLOADS[KEY]
+    kw = dict(n_seq_max=3, n_ubatch=32)
+    for unified in (True, False):
+        ctx, ora = (mk(KEY, kv_unified=unified, **kw) for mk in (G.library_ctx, G.oracle_ctx))
+        for c in (ctx, ora):
+            if c is ora:
+                c.window, c.n_sink = 9, 2
+            else:
+                assert c.set_attn_window(9, 2) == 0
+        rng = np.random.default_rng(17)
+        seq = rng.permutation(np.repeat([0, 1, 2], 30))      # each sequence's tokens in order, among the others'
+        toks = rng.integers(0, w.hp.n_vocab, 90).tolist()
+        pos = [int(np.sum(seq[:i] == seq[i])) for i in range(90)]
+        seqs = [[int(x)] for x in seq]
+        ns = [1] * 90
+        flags = [1] * 90
+        assert ctx.decode(toks, pos=pos, seq_ids=seqs, logits=flags) == 0, ctx.last_error()
+        assert ora.decode(toks, pos=pos, seq_id=seqs, n_seq_id=ns, logits=flags) == 0
+        for i in range(90):
+            assert G.rel_err(ctx.get_logits_ith(i), ora.get_logits_ith(i)) <= 1e-4, (unified, i)
+        ctx.free()
+
+
 SHAPES = {64: HParams(2, 512, 8, 2, 64, 1024, 1024, 10000.0, 1e-5),
           128: HParams(2, 512, 4, 1, 128, 1024, 1024, 10000.0, 1e-5)}
 

@@ -374,6 +374,8 @@ class AttnPlan:
         self.dtype, self.n_head, self.head_dim = dtype, n_head, pages.dim
         self.device = pages.k.device
         self.n_tok = 0
+        self._captured_rows = None          # fewest rows of q and out of the runs that were captured
+        self._capturing = torch._C._cuda_isCurrentStreamCapturing if pages.k.is_cuda else (lambda: False)
         self._run = lib().llm_attn_run
         s = AttnShape(types[dtype], n_head, scale, window, n_sink, max_tok, max_seq, max_table)
         with torch.cuda.device(self.device if pages.k.is_cuda else -1):
@@ -399,6 +401,8 @@ class AttnPlan:
         t = _i32(pages)
         if n_new.ndim != 1 or n_new.shape != n_kv.shape or t.ndim != 2 or len(t) != len(n_new):
             raise ValueError("n_new [n_seq], n_kv [n_seq] and pages [n_seq, n] are needed")
+        if self._captured_rows is not None and n_new.sum() > self._captured_rows:
+            raise ValueError(f"a captured run's q or out has only {self._captured_rows} rows")
         if stream is None:
             import torch
             stream = torch.cuda.current_stream(self.device).cuda_stream
@@ -408,13 +412,17 @@ class AttnPlan:
 
     def run(self, q, pages: KvPages, out, stream: Optional[int] = None) -> None:
         """out[i] = attention of token i of the step; q and out [at least the step's tokens, n_head,
-        head_dim], rows past the tokens are not touched."""
+        head_dim], rows past the tokens are not touched. After a captured run the plan takes no step of
+        more tokens than that run's q and out have rows."""
         sq = _rows(q, "q", self.n_head, self.head_dim)
         so = _rows(out, "out", self.n_head, self.head_dim)
         if q.dtype is not self.dtype or out.dtype is not self.dtype:
             raise TypeError(f"q and out must be {self.dtype}")
         if q.shape[0] < self.n_tok or out.shape[0] < self.n_tok:
             raise ValueError(f"q or out has fewer rows than the step has tokens ({self.n_tok})")
+        if self._capturing():
+            rows = min(q.shape[0], out.shape[0])
+            self._captured_rows = rows if self._captured_rows is None else min(rows, self._captured_rows)
         r = self._run(self.ptr, q.data_ptr(), sq[0], sq[1], pages.ref, out.data_ptr(), so[0], so[1],
                       _stream_of(q, stream))
         if r != 0:

@@ -2062,7 +2062,8 @@ int32_t llm_sample_ith(llm_ctx* c, int32_t i, const llm_sampler_params* p, float
 
 int32_t llm_sample_batch(llm_ctx* c, int32_t n, const int32_t* rows, const llm_sampler_params* params, const float* u,
                          int32_t* tokens) {
-    if (!c || c->host_only || n < 0) return -1;
+    if (!c || c->host_only) return -1;
+    if (n < 0 || n > (1 << 24)) { c->err = "too many or too few rows"; return -1; }
     if (n == 0) return 0;
     if (!rows || !params || !u || !tokens) { c->err = "NULL sampler arguments"; return -1; }
     if (c->hp.n_vocab > sample_rows_max_vocab()) { c->err = "vocabulary too large for the batched sampler"; return -1; }

@@ -420,7 +420,13 @@ int llm_attn_run(llm_attn_plan* p, const void* q, int64_t q_stride_tok, int64_t 
     if (kv->type != p->kv.type || kv->n_head_kv != p->kv.n_head_kv || kv->head_dim != p->kv.head_dim ||
         kv->page_size != p->kv.page_size || kv->n_pages != p->kv.n_pages)
         return refuse("the cache is not of the plan's type and shape");
-    if (p->plan.form() == 0) return 0;
+    if (p->plan.form() == 0) {
+        // (a graph without the kernels would replay later steps as nothing, and nobody would learn of it)
+        cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+        OnDevice on(p->device);
+        if (cudaStreamIsCapturing(static_cast<cudaStream_t>(stream), &cs) != cudaSuccess) cudaGetLastError();
+        return cs == cudaStreamCaptureStatusNone ? 0 : refuse("an empty step cannot be captured");
+    }
     if (!q || !out) return refuse("NULL q or out");
     if (!aligned16(q) || !aligned16(out)) return refuse("rows must start on 16-byte boundaries");
     // checked for max_tok rows: a captured run replays with whatever the plan is set to then
