@@ -21,6 +21,10 @@
 // permutation, but touch K rows in 64-byte pieces: 5.3 TB/s at most for E4M3 rows of 128 bytes, against
 // 7.0 TB/s for whole rows.)
 //
+// Measured, 32 / 8 heads of 128: 32 single f16 tokens over 1 .. 2304 keys 39 us (156 MB, 4.0 TB/s), 16 over 9k .. 33k
+// E4M3 keys 145 us (709 MB, 4.9 TB/s of the 6.8 that the card copies at), one over 513 keys 12 us, which is
+// latency: the plan, the page table, the rows and the parts' join follow from each other.
+//
 // Precision: products of f16 (bf16) terms with float32 sums. F16 activations and caches enter as they
 // are. BF16 or F32 activations over an f16-typed product are scaled per row by a power of two (taken out of the
 // scores again), so that no value leaves f16's range; F32 ones enter as two f16 terms (22 bits). P is
@@ -38,7 +42,6 @@ namespace llm {
 namespace {
 
 using namespace pattn;
-
 
 template <bool BF>
 __device__ __forceinline__ void mma(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {

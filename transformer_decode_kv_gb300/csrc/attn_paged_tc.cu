@@ -1,6 +1,7 @@
 // Attention of new tokens over a paged cache, 256-row tiles on the fifth-generation tensor cores
 // (tcgen05, accumulators in TMEM): chunks of new tokens, where the products are the bound. F16, BF16 and
-// E4M3 caches, head_dim 64 and 128, F16 or BF16 activations.
+// E4M3 caches, head_dim 64 and 128, F16 or BF16 activations (F32 ones rounded to f16 where the caller's precision is
+// that: see attn_paged_tc_ok).
 //
 // A CTA takes a unit: up to 256 rows of (token, query head) pairs of one KV head, as two halves of 128
 // MMA rows, against a range of keys in blocks of 128. Per block and half:
@@ -27,6 +28,11 @@
 // E4M3 rows enter as f16 numbers q * s / s0 with s0 the largest scale of the unit's first block (a power
 // of two like s): exact from s0 2^-15 to s0 2^7. A row of a larger scale sends the unit to the careful path,
 // as do values that are not finite.
+//
+// Measured, 32 / 8 heads of 128: 2048 bf16 tokens at the end of 32768 keys 770 us (1.4 PFLOP/s, 0.73 of the rate of a
+// large bf16 matrix product), bound by the softmax's exponentials and packing; 512 f16 tokens at the end of
+// 8192 78 us, where cut tiles weigh; over E4M3 1350 and 123 us, bound by the conversion of the rows (some 75 cycles for
+// 512 bytes in either producer warp, and 2000 for a tile's keys to be looked up).
 //
 // Every wait is bounded by a wall-clock limit; a timeout sets ERR_TIMEOUT, ends every role's loop, and
 // the CTA leaves after its copies and with its TMEM freed.
