@@ -165,6 +165,25 @@ def test_window_switched_between_steps():
     ctx.free()
 
 
+@pytest.mark.parametrize("tkv,window", [(F8, 0), (F8, 20), (1, 20)])
+def test_a_bad_cell_rolls_back_and_resumes(tkv, window):
+    """A cell past the cache, planted on the host: the write is skipped and reported, never made."""
+    kw = dict(n_seq_max=1, type_k=tkv, type_v=tkv, n_ubatch=32)
+    toks = G.prompts(KEY)[0][:96]
+    ref, ctx = G.library_ctx(KEY, **kw), G.library_ctx(KEY, **kw)
+    for c in (ref, ctx):
+        assert c.set_attn_window(window, 2) == 0
+    assert ref.decode(toks) == 0, ref.last_error()
+    ctx.inject_fault(1, 1)
+    assert ctx.decode(toks) == -3
+    assert ctx.seq_pos_max(0) == 31 and ctx.get_logits_ith(-1) is None
+    assert ctx.decode(toks[32:]) == 0, ctx.last_error()
+    for t in (5, 6):
+        assert G.rel_err(ctx.get_logits_ith(-1), ref.get_logits_ith(-1).astype(np.float64)) <= 1e-5
+        assert ctx.decode([t]) == 0 and ref.decode([t]) == 0
+    ctx.free(); ref.free()
+
+
 def test_sequences_interleaved_at_random():
     w = S.WORKLOADS[KEY]
     kw = dict(n_seq_max=3, n_ubatch=32)
