@@ -364,20 +364,38 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
                 }
                 const int hid_all = hidden_below(a, pmin);
                 struct Key { int64_t off; int pos, cell; float s; };
-                auto lookup = [&](Key* k, int j) {          // keys 32 i + lane of block j
+                // keys 32 i + lane of block j; first every load of a kind, then what follows from them (one key after
+                // the other, each would wait for memory by itself)
+                auto lookup = [&](Key* k, int j) {
+                    const int v = u.v0 + j * kKeys + lane, ps = a.kv.page_size;
+                    const int sh = (ps & (ps - 1)) == 0 ? __ffs(ps) - 1 : -1;
+                    int page[4], at[4];
+                    bool past = false;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        k[i] = Key{-1, INT_MAX, 0, 0.f};
-                        const int v = u.v0 + j * kKeys + 32 * i + lane;
-                        if (v >= u.v1) continue;
-                        const KeyAt at = key_at(a, u, v);
-                        if (at.off >= 0 && sees(at.pos, pmax, hid_all, a.n_sink)) {
-                            k[i].off = at.off;
-                            k[i].pos = at.pos;
-                            k[i].cell = at.cell;
-                            if constexpr (F8) k[i].s = scales[at.soff];
-                        }
+                        const int w = min(v + 32 * i, u.v1 - 1);
+                        const int x = w < u.n_sink_keys ? w : w - u.n_sink_keys + u.key_lo;
+                        const int pg = sh >= 0 ? x >> sh : x / ps;
+                        at[i] = x - pg * ps;
+                        k[i].pos = x;
+                        page[i] = a.table[u.table + pg];
                     }
+                    if (a.key_pos)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) k[i].pos = a.key_pos[u.table + k[i].pos];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const bool there = v + 32 * i < u.v1, bad = (unsigned)page[i] >= (unsigned)a.kv.n_pages;
+                        const bool seen = there && !bad && sees(k[i].pos, pmax, hid_all, a.n_sink);
+                        past = past || (there && bad);
+                        k[i].cell = page[i] * ps + at[i];
+                        k[i].off = seen ? (int64_t)page[i] * a.kv.sb_page + (int64_t)at[i] * a.kv.sb_cell : -1;
+                        if (!seen) k[i].pos = INT_MAX;
+                        k[i].s = 0.f;
+                        if constexpr (F8)
+                            if (seen) k[i].s = scales[(int64_t)page[i] * a.kv.ss_page + (int64_t)at[i] * a.kv.ss_cell];
+                    }
+                    if (past && a.err) atomicOr(a.err, ERR_SLOT_RANGE);
                 };
                 if constexpr (F8) {
                     // Raw rows travel by asynchronous copies into this warp's part of the ring's last place, a tile in
