@@ -16,7 +16,7 @@
 // the same columns, and a completed S means that every product before it is complete too.
 //
 // Roles (12 warps; warps 0-3 give registers to warps 4-11, whose threads hold a row of scores each): warps
-// 0 and 1 bring K and V rows into a ring of 128-byte-swizzled tiles, with the keys' positions: a block whose keys are
+// 0 and 1 (E4M3: 3 too) bring K and V rows into a ring of 128-byte-swizzled tiles, with the keys' positions: a block whose keys are
 // all read in bulk tensor copies of the runs of neighbouring cells that pages are, others in 16-byte
 // asynchronous copies row by row, and E4M3 rows as raw bytes, converted to f16 from there;
 // warp 2 issues the MMAs; warps 4-7 and 8-11 are the two halves' softmax and epilogue (a thread owns a
@@ -31,8 +31,8 @@
 //
 // Measured, 32 / 8 heads of 128: 2048 bf16 tokens at the end of 32768 keys 770 us (1.4 PFLOP/s, 0.73 of the rate of a
 // large bf16 matrix product), bound by the softmax's exponentials and packing; 512 f16 tokens at the end of
-// 8192 78 us, where cut tiles weigh; over E4M3 1350 and 123 us, bound by the conversion of the rows (some 75 cycles for
-// 512 bytes in either producer warp, and 2000 for a tile's keys to be looked up).
+// 8192 78 us, where cut tiles weigh; over E4M3 1190 and 111 us, where the rows' conversion shares issue slots and shared
+// memory with the softmax.
 //
 // Every wait is bounded by a wall-clock limit; a timeout sets ERR_TIMEOUT, ends every role's loop, and
 // the CTA leaves after its copies and with its TMEM freed.
@@ -238,6 +238,58 @@ struct MetaAt {
     __device__ __forceinline__ void next() { if (++s == kMeta) { s = 0; ph ^= 1u; } }
 };
 
+// The least and the largest position of a unit's rows.
+__device__ __forceinline__ void unit_positions(const AttnPagedArgs& a, const AttnUnit& u, int& pmin, int& pmax) {
+    const int r1 = u.row0 + u.n_row - 1;
+    pmin = row_pos(a, u, u.row0, row_token(a, u, u.row0));
+    pmax = row_pos(a, u, r1, row_token(a, u, r1));
+    if (a.tok_pos)                                          // any order: over all of the unit's tokens
+        for (int r = u.row0; r <= r1; r += a.G) {
+            const int p = row_pos(a, u, r, row_token(a, u, r));
+            pmin = min(pmin, p);
+            pmax = max(pmax, p);
+        }
+}
+
+// A key that a producer lane brings: byte offset of its row (-1: not read), position, cell, scale.
+struct Key { int64_t off; int pos, cell; float s; };
+
+// Keys 32 i + lane of a unit's block j. First every load of a kind, then what follows from them (one key after the
+// other, each would wait for memory by itself).
+template <bool F8>
+__device__ __forceinline__ void look_up(const AttnPagedArgs& a, const AttnUnit& u, int j, int pmax, int hid_all,
+                                        const float* scales, Key* k) {
+    const int v = u.v0 + j * kKeys + (threadIdx.x & 31), ps = a.kv.page_size;
+    const int sh = (ps & (ps - 1)) == 0 ? __ffs(ps) - 1 : -1;
+    int page[4], at[4];
+    bool past = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int w = min(v + 32 * i, u.v1 - 1);
+        const int x = w < u.n_sink_keys ? w : w - u.n_sink_keys + u.key_lo;
+        const int pg = sh >= 0 ? x >> sh : x / ps;
+        at[i] = x - pg * ps;
+        k[i].pos = x;
+        page[i] = a.table[u.table + pg];
+    }
+    if (a.key_pos)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) k[i].pos = a.key_pos[u.table + k[i].pos];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const bool there = v + 32 * i < u.v1, bad = (unsigned)page[i] >= (unsigned)a.kv.n_pages;
+        const bool seen = there && !bad && sees(k[i].pos, pmax, hid_all, a.n_sink);
+        past = past || (there && bad);
+        k[i].cell = page[i] * ps + at[i];
+        k[i].off = seen ? (int64_t)page[i] * a.kv.sb_page + (int64_t)at[i] * a.kv.sb_cell : -1;
+        if (!seen) k[i].pos = INT_MAX;
+        k[i].s = 0.f;
+        if constexpr (F8)
+            if (seen) k[i].s = scales[(int64_t)page[i] * a.kv.ss_page + (int64_t)at[i] * a.kv.ss_cell];
+    }
+    if (past && a.err) atomicOr(a.err, ERR_SLOT_RANGE);
+}
+
 template <int HD, int CT, int QT>
 __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, TmaRuns runs, int beside,
                                                                const __grid_constant__ CUtensorMap map_k,
@@ -287,7 +339,7 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
     // Q rows that are changed on their way (scaled to f16's range, rounded to f16, negated for a negative scale) are
     // loaded by the softmax threads; others by warp 3, while the unit before is still in its last block and its epilogue
     constexpr bool SCALED = !BF && QT != W_F16;
-    const bool own_q = SCALED || a.scale_log2 < 0.f;
+    const bool own_q = F8 || SCALED || a.scale_log2 < 0.f;   // (E4M3: warp 3 is a producer)
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) { bar_init(&kv_full[i], 1); bar_init(&kv_empty[i], 1); }
         for (int i = 0; i < 2; ++i) { bar_init(&s_full[i], 1); bar_init(&p_full[i], 128); bar_init(&o_done[i], 1); }
@@ -324,18 +376,145 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
     // Each role walks the CTA's units by itself; the barriers above keep them in step. Registers: three warpgroups
     // of 168 a thread at launch, 504 >= kRegsLow + 2 kRegsHigh. What is spilled comes back from L2 (shared memory
     // leaves L1 little), so both parts count: 2048 new tokens at the end of 32768 E4M3 keys (32 / 8 heads of 128) took
-    // 5360 us with 120 + 192 and 3720 us with 152 + 176 while producers held raw rows in registers, 1350 us as here.
-    constexpr int kRegsLow = F8 ? 104 : 88, kRegsHigh = F8 ? 200 : 208;
+    // 5360 us with 120 + 192 and 3720 us with 152 + 176 while producers held raw rows in registers; with the raw rows in
+    // shared memory 1240 us with 104 + 200 and 1190 us as here.
+    constexpr int kRegsLow = F8 ? 120 : 88, kRegsHigh = F8 ? 192 : 208;
     static_assert(kRegsLow + 2 * kRegsHigh <= 3 * 168, "registers of the launch");
     Ring<NS> ring;
     MetaAt meta;
     if (warp < kSoft0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
-        if (warp < kProdWarps) {
+        if (F8 && warp != kMmaWarp) {
+            // ---- E4M3: three producers take the tiles K, V, K, V ... in turn (two, one for K and one for V: 1300 us
+            // instead of 1190). Raw rows travel by asynchronous
+            // copies into a producer's part of the ring's last place, a tile in eight pieces of 16 rows, the fifth
+            // piece to come brought as soon as one is converted: three or four are under way all the time, and none in
+            // registers. A lane converts the bytes that it copied. Lanes of a quarter warp hold two rows' chunks of
+            // one 64-column block, so that their stores' banks differ (eight chunks of one row, all even, would
+            // meet in pairs); the raw rows' halves are swapped in odd rows for the same reason.
+            constexpr int LR = HD / 16;                     // lanes per row, 16 values each
+            constexpr int RI = 32 / LR;                     // rows at a time
+            constexpr int BX = 16 / RI;                     // ... times in a piece
+            constexpr int PR = 3;
+            static_assert(PR * 64 * HD <= (int)M::tile, "raw rows in the ring's last place");
+            const int pr = warp == 3 ? 2 : warp;
+            const int lr = LR == 8 ? ((lane >> 2) & 1) | ((lane >> 4) << 1) : lane / LR;
+            const int lc = LR == 8 ? (lane & 3) | ((lane >> 1) & 4) : lane % LR;
+            const uint8_t* const raw = sm + M::kv + NS * M::tile + pr * 64 * HD + lr * HD +
+                                       16 * (LR == 8 ? lc ^ ((lr & 1) << 2) : lc);
+            const uint32_t raw_s = sa(raw);
+            uint32_t before = 0;                            // tiles of the units before
+            int with_keys = 0;                              // units with keys
+            bool ok = true;
+            for (int ui = ui0; ui < ui1 && ok; ++ui) {
+                const AttnUnit u = load_unit(a.units2 + ui);
+                const int n_tile = 2 * ((u.v1 - u.v0 + kKeys - 1) / kKeys);
+                if (n_tile == 0) continue;
+                const int slot = with_keys++ & 7;
+                int pmin, pmax;
+                unit_positions(a, u, pmin, pmax);
+                const int hid_all = hidden_below(a, pmin);
+                auto scales = [&](int x) { return ((x & 1) ? a.kv.vs : a.kv.ks) + (int64_t)u.head * a.kv.ss_head; };
+                Key cur[4], nxt[4];
+                auto bring = [&](int64_t row_off, int x, int q) {   // piece q of tile x, its rows' offsets in the lanes
+                    const uint8_t* base = ((x & 1) ? a.kv.v : a.kv.k) + (int64_t)u.head * a.kv.sb_head + 16 * lc;
+#pragma unroll
+                    for (int y = 0; y < BX; ++y) {
+                        const int64_t off = __shfl_sync(0xffffffffu, row_off, 16 * (q & 1) + y * RI + lr);
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(raw_s + (16 * (q & 3) + y * RI) * HD),
+                                     "l"(base + (off >= 0 ? off : 0)), "r"(off >= 0 ? 16 : 0) : "memory");
+                    }
+                };
+                float inv[2];                               // s0 of this unit: the largest scale of its first block
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    look_up<true>(a, u, 0, pmax, hid_all, scales(v), cur);
+                    float mx = fmaxf(fmaxf(cur[0].s, cur[1].s), fmaxf(cur[2].s, cur[3].s));
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                    if (!(mx > 0.f)) mx = 1.f;
+                    if (lane == 0) s0[2 * slot + v] = mx;   // (the same from each producer)
+                    inv[v] = 1.f / mx;
+                }
+                int x = (int)((pr + 2 * before) % PR);      // the first tile of this producer: (before + x) % PR = pr
+                if (x < n_tile) {
+                    look_up<true>(a, u, x >> 1, pmax, hid_all, scales(x), cur);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        bring(cur[q >> 1].off, x, q);
+                        asm volatile("cp.async.commit_group;" ::: "memory");
+                    }
+                }
+                for (; x < n_tile; x += PR) {
+                    const uint32_t it = before + x, stage = it % NS, ph = (it / NS) & 1u;
+                    uint8_t* const dst = sm + M::kv + stage * M::tile;
+                    const bool is_v = x & 1, more = x + PR < n_tile;
+                    if (more) look_up<true>(a, u, (x + PR) >> 1, pmax, hid_all, scales(x + PR), nxt);
+                    bool all = true;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        cur[i].s *= is_v ? inv[1] : inv[0];
+                        all = all && cur[i].off >= 0;
+                        if (cur[i].off >= 0 && !(cur[i].s <= 128.f)) redo_f[slot] = 1;
+                    }
+                    all = __all_sync(0xffffffffu, all);
+                    ok = it < NS || wait(&kv_empty[stage], ph ^ 1u);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+#pragma unroll 1
+                    for (int q = 0; q < 8; ++q) {
+                        asm volatile("cp.async.wait_group 3;" ::: "memory");
+                        float sq = cur[0].s;
+#pragma unroll
+                        for (int i = 1; i < 4; ++i) if (q >> 1 == i) sq = cur[i].s;
+                        uint4 in[BX];                       // (all read before the first store: the two might alias)
+                        __half2 fh[BX];
+#pragma unroll
+                        for (int y = 0; y < BX; ++y) {
+                            in[y] = *reinterpret_cast<const uint4*>(raw + (16 * (q & 3) + y * RI) * HD);
+                            fh[y] = __float2half2_rn(__shfl_sync(0xffffffffu, sq, 16 * (q & 1) + y * RI + lr));
+                        }
+#pragma unroll
+                        for (int y = 0; y < BX; ++y) {
+                            const uint32_t w[4] = {in[y].x, in[y].y, in[y].z, in[y].w};
+                            uint32_t h[8];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) e4m3x4_to_h2(w[i], h[2 * i], h[2 * i + 1]);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const __half2 z = __hmul2(*reinterpret_cast<const __half2*>(&h[i]), fh[y]);
+                                h[i] = *reinterpret_cast<const uint32_t*>(&z);
+                            }
+                            const int row = 16 * q + y * RI + lr;
+                            *reinterpret_cast<uint4*>(dst + swz(row, 2 * lc)) = make_uint4(h[0], h[1], h[2], h[3]);
+                            *reinterpret_cast<uint4*>(dst + swz(row, 2 * lc + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
+                        }
+                        if (q < 4) bring(q < 2 ? cur[2].off : cur[3].off, x, q + 4);
+                        else if (more) bring(q < 6 ? nxt[0].off : nxt[1].off, x + PR, q - 4);
+                        asm volatile("cp.async.commit_group;" ::: "memory");
+                    }
+                    const int m = (int)((it >> 1) % kMeta);
+                    if (!is_v) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) kpos[m * kKeys + 32 * i + lane] = cur[i].pos;
+                        if (lane == 0) full[m] = all;
+                    }
+                    to_async_proxy();
+                    __syncwarp();
+                    if (lane == 0) {
+                        bar_arrive(&kv_full[stage]);
+                        if (!is_v) bar_arrive(&meta_full[m]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) cur[i] = nxt[i];
+                }
+                before += n_tile;
+            }
+            if (!ok) asm volatile("cp.async.wait_group 0;" ::: "memory");
+        } else if (!F8 && warp < kProdWarps) {
             // ---- K (warp 0) and V (warp 1) tiles, the even and odd ones of the ring
             const bool is_v = warp == 1;
             uint32_t it = is_v ? 1 : 0;                     // tile number, over all units
-            int with_keys = 0;                              // units with keys
             bool ok = true;
             int bulk_at[kStages];                           // phase of a stage's last bulk copies, -1: none
 #pragma unroll
@@ -346,167 +525,10 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
                 const int kvh = u.head;
                 const int nt = (u.v1 - u.v0 + kKeys - 1) / kKeys;
                 if (nt == 0) continue;
-                const int slot = with_keys++ & 7;
                 const uint8_t* base = (is_v ? a.kv.v : a.kv.k) + (int64_t)kvh * a.kv.sb_head;
-                const float* scales = F8 ? (is_v ? a.kv.vs : a.kv.ks) + (int64_t)kvh * a.kv.ss_head : nullptr;
                 int pmin, pmax;
-                {
-                    const int r1 = u.row0 + u.n_row - 1;
-                    pmin = row_pos(a, u, u.row0, row_token(a, u, u.row0));
-                    pmax = row_pos(a, u, r1, row_token(a, u, r1));
-                    if (a.tok_pos) {                        // any order: over all of the unit's tokens
-                        for (int r = u.row0; r <= r1; r += a.G) {
-                            const int p = row_pos(a, u, r, row_token(a, u, r));
-                            pmin = min(pmin, p);
-                            pmax = max(pmax, p);
-                        }
-                    }
-                }
+                unit_positions(a, u, pmin, pmax);
                 const int hid_all = hidden_below(a, pmin);
-                struct Key { int64_t off; int pos, cell; float s; };
-                // keys 32 i + lane of block j; first every load of a kind, then what follows from them (one key after
-                // the other, each would wait for memory by itself)
-                auto lookup = [&](Key* k, int j) {
-                    const int v = u.v0 + j * kKeys + lane, ps = a.kv.page_size;
-                    const int sh = (ps & (ps - 1)) == 0 ? __ffs(ps) - 1 : -1;
-                    int page[4], at[4];
-                    bool past = false;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int w = min(v + 32 * i, u.v1 - 1);
-                        const int x = w < u.n_sink_keys ? w : w - u.n_sink_keys + u.key_lo;
-                        const int pg = sh >= 0 ? x >> sh : x / ps;
-                        at[i] = x - pg * ps;
-                        k[i].pos = x;
-                        page[i] = a.table[u.table + pg];
-                    }
-                    if (a.key_pos)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) k[i].pos = a.key_pos[u.table + k[i].pos];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const bool there = v + 32 * i < u.v1, bad = (unsigned)page[i] >= (unsigned)a.kv.n_pages;
-                        const bool seen = there && !bad && sees(k[i].pos, pmax, hid_all, a.n_sink);
-                        past = past || (there && bad);
-                        k[i].cell = page[i] * ps + at[i];
-                        k[i].off = seen ? (int64_t)page[i] * a.kv.sb_page + (int64_t)at[i] * a.kv.sb_cell : -1;
-                        if (!seen) k[i].pos = INT_MAX;
-                        k[i].s = 0.f;
-                        if constexpr (F8)
-                            if (seen) k[i].s = scales[(int64_t)page[i] * a.kv.ss_page + (int64_t)at[i] * a.kv.ss_cell];
-                    }
-                    if (past && a.err) atomicOr(a.err, ERR_SLOT_RANGE);
-                };
-                if constexpr (F8) {
-                    // Raw rows travel by asynchronous copies into this warp's part of the ring's last place, a tile in
-                    // four quarters of 32 rows, each loaded for the next tile as soon as it is converted: three or
-                    // four quarters are under way all the time, and none in registers. A lane converts the bytes
-                    // that it copied. Lanes of a quarter warp hold two rows' chunks of one 64-column block, so that
-                    // their stores' banks differ (eight chunks of one row, all even, would meet in pairs); the raw
-                    // rows' halves are swapped in odd rows for the same reason.
-                    constexpr int LR = HD / 16;             // lanes per row, 16 values each
-                    constexpr int RI = 32 / LR;             // rows at a time
-                    constexpr int BX = 4;                   // 16-byte pieces converted together
-                    const int lr = LR == 8 ? ((lane >> 2) & 1) | ((lane >> 4) << 1) : lane / LR;
-                    const int lc = LR == 8 ? (lane & 3) | ((lane >> 1) & 4) : lane % LR;
-                    const uint8_t* const raw = sm + M::kv + NS * M::tile + (is_v ? kKeys * HD : 0) + lr * HD +
-                                               16 * (LR == 8 ? lc ^ ((lr & 1) << 2) : lc);
-                    const uint32_t raw_s = sa(raw);
-                    Key cur[4], nxt[4];
-                    auto bring = [&](const Key& k, int q) { // quarter q of a tile, its keys' rows in the lanes of k
-#pragma unroll
-                        for (int x = 0; x < LR; ++x) {
-                            const int64_t off = __shfl_sync(0xffffffffu, k.off, x * RI + lr);
-                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(raw_s + (32 * q + x * RI) * HD),
-                                         "l"(base + (off >= 0 ? off : 0) + 16 * lc), "r"(off >= 0 ? 16 : 0) : "memory");
-                        }
-                    };
-                    lookup(cur, 0);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        bring(cur[q], q);
-                        asm volatile("cp.async.commit_group;" ::: "memory");
-                    }
-                    float inv;
-                    {                                       // s0 of this unit: the largest scale of its first block
-                        float mx = fmaxf(fmaxf(cur[0].s, cur[1].s), fmaxf(cur[2].s, cur[3].s));
-#pragma unroll
-                        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                        if (!(mx > 0.f)) mx = 1.f;
-                        if (lane == 0) s0[2 * slot + (is_v ? 1 : 0)] = mx;
-                        inv = 1.f / mx;
-                    }
-                    for (int j = 0; j < nt; ++j, it += 2) {
-                        const uint32_t stage = it % NS, ph = (it / NS) & 1u;
-                        uint8_t* const dst = sm + M::kv + stage * M::tile;
-                        const bool more = j + 1 < nt;
-                        if (more) lookup(nxt, j + 1);
-                        bool all = true;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            cur[i].s *= inv;
-                            all = all && cur[i].off >= 0;
-                            if (cur[i].off >= 0 && !(cur[i].s <= 128.f)) redo_f[slot] = 1;
-                        }
-                        all = __all_sync(0xffffffffu, all);
-                        ok = it < NS || wait(&kv_empty[stage], ph ^ 1u);
-                        ok = __all_sync(0xffffffffu, ok);
-                        if (!ok) break;
-#pragma unroll 1
-                        for (int q = 0; q < 4; ++q) {
-                            asm volatile("cp.async.wait_group 3;" ::: "memory");
-                            float sq = cur[0].s;
-#pragma unroll
-                            for (int i = 1; i < 4; ++i) if (q == i) sq = cur[i].s;
-#pragma unroll
-                            for (int x0 = 0; x0 < LR; x0 += BX) {
-                                uint4 in[BX];               // (all read before the first store: the two might alias)
-                                __half2 fh[BX];
-#pragma unroll
-                                for (int x = 0; x < BX; ++x) {
-                                    in[x] = *reinterpret_cast<const uint4*>(raw + (32 * q + (x0 + x) * RI) * HD);
-                                    fh[x] = __float2half2_rn(__shfl_sync(0xffffffffu, sq, (x0 + x) * RI + lr));
-                                }
-#pragma unroll
-                                for (int x = 0; x < BX; ++x) {
-                                    const uint32_t w[4] = {in[x].x, in[x].y, in[x].z, in[x].w};
-                                    uint32_t h[8];
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i) e4m3x4_to_h2(w[i], h[2 * i], h[2 * i + 1]);
-#pragma unroll
-                                    for (int i = 0; i < 8; ++i) {
-                                        const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&h[i]), fh[x]);
-                                        h[i] = *reinterpret_cast<const uint32_t*>(&y);
-                                    }
-                                    const int r = 32 * q + (x0 + x) * RI + lr;
-                                    *reinterpret_cast<uint4*>(dst + swz(r, 2 * lc)) = make_uint4(h[0], h[1], h[2], h[3]);
-                                    *reinterpret_cast<uint4*>(dst + swz(r, 2 * lc + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
-                                }
-                            }
-                            if (more) {
-                                Key kq = nxt[0];
-#pragma unroll
-                                for (int i = 1; i < 4; ++i) if (q == i) kq.off = nxt[i].off;
-                                bring(kq, q);
-                            }
-                            asm volatile("cp.async.commit_group;" ::: "memory");
-                        }
-                        if (!is_v) {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) kpos[meta.s * kKeys + 32 * i + lane] = cur[i].pos;
-                            if (lane == 0) full[meta.s] = all;
-                        }
-                        to_async_proxy();
-                        __syncwarp();
-                        if (lane == 0) {
-                            bar_arrive(&kv_full[stage]);
-                            if (!is_v) bar_arrive(&meta_full[meta.s]);
-                        }
-                        if (!is_v) meta.next();
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) cur[i] = nxt[i];
-                    }
-                } else {
                 // Blocks that need no look at single keys: positions are indices, the block's pages hold whole runs, and
                 // some row sees each key. A lane brings one box of 64 dims x runs.rows cells.
                 constexpr int HB = HD / 64;
@@ -586,7 +608,7 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
                         }
                     } else {
                         Key cur[4];
-                        lookup(cur, j);
+                        look_up<false>(a, u, j, pmax, hid_all, nullptr, cur);
                         bool all = true;
 #pragma unroll
                         for (int i = 0; i < 4; ++i) all = all && cur[i].off >= 0;
@@ -651,7 +673,6 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
                     }
                 }
                 flush();
-                }
             }
             // after a wait that gave up nobody may wait for the copies under way: they land before the CTA leaves
             if (!ok) {
@@ -728,7 +749,7 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
                 }
                 ok = __all_sync(0xffffffffu, ok);           // the warp goes on, or stops, as one
             }
-        } else if (warp == 3 && !own_q) {
+        } else if (!F8 && warp == 3 && !own_q) {
             // ---- Q tiles: a lane copies 16 bytes, CH lanes a row
             constexpr int RI = 32 / CH;                     // rows per copy
             uint32_t e_ph = 1;                              // (the first unit waits for nothing)
