@@ -192,7 +192,8 @@ __device__ __noinline__ void careful_row(const AttnPagedArgs& a, const AttnUnit&
         for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
         s *= a.scale_log2;
         const float mn = fmaxf(m, s);
-        const float f = m == mn ? 1.f : exp2f(m - mn), e = exp2f(s - mn);
+        // (a score of -inf has no weight, whatever has been seen; one of NaN passes into the sum)
+        const float f = m == mn ? 1.f : exp2f(m - mn), e = s == -INFINITY ? 0.f : exp2f(s - mn);
         l = l * f + e;
 #pragma unroll
         for (int d = 0; d < D; ++d) o[d] = o[d] * f + e * kv_value(a, vr, vs, lane * D + d);
