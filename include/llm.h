@@ -347,7 +347,7 @@ int llm_kv_load(const llm_kv_pages *kv, int32_t type, void *k, void *v,
  * p = the token's position. A sequence with n_kv cached rows and n_new new tokens has its new tokens
  * at positions n_kv - n_new .. n_kv - 1 (their rows are in the cache already, see llm_kv_store); key j
  * is the row at place j % page_size of page table[j / page_size]. A row without a visible key
- * (n_kv < n_new: negative positions) is zeros. What masked or unwritten cells hold (NaN,
+ * (n_kv < n_new: negative positions) is zeros, one whose visible scores are all -infinity NaN (0 / 0). What masked or unwritten cells hold (NaN,
  * infinities) does not reach the output.
  *
  * The plan of a step (which rows attend to which cells, split over the GPU) is made on the host once

@@ -117,3 +117,28 @@ def test_a_score_of_minus_infinity_has_no_weight(L, act, cdt, n_new, n_kv):
     assert np.isnan(ref[:, 1]).all() and np.isfinite(ref[:, [0, 2, 3]]).all()
     # the same key as a sink before a window
     check(L, act, cdt, k, v, q, n_new, n_kv, window=20, n_sink=1)
+
+
+@pytest.mark.parametrize("n_new", [1, 5, 40])
+@pytest.mark.parametrize("act,cdt", [(F16, F16), (BF16, BF16), (F32, F16)])
+def test_a_first_token_with_an_infinite_key(L, act, cdt, n_new):
+    """The first token sees one key of infinite score: 0 / 0 or inf / inf. Those after it see others too."""
+    rng, k, v = rows(11, n_new, 1, 64)
+    k[0, 0, 7] = math.inf
+    q = rng.normal(size=(n_new, 4, 64))
+    q[:, :, 7] = [-1.0, 1.0, -2.0, -0.5]
+    ref = check(L, act, cdt, k, v, q, n_new, n_new)
+    assert np.isnan(ref[0]).all() and np.isfinite(ref[1:, [0, 2, 3]]).all()
+
+
+@pytest.mark.parametrize("n_new,n_kv", [(1, 50), (3, 50), (40, 60), (40, 9000)])
+@pytest.mark.parametrize("act,cdt", [(F16, F16), (BF16, BF16), (F32, F16)])
+def test_scores_of_minus_infinity_only(L, act, cdt, n_new, n_kv):
+    """Softmax over -infinity alone is 0 / 0, however many keys there are; tokens before the first key see nothing."""
+    rng, k, v = rows(6, n_kv, 1, 64)
+    k[:, 0, 3] = math.inf                                   # (heads of one sign: no other score sends the tile elsewhere)
+    q = rng.normal(size=(n_new, 4, 64))
+    q[:, :, 3] = -1.0
+    assert np.isnan(check(L, act, cdt, k, v, q, n_new, n_kv)).all()
+    ref = check(L, act, cdt, k, v, q, n_new, max(n_new - 2, 0))
+    assert (ref[:min(2, n_new)] == 0).all()

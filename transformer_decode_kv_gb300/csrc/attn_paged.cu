@@ -579,10 +579,10 @@ attn_rows_kernel(AttnPagedArgs a) {
                 v[0] += f * o.x; v[1] += f * o.y; v[2] += f * o.z; v[3] += f * o.w;
             }
             if (u.n_chunk == 1) {
-                const float inv = L == 0.f ? 0.f : 1.f / L;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] = L == 0.f ? 0.f : v[j] * inv;
                 const int row = u.row0 + r, tok = row_token(a, u, row);
+                const float inv = 1.f / L, none = L == 0.f ? weightless(a, u, row, tok) : 0.f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] = L == 0.f ? none : v[j] * inv;
                 store_out4(a, (int64_t)tok * a.o_tok + (int64_t)(kvh * a.G + row % a.G) * a.o_head + d, v);
             } else {
                 const int64_t at = (int64_t)(u.part + u.chunk) * ROWS + r;
@@ -664,10 +664,10 @@ attn_rows_kernel(AttnPagedArgs a) {
                 for (int y = 0; y < NP; ++y) {
                     const int x = threadIdx.x + y * kThr, r = x / (HD / 4);
                     if (x >= row_n) break;
-                    const float L = s_l[0][r], inv = L == 0.f ? 0.f : 1.f / L;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[y][e] = L == 0.f ? 0.f : v[y][e] * inv;
                     const int row = u.row0 + r, tok = row_token(a, u, row);
+                    const float L = s_l[0][r], inv = 1.f / L, none = L == 0.f ? weightless(a, u, row, tok) : 0.f;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[y][e] = L == 0.f ? none : v[y][e] * inv;
                     store_out4(a, (int64_t)tok * a.o_tok + (int64_t)(kvh * a.G + row % a.G) * a.o_head + x % (HD / 4) * 4, v[y]);
                 }
             }

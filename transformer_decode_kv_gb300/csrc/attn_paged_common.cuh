@@ -86,6 +86,12 @@ __device__ __forceinline__ bool sees(int kp, int p, int hidden, int n_sink) {
     return kp <= p && (kp > hidden || kp < n_sink);
 }
 
+// What a row without any weight gives: zeros where it sees no key (its position is negative: new tokens that have no
+// cached row; any other sees itself), else 0 / 0, its scores being -inf alone.
+__device__ __forceinline__ float weightless(const AttnPagedArgs& a, const AttnUnit& u, int row, int token) {
+    return row_pos(a, u, row, token) < 0 ? 0.f : NAN;
+}
+
 __device__ __forceinline__ float load_q(const AttnPagedArgs& a, int64_t i) {
     if (a.q_type == W_F32) return static_cast<const float*>(a.q)[i];
     if (a.q_type == W_F16) return __half2float(static_cast<const __half*>(a.q)[i]);
@@ -268,11 +274,11 @@ __device__ void merge_rows(const AttnPagedArgs& a, const float* part_o, const fl
 #pragma unroll
         for (int s = 16; s > 0; s >>= 1) L[k] += __shfl_xor_sync(0xffffffffu, L[k], s);
         if (r0 + k >= u.n_row) continue;
-        const float inv = L[k] == 0.f ? 0.f : 1.f / L[k];
         const int row = u.row0 + r0 + k, tok = row_token(a, u, row);
+        const float inv = 1.f / L[k], none = L[k] == 0.f ? weightless(a, u, row, tok) : 0.f;
         const int64_t at = (int64_t)tok * a.o_tok + (int64_t)(u.head * a.G + row % a.G) * a.o_head + lane * D;
 #pragma unroll
-        for (int d = 0; d < D; ++d) o[k][d] = L[k] == 0.f ? 0.f : o[k][d] * inv;
+        for (int d = 0; d < D; ++d) o[k][d] = L[k] == 0.f ? none : o[k][d] * inv;
         if constexpr (D == 4) store_out4(a, at, o[k]);
         else
 #pragma unroll

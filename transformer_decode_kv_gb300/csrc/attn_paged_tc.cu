@@ -991,7 +991,7 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
             // ---- epilogue: a unit alone writes its rows, one of several its partial result
             if (live) {
                 bool finite = l <= 3.0e38f && m <= 3.0e38f;
-                const float inv = l == 0.f ? 0.f : 1.f / l, sv = F8 && nt > 0 ? s0[2 * slot + 1] : 1.f;
+                const float inv = 1.f / l, none = l == 0.f ? weightless(a, u, row, tok) : 0.f, sv = F8 && nt > 0 ? s0[2 * slot + 1] : 1.f;
                 const int64_t at = (int64_t)(u.part + u.chunk) * kUnitRows2 + 128 * t + r;
                 const int64_t oi = (int64_t)tok * a.o_tok + (int64_t)(kvh * a.G + row % a.G) * a.o_head;
                 if (u.n_chunk > 1 && mine) a.part_ml2[at] = make_float2(m, l);
@@ -1007,7 +1007,7 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
                     for (int i = 0; i < 32; ++i) {
                         x[i] = nt > 0 ? __uint_as_float(o[i]) * sv : 0.f;
                         finite = finite && fabsf(x[i]) <= 3.0e38f;
-                        if (u.n_chunk == 1) x[i] = l == 0.f ? 0.f : x[i] * inv;
+                        if (u.n_chunk == 1) x[i] = l == 0.f ? none : x[i] * inv;
                     }
                     if (!mine) continue;
                     if (u.n_chunk == 1) {
@@ -1030,10 +1030,10 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
                     careful_row<HD>(a, u, kvh, xrow, o, rm, rl);
                     const int64_t at = (int64_t)(u.part + u.chunk) * kUnitRows2 + x;
                     const int64_t oi = (int64_t)xtok * a.o_tok + (int64_t)(kvh * a.G + xrow % a.G) * a.o_head;
-                    const float inv = rl == 0.f ? 0.f : 1.f / rl;
+                    const float inv = 1.f / rl, none = rl == 0.f ? weightless(a, u, xrow, xtok) : 0.f;
 #pragma unroll
                     for (int d = 0; d < HD / 32; ++d) {
-                        if (u.n_chunk == 1) store_out1(a, oi + lane * (HD / 32) + d, rl == 0.f ? 0.f : o[d] * inv);
+                        if (u.n_chunk == 1) store_out1(a, oi + lane * (HD / 32) + d, rl == 0.f ? none : o[d] * inv);
                         else a.part_o2[at * HD + lane * (HD / 32) + d] = o[d];
                     }
                     if (u.n_chunk > 1 && lane == 0) a.part_ml2[at] = make_float2(rm, rl);
