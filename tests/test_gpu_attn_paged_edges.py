@@ -1,4 +1,5 @@
-"""Attention over a paged cache where a key's score is infinite. Against the formula in 64 bits, token by token: what a token does
+"""Attention over a paged cache where a key's score is infinite, or where rows of an E4M3 cache outgrow the
+first ones, so that units leave the tile kernels. Against the formula in 64 bits, token by token: what a token does
 not see has no part in its tolerance.
 
 Tolerances are those of ops_common.attention_tol with the largest |v| that the token itself sees. An E4M3 cache
@@ -142,3 +143,68 @@ def test_scores_of_minus_infinity_only(L, act, cdt, n_new, n_kv):
     assert np.isnan(check(L, act, cdt, k, v, q, n_new, n_kv)).all()
     ref = check(L, act, cdt, k, v, q, n_new, max(n_new - 2, 0))
     assert (ref[:min(2, n_new)] == 0).all()
+
+
+@pytest.mark.parametrize("act", [F16, BF16])
+@pytest.mark.parametrize("n_new,n_kv,at,Hkv", [(16, 700, 400, 1), (64, 700, 690, 1), (150, 5000, 3000, 1),
+                                               (150, 5000, 130, 1), (200, 700, 400, 8)])
+@pytest.mark.parametrize("power", [7, 8, 12, 30])
+def test_e4m3_rows_that_outgrow_the_first_block(L, act, n_new, n_kv, at, Hkv, power):
+    """256-row tiles, cut and (8 KV heads, 56 tiles) whole: rows from position `at` on are 2^power larger than the first."""
+    rng, k, v = rows(9, n_kv, Hkv, 128)
+    q = rng.normal(size=(n_new, 8 * Hkv, 128))
+    big = v.copy()
+    big[at:at + 40] *= 2.0 ** power
+    check(L, act, F8, k, big, q, n_new, n_kv, form=4)
+    big = k.copy()
+    big[at] *= 2.0 ** power
+    check(L, act, F8, big, v, q, n_new, n_kv, form=4)
+
+
+def test_units_done_again_leave_no_trace(L):
+    """One plan, captured and not, over caches with and without rows that the tiles cannot do: each run does what its
+    own cache needs."""
+    n_new, n_kv = [40, 2], [1500, 300]
+    rng, k, v = rows(12, 1808, 1, 64)
+    sets = []
+    for what in ("", "scale", "nan", ""):
+        K, V = k.copy(), v.copy()
+        if what == "scale":
+            V[600:640] *= 2.0 ** 12
+        (kc, ks, kh), (vc, vs, vh) = stored(K, F8), stored(V, F8)
+        if what == "nan":
+            vc.view(-1, 1, 64)[1499, 0, 5] = 0x7f            # the last token alone sees it
+            vh[1499, 0, 5] = np.nan
+        sets.append((kc, ks, vc, vs, kh, vh))
+    cur = [x.clone() for x in sets[0][:4]]
+    pages = L.KvPages(cur[0], cur[2], cur[1], cur[3])
+    q = torch.from_numpy(rng.normal(size=(42, 4, 64))).to(BF16).cuda()
+    out = torch.zeros_like(q)
+    table = np.full((2, 94), -1, np.int32)
+    table[0], table[1, :19] = np.arange(94), 94 + np.arange(19)
+    plan = L.AttnPlan(pages, 4, BF16, 42, 2, table.size)
+    plan.set(n_new, n_kv, table)
+    assert plan.form == 5
+    plan.run(q, pages, out)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        plan.run(q, pages, out)
+    x = q.double().cpu().numpy()
+    for kc, ks, vc, vs, kh, vh in sets * 2:
+        for d, s in zip(cur, (kc, ks, vc, vs)):
+            d.copy_(s)
+        for run in (lambda: plan.run(q, pages, out), g.replay):
+            out.fill_(5)
+            run()
+            got = out.double().cpu().numpy()
+            for t0, n, m, c0 in ((0, 40, 1500, 0), (40, 2, 300, 94 * PAGE)):
+                bad_v = np.isnan(vh[c0:c0 + m]).any()
+                with np.errstate(all="ignore"):
+                    ref, mag, smag, vmax = reference(x[t0:t0 + n], kh[c0:], np.nan_to_num(vh[c0:]), n, m, 0, 0)
+                tol = O.attention_tol(ref, mag, smag, BF16, m, 64, 2 * vmax[..., None])
+                ok = np.abs(got[t0:t0 + n] - ref) <= tol
+                if bad_v:
+                    assert np.isnan(got[n - 1, :, 5]).all()
+                    ok[n - 1, :, 5] = True
+                assert ok.all()
+    assert plan.error() == 0
