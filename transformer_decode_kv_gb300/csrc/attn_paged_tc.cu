@@ -691,11 +691,13 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
             const bool leader = elect_one();
             const uint32_t qd = desc_k(sa(sm + M::q)), kd = desc_k(sa(sm + M::kv)), vd = desc_mn(sa(sm + M::kv));
             bool ok = true;
+            // the warp goes on, or gives up, as one: it meets at warp barriers between the waits
+            auto wait_all = [&](uint64_t* b, uint32_t par) -> bool { return __all_sync(0xffffffffu, wait(b, par)); };
             for (int ui = ui0; ui < ui1 && ok; ++ui) {
                 const AttnUnit u = load_unit(a.units2 + ui);
                 const int nt = (u.v1 - u.v0 + kKeys - 1) / kKeys, halves = u.n_row > 128 ? 2 : 1;
                 if (nt == 0) continue;
-                ok = wait(q_full, q_ph);
+                ok = wait_all(q_full, q_ph);
                 q_ph ^= 1u;
                 auto scores = [&](int t, uint32_t stage) {
                     const uint32_t q = qd + t * (M::tile >> 4), k = kd + stage * (M::tile >> 4), d = tmem + 128 * t;
@@ -705,7 +707,7 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
                     }
                     __syncwarp();                           // (the others do not spin on a barrier before it has issued)
                 };
-                ok = ok && wait(&kv_full[ring.s], ring.ph);
+                ok = ok && wait_all(&kv_full[ring.s], ring.ph);
                 if (ok) {
                     tc_after();
                     for (int t = 0; t < halves; ++t) scores(t, ring.s);
@@ -719,12 +721,12 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
                     ring.next();
                     const Ring<NS> rk = ring;
                     const bool more = j + 1 < nt;
-                    if (!(ok = wait(&kv_full[rv.s], rv.ph))) break;
+                    if (!(ok = wait_all(&kv_full[rv.s], rv.ph))) break;
                     const uint32_t v = vd + rv.s * (M::tile >> 4);
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
                         if (t >= halves) break;
-                        if (!(ok = wait(&p_full[t], p_ph[t]))) break;
+                        if (!(ok = wait_all(&p_full[t], p_ph[t]))) break;
                         p_ph[t] ^= 1u;
                         tc_after();
                         if (leader) {
@@ -733,7 +735,7 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
                         }
                         __syncwarp();
                         if (more) {
-                            if (t == 0 && !(ok = wait(&kv_full[rk.s], rk.ph))) break;
+                            if (t == 0 && !(ok = wait_all(&kv_full[rk.s], rk.ph))) break;
                             tc_after();
                             scores(t, rk.s);
                         } else if (leader) {
@@ -749,7 +751,6 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
                         ring.next();
                     }
                 }
-                ok = __all_sync(0xffffffffu, ok);           // the warp goes on, or stops, as one
             }
         } else if (!F8 && warp == 3 && !own_q) {
             // ---- Q tiles: a lane copies 16 bytes, CH lanes a row
