@@ -313,6 +313,8 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
     // ring place of V tile j (five stages) or K tile j + 1 (four), freed after both halves' softmax of block j.
     uint64_t* meta_full = q_full + 1;
     uint64_t* q_empty = meta_full + kMeta;                  // 1: MMA commit after the unit's last scores
+    uint64_t* drained = q_empty + 1;                        // 1: MMA commit after a wait that gave up
+    static_assert(2 * kStages + 7 + kMeta + 2 <= 24, "places of the barriers");
     int* misc = reinterpret_cast<int*>(sm + M::misc);
     volatile int* abort_f = misc;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 2);
@@ -347,6 +349,7 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
         for (int i = 0; i < 2; ++i) { bar_init(&s_full[i], 1); bar_init(&p_full[i], 128); bar_init(&o_done[i], 1); }
         bar_init(q_full, own_q ? 256 : 1);
         bar_init(q_empty, 1);
+        bar_init(drained, 1);
         for (int i = 0; i < kMeta; ++i) bar_init(&meta_full[i], 1);
         *abort_f = 0;
         for (int i = 0; i < 8; ++i) redo_f[i] = 0;
@@ -751,6 +754,13 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
                         ring.next();
                     }
                 }
+            }
+            // after a wait that gave up, products under way end before shared memory and TMEM are given back
+            if (!ok) {
+                if (leader) commit(drained);
+                __syncwarp();
+                const uint64_t t0 = now_ns();
+                while (!bar_try(drained, 0) && now_ns() - t0 < kWaitNs) {}
             }
         } else if (!F8 && warp == 3 && !own_q) {
             // ---- Q tiles: a lane copies 16 bytes, CH lanes a row
