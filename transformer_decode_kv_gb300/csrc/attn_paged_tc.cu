@@ -325,7 +325,6 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // beside: the small tiles of the same plan run just before; nothing here depends on them, so this kernel
     // starts where they leave SMs free, and waits for them at its end
-    if (a.pdl && !beside) asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     if (form_missing(a)) return;
     if (sa(sm) & 1023u) {                                   // the swizzle patterns repeat every 1024 bytes
@@ -1181,7 +1180,7 @@ bool go(const AttnPagedArgs& a, cudaStream_t st) {
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     const int beside = (a.form & ~ATTN_FORM_TC) != 0;
-    cfg.numAttrs = a.pdl || beside ? 1 : 0;
+    cfg.numAttrs = beside ? 1 : 0;
     CUtensorMap mk{}, mv{};
     TmaRuns runs{0, false, false};
     if (CT != W_F8) runs = cell_runs(a.kv, &mk, &mv);

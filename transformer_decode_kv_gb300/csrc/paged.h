@@ -112,7 +112,6 @@ struct AttnPagedArgs {
     uint32_t* err = nullptr;
     int32_t form = 0;                            // forms the caller launches
     int32_t n_sm = 148;
-    bool pdl = false;
 };
 // Both forms' kernels as the plan's form says; false if a launch failed.
 bool launch_attn_paged(const AttnPagedArgs& a, cudaStream_t st);
