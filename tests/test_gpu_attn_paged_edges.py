@@ -1,5 +1,6 @@
-"""Attention over a paged cache where a key's score is infinite, or where rows of an E4M3 cache outgrow the
-first ones, so that units leave the tile kernels. Against the formula in 64 bits, token by token: what a token does
+"""Attention over a paged cache where a key's score is infinite, or where rows of an E4M3 cache differ so
+much that the tile kernels' 16-bit operands have to be chosen with care: zero rows, rows that only later
+tokens see, rows that outgrow the first ones, so that units leave the tile kernels. Against the formula in 64 bits, token by token: what a token does
 not see has no part in its tolerance.
 
 Tolerances are those of ops_common.attention_tol with the largest |v| that the token itself sees. An E4M3 cache
@@ -143,6 +144,41 @@ def test_scores_of_minus_infinity_only(L, act, cdt, n_new, n_kv):
     assert np.isnan(check(L, act, cdt, k, v, q, n_new, n_kv)).all()
     ref = check(L, act, cdt, k, v, q, n_new, max(n_new - 2, 0))
     assert (ref[:min(2, n_new)] == 0).all()
+
+
+@pytest.mark.parametrize("act,n_new,n_kv", [(a, n, m) for n, m in ((1, 60), (3, 400)) for a in (F16, BF16, F32)] +
+                         [(F32, 40, 300), (F32, 40, 3000)])
+def test_e4m3_rows_of_zeros_have_no_say(L, act, n_new, n_kv):
+    """A row of zeros has scale 1: beside rows of 1e-5 it must not push the others out of f16's range."""
+    rng, k, v = rows(7, n_kv, 2, 128)
+    k *= 1e-5
+    v *= 1e-5
+    for x in (k, v):
+        x[rng.random(x.shape[:2]) < 0.2] = 0
+        x[[0, 5, n_kv // 2]] = 0
+    q = rng.normal(size=(n_new, 8, 128)) * (1e4 if act == F16 else 1e5)
+    check(L, act, F8, k, v, q, n_new, n_kv)
+    k[:n_kv // 2] = 0                                       # whole blocks of zeros first
+    v[:n_kv // 2] = 0
+    check(L, act, F8, k, v, q, n_new, n_kv)
+    check(L, act, F8, 0 * k, 0 * v, q, n_new, n_kv)
+
+
+@pytest.mark.parametrize("act,n_new,n_kv", [(a, n, m) for n, m in ((3, 200), (6, 6)) for a in (F16, BF16, F32)] +
+                         [(F32, 40, 100), (F32, 40, 2900), (F32, 100, 100)])
+@pytest.mark.parametrize("power", [20, 40])
+def test_e4m3_rows_of_later_tokens_do_not_reach_earlier_ones(L, act, n_new, n_kv, power):
+    """The last tokens' V (then K) rows are 2^power larger than the others: the tokens before them do not see that."""
+    rng, k, v = rows(8, n_kv, 2, 64)
+    q = rng.normal(size=(n_new, 8, 64))
+    late = slice(n_kv - max(1, n_new // 4), n_kv)
+    big = v.copy()
+    big[late] *= 2.0 ** power
+    check(L, act, F8, k, big, q, n_new, n_kv)
+    big = k.copy()
+    big[late] *= 2.0 ** power
+    check(L, act, F8, big, v, q, n_new, n_kv)
+    check(L, act, F8, big, v, q, n_new, n_kv, window=3, n_sink=2)
 
 
 @pytest.mark.parametrize("act", [F16, BF16])

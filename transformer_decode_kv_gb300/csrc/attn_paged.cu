@@ -30,8 +30,9 @@
 // scores again), so that no value leaves f16's range; F32 ones enter as two f16 terms (22 bits). P is
 // rounded to f16 (half a step: 2^-11) where activations are f16; for F32 activations and for bf16 products
 // it enters as two terms, so its rounding (2^-8 for bf16) does not show. An E4M3 row's scale multiplies
-// the score (K) or p (V, relative to the largest scale seen so far by the warp, a power of two, so exact
-// down to f16's subnormals).
+// the score (K) or p (V, relative to E, the largest scale of the values that the query row has seen so far, a power
+// of two, so exact down to f16's subnormals). Each query row has an E of its own: a value that only later tokens see
+// does not push a row's own values out of f16's range. Rows of zeros, whose scale is 1 whatever the others are, do not count.
 #include "attn_paged_common.cuh"
 
 #include <algorithm>
@@ -337,7 +338,8 @@ attn_rows_kernel(AttnPagedArgs a) {
             m[r][0] = m[r][1] = -INFINITY;
             l[r][0] = l[r][1] = 0.f;
         }
-        float E = 0.f;                                      // O is in units of E (E4M3 values only)
+        // E4M3 values: O is in units of E, the largest scale seen by a row; invE = 1 / E
+        float E[F8 ? R : 1][2] = {}, invE[F8 ? R : 1][2] = {};
 
         int stage = 0;
         for (int n = 0; n < n_st; ++n) {
@@ -394,6 +396,7 @@ attn_rows_kernel(AttnPagedArgs a) {
             float vs[2][2];
             const int k_lo = kpos[0], k_hi = kpos[31];
             // every row sees every key (positions ascend)
+            float em[F8 ? R : 1][2];                        // largest scale of the values that a row sees here
             const bool open = read == 0xffffffffu && k_hi <= pmin && (k_lo > hid_max || k_hi < a.n_sink);
             bool raise = false;
 #pragma unroll
@@ -415,6 +418,39 @@ attn_rows_kernel(AttnPagedArgs a) {
                                 if (!sees(kp, rp[r][e], rh[r][e], a.n_sink)) S[b][r][2 * h + e] = -INFINITY;
                     }
                 }
+            if constexpr (F8) {
+                if (__any_sync(0xffffffffu, vs[0][0] == 1.f || vs[0][1] == 1.f || vs[1][0] == 1.f || vs[1][1] == 1.f)) {
+                    // rows of zeros? (key `lane` of the stage)
+                    uint32_t bits = 0u;
+#pragma unroll
+                    for (int ch = 0; ch < C::ROWB / 16; ++ch) {
+                        const uint4 x = *reinterpret_cast<const uint4*>(st + 32 * C::ROWB + at16<C::ROWB>(lane, ch));
+                        bits |= x.x | x.y | x.z | x.w;
+                    }
+                    const unsigned zero = __ballot_sync(0xffffffffu, (bits & 0x7f7f7f7fu) == 0u);
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            if (zero >> (16 * b + 8 * h + g) & 1u) vs[b][h] = 0.f;
+                }
+                const float all = fmaxf(fmaxf(vs[0][0], vs[0][1]), fmaxf(vs[1][0], vs[1][1]));
+#pragma unroll
+                for (int r = 0; r < R; ++r) em[r][0] = em[r][1] = all;
+                if (!open) {
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            em[r][e] = 0.f;
+#pragma unroll
+                            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h)
+                                    if (S[b][r][2 * h + e] != -INFINITY) em[r][e] = fmaxf(em[r][e], vs[b][h]);
+                        }
+                }
+            }
             float mx[R][2];
 #pragma unroll
             for (int r = 0; r < R; ++r)
@@ -422,22 +458,9 @@ attn_rows_kernel(AttnPagedArgs a) {
                 for (int e = 0; e < 2; ++e) {
                     mx[r][e] = fmaxf(fmaxf(S[0][r][e], S[0][r][2 + e]), fmaxf(S[1][r][e], S[1][r][2 + e]));
                     raise = raise || mx[r][e] > m[r][e] + 14.f;
+                    if constexpr (F8) raise = raise || em[r][e] > E[r][e];
                 }
-            float em = 0.f;
-            if constexpr (F8) {
-                em = fmaxf(fmaxf(vs[0][0], vs[0][1]), fmaxf(vs[1][0], vs[1][1]));
-                raise = raise || em > E;
-            }
             if (__any_sync(0xffffffffu, raise)) {
-                float fe = 1.f;
-                if constexpr (F8) {
-#pragma unroll
-                    for (int o = 4; o < 32; o <<= 1) em = fmaxf(em, __shfl_xor_sync(0xffffffffu, em, o));
-                    if (em > E) {
-                        fe = E / em;
-                        E = em;
-                    }
-                }
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
                     float f[2];
@@ -452,7 +475,16 @@ attn_rows_kernel(AttnPagedArgs a) {
                             m[r][e] = mx[r][e] - 6.f;
                             l[r][e] *= f[e];
                         }
-                        f[e] *= fe;
+                        if constexpr (F8) {
+#pragma unroll
+                            for (int o = 4; o < 32; o <<= 1)
+                                em[r][e] = fmaxf(em[r][e], __shfl_xor_sync(0xffffffffu, em[r][e], o));
+                            if (em[r][e] > E[r][e]) {
+                                f[e] *= E[r][e] / em[r][e];
+                                E[r][e] = em[r][e];
+                                invE[r][e] = 1.f / em[r][e];
+                            }
+                        }
                     }
 #pragma unroll
                     for (int t = 0; t < C::MT; ++t) {
@@ -461,7 +493,6 @@ attn_rows_kernel(AttnPagedArgs a) {
                     }
                 }
             }
-            const float inv = F8 && E > 0.f ? 1.f / E : 0.f;
             // P^T fragments: pf[b][r][h] holds keys 16 b + 8 h + 2 c, + 1 of row 8 r + g
             uint32_t pf[2][R][2], pl[2][C::SPLIT_P ? R : 1][2];
 #pragma unroll
@@ -475,7 +506,7 @@ attn_rows_kernel(AttnPagedArgs a) {
                         float p0 = ex2(S[b][r][2 * h] - m0), p1 = ex2(S[b][r][2 * h + 1] - m1);
                         l[r][0] += p0;
                         l[r][1] += p1;
-                        if constexpr (F8) { p0 *= vs[b][h] * inv; p1 *= vs[b][h] * inv; }
+                        if constexpr (F8) { p0 *= vs[b][h] * invE[r][0]; p1 *= vs[b][h] * invE[r][1]; }
                         if constexpr (C::SPLIT_P) {
                             uint32_t hi, lo;
                             split2<BF>(p0, p1, hi, lo);
@@ -541,7 +572,7 @@ attn_rows_kernel(AttnPagedArgs a) {
                 for (int t = 0; t < C::MT; ++t)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const float o = F8 ? O[r][t][2 * h + e] * E : O[r][t][2 * h + e];
+                        const float o = F8 ? O[r][t][2 * h + e] * E[F8 ? r : 0][e] : O[r][t][2 * h + e];
                         finite = finite && fabsf(o) <= 3.0e38f;
                         const int i = 2 * t + h;            // the lane's i-th dim
                         s_o[warp][row][(i / C::VP) * 8 * C::VP + C::VP * g + i % C::VP] = o;
