@@ -146,8 +146,8 @@ def test_scores_of_minus_infinity_only(L, act, cdt, n_new, n_kv):
     assert (ref[:min(2, n_new)] == 0).all()
 
 
-@pytest.mark.parametrize("act,n_new,n_kv", [(a, n, m) for n, m in ((1, 60), (3, 400)) for a in (F16, BF16, F32)] +
-                         [(F32, 40, 300), (F32, 40, 3000)])
+@pytest.mark.parametrize("act", [F16, BF16, F32])
+@pytest.mark.parametrize("n_new,n_kv", [(1, 60), (3, 400), (40, 300), (40, 3000)])
 def test_e4m3_rows_of_zeros_have_no_say(L, act, n_new, n_kv):
     """A row of zeros has scale 1: beside rows of 1e-5 it must not push the others out of f16's range."""
     rng, k, v = rows(7, n_kv, 2, 128)
@@ -164,8 +164,8 @@ def test_e4m3_rows_of_zeros_have_no_say(L, act, n_new, n_kv):
     check(L, act, F8, 0 * k, 0 * v, q, n_new, n_kv)
 
 
-@pytest.mark.parametrize("act,n_new,n_kv", [(a, n, m) for n, m in ((3, 200), (6, 6)) for a in (F16, BF16, F32)] +
-                         [(F32, 40, 100), (F32, 40, 2900), (F32, 100, 100)])
+@pytest.mark.parametrize("act", [F16, BF16, F32])
+@pytest.mark.parametrize("n_new,n_kv", [(3, 200), (6, 6), (40, 100), (40, 2900), (100, 100)])
 @pytest.mark.parametrize("power", [20, 40])
 def test_e4m3_rows_of_later_tokens_do_not_reach_earlier_ones(L, act, n_new, n_kv, power):
     """The last tokens' V (then K) rows are 2^power larger than the others: the tokens before them do not see that."""
@@ -195,6 +195,9 @@ def test_e4m3_rows_that_outgrow_the_first_block(L, act, n_new, n_kv, at, Hkv, po
     big = k.copy()
     big[at] *= 2.0 ** power
     check(L, act, F8, big, v, q, n_new, n_kv, form=4)
+    small = v.copy()
+    small[at:] *= 2.0 ** -power                             # and those that shrink
+    check(L, act, F8, k, small, q, n_new, n_kv, window=at // 4, n_sink=3, form=4)
 
 
 def test_units_done_again_leave_no_trace(L):

@@ -26,8 +26,8 @@
 // the output is rounded to bf16 itself).
 //
 // E4M3 rows enter as f16 numbers q * s / s0 with s0 the largest scale of the unit's first block (a power
-// of two like s): exact from s0 2^-15 to s0 2^7. A unit with a row of a larger scale is done key by key, in the
-// kernel that joins cut tiles, as is one with values that are not finite.
+// of two like s; rows of zeros, whose scale is 1, do not count): exact from s0 2^-15 to s0 2^7. A unit with a row out of
+// this range is done key by key, in the kernel that joins cut tiles, as is one with values that are not finite.
 //
 // Measured, 32 / 8 heads of 128: 2048 bf16 tokens at the end of 32768 keys 770 us (1.4 PFLOP/s, 0.73 of the rate of a
 // large bf16 matrix product), bound by the softmax's exponentials and packing; 512 f16 tokens at the end of
@@ -290,6 +290,21 @@ __device__ __forceinline__ void look_up(const AttnPagedArgs& a, const AttnUnit& 
     if (past && a.err) atomicOr(a.err, ERR_SLOT_RANGE);
 }
 
+// s / s0 between which q * s / s0 is exact in f16: the least E4M3 number is 2^-9, the largest 448
+constexpr float kRatioMin = 0x1p-15f, kRatioMax = 0x1p7f;
+
+// whether an E4M3 row of n bytes is zeros (rarely asked: few instructions, and no call, which would cost its caller's
+// registers)
+__device__ __forceinline__ bool row_is_zero(const uint8_t* row, int n) {
+    uint32_t bits = 0u;
+#pragma unroll 1
+    for (int i = 0; i < n; i += 16) {
+        const uint4 x = *reinterpret_cast<const uint4*>(row + i);
+        bits |= x.x | x.y | x.z | x.w;
+    }
+    return (bits & 0x7f7f7f7fu) == 0u;
+}
+
 template <int HD, int CT, int QT>
 __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, TmaRuns runs, int beside,
                                                                const __grid_constant__ CUtensorMap map_k,
@@ -419,9 +434,10 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
                 unit_positions(a, u, pmin, pmax);
                 const int hid_all = hidden_below(a, pmin);
                 auto scales = [&](int x) { return ((x & 1) ? a.kv.vs : a.kv.ks) + (int64_t)u.head * a.kv.ss_head; };
+                auto rows_of = [&](int x) { return ((x & 1) ? a.kv.v : a.kv.k) + (int64_t)u.head * a.kv.sb_head; };
                 Key cur[4], nxt[4];
                 auto bring = [&](int64_t row_off, int x, int q) {   // piece q of tile x, its rows' offsets in the lanes
-                    const uint8_t* base = ((x & 1) ? a.kv.v : a.kv.k) + (int64_t)u.head * a.kv.sb_head + 16 * lc;
+                    const uint8_t* base = rows_of(x) + 16 * lc;
 #pragma unroll
                     for (int y = 0; y < BX; ++y) {
                         const int64_t off = __shfl_sync(0xffffffffu, row_off, 16 * (q & 1) + y * RI + lr);
@@ -433,6 +449,10 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
 #pragma unroll
                 for (int v = 0; v < 2; ++v) {
                     look_up<true>(a, u, 0, pmax, hid_all, scales(v), cur);
+                    if (__any_sync(0xffffffffu, cur[0].s == 1.f || cur[1].s == 1.f || cur[2].s == 1.f || cur[3].s == 1.f))
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (cur[i].s == 1.f && row_is_zero(rows_of(v) + cur[i].off, HD)) cur[i].s = 0.f;
                     float mx = fmaxf(fmaxf(cur[0].s, cur[1].s), fmaxf(cur[2].s, cur[3].s));
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -454,14 +474,22 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
                     uint8_t* const dst = sm + M::kv + stage * M::tile;
                     const bool is_v = x & 1, more = x + PR < n_tile;
                     if (more) look_up<true>(a, u, (x + PR) >> 1, pmax, hid_all, scales(x + PR), nxt);
-                    bool all = true;
+                    bool all = true, fits = true;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         cur[i].s *= is_v ? inv[1] : inv[0];
                         all = all && cur[i].off >= 0;
-                        if (cur[i].off >= 0 && !(cur[i].s <= 128.f)) redo_f[slot] = 1;
+                        fits = fits && (cur[i].off < 0 || (cur[i].s >= kRatioMin && cur[i].s <= kRatioMax));
                     }
                     all = __all_sync(0xffffffffu, all);
+                    if (!__all_sync(0xffffffffu, fits))
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (cur[i].off >= 0 && !(cur[i].s >= kRatioMin && cur[i].s <= kRatioMax)) {
+                                // f16 would not hold it, unless it is zeros
+                                if (cur[i].s != cur[i].s || !row_is_zero(rows_of(x) + cur[i].off, HD)) redo_f[slot] = 1;
+                                cur[i].s = 0.f;
+                            }
                     ok = it < NS || wait(&kv_empty[stage], ph ^ 1u);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
