@@ -27,7 +27,7 @@
 //
 // E4M3 rows enter as f16 numbers q * s / s0 with s0 the largest scale of the unit's first block (a power
 // of two like s; rows of zeros, whose scale is 1, do not count): exact from s0 2^-15 to s0 2^7. A unit with a row out of
-// this range is done key by key, in the kernel that joins cut tiles, as is one with values that are not finite.
+// this range is done key by key, after the CTA's other units, as is one with values that are not finite.
 //
 // Measured, 32 / 8 heads of 128: 2048 bf16 tokens at the end of 32768 keys 770 us (1.4 PFLOP/s, 0.73 of the rate of a
 // large bf16 matrix product), bound by the softmax's exponentials and packing; 512 f16 tokens at the end of
@@ -344,12 +344,10 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
     if (form_missing(a)) return;
     if (sa(sm) & 1023u) {                                   // the swizzle patterns repeat every 1024 bytes
         if (tid == 0 && a.err) atomicOr(a.err, ERR_TIMEOUT);
-        if (tid == 0) a.state2[blockIdx.x] = CTA_GAVE_UP;
         return;
     }
     const int ui0 = a.first2[blockIdx.x], ui1 = a.first2[blockIdx.x + 1];
     if ((a.hdr[PH_FORM] & ATTN_FORM_TC) == 0 || ui0 >= ui1) {
-        if (tid == 0) a.state2[blockIdx.x] = 0;
         if (beside) asm volatile("griddepcontrol.wait;" ::: "memory");
         return;
     }
@@ -835,7 +833,8 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
         const int t = warp >= kSoft0 + 4 ? 1 : 0;
         const int ht = tid - 32 * (kSoft0 + 4 * t);         // thread of the half
         uint32_t s_ph = 0, o_ph = 0;
-        int with_keys = 0, state = 0;
+        int with_keys = 0, done = ui1;                      // units before `done` are written, or marked in redo2
+        bool again = false;
         AttnUnit u = load_unit(a.units2 + ui0);
         for (int ui = ui0; ui < ui1; ++ui) {
             const int kvh = u.head;
@@ -1061,17 +1060,42 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
             }
             tc_before();
             // the unit is written (all softmax warps agree on whether to go on: a wait that gave up ends every role)
-            if (any_of(1, 256, *abort_f != 0)) { state = CTA_GAVE_UP; break; }
-            // not every operand was finite (or an E4M3 row outgrew s0): the join does its rows again. Not here, where
-            // the other roles' waits would run out over a long unit.
-            if (t == 0 && ht == 0) {
-                const int redo = nt > 0 && redo_f[slot];
-                a.redo2[ui] = redo;
-                if (redo) { redo_f[slot] = 0; state = CTA_REDO; }
+            if (any_of(1, 256, *abort_f != 0)) { done = ui; break; }
+            const bool redo = nt > 0 && redo_f[slot];
+            if (t == 0 && ht == 0) a.redo2[ui] = redo;
+            if (redo) {
+                again = true;
+                asm volatile("bar.sync 1, 256;" ::: "memory");   // (all have read the slot's word)
+                if (t == 0 && ht == 0) redo_f[slot] = 0;
             }
             u = u_nxt;
         }
-        if (t == 0 && ht == 0) a.state2[blockIdx.x] = state;
+        // Units with operands that were not finite (or an E4M3 row that f16 did not hold), key by key. That may take long, so it
+        // comes last: no other role waits for it with a limit. Rows that a wait that gave up has cost are NaN, here or
+        // in the join, and the error word tells.
+        if (again || done < ui1) {
+            asm volatile("bar.sync 1, 256;" ::: "memory");   // the marks are written
+            for (int ui = ui0; ui < ui1; ++ui) {
+                if (ui < done && __ldcg(&a.redo2[ui]) == 0) continue;
+                const AttnUnit v = load_unit(a.units2 + ui);
+                for (int x = warp - kSoft0; x < v.n_row; x += 8) {
+                    float o[HD / 32], rm = -INFINITY, rl = NAN;
+#pragma unroll
+                    for (int d = 0; d < HD / 32; ++d) o[d] = NAN;
+                    const int row = v.row0 + x, tok = row_token(a, v, row);
+                    if (ui < done) careful_row<HD>(a, v, v.head, row, o, rm, rl);
+                    const int64_t at = (int64_t)(v.part + v.chunk) * kUnitRows2 + x;
+                    const int64_t oi = (int64_t)tok * a.o_tok + (int64_t)(v.head * a.G + row % a.G) * a.o_head;
+                    const float inv = 1.f / rl, none = rl == 0.f ? weightless(a, v, row, tok) : 0.f;
+#pragma unroll
+                    for (int d = 0; d < HD / 32; ++d) {
+                        if (v.n_chunk == 1) store_out1(a, oi + lane * (HD / 32) + d, rl == 0.f ? none : o[d] * inv);
+                        else a.part_o2[at * HD + lane * (HD / 32) + d] = o[d];
+                    }
+                    if (v.n_chunk > 1 && lane == 0) a.part_ml2[at] = make_float2(rm, rl);
+                }
+            }
+        }
     }
     if (beside) asm volatile("griddepcontrol.wait;" ::: "memory");
     __syncthreads();
@@ -1081,75 +1105,18 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
 // The rows of the cut tiles from their units' partial results, four rows a warp. A kernel of its own: the last unit of a
 // tile to finish would do 256 rows alone while the other SMs are idle (512 tokens over 8192 keys: 170 us so, against
 // 114 us in all with this kernel).
-//
-// Units that the tiles could not do (operands that are not finite, an E4M3 row that outgrew s0) are done here key by
-// key, a warp per row and every SM's warps over the rows: a part of a cut tile by the warp that joins its row, rows of whole
-// tiles before. No wait depends on how long that takes. After a CTA that gave up, parts are missing: nothing is joined.
 constexpr int kMergeThr = 256;
-constexpr int kMergeCtas = 4;                               // per SM
-constexpr int kMergeRows = 4;                               // per warp
-static_assert(kMergeCtas * (kMergeThr / 32) * kMergeRows <= kUnitRows2, "each warp's first cut is within the list, an entry per SM");
-
-// The rows that have to be done again. Whole tiles' are dealt out to n_w warps (this one: w); of the n_cut rows of cut
-// tiles, kMergeRows at a time, this warp does those that it joins afterwards. (Out of the kernel's way: within it this
-// cost every call registers.)
-template <int HD>
-__device__ __noinline__ void redo_units(const AttnPagedArgs& a, int w, int n_w, int n_cut) {
-    constexpr int D = HD / 32;
-    const int lane = threadIdx.x & 31;
-    float o[D], m, l;
-    int at = 0;                                             // rows of whole tiles so far
-    for (int c = 0; c < a.n_sm; ++c) {
-        if (__ldcg(&a.state2[c]) == 0) continue;
-        for (int ui = a.first2[c]; ui < a.first2[c + 1]; ++ui) {
-            if (__ldcg(&a.redo2[ui]) == 0) continue;
-            const AttnUnit u = load_unit(a.units2 + ui);
-            if (u.n_chunk > 1) continue;
-            for (int r = (w + n_w - at) % n_w; r < u.n_row; r += n_w) {
-                const int row = u.row0 + r, tok = row_token(a, u, row);
-                careful_row<HD>(a, u, u.head, row, o, m, l);
-                const float inv = 1.f / l, none = l == 0.f ? weightless(a, u, row, tok) : 0.f;
-                const int64_t oi = (int64_t)tok * a.o_tok + (int64_t)(u.head * a.G + row % a.G) * a.o_head + lane * D;
-#pragma unroll
-                for (int d = 0; d < D; ++d) store_out1(a, oi + d, l == 0.f ? none : o[d] * inv);
-            }
-            at = (at + u.n_row) % n_w;
-        }
-    }
-    for (int x = w; x < n_cut; x += n_w) {
-        const int u0 = a.cuts2[x / (kUnitRows2 / kMergeRows)], r = x % (kUnitRows2 / kMergeRows) * kMergeRows;
-        const int n_chunk = a.units2[u0].n_chunk;
-        for (int c = 0; c < n_chunk; ++c) {
-            if (__ldcg(&a.redo2[u0 + c]) == 0) continue;
-            const AttnUnit u = load_unit(a.units2 + u0 + c);
-            for (int k = r; k < min(r + kMergeRows, u.n_row); ++k) {
-                careful_row<HD>(a, u, u.head, u.row0 + k, o, m, l);
-                const int64_t to = (int64_t)(u.part + c) * kUnitRows2 + k;
-#pragma unroll
-                for (int d = 0; d < D; ++d) a.part_o2[to * HD + lane * D + d] = o[d];
-                if (lane == 0) a.part_ml2[to] = make_float2(m, l);
-            }
-        }
-    }
-    __syncwarp();                                           // (the warp's lanes read one another's)
-}
 
 template <int HD>
-__global__ void __launch_bounds__(kMergeThr, kMergeCtas) attn_tc_merge_kernel(const __grid_constant__ AttnPagedArgs a) {
+__global__ void __launch_bounds__(kMergeThr) attn_tc_merge_kernel(AttnPagedArgs a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int w = blockIdx.x * (kMergeThr / 32) + (threadIdx.x >> 5), n_w = gridDim.x * (kMergeThr / 32);
-    // (these loads are under way together)
-    const int form = a.hdr[PH_FORM], n = a.hdr[PH_CUTS2] * (kUnitRows2 / kMergeRows), cut0 = a.cuts2[w / (kUnitRows2 / kMergeRows)];
-    const uint2 states = __ldcg(reinterpret_cast<const uint2*>(a.state2) + (threadIdx.x & 31));   // eight CTAs each
-    if ((form & ~a.form) != 0 || (form & ATTN_FORM_TC) == 0) return;
-    const uint32_t state = __reduce_or_sync(0xffffffffu, states.x | states.y);
-    if (state & CTA_GAVE_UP * 0x01010101u) return;
-    if (state) redo_units<HD>(a, w, n_w, n);
-    for (int x = w; x < n; x += n_w) {
-        const int u0 = x == w ? cut0 : a.cuts2[x / (kUnitRows2 / kMergeRows)];
-        const AttnUnit u = load_unit(a.units2 + u0);
-        const int r = x % (kUnitRows2 / kMergeRows) * kMergeRows;
-        if (r < u.n_row) merge_rows<HD, kMergeRows>(a, a.part_o2, a.part_ml2, u, kUnitRows2, r);
+    if ((a.hdr[PH_FORM] & ~a.form) != 0 || (a.hdr[PH_FORM] & ATTN_FORM_TC) == 0) return;
+    constexpr int NR = 4;                                   // rows per warp
+    const int n = a.hdr[PH_CUTS2] * (kUnitRows2 / NR);
+    for (int x = blockIdx.x * (kMergeThr / 32) + (threadIdx.x >> 5); x < n; x += gridDim.x * (kMergeThr / 32)) {
+        const AttnUnit u = load_unit(a.units2 + a.cuts2[x / (kUnitRows2 / NR)]);
+        const int r = x % (kUnitRows2 / NR) * NR;
+        if (r < u.n_row) merge_rows<HD, NR>(a, a.part_o2, a.part_ml2, u, kUnitRows2, r);
     }
 }
 
@@ -1195,7 +1162,6 @@ TmaRuns cell_runs(const PagedKv& kv, CUtensorMap* mk, CUtensorMap* mv) {
 
 template <int HD, int CT, int QT>
 bool go(const AttnPagedArgs& a, cudaStream_t st) {
-    if (a.n_sm > kMaxCtas2) return false;
     static std::atomic<uint64_t> done{0};
     if (!allow_smem(reinterpret_cast<const void*>(attn_tc_rows_kernel<HD, CT, QT>), Smem<HD>::bytes, done)) return false;
     cudaLaunchConfig_t cfg = {};
@@ -1214,7 +1180,7 @@ bool go(const AttnPagedArgs& a, cudaStream_t st) {
     if (CT != W_F8) runs = cell_runs(a.kv, &mk, &mv);
     if (cudaLaunchKernelEx(&cfg, attn_tc_rows_kernel<HD, CT, QT>, a, runs, beside, mk, mv) != cudaSuccess) return false;
     // (launched early, it waits for the kernel above)
-    cfg.gridDim = dim3(kMergeCtas * a.n_sm);
+    cfg.gridDim = dim3(4 * a.n_sm);
     cfg.blockDim = dim3(kMergeThr);
     cfg.dynamicSmemBytes = 0;
     cfg.numAttrs = 1;

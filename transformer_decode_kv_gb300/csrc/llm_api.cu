@@ -133,8 +133,7 @@ struct llm_ctx {
     size_t pg_first[2] = {0, 0}, pg_cuts = 0, pg_units[2] = {0, 0}, pg_bytes = 0;
     float* pg_part_o = nullptr;
     float2* pg_part_ml = nullptr;
-    int32_t* pg_tickets = nullptr;
-    uint8_t* pg_state = nullptr;
+    int32_t *pg_tickets = nullptr, *pg_redo = nullptr;
 
     // scratch for one ubatch
     float *x = nullptr, *h = nullptr, *qkv = nullptr, *attn = nullptr, *u = nullptr, *tmp = nullptr;
@@ -523,12 +522,11 @@ bool paged_setup(llm_ctx* c) {
     uint8_t* host = nullptr;
     if (!cuda_ok(c, cudaMallocHost(&host, at), "cudaMallocHost")) return false;
     const bool ok = dalloc(c, &c->pg_part_o, rows * c->hp.head_dim) && dalloc(c, &c->pg_part_ml, rows) &&
-                    dalloc(c, &c->pg_tickets, (size_t)k.tickets) && dalloc(c, &c->pg_state, (size_t)plan_state_bytes(k)) &&
+                    dalloc(c, &c->pg_tickets, (size_t)k.tickets) && dalloc(c, &c->pg_redo, (size_t)k.units2) &&
                     cuda_ok(c, cudaMemsetAsync(c->pg_tickets, 0, sizeof(int32_t) * k.tickets, c->st), "memset") &&
-                    cuda_ok(c, cudaMemsetAsync(c->pg_state, 0, (size_t)plan_state_bytes(k), c->st), "memset") &&
                     dalloc(c, &c->pg_dev, at);
     if (!ok) {
-        dfree(c, c->pg_part_o); dfree(c, c->pg_part_ml); dfree(c, c->pg_tickets); dfree(c, c->pg_state);
+        dfree(c, c->pg_part_o); dfree(c, c->pg_part_ml); dfree(c, c->pg_tickets); dfree(c, c->pg_redo);
         cudaFreeHost(host);
         c->pg_dev = nullptr;
         return false;
@@ -629,8 +627,7 @@ bool paged_attention(llm_ctx* c, const AttnArgs& a, void* kc, void* vc) {
     g.part_ml = c->pg_part_ml;
     g.part_o2 = c->pg_part_o + plan_part_rows(c->pg_caps, false) * a.hd;
     g.part_ml2 = c->pg_part_ml + plan_part_rows(c->pg_caps, false);
-    g.state2 = c->pg_state;
-    g.redo2 = reinterpret_cast<int32_t*>(c->pg_state + kMaxCtas2);
+    g.redo2 = c->pg_redo;
     g.tickets = c->pg_tickets;
     g.err = c->d_err;
     g.form = c->pg_plan.form();

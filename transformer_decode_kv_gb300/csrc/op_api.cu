@@ -251,8 +251,7 @@ struct llm_attn_plan {
     uint8_t *d_buf = nullptr, *h_buf = nullptr;
     float* part_o = nullptr;
     float2* part_ml = nullptr;
-    int32_t* tickets = nullptr;
-    uint8_t* state = nullptr;
+    int32_t *tickets = nullptr, *redo = nullptr;
     uint32_t* err = nullptr;
     cudaEvent_t uploaded = nullptr;
     bool pending = false;
@@ -312,7 +311,7 @@ llm_attn_plan* llm_attn_plan_init(const llm_attn_shape* s, const llm_kv_pages* k
     get(&p->part_o, (size_t)rows * kv->head_dim * sizeof(float));
     get(&p->part_ml, (size_t)rows * sizeof(float2));
     get(&p->tickets, (size_t)p->caps.tickets * sizeof(int32_t));
-    get(&p->state, (size_t)plan_state_bytes(p->caps));
+    get(&p->redo, (size_t)std::max<int64_t>(1, p->caps.units2) * sizeof(int32_t));
     get(&p->err, sizeof(uint32_t));
     if (e == cudaSuccess) {
         void* h = nullptr;
@@ -320,7 +319,6 @@ llm_attn_plan* llm_attn_plan_init(const llm_attn_shape* s, const llm_kv_pages* k
         p->h_buf = static_cast<uint8_t*>(h);
     }
     if (e == cudaSuccess) e = cudaMemset(p->tickets, 0, (size_t)p->caps.tickets * sizeof(int32_t));
-    if (e == cudaSuccess) e = cudaMemset(p->state, 0, (size_t)plan_state_bytes(p->caps));
     if (e == cudaSuccess) e = cudaMemset(p->err, 0, sizeof(uint32_t));
     if (e == cudaSuccess) e = cudaMemset(p->d_buf, 0, p->off_units[0]);
     if (e == cudaSuccess) e = cudaEventCreateWithFlags(&p->uploaded, cudaEventDisableTiming);
@@ -341,7 +339,7 @@ void llm_attn_plan_free(llm_attn_plan* p) {
         cudaFree(p->part_o);
         cudaFree(p->part_ml);
         cudaFree(p->tickets);
-        cudaFree(p->state);
+        cudaFree(p->redo);
         cudaFree(p->err);
         if (p->h_buf) cudaFreeHost(p->h_buf);
         cudaGetLastError();
@@ -468,8 +466,7 @@ int llm_attn_run(llm_attn_plan* p, const void* q, int64_t q_stride_tok, int64_t 
     a.part_o = p->part_o; a.part_ml = p->part_ml;
     a.part_o2 = p->part_o + plan_part_rows(p->caps, false) * kv->head_dim;
     a.part_ml2 = p->part_ml + plan_part_rows(p->caps, false);
-    a.state2 = p->state; a.redo2 = reinterpret_cast<int32_t*>(p->state + kMaxCtas2);
-    a.tickets = p->tickets; a.err = p->err;
+    a.tickets = p->tickets; a.redo2 = p->redo; a.err = p->err;
     a.form = p->plan.form();
     a.n_sm = p->ps.n_sm;
     if (!launch_attn_paged(a, static_cast<cudaStream_t>(stream))) return failed("attention launch", cudaGetLastError());

@@ -74,10 +74,6 @@ constexpr int attn_rows_warps(int hd, int kv_type, int rows) {
 }
 enum AttnOut : int32_t { AO_F16 = 0, AO_BF16 = 1, AO_F32 = 2, AO_BF16_PAIR = 3 };
 
-// What a CTA of the 256-row form leaves to the kernel after it (bits).
-enum : uint8_t { CTA_REDO = 1, CTA_GAVE_UP = 2 };
-constexpr int kMaxCtas2 = 256;                   // of the 256-row form: a warp reads what they left at once
-
 // Header words of a plan's device buffer.
 enum : int32_t { PH_FORM = 0, PH_CUTS2 = 1, PH_WORDS = 8 };
 
@@ -106,7 +102,6 @@ struct AttnPagedArgs {
     float2* part_ml = nullptr;                   // [part][rows] (running max, sum)
     float* part_o2 = nullptr;                    // the same of the 256-row tiles
     float2* part_ml2 = nullptr;
-    uint8_t* state2 = nullptr;                   // [kMaxCtas2] CTA_REDO, CTA_GAVE_UP; zero where there is no CTA
     int32_t* redo2 = nullptr;                    // per 256-row unit: its rows have to be done key by key
     int32_t* tickets = nullptr;                  // zero between launches
     uint32_t* err = nullptr;
@@ -150,8 +145,6 @@ void build_paged_plan(const PlanShape& s, const std::vector<PlanSeq>& seqs, Page
 // Upper bounds for buffers over every plan of at most max_tok tokens in max_seq sequences.
 struct PagedPlanCaps { int64_t units1, units2, ctas1, ctas2, tickets, parts1, parts2; };
 PagedPlanCaps paged_plan_caps(const PlanShape& s, int32_t max_tok, int32_t max_seq);
-// Bytes for state2 and redo2, in this order (zero at first).
-inline int64_t plan_state_bytes(const PagedPlanCaps& c) { return kMaxCtas2 + c.units2 * (int64_t)sizeof(int32_t); }
 // Partial results of both forms: rows of head_dim values, the small tiles' first.
 inline int64_t plan_part_rows(const PagedPlanCaps& c, bool both) { return c.parts1 * 16 + (both ? c.parts2 * kUnitRows2 : 0); }
 
