@@ -364,7 +364,7 @@ typedef struct llm_attn_shape {
     int32_t n_head;          /* a multiple of the cache's n_head_kv, at most 1024 */
     float   scale;           /* 0 = 1 / sqrt(head_dim) */
     int32_t window, n_sink;  /* 0 = no window (n_sink then has no effect) */
-    int32_t max_tok;         /* most new tokens of a step, all sequences together */
+    int32_t max_tok;         /* most new tokens of a step, all sequences together; times n_head below 2^31 */
     int32_t max_seq;         /* most sequences of a step */
     int32_t max_table;       /* most page-table entries of a step, all sequences together */
 } llm_attn_shape;

@@ -208,3 +208,17 @@ def test_steps_past_the_shape_are_refused(B, n_new, n_kv):
     p = lambda x: x.ctypes.data_as(C.POINTER(C.c_int32))
     assert B.lib().llm_debug_attn_units(C.byref(shape), C.byref(kv), 152, 0, len(a), p(a), p(b), None, 0,
                                         None, None, None) == -1
+
+
+def test_rows_past_32_bits_are_refused(B):
+    """Rows (token, query head) are numbered in 32 bits: 2^24 tokens of 128 heads or more are too many."""
+    L = B.lib()
+    n = np.asarray([1], np.int32).ctypes.data_as(C.POINTER(C.c_int32))
+    for heads, tok, ok in ((128, 1 << 24, False), (127, 1 << 24, True), (1024, 1 << 21, False), (1024, (1 << 21) - 1, True)):
+        kv = desc(B, n_head_kv=1)
+        s = B.AttnShape(**{**GOOD_SHAPE, "n_head": heads, "max_tok": tok})
+        r = L.llm_debug_attn_units(C.byref(s), C.byref(kv), 152, 0, 1, n, n, None, 0, None, None, None)
+        assert (r > 0) == ok
+        if not ok:
+            assert r == -1 and b"2^31" in L.llm_op_last_error()
+            assert not L.llm_attn_plan_init(C.byref(s), C.byref(kv))

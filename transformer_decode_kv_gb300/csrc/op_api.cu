@@ -156,6 +156,8 @@ const char* attn_shape_fault(const llm_attn_shape* s, const llm_kv_pages* kv) {
     if (s->max_tok < 1 || s->max_seq < 1 || s->max_table < 1 || s->max_tok > (1 << 24) || s->max_seq > (1 << 20) ||
         s->max_table > (1 << 28))
         return "max_tok, max_seq or max_table out of range";
+    // rows (token, query head) and the units made of them are counted in 32 bits
+    if ((int64_t)s->max_tok * s->n_head > INT32_MAX) return "max_tok times n_head must be below 2^31";
     return nullptr;
 }
 
