@@ -378,8 +378,8 @@ llm_attn_plan *llm_attn_plan_init(const llm_attn_shape *shape, const llm_kv_page
 void llm_attn_plan_free(llm_attn_plan *plan);
 /* n_new, n_kv [n_seq] and pages [n_seq][ld_pages] are host arrays; sequence s uses the first
  * ceil(n_kv[s] / page_size) entries of its row. The rows of q and out are the sequences' new tokens
- * one after the other. -1: a count out of range (n_new < 0, n_kv < 0, sums above the shape's
- * maxima, a row shorter than n_kv needs), a page outside the cache, or a stream being captured; the
+ * one after the other. -1: a count out of range (n_new < 0, n_kv < 0 or above 2^31 - 513, sums above
+ * the shape's maxima, a row shorter than n_kv needs), a page outside the cache, or a stream being captured; the
  * plan then keeps what it held. */
 int llm_attn_plan_set(llm_attn_plan *plan, int32_t n_seq, const int32_t *n_new, const int32_t *n_kv,
                       const int32_t *pages, int32_t ld_pages, void *stream);

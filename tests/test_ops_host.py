@@ -222,3 +222,12 @@ def test_rows_past_32_bits_are_refused(B):
         if not ok:
             assert r == -1 and b"2^31" in L.llm_op_last_error()
             assert not L.llm_attn_plan_init(C.byref(s), C.byref(kv))
+
+
+def test_sequences_of_almost_2_to_31_keys_are_refused(B):
+    """Key numbers run a few blocks past the end of a sequence: they must not wrap."""
+    shape, kv = B.AttnShape(**GOOD_SHAPE), desc(B, n_pages=2, page_size=1 << 29)
+    p = lambda x: np.asarray([x], np.int32).ctypes.data_as(C.POINTER(C.c_int32))
+    for n, ok in ((2 ** 31 - 513, True), (2 ** 31 - 512, False), (2 ** 31 - 128, False), (2 ** 31 - 2, False)):
+        r = B.lib().llm_debug_attn_units(C.byref(shape), C.byref(kv), 152, 1, 1, p(64), p(n), None, 0, None, None, None)
+        assert (r > 0) == ok

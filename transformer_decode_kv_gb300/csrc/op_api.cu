@@ -175,6 +175,7 @@ PlanShape plan_shape(const llm_attn_shape* s, const llm_kv_pages* kv, int32_t n_
     return p;
 }
 
+constexpr int32_t kMaxKeys = INT32_MAX - 512;    // of a sequence
 int64_t pages_of(const llm_kv_pages& kv, int32_t n_kv) { return ((int64_t)n_kv + kv.page_size - 1) / kv.page_size; }
 
 // Why a step's lengths do not fit the shape (null: they do).
@@ -184,7 +185,8 @@ const char* step_fault(const llm_attn_shape* s, const llm_kv_pages& kv, int32_t 
     if (n_seq > 0 && (!n_new || !n_kv)) return "NULL lengths";
     int64_t tok = 0, tab = 0;
     for (int32_t i = 0; i < n_seq; ++i) {
-        if (n_new[i] < 0 || n_kv[i] < 0 || n_kv[i] == INT32_MAX) return "a length out of range";
+        // (the kernels number keys in 32 bits, up to a few blocks past the last one)
+        if (n_new[i] < 0 || n_kv[i] < 0 || n_kv[i] > kMaxKeys) return "a length out of range";
         tok += n_new[i];
         tab += pages_of(kv, n_kv[i]);
     }
