@@ -121,3 +121,17 @@ def test_oracle_window_and_f8_cache_equal_the_no_cache_forward():
     assert c.decode(toks, logits=[1] * 12) == 0
     one = forward_no_cache(w, MICRO, toks[:1])               # (attention of one key is its value row, at any position)
     assert np.max(np.abs(c.logits[0] - one[0])) <= 1e-9 * np.max(np.abs(one))
+
+
+def test_a_mask_is_that_of_the_decode_it_belongs_to(T):
+    """The window set after a decode does not change what that decode's tokens saw."""
+    c = T.Context(HP, n_ctx=256, host_only=True)
+    c.debug_capture(True)
+    assert c.set_attn_window(3, 1) == 0
+    assert c.decode([1] * 8) == 0
+    j = np.arange(8)
+    want = (j[None] <= j[:, None]) & ((j[None] > j[:, None] - 3) | (j[None] < 1))
+    for window, n_sink in ((3, 1), (0, 0), (5, 2)):
+        assert c.set_attn_window(window, n_sink) == 0
+        assert np.array_equal(c.ubatch_mask(0)[:, :8], want)
+    c.free()

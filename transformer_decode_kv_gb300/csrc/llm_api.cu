@@ -93,11 +93,16 @@ struct InLayout {
 
 // Record of one ubatch for the debug hooks.
 struct UbDebug {
-    int32_t n_kv = 0;
+    int32_t n_kv = 0, window = 0, n_sink = 0;
     std::vector<int32_t> pos, tok_list, list_off, list_cells, list_pos;
 };
 
 }  // namespace
+
+// whether token position p sees a cell at position kp (causal, window, sinks)
+static bool in_sight(int32_t p, int32_t kp, int32_t window, int32_t n_sink) {
+    return kp <= p && (window == 0 || (int64_t)kp > (int64_t)p - window || kp < n_sink);
+}
 
 struct llm_ctx {
     llm_hparams hp{};
@@ -237,10 +242,7 @@ struct llm_ctx {
     double kv_value_bytes() const {
         return kv_f8() ? 1.0 + 4.0 / hp.head_dim : kv_q8() ? 34.0 / 32.0 : (double)type_size(type_k);
     }
-    // whether token position p sees a cell at position kp (causal, window, sinks)
-    bool sees(int32_t p, int32_t kp) const {
-        return kp <= p && (window == 0 || (int64_t)kp > (int64_t)p - window || kp < n_sink);
-    }
+    bool sees(int32_t p, int32_t kp) const { return in_sight(p, kp, window, n_sink); }
 };
 
 namespace {
@@ -1529,6 +1531,8 @@ int32_t llm_decode(llm_ctx* c, llm_batch bt) {
         if (c->debug) {
             UbDebug u;
             u.n_kv = c->cells.n_kv();
+            u.window = c->window;
+            u.n_sink = c->n_sink;
             u.pos.assign(b.pos.begin() + i0, b.pos.begin() + i0 + T);
             u.tok_list = c->plan.tok_list;
             u.list_off = c->plan.list_off;
@@ -1790,7 +1794,7 @@ int64_t llm_debug_ubatch_mask(llm_ctx* c, int32_t ub, uint8_t* out, int64_t cap,
     for (int64_t t = 0; t < T; ++t) {
         const int32_t l = u.tok_list[t];
         for (int32_t k = u.list_off[l]; k < u.list_off[l + 1]; ++k)
-            if (c->sees(u.pos[t], u.list_pos[k]) && u.list_cells[k] < nkv) m[t * nkv + u.list_cells[k]] = 1;
+            if (in_sight(u.pos[t], u.list_pos[k], u.window, u.n_sink) && u.list_cells[k] < nkv) m[t * nkv + u.list_cells[k]] = 1;
     }
     std::memcpy(out, m.data(), (size_t)std::min(n, cap));
     return n;
