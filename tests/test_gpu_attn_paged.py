@@ -393,3 +393,29 @@ def test_a_serving_step(L):
         assert (np.abs(out.double().cpu().numpy() - ref) <= tol).all()
         assert token.tolist() == logits.argmax(1).tolist()
     assert plan.error() == 0
+
+
+def test_a_run_captured_on_a_stream_of_its_own(L):
+    """The stream is named in the call and is not torch's current one: the captured run's rows bound later steps all
+    the same."""
+    (k, _, _), (v, _, _) = O.cache(64, 16, 2, 64, torch.float16, 16)
+    pages = L.KvPages(k, v)
+    plan = L.AttnPlan(pages, 8, torch.float16, 64, 4, 256)
+    q = torch.randn(9, 8, 64, device="cuda", dtype=torch.float16)
+    out, want = torch.zeros_like(q), torch.zeros_like(q)
+    table = np.arange(64).reshape(1, 64)
+    plan.set([1], [300], table)
+    plan.run(q, pages, want, stream=0)
+    st, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        g.capture_begin()
+    plan.run(q, pages, out, stream=st.cuda_stream)
+    with torch.cuda.stream(st):
+        g.capture_end()
+    with pytest.raises(ValueError, match="captured run"):
+        plan.set([10], [300], table)
+    plan.set([1], [300], table)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)

@@ -410,6 +410,14 @@ class AttnPlan:
                                     _ptr(n_kv, C.c_int32), _ptr(t, C.c_int32), t.shape[1], stream))
         self.n_tok = int(n_new.sum())
 
+    def _captures(self, stream: Optional[int]) -> bool:
+        """Whether a run on this stream (None: torch's current one) is recorded into a graph."""
+        if stream is None or stream == 0:                   # (the legacy stream, 0, cannot be captured)
+            return stream is None and self._capturing()
+        import torch
+        with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=self.device)):
+            return self._capturing()
+
     def run(self, q, pages: KvPages, out, stream: Optional[int] = None) -> None:
         """out[i] = attention of token i of the step; q and out [at least the step's tokens, n_head,
         head_dim], rows past the tokens are not touched. After a captured run the plan takes no step of
@@ -420,7 +428,7 @@ class AttnPlan:
             raise TypeError(f"q and out must be {self.dtype}")
         if q.shape[0] < self.n_tok or out.shape[0] < self.n_tok:
             raise ValueError(f"q or out has fewer rows than the step has tokens ({self.n_tok})")
-        if self._capturing():
+        if self._captures(stream):
             rows = min(q.shape[0], out.shape[0])
             self._captured_rows = rows if self._captured_rows is None else min(rows, self._captured_rows)
         r = self._run(self.ptr, q.data_ptr(), sq[0], sq[1], pages.ref, out.data_ptr(), so[0], so[1],
