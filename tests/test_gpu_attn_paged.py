@@ -419,3 +419,27 @@ def test_a_run_captured_on_a_stream_of_its_own(L):
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+def test_one_token_whose_token_stride_says_nothing(L):
+    """A tensor of one token may have any stride along the tokens (a transposed [heads, 1, dim], a column of a larger
+    one): it is a step of one token all the same."""
+    (k, _, _), (v, _, _) = O.cache(4, 16, 2, 64, torch.float16, 17)
+    pages = L.KvPages(k, v)
+    plan = L.AttnPlan(pages, 8, torch.float16, 4, 2, 4)
+    plan.set([1], [50], [[0, 1, 2, 3]])
+    q = torch.randn(1, 8, 64, device="cuda", dtype=torch.float16)
+    want = torch.zeros_like(q)
+    plan.run(q, pages, want)
+    for out in (torch.zeros(8, 1, 64, device="cuda", dtype=torch.float16).transpose(0, 1),
+                torch.zeros(512, device="cuda", dtype=torch.float16).as_strided((1, 8, 64), (3, 64, 1))):
+        plan.run(q.as_strided((1, 8, 64), (5, 64, 1)), pages, out)
+        assert torch.equal(out, want)
+    (k1, _, _), (v1, _, _) = O.cache(4, 16, 1, 64, torch.float16, 18)
+    plan = L.AttnPlan(L.KvPages(k1, v1), 1, torch.float16, 4, 2, 4)   # one head: its stride says nothing either
+    plan.set([1], [50], [[0, 1, 2, 3]])
+    out = torch.zeros(64, device="cuda", dtype=torch.float16).as_strided((1, 1, 64), (7, 9, 1))
+    plan.run(q[:, :1], L.KvPages(k1, v1), out)
+    want = torch.zeros(1, 1, 64, device="cuda", dtype=torch.float16)
+    plan.run(q[:, :1].contiguous(), L.KvPages(k1, v1), want)
+    assert torch.equal(out, want) and out.abs().sum() > 0

@@ -211,3 +211,17 @@ def test_host_memory_and_wrong_shapes_are_refused(L):
         L.kv_store(pages, x.cuda(), x.cuda(), cell[:2])
     with pytest.raises(ValueError):
         L.KvPages(kc, vc, ks, torch.zeros(2, 4, 2, device="cuda"))
+
+
+def test_one_row_whose_token_stride_says_nothing(L):
+    kc, vc = (torch.zeros(2, 4, 2, 32, device="cuda", dtype=torch.float16) for _ in range(2))
+    pages = L.KvPages(kc, vc)
+    k = torch.randn(64, device="cuda", dtype=torch.float16).as_strided((1, 2, 32), (5, 32, 1))
+    v = torch.randn(64, device="cuda", dtype=torch.float16).as_strided((1, 2, 32), (64, 32, 1))
+    cell = torch.tensor([5], dtype=torch.int32, device="cuda")
+    L.kv_store(pages, k, v, cell)
+    assert torch.equal(kc[1, 1], k[0]) and torch.equal(vc[1, 1], v[0])
+    ko = torch.zeros(64, device="cuda", dtype=torch.float16).as_strided((1, 2, 32), (1, 32, 1))
+    vo = torch.zeros(2, 1, 32, device="cuda", dtype=torch.float16).transpose(0, 1)
+    L.kv_load(pages, cell, ko, vo)
+    assert torch.equal(ko, k) and torch.equal(vo, v)

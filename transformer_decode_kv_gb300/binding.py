@@ -302,6 +302,8 @@ def _rows(t, name: str, heads: int, dim: int):
     if len(sh) != 3 or sh[1] != heads or sh[2] != dim or st[2] != 1:
         raise ValueError(f"{name} must be [tokens, {heads}, {dim}] with dense rows, "
                          f"not {tuple(sh)} with strides {st}")
+    if sh[0] == 1:                          # one row: torch's stride from it to the next says nothing
+        return (heads * st[1] if heads > 1 else dim), st[1], 1
     return st
 
 
@@ -339,7 +341,7 @@ class KvPages:
     def _kv_rows(self, fn, k, v, cell, err, stream):
         st = _rows(k, "k", self.heads, self.dim)
         n = k.shape[0]
-        if v.shape != k.shape or v.dtype is not k.dtype or v.stride() != st:
+        if v.shape != k.shape or v.dtype is not k.dtype or _rows(v, "v", self.heads, self.dim) != st:
             raise ValueError("k and v must be alike")
         cells = _need(cell, "cell", "int32", (n,))
         r = fn(self.ref, _type_of(k), k.data_ptr(), v.data_ptr(), st[0], st[1], cells, n,
