@@ -487,7 +487,11 @@ uint32_t llm_attn_plan_error(llm_attn_plan* p) {
         failed("llm_attn_plan_error", cudaGetLastError());
         return ~0u;
     }
-    if (e) cudaMemset(p->err, 0, sizeof(e));
+    // (a memset returns before it is done: a run on a stream of its own could set a bit in between, to be lost)
+    if (e && (cudaMemset(p->err, 0, sizeof(e)) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess)) {
+        failed("llm_attn_plan_error", cudaGetLastError());
+        return ~0u;
+    }
     return e;
 }
 
