@@ -297,8 +297,9 @@ int32_t llm_sample_batch(llm_ctx *ctx, int32_t n, const int32_t *rows, const llm
 
 /* ---- operators on the caller's own device buffers ---------------------------------------------
  * For programs that keep their own KV cache (pages handed out by their own allocator) or their own
- * logits and want this library's kernels on them. They are the kernels a context runs for F8_E4M3
- * caches, attention windows (llm_set_attn_window) and llm_sample_batch. Conventions:
+ * logits and want this library's kernels on them. A context runs some of them over its own cache, as pages of one
+ * cell: the store and the attention for an F8_E4M3 cache, the attention with a window (llm_set_attn_window), and the
+ * sampler in llm_sample_batch. Conventions:
  *   - every data pointer is device memory of one GPU (a host pointer is refused, -1); the call runs
  *     on that GPU whichever device is current, and leaves the current device as it was;
  *   - work is enqueued on `stream` (a cudaStream_t of that GPU, NULL = the legacy default stream)
@@ -347,13 +348,23 @@ int llm_kv_load(const llm_kv_pages *kv, int32_t type, void *k, void *v,
  * p = the token's position. A sequence with n_kv cached rows and n_new new tokens has its new tokens
  * at positions n_kv - n_new .. n_kv - 1 (their rows are in the cache already, see llm_kv_store); key j
  * is the row at place j % page_size of page table[j / page_size]. A row without a visible key
- * (n_kv < n_new: negative positions) is zeros, one whose visible scores are all -infinity NaN (0 / 0). What masked or unwritten cells hold (NaN,
- * infinities) does not reach the output.
+ * (n_kv < n_new: negative positions) is zeros, one whose visible scores are all -infinity NaN (0 / 0). What masked
+ * or unwritten cells hold (NaN, infinities) does not reach the output.
+ *
+ * Scores, softmax sums and outputs are float32, the output rounded once. The weights enter the product with V as f16
+ * (half a step is 2^-11) where activations are F16, or BF16 over an F8_E4M3 cache; as two terms (2^-17 or better) for
+ * F32 activations and for BF16 caches, but as one bf16 (2^-8) for a BF16 cache where a sequence has 64 rows (token,
+ * query head) per KV head or more. Weights below f16's normal range add up to 2^-30 of the largest |v| that the token
+ * sees, per key. Rows of an F8_E4M3 cache may have any scales; a chunk of tokens takes far longer (it computes rows
+ * one key at a time) where, within the keys of one unit of work, a row that is not zeros has a scale above 2^7
+ * or below 2^-15 times the largest of the unit's first 128 keys. So it does where visible cells hold NaN or
+ * infinities.
  *
  * The plan of a step (which rows attend to which cells, split over the GPU) is made on the host once
  * and serves every layer: llm_attn_plan_set validates it and uploads it on `stream`; llm_attn_run
- * launches. A plan owns its workspace, so two runs of one plan must not overlap in time (use one
- * plan per stream, or order the streams); two graphs that may run at the same time need two plans.
+ * launches. A plan owns its workspace, so two runs of one plan must not overlap in time, nor a set and
+ * a run (use one plan per stream, or order the streams); two graphs that may run at the same time need two
+ * plans. A plan, and the memory that its captured runs were given, outlives the graphs that hold them.
  * llm_attn_run may be captured: the graph replays with whatever the plan was last set to, provided
  * that needs no other kernels (the bits of its llm_attn_plan_form are among those of the captured form),
  * else it leaves the output alone and sets bit 16 of the plan's error word. q and out of a captured run
@@ -391,7 +402,8 @@ int llm_attn_run(llm_attn_plan *plan, const void *q, int64_t q_stride_tok, int64
 /* The kernels the plan needs: 0 nothing to run, else the sum of 1 (8-row tiles: a token or two per
  * sequence), 2 (16-row tiles: a few) and 4 (256-row tensor-core tiles: chunks). -1: NULL. */
 int llm_attn_plan_form(const llm_attn_plan *plan);
-/* The plan's error word (0 = none) after waiting for its device; cleared by the call. */
+/* The plan's error word (0 = none, ~0 = the device could not be read) after waiting for its device; cleared by
+ * the call. Besides the bits above: 8, a wait inside a kernel gave up (rows that this cost are NaN). */
 uint32_t llm_attn_plan_error(llm_attn_plan *plan);
 
 /* The sampler chain of llm_sample_ith for n_rows rows of logits at once, one token per row, without
