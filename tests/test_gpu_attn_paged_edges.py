@@ -181,6 +181,46 @@ def test_e4m3_rows_of_later_tokens_do_not_reach_earlier_ones(L, act, n_new, n_kv
     check(L, act, F8, big, v, q, n_new, n_kv, window=3, n_sink=2)
 
 
+@pytest.mark.parametrize("act", [F16, BF16, F32])
+@pytest.mark.parametrize("n_new,n_kv", [(1, 700), (3, 300)])
+@pytest.mark.parametrize("power", [-110, -85, -60, 60, 90, 110])
+def test_e4m3_values_at_the_ends_of_float32(L, act, n_new, n_kv, power):
+    """Value rows of 2^power, alone and among rows of zeros; and beside large scores."""
+    if act == F16:
+        power //= 8                                         # (outputs that f16 holds)
+    rng, k, v = rows(13, n_kv, 2, 64)
+    q = rng.normal(size=(n_new, 8, 64))
+    check(L, act, F8, k, v * 2.0 ** power, q, n_new, n_kv)
+    v[rng.random(v.shape[:2]) < 0.5] = 0
+    v[:200] = 0
+    check(L, act, F8, k, v * 2.0 ** power, q, n_new, n_kv)
+    k[7] *= 2.0 ** 30                                       # one key takes it all, or nothing
+    check(L, act, F8, k, v * 2.0 ** power, q, n_new, n_kv)
+
+
+@pytest.mark.parametrize("act", [BF16, F32])
+def test_e4m3_equal_scores_past_2_to_24(L, act):
+    """Scores of 2^30 that are equal: every key has the same weight, whatever the scales of its values."""
+    rng, k, v = rows(14, 1500, 1, 64)
+    k[:] = 0
+    k[:, 0, 0] = 2.0 ** 15
+    v *= 2.0 ** rng.integers(-30, 30, size=(v.shape[0], 1, 1))
+    q = np.zeros((2, 4, 64))
+    q[:, :, 0] = 2.0 ** 18
+    kc, ks, kh = stored(k, F8)
+    vc, vs, vh = stored(v, F8)
+    plan = L.AttnPlan(L.KvPages(kc, vc, ks, vs), 4, act, 2, 1, 100)
+    plan.set([2], [1500], np.arange(94)[None])
+    qd = torch.from_numpy(q).to(act).cuda()
+    out = torch.zeros_like(qd)
+    plan.run(qd, L.KvPages(kc, vc, ks, vs), out)
+    got = out.double().cpu().numpy()
+    for t, n in ((0, 1499), (1, 1500)):
+        want, mag = vh[:n, 0].mean(0), np.abs(vh[:n, 0]).mean(0)
+        tol = O.attention_tol(want, mag, np.zeros(()), act, n, 64, 2 * np.abs(vh[:n]).max())
+        assert (np.abs(got[t] - want) <= tol).all()
+
+
 @pytest.mark.parametrize("act", [F16, BF16])
 @pytest.mark.parametrize("n_new,n_kv,at,Hkv", [(16, 700, 400, 1), (64, 700, 690, 1), (150, 5000, 3000, 1),
                                                (150, 5000, 130, 1), (200, 700, 400, 8)])

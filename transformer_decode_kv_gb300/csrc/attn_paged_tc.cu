@@ -29,10 +29,11 @@
 // of two like s; rows of zeros, whose scale is 1, do not count): exact from s0 2^-15 to s0 2^7. A unit with a row out of
 // this range is done key by key, after the CTA's other units, as is one with values that are not finite.
 //
-// Measured, 32 / 8 heads of 128: 2048 bf16 tokens at the end of 32768 keys 770 us (1.4 PFLOP/s, 0.73 of the rate of a
-// large bf16 matrix product), bound by the softmax's exponentials and packing; 512 f16 tokens at the end of
-// 8192 78 us, where cut tiles weigh; over E4M3 1190 and 111 us, where the rows' conversion shares issue slots and shared
-// memory with the softmax.
+// Measured, 32 / 8 heads of 128: 2048 bf16 tokens at the end of 32768 keys 769 us (1.4 PFLOP/s, 0.72 of the rate of a
+// large bf16 matrix product), bound by what stands between a half's two products (scores out of TMEM, exponentials, P
+// back into TMEM): at the end of 8192 keys the tensor pipe is active for 56% of the time, issue slots are used for 38%, the
+// exponential unit for 29%. 512 f16 tokens at the end of 8192 take 80 us, where cut tiles weigh; over E4M3 1203 and 113
+// us, where the rows' conversion shares issue slots and shared memory with the softmax (tensor pipe 30%, issue slots 37%).
 //
 // Every wait is bounded by a wall-clock limit; a timeout sets ERR_TIMEOUT, ends every role's loop, and
 // the CTA leaves after its copies and with its TMEM freed.
