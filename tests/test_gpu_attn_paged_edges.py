@@ -287,3 +287,73 @@ def test_units_done_again_leave_no_trace(L):
                     ok[n - 1, :, 5] = True
                 assert ok.all()
     assert plan.error() == 0
+
+
+@pytest.mark.parametrize("act,cdt,page", [(F16, F16, 64), (BF16, BF16, 17), (F32, F16, 1), (BF16, F8, 64), (F32, F8, 17)])
+def test_cells_past_32_bit_offsets(L, act, cdt, page):
+    """A cache of more than 2^32 bytes a tensor (E4M3: 2^32 codes), its last pages used: bulk copies, row copies, scales."""
+    Hkv, hd = 8, 128
+    n_pages = (2 ** 32 + 2 ** 28) // ((1 if cdt == F8 else 2) * page * Hkv * hd)
+    n_new, n_kv = [1, 40], [150, 300]
+    need = [-(-n // page) for n in n_kv]
+    small, spare = sum(need), 3
+    rng = np.random.default_rng(19)
+    use = np.concatenate([np.arange(n_pages - small + 2, n_pages), [spare, 0]])   # the last pages, and two of the first
+    rng.shuffle(use)
+    caches = []
+    for i in range(2):
+        x = rng.normal(size=(small * page, Hkv, hd))
+        held, sc = x, None
+        if cdt == F8:
+            code, s = O.quantise(x)
+            held = O.E4M3[code] * s[..., None]
+            sc = torch.empty((n_pages, page, Hkv), device="cuda")
+            sc[torch.from_numpy(use).cuda()] = torch.from_numpy(s.astype(np.float32)).view(small, page, Hkv).cuda()
+            rows_ = torch.from_numpy(code)
+        else:
+            rows_ = torch.from_numpy(x).to(cdt)
+            held = rows_.double().numpy()
+        big = torch.empty((n_pages, page, Hkv, hd), dtype=cdt, device="cuda")
+        big[torch.from_numpy(use).cuda()] = rows_.view(small, page, Hkv, hd).cuda()
+        caches.append((big, sc, held))
+    (k, ks, kh), (v, vs, vh) = caches
+    assert k.numel() * k.element_size() > 2 ** 32
+    pages = L.KvPages(k, v, ks, vs)
+    q = torch.from_numpy(rng.normal(size=(41, 16, hd))).to(act).cuda()
+    out = torch.zeros_like(q)
+    table = np.full((2, max(need)), -1, np.int32)
+    table[0, :need[0]], table[1, :need[1]] = use[:need[0]], use[need[0]:]
+    plan = L.AttnPlan(pages, 16, act, 41, 2, table.size)
+    plan.set(n_new, n_kv, table)
+    plan.run(q, pages, out)
+    assert plan.error() == 0
+    x, got = q.double().cpu().numpy(), out.double().cpu().numpy()
+    for t0, n, m, c0 in ((0, 1, 150, 0), (1, 40, 300, need[0] * page)):
+        ref, mag, smag, vmax = reference(x[t0:t0 + n], kh[c0:], vh[c0:], n, m, 0, 0)
+        tol = O.attention_tol(ref, mag, smag, act, m, hd, 2 * vmax[..., None])
+        assert (np.abs(got[t0:t0 + n] - ref) <= tol).all()
+
+
+@pytest.mark.parametrize("act,cdt", [(F16, F16), (BF16, BF16), (F32, F16), (BF16, F8)])
+@pytest.mark.parametrize("n_new", [1, 5, 70])
+def test_rows_on_odd_16_byte_boundaries(L, act, cdt, n_new):
+    """q and out begin 16 bytes past a 32-byte boundary, and their rows are an odd number of 16 bytes apart."""
+    rng, k, v = rows(20, 200, 2, 64)
+    kc, ks, kh = stored(k, cdt)
+    vc, vs, vh = stored(v, cdt)
+    pages = L.KvPages(kc, vc, ks, vs)
+    es = 4 if act == F32 else 2
+    step = 64 + 16 // es
+    buf = [torch.full((n_new * 8 * step + 64,), 9.0, dtype=act, device="cuda") for _ in range(2)]
+    q, out = (b[16 // es:].as_strided((n_new, 8, 64), (8 * step, step, 1)) for b in buf)
+    assert out.data_ptr() % 32 == 16
+    x = rng.normal(size=(n_new, 8, 64))
+    q.copy_(torch.from_numpy(x))
+    plan = L.AttnPlan(pages, 8, act, n_new, 1, 16)
+    plan.set([n_new], [200], np.arange(13)[None])
+    plan.run(q, pages, out)
+    ref, mag, smag, vmax = reference(q.double().cpu().numpy(), kh, vh, n_new, 200, 0, 0)
+    tol = O.attention_tol(ref, mag, smag, act, 200, 64, 2 * vmax[..., None]) + (2.0 ** -25 if act == F16 else 0)
+    assert (np.abs(out.double().cpu().numpy() - ref) <= tol).all()
+    out.fill_(9.0)
+    assert (buf[1] == 9.0).all()                            # nothing was written between the rows

@@ -234,3 +234,13 @@ def test_strides_graph_and_many_rows(L):
         L.sample_rows(x, token.long())
     with pytest.raises(L.LlmError, match="device memory"):
         L.sample_rows(x.cpu(), token)
+
+
+def test_rows_past_32_bit_offsets(L):
+    """Rows 1.5 * 2^30 elements apart: the last begins past 2^32 bytes (and 2^31 elements)."""
+    base = torch.empty(3 * 2 ** 30 + 2000, dtype=torch.float16, device="cuda")
+    logits = base.as_strided((3, 2000), (3 * 2 ** 29, 1))
+    rng = np.random.default_rng(7)
+    logits.copy_(torch.from_numpy(rng.normal(size=(3, 2000)) * 2))
+    for kw in (dict(top_k=40), dict(top_k=10 ** 9, top_p=0.9)):
+        check(L, logits, [SamplerParams(**kw)] * 3, rng.random(3))
