@@ -231,3 +231,18 @@ def test_sequences_of_almost_2_to_31_keys_are_refused(B):
     for n, ok in ((2 ** 31 - 513, True), (2 ** 31 - 512, False), (2 ** 31 - 128, False), (2 ** 31 - 2, False)):
         r = B.lib().llm_debug_attn_units(C.byref(shape), C.byref(kv), 152, 1, 1, p(64), p(n), None, 0, None, None, None)
         assert (r > 0) == ok
+
+
+def test_host_integers_are_not_wrapped(B):
+    """A page number or length that int32 does not hold must not become another one."""
+    plan = B.AttnPlan.__new__(B.AttnPlan)                  # (no device is reached: the arguments are refused first)
+    plan.ptr, plan._captured_rows, plan.device = None, None, None
+    big = np.array([2 ** 32 + 1])
+    for n_new, n_kv, pages in ((big, [1], [[0]]), ([1], big, [[0]]), ([1], [1], big[None]), ([1], [1], [[-2 ** 31 - 1]])):
+        with pytest.raises(ValueError, match="int32"):
+            plan.set(n_new, n_kv, pages, stream=0)
+    for n_new, n_kv, pages in (([1.0], [1], [[0]]), ([1], [1], [[0.5]]), ([1], ["1"], [[0]])):
+        with pytest.raises(TypeError, match="integers"):
+            plan.set(n_new, n_kv, pages, stream=0)
+    with pytest.raises(B.LlmError, match="NULL plan"):     # good ones reach the library
+        plan.set(np.array([1], np.int64), [1], np.array([[3]], np.uint8), stream=0)

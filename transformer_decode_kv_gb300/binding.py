@@ -274,6 +274,17 @@ def _type_of(t) -> int:
     return r
 
 
+def _host_ints(a, name: str) -> np.ndarray:
+    """Host integers as int32; one that int32 does not hold is refused, not wrapped."""
+    x = np.asarray(a)
+    if x.dtype != np.int32 and x.size:
+        if x.dtype.kind not in "iu":
+            raise TypeError(f"{name} must be integers, not {x.dtype}")
+        if x.min() < -2 ** 31 or x.max() >= 2 ** 31:
+            raise ValueError(f"{name} must fit int32")
+    return _i32(x)
+
+
 def _stream_of(t, stream: Optional[int]) -> Optional[int]:
     """The given cudaStream_t, or torch's current stream of t's device."""
     if stream is not None or not t.is_cuda:
@@ -399,8 +410,8 @@ class AttnPlan:
     def set(self, n_new, n_kv, pages, stream: Optional[int] = None) -> None:
         """The step's sequences: n_new tokens each, n_kv cached rows each (the new ones included), page
         table [n_seq, at least ceil(n_kv / page_size)]; host integers."""
-        n_new, n_kv = _i32(n_new), _i32(n_kv)
-        t = _i32(pages)
+        n_new, n_kv = _host_ints(n_new, "n_new"), _host_ints(n_kv, "n_kv")
+        t = _host_ints(pages, "pages")
         if n_new.ndim != 1 or n_new.shape != n_kv.shape or t.ndim != 2 or len(t) != len(n_new):
             raise ValueError("n_new [n_seq], n_kv [n_seq] and pages [n_seq, n] are needed")
         if self._captured_rows is not None and n_new.sum() > self._captured_rows:
