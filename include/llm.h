@@ -43,13 +43,21 @@ typedef enum {
     LLM_TYPE_F16  = 1,
     LLM_TYPE_BF16 = 2,
     LLM_TYPE_Q8_0 = 8,
-    LLM_TYPE_F8_E4M3 = 100   /* cache rows only (a number GGUF does not use): 8-bit floats of 4 exponent
+    LLM_TYPE_F8_E4M3 = 100,  /* cache rows only (a number GGUF does not use): 8-bit floats of 4 exponent
                               * and 3 mantissa bits (no infinities, largest 448), value = scale * q with
                               * one float32 power-of-two scale per row of head_dim values: the least
                               * 2^e >= 2^-126 with max|x| / 2^e <= 448 over the row's finite values (1 for a
                               * row of zeros). Scaling by a power of two is exact, so the only rounding
                               * is x / scale to the nearest E4M3 value, ties to even; infinities become
                               * +-448 * scale and NaN stays NaN. */
+    LLM_TYPE_F4_E2M1 = 101   /* cache rows of the operators only: 4-bit floats (sign, 2 exponent bits, 1 mantissa bit: 0,
+                              * 0.5, 1, 1.5, 2, 3, 4, 6), value = scale * block * q with one float32 power-of-two
+                              * scale per row, the least 2^e >= 2^-126 with max|x| / 2^e <= 2688 = 6 * 448 over the
+                              * row's finite values (1 for a row of zeros), and one E4M3 number per 16 values:
+                              * the nearest to max|x| / (6 scale) of the block's finite values (ties to even), at least
+                              * 2^-9. q is the value nearest to x / (scale * block), ties to the even code, at most 6;
+                              * infinities become +-6 * block * scale. There is no code for NaN: a NaN makes its
+                              * block's number NaN, and so the 16 values. 4.75 bits a value in rows of 128. */
 } llm_type;
 
 /* Model hyper-parameters ([P2] Example 8, print_info). head_dim * n_head is the width of the Q
@@ -314,29 +322,35 @@ const char *llm_op_last_error(void);
 /* A paged K/V cache: n_pages pages of page_size cells, a cell holds one row of head_dim values per KV
  * head for K and one for V. Cell number = page * page_size + place in the page (below 2^31). The row of
  * (page, place, head) starts page * stride_page + place * stride_cell + head * stride_head elements
- * after k (and v): any order of the dimensions fits. type: F16, BF16 or F8_E4M3; head_dim 32, 64 or
- * 128; rows start on 16-byte boundaries. F8_E4M3: k_scale / v_scale hold the rows' float32
+ * after k (and v): any order of the dimensions fits. type: F16, BF16, F8_E4M3 or F4_E2M1; head_dim 32, 64 or
+ * 128; rows start on 16-byte boundaries. F8_E4M3 and F4_E2M1: k_scale / v_scale hold the rows' float32
  * scales, (page, place, head) at page * sstride_page + place * sstride_cell + head * sstride_head
- * (NULL for the other types). Strides are not negative and rows must not overlap. */
+ * (NULL for the other types). F4_E2M1: an element of k and v is a byte of two codes, value 2 i in the low half of a
+ * row's byte i; k_block / v_block hold head_dim / 16 E4M3 bytes per row, the row of (page, place, head) at page *
+ * bstride_page + place * bstride_cell + head * bstride_head bytes, all multiples of head_dim / 16. (The other
+ * types do not read these five fields.) Such rows are short: the attention reads them fastest where a head's cells of a
+ * page follow each other, rows, scales and block scales alike. Strides are not negative and rows must not overlap. */
 typedef struct llm_kv_pages {
     int32_t type, n_head_kv, head_dim, page_size, n_pages;
     void   *k, *v;
     int64_t stride_page, stride_cell, stride_head;
     float  *k_scale, *v_scale;
     int64_t sstride_page, sstride_cell, sstride_head;
+    uint8_t *k_block, *v_block;
+    int64_t bstride_page, bstride_cell, bstride_head;
 } llm_kv_pages;
 
 /* Write n rows of new keys and values into the cells cell[0..n) (device), cast to the cache's type or
- * quantised as LLM_TYPE_F8_E4M3 says. k / v: F32, F16 or BF16 (`type`), row (i, head) at
+ * quantised as LLM_TYPE_F8_E4M3 and LLM_TYPE_F4_E2M1 say. k / v: F32, F16 or BF16 (`type`), row (i, head) at
  * i * stride_tok + head * stride_head elements, 16-byte aligned rows. A negative cell skips the row
  * (padding); a cell past the cache is skipped and sets err bit 1. The cells named by one call must
- * differ (a cell named twice keeps one of the rows, or for F8_E4M3 a mix of them). n = 0 is a no-op. */
+ * differ (a cell named twice keeps one of the rows, or for F8_E4M3 and F4_E2M1 a mix of them). n = 0 is a no-op. */
 int llm_kv_store(const llm_kv_pages *kv, int32_t type, const void *k, const void *v,
                  int64_t stride_tok, int64_t stride_head, const int32_t *cell, int32_t n,
                  uint32_t *err, void *stream);
 
 /* Read the rows of cells cell[0..n) back into k / v (the same arguments, now outputs): value = scale *
- * q for F8_E4M3, rounded once to `type`. The row of a negative cell is left as it was, and so is that of
+ * q for F8_E4M3 (scale * block * q for F4_E2M1), rounded once to `type`. The row of a negative cell is left as it was, and so is that of
  * a cell past the cache (err bit 1). A cell may be named any number of times. */
 int llm_kv_load(const llm_kv_pages *kv, int32_t type, void *k, void *v,
                 int64_t stride_tok, int64_t stride_head, const int32_t *cell, int32_t n,
@@ -382,7 +396,7 @@ typedef struct llm_attn_shape {
 typedef struct llm_attn_plan llm_attn_plan;
 
 /* A plan for caches of kv's type, head count, head_dim, page size and page count (kv's pointers are
- * not kept; F16 caches take F16 or F32 activations, BF16 caches BF16, F8_E4M3 all three). Device
+ * not kept; F16 caches take F16 or F32 activations, BF16 caches BF16, F8_E4M3 and F4_E2M1 all three). Device
  * memory is allocated on the current device here and nowhere else. NULL on invalid parameters or a
  * failed allocation. */
 llm_attn_plan *llm_attn_plan_init(const llm_attn_shape *shape, const llm_kv_pages *kv);

@@ -1,0 +1,86 @@
+"""The 4-bit cache, the page lists and plans set from the device on a machine without a GPU: what the entry points
+refuse before anything touches a device."""
+import ctypes as C
+import os
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def B():
+    from transformer_decode_kv_gb300 import binding, build
+    if not os.path.exists(binding.LIB_PATH):
+        build.build()
+    return binding
+
+
+PTR = 0x10000                       # an aligned address that is never read
+
+
+def desc(B, **kw):
+    """A 4-bit cache [8 pages][2 heads][16 cells] of rows of 128 values."""
+    d = B.KvPagesDesc()
+    base = dict(type=B.F4_E2M1, n_head_kv=2, head_dim=128, page_size=16, n_pages=8, k=PTR, v=PTR, stride_page=2048,
+                stride_cell=64, stride_head=1024, k_scale=PTR, v_scale=PTR, sstride_page=32, sstride_cell=1,
+                sstride_head=16, k_block=PTR, v_block=PTR, bstride_page=256, bstride_cell=8, bstride_head=128)
+    base.update(kw)
+    for n, v in base.items():
+        setattr(d, n, v)
+    return d
+
+
+@pytest.mark.parametrize("bad,why", [
+    (dict(k=PTR + 8), "16-byte"), (dict(v=None), "NULL"), (dict(stride_cell=72), "strides"), (dict(stride_cell=48), "strides"),
+    (dict(stride_head=512), "strides"), (dict(k_scale=None), "scales"), (dict(v_scale=PTR + 2), "4-byte"),
+    (dict(sstride_cell=0), "scale strides"), (dict(k_block=None), "block scales"), (dict(v_block=None), "block scales"),
+    (dict(k_block=PTR + 4), "block scales"), (dict(bstride_cell=4), "block-scale"), (dict(bstride_cell=12), "block-scale"),
+    (dict(bstride_cell=-8), "block-scale"), (dict(bstride_head=64), "block-scale"), (dict(bstride_page=1 << 50), "block-scale"),
+    (dict(head_dim=96), "head_dim"), (dict(type=102), "paged cache")])
+def test_bad_caches_are_refused(B, bad, why):
+    L, d = B.lib(), desc(B, **bad)
+    for fn in (L.llm_kv_store, L.llm_kv_load):
+        assert fn(C.byref(d), B.F16, PTR, PTR, 256, 128, PTR, 4, None, None) == -1
+        assert why in L.llm_op_last_error().decode()
+
+
+def test_good_caches_reach_the_device_check(B):
+    L = B.lib()
+    one = dict(n_pages=1, stride_page=-1, sstride_page=-1, bstride_page=-1)      # (a stride that is never used)
+    for kw in ({}, one, dict(head_dim=32, stride_page=512, stride_cell=16, stride_head=256, k_block=PTR + 2, bstride_cell=2,
+                             bstride_head=32, bstride_page=64)):
+        d = desc(B, **kw)
+        r = L.llm_kv_store(C.byref(d), B.F16, PTR, PTR, 256, 128, PTR, 4, None, None)
+        assert r != 0 and not any(w in L.llm_op_last_error() for w in (b"stride", b"boundar", b"scales")), L.llm_op_last_error()
+
+
+def test_activations_of_a_4_bit_cache(B):
+    L, d = B.lib(), desc(B)
+    one = (C.c_int32 * 1)(1)
+    for t, ok in ((B.F32, True), (B.F16, True), (B.BF16, True), (B.F8_E4M3, False), (B.F4_E2M1, False), (B.Q8_0, False)):
+        s = B.AttnShape(type=t, n_head=8, scale=0.0, window=0, n_sink=0, max_tok=64, max_seq=8, max_table=64)
+        r = L.llm_debug_attn_units(C.byref(s), C.byref(d), 152, 1, 1, one, one, None, 0, None, None, None)
+        assert (r > 0) == ok
+
+
+def test_a_context_does_not_take_a_4_bit_cache(B):
+    cp = B.lib().llm_cparams_default()
+    cp.type_k = cp.type_v = B.F4_E2M1
+    cp.flags = B.CTX_HOST_ONLY
+    hp = B.HParams(2, 64, 2, 1, 32, 128, 100, 10000.0, 1e-5, 0)
+    assert not B.lib().llm_ctx_init(C.byref(hp), C.byref(cp))
+
+
+def test_python_checks_of_the_cache(B):
+    u8 = lambda *s: torch.zeros(s, dtype=torch.uint8)
+    k, s, b = u8(4, 16, 2, 64), torch.zeros(4, 16, 2), u8(4, 16, 2, 8)
+    d = B.KvPages(k, k, s, s, b, b)
+    assert d.desc.type == B.F4_E2M1 and d.dim == 128 and d.desc.stride_cell == 128 and d.desc.bstride_cell == 16
+    assert B.KvPages(k, k, s, s).desc.type == B.F8_E4M3          # without block scales: E4M3 codes
+    assert B.KvPages(k, k, s, s, b.view(torch.float8_e4m3fn), b.view(torch.float8_e4m3fn)).desc.type == B.F4_E2M1
+    for args in ((k, k, s, s, b, None), (k, k, None, None, b, b), (k, k, s, s, u8(4, 16, 2, 4), b),
+                 (k, k, s, s, b, u8(4, 2, 16, 8).transpose(1, 2)), (k, k, s, s, u8(4, 16, 2, 16)[..., ::2], u8(4, 16, 2, 16)[..., ::2])):
+        with pytest.raises(ValueError):
+            B.KvPages(*args)
+    with pytest.raises(TypeError):
+        B.KvPages(k.half(), k.half(), s, s, b, b)

@@ -15,7 +15,7 @@ import numpy as np
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libllm.so")
 
-F32, F16, BF16, Q8_0, F8_E4M3 = 0, 1, 2, 8, 100
+F32, F16, BF16, Q8_0, F8_E4M3, F4_E2M1 = 0, 1, 2, 8, 100, 101
 CTX_HOST_ONLY = 1
 CTX_FUSED_STEP = 2
 CTX_KV_SPLIT = 4
@@ -53,7 +53,9 @@ class KvPagesDesc(C.Structure):
                 ("stride_page", C.c_int64), ("stride_cell", C.c_int64), ("stride_head", C.c_int64),
                 ("k_scale", C.c_void_p), ("v_scale", C.c_void_p),
                 ("sstride_page", C.c_int64), ("sstride_cell", C.c_int64),
-                ("sstride_head", C.c_int64)]
+                ("sstride_head", C.c_int64), ("k_block", C.c_void_p), ("v_block", C.c_void_p),
+                ("bstride_page", C.c_int64), ("bstride_cell", C.c_int64),
+                ("bstride_head", C.c_int64)]
 
 
 class AttnShape(C.Structure):
@@ -322,20 +324,40 @@ class KvPages:
     """A paged K/V cache held in torch CUDA tensors: k and v [n_pages, page_size, n_head_kv, head_dim]
     (float16, bfloat16, or E4M3 codes as float8_e4m3fn or uint8), in any memory order that keeps the
     rows of head_dim values dense (a [page, head, cell, dim] cache is passed as its transpose).
-    k_scale and v_scale [n_pages, page_size, n_head_kv] float32 belong to an E4M3 cache."""
+    k_scale and v_scale [n_pages, page_size, n_head_kv] float32 belong to an E4M3 cache. With k_block and
+    v_block [n_pages, page_size, n_head_kv, head_dim / 16] too (E4M3 numbers as float8_e4m3fn or uint8, dense
+    rows) it is a 4-bit cache: k and v are uint8 (or float4_e2m1fn_x2) [n_pages, page_size, n_head_kv,
+    head_dim / 2], two E2M1 codes a byte, the first value in the low half."""
 
-    def __init__(self, k, v, k_scale=None, v_scale=None):
+    def __init__(self, k, v, k_scale=None, v_scale=None, k_block=None, v_block=None):
+        import torch
         if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.stride() != v.stride():
             raise ValueError("k and v must be alike, [n_pages, page_size, n_head_kv, head_dim]")
         if k.stride(3) != 1:
             raise ValueError("cache rows must be dense")
         d = KvPagesDesc()
-        d.type = _type_of(k)
+        if (k_block is None) != (v_block is None):
+            raise ValueError("k_block and v_block come together")
+        f4 = k_block is not None
+        if f4 and not (k.dtype is torch.uint8 or k.dtype is getattr(torch, "float4_e2m1fn_x2", torch.uint8)):
+            raise TypeError(f"a 4-bit cache holds bytes of two codes (uint8), not {k.dtype}")
+        d.type = F4_E2M1 if f4 else _type_of(k)
         d.n_pages, d.page_size, d.n_head_kv, d.head_dim = k.shape
         d.k, d.v = k.data_ptr(), v.data_ptr()
         d.stride_page, d.stride_cell, d.stride_head = k.stride()[:3]
-        if (d.type == F8_E4M3) != (k_scale is not None) or (k_scale is None) != (v_scale is None):
-            raise ValueError("an E4M3 cache has scales, other caches have none")
+        if (d.type in (F8_E4M3, F4_E2M1)) != (k_scale is not None) or (k_scale is None) != (v_scale is None):
+            raise ValueError("E4M3 and 4-bit caches have scales, other caches have none")
+        if f4:
+            d.head_dim *= 2
+            for b in (k_block, v_block):
+                if _type(b) != F8_E4M3 or b.shape != k.shape[:3] + (d.head_dim // 16,) or \
+                        (b.shape[3] > 1 and b.stride(3) != 1):
+                    raise ValueError("block scales must be E4M3 bytes [n_pages, page_size, n_head_kv, head_dim / 16] "
+                                     "with dense rows")
+            if k_block.stride() != v_block.stride():
+                raise ValueError("k_block and v_block must be laid out alike")
+            d.k_block, d.v_block = k_block.data_ptr(), v_block.data_ptr()
+            d.bstride_page, d.bstride_cell, d.bstride_head = k_block.stride()[:3]
         if k_scale is not None:
             for s in (k_scale, v_scale):
                 if _type(s) != F32 or s.shape != k.shape[:3]:
@@ -348,6 +370,7 @@ class KvPages:
         self.ref = C.byref(d)
         self.heads, self.dim = d.n_head_kv, d.head_dim
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.k_block, self.v_block = k_block, v_block
 
     def _kv_rows(self, fn, k, v, cell, err, stream):
         st = _rows(k, "k", self.heads, self.dim)

@@ -94,7 +94,10 @@ __device__ __forceinline__ void fetch16(uint32_t dst, const uint8_t* src) {
 __device__ __forceinline__ void fetch16z(uint32_t dst, const uint8_t* src, bool ok) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ void fetch4z(uint32_t dst, const float* src, bool ok) {
+__device__ __forceinline__ void fetch8z(uint32_t dst, const uint8_t* src, bool ok) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(ok ? 8 : 0) : "memory");
+}
+__device__ __forceinline__ void fetch4z(uint32_t dst, const void* src, bool ok) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(ok ? 4 : 0) : "memory");
 }
 // Byte offset of 16-byte chunk `ch` of row `row` in a tile of rows of ROWB bytes. The chunks of a 128-byte line are
@@ -105,7 +108,9 @@ __device__ __forceinline__ uint32_t at16(int row, int ch) {
     if constexpr (ROWB >= 128) return (uint32_t)(row * ROWB + ((ch ^ (((row >> 1) & 3) << 1) ^ ((row & 1) << 2)) << 4));
     else if constexpr (ROWB == 64)
         return (uint32_t)((row >> 1) * 128 + (((((row & 1) << 2) | ch) ^ (((row >> 1) & 3) << 1)) << 4));
-    else return (uint32_t)((row >> 2) * 128 + (((((row & 3) << 1) | ch) ^ (((row >> 2) & 1) << 1)) << 4));
+    else if constexpr (ROWB == 32)
+        return (uint32_t)((row >> 2) * 128 + (((((row & 3) << 1) | ch) ^ (((row >> 2) & 1) << 1)) << 4));
+    else return (uint32_t)(row * 16);
 }
 template <int N>
 __device__ __forceinline__ void take(uint32_t* d, const uint8_t* p) {
@@ -122,38 +127,41 @@ __device__ __forceinline__ void take(uint32_t* d, const uint8_t* p) {
 
 constexpr int kMaxSm = 160;
 
-// Where this lane's key of 32 lies (off < 0: not read) and its position.
-struct Info { int64_t off, soff; int pos; };
+// Where this lane's key of 32 lies (off < 0: not read) and its position; F4_E2M1: its block scales, or, where they are too
+// short for an asynchronous copy (head_dim 32), the scales themselves.
+struct Info { int64_t off, soff, boff; int pos; uint32_t blk; };
 
 template <int HD, int CT, int QT, int ROWS>
 struct Cfg {
-    static constexpr bool F8 = CT == W_F8, BF = CT == W_BF16;
+    static constexpr bool F8 = CT == W_F8, F4 = CT == W_F4, BF = CT == W_BF16;
+    static constexpr bool RS = F8 || F4;                        // rows have scales
     static constexpr bool SPLIT_Q = QT == W_F32;
     static constexpr bool SPLIT_P = QT == W_F32 || BF;
     static constexpr bool ROW_SCALE = !BF && QT != W_F16;
     static constexpr int W = attn_rows_warps(HD, CT, ROWS);     // warps
     static constexpr int R = ROWS / 8;                          // 8-row column tiles
     static constexpr int KS = HD / 16;                          // k-steps of K Q^T
-    static constexpr int KW = F8 ? HD / 16 : HD / 8;            // words of a key a lane holds
+    static constexpr int KW = F4 ? HD / 32 : F8 ? HD / 16 : HD / 8;   // words of a key a lane holds
     static constexpr int KC = KW < 4 ? KW : 4;                  // ... copied KC at a time
     static constexpr int KP = KW / KC;
     static constexpr int MT = HD / 16;                          // 16-dim row tiles of O^T
-    static constexpr int VP = F8 ? HD / 8 : (HD / 8 < 8 ? HD / 8 : 8);   // contiguous dims of a value per lane
+    static constexpr int VP = RS ? HD / 8 : (HD / 8 < 8 ? HD / 8 : 8);   // contiguous dims of a value per lane
     static constexpr int VH = HD / 8 / VP;                      // ... in VH places 8 * VP dims apart
-    static constexpr int VW = F8 ? VP / 4 : VP / 2;             // words of one place
-    // a stage: 32 rows of K and of V, then the keys' positions, which of them are read, and, for E4M3, scales
-    static constexpr int ROWB = F8 ? HD : 2 * HD;
+    static constexpr int VW = F4 ? (VP + 7) / 8 : F8 ? VP / 4 : VP / 2;   // words of one place (F4, 32 dims: half of one)
+    // a stage: 32 rows of K and of V, then the keys' positions, which of them are read, and, for E4M3 and E2M1, scales
+    static constexpr int ROWB = F4 ? HD / 2 : F8 ? HD : 2 * HD;
     static constexpr int META = 64 * ROWB;
-    static constexpr int STAGE = META + 128 + 16 + (F8 ? 256 : 0);
+    static constexpr int NB = HD / kF4Block, BLK = META + 144 + 256;   // block scales: 32 rows of K, then of V
+    static constexpr int STAGE = META + 128 + 16 + (RS ? 256 : 0) + (F4 ? 64 * NB : 0);
     static constexpr int OUT = W * ROWS * (HD + 4) * 4;          // the warps' results, over the stages
     static constexpr int FIT = (227 * 1024 / kAttnRowsCtas - 4096) / (W * STAGE);
     static constexpr int S = FIT < 6 ? FIT : 6;
     static constexpr int RING = W * S * STAGE;
-    static constexpr int END = RING > OUT ? RING : OUT;
+    // the join of a cut tile: (reference, sum) of its rows from every CTA, and a part at least
+    static constexpr int JOIN = 8 * ROWS * kAttnRowsCtas * kMaxSm + ROWS * HD * 4;
+    static constexpr int END = RING > OUT ? (RING > JOIN ? RING : JOIN) : (OUT > JOIN ? OUT : JOIN);
     static constexpr int BYTES = END + W * 256 + 2 * W * ROWS * 4 + 16;
     static_assert(S >= 2, "a stage to read and one to fill");
-    // the join of a cut tile: (reference, sum) of its rows from every CTA, and a part at least
-    static_assert(END >= 8 * ROWS * kAttnRowsCtas * kMaxSm + ROWS * HD * 4, "parts of a cut tile");
 };
 
 template <int HD, int CT, int QT, int ROWS>
@@ -161,7 +169,7 @@ __global__ void __launch_bounds__(32 * attn_rows_warps(HD, CT, ROWS), kAttnRowsC
 attn_rows_kernel(AttnPagedArgs a) {
     using C = Cfg<HD, CT, QT, ROWS>;
     constexpr int kWarps = C::W, kThr = 32 * kWarps;
-    constexpr bool F8 = C::F8, BF = C::BF;
+    constexpr bool F8 = C::F8, F4 = C::F4, RS = C::RS, BF = C::BF;
     constexpr int R = C::R;
     extern __shared__ __align__(16) uint8_t sm[];
     float (*s_o)[ROWS][HD + 4] = reinterpret_cast<float (*)[ROWS][HD + 4]>(sm);
@@ -179,8 +187,10 @@ attn_rows_kernel(AttnPagedArgs a) {
         const int kvh = u.head;
         const uint8_t* kbase = a.kv.k + (int64_t)kvh * a.kv.sb_head;
         const uint8_t* vbase = a.kv.v + (int64_t)kvh * a.kv.sb_head;
-        const float* ksb = F8 ? a.kv.ks + (int64_t)kvh * a.kv.ss_head : nullptr;
-        const float* vsb = F8 ? a.kv.vs + (int64_t)kvh * a.kv.ss_head : nullptr;
+        const float* ksb = RS ? a.kv.ks + (int64_t)kvh * a.kv.ss_head : nullptr;
+        const float* vsb = RS ? a.kv.vs + (int64_t)kvh * a.kv.ss_head : nullptr;
+        const uint8_t* kbb = F4 ? a.kv.kb + (int64_t)kvh * a.kv.sk_head : nullptr;
+        const uint8_t* vbb = F4 ? a.kv.vb + (int64_t)kvh * a.kv.sk_head : nullptr;
 
         // positions of the tile's rows: a row per lane, then what every lane needs of them
         int rpos = INT_MIN, pmin = INT_MAX, pmax = INT_MIN, rtok = 0;
@@ -197,7 +207,7 @@ attn_rows_kernel(AttnPagedArgs a) {
         // this warp's groups of 32 keys: 32 (warp + kWarps i)
         const int n_st = max(0, (n_keys - 32 * warp + 32 * kWarps - 1) / (32 * kWarps));
         auto lookup = [&](int i) {
-            Info f{-1, 0, INT_MAX};
+            Info f{-1, 0, 0, INT_MAX, 0u};
             const int v = 32 * (warp + kWarps * i) + lane;
             if (v < n_keys) {
                 const KeyAt k = key_at(a, u, u.v0 + v);
@@ -205,7 +215,11 @@ attn_rows_kernel(AttnPagedArgs a) {
                 if (k.off >= 0 && sees(k.pos, pmax, hid_min, a.n_sink)) {
                     f.off = k.off;
                     f.soff = k.soff;
+                    f.boff = k.boff;
                     f.pos = k.pos;
+                    if constexpr (F4 && C::NB == 2)
+                        f.blk = *reinterpret_cast<const uint16_t*>(kbb + k.boff) |
+                                (uint32_t)*reinterpret_cast<const uint16_t*>(vbb + k.boff) << 16;
                 }
             }
             return f;
@@ -224,10 +238,24 @@ attn_rows_kernel(AttnPagedArgs a) {
                 s_off[warp][lane] = f.off >= 0 ? f.off : 0;
                 reinterpret_cast<int*>(st + C::META)[lane] = f.pos;
                 if (lane == 0) *reinterpret_cast<unsigned*>(st + C::META + 128) = read;
-                if constexpr (F8) {
+                if constexpr (RS) {
                     const int64_t so = f.off >= 0 ? f.soff : 0;
                     fetch4z(sa + C::META + 144 + 4 * lane, ksb + so, f.off >= 0);
                     fetch4z(sa + C::META + 272 + 4 * lane, vsb + so, f.off >= 0);
+                }
+                if constexpr (F4 && C::NB == 2) {
+                    reinterpret_cast<uint16_t*>(st + C::BLK)[lane] = (uint16_t)f.blk;
+                    reinterpret_cast<uint16_t*>(st + C::BLK)[32 + lane] = (uint16_t)(f.blk >> 16);
+                } else if constexpr (F4) {
+                    const int64_t bo = f.off >= 0 ? f.boff : 0;
+                    const uint32_t kd = sa + C::BLK + C::NB * lane, vd = kd + 32 * C::NB;
+                    if constexpr (C::NB == 8) {
+                        fetch8z(kd, kbb + bo, f.off >= 0);
+                        fetch8z(vd, vbb + bo, f.off >= 0);
+                    } else {
+                        fetch4z(kd, kbb + bo, f.off >= 0);
+                        fetch4z(vd, vbb + bo, f.off >= 0);
+                    }
                 }
                 __syncwarp();
                 constexpr int LPR = C::ROWB / 16, RPI = 32 / LPR;   // lanes per row, rows per copy
@@ -275,7 +303,7 @@ attn_rows_kernel(AttnPagedArgs a) {
                 const int64_t qo = (int64_t)tok * a.q_tok + (int64_t)(kvh * a.G + row % a.G) * a.q_head;
 #pragma unroll
                 for (int s = 0; s < C::KS; ++s) {
-                    const int d = !F8 ? 32 * (s / 2) + 8 * c + 4 * (s % 2)
+                    const int d = F4 ? (HD / 4) * c + 4 * s : !F8 ? 32 * (s / 2) + 8 * c + 4 * (s % 2)
                                 : HD >= 64 ? 64 * (s / 4) + 16 * c + 4 * (s % 4) : 8 * c + 4 * s;
                     if constexpr (QT == W_F32) {
                         const float4 f = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + qo + d);
@@ -345,7 +373,7 @@ attn_rows_kernel(AttnPagedArgs a) {
         // m + log2 E. E stays within 2^-80 .. 2^80, so that weights in its units neither pass float32 nor vanish: below, the
         // unit is done key by key, above, values that f16 does not hold send it there.
         constexpr float kMinE = 0x1p-80f, kMaxE = 0x1p80f;
-        float E[F8 ? R : 1][2] = {}, mE[F8 ? R : 1][2] = {};
+        float E[RS ? R : 1][2] = {}, mE[RS ? R : 1][2] = {};
         float least = 0.f;                                  // the least E of the lane's rows
         bool lost = false;                                  // E too small, or mE not exact (scores past 2^24)
 
@@ -368,6 +396,22 @@ attn_rows_kernel(AttnPagedArgs a) {
                         const int at = 4 * C::KC * (4 * i + c);   // byte of the row
                         take<C::KC>(&k[b][t][C::KC * i], st + at16<C::ROWB>(16 * b + 8 * t + g, at >> 4) + (at & 15));
                     }
+            uint32_t kbs[2][2][2], kh[2][2][4];             // E2M1: scales of the lane's blocks, as f16 pairs; a word's values
+            if constexpr (F4) {
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const uint8_t* p = st + C::BLK + C::NB * (16 * b + 8 * t + g);
+                        if constexpr (C::NB == 8) {
+                            const uint32_t h = e4m3x2_to_h2(reinterpret_cast<const uint16_t*>(p)[c]);
+                            kbs[b][t][0] = __byte_perm(h, h, 0x1010);
+                            kbs[b][t][1] = __byte_perm(h, h, 0x3232);
+                        } else {
+                            kbs[b][t][0] = e4m3x2_to_h2(0x101u * p[C::NB == 4 ? c : c >> 1]);
+                        }
+                    }
+            }
             issue();
             if (read == 0u) continue;
             // S[b][r][2 h + e] is key 16 b + 8 h + g, row 8 r + 2 c + e
@@ -378,13 +422,24 @@ attn_rows_kernel(AttnPagedArgs a) {
                 for (int r = 0; r < R; ++r) S[b][r][0] = S[b][r][1] = S[b][r][2] = S[b][r][3] = 0.f;
 #pragma unroll
             for (int i = 0; i < C::KP; ++i) {
-                constexpr int PER = F8 ? C::KC : C::KC / 2;  // k-steps of a piece
+                constexpr int PER = F4 ? 2 * C::KC : F8 ? C::KC : C::KC / 2;   // k-steps of a piece
 #pragma unroll
                 for (int j = 0; j < PER; ++j)
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
                         uint32_t ka[4];
-                        if constexpr (F8) {
+                        if constexpr (F4) {
+                            // two k-steps to a word of eight codes: f16 values times their block's scale
+                            if (j % 2 == 0) {
+                                e2m1x8_to_h2(k[b][0][j / 2], kh[b][0]);
+                                e2m1x8_to_h2(k[b][1][j / 2], kh[b][1]);
+                            }
+                            const int y = C::NB == 8 ? j / 4 : 0;   // (32 dims of a lane: two blocks)
+                            ka[0] = mul_h2(kh[b][0][2 * (j % 2)], kbs[b][0][y]);
+                            ka[1] = mul_h2(kh[b][1][2 * (j % 2)], kbs[b][1][y]);
+                            ka[2] = mul_h2(kh[b][0][2 * (j % 2) + 1], kbs[b][0][y]);
+                            ka[3] = mul_h2(kh[b][1][2 * (j % 2) + 1], kbs[b][1][y]);
+                        } else if constexpr (F8) {
                             e4m3x4_to_h2(k[b][0][C::KC * i + j], ka[0], ka[2]);
                             e4m3x4_to_h2(k[b][1][C::KC * i + j], ka[1], ka[3]);
                         } else {
@@ -410,12 +465,12 @@ attn_rows_kernel(AttnPagedArgs a) {
             for (int b = 0; b < 2; ++b)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const float ks = F8 ? sc[16 * b + 8 * h + g] : 1.f;
-                    vs[b][h] = F8 ? sc[32 + 16 * b + 8 * h + g] : 1.f;
+                    const float ks = RS ? sc[16 * b + 8 * h + g] : 1.f;
+                    vs[b][h] = RS ? sc[32 + 16 * b + 8 * h + g] : 1.f;
 #pragma unroll
                     for (int r = 0; r < R; ++r)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) S[b][r][2 * h + e] *= F8 ? rs[r][e] * ks : rs[r][e];
+                        for (int e = 0; e < 2; ++e) S[b][r][2 * h + e] *= RS ? rs[r][e] * ks : rs[r][e];
                     if (!open) {
                         const int kp = kpos[16 * b + 8 * h + g];
 #pragma unroll
@@ -434,9 +489,9 @@ attn_rows_kernel(AttnPagedArgs a) {
                     raise = raise || mx[r][e] > m[r][e] + 14.f;
                 }
             // (scales above that of some row: whether it sees them, and whether they are of zeros, is looked into below)
-            if constexpr (F8) raise = raise || fmaxf(fmaxf(vs[0][0], vs[0][1]), fmaxf(vs[1][0], vs[1][1])) > least;
+            if constexpr (RS) raise = raise || fmaxf(fmaxf(vs[0][0], vs[0][1]), fmaxf(vs[1][0], vs[1][1])) > least;
             if (__any_sync(0xffffffffu, raise)) {
-                if constexpr (F8) {
+                if constexpr (RS) {
                     if (__any_sync(0xffffffffu, vs[0][0] == 1.f || vs[0][1] == 1.f || vs[1][0] == 1.f || vs[1][1] == 1.f)) {
                         // rows of zeros? (key `lane` of the stage)
                         uint32_t bits = 0u;
@@ -445,7 +500,7 @@ attn_rows_kernel(AttnPagedArgs a) {
                             const uint4 x = *reinterpret_cast<const uint4*>(st + 32 * C::ROWB + at16<C::ROWB>(lane, ch));
                             bits |= x.x | x.y | x.z | x.w;
                         }
-                        const unsigned zero = __ballot_sync(0xffffffffu, (bits & 0x7f7f7f7fu) == 0u);
+                        const unsigned zero = __ballot_sync(0xffffffffu, (bits & (F4 ? 0x77777777u : 0x7f7f7f7fu)) == 0u);
 #pragma unroll
                         for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -464,11 +519,11 @@ attn_rows_kernel(AttnPagedArgs a) {
                             mx[r][e] = fmaxf(mx[r][e], __shfl_xor_sync(0xffffffffu, mx[r][e], o));
                         f[e] = 1.f;
                         if (mx[r][e] > m[r][e] + 14.f) {    // true from nothing too
-                            const float to = F8 ? floorf(mx[r][e] - 6.f) : mx[r][e] - 6.f;
+                            const float to = RS ? floorf(mx[r][e] - 6.f) : mx[r][e] - 6.f;
                             f[e] = ex2(m[r][e] - to);       // 0 from nothing
                             m[r][e] = to;
                         }
-                        if constexpr (F8) {
+                        if constexpr (RS) {
                             float em = 0.f;                 // the largest scale that the row sees here
 #pragma unroll
                             for (int b = 0; b < 2; ++b)
@@ -503,8 +558,8 @@ attn_rows_kernel(AttnPagedArgs a) {
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 // (nothing seen yet: scores of -inf, or NaN, which has to show)
-                const float m0 = m[r][0] == -INFINITY ? 0.f : F8 ? mE[F8 ? r : 0][0] : m[r][0];
-                const float m1 = m[r][1] == -INFINITY ? 0.f : F8 ? mE[F8 ? r : 0][1] : m[r][1];
+                const float m0 = m[r][0] == -INFINITY ? 0.f : RS ? mE[RS ? r : 0][0] : m[r][0];
+                const float m1 = m[r][1] == -INFINITY ? 0.f : RS ? mE[RS ? r : 0][1] : m[r][1];
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -512,7 +567,7 @@ attn_rows_kernel(AttnPagedArgs a) {
                         float p0 = ex2(S[b][r][2 * h] - m0), p1 = ex2(S[b][r][2 * h + 1] - m1);
                         l[r][0] += p0;
                         l[r][1] += p1;
-                        if constexpr (F8) { p0 *= vs[b][h]; p1 *= vs[b][h]; }
+                        if constexpr (RS) { p0 *= vs[b][h]; p1 *= vs[b][h]; }
                         if constexpr (C::SPLIT_P) {
                             uint32_t hi, lo;
                             split2<BF>(p0, p1, hi, lo);
@@ -537,14 +592,40 @@ attn_rows_kernel(AttnPagedArgs a) {
                 for (int p = 0; p < C::VH; ++p) {
                     uint32_t vr[4][C::VW];                  // keys 16 b + 2c, 2c + 1, 2c + 8, 2c + 9
                     const int at = 4 * C::VW * (8 * p + g);
+                    if constexpr (F4 && HD == 32) {         // (half a word)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            vr[e][0] = *reinterpret_cast<const uint16_t*>(
+                                st + 32 * C::ROWB + 2 * g + at16<C::ROWB>(16 * b + 2 * c + (e & 1) + 8 * (e >> 1), 0));
+                    } else
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         take<C::VW>(vr[e], st + 32 * C::ROWB + (at & 15) +
                                                at16<C::ROWB>(16 * b + 2 * c + (e & 1) + 8 * (e >> 1), at >> 4));
+                    uint32_t s01 = 0u, s23 = 0u;            // E2M1: the lane's block scales of keys 0, 1 and of 2, 3
+                    if constexpr (F4) {
+                        const uint8_t* p = st + C::BLK + C::NB * (32 + 16 * b + 2 * c) + g * C::NB / 8;
+                        s01 = e4m3x2_to_h2(p[0] | (uint32_t)p[C::NB] << 8);
+                        s23 = e4m3x2_to_h2(p[8 * C::NB] | (uint32_t)p[9 * C::NB] << 8);
+                    }
 #pragma unroll
                     for (int w = 0; w < C::VW; ++w) {
                         const uint32_t w0 = vr[0][w], w1 = vr[1][w], w2 = vr[2][w], w3 = vr[3][w];
-                        if constexpr (F8) {
+                        if constexpr (F4) {
+                            // bytes of two keys' codes of one dim: even dims, odd dims
+                            constexpr uint32_t lo = 0x0f0f0f0fu;
+                            uint32_t h[4][4];
+                            e2m1x8_to_h2((w0 & lo) | (w1 << 4 & ~lo), h[0]);
+                            e2m1x8_to_h2((w0 >> 4 & lo) | (w1 & ~lo), h[1]);
+                            e2m1x8_to_h2((w2 & lo) | (w3 << 4 & ~lo), h[2]);
+                            e2m1x8_to_h2((w2 >> 4 & lo) | (w3 & ~lo), h[3]);
+#pragma unroll
+                            for (int i = 0; i < (HD == 32 ? 2 : 4); ++i) {
+                                const uint32_t va[4] = {mul_h2(h[0][i], s01), mul_h2(h[1][i], s01), mul_h2(h[2][i], s23),
+                                                        mul_h2(h[3][i], s23)};
+                                pv(4 * w + i, va);
+                            }
+                        } else if constexpr (F8) {
                             uint32_t a0[4], a1[4];
                             e4m3x4_to_h2(__byte_perm(w0, w1, 0x5140), a0[0], a0[1]);
                             e4m3x4_to_h2(__byte_perm(w2, w3, 0x5140), a0[2], a0[3]);
@@ -569,8 +650,8 @@ attn_rows_kernel(AttnPagedArgs a) {
         for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float unit = F8 && E[F8 ? r : 0][e] > 0.f ? E[F8 ? r : 0][e] : 1.f;
-                if constexpr (F8) l[r][e] *= unit;
+                const float unit = RS && E[RS ? r : 0][e] > 0.f ? E[RS ? r : 0][e] : 1.f;
+                if constexpr (RS) l[r][e] *= unit;
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) l[r][e] += __shfl_xor_sync(0xffffffffu, l[r][e], o);
                 const int row = 8 * r + 2 * c + e;
@@ -580,7 +661,7 @@ attn_rows_kernel(AttnPagedArgs a) {
                 for (int t = 0; t < C::MT; ++t)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const float o = F8 ? O[r][t][2 * h + e] * unit : O[r][t][2 * h + e];
+                        const float o = RS ? O[r][t][2 * h + e] * unit : O[r][t][2 * h + e];
                         finite = finite && fabsf(o) <= 3.0e38f;
                         const int i = 2 * t + h;            // the lane's i-th dim
                         s_o[warp][row][(i / C::VP) * 8 * C::VP + C::VP * g + i % C::VP] = o;
@@ -732,6 +813,10 @@ bool go_types(const AttnPagedArgs& a, cudaStream_t st) {
     if (a.kv.type == W_F16)
         return a.q_type == W_F16 ? go<HD, W_F16, W_F16, ROWS>(a, st) : go<HD, W_F16, W_F32, ROWS>(a, st);
     if (a.kv.type == W_BF16) return go<HD, W_BF16, W_BF16, ROWS>(a, st);
+    if (a.kv.type == W_F4) {
+        if (a.q_type == W_F16) return go<HD, W_F4, W_F16, ROWS>(a, st);
+        return a.q_type == W_BF16 ? go<HD, W_F4, W_BF16, ROWS>(a, st) : go<HD, W_F4, W_F32, ROWS>(a, st);
+    }
     if (a.q_type == W_F16) return go<HD, W_F8, W_F16, ROWS>(a, st);
     return a.q_type == W_BF16 ? go<HD, W_F8, W_BF16, ROWS>(a, st) : go<HD, W_F8, W_F32, ROWS>(a, st);
 }
@@ -750,7 +835,7 @@ bool go_rows(const AttnPagedArgs& a, cudaStream_t st) {
 bool attn_paged_types_ok(int32_t q, int32_t kv) {
     if (kv == W_F16) return q == W_F16 || q == W_F32;
     if (kv == W_BF16) return q == W_BF16;
-    return kv == W_F8 && (q == W_F16 || q == W_BF16 || q == W_F32);
+    return (kv == W_F8 || kv == W_F4) && (q == W_F16 || q == W_BF16 || q == W_F32);
 }
 
 bool launch_attn_paged(const AttnPagedArgs& a, cudaStream_t st) {

@@ -41,9 +41,19 @@ __device__ __forceinline__ void e4m3x4_to_h2(uint32_t four, uint32_t& lo, uint32
         : "=r"(lo), "=r"(hi) : "r"(four));
 }
 
-// A key of a unit: its cell as byte and scale offsets (without the head) and number, its position. off < 0: a cell
-// outside the cache.
-struct KeyAt { int64_t off, soff; int pos, cell; };
+// E2M1 codes of eight values, the least significant first, to four f16 pairs (exact)
+__device__ __forceinline__ void e2m1x8_to_h2(uint32_t w, uint32_t* h) {
+    asm("{\n .reg .b8 b0, b1, b2, b3;\n mov.b32 {b0, b1, b2, b3}, %4;\n cvt.rn.f16x2.e2m1x2 %0, b0;\n cvt.rn.f16x2.e2m1x2 %1, b1;\n"
+        " cvt.rn.f16x2.e2m1x2 %2, b2;\n cvt.rn.f16x2.e2m1x2 %3, b3;\n}\n" : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(w));
+}
+__device__ __forceinline__ uint32_t mul_h2(uint32_t x, uint32_t y) {
+    const __half2 z = __hmul2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
+    return *reinterpret_cast<const uint32_t*>(&z);
+}
+
+// A key of a unit: its cell as byte, scale and block-scale offsets (without the head) and number, its position.
+// off < 0: a cell outside the cache.
+struct KeyAt { int64_t off, soff, boff; int pos, cell; };
 
 __device__ __forceinline__ KeyAt key_at(const AttnPagedArgs& a, const AttnUnit& u, int v) {
     const int j = v < u.n_sink_keys ? v : v - u.n_sink_keys + u.key_lo;
@@ -59,11 +69,12 @@ __device__ __forceinline__ KeyAt key_at(const AttnPagedArgs& a, const AttnUnit& 
     k.cell = page * ps + at;
     if ((unsigned)page >= (unsigned)a.kv.n_pages) {
         if (a.err) atomicOr(a.err, ERR_SLOT_RANGE);
-        k.off = k.soff = -1;
+        k.off = k.soff = k.boff = -1;
         k.pos = INT_MAX;
     } else {
         k.off = (int64_t)page * a.kv.sb_page + (int64_t)at * a.kv.sb_cell;
         k.soff = (int64_t)page * a.kv.ss_page + (int64_t)at * a.kv.ss_cell;
+        k.boff = (int64_t)page * a.kv.sk_page + (int64_t)at * a.kv.sk_cell;
     }
     return k;
 }
@@ -155,8 +166,14 @@ __device__ __forceinline__ void store_out32(const AttnPagedArgs& a, int64_t i, c
     }
 }
 
-// One value of a cached row as float32.
-__device__ __forceinline__ float kv_value(const AttnPagedArgs& a, const uint8_t* row, float s, int d) {
+// One value of a cached row as float32; blk: its block scales (F4_E2M1).
+__device__ __forceinline__ float kv_value(const AttnPagedArgs& a, const uint8_t* row, const uint8_t* blk, float s, int d) {
+    if (a.kv.type == W_F4) {
+        uint32_t h[4];
+        e2m1x8_to_h2((uint32_t)row[d >> 1] >> (4 * (d & 1)), h);
+        const uint32_t b = e4m3x2_to_h2(blk[d / kF4Block]);
+        return s * __half2float(__ushort_as_half((unsigned short)(mul_h2(h[0], b) & 0xffffu)));
+    }
     if (a.kv.type == W_F16) return __half2float(reinterpret_cast<const __half*>(row)[d]);
     if (a.kv.type == W_BF16) return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(row)[d]);
     const uint32_t h = e4m3x2_to_h2(row[d]);
@@ -186,14 +203,16 @@ __device__ __noinline__ void careful_row(const AttnPagedArgs& a, const AttnUnit&
         if (k.off < 0 || !sees(k.pos, p, hid, a.n_sink)) continue;
         const uint8_t* kr = a.kv.k + k.off + kvh * a.kv.sb_head;
         const uint8_t* vr = a.kv.v + k.off + kvh * a.kv.sb_head;
+        const uint8_t* kb = a.kv.kb + k.boff + kvh * a.kv.sk_head;
+        const uint8_t* vb = a.kv.vb + k.boff + kvh * a.kv.sk_head;
         float ks = 1.f, vs = 1.f;
-        if (a.kv.type == W_F8) {
+        if (a.kv.type == W_F8 || a.kv.type == W_F4) {
             ks = a.kv.ks[k.soff + kvh * a.kv.ss_head];
             vs = a.kv.vs[k.soff + kvh * a.kv.ss_head];
         }
         float s = 0.f;
 #pragma unroll
-        for (int d = 0; d < D; ++d) s = fmaf(q[d], kv_value(a, kr, ks, lane * D + d), s);
+        for (int d = 0; d < D; ++d) s = fmaf(q[d], kv_value(a, kr, kb, ks, lane * D + d), s);
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
         s *= a.scale_log2;
@@ -202,7 +221,7 @@ __device__ __noinline__ void careful_row(const AttnPagedArgs& a, const AttnUnit&
         const float f = m == mn ? 1.f : exp2f(m - mn), e = s == -INFINITY ? 0.f : exp2f(s - mn);
         l = l * f + e;
 #pragma unroll
-        for (int d = 0; d < D; ++d) o[d] = o[d] * f + e * kv_value(a, vr, vs, lane * D + d);
+        for (int d = 0; d < D; ++d) o[d] = o[d] * f + e * kv_value(a, vr, vb, vs, lane * D + d);
         m = mn;
     }
 }

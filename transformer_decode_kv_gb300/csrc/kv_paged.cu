@@ -7,6 +7,13 @@
 // range (E4M3 has 4 significant bits). A free scale (max|x| / 448) would use at most one more of the format's
 // 18 binades and would add a rounding in each direction.
 //
+// F4_E2M1 rows carry such a scale too, the least with max|x| / s <= 2688 = 6 * 448, and an E4M3 scale b per 16 values: the
+// nearest to max|x / s| / 6 of the block. A code is the E2M1 value nearest to x / (s b). Two quotients round before the
+// conversion does, and neither moves a value over a border: a border is 6 m or m b, m a midpoint, of a few significant bits, so a
+// float32 number that is not on it is a whole step of float32 away, and at the quotient's size that is more than half of one.
+// The quotients by b are correctly rounded with r = 1 / b (rounded once per block) and an exact remainder: q0 = y r,
+// q = q0 + (y - q0 b) r (P. Markstein's theorem, IBM J. Res. Dev. 34, 1990).
+//
 // Both kernels move every byte once. 8192 rows of K and V (8 heads of 128, bf16 values, E4M3 cache), stored and read back,
 // take 23.8 us for 101 MB (4.3 TB/s; 15.0 us at the card's copy rate): a step's few rows are bound by the launch,
 // large calls by what a row costs beside its bytes (its place: two quotients and 64-bit addresses). So a thread
@@ -95,6 +102,26 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t two) {
     return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
+// four pairs of E2M1 codes (nearest even, saturating to +-6) and back
+__device__ __forceinline__ uint32_t to_e2m1x8(const float* x) {
+    uint32_t r;
+    asm("{\n .reg .b8 b0, b1, b2, b3;\n cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n mov.b32 %0, {b0, b1, b2, b3};\n}\n"
+        : "=r"(r) : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+    return r;
+}
+__device__ __forceinline__ void from_e2m1x8(uint32_t w, float s, float* x) {
+    uint32_t h[4];
+    asm("{\n .reg .b8 b0, b1, b2, b3;\n mov.b32 {b0, b1, b2, b3}, %4;\n cvt.rn.f16x2.e2m1x2 %0, b0;\n cvt.rn.f16x2.e2m1x2 %1, b1;\n"
+        " cvt.rn.f16x2.e2m1x2 %2, b2;\n cvt.rn.f16x2.e2m1x2 %3, b3;\n}\n" : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(w));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+        x[2 * i] = f.x * s;
+        x[2 * i + 1] = f.y * s;
+    }
+}
+
 // A thread's part of a row, and where the row goes; rows in the order token, K or V, head. cell -1: nothing to do.
 struct RowAt {
     int64_t dense;                                          // first value of the thread's part in the buffers
@@ -133,12 +160,17 @@ __device__ __forceinline__ float* scale_ptr(const PagedKv& kv, const RowAt& r) {
     return (r.v ? kv.vs : kv.ks) + (int64_t)r.page * kv.ss_page + r.at * kv.ss_cell + r.g * kv.ss_head;
 }
 
+__device__ __forceinline__ uint8_t* block_ptr(const PagedKv& kv, const RowAt& r) {
+    return (r.v ? kv.vb : kv.kb) + (int64_t)r.page * kv.sk_page + r.at * kv.sk_cell + r.g * kv.sk_head + r.part;
+}
+
 template <int HD, int CT, int T>
 __global__ void __launch_bounds__(kThr) kv_store_kernel(KvRowsArgs a) {
     const RowAt r = row_at<HD>(a);
     float x[kVals] = {};
     if (r.cell >= 0) load_vals<T>(r.v ? a.v : a.k, r.dense, x);
-    if constexpr (CT == W_F8) {
+    if constexpr (CT == W_F8 || CT == W_F4) {
+        float bmax = 0.f;                                   // of the thread's part
         auto row_max = [&](bool finite) {
             float m = 0.f;                                  // (fmaxf passes over NaN)
 #pragma unroll
@@ -146,6 +178,7 @@ __global__ void __launch_bounds__(kThr) kv_store_kernel(KvRowsArgs a) {
                 const float f = fabsf(x[e]);
                 if (!finite || f <= FLT_MAX) m = fmaxf(m, f);
             }
+            bmax = m;
 #pragma unroll
             for (int o = HD / kVals / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
             return m;
@@ -153,6 +186,28 @@ __global__ void __launch_bounds__(kThr) kv_store_kernel(KvRowsArgs a) {
         float amax = row_max(false);
         if (__any_sync(0xffffffffu, amax > FLT_MAX)) amax = row_max(true);
         if (r.cell < 0) return;
+        if constexpr (CT == W_F4) {
+            // 2688 = 1.3125 * 2^11
+            const uint32_t a2 = __float_as_uint(amax);
+            int e = (int)(a2 >> 23) - 127 - 11 + ((a2 & 0x7fffffu) > 0x280000u);
+            e = amax == 0.f ? 0 : max(e, -126);
+            const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+            uint32_t bc = to_e4m3x2(fmaxf(__fdiv_rn(bmax * inv, 6.f), 0x1p-9f), 0.f);
+            const float b = from_e4m3x2(bc).x, rb = __frcp_rn(b);
+            bool nan = false;
+#pragma unroll
+            for (int i = 0; i < kVals; ++i) {
+                nan = nan || x[i] != x[i];
+                // (infinities become 2^12, which is above 6 b: no remainder of theirs is taken)
+                const float y = fminf(fmaxf(x[i] * inv, -0x1p12f), 0x1p12f), q0 = y * rb;
+                x[i] = copysignf(fmaf(fmaf(-q0, b, y), rb, q0), x[i]);
+            }
+            if (nan) bc = 0x7fu;                            // there is no code for NaN: the block is
+            *reinterpret_cast<uint2*>(row_ptr(a.kv, r) + r.part * (kVals / 2)) = make_uint2(to_e2m1x8(x), to_e2m1x8(x + 8));
+            *block_ptr(a.kv, r) = (uint8_t)bc;
+            if (r.part == 0) *scale_ptr(a.kv, r) = __uint_as_float((uint32_t)(e + 127) << 23);
+            return;
+        }
         // 448 = 1.75 * 2^8: e = exponent(amax) - 8, one more above a mantissa of 1.75
         const uint32_t b = __float_as_uint(amax);
         int e = (int)(b >> 23) - 127 - 8 + ((b & 0x7fffffu) > 0x600000u);
@@ -186,6 +241,15 @@ __global__ void __launch_bounds__(kThr) kv_load_kernel(KvRowsArgs a) {
             x[4 * i + 2] = f1.x * s;
             x[4 * i + 3] = f1.y * s;
         }
+    } else if constexpr (CT == W_F4) {
+        const uint2 u = *reinterpret_cast<const uint2*>(row_ptr(a.kv, r) + r.part * (kVals / 2));
+        const float2 b = from_e4m3x2(*block_ptr(a.kv, r));
+        const float s = *scale_ptr(a.kv, r);
+        // (the product with b is exact; with s it rounds where a value is below float32's normal range)
+        from_e2m1x8(u.x, b.x, x);
+        from_e2m1x8(u.y, b.x, x + 8);
+#pragma unroll
+        for (int i = 0; i < kVals; ++i) x[i] *= s;
     } else {
         load_vals<CT>(row_ptr(a.kv, r), r.part * kVals, x);
     }
@@ -216,6 +280,7 @@ bool go_ct(const KvRowsArgs& a, bool store, cudaStream_t st) {
         case W_F16: return go_t<HD, W_F16>(a, store, st);
         case W_BF16: return go_t<HD, W_BF16>(a, store, st);
         case W_F8: return go_t<HD, W_F8>(a, store, st);
+        case W_F4: return go_t<HD, W_F4>(a, store, st);
     }
     return false;
 }

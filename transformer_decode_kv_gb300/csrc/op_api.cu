@@ -17,7 +17,7 @@
 
 using namespace llm;
 
-static_assert(W_F8 == LLM_TYPE_F8_E4M3, "type numbers");
+static_assert(W_F8 == LLM_TYPE_F8_E4M3 && W_F4 == LLM_TYPE_F4_E2M1, "type numbers");
 
 namespace {
 
@@ -64,7 +64,9 @@ int device_of(const void* p, const char* name, int* dev) {
     return 0;
 }
 
-int32_t esize(int32_t t) { return t == LLM_TYPE_F32 ? 4 : t == LLM_TYPE_F8_E4M3 ? 1 : 2; }
+// (F4_E2M1: of two codes)
+int32_t esize(int32_t t) { return t == LLM_TYPE_F32 ? 4 : t == LLM_TYPE_F8_E4M3 || t == LLM_TYPE_F4_E2M1 ? 1 : 2; }
+bool scaled_type(int32_t t) { return t == LLM_TYPE_F8_E4M3 || t == LLM_TYPE_F4_E2M1; }
 bool act_type(int32_t t) { return t == LLM_TYPE_F32 || t == LLM_TYPE_F16 || t == LLM_TYPE_BF16; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
@@ -90,8 +92,8 @@ bool strides_ok(const int64_t* stride, const int64_t* n, int dims, int64_t row, 
 
 const char* kv_shape_fault(const llm_kv_pages* kv) {
     if (!kv) return "NULL cache";
-    if (kv->type != LLM_TYPE_F16 && kv->type != LLM_TYPE_BF16 && kv->type != LLM_TYPE_F8_E4M3)
-        return "a paged cache is F16, BF16 or F8_E4M3";
+    if (kv->type != LLM_TYPE_F16 && kv->type != LLM_TYPE_BF16 && !scaled_type(kv->type))
+        return "a paged cache is F16, BF16, F8_E4M3 or F4_E2M1";
     if (kv->head_dim != 32 && kv->head_dim != 64 && kv->head_dim != 128) return "head_dim must be 32, 64 or 128";
     if (kv->n_head_kv < 1 || kv->n_head_kv > 1024) return "n_head_kv out of range";
     if (kv->page_size < 1 || kv->n_pages < 1) return "page_size and n_pages must be positive";
@@ -105,14 +107,23 @@ const char* kv_fault(const llm_kv_pages* kv) {
     if (!aligned16(kv->k) || !aligned16(kv->v)) return "cache rows must start on 16-byte boundaries";
     const int64_t n[3] = {kv->n_pages, kv->page_size, kv->n_head_kv};
     const int64_t s[3] = {kv->stride_page, kv->stride_cell, kv->stride_head};
-    if (!strides_ok(s, n, 3, kv->head_dim, 16 / esize(kv->type), true))
+    if (!strides_ok(s, n, 3, kv->type == LLM_TYPE_F4_E2M1 ? kv->head_dim / 2 : kv->head_dim, 16 / esize(kv->type), true))
         return "cache strides must keep rows on 16-byte boundaries and apart";
-    if (kv->type == LLM_TYPE_F8_E4M3) {
-        if (!kv->k_scale || !kv->v_scale) return "an F8_E4M3 cache needs its scales";
+    if (scaled_type(kv->type)) {
+        if (!kv->k_scale || !kv->v_scale) return "F8_E4M3 and F4_E2M1 caches need their scales";
         if ((reinterpret_cast<uintptr_t>(kv->k_scale) | reinterpret_cast<uintptr_t>(kv->v_scale)) & 3)
             return "scales must be 4-byte aligned";
         const int64_t ss[3] = {kv->sstride_page, kv->sstride_cell, kv->sstride_head};
         if (!strides_ok(ss, n, 3, 1, 1, true)) return "scale strides must keep the scales apart";
+    }
+    if (kv->type == LLM_TYPE_F4_E2M1) {
+        const int64_t row = kv->head_dim / kF4Block;
+        if (!kv->k_block || !kv->v_block) return "an F4_E2M1 cache needs its block scales";
+        if ((reinterpret_cast<uintptr_t>(kv->k_block) | reinterpret_cast<uintptr_t>(kv->v_block)) & (uintptr_t)(row - 1))
+            return "rows of block scales must start on multiples of their size";
+        const int64_t bs[3] = {kv->bstride_page, kv->bstride_cell, kv->bstride_head};
+        if (!strides_ok(bs, n, 3, row, row, true))
+            return "block-scale strides must be multiples of a row of block scales and keep the rows apart";
     }
     return nullptr;
 }
@@ -127,11 +138,17 @@ PagedKv paged_kv(const llm_kv_pages* kv) {
     p.sb_page = kv->n_pages > 1 ? kv->stride_page * es : 0;
     p.sb_cell = kv->page_size > 1 ? kv->stride_cell * es : 0;
     p.sb_head = kv->n_head_kv > 1 ? kv->stride_head * es : 0;
-    if (kv->type == LLM_TYPE_F8_E4M3) {
+    if (scaled_type(kv->type)) {
         p.ks = kv->k_scale; p.vs = kv->v_scale;
         p.ss_page = kv->n_pages > 1 ? kv->sstride_page : 0;
         p.ss_cell = kv->page_size > 1 ? kv->sstride_cell : 0;
         p.ss_head = kv->n_head_kv > 1 ? kv->sstride_head : 0;
+    }
+    if (kv->type == LLM_TYPE_F4_E2M1) {
+        p.kb = kv->k_block; p.vb = kv->v_block;
+        p.sk_page = kv->n_pages > 1 ? kv->bstride_page : 0;
+        p.sk_cell = kv->page_size > 1 ? kv->bstride_cell : 0;
+        p.sk_head = kv->n_head_kv > 1 ? kv->bstride_head : 0;
     }
     return p;
 }
@@ -139,8 +156,10 @@ PagedKv paged_kv(const llm_kv_pages* kv) {
 int kv_devices(const llm_kv_pages* kv, int* dev) {
     int r = device_of(kv->k, "k", dev);
     if (!r) r = device_of(kv->v, "v", dev);
-    if (!r && kv->type == LLM_TYPE_F8_E4M3) r = device_of(kv->k_scale, "k_scale", dev);
-    if (!r && kv->type == LLM_TYPE_F8_E4M3) r = device_of(kv->v_scale, "v_scale", dev);
+    if (!r && scaled_type(kv->type)) r = device_of(kv->k_scale, "k_scale", dev);
+    if (!r && scaled_type(kv->type)) r = device_of(kv->v_scale, "v_scale", dev);
+    if (!r && kv->type == LLM_TYPE_F4_E2M1) r = device_of(kv->k_block, "k_block", dev);
+    if (!r && kv->type == LLM_TYPE_F4_E2M1) r = device_of(kv->v_block, "v_block", dev);
     return r;
 }
 
@@ -148,7 +167,7 @@ const char* attn_shape_fault(const llm_attn_shape* s, const llm_kv_pages* kv) {
     if (!s) return "NULL shape";
     if (const char* w = kv_shape_fault(kv)) return w;
     if (!act_type(s->type) || !attn_paged_types_ok(s->type, kv->type))
-        return "F16 caches take F16 or F32 activations, BF16 caches BF16, F8_E4M3 caches all three";
+        return "F16 caches take F16 or F32 activations, BF16 caches BF16, F8_E4M3 and F4_E2M1 caches all three";
     if (s->n_head < 1 || s->n_head > 1024 || s->n_head % kv->n_head_kv != 0)
         return "n_head must be a multiple of n_head_kv, at most 1024";
     if (!std::isfinite(s->scale)) return "scale must be finite";
@@ -288,7 +307,9 @@ llm_attn_plan* llm_attn_plan_init(const llm_attn_shape* s, const llm_kv_pages* k
         return nullptr;
     };
     p->shape = *s;
-    p->kv = *kv;
+    p->kv = llm_kv_pages{};                      // (fields of other types are not read)
+    p->kv.type = kv->type; p->kv.n_head_kv = kv->n_head_kv; p->kv.head_dim = kv->head_dim;
+    p->kv.page_size = kv->page_size; p->kv.n_pages = kv->n_pages;
     p->scale_log2 = (float)((s->scale == 0.f ? 1.0 / std::sqrt((double)kv->head_dim) : (double)s->scale) *
                             1.4426950408889634);
     int n_sm = 0;

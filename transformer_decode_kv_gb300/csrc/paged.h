@@ -14,6 +14,8 @@
 namespace llm {
 
 constexpr int32_t W_F8 = 100;                    // LLM_TYPE_F8_E4M3
+constexpr int32_t W_F4 = 101;                    // LLM_TYPE_F4_E2M1
+constexpr int kF4Block = 16;                     // values that share a block scale
 enum : uint32_t { ERR_PLAN_FORM = 16u };         // beside the bits of kernels.h
 
 // Allow a kernel its dynamic shared memory, once per device (`done`: a bit per device; the call costs about as much
@@ -28,13 +30,16 @@ inline bool allow_smem(const void* kernel, size_t bytes, std::atomic<uint64_t>& 
     return true;
 }
 
-// A paged cache as the kernels see it; strides in bytes (scales: elements).
+// A paged cache as the kernels see it; strides in bytes (scales: elements). A row of F4_E2M1 is hd / 2 bytes of codes, hd / 16
+// of block scales (kb, vb) and its scale.
 struct PagedKv {
     int32_t type = W_F16, Hkv = 0, hd = 0, page_size = 1, n_pages = 0;
     uint8_t *k = nullptr, *v = nullptr;
     int64_t sb_page = 0, sb_cell = 0, sb_head = 0;
     float *ks = nullptr, *vs = nullptr;
     int64_t ss_page = 0, ss_cell = 0, ss_head = 0;
+    uint8_t *kb = nullptr, *vb = nullptr;
+    int64_t sk_page = 0, sk_cell = 0, sk_head = 0;   // of the block scales
 };
 
 // Rows between dense token-major buffers and cache cells (kv_paged.cu); strides in elements.
@@ -70,7 +75,7 @@ constexpr int kUnitRows2 = 256;
 // 16-row form needs the registers.
 constexpr int kAttnRowsCtas = 2;
 constexpr int attn_rows_warps(int hd, int kv_type, int rows) {
-    return hd == 128 && kv_type != W_F8 ? 3 : rows == 8 ? 6 : 4;
+    return hd == 128 && kv_type != W_F8 && kv_type != W_F4 ? 3 : rows == 8 ? 6 : 4;
 }
 enum AttnOut : int32_t { AO_F16 = 0, AO_BF16 = 1, AO_F32 = 2, AO_BF16_PAIR = 3 };
 
