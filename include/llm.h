@@ -314,8 +314,8 @@ int32_t llm_sample_batch(llm_ctx *ctx, int32_t n, const int32_t *rows, const llm
  *     and the call returns without waiting; it allocates nothing, so it may be captured in a graph;
  *   - returns 0, -1 for arguments the call refuses (nothing is enqueued), -3 if CUDA refuses the launch;
  *   - `err`, where taken, is a device word (or NULL) that kernels OR bits into when an index they
- *     read on the device is out of range (1: a cell or page, 4: a row); the access is skipped. The
- *     caller zeroes it.
+ *     read on the device is out of range (1: a cell or page, 4: a row; the access is skipped), or 32 where lengths
+ *     or counts that they read do not fit (what then happens is said at the call). The caller zeroes it.
  * llm_op_last_error() describes the calling thread's last refused or failed operator call. */
 const char *llm_op_last_error(void);
 
@@ -355,6 +355,37 @@ int llm_kv_store(const llm_kv_pages *kv, int32_t type, const void *k, const void
 int llm_kv_load(const llm_kv_pages *kv, int32_t type, void *k, void *v,
                 int64_t stride_tok, int64_t stride_head, const int32_t *cell, int32_t n,
                 uint32_t *err, void *stream);
+
+/* The pages of n_seq sequences, for programs that hand out pages on the GPU. All arrays are device memory (int32):
+ * table [n_seq][ld_table], the pages of a sequence in order; n_kv [n_seq], the rows it holds, in its first
+ * ceil(n_kv / page_size) pages; free_pages [max_free], of which the first *n_free are free, the last of them handed out
+ * first. Pages have numbers below n_pages; page_size times n_pages is below 2^31, n_seq at most 2^20. Arrays of a call must
+ * not overlap but where this says so. Both calls below leave the same result however they are run. */
+typedef struct llm_seq_pages {
+    int32_t n_seq, page_size, n_pages, ld_table, max_free;
+    int32_t *table, *n_kv, *free_pages, *n_free;
+} llm_seq_pages;
+
+/* Room for new tokens: sequence s gets n_new[s] of them behind its n_kv[s] rows, with pages from the stack where it
+ * reaches new ones (the stack's last page to the first sequence's first new page, and so on; their table entries are
+ * written). For the tokens of all sequences one after the other, start[s] (start [n_seq + 1]) is the first of sequence s and
+ * start[n_seq] their number; cell[i] is the cell of token i (see llm_kv_store) and pos[i] its position (cell and pos
+ * [max_tok], -1 behind the last token, so that a store of max_tok rows skips what is padding). n_kv_out [n_seq] and
+ * n_free_out receive the new lengths and the stack's new size; they may be n_kv and n_free. max_tok is at most 2^24.
+ * All or nothing: where a length is negative, a sequence would pass ld_table pages or 2^31 - 1 rows, the tokens max_tok,
+ * or the pages *n_free (or that is not in 0 .. max_free), bit 32 of err is set and the step has no tokens: start is zeros, cell and
+ * pos are -1, lengths, stack and table stay. A page outside 0 .. n_pages - 1 (in the stack, or the last one of a
+ * sequence) gives its tokens cell -1 and err bit 1. */
+int llm_pages_extend(const llm_seq_pages *p, const int32_t *n_new, int32_t *n_kv_out, int32_t *n_free_out,
+                     int32_t max_tok, int32_t *cell, int32_t *pos, int32_t *start, uint32_t *err, void *stream);
+
+/* Shorten sequences to keep[s] rows (negative: as it is; 0: the sequence is done) and put the pages that this leaves
+ * without rows on the stack, sequence by sequence, each's in table order. n_kv_out and n_free_out as above. All or nothing: where
+ * keep[s] > n_kv[s], a length is negative or needs more than ld_table pages, or the stack would pass max_free, bit
+ * 32 of err is set and nothing changes. Table entries stay as they are. A page outside 0 .. n_pages - 1 is put on the stack
+ * as it is and sets err bit 1. */
+int llm_pages_trim(const llm_seq_pages *p, const int32_t *keep, int32_t *n_kv_out, int32_t *n_free_out, uint32_t *err,
+                   void *stream);
 
 /* Attention of new tokens over a paged cache:
  *   out[i][h] = sum_j softmax_j(scale * q[i][h] . k[j][h / G]) v[j][h / G],  G = n_head / n_head_kv,

@@ -84,3 +84,38 @@ def test_python_checks_of_the_cache(B):
             B.KvPages(*args)
     with pytest.raises(TypeError):
         B.KvPages(k.half(), k.half(), s, s, b, b)
+
+
+def lists(B, **kw):
+    d = B.SeqPagesDesc()
+    base = dict(n_seq=2, page_size=16, n_pages=8, ld_table=4, max_free=8, table=PTR, n_kv=PTR, free_pages=PTR, n_free=PTR)
+    base.update(kw)
+    for n, v in base.items():
+        setattr(d, n, v)
+    return d
+
+
+@pytest.mark.parametrize("bad,why", [
+    (dict(n_seq=-1), "n_seq"), (dict(n_seq=(1 << 20) + 1), "n_seq"), (dict(page_size=0), "page_size"), (dict(n_pages=0), "n_pages"),
+    (dict(page_size=1 << 16, n_pages=1 << 15), "cells"), (dict(ld_table=-1), "ld_table"), (dict(max_free=-1), "max_free"),
+    (dict(table=None), "NULL"), (dict(n_kv=None), "NULL"), (dict(free_pages=None), "NULL"), (dict(n_free=None), "NULL"),
+    (dict(n_kv=PTR + 2), "aligned"), (dict(table=PTR + 1), "aligned")])
+def test_bad_page_lists_are_refused(B, bad, why):
+    L, d = B.lib(), lists(B, **bad)
+    assert L.llm_pages_extend(C.byref(d), PTR, PTR, PTR, 4, PTR, PTR, PTR, None, None) == -1
+    assert why in L.llm_op_last_error().decode()
+    assert L.llm_pages_trim(C.byref(d), PTR, PTR, PTR, None, None) == -1
+    assert why in L.llm_op_last_error().decode()
+
+
+@pytest.mark.parametrize("args", [
+    dict(n_new=None), dict(kv_out=None), dict(free_out=None), dict(max_tok=-1), dict(max_tok=(1 << 24) + 1), dict(cell=None),
+    dict(pos=None), dict(start=None), dict(cell=PTR + 2), dict(start=PTR + 1), dict(err=PTR + 3)])
+def test_bad_extensions_are_refused(B, args):
+    a = dict(n_new=PTR, kv_out=PTR, free_out=PTR, max_tok=4, cell=PTR, pos=PTR, start=PTR, err=None)
+    a.update(args)
+    d = lists(B)
+    assert B.lib().llm_pages_extend(C.byref(d), a["n_new"], a["kv_out"], a["free_out"], a["max_tok"], a["cell"], a["pos"], a["start"],
+                                    a["err"], None) == -1
+    assert B.lib().llm_pages_extend(None, PTR, PTR, PTR, 4, PTR, PTR, PTR, None, None) == -1
+    assert B.lib().llm_pages_trim(None, PTR, PTR, PTR, None, None) == -1

@@ -58,6 +58,13 @@ class KvPagesDesc(C.Structure):
                 ("bstride_head", C.c_int64)]
 
 
+class SeqPagesDesc(C.Structure):
+    _fields_ = [("n_seq", C.c_int32), ("page_size", C.c_int32), ("n_pages", C.c_int32),
+                ("ld_table", C.c_int32), ("max_free", C.c_int32),
+                ("table", C.c_void_p), ("n_kv", C.c_void_p), ("free_pages", C.c_void_p),
+                ("n_free", C.c_void_p)]
+
+
 class AttnShape(C.Structure):
     _fields_ = [("type", C.c_int32), ("n_head", C.c_int32), ("scale", C.c_float),
                 ("window", C.c_int32), ("n_sink", C.c_int32), ("max_tok", C.c_int32),
@@ -144,6 +151,10 @@ SIGNATURES = {
                                C.c_int64, C.c_void_p, C.c_int32, C.c_void_p, C.c_void_p]),
     "llm_kv_load": (C.c_int, [C.POINTER(KvPagesDesc), C.c_int32, C.c_void_p, C.c_void_p, C.c_int64,
                               C.c_int64, C.c_void_p, C.c_int32, C.c_void_p, C.c_void_p]),
+    "llm_pages_extend": (C.c_int, [C.POINTER(SeqPagesDesc), C.c_void_p, C.c_void_p, C.c_void_p, C.c_int32,
+                                   C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p]),
+    "llm_pages_trim": (C.c_int, [C.POINTER(SeqPagesDesc), C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
+                                 C.c_void_p]),
     "llm_attn_plan_init": (C.c_void_p, [C.POINTER(AttnShape), C.POINTER(KvPagesDesc)]),
     "llm_attn_plan_free": (None, [C.c_void_p]),
     "llm_attn_plan_set": (C.c_int, [C.c_void_p, C.c_int32, C.POINTER(C.c_int32),
@@ -394,6 +405,57 @@ def kv_load(pages: KvPages, cell, k, v, err=None, stream: Optional[int] = None) 
     """Read the rows of cells cell [n] back into k, v [n, n_head_kv, head_dim] (rows of negative cells
     are left as they were)."""
     pages._kv_rows(lib().llm_kv_load, k, v, cell, err, stream)
+
+
+class SeqPages:
+    """The pages of a step's sequences, in torch CUDA tensors (int32): table [n_seq, ld], each sequence's pages in
+    order; n_kv [n_seq], the rows it holds; free [max_free], the stack of free pages, of which the first n_free [1] count
+    (the last of them is handed out first). Pages of page_size cells, numbers below n_pages."""
+
+    def __init__(self, table, n_kv, free, n_free, page_size: int, n_pages: int):
+        if table.dim() != 2 or free.dim() != 1:
+            raise ValueError("table must be [n_seq, pages] and free [max_free]")
+        d = SeqPagesDesc()
+        d.n_seq, d.ld_table = table.shape
+        d.page_size, d.n_pages, d.max_free = page_size, n_pages, free.shape[0]
+        self.n_seq = d.n_seq
+        d.table = _need(table, "table", "int32", table.shape)
+        d.n_kv = _need(n_kv, "n_kv", "int32", (d.n_seq,))
+        d.free_pages = _need(free, "free", "int32", free.shape)
+        d.n_free = _need(n_free, "n_free", "int32", (1,))
+        self.desc, self.ref = d, C.byref(d)
+        self.table, self.n_kv, self.free, self.n_free = table, n_kv, free, n_free
+
+    def _outs(self, n_kv_out, n_free_out, err):
+        d = self.desc
+        return (d.n_kv if n_kv_out is None else _need(n_kv_out, "n_kv_out", "int32", (self.n_seq,)),
+                d.n_free if n_free_out is None else _need(n_free_out, "n_free_out", "int32", (1,)),
+                None if err is None else _need(err, "err", "int32", (1,)))
+
+
+def pages_extend(lists: SeqPages, n_new, cell, pos, start, n_kv_out=None, n_free_out=None, err=None,
+                 stream: Optional[int] = None) -> None:
+    """Room for n_new [n_seq] tokens behind the sequences' rows, with pages from the stack: cell and pos [max_tok]
+    receive the cell and position of every new token (-1 behind the last), start [n_seq + 1] the first token of each sequence,
+    n_kv_out and n_free_out (None: in place) the new lengths and the stack's size. A step that does not fit sets
+    bit 32 of err, an optional device word (int32 [1]), and has no tokens."""
+    kv_out, free_out, e = lists._outs(n_kv_out, n_free_out, err)
+    n = cell.numel()
+    r = lib().llm_pages_extend(lists.ref, _need(n_new, "n_new", "int32", (lists.n_seq,)), kv_out, free_out, n,
+                               _need(cell, "cell", "int32", (n,)), _need(pos, "pos", "int32", (n,)),
+                               _need(start, "start", "int32", (lists.n_seq + 1,)), e, _stream_of(lists.n_free, stream))
+    if r != 0:
+        _op(r)
+
+
+def pages_trim(lists: SeqPages, keep, n_kv_out=None, n_free_out=None, err=None, stream: Optional[int] = None) -> None:
+    """Shorten sequences to keep [n_seq] rows (negative: as it is) and put the pages that this leaves without rows
+    on the stack. A call that does not fit sets bit 32 of err and changes nothing."""
+    kv_out, free_out, e = lists._outs(n_kv_out, n_free_out, err)
+    r = lib().llm_pages_trim(lists.ref, _need(keep, "keep", "int32", (lists.n_seq,)), kv_out, free_out, e,
+                             _stream_of(lists.n_free, stream))
+    if r != 0:
+        _op(r)
 
 
 class AttnPlan:

@@ -259,6 +259,34 @@ int kv_rows(const llm_kv_pages* kv, int32_t type, void* k, void* v, int64_t s_to
     return 0;
 }
 
+// Checks and arguments that extending and trimming share; null pointers are for arrays without entries only.
+int seq_pages(const llm_seq_pages* p, const int32_t* per_seq, int32_t* n_kv_out, int32_t* n_free_out, uint32_t* err,
+              PageListArgs* a, int* dev) {
+    if (!p) return refuse("NULL pages");
+    if (p->n_seq < 0 || p->n_seq > (1 << 20)) return refuse("n_seq out of range");
+    if (p->page_size < 1 || p->n_pages < 1 || (int64_t)p->page_size * p->n_pages > INT32_MAX)
+        return refuse("page_size and n_pages must be positive, with fewer than 2^31 cells");
+    if (p->ld_table < 0 || p->max_free < 0) return refuse("ld_table or max_free is negative");
+    struct { const void* q; const char* name; bool need; } list[] = {
+        {p->table, "table", p->n_seq > 0 && p->ld_table > 0}, {p->n_kv, "n_kv", p->n_seq > 0},
+        {p->free_pages, "free_pages", p->max_free > 0}, {p->n_free, "n_free", true}, {per_seq, "the lengths", p->n_seq > 0},
+        {n_kv_out, "n_kv_out", p->n_seq > 0}, {n_free_out, "n_free_out", true}, {err, "err", false}};
+    for (const auto& x : list) {
+        if (x.need && !x.q) return refuse("NULL page lists or lengths");
+        if (reinterpret_cast<uintptr_t>(x.q) & 3) return refuse("page lists must be 4-byte aligned");
+    }
+    for (const auto& x : list)
+        if (x.q && (x.need || x.q == err))
+            if (const int r = device_of(x.q, x.name, dev)) return r;
+    a->n_seq = p->n_seq; a->page_size = p->page_size; a->n_pages = p->n_pages;
+    a->ld_table = p->ld_table; a->max_free = p->max_free;
+    a->table = p->table; a->n_kv = p->n_kv; a->n_new = per_seq;
+    a->free_pages = p->free_pages; a->n_free = p->n_free;
+    a->n_kv_out = n_kv_out; a->n_free_out = n_free_out;
+    a->err = err;
+    return 0;
+}
+
 }  // namespace
 
 struct llm_attn_plan {
@@ -293,6 +321,37 @@ int llm_kv_store(const llm_kv_pages* kv, int32_t type, const void* k, const void
 int llm_kv_load(const llm_kv_pages* kv, int32_t type, void* k, void* v, int64_t stride_tok, int64_t stride_head,
                 const int32_t* cell, int32_t n, uint32_t* err, void* stream) {
     return kv_rows(kv, type, k, v, stride_tok, stride_head, cell, n, err, stream, false);
+}
+
+int llm_pages_extend(const llm_seq_pages* p, const int32_t* n_new, int32_t* n_kv_out, int32_t* n_free_out, int32_t max_tok,
+                     int32_t* cell, int32_t* pos, int32_t* start, uint32_t* err, void* stream) {
+    if (max_tok < 0 || max_tok > (1 << 24)) return refuse("max_tok out of range");
+    if (!start || (max_tok > 0 && (!cell || !pos))) return refuse("NULL cell, pos or start");
+    if ((reinterpret_cast<uintptr_t>(cell) | reinterpret_cast<uintptr_t>(pos) | reinterpret_cast<uintptr_t>(start)) & 3)
+        return refuse("cell, pos and start must be 4-byte aligned");
+    PageListArgs a;
+    int dev = -1;
+    int r = seq_pages(p, n_new, n_kv_out, n_free_out, err, &a, &dev);
+    if (!r && max_tok > 0) r = device_of(cell, "cell", &dev);
+    if (!r && max_tok > 0) r = device_of(pos, "pos", &dev);
+    if (!r) r = device_of(start, "start", &dev);
+    if (r) return r;
+    a.max_tok = max_tok; a.cell = cell; a.pos = pos; a.start = start;
+    OnDevice on(dev);
+    if (!on.ok()) return failed("cudaSetDevice", cudaGetLastError());
+    if (!launch_pages_extend(a, static_cast<cudaStream_t>(stream))) return failed("pages_extend launch", cudaGetLastError());
+    return 0;
+}
+
+int llm_pages_trim(const llm_seq_pages* p, const int32_t* keep, int32_t* n_kv_out, int32_t* n_free_out, uint32_t* err,
+                   void* stream) {
+    PageListArgs a;
+    int dev = -1;
+    if (const int r = seq_pages(p, keep, n_kv_out, n_free_out, err, &a, &dev)) return r;
+    OnDevice on(dev);
+    if (!on.ok()) return failed("cudaSetDevice", cudaGetLastError());
+    if (!launch_pages_trim(a, static_cast<cudaStream_t>(stream))) return failed("pages_trim launch", cudaGetLastError());
+    return 0;
 }
 
 llm_attn_plan* llm_attn_plan_init(const llm_attn_shape* s, const llm_kv_pages* kv) {

@@ -16,7 +16,7 @@ namespace llm {
 constexpr int32_t W_F8 = 100;                    // LLM_TYPE_F8_E4M3
 constexpr int32_t W_F4 = 101;                    // LLM_TYPE_F4_E2M1
 constexpr int kF4Block = 16;                     // values that share a block scale
-enum : uint32_t { ERR_PLAN_FORM = 16u };         // beside the bits of kernels.h
+enum : uint32_t { ERR_PLAN_FORM = 16u, ERR_STEP_RANGE = 32u };   // beside the bits of kernels.h
 
 // Allow a kernel its dynamic shared memory, once per device (`done`: a bit per device; the call costs about as much
 // as a launch).
@@ -54,6 +54,21 @@ struct KvRowsArgs {
 };
 bool launch_kv_rows_store(const KvRowsArgs& a, cudaStream_t st);
 bool launch_kv_rows_load(const KvRowsArgs& a, cudaStream_t st);
+
+// Page tables of a step's sequences on the device (page_lists.cu); everything in device memory.
+struct PageListArgs {
+    int32_t n_seq = 0, page_size = 1, n_pages = 0, ld_table = 0, max_free = 0;
+    int32_t* table = nullptr;                    // [n_seq][ld_table]
+    const int32_t *n_kv = nullptr, *n_new = nullptr;   // (a trim: n_new is what to keep)
+    int32_t* free_pages = nullptr;
+    const int32_t* n_free = nullptr;
+    int32_t *n_kv_out = nullptr, *n_free_out = nullptr;   // may be n_kv and n_free
+    int32_t max_tok = 0;
+    int32_t *cell = nullptr, *pos = nullptr, *start = nullptr;
+    uint32_t* err = nullptr;
+};
+bool launch_pages_extend(const PageListArgs& a, cudaStream_t st);
+bool launch_pages_trim(const PageListArgs& a, cudaStream_t st);
 
 // One unit of attention work: rows of one tile of a sequence for one KV head against a range of the keys
 // those rows may see. A tile's rows are (token, query head) pairs of the KV head's group, row
