@@ -1200,7 +1200,7 @@ bool go_hd(const AttnPagedArgs& a, cudaStream_t st) {
 // F32 activations stay with the 16-row tiles, which carry Q and P as two terms each, unless the caller's precision is
 // that of f16 activations (round_q: the context's f16 forward passes).
 bool attn_paged_tc_ok(int32_t hd, int32_t kv_type, int32_t q_type, bool round_q) {
-    return (hd == 64 || hd == 128) && (q_type != W_F32 || round_q) && attn_paged_types_ok(q_type, kv_type);
+    return kv_type != W_F4 && (hd == 64 || hd == 128) && (q_type != W_F32 || round_q) && attn_paged_types_ok(q_type, kv_type);
 }
 
 bool launch_attn_paged_tc(const AttnPagedArgs& a, cudaStream_t st) {
