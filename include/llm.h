@@ -439,6 +439,17 @@ void llm_attn_plan_free(llm_attn_plan *plan);
  * plan then keeps what it held. */
 int llm_attn_plan_set(llm_attn_plan *plan, int32_t n_seq, const int32_t *n_new, const int32_t *n_kv,
                       const int32_t *pages, int32_t ld_pages, void *stream);
+/* The plan of a step whose lengths are on the device, with nothing for the host to wait for: start [n_seq + 1] and n_kv
+ * [n_seq], as llm_pages_extend leaves them (sequence s has start[s + 1] - start[s] new tokens, start[0] = 0, and n_kv[s] rows
+ * with the new ones), and pages [n_seq][ld_pages] are device arrays. The work is enqueued on `stream`; the arrays are free
+ * again when it has run. The call may be captured, and a graph of it, the stores and the runs follows the lengths.
+ * max_new, at most max_tok, bounds the new tokens of one sequence: 1 for a decode step. It decides which kernels
+ * the runs after this call launch (llm_attn_plan_form): give what the steps need. A step that is out of range
+ * (llm_attn_plan_set's -1, or more than max_new tokens of a sequence) sets bit 32 of the plan's error word, and the
+ * runs leave the output alone. A run of such a plan may be captured whatever the step, an empty one too; its q and out
+ * need rows for max_tok tokens. Pages outside the cache are found by the runs (bit 1; their keys are not seen). */
+int llm_attn_plan_set_device(llm_attn_plan *plan, int32_t n_seq, const int32_t *start, const int32_t *n_kv,
+                             const int32_t *pages, int32_t ld_pages, int32_t max_new, void *stream);
 /* q row (i, h) at i * q_stride_tok + h * q_stride_head elements, out likewise; 16-byte aligned rows.
  * Rows behind the last sequence's tokens are neither read nor written. out may not overlap q. */
 int llm_attn_run(llm_attn_plan *plan, const void *q, int64_t q_stride_tok, int64_t q_stride_head,

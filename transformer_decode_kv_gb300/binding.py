@@ -160,6 +160,8 @@ SIGNATURES = {
     "llm_attn_plan_set": (C.c_int, [C.c_void_p, C.c_int32, C.POINTER(C.c_int32),
                                     C.POINTER(C.c_int32), C.POINTER(C.c_int32), C.c_int32,
                                     C.c_void_p]),
+    "llm_attn_plan_set_device": (C.c_int, [C.c_void_p, C.c_int32, C.c_void_p, C.c_void_p, C.c_void_p,
+                                           C.c_int32, C.c_int32, C.c_void_p]),
     "llm_attn_run": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int64, C.c_int64,
                                C.POINTER(KvPagesDesc), C.c_void_p, C.c_int64, C.c_int64,
                                C.c_void_p]),
@@ -471,7 +473,7 @@ class AttnPlan:
             raise TypeError(f"unsupported activation type {dtype}")
         self.dtype, self.n_head, self.head_dim = dtype, n_head, pages.dim
         self.device = pages.k.device
-        self.n_tok = 0
+        self.n_tok, self.max_tok = 0, max_tok
         self._captured_rows = None          # fewest rows of q and out of the runs that were captured
         self._capturing = torch._C._cuda_isCurrentStreamCapturing if pages.k.is_cuda else (lambda: False)
         self._run = lib().llm_attn_run
@@ -507,6 +509,22 @@ class AttnPlan:
         _op(lib().llm_attn_plan_set(self.ptr, len(n_new), _ptr(n_new, C.c_int32),
                                     _ptr(n_kv, C.c_int32), _ptr(t, C.c_int32), t.shape[1], stream))
         self.n_tok = int(n_new.sum())
+
+    def set_device(self, start, n_kv, pages, max_new: int, stream: Optional[int] = None) -> None:
+        """The same from device tensors (int32), as pages_extend leaves them, without a wait: start [n_seq + 1], the
+        first new token of each sequence and their number; n_kv [n_seq], cached rows with the new ones; page table
+        [n_seq, ld]. max_new bounds a sequence's new tokens. Runs then need q and out of max_tok rows."""
+        n = n_kv.shape[0]
+        if pages.dim() != 2 or pages.shape[0] != n:
+            raise ValueError("pages must be [n_seq, n]")
+        if self._captured_rows is not None and self.max_tok > self._captured_rows:
+            raise ValueError(f"a captured run's q or out has only {self._captured_rows} rows, and a step that is set on the "
+                             f"device may have {self.max_tok} tokens")
+        ld = pages.shape[1]
+        _op(lib().llm_attn_plan_set_device(self.ptr, n, _need(start, "start", "int32", (n + 1,)),
+                                           _need(n_kv, "n_kv", "int32", (n,)), _need(pages, "pages", "int32", (n, ld)), ld,
+                                           max_new, _stream_of(start, stream)))
+        self.n_tok = self.max_tok
 
     def _captures(self, stream: Optional[int]) -> bool:
         """Whether a run on this stream (None: torch's current one) is recorded into a graph."""

@@ -25,6 +25,13 @@ constexpr int64_t kTcRows = 64;
 
 int64_t ctas(const PlanShape& s, int f) { return (int64_t)s.n_sm * (f ? 1 : kAttnRowsCtas); }
 
+// Where the 256-row form's key ranges begin: at multiples of a run of a page's cells.
+int64_t block_align(const PlanShape& s) {
+    int64_t align = 64;
+    while (align > 1 && s.page_size % align) align /= 2;
+    return align;
+}
+
 int64_t up_to(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
 // The virtual key range of the rows [row0, row0 + n) of a sequence: sink keys, then [lo, hi).
@@ -70,8 +77,7 @@ void build_paged_plan(const PlanShape& s, const std::vector<PlanSeq>& seqs, Page
     plan.rows1 = 8;
     for (const PlanSeq& q : seqs)
         if (!tc(q) && (int64_t)q.n_new * s.G > 8) plan.rows1 = 16;
-    int64_t align = 64;
-    while (align > 1 && s.page_size % align) align /= 2;
+    const int64_t align = block_align(s);
     struct Tile { int32_t seq, row0, n_row; Keys keys; };
     std::vector<Tile> tiles[2];
     int64_t total[2] = {0, 0};
@@ -161,7 +167,25 @@ PagedPlanCaps paged_plan_caps(const PlanShape& s, int32_t max_tok, int32_t max_s
     c.tickets = c.ctas1;
     c.parts1 = 2 * c.ctas1;
     c.parts2 = 2 * c.ctas2;
+    c.tiles1 = t1;
+    c.tiles2 = t2;
     return c;
+}
+
+int32_t plan_numbers(const PlanShape& s, int32_t max_new, PlanDeviceArgs& a) {
+    const int64_t rows = (int64_t)max_new * s.G;
+    a.G = s.G; a.Hkv = s.Hkv; a.window = s.window; a.n_sink = s.n_sink; a.page_size = s.page_size;
+    a.rows1 = rows <= 8 ? 8 : 16;
+    a.tc = s.tc && rows >= kTcRows;
+    a.tc_rows = (int32_t)kTcRows;
+    a.align = (int32_t)block_align(s);
+    for (int f = 0; f < 2; ++f) {
+        a.bk[f] = (int32_t)block_keys(s, f, a.rows1);
+        a.cost[f] = (int32_t)kUnitCost[f];
+        a.n_cta[f] = (int32_t)ctas(s, f);
+    }
+    a.max_new = max_new;
+    return (a.rows1 == 8 ? ATTN_FORM_ROWS8 : ATTN_FORM_ROWS16) | (a.tc ? ATTN_FORM_TC : 0);
 }
 
 }  // namespace llm

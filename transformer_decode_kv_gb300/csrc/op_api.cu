@@ -304,6 +304,11 @@ struct llm_attn_plan {
     float2* part_ml = nullptr;
     int32_t *tickets = nullptr, *redo = nullptr;
     uint32_t* err = nullptr;
+    // set from the device: the forms that the plan may then have (0: set from the host), and the scratch of making it
+    int32_t device_form = 0;
+    int32_t* lists = nullptr;
+    int64_t* tile_pre = nullptr;
+    int32_t form() const { return device_form ? device_form : plan.form(); }
     cudaEvent_t uploaded = nullptr;
     bool pending = false;
 };
@@ -397,6 +402,8 @@ llm_attn_plan* llm_attn_plan_init(const llm_attn_shape* s, const llm_kv_pages* k
     get(&p->tickets, (size_t)p->caps.tickets * sizeof(int32_t));
     get(&p->redo, (size_t)std::max<int64_t>(1, p->caps.units2) * sizeof(int32_t));
     get(&p->err, sizeof(uint32_t));
+    get(&p->lists, (3 * (size_t)s->max_seq + 2) * sizeof(int32_t));
+    get(&p->tile_pre, (size_t)(p->caps.tiles1 + p->caps.tiles2) * sizeof(int64_t));
     if (e == cudaSuccess) {
         void* h = nullptr;
         e = cudaMallocHost(&h, p->bytes);
@@ -425,6 +432,8 @@ void llm_attn_plan_free(llm_attn_plan* p) {
         cudaFree(p->tickets);
         cudaFree(p->redo);
         cudaFree(p->err);
+        cudaFree(p->lists);
+        cudaFree(p->tile_pre);
         if (p->h_buf) cudaFreeHost(p->h_buf);
         cudaGetLastError();
     }
@@ -496,6 +505,44 @@ int llm_attn_plan_set(llm_attn_plan* p, int32_t n_seq, const int32_t* n_new, con
     if (e != cudaSuccess) { cudaGetLastError(); return failed("plan upload", e); }
     p->pending = true;
     p->plan = std::move(plan);
+    p->device_form = 0;
+    return 0;
+}
+
+int llm_attn_plan_set_device(llm_attn_plan* p, int32_t n_seq, const int32_t* start, const int32_t* n_kv,
+                             const int32_t* pages, int32_t ld_pages, int32_t max_new, void* stream) {
+    if (!p) return refuse("NULL plan");
+    if (n_seq < 0 || n_seq > p->shape.max_seq) return refuse("more sequences than the plan's max_seq");
+    if (max_new < 0 || max_new > p->shape.max_tok) return refuse("max_new must be between 0 and the plan's max_tok");
+    if (ld_pages < 0) return refuse("ld_pages is negative");
+    if (!start || (n_seq > 0 && (!n_kv || (ld_pages > 0 && !pages)))) return refuse("NULL start, lengths or pages");
+    if ((reinterpret_cast<uintptr_t>(start) | reinterpret_cast<uintptr_t>(n_kv) | reinterpret_cast<uintptr_t>(pages)) & 3)
+        return refuse("start, lengths and pages must be 4-byte aligned");
+    int dev = p->device;
+    int r = device_of(start, "start", &dev);
+    if (!r && n_seq > 0) r = device_of(n_kv, "n_kv", &dev);
+    if (!r && n_seq > 0 && ld_pages > 0) r = device_of(pages, "pages", &dev);
+    if (r) return r;
+    OnDevice on(dev);
+    if (!on.ok()) return failed("cudaSetDevice", cudaGetLastError());
+    PlanDeviceArgs a;
+    const int32_t form = plan_numbers(p->ps, max_new, a);
+    a.n_seq = n_seq; a.ld_table = ld_pages;
+    a.max_tok = p->shape.max_tok; a.max_keys = kMaxKeys; a.max_table = p->shape.max_table;
+    a.start = start; a.n_kv = n_kv; a.table = pages;
+    a.hdr = reinterpret_cast<int32_t*>(p->d_buf);
+    a.cuts = reinterpret_cast<int32_t*>(p->d_buf + p->off_cuts);
+    a.table_out = reinterpret_cast<int32_t*>(p->d_buf + p->off_table);
+    for (int f = 0; f < 2; ++f) {
+        a.first[f] = reinterpret_cast<int32_t*>(p->d_buf + p->off_first[f]);
+        a.units[f] = reinterpret_cast<AttnUnit*>(p->d_buf + p->off_units[f]);
+        a.tile_base[f] = p->lists + f * ((size_t)p->shape.max_seq + 1);
+        a.tile_pre[f] = p->tile_pre + f * p->caps.tiles1;
+    }
+    a.table_off = p->lists + 2 * ((size_t)p->shape.max_seq + 1);
+    a.err = p->err;
+    if (!launch_attn_plan_device(a, static_cast<cudaStream_t>(stream))) return failed("plan launch", cudaGetLastError());
+    p->device_form = form;
     return 0;
 }
 
@@ -506,7 +553,7 @@ int llm_attn_run(llm_attn_plan* p, const void* q, int64_t q_stride_tok, int64_t 
     if (kv->type != p->kv.type || kv->n_head_kv != p->kv.n_head_kv || kv->head_dim != p->kv.head_dim ||
         kv->page_size != p->kv.page_size || kv->n_pages != p->kv.n_pages)
         return refuse("the cache is not of the plan's type and shape");
-    if (p->plan.form() == 0) {
+    if (p->form() == 0) {
         // (a graph without the kernels would replay later steps as nothing, and nobody would learn of it)
         cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
         OnDevice on(p->device);
@@ -551,13 +598,13 @@ int llm_attn_run(llm_attn_plan* p, const void* q, int64_t q_stride_tok, int64_t 
     a.part_o2 = p->part_o + plan_part_rows(p->caps, false) * kv->head_dim;
     a.part_ml2 = p->part_ml + plan_part_rows(p->caps, false);
     a.tickets = p->tickets; a.redo2 = p->redo; a.err = p->err;
-    a.form = p->plan.form();
+    a.form = p->form();
     a.n_sm = p->ps.n_sm;
     if (!launch_attn_paged(a, static_cast<cudaStream_t>(stream))) return failed("attention launch", cudaGetLastError());
     return 0;
 }
 
-int llm_attn_plan_form(const llm_attn_plan* p) { return p ? p->plan.form() : refuse("NULL plan"); }
+int llm_attn_plan_form(const llm_attn_plan* p) { return p ? p->form() : refuse("NULL plan"); }
 
 uint32_t llm_attn_plan_error(llm_attn_plan* p) {
     if (!p) return 0;

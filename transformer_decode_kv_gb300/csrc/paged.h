@@ -163,10 +163,34 @@ struct PagedPlan {
 };
 void build_paged_plan(const PlanShape& s, const std::vector<PlanSeq>& seqs, PagedPlan& plan);
 // Upper bounds for buffers over every plan of at most max_tok tokens in max_seq sequences.
-struct PagedPlanCaps { int64_t units1, units2, ctas1, ctas2, tickets, parts1, parts2; };
+struct PagedPlanCaps { int64_t units1, units2, ctas1, ctas2, tickets, parts1, parts2, tiles1, tiles2; };
 PagedPlanCaps paged_plan_caps(const PlanShape& s, int32_t max_tok, int32_t max_seq);
 // Partial results of both forms: rows of head_dim values, the small tiles' first.
 inline int64_t plan_part_rows(const PagedPlanCaps& c, bool both) { return c.parts1 * 16 + (both ? c.parts2 * kUnitRows2 : 0); }
+
+// The same plan from lengths and page tables in device memory (attn_plan_device.cu).
+struct PlanDeviceArgs {
+    // the shape, and how the plan deals out its work (plan_numbers): keys per block, a unit's cost in blocks and CTAs of each
+    // form, key alignment and rows of a sequence that take 256-row tiles
+    int32_t G = 1, Hkv = 1, window = 0, n_sink = 0, page_size = 1;
+    int32_t bk[2] = {1, 1}, cost[2] = {1, 1}, n_cta[2] = {1, 1}, align = 1, tc_rows = 1;
+    bool tc = false;
+    int32_t rows1 = 8;                           // rows of the small tiles
+    // the step, and what it may hold
+    int32_t n_seq = 0, ld_table = 0, max_new = 0, max_tok = 0, max_keys = 0;
+    int64_t max_table = 0;
+    const int32_t *start = nullptr, *n_kv = nullptr, *table = nullptr;
+    // the plan's buffers; scratch: tiles before each sequence [max_seq + 1], each tile's place, each sequence's table
+    int32_t* hdr = nullptr;
+    int32_t *first[2] = {nullptr, nullptr}, *cuts = nullptr, *table_out = nullptr;
+    AttnUnit* units[2] = {nullptr, nullptr};
+    int32_t *tile_base[2] = {nullptr, nullptr}, *table_off = nullptr;
+    int64_t* tile_pre[2] = {nullptr, nullptr};
+    uint32_t* err = nullptr;
+};
+// Fills in the numbers; max_new: the most new tokens of a sequence, which decides the forms that such a plan may have.
+int32_t plan_numbers(const PlanShape& s, int32_t max_new, PlanDeviceArgs& a);
+bool launch_attn_plan_device(const PlanDeviceArgs& a, cudaStream_t st);
 
 // ---- the sampler chain per row (sample_rows.cu)
 struct SampleRowsArgs {
