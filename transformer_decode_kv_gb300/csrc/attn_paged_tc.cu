@@ -54,6 +54,8 @@ constexpr int kProdWarps = 2;
 constexpr int kMmaWarp = 2;
 constexpr int kSoft0 = 4;                                  // first softmax warp
 constexpr int kThr = 12 * 32;
+constexpr int kConv0 = 12, kConvWarps = 4;                 // E2M1: four more warps convert
+constexpr int kRaw = 3;                                    // E2M1: raw tiles in flight
 constexpr int kKeys = 128;                                 // keys per block
 constexpr int kStages = 5;                                 // K or V tiles in flight (E4M3: one less, its place holds raw rows)
 constexpr int kMeta = 3;                                   // blocks whose positions are kept (see meta_full)
@@ -70,8 +72,11 @@ struct Smem {
     static constexpr uint32_t full = kpos + kMeta * kKeys * 4;   // uint32 [kMeta]: every key is read
     static constexpr uint32_t rs = full + 16;               // float [256]: scale of a row's scores, where they differ
     static constexpr uint32_t bars = rs + 256 * 4;
-    static constexpr uint32_t misc = bars + 24 * 8;
+    static constexpr uint32_t misc = bars + 32 * 8;
     static constexpr uint32_t bytes = misc + 28 * 4;
+    // E2M1: raw tiles in the ring's last place: codes, block scales, the rows' factors (f16), positions and whether all are read
+    static constexpr uint32_t raw = kv + (kStages - 1) * tile, raw_blk = kKeys * HD / 2, raw_fac = raw_blk + kKeys * HD / 16,
+                              raw_pos = raw_fac + kKeys * 2, raw_all = raw_pos + kKeys * 4, raw_tile = raw_all + 16;
 };
 static_assert(Smem<128>::bytes <= 227 * 1024, "shared memory of one CTA");
 
@@ -291,11 +296,49 @@ __device__ __forceinline__ void look_up(const AttnPagedArgs& a, const AttnUnit& 
     if (past && a.err) atomicOr(a.err, ERR_SLOT_RANGE);
 }
 
-// s / s0 between which q * s / s0 is exact in f16: the least E4M3 number is 2^-9, the largest 448
-constexpr float kRatioMin = 0x1p-15f, kRatioMax = 0x1p7f;
+// The same of an E2M1 cache, whose rows have two offsets: page -1: not read.
+struct Key4 { int page, at, pos; float s; };
+__device__ __forceinline__ void look_up4(const AttnPagedArgs& a, const AttnUnit& u, int j, int pmax, int hid_all,
+                                         const float* scales, Key4* k) {
+    const int v = u.v0 + j * kKeys + (threadIdx.x & 31), ps = a.kv.page_size;
+    const int sh = (ps & (ps - 1)) == 0 ? __ffs(ps) - 1 : -1;
+    bool past = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int w = min(v + 32 * i, u.v1 - 1);
+        const int x = w < u.n_sink_keys ? w : w - u.n_sink_keys + u.key_lo;
+        const int pg = sh >= 0 ? x >> sh : x / ps;
+        k[i].at = x - pg * ps;
+        k[i].pos = x;
+        k[i].page = a.table[u.table + pg];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const bool there = v + 32 * i < u.v1, bad = (unsigned)k[i].page >= (unsigned)a.kv.n_pages;
+        const bool seen = there && !bad && sees(k[i].pos, pmax, hid_all, a.n_sink);
+        past = past || (there && bad);
+        k[i].s = 0.f;
+        if (seen) {
+            k[i].s = scales[(int64_t)k[i].page * a.kv.ss_page + (int64_t)k[i].at * a.kv.ss_cell];
+        } else {
+            k[i].page = -1;
+            k[i].pos = INT_MAX;
+        }
+    }
+    if (past && a.err) atomicOr(a.err, ERR_SLOT_RANGE);
+}
+__device__ __forceinline__ int64_t row_off(const AttnPagedArgs& a, const Key4& k) {
+    return (int64_t)k.page * a.kv.sb_page + (int64_t)k.at * a.kv.sb_cell;
+}
 
-// whether an E4M3 row of n bytes is zeros (rarely asked: few instructions, and no call, which would cost its caller's
+// s / s0 between which q * s / s0 is exact in f16: the least E4M3 number is 2^-9, the largest 448; of E2M1 with its block
+// scale 2^-10 and 2688
+template <bool F4> constexpr float kRatioMin = F4 ? 0x1p-14f : 0x1p-15f;
+template <bool F4> constexpr float kRatioMax = F4 ? 0x1p4f : 0x1p7f;
+
+// whether an E4M3 (E2M1) row of n bytes is zeros (rarely asked: few instructions, and no call, which would cost its caller's
 // registers)
+template <bool F4 = false>
 __device__ __forceinline__ bool row_is_zero(const uint8_t* row, int n) {
     uint32_t bits = 0u;
 #pragma unroll 1
@@ -303,23 +346,26 @@ __device__ __forceinline__ bool row_is_zero(const uint8_t* row, int n) {
         const uint4 x = *reinterpret_cast<const uint4*>(row + i);
         bits |= x.x | x.y | x.z | x.w;
     }
-    return (bits & 0x7f7f7f7fu) == 0u;
+    return (bits & (F4 ? 0x77777777u : 0x7f7f7f7fu)) == 0u;
 }
 
+constexpr int threads_of(int ct) { return kThr + (ct == W_F4 ? 32 * kConvWarps : 0); }
+
 template <int HD, int CT, int QT>
-__global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, TmaRuns runs, int beside,
+__global__ void __launch_bounds__(threads_of(CT), 1) attn_tc_rows_kernel(AttnPagedArgs a, TmaRuns runs, int beside,
                                                                const __grid_constant__ CUtensorMap map_k,
                                                                const __grid_constant__ CUtensorMap map_v) {
     using M = Smem<HD>;
-    constexpr bool F8 = CT == W_F8, BF = CT == W_BF16;
+    constexpr bool F8 = CT == W_F8, F4 = CT == W_F4, RS = F8 || F4, BF = CT == W_BF16;
     constexpr int CH = HD / 8;                              // 16-byte chunks of a 16-bit row
-    constexpr int NS = F8 ? kStages - 1 : kStages;
+    constexpr int NS = RS ? kStages - 1 : kStages;
     extern __shared__ __align__(1024) uint8_t sm[];
     int* kpos = reinterpret_cast<int*>(sm + M::kpos);
     volatile uint32_t* full = reinterpret_cast<volatile uint32_t*>(sm + M::full);
     float* rs_s = reinterpret_cast<float*>(sm + M::rs);
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + M::bars);
-    uint64_t* kv_full = bars;                               // [kStages] 1: the producing warp (and its bulk copies' bytes)
+    // [kStages] 1: the producing warp (and its bulk copies' bytes), or 4: the converting warps
+    uint64_t* kv_full = bars;
     uint64_t* kv_empty = bars + kStages;                    // [kStages] 1: MMA commit
     uint64_t* s_full = bars + 2 * kStages;                  // [2] 1: MMA commit
     uint64_t* p_full = s_full + 2;                          // [2] 128: the softmax threads
@@ -330,7 +376,10 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
     uint64_t* meta_full = q_full + 1;
     uint64_t* q_empty = meta_full + kMeta;                  // 1: MMA commit after the unit's last scores
     uint64_t* drained = q_empty + 1;                        // 1: MMA commit after a wait that gave up
-    static_assert(2 * kStages + 7 + kMeta + 2 <= 24, "places of the barriers");
+    uint64_t* raw_full = drained + 1;                       // [kRaw] 33: the loading warp, its lanes' copies
+    uint64_t* raw_empty = raw_full + kRaw;                  // [kRaw] 4: the converting warps
+    static_assert(2 * kStages + 7 + kMeta + 2 + 2 * kRaw <= 32, "places of the barriers");
+    static_assert(!F4 || kRaw * M::raw_tile <= M::tile, "raw tiles in the ring's last place");
     int* misc = reinterpret_cast<int*>(sm + M::misc);
     volatile int* abort_f = misc;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 2);
@@ -358,12 +407,14 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
     constexpr bool SCALED = !BF && QT != W_F16;
     const bool own_q = F8 || SCALED || a.scale_log2 < 0.f;   // (E4M3: warp 3 is a producer)
     if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) { bar_init(&kv_full[i], 1); bar_init(&kv_empty[i], 1); }
+        for (int i = 0; i < kStages; ++i) { bar_init(&kv_full[i], F4 ? kConvWarps : 1); bar_init(&kv_empty[i], 1); }
+        if (F4)
+            for (int i = 0; i < kRaw; ++i) { bar_init(&raw_full[i], 33); bar_init(&raw_empty[i], kConvWarps); }
         for (int i = 0; i < 2; ++i) { bar_init(&s_full[i], 1); bar_init(&p_full[i], 128); bar_init(&o_done[i], 1); }
         bar_init(q_full, own_q ? 256 : 1);
         bar_init(q_empty, 1);
         bar_init(drained, 1);
-        for (int i = 0; i < kMeta; ++i) bar_init(&meta_full[i], 1);
+        for (int i = 0; i < kMeta; ++i) bar_init(&meta_full[i], F4 ? kConvWarps : 1);
         *abort_f = 0;
         for (int i = 0; i < 8; ++i) redo_f[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -396,13 +447,95 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
     // leaves L1 little), so both parts count: 2048 new tokens at the end of 32768 E4M3 keys (32 / 8 heads of 128) took
     // 5360 us with 120 + 192 and 3720 us with 152 + 176 while producers held raw rows in registers; with the raw rows in
     // shared memory 1240 us with 104 + 200 and 1190 us as here.
-    constexpr int kRegsLow = F8 ? 120 : 88, kRegsHigh = F8 ? 192 : 208;
-    static_assert(kRegsLow + 2 * kRegsHigh <= 3 * 168, "registers of the launch");
+    constexpr int kRegsLow = F4 ? 72 : F8 ? 120 : 88, kRegsHigh = F4 ? 184 : F8 ? 192 : 208;
+    static_assert(F4 ? 2 * (kRegsLow + kRegsHigh) <= 4 * 128 : kRegsLow + 2 * kRegsHigh <= 3 * 168, "registers of the launch");
     Ring<NS> ring;
     MetaAt meta;
     if (warp < kSoft0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
-        if (F8 && warp != kMmaWarp) {
+        if (F4 && warp < 2) {
+            // ---- E2M1: warp 0 brings the raw rows of K tiles, warp 1 those of V tiles, by asynchronous copies whose landing the
+            // converting warps wait for; a row's factor s / s0 and its position go with them.
+            constexpr int LR = HD / 32, RI = 32 / LR, NB = HD / kF4Block;   // lanes per row of codes, rows at a time; block scales
+            const bool is_v = warp == 1;
+            uint32_t it = is_v ? 1 : 0;                     // tile number, over all units
+            int with_keys = 0;
+            bool ok = true;
+            for (int ui = ui0; ui < ui1 && ok; ++ui) {
+                const AttnUnit u = load_unit(a.units2 + ui);
+                const int nt = (u.v1 - u.v0 + kKeys - 1) / kKeys;
+                if (nt == 0) continue;
+                const int slot = with_keys++ & 7;
+                int pmin, pmax;
+                unit_positions(a, u, pmin, pmax);
+                const int hid_all = hidden_below(a, pmin);
+                const uint8_t* const rows = (is_v ? a.kv.v : a.kv.k) + (int64_t)u.head * a.kv.sb_head;
+                const uint8_t* const blks = (is_v ? a.kv.vb : a.kv.kb) + (int64_t)u.head * a.kv.sk_head;
+                const float* const scales = (is_v ? a.kv.vs : a.kv.ks) + (int64_t)u.head * a.kv.ss_head;
+                // s0: four times the largest scale of the unit's first block (rows of zeros do not count)
+                Key4 cur[4], nxt[4];
+                auto unit_scale = [&](const float* sc, const uint8_t* r) {
+                    look_up4(a, u, 0, pmax, hid_all, sc, cur);
+                    float mx = 0.f;
+                    if (__any_sync(0xffffffffu, cur[0].s == 1.f || cur[1].s == 1.f || cur[2].s == 1.f || cur[3].s == 1.f))
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (cur[i].s == 1.f && row_is_zero<true>(r + row_off(a, cur[i]), HD / 2)) cur[i].s = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) mx = fmaxf(mx, cur[i].s);
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                    return mx > 0.f ? 4.f * mx : 1.f;
+                };
+                if (!is_v) {                                // (both before the unit's first positions are announced)
+                    const float sv = unit_scale(a.kv.vs + (int64_t)u.head * a.kv.ss_head, a.kv.v + (int64_t)u.head * a.kv.sb_head);
+                    if (lane == 0) s0[2 * slot + 1] = sv;
+                }
+                const float su = unit_scale(scales, rows), inv = 1.f / su;
+                if (!is_v && lane == 0) s0[2 * slot] = su;
+                for (int j = 0; j < nt; ++j, it += 2) {
+                    const uint32_t rs = it % kRaw, ph = (it / kRaw) & 1u;
+                    uint8_t* const raw = sm + M::raw + rs * M::raw_tile;
+                    if (j + 1 < nt) look_up4(a, u, j + 1, pmax, hid_all, scales, nxt);
+                    ok = it < kRaw || wait(&raw_empty[rs], ph ^ 1u);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    bool all = true;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const bool there = cur[i].page >= 0;
+                        const int64_t off = there ? row_off(a, cur[i]) : -1;
+                        all = all && there;
+#pragma unroll
+                        for (int y = 0; y < LR; ++y) {
+                            const int r = y * RI + lane / LR;
+                            const int64_t o = __shfl_sync(0xffffffffu, off, r);
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sa(raw) + (32 * i + r) * (HD / 2) + 16 * (lane % LR)),
+                                         "l"(rows + (o >= 0 ? o : 0) + 16 * (lane % LR)), "r"(o >= 0 ? 16 : 0) : "memory");
+                        }
+                        const int64_t bo = there ? (int64_t)cur[i].page * a.kv.sk_page + (int64_t)cur[i].at * a.kv.sk_cell : 0;
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(sa(raw) + M::raw_blk + (32 * i + lane) * NB),
+                                     "l"(blks + bo), "n"(NB), "r"(there ? NB : 0) : "memory");
+                        float f = cur[i].s * inv;
+                        if (there && !(f >= kRatioMin<F4> && f <= kRatioMax<F4>)) {
+                            // f16 would not hold it, unless it is zeros
+                            if (f != f || !row_is_zero<true>(rows + off, HD / 2)) redo_f[slot] = 1;
+                            f = 0.f;
+                        }
+                        reinterpret_cast<__half*>(raw + M::raw_fac)[32 * i + lane] = __float2half_rn(f);
+                        if (!is_v) reinterpret_cast<int*>(raw + M::raw_pos)[32 * i + lane] = cur[i].pos;
+                    }
+                    all = __all_sync(0xffffffffu, all);
+                    if (lane == 0) *reinterpret_cast<uint32_t*>(raw + M::raw_all) = all;
+                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sa(&raw_full[rs])) : "memory");
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(&raw_full[rs]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) cur[i] = nxt[i];
+                }
+            }
+            if (!ok) asm volatile("cp.async.wait_all;" ::: "memory");
+        } else if (F8 && warp != kMmaWarp) {
             // ---- E4M3: three producers take the tiles K, V, K, V ... in turn (two, one for K and one for V: 1300 us
             // instead of 1190). Raw rows travel by asynchronous
             // copies into a producer's part of the ring's last place, a tile in eight pieces of 16 rows, the fifth
@@ -478,13 +611,13 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
                     for (int i = 0; i < 4; ++i) {
                         cur[i].s *= is_v ? inv[1] : inv[0];
                         all = all && cur[i].off >= 0;
-                        fits = fits && (cur[i].off < 0 || (cur[i].s >= kRatioMin && cur[i].s <= kRatioMax));
+                        fits = fits && (cur[i].off < 0 || (cur[i].s >= kRatioMin<F4> && cur[i].s <= kRatioMax<F4>));
                     }
                     all = __all_sync(0xffffffffu, all);
                     if (!__all_sync(0xffffffffu, fits))
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            if (cur[i].off >= 0 && !(cur[i].s >= kRatioMin && cur[i].s <= kRatioMax)) {
+                            if (cur[i].off >= 0 && !(cur[i].s >= kRatioMin<F4> && cur[i].s <= kRatioMax<F4>)) {
                                 // f16 would not hold it, unless it is zeros
                                 if (cur[i].s != cur[i].s || !row_is_zero(rows_of(x) + cur[i].off, HD)) redo_f[slot] = 1;
                                 cur[i].s = 0.f;
@@ -542,7 +675,7 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
                 before += n_tile;
             }
             if (!ok) asm volatile("cp.async.wait_group 0;" ::: "memory");
-        } else if (!F8 && warp < kProdWarps) {
+        } else if (!RS && warp < kProdWarps) {
             // ---- K (warp 0) and V (warp 1) tiles, the even and odd ones of the ring
             const bool is_v = warp == 1;
             uint32_t it = is_v ? 1 : 0;                     // tile number, over all units
@@ -828,6 +961,57 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
             }
         }
         __syncwarp();
+    } else if (F4 && warp >= kConv0) {
+        // ---- E2M1: four warps convert the tiles K, V, K, V ... in turn, 32 rows each: a lane 16 values of a row, which share a
+        // block scale, times the scale and the row's factor (exact in f16). Lanes of a quarter warp hold two rows' blocks of
+        // one 64-column block, so that their stores' banks differ.
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
+        constexpr int NB = HD / kF4Block, RI = 32 / NB;     // blocks of a row, rows at a time
+        const int cw = warp - kConv0;
+        const int lr = NB == 8 ? ((lane >> 2) & 1) | ((lane >> 4) << 1) : lane / NB;
+        const int lc = NB == 8 ? (lane & 3) | ((lane >> 1) & 4) : lane % NB;
+        uint32_t it = 0;                                    // tile number, over all units
+        bool ok = true;
+        for (int ui = ui0; ui < ui1 && ok; ++ui) {
+            const AttnUnit u = load_unit(a.units2 + ui);
+            const int n_tile = 2 * ((u.v1 - u.v0 + kKeys - 1) / kKeys);
+            for (int x = 0; x < n_tile; ++x, ++it) {
+                const uint32_t rs = it % kRaw, stage = it % NS;
+                const uint8_t* const raw = sm + M::raw + rs * M::raw_tile;
+                uint8_t* const dst = sm + M::kv + stage * M::tile;
+                ok = wait(&raw_full[rs], (it / kRaw) & 1u) && (it < NS || wait(&kv_empty[stage], ((it / NS) & 1u) ^ 1u));
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+#pragma unroll
+                for (int y = 0; y < 32 / RI; ++y) {
+                    const int row = 32 * cw + y * RI + lr;
+                    const uint2 w = *reinterpret_cast<const uint2*>(raw + row * (HD / 2) + 8 * lc);
+                    const uint32_t b = raw[M::raw_blk + row * NB + lc];
+                    const uint32_t f = reinterpret_cast<const uint16_t*>(raw + M::raw_fac)[row];
+                    const uint32_t s = mul_h2(e4m3x2_to_h2(0x101u * b), 0x10001u * f);
+                    uint32_t h[8];
+                    e2m1x8_to_h2(w.x, h);
+                    e2m1x8_to_h2(w.y, h + 4);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) h[i] = mul_h2(h[i], s);
+                    *reinterpret_cast<uint4*>(dst + swz(row, 2 * lc)) = make_uint4(h[0], h[1], h[2], h[3]);
+                    *reinterpret_cast<uint4*>(dst + swz(row, 2 * lc + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
+                }
+                const int m = (int)((it >> 1) % kMeta);
+                if (!(x & 1)) {
+                    kpos[m * kKeys + 32 * cw + lane] = reinterpret_cast<const int*>(raw + M::raw_pos)[32 * cw + lane];
+                    if (cw == 0 && lane == 0) full[m] = *reinterpret_cast<const uint32_t*>(raw + M::raw_all);
+                }
+                to_async_proxy();
+                __syncwarp();
+                if (lane == 0) {
+                    bar_arrive(&kv_full[stage]);
+                    bar_arrive(&raw_empty[rs]);
+                    if (!(x & 1)) bar_arrive(&meta_full[m]);
+                }
+            }
+        }
+        __syncwarp();
     } else {
         // ---- the two halves: Q tile, softmax, epilogue
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsHigh));
@@ -935,7 +1119,7 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
                 if (!__all_sync(0xffffffffu, got)) { live = false; break; }
                 tc_after();
                 s_ph ^= 1u;
-                if (F8 && j == 0) rs *= s0[2 * slot];
+                if (RS && j == 0) rs *= s0[2 * slot];
                 const int* kp = kpos + meta.s * kKeys;
                 const int4* kp4 = reinterpret_cast<const int4*>(kp);
                 const bool open = full[meta.s] != 0u &&
@@ -1031,7 +1215,7 @@ __global__ void __launch_bounds__(kThr, 1) attn_tc_rows_kernel(AttnPagedArgs a, 
             // ---- epilogue: a unit alone writes its rows, one of several its partial result
             if (live) {
                 bool finite = l <= 3.0e38f && m <= 3.0e38f;
-                const float inv = 1.f / l, none = l == 0.f ? weightless(a, u, row, tok) : 0.f, sv = F8 && nt > 0 ? s0[2 * slot + 1] : 1.f;
+                const float inv = 1.f / l, none = l == 0.f ? weightless(a, u, row, tok) : 0.f, sv = RS && nt > 0 ? s0[2 * slot + 1] : 1.f;
                 const int64_t at = (int64_t)(u.part + u.chunk) * kUnitRows2 + 128 * t + r;
                 const int64_t oi = (int64_t)tok * a.o_tok + (int64_t)(kvh * a.G + row % a.G) * a.o_head;
                 if (u.n_chunk > 1 && mine) a.part_ml2[at] = make_float2(m, l);
@@ -1167,7 +1351,7 @@ bool go(const AttnPagedArgs& a, cudaStream_t st) {
     if (!allow_smem(reinterpret_cast<const void*>(attn_tc_rows_kernel<HD, CT, QT>), Smem<HD>::bytes, done)) return false;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.n_sm);                             // one CTA per SM, each walking its units
-    cfg.blockDim = dim3(kThr);
+    cfg.blockDim = dim3(threads_of(CT));
     cfg.dynamicSmemBytes = Smem<HD>::bytes;
     cfg.stream = st;
     cudaLaunchAttribute at[1];
@@ -1178,7 +1362,7 @@ bool go(const AttnPagedArgs& a, cudaStream_t st) {
     cfg.numAttrs = beside ? 1 : 0;
     CUtensorMap mk{}, mv{};
     TmaRuns runs{0, false, false};
-    if (CT != W_F8) runs = cell_runs(a.kv, &mk, &mv);
+    if (CT != W_F8 && CT != W_F4) runs = cell_runs(a.kv, &mk, &mv);
     if (cudaLaunchKernelEx(&cfg, attn_tc_rows_kernel<HD, CT, QT>, a, runs, beside, mk, mv) != cudaSuccess) return false;
     // (launched early, it waits for the kernel above)
     cfg.gridDim = dim3(4 * a.n_sm);
@@ -1191,6 +1375,10 @@ template <int HD>
 bool go_hd(const AttnPagedArgs& a, cudaStream_t st) {
     if (a.kv.type == W_F16) return a.q_type == W_F16 ? go<HD, W_F16, W_F16>(a, st) : go<HD, W_F16, W_F32>(a, st);
     if (a.kv.type == W_BF16) return go<HD, W_BF16, W_BF16>(a, st);
+    if (a.kv.type == W_F4) {
+        if (a.q_type == W_F16) return go<HD, W_F4, W_F16>(a, st);
+        return a.q_type == W_BF16 ? go<HD, W_F4, W_BF16>(a, st) : false;
+    }
     if (a.q_type == W_F16) return go<HD, W_F8, W_F16>(a, st);
     return a.q_type == W_BF16 ? go<HD, W_F8, W_BF16>(a, st) : go<HD, W_F8, W_F32>(a, st);
 }
@@ -1200,7 +1388,7 @@ bool go_hd(const AttnPagedArgs& a, cudaStream_t st) {
 // F32 activations stay with the 16-row tiles, which carry Q and P as two terms each, unless the caller's precision is
 // that of f16 activations (round_q: the context's f16 forward passes).
 bool attn_paged_tc_ok(int32_t hd, int32_t kv_type, int32_t q_type, bool round_q) {
-    return kv_type != W_F4 && (hd == 64 || hd == 128) && (q_type != W_F32 || round_q) && attn_paged_types_ok(q_type, kv_type);
+    return (hd == 64 || hd == 128) && (q_type != W_F32 || (round_q && kv_type != W_F4)) && attn_paged_types_ok(q_type, kv_type);
 }
 
 bool launch_attn_paged_tc(const AttnPagedArgs& a, cudaStream_t st) {
