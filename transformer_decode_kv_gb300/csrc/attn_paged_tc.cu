@@ -68,15 +68,16 @@ struct Smem {
     static constexpr uint32_t tile = HD / 64 * kBlk;
     static constexpr uint32_t q = 0;                        // [2] tiles
     static constexpr uint32_t kv = q + 2 * tile;            // [kStages] tiles
-    static constexpr uint32_t kpos = kv + kStages * tile;   // int [kMeta][kKeys]
+    // E2M1: raw tiles in the ring's last place: codes, block scales, the rows' scales, positions and whether all are read
+    static constexpr uint32_t raw = kv + (kStages - 1) * tile, raw_blk = kKeys * HD / 2, raw_sc = raw_blk + kKeys * HD / 16,
+                              raw_pos = raw_sc + kKeys * 4, raw_all = raw_pos + kKeys * 4, raw_tile = raw_all + 16;
+    static constexpr uint32_t kv_end = kv + kStages * tile, raw_end = raw + kRaw * raw_tile;
+    static constexpr uint32_t kpos = kv_end > raw_end ? kv_end : raw_end;   // int [kMeta][kKeys]
     static constexpr uint32_t full = kpos + kMeta * kKeys * 4;   // uint32 [kMeta]: every key is read
     static constexpr uint32_t rs = full + 16;               // float [256]: scale of a row's scores, where they differ
     static constexpr uint32_t bars = rs + 256 * 4;
     static constexpr uint32_t misc = bars + 32 * 8;
     static constexpr uint32_t bytes = misc + 28 * 4;
-    // E2M1: raw tiles in the ring's last place: codes, block scales, the rows' factors (f16), positions and whether all are read
-    static constexpr uint32_t raw = kv + (kStages - 1) * tile, raw_blk = kKeys * HD / 2, raw_fac = raw_blk + kKeys * HD / 16,
-                              raw_pos = raw_fac + kKeys * 2, raw_all = raw_pos + kKeys * 4, raw_tile = raw_all + 16;
 };
 static_assert(Smem<128>::bytes <= 227 * 1024, "shared memory of one CTA");
 
@@ -296,41 +297,6 @@ __device__ __forceinline__ void look_up(const AttnPagedArgs& a, const AttnUnit& 
     if (past && a.err) atomicOr(a.err, ERR_SLOT_RANGE);
 }
 
-// The same of an E2M1 cache, whose rows have two offsets: page -1: not read.
-struct Key4 { int page, at, pos; float s; };
-__device__ __forceinline__ void look_up4(const AttnPagedArgs& a, const AttnUnit& u, int j, int pmax, int hid_all,
-                                         const float* scales, Key4* k) {
-    const int v = u.v0 + j * kKeys + (threadIdx.x & 31), ps = a.kv.page_size;
-    const int sh = (ps & (ps - 1)) == 0 ? __ffs(ps) - 1 : -1;
-    bool past = false;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int w = min(v + 32 * i, u.v1 - 1);
-        const int x = w < u.n_sink_keys ? w : w - u.n_sink_keys + u.key_lo;
-        const int pg = sh >= 0 ? x >> sh : x / ps;
-        k[i].at = x - pg * ps;
-        k[i].pos = x;
-        k[i].page = a.table[u.table + pg];
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const bool there = v + 32 * i < u.v1, bad = (unsigned)k[i].page >= (unsigned)a.kv.n_pages;
-        const bool seen = there && !bad && sees(k[i].pos, pmax, hid_all, a.n_sink);
-        past = past || (there && bad);
-        k[i].s = 0.f;
-        if (seen) {
-            k[i].s = scales[(int64_t)k[i].page * a.kv.ss_page + (int64_t)k[i].at * a.kv.ss_cell];
-        } else {
-            k[i].page = -1;
-            k[i].pos = INT_MAX;
-        }
-    }
-    if (past && a.err) atomicOr(a.err, ERR_SLOT_RANGE);
-}
-__device__ __forceinline__ int64_t row_off(const AttnPagedArgs& a, const Key4& k) {
-    return (int64_t)k.page * a.kv.sb_page + (int64_t)k.at * a.kv.sb_cell;
-}
-
 // s / s0 between which q * s / s0 is exact in f16: the least E4M3 number is 2^-9, the largest 448; of E2M1 with its block
 // scale 2^-10 and 2688
 template <bool F4> constexpr float kRatioMin = F4 ? 0x1p-14f : 0x1p-15f;
@@ -379,7 +345,6 @@ __global__ void __launch_bounds__(threads_of(CT), 1) attn_tc_rows_kernel(AttnPag
     uint64_t* raw_full = drained + 1;                       // [kRaw] 33: the loading warp, its lanes' copies
     uint64_t* raw_empty = raw_full + kRaw;                  // [kRaw] 4: the converting warps
     static_assert(2 * kStages + 7 + kMeta + 2 + 2 * kRaw <= 32, "places of the barriers");
-    static_assert(!F4 || kRaw * M::raw_tile <= M::tile, "raw tiles in the ring's last place");
     int* misc = reinterpret_cast<int*>(sm + M::misc);
     volatile int* abort_f = misc;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 2);
@@ -447,20 +412,24 @@ __global__ void __launch_bounds__(threads_of(CT), 1) attn_tc_rows_kernel(AttnPag
     // leaves L1 little), so both parts count: 2048 new tokens at the end of 32768 E4M3 keys (32 / 8 heads of 128) took
     // 5360 us with 120 + 192 and 3720 us with 152 + 176 while producers held raw rows in registers; with the raw rows in
     // shared memory 1240 us with 104 + 200 and 1190 us as here.
-    constexpr int kRegsLow = F4 ? 72 : F8 ? 120 : 88, kRegsHigh = F4 ? 184 : F8 ? 192 : 208;
+    constexpr int kRegsLow = F4 ? 64 : F8 ? 120 : 88, kRegsHigh = F4 ? 192 : F8 ? 192 : 208;
     static_assert(F4 ? 2 * (kRegsLow + kRegsHigh) <= 4 * 128 : kRegsLow + 2 * kRegsHigh <= 3 * 168, "registers of the launch");
     Ring<NS> ring;
     MetaAt meta;
     if (warp < kSoft0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
         if (F4 && warp < 2) {
-            // ---- E2M1: warp 0 brings the raw rows of K tiles, warp 1 those of V tiles, by asynchronous copies whose landing the
-            // converting warps wait for; a row's factor s / s0 and its position go with them.
+            // ---- E2M1: warp 0 brings the raw rows of K tiles, warp 1 those of V tiles: codes, block scales and scales by
+            // asynchronous copies whose landing the converting warps wait for. Runs of cells that follow each other in memory (a
+            // head's cells of a page) come by bulk copies, other rows by themselves. This warp's code is short: all roles share
+            // the instruction cache, and a loop that is unrolled here costs the softmax (see the converting warps).
             constexpr int LR = HD / 32, RI = 32 / LR, NB = HD / kF4Block;   // lanes per row of codes, rows at a time; block scales
             const bool is_v = warp == 1;
+            const int ps = a.kv.page_size, sh = (ps & (ps - 1)) == 0 ? __ffs(ps) - 1 : -1;
             uint32_t it = is_v ? 1 : 0;                     // tile number, over all units
             int with_keys = 0;
-            bool ok = true;
+            bool ok = true, past = false;
+            int bulk_at[kRaw] = {-1, -1, -1};               // phase of a raw tile's last bulk copies, -1: none
             for (int ui = ui0; ui < ui1 && ok; ++ui) {
                 const AttnUnit u = load_unit(a.units2 + ui);
                 const int nt = (u.v1 - u.v0 + kKeys - 1) / kKeys;
@@ -472,69 +441,136 @@ __global__ void __launch_bounds__(threads_of(CT), 1) attn_tc_rows_kernel(AttnPag
                 const uint8_t* const rows = (is_v ? a.kv.v : a.kv.k) + (int64_t)u.head * a.kv.sb_head;
                 const uint8_t* const blks = (is_v ? a.kv.vb : a.kv.kb) + (int64_t)u.head * a.kv.sk_head;
                 const float* const scales = (is_v ? a.kv.vs : a.kv.ks) + (int64_t)u.head * a.kv.ss_head;
+                // blocks whose keys are runs of neighbouring cells that some row sees: a lane brings a run, three bulk copies
+                const int n_run = runs.rows > 0 ? kKeys / runs.rows : 0;
+                auto plain = [&](int j) {
+                    const int v = u.v0 + j * kKeys;
+                    if (n_run == 0 || a.key_pos || v + kKeys > u.v1) return false;
+                    if (v < u.n_sink_keys) return v + kKeys <= u.n_sink_keys && v + kKeys <= min(a.n_sink, pmax + 1);
+                    const int k = v - u.n_sink_keys + u.key_lo;
+                    return k + kKeys - 1 <= pmax && (k > hid_all || k + kKeys <= a.n_sink);
+                };
+                auto index = [&](int w) {                   // of the unit's key w in its sequence
+                    w = min(w, u.v1 - 1);
+                    return w < u.n_sink_keys ? w : w - u.n_sink_keys + u.key_lo;
+                };
+                auto page_of = [&](int x) { return sh >= 0 ? x >> sh : x / ps; };
+                auto run_page = [&](int j) {                // the page of this lane's run
+                    return a.table[u.table + page_of(index(u.v0 + j * kKeys + min(lane, n_run - 1) * runs.rows))];
+                };
+                bool plain_nxt = plain(0);
+                int page_nxt = plain_nxt ? run_page(0) : 0;
+                // a key's position (INT_MAX: not read), page and place there
+                auto position = [&](int w, int& page, int& at) {
+                    const int x = index(w), pg = page_of(x);
+                    at = x - pg * ps;
+                    page = a.table[u.table + pg];
+                    const bool there = w < u.v1, bad = (unsigned)page >= (unsigned)a.kv.n_pages;
+                    past = past || (there && bad);
+                    const int pos = a.key_pos ? a.key_pos[u.table + x] : x;
+                    return there && !bad && sees(pos, pmax, hid_all, a.n_sink) ? pos : INT_MAX;
+                };
                 // s0: four times the largest scale of the unit's first block (rows of zeros do not count)
-                Key4 cur[4], nxt[4];
-                auto unit_scale = [&](const float* sc, const uint8_t* r) {
-                    look_up4(a, u, 0, pmax, hid_all, sc, cur);
+                auto unit_scale = [&](const float* sc, const uint8_t* rw) {
                     float mx = 0.f;
-                    if (__any_sync(0xffffffffu, cur[0].s == 1.f || cur[1].s == 1.f || cur[2].s == 1.f || cur[3].s == 1.f))
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (cur[i].s == 1.f && row_is_zero<true>(r + row_off(a, cur[i]), HD / 2)) cur[i].s = 0.f;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) mx = fmaxf(mx, cur[i].s);
+#pragma unroll 1
+                    for (int i = lane; i < kKeys; i += 32) {
+                        int page, at;
+                        if (position(u.v0 + i, page, at) == INT_MAX) continue;
+                        const float x = sc[(int64_t)page * a.kv.ss_page + (int64_t)at * a.kv.ss_cell];
+                        if (x != 1.f || !row_is_zero<true>(rw + (int64_t)page * a.kv.sb_page + (int64_t)at * a.kv.sb_cell, HD / 2))
+                            mx = fmaxf(mx, x);
+                    }
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
                     return mx > 0.f ? 4.f * mx : 1.f;
                 };
-                if (!is_v) {                                // (both before the unit's first positions are announced)
+                if (!is_v) {                                // (both before the unit's first tile is announced)
                     const float sv = unit_scale(a.kv.vs + (int64_t)u.head * a.kv.ss_head, a.kv.v + (int64_t)u.head * a.kv.sb_head);
-                    if (lane == 0) s0[2 * slot + 1] = sv;
+                    const float sk = unit_scale(scales, rows);
+                    if (lane == 0) { s0[2 * slot] = sk; s0[2 * slot + 1] = sv; }
                 }
-                const float su = unit_scale(scales, rows), inv = 1.f / su;
-                if (!is_v && lane == 0) s0[2 * slot] = su;
                 for (int j = 0; j < nt; ++j, it += 2) {
                     const uint32_t rs = it % kRaw, ph = (it / kRaw) & 1u;
-                    uint8_t* const raw = sm + M::raw + rs * M::raw_tile;
-                    if (j + 1 < nt) look_up4(a, u, j + 1, pmax, hid_all, scales, nxt);
+                    const uint32_t raw = sa(sm) + M::raw + rs * M::raw_tile;
+                    const uint32_t fb = sa(&raw_full[rs]);
+                    const int run = page_nxt;
+                    bool now = plain_nxt;
+                    plain_nxt = j + 1 < nt && plain(j + 1);
+                    if (plain_nxt) page_nxt = run_page(j + 1);
+                    if (now && __any_sync(0xffffffffu, (unsigned)run >= (unsigned)a.kv.n_pages)) now = false;
                     ok = it < kRaw || wait(&raw_empty[rs], ph ^ 1u);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
+                    if (now) {
+                        const int w = u.v0 + j * kKeys;
+                        if (lane == 0) {
+                            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(fb), "n"(kKeys * (HD / 2 + NB + 4))
+                                         : "memory");
+                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(raw + M::raw_all), "r"(1) : "memory");
+                        }
+                        __syncwarp();
+                        bulk_at[0] = rs == 0 ? (int)ph : bulk_at[0];
+                        bulk_at[1] = rs == 1 ? (int)ph : bulk_at[1];
+                        bulk_at[2] = rs == 2 ? (int)ph : bulk_at[2];
+                        if (lane < n_run) {
+                            const int k = lane * runs.rows, x = index(w + k);
+                            const int64_t pg = run, at = x - page_of(x) * ps;
+                            auto bulk = [&](uint32_t d, const void* src, int bytes) {
+                                asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(d),
+                                             "l"(src), "r"(bytes), "r"(fb) : "memory");
+                            };
+                            bulk(raw + k * (HD / 2), rows + (pg * a.kv.sb_page + at * a.kv.sb_cell), runs.rows * (HD / 2));
+                            bulk(raw + M::raw_blk + k * NB, blks + (pg * a.kv.sk_page + at * a.kv.sk_cell), runs.rows * NB);
+                            bulk(raw + M::raw_sc + k * 4, scales + (pg * a.kv.ss_page + at * a.kv.ss_cell), runs.rows * 4);
+                        }
+                        if (!is_v) {
+                            const int p = index(w) + 4 * lane;
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(raw + M::raw_pos + 16 * lane), "r"(p), "r"(p + 1),
+                                         "r"(p + 2), "r"(p + 3) : "memory");
+                        }
+                        __syncwarp();
+                        if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], 32;" ::"r"(fb) : "memory");
+                        continue;
+                    }
                     bool all = true;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const bool there = cur[i].page >= 0;
-                        const int64_t off = there ? row_off(a, cur[i]) : -1;
+#pragma unroll 1
+                    for (int i = 0; i < kKeys; i += 32) {
+                        int page, at;
+                        const int pos = position(u.v0 + j * kKeys + i + lane, page, at);
+                        const bool there = pos != INT_MAX;
                         all = all && there;
+                        const int64_t pg = there ? page : 0, c = there ? at : 0;
+                        const int64_t off = there ? pg * a.kv.sb_page + c * a.kv.sb_cell : -1;
 #pragma unroll
                         for (int y = 0; y < LR; ++y) {
                             const int r = y * RI + lane / LR;
                             const int64_t o = __shfl_sync(0xffffffffu, off, r);
-                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sa(raw) + (32 * i + r) * (HD / 2) + 16 * (lane % LR)),
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(raw + (i + r) * (HD / 2) + 16 * (lane % LR)),
                                          "l"(rows + (o >= 0 ? o : 0) + 16 * (lane % LR)), "r"(o >= 0 ? 16 : 0) : "memory");
                         }
-                        const int64_t bo = there ? (int64_t)cur[i].page * a.kv.sk_page + (int64_t)cur[i].at * a.kv.sk_cell : 0;
-                        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(sa(raw) + M::raw_blk + (32 * i + lane) * NB),
-                                     "l"(blks + bo), "n"(NB), "r"(there ? NB : 0) : "memory");
-                        float f = cur[i].s * inv;
-                        if (there && !(f >= kRatioMin<F4> && f <= kRatioMax<F4>)) {
-                            // f16 would not hold it, unless it is zeros
-                            if (f != f || !row_is_zero<true>(rows + off, HD / 2)) redo_f[slot] = 1;
-                            f = 0.f;
-                        }
-                        reinterpret_cast<__half*>(raw + M::raw_fac)[32 * i + lane] = __float2half_rn(f);
-                        if (!is_v) reinterpret_cast<int*>(raw + M::raw_pos)[32 * i + lane] = cur[i].pos;
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(raw + M::raw_blk + (i + lane) * NB),
+                                     "l"(blks + (pg * a.kv.sk_page + c * a.kv.sk_cell)), "n"(NB), "r"(there ? NB : 0) : "memory");
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(raw + M::raw_sc + (i + lane) * 4),
+                                     "l"(scales + (pg * a.kv.ss_page + c * a.kv.ss_cell)), "r"(there ? 4 : 0) : "memory");
+                        if (!is_v) asm volatile("st.shared.b32 [%0], %1;" ::"r"(raw + M::raw_pos + (i + lane) * 4), "r"(pos) : "memory");
                     }
                     all = __all_sync(0xffffffffu, all);
-                    if (lane == 0) *reinterpret_cast<uint32_t*>(raw + M::raw_all) = all;
-                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sa(&raw_full[rs])) : "memory");
+                    if (lane == 0) asm volatile("st.shared.b32 [%0], %1;" ::"r"(raw + M::raw_all), "r"((uint32_t)all) : "memory");
+                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(fb) : "memory");
                     __syncwarp();
                     if (lane == 0) bar_arrive(&raw_full[rs]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) cur[i] = nxt[i];
                 }
             }
-            if (!ok) asm volatile("cp.async.wait_all;" ::: "memory");
+            if (past && a.err) atomicOr(a.err, ERR_SLOT_RANGE);
+            // after a wait that gave up nobody may wait for the copies under way: they land before the CTA leaves
+            if (!ok) {
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                for (int i = 0; i < kRaw; ++i) {
+                    const uint64_t t0 = now_ns();
+                    while (bulk_at[i] >= 0 && !bar_try(&raw_full[i], (uint32_t)bulk_at[i]) && now_ns() - t0 < kWaitNs) {}
+                }
+            }
         } else if (F8 && warp != kMmaWarp) {
             // ---- E4M3: three producers take the tiles K, V, K, V ... in turn (two, one for K and one for V: 1300 us
             // instead of 1190). Raw rows travel by asynchronous
@@ -963,7 +999,7 @@ __global__ void __launch_bounds__(threads_of(CT), 1) attn_tc_rows_kernel(AttnPag
         __syncwarp();
     } else if (F4 && warp >= kConv0) {
         // ---- E2M1: four warps convert the tiles K, V, K, V ... in turn, 32 rows each: a lane 16 values of a row, which share a
-        // block scale, times the scale and the row's factor (exact in f16). Lanes of a quarter warp hold two rows' blocks of
+        // block scale, times that and s / s0 of the row (exact in f16). Lanes of a quarter warp hold two rows' blocks of
         // one 64-column block, so that their stores' banks differ.
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
         constexpr int NB = HD / kF4Block, RI = 32 / NB;     // blocks of a row, rows at a time
@@ -971,10 +1007,14 @@ __global__ void __launch_bounds__(threads_of(CT), 1) attn_tc_rows_kernel(AttnPag
         const int lr = NB == 8 ? ((lane >> 2) & 1) | ((lane >> 4) << 1) : lane / NB;
         const int lc = NB == 8 ? (lane & 3) | ((lane >> 1) & 4) : lane % NB;
         uint32_t it = 0;                                    // tile number, over all units
+        int with_keys = 0;
         bool ok = true;
         for (int ui = ui0; ui < ui1 && ok; ++ui) {
-            const AttnUnit u = load_unit(a.units2 + ui);
-            const int n_tile = 2 * ((u.v1 - u.v0 + kKeys - 1) / kKeys);
+            const int4 w3 = reinterpret_cast<const int4*>(a.units2 + ui)[1], w4 = reinterpret_cast<const int4*>(a.units2 + ui)[2];
+            const int n_tile = 2 * ((w4.x - w3.w + kKeys - 1) / kKeys);   // (v1 - v0)
+            if (n_tile == 0) continue;
+            const int slot = with_keys++ & 7;
+            float inv[2] = {0.f, 0.f};
             for (int x = 0; x < n_tile; ++x, ++it) {
                 const uint32_t rs = it % kRaw, stage = it % NS;
                 const uint8_t* const raw = sm + M::raw + rs * M::raw_tile;
@@ -982,13 +1022,24 @@ __global__ void __launch_bounds__(threads_of(CT), 1) attn_tc_rows_kernel(AttnPag
                 ok = wait(&raw_full[rs], (it / kRaw) & 1u) && (it < NS || wait(&kv_empty[stage], ((it / NS) & 1u) ^ 1u));
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-#pragma unroll
+                // (Unrolled, this loop is what the instruction cache does not hold beside the softmax: 2048 tokens at the end of 32768
+                // keys took 1395 us unrolled by 8, 1194 by 4, 1129 by 2 and 1080 so.)
+                if (x == 0) { inv[0] = 1.f / s0[2 * slot]; inv[1] = 1.f / s0[2 * slot + 1]; }
+                const float to = (x & 1) ? inv[1] : inv[0];
+                bool lost = false;
+#pragma unroll 1
                 for (int y = 0; y < 32 / RI; ++y) {
                     const int row = 32 * cw + y * RI + lr;
                     const uint2 w = *reinterpret_cast<const uint2*>(raw + row * (HD / 2) + 8 * lc);
                     const uint32_t b = raw[M::raw_blk + row * NB + lc];
-                    const uint32_t f = reinterpret_cast<const uint16_t*>(raw + M::raw_fac)[row];
-                    const uint32_t s = mul_h2(e4m3x2_to_h2(0x101u * b), 0x10001u * f);
+                    float f = reinterpret_cast<const float*>(raw + M::raw_sc)[row] * to;
+                    if (!(f >= kRatioMin<F4> && f <= kRatioMax<F4>)) {
+                        // f16 would not hold it, unless it is zeros (or not read, which is zeros too)
+                        lost = lost || f != f || ((w.x | w.y) & 0x77777777u) != 0u;
+                        f = 0.f;
+                    }
+                    const __half2 f2 = __float2half2_rn(f);
+                    const uint32_t s = mul_h2(e4m3x2_to_h2(0x101u * b), *reinterpret_cast<const uint32_t*>(&f2));
                     uint32_t h[8];
                     e2m1x8_to_h2(w.x, h);
                     e2m1x8_to_h2(w.y, h + 4);
@@ -997,6 +1048,7 @@ __global__ void __launch_bounds__(threads_of(CT), 1) attn_tc_rows_kernel(AttnPag
                     *reinterpret_cast<uint4*>(dst + swz(row, 2 * lc)) = make_uint4(h[0], h[1], h[2], h[3]);
                     *reinterpret_cast<uint4*>(dst + swz(row, 2 * lc + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
                 }
+                if (lost) redo_f[slot] = 1;
                 const int m = (int)((it >> 1) % kMeta);
                 if (!(x & 1)) {
                     kpos[m * kKeys + 32 * cw + lane] = reinterpret_cast<const int*>(raw + M::raw_pos)[32 * cw + lane];
@@ -1345,6 +1397,19 @@ TmaRuns cell_runs(const PagedKv& kv, CUtensorMap* mk, CUtensorMap* mv) {
     return r;
 }
 
+// The runs of cells of an E2M1 cache that bulk copies take: cells of a page that follow each other, rows, block scales and scales,
+// on 16-byte boundaries (four cells have 16 bytes of scales; shorter runs than eight are not worth a lane's three copies).
+TmaRuns cell_runs4(const PagedKv& kv) {
+    TmaRuns r{0, false, false};
+    int rows = 64;
+    while (rows >= 8 && kv.page_size % rows) rows /= 2;
+    auto even = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
+    if (rows >= 8 && kv.sb_cell == kv.hd / 2 && kv.sk_cell == kv.hd / kF4Block && kv.ss_cell == 1 && even(kv.kb) && even(kv.vb) &&
+        even(kv.ks) && even(kv.vs) && (kv.sk_page | kv.sk_head) % 16 == 0 && (kv.ss_page | kv.ss_head) % 4 == 0)
+        r.rows = rows;
+    return r;
+}
+
 template <int HD, int CT, int QT>
 bool go(const AttnPagedArgs& a, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
@@ -1362,7 +1427,8 @@ bool go(const AttnPagedArgs& a, cudaStream_t st) {
     cfg.numAttrs = beside ? 1 : 0;
     CUtensorMap mk{}, mv{};
     TmaRuns runs{0, false, false};
-    if (CT != W_F8 && CT != W_F4) runs = cell_runs(a.kv, &mk, &mv);
+    if (CT == W_F4) runs = cell_runs4(a.kv);
+    else if (CT != W_F8) runs = cell_runs(a.kv, &mk, &mv);
     if (cudaLaunchKernelEx(&cfg, attn_tc_rows_kernel<HD, CT, QT>, a, runs, beside, mk, mv) != cudaSuccess) return false;
     // (launched early, it waits for the kernel above)
     cfg.gridDim = dim3(4 * a.n_sm);
