@@ -1022,24 +1022,28 @@ __global__ void __launch_bounds__(threads_of(CT), 1) attn_tc_rows_kernel(AttnPag
                 ok = wait(&raw_full[rs], (it / kRaw) & 1u) && (it < NS || wait(&kv_empty[stage], ((it / NS) & 1u) ^ 1u));
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                // (Unrolled, this loop is what the instruction cache does not hold beside the softmax: 2048 tokens at the end of 32768
-                // keys took 1395 us unrolled by 8, 1194 by 4, 1129 by 2 and 1080 so.)
                 if (x == 0) { inv[0] = 1.f / s0[2 * slot]; inv[1] = 1.f / s0[2 * slot + 1]; }
-                const float to = (x & 1) ? inv[1] : inv[0];
-                bool lost = false;
-#pragma unroll 1
+                // s / s0 of the warp's rows, a row a lane
+                float f = reinterpret_cast<const float*>(raw + M::raw_sc)[32 * cw + lane] * ((x & 1) ? inv[1] : inv[0]);
+                const bool fits = f >= kRatioMin<F4> && f <= kRatioMax<F4>;
+                if (!__all_sync(0xffffffffu, fits)) {
+                    if (!fits) {
+                        // f16 would not hold it, unless it is zeros (or not read, which is zeros too)
+                        if (f != f || !row_is_zero<true>(raw + (32 * cw + lane) * (HD / 2), HD / 2)) redo_f[slot] = 1;
+                        f = 0.f;
+                    }
+                    __syncwarp();
+                }
+                const __half2 f2 = __float2half2_rn(f);
+                const uint32_t fw = *reinterpret_cast<const uint32_t*>(&f2);
+                // (By 2: the instruction cache has to hold it beside the softmax. 2048 tokens at the end of 32768 keys take 833 us so,
+                // 843 rolled; while the loading warps' loops were long, 1395 unrolled by 8 and 1080 rolled.)
+#pragma unroll 2
                 for (int y = 0; y < 32 / RI; ++y) {
                     const int row = 32 * cw + y * RI + lr;
                     const uint2 w = *reinterpret_cast<const uint2*>(raw + row * (HD / 2) + 8 * lc);
                     const uint32_t b = raw[M::raw_blk + row * NB + lc];
-                    float f = reinterpret_cast<const float*>(raw + M::raw_sc)[row] * to;
-                    if (!(f >= kRatioMin<F4> && f <= kRatioMax<F4>)) {
-                        // f16 would not hold it, unless it is zeros (or not read, which is zeros too)
-                        lost = lost || f != f || ((w.x | w.y) & 0x77777777u) != 0u;
-                        f = 0.f;
-                    }
-                    const __half2 f2 = __float2half2_rn(f);
-                    const uint32_t s = mul_h2(e4m3x2_to_h2(0x101u * b), *reinterpret_cast<const uint32_t*>(&f2));
+                    const uint32_t s = mul_h2(e4m3x2_to_h2(__byte_perm(b, b, 0x0000)), __shfl_sync(0xffffffffu, fw, y * RI + lr));
                     uint32_t h[8];
                     e2m1x8_to_h2(w.x, h);
                     e2m1x8_to_h2(w.y, h + 4);
@@ -1048,7 +1052,6 @@ __global__ void __launch_bounds__(threads_of(CT), 1) attn_tc_rows_kernel(AttnPag
                     *reinterpret_cast<uint4*>(dst + swz(row, 2 * lc)) = make_uint4(h[0], h[1], h[2], h[3]);
                     *reinterpret_cast<uint4*>(dst + swz(row, 2 * lc + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
                 }
-                if (lost) redo_f[slot] = 1;
                 const int m = (int)((it >> 1) % kMeta);
                 if (!(x & 1)) {
                     kpos[m * kKeys + 32 * cw + lane] = reinterpret_cast<const int*>(raw + M::raw_pos)[32 * cw + lane];

@@ -90,7 +90,8 @@ constexpr int kUnitRows2 = 256;
 // 16-row form needs the registers.
 constexpr int kAttnRowsCtas = 2;
 constexpr int attn_rows_warps(int hd, int kv_type, int rows) {
-    return hd == 128 && kv_type != W_F8 && kv_type != W_F4 ? 3 : rows == 8 ? 6 : 4;
+    if (kv_type == W_F4) return rows == 8 ? 6 : 4;
+    return hd == 128 && kv_type != W_F8 ? 3 : rows == 8 ? 6 : 4;
 }
 enum AttnOut : int32_t { AO_F16 = 0, AO_BF16 = 1, AO_F32 = 2, AO_BF16_PAIR = 3 };
 
