@@ -8,8 +8,9 @@
 // numbers from how many cuts lie before it, which a running sum over the CTAs' ends tells. The same bounds hold as
 // on the host: a CTA end cuts one tile at most, so there are at most (tiles + CTAs) units, two cut ones per CTA.
 //
-// One CTA makes the units, the others copy the page table. It is latency: lengths, three running sums, two walks over the
-// tiles.
+// One CTA makes the units, the others copy the page table. It is latency: lengths, four running sums, and two rounds of
+// independent items, the CTAs' ends (a thread finds the tile that its end falls into, and makes the unit that begins there)
+// and the tiles (each its first unit).
 #include "paged.h"
 
 namespace llm {
@@ -17,8 +18,8 @@ namespace llm {
 namespace {
 
 constexpr int kThr = 512;
-constexpr int kLanes = 8;                                   // threads that share a tile
 constexpr int kMaxCtas = 2 * 160;
+constexpr int kSeqs = 512, kTiles = 1024;                   // steps up to this size are planned in shared memory
 static_assert(kMaxCtas + 1 <= kThr, "one thread per CTA end");
 
 // Running sums of a number per thread over the block, without the thread's own; `all` receives the total.
@@ -62,137 +63,176 @@ __device__ __forceinline__ Keys tile_keys(const PlanDeviceArgs& a, int p0, int n
     return k;
 }
 
-__device__ __forceinline__ int n_new_of(const PlanDeviceArgs& a, int s) { return a.start[s + 1] - a.start[s]; }
-__device__ __forceinline__ int64_t pages_of(const PlanDeviceArgs& a, int s) {
-    const int n = a.n_kv[s];
-    return n <= 0 ? 0 : ((int64_t)n + a.page_size - 1) / a.page_size;
-}
-__device__ __forceinline__ int form_of(const PlanDeviceArgs& a, int n_new) {
-    return a.tc && (int64_t)n_new * a.G >= a.tc_rows ? 1 : 0;
-}
-
-// The sequence whose tiles contain tile x: the last with base[s] <= x.
-__device__ __forceinline__ int seq_of(const int32_t* base, int n, int x) {
-    int lo = 0;
-    for (int w = n; w > 1;) {
-        const int h = w >> 1;
-        if (base[lo + h] <= x) { lo += h; w -= h; }
-        else w = h;
-    }
-    return lo;
-}
-
-struct Tile { int s, head, row0, n_row, p0; Keys keys; int64_t at, len, rank; };
-
-template <int F>
-__device__ __forceinline__ int tile_rows(const PlanDeviceArgs& a) { return F ? kUnitRows2 : a.rows1; }
-template <int F>
-__device__ __forceinline__ Tile tile_of(const PlanDeviceArgs& a, int s, int t) {
-    Tile x;
-    const int n_new = n_new_of(a, s);
-    x.s = s;
-    x.p0 = a.n_kv[s] - n_new;
-    x.row0 = t * tile_rows<F>(a);
-    x.n_row = min(tile_rows<F>(a), n_new * a.G - x.row0);
-    x.keys = tile_keys(a, x.p0, a.n_kv[s], x.row0, x.n_row, F ? a.align : 1);
-    x.len = (x.keys.n + a.bk[F] - 1) / a.bk[F] + a.cost[F];
-    return x;
-}
-// (tile, head) r in the plan's order: sequences, heads, tiles
-template <int F>
-__device__ __forceinline__ Tile ranked(const PlanDeviceArgs& a, int64_t r, int64_t total) {
-    const int32_t* base = a.tile_base[F];
-    const int s = seq_of(base, a.n_seq, (int)(r / a.Hkv));
-    const int T = base[s + 1] - base[s], rem = (int)(r - (int64_t)base[s] * a.Hkv);
-    const int head = rem / T, t = rem - head * T;
-    Tile x = tile_of<F>(a, s, t);
-    x.head = head;
-    x.rank = r;
-    const int64_t pre0 = a.tile_pre[F][base[s]], pre = a.tile_pre[F][base[s] + t];
-    const int64_t one = (base[s + 1] < base[a.n_seq] ? a.tile_pre[F][base[s + 1]] : total) - pre0;   // a head's tiles
-    x.at = pre0 * a.Hkv + head * one + pre - pre0;
-    return x;
+__device__ __forceinline__ int64_t pages_of(const PlanDeviceArgs& a, int n_kv) {
+    return n_kv <= 0 ? 0 : ((int64_t)n_kv + a.page_size - 1) / a.page_size;
 }
 
 struct Shared {
     int64_t scan[32];
     int32_t cut[kMaxCtas + 1], cut_tile[kMaxCtas + 1];      // CTA ends that cut a tile; of these, a tile's first
+    int32_t start[kSeqs + 1], n_kv[kSeqs], off[kSeqs], base[2][kSeqs + 1];
+    int64_t pre[kTiles + 1];
+};
+// The step's lists, in shared memory or, where they are long, in the plan's scratch.
+struct Lists { const int32_t *start, *n_kv; int32_t* off; int32_t* base[2]; };
+
+// The last i of a[0 .. n) (ascending, a[0] <= x) with a[i] <= x.
+template <typename T>
+__device__ __forceinline__ int last_at_most(const T* a, int n, T x) {
+    int lo = 0;
+    for (int w = n; w > 1;) {
+        const int h = w >> 1;
+        if (a[lo + h] <= x) { lo += h; w -= h; }
+        else w = h;
+    }
+    return lo;
+}
+
+// Tile t of sequence s for one head, its place on the line and its number.
+struct Tile { int s, head, row0, n_row, p0; Keys keys; int64_t at, rank; int blocks; };
+
+template <int F>
+struct Line {
+    const PlanDeviceArgs& a;
+    const Lists& l;
+    const int64_t* pre;                                     // places of a head's tiles [n_tile + 1]
+    int n_tile;
+    int64_t share;
+
+    __device__ __forceinline__ Tile shape(int s, int t) const {
+        Tile x;
+        const int n_new = l.start[s + 1] - l.start[s], rows = F ? kUnitRows2 : a.rows1;
+        x.s = s;
+        x.p0 = l.n_kv[s] - n_new;
+        x.row0 = t * rows;
+        x.n_row = min(rows, n_new * a.G - x.row0);
+        x.keys = tile_keys(a, x.p0, l.n_kv[s], x.row0, x.n_row, F ? a.align : 1);
+        x.blocks = (int)(((int64_t)x.keys.n + a.bk[F] - 1) / a.bk[F]);
+        return x;
+    }
+    __device__ __forceinline__ Tile tile(int s, int head, int t) const {
+        Tile x = shape(s, t);
+        const int b0 = l.base[F][s], b1 = l.base[F][s + 1];
+        x.head = head;
+        x.rank = (int64_t)b0 * a.Hkv + (int64_t)head * (b1 - b0) + t;
+        x.at = pre[b0] * a.Hkv + head * (pre[b1] - pre[b0]) + pre[b0 + t] - pre[b0];
+        return x;
+    }
+    // number r in the plan's order: sequences, heads, tiles
+    __device__ __forceinline__ Tile ranked(int64_t r) const {
+        const int32_t* base = l.base[F];
+        const int s = last_at_most(base, a.n_seq, (int)(r / a.Hkv));
+        const int T = base[s + 1] - base[s], rem = (int)(r - (int64_t)base[s] * a.Hkv), head = rem / T;
+        return tile(s, head, rem - head * T);
+    }
+    // the tile at place x of the line
+    __device__ __forceinline__ Tile at(int64_t x) const {
+        const int32_t* base = l.base[F];
+        // tiles of a sequence: the sequence of the last tile whose place, all heads before it counted, is not after x
+        int lo = 0;
+        for (int w = n_tile; w > 1;) {
+            const int h = w >> 1;
+            if (pre[lo + h] * a.Hkv <= x) { lo += h; w -= h; }
+            else w = h;
+        }
+        // (lo may be any tile of the sequence: its own head's place comes first in the sequence's stretch)
+        const int s = last_at_most(base, a.n_seq, lo);
+        const int b0 = base[s], T = base[s + 1] - b0;
+        const int64_t one = pre[b0 + T] - pre[b0], in = x - pre[b0] * a.Hkv;
+        const int head = (int)quotient(in, one);
+        const int64_t y = pre[b0] + in - head * one;
+        return tile(s, head, last_at_most(pre + b0, T, y));
+    }
+    __device__ __forceinline__ static int64_t quotient(int64_t x, int64_t y) {
+        return (x | y) >> 32 ? x / y : (int64_t)((uint32_t)x / (uint32_t)y);
+    }
+    __device__ __forceinline__ int cta_at(int64_t x) const { return (int)quotient(x, share); }
+    // block at which CTA c's part of a tile begins
+    __device__ __forceinline__ int cut_at(const Tile& x, int c) const {
+        return (int)min(max(c * share - x.at - a.cost[F], (int64_t)0), (int64_t)x.blocks);
+    }
+    // the CTAs of a tile's first place, first unit (another where only the fixed cost lies in the former) and last unit
+    __device__ __forceinline__ void span(const Tile& x, int& c0, int& cf, int& c1) const {
+        c0 = cta_at(x.at);
+        c1 = cta_at(x.at + x.blocks + a.cost[F] - 1);
+        cf = c1 > c0 && (c0 + 1) * share - x.at <= a.cost[F] ? c0 + 1 : c0;
+    }
 };
 
 // The units of form F; returns its number of cut tiles, -1 without units.
 template <int F>
-__device__ int make_units(const PlanDeviceArgs& a, Shared& sh) {
-    const int tid = threadIdx.x, n_tile = a.tile_base[F][a.n_seq];
+__device__ int make_units(const PlanDeviceArgs& a, const Lists& l, Shared& sh) {
+    const int tid = threadIdx.x, n_tile = l.base[F][a.n_seq];
     if (n_tile == 0) return -1;
+    int64_t* pre = n_tile <= kTiles ? sh.pre : a.tile_pre[F];
+    Line<F> line{a, l, pre, n_tile, 1};
     int64_t total = 0;
     for (int t0 = 0; t0 < n_tile; t0 += kThr) {
         const int t = t0 + tid;
         int64_t len = 0, all;
         if (t < n_tile) {
-            const int s = seq_of(a.tile_base[F], a.n_seq, t);
-            len = tile_of<F>(a, s, t - a.tile_base[F][s]).len;
+            const int s = last_at_most(l.base[F], a.n_seq, t);
+            len = line.shape(s, t - l.base[F][s]).blocks + a.cost[F];
         }
         const int64_t before = block_sum(len, sh.scan, all);
-        if (t < n_tile) a.tile_pre[F][t] = total + before;
+        if (t < n_tile) pre[t] = total + before;
         total += all;
     }
+    if (tid == 0) pre[n_tile] = total;
     const int n_cta = a.n_cta[F], cost = a.cost[F], bk = a.bk[F];
-    const int64_t line = total * a.Hkv, share = max((line + n_cta - 1) / n_cta, (int64_t)cost + 1);
-    auto cta_at = [&](int64_t x) { return (int)((x | share) >> 32 ? x / share : (int64_t)((uint32_t)x / (uint32_t)share)); };
-    for (int c = tid; c <= n_cta; c += kThr) sh.cut[c] = sh.cut_tile[c] = 0;
+    const int64_t length = total * a.Hkv, n_rank = (int64_t)n_tile * a.Hkv;
+    const int64_t share = max(Line<F>::quotient(length + n_cta - 1, n_cta), (int64_t)cost + 1);
+    line.share = share;
     __syncthreads();
-    const int64_t n_rank = (int64_t)n_tile * a.Hkv;
-    const int lane = tid % kLanes;
-    for (int64_t r = tid / kLanes; r < n_rank; r += kThr / kLanes) {
-        const Tile x = ranked<F>(a, r, total);
-        const int c0 = cta_at(x.at), c1 = cta_at(x.at + x.len - 1);
-        for (int c = c0 + 1 + lane; c <= c1; c += kLanes)
-            if (c * share - x.at > cost) {
-                sh.cut[c] = 1;
-                sh.cut_tile[c] = c == c0 + 1 || (c - 1) * share - x.at <= cost;
-            }
+    // a thread per CTA end: the tile that it falls into, and whether it cuts it
+    const int c = tid;
+    const bool end = c <= n_cta && c * share < length;
+    Tile mine;
+    int c0 = 0, cf = 0, c1 = 0;
+    bool cuts = false;
+    int64_t own = 0, all;
+    if (end) {
+        mine = line.at(c * share);
+        line.span(mine, c0, cf, c1);
+        cuts = c > c0 && c * share - mine.at > cost;
+        own = cuts ? (int64_t)1 << 32 | (c == cf + 1) : 0;
     }
+    const int64_t sum = block_sum(own, sh.scan, all) + own;
+    if (c <= n_cta) { sh.cut[c] = (int)(sum >> 32); sh.cut_tile[c] = (int)(sum & 0x7fffffff); }
     __syncthreads();
-    {   // (both sums at once)
-        int64_t all;
-        const int64_t own = tid <= n_cta ? (int64_t)sh.cut[tid] << 32 | sh.cut_tile[tid] : 0;
-        const int64_t sum = block_sum(own, sh.scan, all) + own;
-        if (tid <= n_cta) { sh.cut[tid] = (int)(sum >> 32); sh.cut_tile[tid] = (int)(sum & 0x7fffffff); }
-        __syncthreads();
+    // the unit of tile x that belongs to CTA u_c
+    auto write = [&](const Tile& x, int t0, int tf, int t1, int u_c) {
+        const int u0 = (int)x.rank + sh.cut[t0], n = t1 - tf + 1;
+        AttnUnit u{};
+        u.tok0 = l.start[x.s];
+        u.row0 = x.row0;
+        u.n_row = x.n_row;
+        u.p0 = x.p0;
+        u.table = l.off[x.s];
+        u.n_sink_keys = x.keys.n_sink;
+        u.key_lo = x.keys.lo;
+        u.v0 = u_c == tf ? 0 : line.cut_at(x, u_c) * bk;
+        u.v1 = u_c == t1 ? x.keys.n : line.cut_at(x, u_c + 1) * bk;
+        u.n_chunk = n;
+        u.chunk = u_c - tf;
+        u.part = n > 1 ? sh.cut[t0] + sh.cut_tile[t0] : 0;
+        u.ticket = n > 1 ? sh.cut_tile[t0] : 0;
+        u.head = x.head;
+        int4* d = reinterpret_cast<int4*>(a.units[F] + u0 + u.chunk);
+        const int4* q = reinterpret_cast<const int4*>(&u);
+        d[0] = q[0]; d[1] = q[1]; d[2] = q[2]; d[3] = q[3];
+        if (F && n > 1 && u_c == tf) a.cuts[u.ticket] = u0;
+    };
+    if (cuts) write(mine, c0, cf, c1, c);
+    // where each CTA's units begin
+    if (c <= n_cta) a.first[F][c] = end ? (int)mine.rank + sh.cut[c0] + max(0, c - cf) : (int)n_rank + sh.cut[n_cta];
+    // and each tile's first unit
+    for (int64_t r = tid; r < n_rank; r += kThr) {
+        const Tile x = line.ranked(r);
+        int t0, tf, t1;
+        line.span(x, t0, tf, t1);
+        write(x, t0, tf, t1, tf);
     }
-    for (int64_t r = tid / kLanes; r < n_rank; r += kThr / kLanes) {
-        const Tile x = ranked<F>(a, r, total);
-        const int c0 = cta_at(x.at), c1 = cta_at(x.at + x.len - 1);
-        // the CTA of the first unit: not c0 where only the fixed cost lies there
-        const int cf = c1 > c0 && (c0 + 1) * share - x.at <= cost ? c0 + 1 : c0;
-        const int u0 = (int)x.rank + sh.cut[c0], n = c1 - cf + 1;
-        const int blocks = (int)(x.len - cost);
-        auto cut_at = [&](int c) { return (int)min(max(c * share - x.at - cost, (int64_t)0), (int64_t)blocks); };
-        for (int c = cf + lane; c <= c1; c += kLanes) {
-            AttnUnit u{};
-            u.tok0 = a.start[x.s];
-            u.row0 = x.row0;
-            u.n_row = x.n_row;
-            u.p0 = x.p0;
-            u.table = a.table_off[x.s];
-            u.n_sink_keys = x.keys.n_sink;
-            u.key_lo = x.keys.lo;
-            u.v0 = c == cf ? 0 : cut_at(c) * bk;
-            u.v1 = c == c1 ? x.keys.n : cut_at(c + 1) * bk;
-            u.n_chunk = n;
-            u.chunk = c - cf;
-            u.part = n > 1 ? sh.cut[c0] + sh.cut_tile[c0] : 0;
-            u.ticket = n > 1 ? sh.cut_tile[c0] : 0;
-            u.head = x.head;
-            int4* d = reinterpret_cast<int4*>(a.units[F] + u0 + u.chunk);
-            const int4* q = reinterpret_cast<const int4*>(&u);
-            d[0] = q[0]; d[1] = q[1]; d[2] = q[2]; d[3] = q[3];
-            if (F && n > 1 && c == cf) a.cuts[u.ticket] = u0;
-        }
-        // CTA ends in this tile: where the CTA's units begin
-        for (int c = c0 + (c0 * share < x.at) + lane; c <= c1; c += kLanes) a.first[F][c] = u0 + max(0, c - cf);
-    }
-    for (int c = cta_at(line - 1) + 1 + tid; c <= n_cta; c += kThr) a.first[F][c] = (int)n_rank + sh.cut[n_cta];
     return sh.cut_tile[n_cta];
 }
 
@@ -205,18 +245,21 @@ __global__ void __launch_bounds__(kThr) attn_plan_kernel(PlanDeviceArgs a) {
         int done = 0;
         for (int s = blockIdx.x - 1; s < a.n_seq; s += gridDim.x - 1) {
             int64_t mine = 0, all;
-            for (int i = done + tid; i < s; i += kThr) mine += pages_of(a, i);
+            for (int i = done + tid; i < s; i += kThr) mine += pages_of(a, a.n_kv[i]);
             block_sum(mine, sh.scan, all);
             at += all;
             done = s;
-            const int64_t n = min(min(pages_of(a, s), (int64_t)a.ld_table), a.max_table - at);
+            const int64_t n = min(min(pages_of(a, a.n_kv[s]), (int64_t)a.ld_table), a.max_table - at);
             const int32_t* from = a.table + (int64_t)s * a.ld_table;
             for (int64_t i = tid; i < n; i += kThr) a.table_out[at + i] = from[i];
         }
         return;
     }
     // the step's lengths
-    bool bad = tid == 0 && (a.start[0] != 0 || a.start[a.n_seq] > a.max_tok);
+    const bool small = a.n_seq <= kSeqs;
+    const Lists l{small ? sh.start : a.start, small ? sh.n_kv : a.n_kv, small ? sh.off : a.table_off,
+                  {small ? sh.base[0] : a.tile_base[0], small ? sh.base[1] : a.tile_base[1]}};
+    bool bad = tid == 0 && a.start[0] != 0;
     int64_t pages = 0;
     int tiles[2] = {0, 0};
     for (int s0 = 0; s0 < a.n_seq; s0 += kThr) {
@@ -224,35 +267,42 @@ __global__ void __launch_bounds__(kThr) attn_plan_kernel(PlanDeviceArgs a) {
         int64_t pg = 0, all;
         int T[2] = {0, 0};
         if (s < a.n_seq) {
-            const int64_t n_new = (int64_t)a.start[s + 1] - a.start[s];
-            const int n_kv = a.n_kv[s];
-            pg = pages_of(a, s);
-            if (n_new < 0 || n_new > a.max_new || n_new > a.max_tok || n_kv < 0 || n_kv > a.max_keys || pg > a.ld_table) {
+            const int from = a.start[s], to = a.start[s + 1], n_kv = a.n_kv[s];
+            const int64_t n_new = (int64_t)to - from;
+            if (small) {
+                sh.start[s] = from;
+                sh.start[s + 1] = to;                       // (the next thread writes the same)
+                sh.n_kv[s] = n_kv;
+            }
+            pg = pages_of(a, n_kv);
+            if (n_new < 0 || n_new > a.max_new || to > a.max_tok || n_kv < 0 || n_kv > a.max_keys || pg > a.ld_table) {
                 bad = true;
             } else {
-                const int f = form_of(a, (int)n_new), step = f ? kUnitRows2 : a.rows1;
+                const int f = a.tc && n_new * a.G >= a.tc_rows ? 1 : 0, step = f ? kUnitRows2 : a.rows1;
                 T[f] = ((int)n_new * a.G + step - 1) / step;
             }
         }
         const int64_t p = block_sum(pg, sh.scan, all);
-        if (s < a.n_seq) a.table_off[s] = (int)min(pages + p, a.max_table);
+        if (s < a.n_seq) l.off[s] = (int)min(pages + p, a.max_table);
         pages += all;
         const int64_t t = block_sum((int64_t)T[1] << 32 | (uint32_t)T[0], sh.scan, all);
         if (s < a.n_seq) {
-            a.tile_base[0][s] = tiles[0] + (int)(uint32_t)t;
-            a.tile_base[1][s] = tiles[1] + (int)(t >> 32);
+            l.base[0][s] = tiles[0] + (int)(uint32_t)t;
+            l.base[1][s] = tiles[1] + (int)(t >> 32);
         }
         // (a bad step may have any sums; nobody looks at them)
         tiles[0] += (int)(uint32_t)all;
         tiles[1] += (int)(all >> 32);
     }
-    if (tid < 2) a.tile_base[tid][a.n_seq] = tiles[tid];
+    if (tid < 2) l.base[tid][a.n_seq] = tiles[tid];
     bad = __syncthreads_or(bad) || pages > a.max_table;
     int n0 = -1, n1 = -1;
     if (!bad) {
-        n0 = make_units<0>(a, sh);
-        __syncthreads();
-        n1 = make_units<1>(a, sh);
+        n0 = make_units<0>(a, l, sh);
+        if (a.tc) {
+            __syncthreads();
+            n1 = make_units<1>(a, l, sh);
+        }
     }
     if (tid == 0) {
         a.hdr[PH_FORM] = (n0 >= 0 ? a.rows1 == 8 ? ATTN_FORM_ROWS8 : ATTN_FORM_ROWS16 : 0) | (n1 >= 0 ? ATTN_FORM_TC : 0);

@@ -403,7 +403,7 @@ llm_attn_plan* llm_attn_plan_init(const llm_attn_shape* s, const llm_kv_pages* k
     get(&p->redo, (size_t)std::max<int64_t>(1, p->caps.units2) * sizeof(int32_t));
     get(&p->err, sizeof(uint32_t));
     get(&p->lists, (3 * (size_t)s->max_seq + 2) * sizeof(int32_t));
-    get(&p->tile_pre, (size_t)(p->caps.tiles1 + p->caps.tiles2) * sizeof(int64_t));
+    get(&p->tile_pre, (size_t)(p->caps.tiles1 + p->caps.tiles2 + 2) * sizeof(int64_t));
     if (e == cudaSuccess) {
         void* h = nullptr;
         e = cudaMallocHost(&h, p->bytes);
@@ -537,7 +537,7 @@ int llm_attn_plan_set_device(llm_attn_plan* p, int32_t n_seq, const int32_t* sta
         a.first[f] = reinterpret_cast<int32_t*>(p->d_buf + p->off_first[f]);
         a.units[f] = reinterpret_cast<AttnUnit*>(p->d_buf + p->off_units[f]);
         a.tile_base[f] = p->lists + f * ((size_t)p->shape.max_seq + 1);
-        a.tile_pre[f] = p->tile_pre + f * p->caps.tiles1;
+        a.tile_pre[f] = p->tile_pre + f * (p->caps.tiles1 + 1);
     }
     a.table_off = p->lists + 2 * ((size_t)p->shape.max_seq + 1);
     a.err = p->err;

@@ -70,11 +70,12 @@ __device__ __forceinline__ int last_at_most(const uint32_t* a, int n, uint32_t x
     return lo;
 }
 
-struct Seq { uint32_t have, add, held, need; bool bad; };
+struct Seq { uint32_t have, add, held, need; int given; bool bad; };
 __device__ __forceinline__ Seq seq_extend(const PageListArgs& a, int i) {
-    Seq q{0u, 0u, 0u, 0u, false};
+    Seq q{0u, 0u, 0u, 0u, 0, false};
     if (i >= a.n_seq) return q;
     const int have = a.n_kv[i], add = a.n_new[i];
+    q.given = have;
     const uint32_t ps = (uint32_t)a.page_size;
     q.bad = have < 0 || add < 0 || add > a.max_tok || (int64_t)have + add > INT32_MAX;
     if (q.bad) return q;
@@ -96,9 +97,11 @@ __global__ void __launch_bounds__(kThr) pages_extend_kernel(PageListArgs a, int 
     // whether the step fits: sums over all sequences
     uint32_t tok = 0u, page = 0u;
     bool bad = n_free < 0 || n_free > a.max_free;
+    int mine = 0;                                           // the new length, where a thread has one sequence
     Sums at{};
     for (int c = 0; c < n_chunk; ++c) {
         const Seq q = seq_extend(a, c * nt + tid);
+        mine = q.given + (int)q.add;
         bad = bad || q.bad;
         at = block_sums(q.add, q.need, s_scan);
         tok = add_sat(tok, at.all_x);
@@ -106,6 +109,7 @@ __global__ void __launch_bounds__(kThr) pages_extend_kernel(PageListArgs a, int 
         s_tok[tid] = at.x; s_page[tid] = at.y; s_have[tid] = q.have;
     }
     bad = __syncthreads_or(bad) || tok > (uint32_t)a.max_tok || page > (uint32_t)n_free;
+    if (bad && n_chunk == 1) mine = tid < a.n_seq ? a.n_kv[tid] : 0;
     if (!bad) {
         uint32_t tok0 = 0u, page0 = 0u;                     // before the sequences at hand
         for (int c = 0; c < n_chunk; ++c) {
@@ -145,9 +149,14 @@ __global__ void __launch_bounds__(kThr) pages_extend_kernel(PageListArgs a, int 
         }
     }
     for (int t = (int)tok + rank * nt + tid; t < a.max_tok; t += n_cta * nt) a.cell[t] = a.pos[t] = -1;
-    cluster_sync();                                         // everybody has read the lengths
+    if (n_cta > 1) cluster_sync();                          // everybody has read the lengths
+    else __syncthreads();
     if (rank == 0) {
-        for (int i = tid; i < a.n_seq; i += nt) a.n_kv_out[i] = a.n_kv[i] + (bad ? 0 : a.n_new[i]);
+        if (n_chunk == 1) {
+            if (tid < a.n_seq) a.n_kv_out[tid] = mine;
+        } else {
+            for (int i = tid; i < a.n_seq; i += nt) a.n_kv_out[i] = a.n_kv[i] + (bad ? 0 : a.n_new[i]);
+        }
         if (tid == 0) {
             a.start[a.n_seq] = (int)tok;
             *a.n_free_out = n_free - (int)page;
@@ -210,7 +219,8 @@ __global__ void __launch_bounds__(kThr) pages_trim_kernel(PageListArgs a, int n_
         page = 0u;
         if (rank == 0 && tid == 0 && a.err) atomicOr(a.err, ERR_STEP_RANGE);
     }
-    cluster_sync();
+    if (n_cta > 1) cluster_sync();
+    else __syncthreads();
     if (rank == 0) {
         for (int i = tid; i < a.n_seq; i += nt) a.n_kv_out[i] = bad ? a.n_kv[i] : seq_trim(a, i).left;
         if (tid == 0) *a.n_free_out = n_free + (int)page;
@@ -222,7 +232,8 @@ bool go(void (*kernel)(PageListArgs, int), const PageListArgs& a, int64_t work, 
     const int n_cta = (int)(work <= 2 * kThr ? 1 : work <= 8 * kThr ? 4 : 8);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(n_cta);
-    cfg.blockDim = dim3(kThr);
+    // fewer threads meet faster at the barriers
+    cfg.blockDim = dim3(a.n_seq <= 256 && work <= 512 ? 256 : kThr);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;

@@ -181,7 +181,7 @@ struct PlanDeviceArgs {
     int32_t n_seq = 0, ld_table = 0, max_new = 0, max_tok = 0, max_keys = 0;
     int64_t max_table = 0;
     const int32_t *start = nullptr, *n_kv = nullptr, *table = nullptr;
-    // the plan's buffers; scratch: tiles before each sequence [max_seq + 1], each tile's place, each sequence's table
+    // the plan's buffers; scratch: tiles before each sequence [max_seq + 1], each tile's place [tiles + 1], each sequence's table
     int32_t* hdr = nullptr;
     int32_t *first[2] = {nullptr, nullptr}, *cuts = nullptr, *table_out = nullptr;
     AttnUnit* units[2] = {nullptr, nullptr};
