@@ -396,7 +396,8 @@ attn_rows_kernel(AttnPagedArgs a) {
                         const int at = 4 * C::KC * (4 * i + c);   // byte of the row
                         take<C::KC>(&k[b][t][C::KC * i], st + at16<C::ROWB>(16 * b + 8 * t + g, at >> 4) + (at & 15));
                     }
-            uint32_t kbs[2][2][2], kh[2][2][4];             // E2M1: scales of the lane's blocks, as f16 pairs; a word's values
+            __half2 kbs[2][2];                              // E2M1: the scales of the lane's two blocks (of its one: twice)
+            uint32_t kh[2][2][4];                           // ... and a word's values
             if constexpr (F4) {
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
@@ -405,10 +406,10 @@ attn_rows_kernel(AttnPagedArgs a) {
                         const uint8_t* p = st + C::BLK + C::NB * (16 * b + 8 * t + g);
                         if constexpr (C::NB == 8) {
                             const uint32_t h = e4m3x2_to_h2(reinterpret_cast<const uint16_t*>(p)[c]);
-                            kbs[b][t][0] = __byte_perm(h, h, 0x1010);
-                            kbs[b][t][1] = __byte_perm(h, h, 0x3232);
+                            kbs[b][t] = *reinterpret_cast<const __half2*>(&h);
                         } else {
-                            kbs[b][t][0] = e4m3x2_to_h2(0x101u * p[C::NB == 4 ? c : c >> 1]);
+                            const uint32_t h = e4m3x2_to_h2(0x101u * p[C::NB == 4 ? c : c >> 1]);
+                            kbs[b][t] = *reinterpret_cast<const __half2*>(&h);
                         }
                     }
             }
@@ -434,11 +435,12 @@ attn_rows_kernel(AttnPagedArgs a) {
                                 e2m1x8_to_h2(k[b][0][j / 2], kh[b][0]);
                                 e2m1x8_to_h2(k[b][1][j / 2], kh[b][1]);
                             }
-                            const int y = C::NB == 8 ? j / 4 : 0;   // (32 dims of a lane: two blocks)
-                            ka[0] = mul_h2(kh[b][0][2 * (j % 2)], kbs[b][0][y]);
-                            ka[1] = mul_h2(kh[b][1][2 * (j % 2)], kbs[b][1][y]);
-                            ka[2] = mul_h2(kh[b][0][2 * (j % 2) + 1], kbs[b][0][y]);
-                            ka[3] = mul_h2(kh[b][1][2 * (j % 2) + 1], kbs[b][1][y]);
+                            // (both halves of a product take one scale: the instruction picks it)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const __half2 s = C::NB == 8 && j >= 4 ? __high2half2(kbs[b][e & 1]) : __low2half2(kbs[b][e & 1]);
+                                ka[e] = mul_h2(kh[b][e & 1][2 * (j % 2) + (e >> 1)], *reinterpret_cast<const uint32_t*>(&s));
+                            }
                         } else if constexpr (F8) {
                             e4m3x4_to_h2(k[b][0][C::KC * i + j], ka[0], ka[2]);
                             e4m3x4_to_h2(k[b][1][C::KC * i + j], ka[1], ka[3]);

@@ -22,27 +22,41 @@ constexpr int kMaxCtas = 2 * 160;
 constexpr int kSeqs = 512, kTiles = 1024;                   // steps up to this size are planned in shared memory
 static_assert(kMaxCtas + 1 <= kThr, "one thread per CTA end");
 
-// Running sums of a number per thread over the block, without the thread's own; `all` receives the total.
-__device__ __forceinline__ int64_t block_sum(int64_t x, int64_t* s /* [32] */, int64_t& all) {
+// Running sums of N numbers per thread over the block, without the thread's own; `all` receives the totals.
+template <int N>
+__device__ __forceinline__ void block_sums(const int64_t* x, int64_t* s /* [16 N] */, int64_t* before, int64_t* all) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t in = x;
+    constexpr int W = kThr / 32;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t p = __shfl_up_sync(0xffffffffu, in, o);
-        if (lane >= o) in += p;
+    for (int i = 0; i < N; ++i) {
+        int64_t in = x[i];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t p = __shfl_up_sync(0xffffffffu, in, o);
+            if (lane >= o) in += p;
+        }
+        if (lane == 31) s[W * i + warp] = in;
+        before[i] = in - x[i];
     }
-    if (lane == 31) s[warp] = in;
     __syncthreads();
-    int64_t w = lane < kThr / 32 ? s[lane] : 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t p = __shfl_up_sync(0xffffffffu, w, o);
-        if (lane >= o) w += p;
+    for (int i = 0; i < N; ++i) {
+        int64_t w = lane < W ? s[W * i + lane] : 0;
+#pragma unroll
+        for (int o = 1; o < W; o <<= 1) {
+            const int64_t p = __shfl_up_sync(0xffffffffu, w, o);
+            if (lane >= o) w += p;
+        }
+        all[i] = __shfl_sync(0xffffffffu, w, W - 1);
+        const int64_t b = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
+        if (warp) before[i] += b;
     }
-    all = __shfl_sync(0xffffffffu, w, 31);
-    const int64_t before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
     __syncthreads();                                        // s may be written again
-    return (warp ? before : 0) + in - x;
+}
+__device__ __forceinline__ int64_t block_sum(int64_t x, int64_t* s, int64_t& all) {
+    int64_t before;
+    block_sums<1>(&x, s, &before, &all);
+    return before;
 }
 
 struct Keys { int32_t n_sink, lo, n; };
@@ -57,14 +71,14 @@ __device__ __forceinline__ Keys tile_keys(const PlanDeviceArgs& a, int p0, int n
         k.n = hi;
         return k;
     }
-    k.lo = min(hi, first(pmin - a.window + 1)) / align * align;
-    k.n_sink = min(k.lo, (first(a.n_sink) + align - 1) / align * align);
+    k.lo = min(hi, first(pmin - a.window + 1)) & -align;    // (a power of two)
+    k.n_sink = min(k.lo, (first(a.n_sink) + align - 1) & -align);
     k.n = k.n_sink + hi - k.lo;
     return k;
 }
 
 __device__ __forceinline__ int64_t pages_of(const PlanDeviceArgs& a, int n_kv) {
-    return n_kv <= 0 ? 0 : ((int64_t)n_kv + a.page_size - 1) / a.page_size;
+    return n_kv <= 0 ? 0 : ((uint32_t)n_kv + (uint32_t)a.page_size - 1u) / (uint32_t)a.page_size;
 }
 
 struct Shared {
@@ -89,7 +103,8 @@ __device__ __forceinline__ int last_at_most(const T* a, int n, T x) {
 }
 
 // Tile t of sequence s for one head, its place on the line and its number.
-struct Tile { int s, head, row0, n_row, p0; Keys keys; int64_t at, rank; int blocks; };
+// (The numbers of all tiles and heads fit 32 bits: there are not more of them than rows.)
+struct Tile { int s, head, row0, n_row, p0, rank, blocks; Keys keys; int64_t at; };
 
 template <int F>
 struct Line {
@@ -107,22 +122,22 @@ struct Line {
         x.row0 = t * rows;
         x.n_row = min(rows, n_new * a.G - x.row0);
         x.keys = tile_keys(a, x.p0, l.n_kv[s], x.row0, x.n_row, F ? a.align : 1);
-        x.blocks = (int)(((int64_t)x.keys.n + a.bk[F] - 1) / a.bk[F]);
+        x.blocks = (int)(((uint32_t)x.keys.n + (uint32_t)a.bk[F] - 1u) / (uint32_t)a.bk[F]);
         return x;
     }
     __device__ __forceinline__ Tile tile(int s, int head, int t) const {
         Tile x = shape(s, t);
         const int b0 = l.base[F][s], b1 = l.base[F][s + 1];
         x.head = head;
-        x.rank = (int64_t)b0 * a.Hkv + (int64_t)head * (b1 - b0) + t;
+        x.rank = b0 * a.Hkv + head * (b1 - b0) + t;
         x.at = pre[b0] * a.Hkv + head * (pre[b1] - pre[b0]) + pre[b0 + t] - pre[b0];
         return x;
     }
     // number r in the plan's order: sequences, heads, tiles
-    __device__ __forceinline__ Tile ranked(int64_t r) const {
+    __device__ __forceinline__ Tile ranked(int r) const {
         const int32_t* base = l.base[F];
-        const int s = last_at_most(base, a.n_seq, (int)(r / a.Hkv));
-        const int T = base[s + 1] - base[s], rem = (int)(r - (int64_t)base[s] * a.Hkv), head = rem / T;
+        const int s = last_at_most(base, a.n_seq, r / a.Hkv);
+        const int T = base[s + 1] - base[s], rem = r - base[s] * a.Hkv, head = rem / T;
         return tile(s, head, rem - head * T);
     }
     // the tile at place x of the line
@@ -180,7 +195,8 @@ __device__ int make_units(const PlanDeviceArgs& a, const Lists& l, Shared& sh) {
     }
     if (tid == 0) pre[n_tile] = total;
     const int n_cta = a.n_cta[F], cost = a.cost[F], bk = a.bk[F];
-    const int64_t length = total * a.Hkv, n_rank = (int64_t)n_tile * a.Hkv;
+    const int64_t length = total * a.Hkv;
+    const int n_rank = n_tile * a.Hkv;
     const int64_t share = max(Line<F>::quotient(length + n_cta - 1, n_cta), (int64_t)cost + 1);
     line.share = share;
     __syncthreads();
@@ -202,7 +218,7 @@ __device__ int make_units(const PlanDeviceArgs& a, const Lists& l, Shared& sh) {
     __syncthreads();
     // the unit of tile x that belongs to CTA u_c
     auto write = [&](const Tile& x, int t0, int tf, int t1, int u_c) {
-        const int u0 = (int)x.rank + sh.cut[t0], n = t1 - tf + 1;
+        const int u0 = x.rank + sh.cut[t0], n = t1 - tf + 1;
         AttnUnit u{};
         u.tok0 = l.start[x.s];
         u.row0 = x.row0;
@@ -225,9 +241,9 @@ __device__ int make_units(const PlanDeviceArgs& a, const Lists& l, Shared& sh) {
     };
     if (cuts) write(mine, c0, cf, c1, c);
     // where each CTA's units begin
-    if (c <= n_cta) a.first[F][c] = end ? (int)mine.rank + sh.cut[c0] + max(0, c - cf) : (int)n_rank + sh.cut[n_cta];
+    if (c <= n_cta) a.first[F][c] = end ? mine.rank + sh.cut[c0] + max(0, c - cf) : n_rank + sh.cut[n_cta];
     // and each tile's first unit
-    for (int64_t r = tid; r < n_rank; r += kThr) {
+    for (int r = tid; r < n_rank; r += kThr) {
         const Tile x = line.ranked(r);
         int t0, tf, t1;
         line.span(x, t0, tf, t1);
@@ -264,7 +280,7 @@ __global__ void __launch_bounds__(kThr) attn_plan_kernel(PlanDeviceArgs a) {
     int tiles[2] = {0, 0};
     for (int s0 = 0; s0 < a.n_seq; s0 += kThr) {
         const int s = s0 + tid;
-        int64_t pg = 0, all;
+        int64_t pg = 0;
         int T[2] = {0, 0};
         if (s < a.n_seq) {
             const int from = a.start[s], to = a.start[s + 1], n_kv = a.n_kv[s];
@@ -282,17 +298,18 @@ __global__ void __launch_bounds__(kThr) attn_plan_kernel(PlanDeviceArgs a) {
                 T[f] = ((int)n_new * a.G + step - 1) / step;
             }
         }
-        const int64_t p = block_sum(pg, sh.scan, all);
-        if (s < a.n_seq) l.off[s] = (int)min(pages + p, a.max_table);
-        pages += all;
-        const int64_t t = block_sum((int64_t)T[1] << 32 | (uint32_t)T[0], sh.scan, all);
+        const int64_t x[2] = {pg, (int64_t)T[1] << 32 | (uint32_t)T[0]};
+        int64_t before[2], all[2];
+        block_sums<2>(x, sh.scan, before, all);
         if (s < a.n_seq) {
-            l.base[0][s] = tiles[0] + (int)(uint32_t)t;
-            l.base[1][s] = tiles[1] + (int)(t >> 32);
+            l.off[s] = (int)min(pages + before[0], a.max_table);
+            l.base[0][s] = tiles[0] + (int)(uint32_t)before[1];
+            l.base[1][s] = tiles[1] + (int)(before[1] >> 32);
         }
         // (a bad step may have any sums; nobody looks at them)
-        tiles[0] += (int)(uint32_t)all;
-        tiles[1] += (int)(all >> 32);
+        pages += all[0];
+        tiles[0] += (int)(uint32_t)all[1];
+        tiles[1] += (int)(all[1] >> 32);
     }
     if (tid < 2) l.base[tid][a.n_seq] = tiles[tid];
     bad = __syncthreads_or(bad) || pages > a.max_table;
