@@ -160,17 +160,12 @@ __device__ __forceinline__ float* scale_ptr(const PagedKv& kv, const RowAt& r) {
     return (r.v ? kv.vs : kv.ks) + (int64_t)r.page * kv.ss_page + r.at * kv.ss_cell + r.g * kv.ss_head;
 }
 
-__device__ __forceinline__ uint8_t* block_ptr(const PagedKv& kv, const RowAt& r) {
-    return (r.v ? kv.vb : kv.kb) + (int64_t)r.page * kv.sk_page + r.at * kv.sk_cell + r.g * kv.sk_head + r.part;
-}
-
 template <int HD, int CT, int T>
 __global__ void __launch_bounds__(kThr) kv_store_kernel(KvRowsArgs a) {
     const RowAt r = row_at<HD>(a);
     float x[kVals] = {};
     if (r.cell >= 0) load_vals<T>(r.v ? a.v : a.k, r.dense, x);
-    if constexpr (CT == W_F8 || CT == W_F4) {
-        float bmax = 0.f;                                   // of the thread's part
+    if constexpr (CT == W_F8) {
         auto row_max = [&](bool finite) {
             float m = 0.f;                                  // (fmaxf passes over NaN)
 #pragma unroll
@@ -178,7 +173,6 @@ __global__ void __launch_bounds__(kThr) kv_store_kernel(KvRowsArgs a) {
                 const float f = fabsf(x[e]);
                 if (!finite || f <= FLT_MAX) m = fmaxf(m, f);
             }
-            bmax = m;
 #pragma unroll
             for (int o = HD / kVals / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
             return m;
@@ -186,28 +180,6 @@ __global__ void __launch_bounds__(kThr) kv_store_kernel(KvRowsArgs a) {
         float amax = row_max(false);
         if (__any_sync(0xffffffffu, amax > FLT_MAX)) amax = row_max(true);
         if (r.cell < 0) return;
-        if constexpr (CT == W_F4) {
-            // 2688 = 1.3125 * 2^11
-            const uint32_t a2 = __float_as_uint(amax);
-            int e = (int)(a2 >> 23) - 127 - 11 + ((a2 & 0x7fffffu) > 0x280000u);
-            e = amax == 0.f ? 0 : max(e, -126);
-            const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-            uint32_t bc = to_e4m3x2(fmaxf(__fdiv_rn(bmax * inv, 6.f), 0x1p-9f), 0.f);
-            const float b = from_e4m3x2(bc).x, rb = __frcp_rn(b);
-            bool nan = false;
-#pragma unroll
-            for (int i = 0; i < kVals; ++i) {
-                nan = nan || x[i] != x[i];
-                // (infinities become 2^12, which is above 6 b: no remainder of theirs is taken)
-                const float y = fminf(fmaxf(x[i] * inv, -0x1p12f), 0x1p12f), q0 = y * rb;
-                x[i] = copysignf(fmaf(fmaf(-q0, b, y), rb, q0), x[i]);
-            }
-            if (nan) bc = 0x7fu;                            // there is no code for NaN: the block is
-            *reinterpret_cast<uint2*>(row_ptr(a.kv, r) + r.part * (kVals / 2)) = make_uint2(to_e2m1x8(x), to_e2m1x8(x + 8));
-            *block_ptr(a.kv, r) = (uint8_t)bc;
-            if (r.part == 0) *scale_ptr(a.kv, r) = __uint_as_float((uint32_t)(e + 127) << 23);
-            return;
-        }
         // 448 = 1.75 * 2^8: e = exponent(amax) - 8, one more above a mantissa of 1.75
         const uint32_t b = __float_as_uint(amax);
         int e = (int)(b >> 23) - 127 - 8 + ((b & 0x7fffffu) > 0x600000u);
@@ -241,19 +213,192 @@ __global__ void __launch_bounds__(kThr) kv_load_kernel(KvRowsArgs a) {
             x[4 * i + 2] = f1.x * s;
             x[4 * i + 3] = f1.y * s;
         }
-    } else if constexpr (CT == W_F4) {
-        const uint2 u = *reinterpret_cast<const uint2*>(row_ptr(a.kv, r) + r.part * (kVals / 2));
-        const float2 b = from_e4m3x2(*block_ptr(a.kv, r));
-        const float s = *scale_ptr(a.kv, r);
-        // (the product with b is exact; with s it rounds where a value is below float32's normal range)
-        from_e2m1x8(u.x, b.x, x);
-        from_e2m1x8(u.y, b.x, x + 8);
-#pragma unroll
-        for (int i = 0; i < kVals; ++i) x[i] *= s;
     } else {
         load_vals<CT>(row_ptr(a.kv, r), r.part * kVals, x);
     }
     store_vals<T>(r.v ? a.v : a.k, r.dense, x);
+}
+
+// ---- F4_E2M1: a thread holds 16 values of K and the same of V, a block each; where they go is worked out once for both.
+struct At4 { int64_t dense, row, blk, scale; int part; bool there; };
+
+template <int HD>
+__device__ __forceinline__ At4 at4(const KvRowsArgs& a) {
+    constexpr uint32_t P = HD / kVals;
+    const uint32_t Hkv = (uint32_t)a.kv.Hkv, ps = (uint32_t)a.kv.page_size;
+    const uint64_t row = (uint64_t)blockIdx.x * (kThr / P) + threadIdx.x / P;   // (token, head)
+    const uint64_t i = (Hkv & (Hkv - 1)) == 0 ? row >> (__ffs(Hkv) - 1) : row >> 32 ? row / Hkv : (uint32_t)row / Hkv;
+    const uint32_t g = (uint32_t)(row - i * Hkv);
+    At4 r;
+    r.part = threadIdx.x % P;
+    const int cell = i < (uint64_t)a.n ? a.cell[i] : -1;
+    const uint32_t c = (uint32_t)max(cell, 0), page = (ps & (ps - 1)) == 0 ? c >> (__ffs(ps) - 1) : c / ps, at = c - page * ps;
+    r.there = cell >= 0 && page < (uint32_t)a.kv.n_pages;
+    if (r.part == 0 && cell >= 0 && !r.there && a.err) atomicOr(a.err, ERR_SLOT_RANGE);
+    r.dense = (int64_t)i * a.s_tok + g * a.s_head + r.part * kVals;
+    r.row = page * a.kv.sb_page + at * a.kv.sb_cell + g * a.kv.sb_head + r.part * (kVals / 2);
+    r.blk = page * a.kv.sk_page + at * a.kv.sk_cell + g * a.kv.sk_head + r.part;
+    r.scale = page * a.kv.ss_page + at * a.kv.ss_cell + g * a.kv.ss_head;
+    return r;
+}
+// A thread's 16 values of the dense rows: whole 32-byte sectors at once where rows lie on their boundaries (two half
+// sectors 16 bytes apart in two instructions cost the load 2 us of 13 for 8192 rows of 8 heads of 128).
+template <int T>
+__device__ __forceinline__ void load_dense(const void* base, int64_t elem, bool wide, float* x) {
+    if (!wide) {
+        load_vals<T>(base, elem, x);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < (T == W_F32 ? 2 : 1); ++i) {
+        uint32_t w[8];
+        const uint8_t* p = static_cast<const uint8_t*>(base) + elem * (T == W_F32 ? 4 : 2) + 32 * i;
+        asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7]) : "l"(p));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if constexpr (T == W_F32) {
+                x[8 * i + j] = __uint_as_float(w[j]);
+            } else if constexpr (T == W_F16) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+                x[2 * j] = f.x; x[2 * j + 1] = f.y;
+            } else {
+                x[2 * j] = __uint_as_float(w[j] << 16);
+                x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+            }
+        }
+    }
+}
+template <int T>
+__device__ __forceinline__ void store_dense(void* base, int64_t elem, bool wide, const float* x) {
+    if (!wide) {
+        store_vals<T>(base, elem, x);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < (T == W_F32 ? 2 : 1); ++i) {
+        uint32_t w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if constexpr (T == W_F32) {
+                w[j] = __float_as_uint(x[8 * i + j]);
+            } else if constexpr (T == W_F16) {
+                const __half2 h = __floats2half2_rn(x[2 * j], x[2 * j + 1]);
+                w[j] = *reinterpret_cast<const uint32_t*>(&h);
+            } else {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
+                w[j] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+        }
+        uint8_t* p = static_cast<uint8_t*>(base) + elem * (T == W_F32 ? 4 : 2) + 32 * i;
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                     "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
+    }
+}
+// the largest of three magnitudes, NaN if one is
+__device__ __forceinline__ float max3_abs(float x, float y, float z) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    return r;
+}
+
+template <int HD, int T>
+__global__ void __launch_bounds__(kThr) kv_store4_kernel(KvRowsArgs a) {
+    const At4 r = at4<HD>(a);
+    float x[2][kVals] = {};
+    if (r.there) {
+        load_dense<T>(a.k, r.dense, a.wide, x[0]);
+        load_dense<T>(a.v, r.dense, a.wide, x[1]);
+    }
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+        float bmax = 0.f;                                   // of the block
+#pragma unroll
+        for (int e = 0; e < kVals; e += 2) bmax = max3_abs(bmax, x[v][e], x[v][e + 1]);
+        bool nan = false;
+        const bool odd = __any_sync(0xffffffffu, !(bmax <= FLT_MAX));
+        if (odd) {                                          // NaN or infinities: the largest of the others
+            bmax = 0.f;
+#pragma unroll
+            for (int e = 0; e < kVals; ++e) {
+                const float f = fabsf(x[v][e]);
+                nan = nan || f != f;
+                if (f <= FLT_MAX) bmax = fmaxf(bmax, f);
+            }
+        }
+        float amax = bmax;
+#pragma unroll
+        for (int o = HD / kVals / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        // 2688 = 1.3125 * 2^11: e = exponent(amax) - 11, one more above that mantissa
+        const uint32_t bits = __float_as_uint(amax);
+        int e = (int)(bits >> 23) - 127 - 11 + ((bits & 0x7fffffu) > 0x280000u);
+        e = amax == 0.f ? 0 : max(e, -126);
+        const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+        uint32_t bc = to_e4m3x2(fmaxf(__fdiv_rn(bmax * inv, 6.f), 0x1p-9f), 0.f);
+        const float b = from_e4m3x2(bc).x, rb = __frcp_rn(b);
+        if (odd) {                                          // infinities: a number that is above 6 b
+            const float top = e + 12 > 127 ? FLT_MAX : __uint_as_float((uint32_t)(e + 12 + 127) << 23);
+#pragma unroll
+            for (int i = 0; i < kVals; ++i) x[v][i] = fminf(fmaxf(x[v][i], -top), top);
+        }
+        // The remainder is exact whatever its rounding mode; downwards, that of -0 is -0, and so the quotient keeps its sign.
+#pragma unroll
+        for (int i = 0; i < kVals; ++i) {
+            const float y = x[v][i] * inv, q0 = y * rb;
+            x[v][i] = fmaf(__fmaf_rd(-q0, b, y), rb, q0);
+        }
+        if (nan) bc = 0x7fu;                                // there is no code for NaN: the block is
+        if (r.there) {
+            *reinterpret_cast<uint2*>((v ? a.kv.v : a.kv.k) + r.row) = make_uint2(to_e2m1x8(x[v]), to_e2m1x8(x[v] + 8));
+            (v ? a.kv.vb : a.kv.kb)[r.blk] = (uint8_t)bc;
+            if (r.part == 0) (v ? a.kv.vs : a.kv.ks)[r.scale] = __uint_as_float((uint32_t)(e + 127) << 23);
+        }
+    }
+}
+
+template <int HD, int T>
+__global__ void __launch_bounds__(kThr) kv_load4_kernel(KvRowsArgs a) {
+    const At4 r = at4<HD>(a);
+    if (!r.there) return;
+    uint2 u[2];
+    uint32_t b[2];
+    float s[2];
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+        u[v] = *reinterpret_cast<const uint2*>((v ? a.kv.v : a.kv.k) + r.row);
+        b[v] = (v ? a.kv.vb : a.kv.kb)[r.blk];
+        s[v] = (v ? a.kv.vs : a.kv.ks)[r.scale];
+    }
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+        // (the product of code and block scale is exact; with s it rounds where a value is below float32's normal range)
+        float x[kVals];
+        const float bs = from_e4m3x2(b[v]).x;
+        from_e2m1x8(u[v].x, bs, x);
+        from_e2m1x8(u[v].y, bs, x + 8);
+#pragma unroll
+        for (int i = 0; i < kVals; ++i) x[i] *= s[v];
+        store_dense<T>(v ? a.v : a.k, r.dense, a.wide, x);
+    }
+}
+
+template <int HD>
+bool go4(KvRowsArgs a, bool store, cudaStream_t st) {
+    const int64_t es = a.type == W_F32 ? 4 : 2;
+    a.wide = ((reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v)) & 31) == 0 && ((a.s_tok | a.s_head) * es) % 32 == 0;
+    constexpr int64_t per = kThr * kVals / HD;
+    const int64_t blocks = ((int64_t)a.n * a.kv.Hkv + per - 1) / per;
+    if (blocks > 0x7fffffff) return false;
+    auto launch = [&](void (*kernel)(KvRowsArgs)) {
+        kernel<<<(unsigned)blocks, kThr, 0, st>>>(a);
+        return cudaGetLastError() == cudaSuccess;
+    };
+    switch (a.type) {
+        case W_F32: return launch(store ? kv_store4_kernel<HD, W_F32> : kv_load4_kernel<HD, W_F32>);
+        case W_F16: return launch(store ? kv_store4_kernel<HD, W_F16> : kv_load4_kernel<HD, W_F16>);
+        case W_BF16: return launch(store ? kv_store4_kernel<HD, W_BF16> : kv_load4_kernel<HD, W_BF16>);
+    }
+    return false;
 }
 
 template <int HD, int CT, int T>
@@ -280,7 +425,7 @@ bool go_ct(const KvRowsArgs& a, bool store, cudaStream_t st) {
         case W_F16: return go_t<HD, W_F16>(a, store, st);
         case W_BF16: return go_t<HD, W_BF16>(a, store, st);
         case W_F8: return go_t<HD, W_F8>(a, store, st);
-        case W_F4: return go_t<HD, W_F4>(a, store, st);
+        case W_F4: return go4<HD>(a, store, st);
     }
     return false;
 }

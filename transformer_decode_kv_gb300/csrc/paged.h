@@ -51,6 +51,7 @@ struct KvRowsArgs {
     const int32_t* cell = nullptr;
     int32_t n = 0;
     uint32_t* err = nullptr;
+    bool wide = false;                           // the dense rows start on 32-byte boundaries
 };
 bool launch_kv_rows_store(const KvRowsArgs& a, cudaStream_t st);
 bool launch_kv_rows_load(const KvRowsArgs& a, cudaStream_t st);
