@@ -427,14 +427,12 @@ __global__ void __launch_bounds__(threads_of(CT), 1) attn_tc_rows_kernel(AttnPag
             const bool is_v = warp == 1;
             const int ps = a.kv.page_size, sh = (ps & (ps - 1)) == 0 ? __ffs(ps) - 1 : -1;
             uint32_t it = is_v ? 1 : 0;                     // tile number, over all units
-            int with_keys = 0;
             bool ok = true, past = false;
             int bulk_at[kRaw] = {-1, -1, -1};               // phase of a raw tile's last bulk copies, -1: none
             for (int ui = ui0; ui < ui1 && ok; ++ui) {
                 const AttnUnit u = load_unit(a.units2 + ui);
                 const int nt = (u.v1 - u.v0 + kKeys - 1) / kKeys;
                 if (nt == 0) continue;
-                const int slot = with_keys++ & 7;
                 int pmin, pmax;
                 unit_positions(a, u, pmin, pmax);
                 const int hid_all = hidden_below(a, pmin);
@@ -470,26 +468,6 @@ __global__ void __launch_bounds__(threads_of(CT), 1) attn_tc_rows_kernel(AttnPag
                     const int pos = a.key_pos ? a.key_pos[u.table + x] : x;
                     return there && !bad && sees(pos, pmax, hid_all, a.n_sink) ? pos : INT_MAX;
                 };
-                // s0: four times the largest scale of the unit's first block (rows of zeros do not count)
-                auto unit_scale = [&](const float* sc, const uint8_t* rw) {
-                    float mx = 0.f;
-#pragma unroll 1
-                    for (int i = lane; i < kKeys; i += 32) {
-                        int page, at;
-                        if (position(u.v0 + i, page, at) == INT_MAX) continue;
-                        const float x = sc[(int64_t)page * a.kv.ss_page + (int64_t)at * a.kv.ss_cell];
-                        if (x != 1.f || !row_is_zero<true>(rw + (int64_t)page * a.kv.sb_page + (int64_t)at * a.kv.sb_cell, HD / 2))
-                            mx = fmaxf(mx, x);
-                    }
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                    return mx > 0.f ? 4.f * mx : 1.f;
-                };
-                if (!is_v) {                                // (both before the unit's first tile is announced)
-                    const float sv = unit_scale(a.kv.vs + (int64_t)u.head * a.kv.ss_head, a.kv.v + (int64_t)u.head * a.kv.sb_head);
-                    const float sk = unit_scale(scales, rows);
-                    if (lane == 0) { s0[2 * slot] = sk; s0[2 * slot + 1] = sv; }
-                }
                 for (int j = 0; j < nt; ++j, it += 2) {
                     const uint32_t rs = it % kRaw, ph = (it / kRaw) & 1u;
                     const uint32_t raw = sa(sm) + M::raw + rs * M::raw_tile;
@@ -1022,7 +1000,22 @@ __global__ void __launch_bounds__(threads_of(CT), 1) attn_tc_rows_kernel(AttnPag
                 ok = wait(&raw_full[rs], (it / kRaw) & 1u) && (it < NS || wait(&kv_empty[stage], ((it / NS) & 1u) ^ 1u));
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                if (x == 0) { inv[0] = 1.f / s0[2 * slot]; inv[1] = 1.f / s0[2 * slot + 1]; }
+                if (x < 2) {
+                    // s0 of the unit's K or V: four times the largest scale of its first block (rows of zeros do not count), from
+                    // the scales that have landed (each of the warps finds the same)
+                    float mx = 0.f;
+#pragma unroll 1
+                    for (int i = lane; i < kKeys; i += 32) {
+                        const float sc = reinterpret_cast<const float*>(raw + M::raw_sc)[i];
+                        if (sc != 1.f || !row_is_zero<true>(raw + i * (HD / 2), HD / 2)) mx = fmaxf(mx, sc);
+                    }
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                    mx = mx > 0.f ? 4.f * mx : 1.f;
+                    if (cw == 0 && lane == 0) s0[2 * slot + x] = mx;
+                    if (x) inv[1] = 1.f / mx;
+                    else inv[0] = 1.f / mx;
+                }
                 // s / s0 of the warp's rows, a row a lane
                 float f = reinterpret_cast<const float*>(raw + M::raw_sc)[32 * cw + lane] * ((x & 1) ? inv[1] : inv[0]);
                 const bool fits = f >= kRatioMin<F4> && f <= kRatioMax<F4>;
