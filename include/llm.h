@@ -397,17 +397,17 @@ int llm_pages_trim(const llm_seq_pages *p, const int32_t *keep, int32_t *n_kv_ou
  * or unwritten cells hold (NaN, infinities) does not reach the output.
  *
  * Scores, softmax sums and outputs are float32, the output rounded once. The weights enter the product with V as f16
- * (half a step is 2^-11) where activations are F16, or BF16 over an F8_E4M3 cache; as two terms (2^-17 or better) for
+ * (half a step is 2^-11) where activations are F16, or BF16 over an F8_E4M3 or F4_E2M1 cache; as two terms (2^-17 or better) for
  * F32 activations and for BF16 caches, but as one bf16 (2^-8) for a BF16 cache where a sequence has 64 rows (token,
  * query head) per KV head or more. Weights below f16's normal range add up to 2^-30 of the largest |v| that the token
  * sees, per key. Rows of an F8_E4M3 cache may have any scales; a chunk of tokens takes far longer (it computes rows
  * one key at a time) where, within the keys of one unit of work, a row that is not zeros has a scale above 2^7
- * or below 2^-15 times the largest of the unit's first 128 keys. So it does where visible cells hold NaN or
- * infinities.
+ * or below 2^-15 times the largest of the unit's first 128 keys (F4_E2M1: 2^6 and 2^-12). So it does where visible cells
+ * hold NaN or infinities.
  *
- * The plan of a step (which rows attend to which cells, split over the GPU) is made on the host once
- * and serves every layer: llm_attn_plan_set validates it and uploads it on `stream`; llm_attn_run
- * launches. A plan owns its workspace, so two runs of one plan must not overlap in time, nor a set and
+ * The plan of a step (which rows attend to which cells, split over the GPU) is made once and serves every layer: on the
+ * host by llm_attn_plan_set, which validates it and uploads it on `stream`, or on the device by
+ * llm_attn_plan_set_device; llm_attn_run launches. Runs work on whichever came last on the device. A plan owns its workspace, so two runs of one plan must not overlap in time, nor a set and
  * a run (use one plan per stream, or order the streams); two graphs that may run at the same time need two
  * plans. A plan, and the memory that its captured runs were given, outlives the graphs that hold them.
  * llm_attn_run may be captured: the graph replays with whatever the plan was last set to, provided

@@ -15,21 +15,26 @@
 // bound. A contraction may be taken in any order, so a lane's 16 bytes of a key row simply are the dims its
 // A fragments hold (Q is loaded in the same order), and a lane's values of four keys become fragments
 // by byte permutes (f16/bf16: pairs of keys; E4M3: 4 x 4 bytes, then the conversion to f16, which is
-// exact). Rows come by asynchronous 16-byte copies, a row by neighbouring lanes, into a warp's own ring in
+// exact; E2M1: nibbles of two keys interleaved by masks, the conversion, and a product with the pair's block scales, which
+// is exact too: 2 and 4 significant bits). Rows come by asynchronous 16-byte copies, a row by neighbouring lanes, into a warp's own ring in
 // shared memory: 32 keys are used while the next are under way, and a ring's 16-byte chunks are permuted so that
 // both ways of reading them are free of bank conflicts. (Lanes copying just the bytes they use would need no
 // permutation, but touch K rows in 64-byte pieces: 5.3 TB/s at most for E4M3 rows of 128 bytes, against
 // 7.0 TB/s for whole rows.)
 //
 // Measured, 32 / 8 heads of 128: 32 single f16 tokens over 1 .. 2304 keys 39 us (156 MB, 4.0 TB/s), 16 over 9k .. 33k
-// E4M3 keys 145 us (709 MB, 4.9 TB/s of the 6.8 that the card copies at), one over 513 keys 12 us, which is
-// latency: the plan, the page table, the rows and the parts' join follow from each other.
+// E4M3 keys 145 us (709 MB, 4.9 TB/s of the 6.8 that the card copies at), over E2M1 keys 103 us (409 MB, 4.0 TB/s), one
+// over 513 keys 12 us, which is latency: the plan, the page table, the rows and the parts' join follow from each other.
+// Over E2M1 keys the arithmetic is as long as the copies: the copies alone take 78 us, all but the copies 86, all
+// but the conversions (two or two and a half instructions per pair of values, one of them on a half-rate pipe) 83, and three
+// warps a scheduler cover each other's latencies only so far (issue slots 57%). Whole runs of a page by bulk copies, from each warp
+// or from one that does nothing else, by wider asynchronous copies, or V converted before the scores are ready, took 107 to 123.
 //
 // Precision: products of f16 (bf16) terms with float32 sums. F16 activations and caches enter as they
 // are. BF16 or F32 activations over an f16-typed product are scaled per row by a power of two (taken out of the
 // scores again), so that no value leaves f16's range; F32 ones enter as two f16 terms (22 bits). P is
 // rounded to f16 (half a step: 2^-11) where activations are f16; for F32 activations and for bf16 products
-// it enters as two terms, so its rounding (2^-8 for bf16) does not show. An E4M3 row's scale multiplies
+// it enters as two terms, so its rounding (2^-8 for bf16) does not show. An E4M3 (or E2M1) row's scale multiplies
 // the score (K) or p (V, relative to E, the largest scale of the values that the query row has seen so far, a power
 // of two, so exact down to f16's subnormals). Each query row has an E of its own: a value that only later tokens see
 // does not push a row's own values out of f16's range. Rows of zeros, whose scale is 1 whatever the others are, do not

@@ -1,6 +1,6 @@
 // Attention of new tokens over a paged cache, 256-row tiles on the fifth-generation tensor cores
-// (tcgen05, accumulators in TMEM): chunks of new tokens, where the products are the bound. F16, BF16 and
-// E4M3 caches, head_dim 64 and 128, F16 or BF16 activations (F32 ones rounded to f16 where the caller's precision is
+// (tcgen05, accumulators in TMEM): chunks of new tokens, where the products are the bound. F16, BF16, E4M3
+// and E2M1 caches, head_dim 64 and 128, F16 or BF16 activations (F32 ones rounded to f16 where the caller's precision is
 // that: see attn_paged_tc_ok).
 //
 // A CTA takes a unit: up to 256 rows of (token, query head) pairs of one KV head, as two halves of 128
@@ -18,7 +18,8 @@
 // Roles (12 warps; warps 0-3 give registers to warps 4-11, whose threads hold a row of scores each): warps
 // 0 and 1 (E4M3: 3 too) bring K and V rows into a ring of 128-byte-swizzled tiles, with the keys' positions: a block whose keys are
 // all read in bulk tensor copies of the runs of neighbouring cells that pages are, others in 16-byte
-// asynchronous copies row by row, and E4M3 rows as raw bytes, converted to f16 from there;
+// asynchronous copies row by row, and E4M3 rows as raw bytes, converted to f16 from there; E2M1: raw rows and scales in a
+// ring of their own, from where four more warps convert them;
 // warp 2 issues the MMAs; warps 4-7 and 8-11 are the two halves' softmax and epilogue (a thread owns a
 // TMEM lane: warp w reads lanes 32 (w % 4) on). m is 6 below a row maximum and raised lazily, when p would
 // pass 2^14: O, in TMEM, is rarely rescaled, and never more than it must. P is rounded to f16 (half a step 2^-11)
@@ -26,14 +27,18 @@
 // the output is rounded to bf16 itself).
 //
 // E4M3 rows enter as f16 numbers q * s / s0 with s0 the largest scale of the unit's first block (a power
-// of two like s; rows of zeros, whose scale is 1, do not count): exact from s0 2^-15 to s0 2^7. A unit with a row out of
+// of two like s; rows of zeros, whose scale is 1, do not count): exact from s0 2^-15 to s0 2^7. E2M1 rows enter as q * b * s /
+// s0, b the block's scale and s0 four times the largest: exact from 2^-12 to 2^6 of that. A unit with a row out of
 // this range is done key by key, after the CTA's other units, as is one with values that are not finite.
 //
 // Measured, 32 / 8 heads of 128: 2048 bf16 tokens at the end of 32768 keys 769 us (1.4 PFLOP/s, 0.72 of the rate of a
 // large bf16 matrix product), bound by what stands between a half's two products (scores out of TMEM, exponentials, P
 // back into TMEM): at the end of 8192 keys the tensor pipe is active for 56% of the time, issue slots are used for 38%, the
 // exponential unit for 29%. 512 f16 tokens at the end of 8192 take 80 us, where cut tiles weigh; over E4M3 1203 and 113
-// us, where the rows' conversion shares issue slots and shared memory with the softmax (tensor pipe 30%, issue slots 37%).
+// us, where the rows' conversion shares issue slots and shared memory with the softmax (tensor pipe 30%, issue slots 37%);
+// over E2M1 814 and 87 us (tensor pipe 41%, issue slots 47%): a third fewer raw bytes, converters that wait for nothing but
+// landed bytes, and code that the instruction cache holds beside the softmax. A unit costs about 20 000 cycles beside its blocks
+// (Q in, hidden keys, epilogue), which is what small units of windowed chunks consist of.
 //
 // Every wait is bounded by a wall-clock limit; a timeout sets ERR_TIMEOUT, ends every role's loop, and
 // the CTA leaves after its copies and with its TMEM freed.
@@ -408,7 +413,8 @@ __global__ void __launch_bounds__(threads_of(CT), 1) attn_tc_rows_kernel(AttnPag
     };
 
     // Each role walks the CTA's units by itself; the barriers above keep them in step. Registers: three warpgroups
-    // of 168 a thread at launch, 504 >= kRegsLow + 2 kRegsHigh. What is spilled comes back from L2 (shared memory
+    // of 168 a thread at launch, 504 >= kRegsLow + 2 kRegsHigh (E2M1: four of 128, of which two keep kRegsLow; 72 + 184 and
+    // 56 + 200 were 1 and 0 % slower). What is spilled comes back from L2 (shared memory
     // leaves L1 little), so both parts count: 2048 new tokens at the end of 32768 E4M3 keys (32 / 8 heads of 128) took
     // 5360 us with 120 + 192 and 3720 us with 152 + 176 while producers held raw rows in registers; with the raw rows in
     // shared memory 1240 us with 104 + 200 and 1190 us as here.

@@ -10,7 +10,8 @@
 //
 // One CTA makes the units, the others copy the page table. It is latency: lengths, four running sums, and two rounds of
 // independent items, the CTAs' ends (a thread finds the tile that its end falls into, and makes the unit that begins there)
-// and the tiles (each its first unit).
+// and the tiles (each its first unit). 32 single tokens with 8 KV heads take 9.5 us (18.5 with the lists in global memory and
+// eight lanes a tile), six chunks of 1228 tokens together 11.
 #include "paged.h"
 
 namespace llm {
