@@ -824,6 +824,7 @@ bool go_types(const AttnPagedArgs& a, cudaStream_t st) {
         if (a.q_type == W_F16) return go<HD, W_F4, W_F16, ROWS>(a, st);
         return a.q_type == W_BF16 ? go<HD, W_F4, W_BF16, ROWS>(a, st) : go<HD, W_F4, W_F32, ROWS>(a, st);
     }
+    if (a.kv.type != W_F8) return false;
     if (a.q_type == W_F16) return go<HD, W_F8, W_F16, ROWS>(a, st);
     return a.q_type == W_BF16 ? go<HD, W_F8, W_BF16, ROWS>(a, st) : go<HD, W_F8, W_F32, ROWS>(a, st);
 }

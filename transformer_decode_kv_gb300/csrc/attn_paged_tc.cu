@@ -1447,6 +1447,7 @@ bool go_hd(const AttnPagedArgs& a, cudaStream_t st) {
         if (a.q_type == W_F16) return go<HD, W_F4, W_F16>(a, st);
         return a.q_type == W_BF16 ? go<HD, W_F4, W_BF16>(a, st) : false;
     }
+    if (a.kv.type != W_F8) return false;
     if (a.q_type == W_F16) return go<HD, W_F8, W_F16>(a, st);
     return a.q_type == W_BF16 ? go<HD, W_F8, W_BF16>(a, st) : go<HD, W_F8, W_F32>(a, st);
 }
