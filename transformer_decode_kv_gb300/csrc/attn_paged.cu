@@ -183,7 +183,10 @@ attn_rows_kernel(AttnPagedArgs a) {
     float (*s_l)[ROWS] = s_m + kWarps;
     int& s_flag = *reinterpret_cast<int*>(s_l + kWarps);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    asm volatile("griddepcontrol.launch_dependents;");      // the 256-row tiles of a mixed plan may start
+    // Launched early (after a plan that was made on the device), nothing is read before the kernel in front has ended; otherwise
+    // there is nothing to wait for. Then the 256-row tiles of a mixed plan may start.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
     const int ui0 = a.first1[blockIdx.x], ui1 = a.first1[blockIdx.x + 1];   // (on their way with the header)
     if (form_missing(a) || (a.hdr[PH_FORM] & (ROWS == 8 ? ATTN_FORM_ROWS8 : ATTN_FORM_ROWS16)) == 0) return;
 
@@ -813,6 +816,11 @@ bool go(const AttnPagedArgs& a, cudaStream_t st) {
     cfg.blockDim = dim3(32 * C::W);
     cfg.dynamicSmemBytes = C::BYTES;
     cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = a.early ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, attn_rows_kernel<HD, CT, QT, ROWS>, a) == cudaSuccess;
 }
 template <int HD, int ROWS>

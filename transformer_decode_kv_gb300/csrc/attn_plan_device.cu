@@ -256,6 +256,9 @@ __device__ int make_units(const PlanDeviceArgs& a, const Lists& l, Shared& sh) {
 __global__ void __launch_bounds__(kThr) attn_plan_kernel(PlanDeviceArgs a) {
     __shared__ Shared sh;
     const int tid = threadIdx.x;
+    // The attention may be launched while this runs (it waits for the end of it), as this may be while the kernel in front runs.
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (blockIdx.x > 0) {
         // the page tables, one behind the other
         int64_t at = 0;
@@ -334,8 +337,16 @@ __global__ void __launch_bounds__(kThr) attn_plan_kernel(PlanDeviceArgs a) {
 bool launch_attn_plan_device(const PlanDeviceArgs& a, cudaStream_t st) {
     if (a.n_cta[0] > kMaxCtas || a.n_cta[1] > kMaxCtas) return false;
     const int copies = a.n_seq < kMaxCtas ? a.n_seq : kMaxCtas;
-    attn_plan_kernel<<<1 + copies, kThr, 0, st>>>(a);
-    return cudaGetLastError() == cudaSuccess;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1 + copies);
+    cfg.blockDim = dim3(kThr);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_plan_kernel, a) == cudaSuccess;
 }
 
 }  // namespace llm
