@@ -309,6 +309,9 @@ __device__ __forceinline__ float max3_abs(float x, float y, float z) {
 
 template <int HD, int T>
 __global__ void __launch_bounds__(kThr) kv_store4_kernel(KvRowsArgs a) {
+    // (launched early: nothing is read or written before the kernel in front has ended)
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const At4 r = at4<HD>(a);
     float x[2][kVals] = {};
     if (r.there) {
@@ -363,6 +366,8 @@ __global__ void __launch_bounds__(kThr) kv_store4_kernel(KvRowsArgs a) {
 
 template <int HD, int T>
 __global__ void __launch_bounds__(kThr) kv_load4_kernel(KvRowsArgs a) {
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const At4 r = at4<HD>(a);
     if (!r.there) return;
     uint2 u[2];
@@ -395,8 +400,16 @@ bool go4(KvRowsArgs a, bool store, cudaStream_t st) {
     const int64_t blocks = ((int64_t)a.n * a.kv.Hkv + per - 1) / per;
     if (blocks > 0x7fffffff) return false;
     auto launch = [&](void (*kernel)(KvRowsArgs)) {
-        kernel<<<(unsigned)blocks, kThr, 0, st>>>(a);
-        return cudaGetLastError() == cudaSuccess;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)blocks);
+        cfg.blockDim = dim3(kThr);
+        cfg.stream = st;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess;
     };
     switch (a.type) {
         case W_F32: return launch(store ? kv_store4_kernel<HD, W_F32> : kv_load4_kernel<HD, W_F32>);

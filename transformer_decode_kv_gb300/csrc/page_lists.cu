@@ -59,6 +59,12 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
 }
 
+// The launch may overlap the end of the kernel in front; nothing is read or written before that has ended.
+__device__ __forceinline__ void begin() {
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 __device__ __forceinline__ uint32_t div_up(uint32_t n, uint32_t ps) { return n / ps + (n % ps != 0); }
 
 // The last i of a[0 .. n) (ascending, a[0] <= x) with a[i] <= x.
@@ -93,6 +99,7 @@ __device__ __forceinline__ Seq seq_extend(const PageListArgs& a, int i) {
 __global__ void __launch_bounds__(kThr) pages_extend_kernel(PageListArgs a, int n_cta) {
     __shared__ uint32_t s_scan[64], s_tok[kThr], s_page[kThr], s_have[kThr];
     const int tid = threadIdx.x, nt = blockDim.x, rank = blockIdx.x;
+    begin();
     const uint32_t ps = (uint32_t)a.page_size;
     const int n_free = *a.n_free;
     const int n_chunk = max(1, (a.n_seq + nt - 1) / nt);
@@ -185,6 +192,7 @@ __device__ __forceinline__ Cut seq_trim(const PageListArgs& a, int i) {
 __global__ void __launch_bounds__(kThr) pages_trim_kernel(PageListArgs a, int n_cta) {
     __shared__ uint32_t s_scan[64], s_page[kThr], s_from[kThr];
     const int tid = threadIdx.x, nt = blockDim.x, rank = blockIdx.x;
+    begin();
     const int n_free = *a.n_free;
     const int n_chunk = max(1, (a.n_seq + nt - 1) / nt);
     uint32_t page = 0u;
@@ -237,12 +245,14 @@ bool go(void (*kernel)(PageListArgs, int), const PageListArgs& a, int64_t work, 
     // fewer threads meet faster at the barriers
     cfg.blockDim = dim3(a.n_seq <= 256 && work <= 512 ? 256 : kThr);
     cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = n_cta;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = n_cta;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = n_cta > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, a, n_cta) == cudaSuccess;
 }
 
