@@ -23,9 +23,9 @@
 // 7.0 TB/s for whole rows.)
 //
 // Measured, 32 / 8 heads of 128: 32 single f16 tokens over 1 .. 2304 keys 39 us (156 MB, 4.0 TB/s), 16 over 9k .. 33k
-// E4M3 keys 145 us (709 MB, 4.9 TB/s of the 6.8 that the card copies at), over E2M1 keys 103 us (409 MB, 4.0 TB/s), one
-// over 513 keys 12 us, which is latency: the plan, the page table, the rows and the parts' join follow from each other.
-// Over E2M1 keys the arithmetic is as long as the copies: the copies alone take 78 us, all but the copies 86, all
+// E4M3 keys 145 us (709 MB, 4.9 TB/s of the 6.8 that the card copies at), over E2M1 keys 100 us (409 MB, 4.1 TB/s), one
+// over 513 keys 12 us (launched early, over E2M1, 9.5), which is latency: the plan, the page table, the rows and the parts' join follow from each other.
+// Over E2M1 keys the arithmetic is as long as the copies: of 103 us (not launched early) the copies alone take 78, all but the copies 86, all
 // but the conversions (two or two and a half instructions per pair of values, one of them on a half-rate pipe) 83, and three
 // warps a scheduler cover each other's latencies only so far (issue slots 57%). Whole runs of a page by bulk copies, from each warp
 // or from one that does nothing else, by wider asynchronous copies, or V converted before the scores are ready, took 107 to 123.
@@ -183,8 +183,7 @@ attn_rows_kernel(AttnPagedArgs a) {
     float (*s_l)[ROWS] = s_m + kWarps;
     int& s_flag = *reinterpret_cast<int*>(s_l + kWarps);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    // Launched early (after a plan that was made on the device), nothing is read before the kernel in front has ended; otherwise
-    // there is nothing to wait for. Then the 256-row tiles of a mixed plan may start.
+    // Launched early, nothing is read before the kernel in front has ended; otherwise there is nothing to wait for. Then the 256-row tiles of a mixed plan may start.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     const int ui0 = a.first1[blockIdx.x], ui1 = a.first1[blockIdx.x + 1];   // (on their way with the header)

@@ -36,7 +36,7 @@
 // back into TMEM): at the end of 8192 keys the tensor pipe is active for 56% of the time, issue slots are used for 38%, the
 // exponential unit for 29%. 512 f16 tokens at the end of 8192 take 80 us, where cut tiles weigh; over E4M3 1203 and 113
 // us, where the rows' conversion shares issue slots and shared memory with the softmax (tensor pipe 30%, issue slots 37%);
-// over E2M1 814 and 87 us (tensor pipe 41%, issue slots 47%): a third fewer raw bytes, converters that wait for nothing but
+// over E2M1 812 and 84 us (tensor pipe 41%, issue slots 47%): a third fewer raw bytes, converters that wait for nothing but
 // landed bytes, and code that the instruction cache holds beside the softmax. A unit costs about 20 000 cycles beside its blocks
 // (Q in, hidden keys, epilogue), which is what small units of windowed chunks consist of.
 //
@@ -359,8 +359,9 @@ __global__ void __launch_bounds__(threads_of(CT), 1) attn_tc_rows_kernel(AttnPag
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // beside: the small tiles of the same plan run just before; nothing here depends on them, so this kernel
-    // starts where they leave SMs free, and waits for them at its end
+    // starts where they leave SMs free, and waits for them at its end. Otherwise, launched early, it waits for the kernel in front
     asm volatile("griddepcontrol.launch_dependents;");
+    if (!beside) asm volatile("griddepcontrol.wait;" ::: "memory");
     if (form_missing(a)) return;
     if (sa(sm) & 1023u) {                                   // the swizzle patterns repeat every 1024 bytes
         if (tid == 0 && a.err) atomicOr(a.err, ERR_TIMEOUT);
@@ -1426,7 +1427,7 @@ bool go(const AttnPagedArgs& a, cudaStream_t st) {
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     const int beside = (a.form & ~ATTN_FORM_TC) != 0;
-    cfg.numAttrs = beside ? 1 : 0;
+    cfg.numAttrs = beside || a.early ? 1 : 0;
     CUtensorMap mk{}, mv{};
     TmaRuns runs{0, false, false};
     if (CT == W_F4) runs = cell_runs4(a.kv);

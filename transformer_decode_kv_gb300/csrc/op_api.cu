@@ -599,7 +599,7 @@ int llm_attn_run(llm_attn_plan* p, const void* q, int64_t q_stride_tok, int64_t 
     a.part_ml2 = p->part_ml + plan_part_rows(p->caps, false);
     a.tickets = p->tickets; a.redo2 = p->redo; a.err = p->err;
     a.form = p->form();
-    a.early = p->device_form != 0;
+    a.early = p->device_form != 0 || kv->type == LLM_TYPE_F4_E2M1;
     a.n_sm = p->ps.n_sm;
     if (!launch_attn_paged(a, static_cast<cudaStream_t>(stream))) return failed("attention launch", cudaGetLastError());
     return 0;

@@ -128,7 +128,7 @@ struct AttnPagedArgs {
     int32_t* tickets = nullptr;                  // zero between launches
     uint32_t* err = nullptr;
     int32_t form = 0;                            // forms the caller launches
-    bool early = false;                          // the launch may overlap the end of the kernel before it (a plan made there)
+    bool early = false;                          // the launch may overlap the end of the kernel in front
     int32_t n_sm = 148;
 };
 // Both forms' kernels as the plan's form says; false if a launch failed.
