@@ -459,7 +459,8 @@ int llm_attn_run(llm_attn_plan *plan, const void *q, int64_t q_stride_tok, int64
  * sequence), 2 (16-row tiles: a few) and 4 (256-row tensor-core tiles: chunks). -1: NULL. */
 int llm_attn_plan_form(const llm_attn_plan *plan);
 /* The plan's error word (0 = none, ~0 = the device could not be read) after waiting for its device; cleared by
- * the call. Besides the bits above: 8, a wait inside a kernel gave up (rows that this cost are NaN). */
+ * the call. Besides the bits above: 8, a wait inside a kernel gave up (rows that this cost are NaN); 16 and 32 as said at
+ * the calls that set plans. */
 uint32_t llm_attn_plan_error(llm_attn_plan *plan);
 
 /* The sampler chain of llm_sample_ith for n_rows rows of logits at once, one token per row, without

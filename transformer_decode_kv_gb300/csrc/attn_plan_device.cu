@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(kThr) attn_plan_kernel(PlanDeviceArgs a) {
                 bad = true;
             } else {
                 const int f = a.tc && n_new * a.G >= a.tc_rows ? 1 : 0, step = f ? kUnitRows2 : a.rows1;
-                T[f] = ((int)n_new * a.G + step - 1) / step;
+                T[f] = (int)(((uint32_t)n_new * (uint32_t)a.G + (uint32_t)step - 1u) / (uint32_t)step);   // (rows are below 2^31)
             }
         }
         const int64_t x[2] = {pg, (int64_t)T[1] << 32 | (uint32_t)T[0]};

@@ -19,7 +19,7 @@ namespace llm {
 namespace {
 
 constexpr int kThr = 1024;                                  // sequences at a time
-constexpr uint32_t kMany = 0x7fffffffu;                     // sums stop here
+constexpr uint32_t kMany = 0x7fffffffu;                     // sums stop here: more than fits anything
 
 __device__ __forceinline__ uint32_t add_sat(uint32_t a, uint32_t b) { return min(a + b, kMany); }
 
@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(kThr) pages_extend_kernel(PageListArgs a, int 
         page = add_sat(page, at.all_y);
         s_tok[tid] = at.x; s_page[tid] = at.y; s_have[tid] = q.have;
     }
-    bad = __syncthreads_or(bad) || tok > (uint32_t)a.max_tok || page > (uint32_t)n_free;
+    bad = __syncthreads_or(bad) || tok > (uint32_t)a.max_tok || page > (uint32_t)n_free || page >= kMany;
     if (bad && n_chunk == 1) mine = tid < a.n_seq ? a.n_kv[tid] : 0;
     if (!bad) {
         uint32_t tok0 = 0u, page0 = 0u;                     // before the sequences at hand
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kThr) pages_trim_kernel(PageListArgs a, int n_
         page = add_sat(page, at.all_x);
         s_page[tid] = at.x; s_from[tid] = q.from;
     }
-    bad = __syncthreads_or(bad) || (int64_t)n_free + page > a.max_free;
+    bad = __syncthreads_or(bad) || (int64_t)n_free + page > a.max_free || page >= kMany;
     if (!bad) {
         uint32_t page0 = 0u;
         for (int c = 0; c < n_chunk; ++c) {
