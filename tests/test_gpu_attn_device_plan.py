@@ -137,6 +137,28 @@ def test_the_same_rows_as_a_plan_set_from_the_host(L):
         verify(out.double().cpu().numpy(), q, kval, vval, tables, n_new, n_kv, page, 0, 0, torch.float16)
 
 
+def test_the_planner_of_64_bits_makes_the_same_plan(L):
+    """Bounds under which places on the plan's line may pass 32 bits (long table rows, many tokens) select wider sums."""
+    rng = np.random.default_rng(4)
+    n_new, n_kv, page = [1, 30, 70, 0], [900, 40, 300, 5], 256
+    tables, n_pages = tables_of(n_kv, page, rng)
+    wide = np.zeros((4, 1 << 20), np.int32)
+    wide[:, :tables.shape[1]] = tables
+    for act, cdt in (PAIRS[0], PAIRS[5]):
+        pages, kval, vval = caches(L, cdt, n_pages, page, 2, 64, 3)
+        q = torch.from_numpy(rng.normal(size=(4096, 8, 64))).to(act).cuda()
+        outs = []
+        for table, max_tok, max_table in ((tables, 101, 16), (wide, 4096, 1 << 22)):
+            plan = L.AttnPlan(pages, n_head=8, dtype=act, max_tok=max_tok, max_seq=4, max_table=max_table)
+            out = torch.zeros_like(q)
+            plan.set_device(ints([0, 1, 31, 101, 101]), ints(n_kv), ints(table), 70)
+            plan.run(q, pages, out)
+            assert plan.error() == 0
+            outs.append(out)
+        assert torch.equal(*outs)
+        verify(outs[0].double().cpu().numpy(), q, kval, vval, tables, n_new, n_kv, page, 0, 0, act)
+
+
 @pytest.mark.parametrize("bad", [
     dict(start=[1, 2, 3]), dict(start=[0, 2, 1]), dict(start=[0, 1, 9]), dict(start=[0, 4, 5]), dict(n_kv=[-1, 9]),
     dict(n_kv=[9, 33]), dict(n_kv=[2 ** 31 - 1, 9]), dict(n_kv=[32, 32], max_table=3), dict(start=[0, 2 ** 31 - 1, -2])])

@@ -10,9 +10,11 @@
 //
 // One CTA makes the units, the others copy the page table. It is latency: lengths, four running sums, and two rounds of
 // independent items, the CTAs' ends (a thread finds the tile that its end falls into, and makes the unit that begins there)
-// and the tiles (each its first unit). 32 single tokens with 8 KV heads take 9.5 us (18.5 with the lists in global memory and
-// eight lanes a tile), six chunks of 1228 tokens together 11.
+// and the tiles (each its first unit). 32 single tokens with 8 KV heads take 7.8 us (18.5 with the lists in global memory and
+// eight lanes a tile, 9.5 with all places in 64 bits), six chunks of 1228 tokens together 9.8.
 #include "paged.h"
+
+#include <algorithm>
 
 namespace llm {
 
@@ -24,16 +26,16 @@ constexpr int kSeqs = 512, kTiles = 1024;                   // steps up to this 
 static_assert(kMaxCtas + 1 <= kThr, "one thread per CTA end");
 
 // Running sums of N numbers per thread over the block, without the thread's own; `all` receives the totals.
-template <int N>
-__device__ __forceinline__ void block_sums(const int64_t* x, int64_t* s /* [16 N] */, int64_t* before, int64_t* all) {
+template <int N, typename I>
+__device__ __forceinline__ void block_sums(const I* x, I* s /* [16 N] */, I* before, I* all) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     constexpr int W = kThr / 32;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        int64_t in = x[i];
+        I in = x[i];
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t p = __shfl_up_sync(0xffffffffu, in, o);
+            const I p = __shfl_up_sync(0xffffffffu, in, o);
             if (lane >= o) in += p;
         }
         if (lane == 31) s[W * i + warp] = in;
@@ -42,21 +44,22 @@ __device__ __forceinline__ void block_sums(const int64_t* x, int64_t* s /* [16 N
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        int64_t w = lane < W ? s[W * i + lane] : 0;
+        I w = lane < W ? s[W * i + lane] : 0;
 #pragma unroll
         for (int o = 1; o < W; o <<= 1) {
-            const int64_t p = __shfl_up_sync(0xffffffffu, w, o);
+            const I p = __shfl_up_sync(0xffffffffu, w, o);
             if (lane >= o) w += p;
         }
         all[i] = __shfl_sync(0xffffffffu, w, W - 1);
-        const int64_t b = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
+        const I b = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
         if (warp) before[i] += b;
     }
     __syncthreads();                                        // s may be written again
 }
-__device__ __forceinline__ int64_t block_sum(int64_t x, int64_t* s, int64_t& all) {
-    int64_t before;
-    block_sums<1>(&x, s, &before, &all);
+template <typename I>
+__device__ __forceinline__ I block_sum(I x, int64_t* s, I& all) {
+    I before;
+    block_sums<1>(&x, reinterpret_cast<I*>(s), &before, &all);
     return before;
 }
 
@@ -110,18 +113,19 @@ __device__ __forceinline__ int last_at_most(const T* a, int n, T x) {
 
 // Tile t of sequence s for one head, its place on the line and its number.
 // (The numbers of all tiles and heads fit 32 bits: there are not more of them than rows.)
-struct Tile { int s, head, row0, n_row, p0, rank, blocks; Keys keys; int64_t at; };
+template <typename I> struct Tile { int s, head, row0, n_row, p0, rank, blocks; Keys keys; I at; };
 
-template <int F>
+// I: the type of places on the line, 32 bits where the plan's bounds allow.
+template <int F, typename I>
 struct Line {
     const PlanDeviceArgs& a;
     const Lists& l;
-    const int64_t* pre;                                     // places of a head's tiles [n_tile + 1]
+    const I* pre;                                           // places of a head's tiles [n_tile + 1]
     int n_tile;
-    int64_t share;
+    I share;
 
-    __device__ __forceinline__ Tile shape(int s, int t) const {
-        Tile x;
+    __device__ __forceinline__ Tile<I> shape(int s, int t) const {
+        Tile<I> x;
         const int n_new = l.start[s + 1] - l.start[s], rows = F ? kUnitRows2 : a.rows1;
         x.s = s;
         x.p0 = l.n_kv[s] - n_new;
@@ -131,8 +135,8 @@ struct Line {
         x.blocks = (int)(((uint32_t)x.keys.n + (uint32_t)a.bk[F] - 1u) / (uint32_t)a.bk[F]);
         return x;
     }
-    __device__ __forceinline__ Tile tile(int s, int head, int t) const {
-        Tile x = shape(s, t);
+    __device__ __forceinline__ Tile<I> tile(int s, int head, int t) const {
+        Tile<I> x = shape(s, t);
         const int b0 = l.base[F][s], b1 = l.base[F][s + 1];
         x.head = head;
         x.rank = b0 * a.Hkv + head * (b1 - b0) + t;
@@ -140,14 +144,14 @@ struct Line {
         return x;
     }
     // number r in the plan's order: sequences, heads, tiles
-    __device__ __forceinline__ Tile ranked(int r) const {
+    __device__ __forceinline__ Tile<I> ranked(int r) const {
         const int32_t* base = l.base[F];
         const int s = last_at_most(base, a.n_seq, by(r, a.Hkv));
         const int T = base[s + 1] - base[s], rem = r - base[s] * a.Hkv, head = by(rem, T);
         return tile(s, head, rem - head * T);
     }
     // the tile at place x of the line
-    __device__ __forceinline__ Tile at(int64_t x) const {
+    __device__ __forceinline__ Tile<I> at(I x) const {
         const int32_t* base = l.base[F];
         // tiles of a sequence: the sequence of the last tile whose place, all heads before it counted, is not after x
         int lo = 0;
@@ -159,21 +163,23 @@ struct Line {
         // (lo may be any tile of the sequence: its own head's place comes first in the sequence's stretch)
         const int s = last_at_most(base, a.n_seq, lo);
         const int b0 = base[s], T = base[s + 1] - b0;
-        const int64_t one = pre[b0 + T] - pre[b0], in = x - pre[b0] * a.Hkv;
+        const I one = pre[b0 + T] - pre[b0], in = x - pre[b0] * a.Hkv;
         const int head = (int)quotient(in, one);
-        const int64_t y = pre[b0] + in - head * one;
+        const I y = pre[b0] + in - head * one;
         return tile(s, head, last_at_most(pre + b0, T, y));
     }
-    __device__ __forceinline__ static int64_t quotient(int64_t x, int64_t y) {
-        return (x | y) >> 32 ? x / y : (int64_t)((uint32_t)x / (uint32_t)y);
+    __device__ __forceinline__ static I quotient(I x, I y) {
+        if constexpr (sizeof(I) > 4)
+            if ((x | y) >> 32) return x / y;
+        return (I)((uint32_t)x / (uint32_t)y);
     }
-    __device__ __forceinline__ int cta_at(int64_t x) const { return (int)quotient(x, share); }
+    __device__ __forceinline__ int cta_at(I x) const { return (int)quotient(x, share); }
     // block at which CTA c's part of a tile begins
-    __device__ __forceinline__ int cut_at(const Tile& x, int c) const {
-        return (int)min(max(c * share - x.at - a.cost[F], (int64_t)0), (int64_t)x.blocks);
+    __device__ __forceinline__ int cut_at(const Tile<I>& x, int c) const {
+        return (int)min(max(c * share - x.at - a.cost[F], (I)0), (I)x.blocks);
     }
     // the CTAs of a tile's first place, first unit (another where only the fixed cost lies in the former) and last unit
-    __device__ __forceinline__ void span(const Tile& x, int& c0, int& cf, int& c1) const {
+    __device__ __forceinline__ void span(const Tile<I>& x, int& c0, int& cf, int& c1) const {
         c0 = cta_at(x.at);
         c1 = cta_at(x.at + x.blocks + a.cost[F] - 1);
         cf = c1 > c0 && (c0 + 1) * share - x.at <= a.cost[F] ? c0 + 1 : c0;
@@ -181,49 +187,49 @@ struct Line {
 };
 
 // The units of form F; returns its number of cut tiles, -1 without units.
-template <int F>
+template <int F, typename I>
 __device__ int make_units(const PlanDeviceArgs& a, const Lists& l, Shared& sh) {
     const int tid = threadIdx.x, n_tile = l.base[F][a.n_seq];
     if (n_tile == 0) return -1;
-    int64_t* pre = n_tile <= kTiles ? sh.pre : a.tile_pre[F];
-    Line<F> line{a, l, pre, n_tile, 1};
-    int64_t total = 0;
+    I* pre = reinterpret_cast<I*>(n_tile <= kTiles ? sh.pre : a.tile_pre[F]);
+    Line<F, I> line{a, l, pre, n_tile, 1};
+    I total = 0;
     for (int t0 = 0; t0 < n_tile; t0 += kThr) {
         const int t = t0 + tid;
-        int64_t len = 0, all;
+        I len = 0, all;
         if (t < n_tile) {
             const int s = last_at_most(l.base[F], a.n_seq, t);
             len = line.shape(s, t - l.base[F][s]).blocks + a.cost[F];
         }
-        const int64_t before = block_sum(len, sh.scan, all);
+        const I before = block_sum(len, sh.scan, all);
         if (t < n_tile) pre[t] = total + before;
         total += all;
     }
     if (tid == 0) pre[n_tile] = total;
     const int n_cta = a.n_cta[F], cost = a.cost[F], bk = a.bk[F];
-    const int64_t length = total * a.Hkv;
+    const I length = total * a.Hkv;
     const int n_rank = n_tile * a.Hkv;
-    const int64_t share = max(Line<F>::quotient(length + n_cta - 1, n_cta), (int64_t)cost + 1);
+    const I share = max(Line<F, I>::quotient(length + n_cta - 1, n_cta), (I)cost + 1);
     line.share = share;
     __syncthreads();
     // a thread per CTA end: the tile that it falls into, and whether it cuts it
     const int c = tid;
     const bool end = c <= n_cta && c * share < length;
-    Tile mine;
+    Tile<I> mine;
     int c0 = 0, cf = 0, c1 = 0;
     bool cuts = false;
-    int64_t own = 0, all;
+    int own = 0, all;                                       // (cuts above, tiles' first cuts below: fewer than 2^15 of each)
     if (end) {
         mine = line.at(c * share);
         line.span(mine, c0, cf, c1);
         cuts = c > c0 && c * share - mine.at > cost;
-        own = cuts ? (int64_t)1 << 32 | (c == cf + 1) : 0;
+        own = cuts ? 1 << 16 | (c == cf + 1) : 0;
     }
-    const int64_t sum = block_sum(own, sh.scan, all) + own;
-    if (c <= n_cta) { sh.cut[c] = (int)(sum >> 32); sh.cut_tile[c] = (int)(sum & 0x7fffffff); }
+    const int sum = block_sum(own, sh.scan, all) + own;
+    if (c <= n_cta) { sh.cut[c] = sum >> 16; sh.cut_tile[c] = sum & 0xffff; }
     __syncthreads();
     // the unit of tile x that belongs to CTA u_c
-    auto write = [&](const Tile& x, int t0, int tf, int t1, int u_c) {
+    auto write = [&](const Tile<I>& x, int t0, int tf, int t1, int u_c) {
         const int u0 = x.rank + sh.cut[t0], n = t1 - tf + 1;
         AttnUnit u{};
         u.tok0 = l.start[x.s];
@@ -250,7 +256,7 @@ __device__ int make_units(const PlanDeviceArgs& a, const Lists& l, Shared& sh) {
     if (c <= n_cta) a.first[F][c] = end ? mine.rank + sh.cut[c0] + max(0, c - cf) : n_rank + sh.cut[n_cta];
     // and each tile's first unit
     for (int r = tid; r < n_rank; r += kThr) {
-        const Tile x = line.ranked(r);
+        const Tile<I> x = line.ranked(r);
         int t0, tf, t1;
         line.span(x, t0, tf, t1);
         write(x, t0, tf, t1, tf);
@@ -258,6 +264,7 @@ __device__ int make_units(const PlanDeviceArgs& a, const Lists& l, Shared& sh) {
     return sh.cut_tile[n_cta];
 }
 
+template <typename I>
 __global__ void __launch_bounds__(kThr) attn_plan_kernel(PlanDeviceArgs a) {
     __shared__ Shared sh;
     const int tid = threadIdx.x;
@@ -284,7 +291,7 @@ __global__ void __launch_bounds__(kThr) attn_plan_kernel(PlanDeviceArgs a) {
     const bool small = a.n_seq <= kSeqs;
     const Lists l{small ? sh.start : a.start, small ? sh.n_kv : a.n_kv, small ? sh.off : a.table_off,
                   {small ? sh.base[0] : a.tile_base[0], small ? sh.base[1] : a.tile_base[1]}};
-    bool bad = tid == 0 && a.start[0] != 0;
+    bool bad = a.n_seq == 0 && a.start[0] != 0;
     int64_t pages = 0;
     int tiles[2] = {0, 0};
     for (int s0 = 0; s0 < a.n_seq; s0 += kThr) {
@@ -300,7 +307,7 @@ __global__ void __launch_bounds__(kThr) attn_plan_kernel(PlanDeviceArgs a) {
                 sh.n_kv[s] = n_kv;
             }
             pg = pages_of(a, n_kv);
-            if (n_new < 0 || n_new > a.max_new || to > a.max_tok || n_kv < 0 || n_kv > a.max_keys || pg > a.ld_table) {
+            if ((s == 0 && from != 0) || n_new < 0 || n_new > a.max_new || to > a.max_tok || n_kv < 0 || n_kv > a.max_keys || pg > a.ld_table) {
                 bad = true;
             } else {
                 const int f = a.tc && n_new * a.G >= a.tc_rows ? 1 : 0, step = f ? kUnitRows2 : a.rows1;
@@ -324,10 +331,10 @@ __global__ void __launch_bounds__(kThr) attn_plan_kernel(PlanDeviceArgs a) {
     bad = __syncthreads_or(bad) || pages > a.max_table;
     int n0 = -1, n1 = -1;
     if (!bad) {
-        n0 = make_units<0>(a, l, sh);
+        n0 = make_units<0, I>(a, l, sh);
         if (a.tc) {
             __syncthreads();
-            n1 = make_units<1>(a, l, sh);
+            n1 = make_units<1, I>(a, l, sh);
         }
     }
     if (tid == 0) {
@@ -351,7 +358,15 @@ bool launch_attn_plan_device(const PlanDeviceArgs& a, cudaStream_t st) {
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_plan_kernel, a) == cudaSuccess;
+    // The line is no longer than the most tiles of the most keys; every multiple of a CTA's share up to its end, and one share more,
+    // has to fit.
+    const int64_t keys = std::min<int64_t>(std::min<int64_t>(a.max_table, a.ld_table) * a.page_size, a.max_keys);
+    bool fits = true;
+    for (int f = 0; f < 2; ++f) {
+        const double line = (double)a.max_tiles[f] * (double)(keys / a.bk[f] + 2 + a.cost[f]) * a.Hkv;
+        fits = fits && line + 2.0 * a.n_cta[f] * (a.cost[f] + 2) + line / a.n_cta[f] < 2147483000.0;
+    }
+    return cudaLaunchKernelEx(&cfg, fits ? attn_plan_kernel<int32_t> : attn_plan_kernel<int64_t>, a) == cudaSuccess;
 }
 
 }  // namespace llm

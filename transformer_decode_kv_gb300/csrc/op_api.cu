@@ -529,6 +529,7 @@ int llm_attn_plan_set_device(llm_attn_plan* p, int32_t n_seq, const int32_t* sta
     const int32_t form = plan_numbers(p->ps, max_new, a);
     a.n_seq = n_seq; a.ld_table = ld_pages;
     a.max_tok = p->shape.max_tok; a.max_keys = kMaxKeys; a.max_table = p->shape.max_table;
+    a.max_tiles[0] = p->caps.tiles1; a.max_tiles[1] = p->caps.tiles2;
     a.start = start; a.n_kv = n_kv; a.table = pages;
     a.hdr = reinterpret_cast<int32_t*>(p->d_buf);
     a.cuts = reinterpret_cast<int32_t*>(p->d_buf + p->off_cuts);

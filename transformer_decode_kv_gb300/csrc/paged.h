@@ -181,7 +181,7 @@ struct PlanDeviceArgs {
     int32_t rows1 = 8;                           // rows of the small tiles
     // the step, and what it may hold
     int32_t n_seq = 0, ld_table = 0, max_new = 0, max_tok = 0, max_keys = 0;
-    int64_t max_table = 0;
+    int64_t max_table = 0, max_tiles[2] = {0, 0};
     const int32_t *start = nullptr, *n_kv = nullptr, *table = nullptr;
     // the plan's buffers; scratch: tiles before each sequence [max_seq + 1], each tile's place [tiles + 1], each sequence's table
     int32_t* hdr = nullptr;
