@@ -300,18 +300,26 @@ def _host_ints(a, name: str) -> np.ndarray:
     return _i32(x)
 
 
+_raw_stream = None
+
+
 def _stream_of(t, stream: Optional[int]) -> Optional[int]:
     """The given cudaStream_t, or torch's current stream of t's device."""
+    global _raw_stream
     if stream is not None or not t.is_cuda:
         return stream
-    import torch
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
+    if _raw_stream is None:
+        import torch
+        _raw_stream = torch._C._cuda_getCurrentRawStream
+    return _raw_stream(t.get_device())
 
 
 def _need(t, name: str, dtype, shape) -> int:
     """The address of t, which must be a dense tensor of this type and shape: the library reads it
     as such."""
-    if _type(t) != dtype or t.shape != shape or not t.is_contiguous():
+    if not _types:
+        _type(t)
+    if _types.get(t.dtype) != dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)} (int32 or "
                          f"float32 as documented), not {t.dtype} {tuple(t.shape)}")
     return t.data_ptr()
@@ -442,10 +450,12 @@ def pages_extend(lists: SeqPages, n_new, cell, pos, start, n_kv_out=None, n_free
     n_kv_out and n_free_out (None: in place) the new lengths and the stack's size. A step that does not fit sets
     bit 32 of err, an optional device word (int32 [1]), and has no tokens."""
     kv_out, free_out, e = lists._outs(n_kv_out, n_free_out, err)
-    n = cell.numel()
-    r = lib().llm_pages_extend(lists.ref, _need(n_new, "n_new", "int32", (lists.n_seq,)), kv_out, free_out, n,
-                               _need(cell, "cell", "int32", (n,)), _need(pos, "pos", "int32", (n,)),
-                               _need(start, "start", "int32", (lists.n_seq + 1,)), e, _stream_of(lists.n_free, stream))
+    n_seq, n = lists.n_seq, cell.numel()
+    row = (n,)
+    r = (_lib or lib()).llm_pages_extend(
+        lists.ref, _need(n_new, "n_new", "int32", (n_seq,)), kv_out, free_out, n, _need(cell, "cell", "int32", row),
+        _need(pos, "pos", "int32", row), _need(start, "start", "int32", (n_seq + 1,)), e,
+        _stream_of(lists.n_free, stream))
     if r != 0:
         _op(r)
 
