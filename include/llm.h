@@ -311,7 +311,9 @@ int32_t llm_sample_batch(llm_ctx *ctx, int32_t n, const int32_t *rows, const llm
  *   - every data pointer is device memory of one GPU (a host pointer is refused, -1); the call runs
  *     on that GPU whichever device is current, and leaves the current device as it was;
  *   - work is enqueued on `stream` (a cudaStream_t of that GPU, NULL = the legacy default stream)
- *     and the call returns without waiting; it allocates nothing, so it may be captured in a graph;
+ *     and the call returns without waiting; it allocates nothing, so it may be captured in a graph. Some kernels are
+ *     launched programmatically: in place before the kernel in front has ended, they wait for its end inside. (A kernel of
+ *     the caller's that is launched so as well must do the same before it ends, as such kernels do.);
  *   - returns 0, -1 for arguments the call refuses (nothing is enqueued), -3 if CUDA refuses the launch;
  *   - `err`, where taken, is a device word (or NULL) that kernels OR bits into when an index they
  *     read on the device is out of range (1: a cell or page, 4: a row; the access is skipped), or 32 where lengths
