@@ -489,6 +489,7 @@ __global__ void __launch_bounds__(threads_of(CT), 1) attn_tc_rows_kernel(AttnPag
                     if (!ok) break;
                     if (now) {
                         const int w = u.v0 + j * kKeys;
+                        to_async_proxy();                   // (rows may have come by themselves where the copies go)
                         if (lane == 0) {
                             asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(fb), "n"(kKeys * (HD / 2 + NB + 4))
                                          : "memory");
@@ -1036,7 +1037,7 @@ __global__ void __launch_bounds__(threads_of(CT), 1) attn_tc_rows_kernel(AttnPag
                 }
                 const __half2 f2 = __float2half2_rn(f);
                 const uint32_t fw = *reinterpret_cast<const uint32_t*>(&f2);
-                // (By 2: the instruction cache has to hold it beside the softmax. 2048 tokens at the end of 32768 keys take 833 us so,
+                // (By 2: the instruction cache has to hold it beside the softmax. 2048 tokens at the end of 32768 keys took 833 us so,
                 // 843 rolled; while the loading warps' loops were long, 1395 unrolled by 8 and 1080 rolled.)
 #pragma unroll 2
                 for (int y = 0; y < 32 / RI; ++y) {
