@@ -119,3 +119,26 @@ def test_bad_extensions_are_refused(B, args):
                                     a["err"], None) == -1
     assert B.lib().llm_pages_extend(None, PTR, PTR, PTR, 4, PTR, PTR, PTR, None, None) == -1
     assert B.lib().llm_pages_trim(None, PTR, PTR, PTR, None, None) == -1
+
+
+def test_numbers_that_int32_does_not_hold_are_refused_not_wrapped(B):
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)
+    for page_size, n_pages in ((2 ** 32 + 16, 8), (16, 2 ** 32 + 8), (16, -2 ** 32 + 8)):
+        with pytest.raises(ValueError, match="int32"):
+            B.SeqPages(i(2, 4), i(2), i(8), i(1), page_size, n_pages)
+    plan = B.AttnPlan.__new__(B.AttnPlan)                  # (no device is reached: the arguments are refused first)
+    plan.ptr, plan._captured_rows, plan.max_tok = None, None, 8
+    with pytest.raises(ValueError, match="int32"):
+        plan.set_device(i(3), i(2), i(2, 4), 2 ** 32 + 1, stream=0)
+    with pytest.raises(B.LlmError, match="NULL plan"):     # good ones reach the library
+        plan.set_device(i(3), i(2), i(2, 4), 1, stream=0)
+
+
+def test_python_checks_of_the_page_lists(B):
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)
+    ok = dict(table=i(2, 4), n_kv=i(2), free=i(8), n_free=i(1), page_size=16, n_pages=8)
+    B.SeqPages(**ok)
+    for bad in (dict(table=i(8)), dict(table=i(2, 8)[:, ::2]), dict(table=i(2, 4).long()), dict(n_kv=i(3)), dict(free=i(2, 4)),
+                dict(n_free=i(2)), dict(n_free=i(1).float())):
+        with pytest.raises(ValueError):
+            B.SeqPages(**{**ok, **bad})

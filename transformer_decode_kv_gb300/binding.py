@@ -425,6 +425,8 @@ class SeqPages:
     def __init__(self, table, n_kv, free, n_free, page_size: int, n_pages: int):
         if table.dim() != 2 or free.dim() != 1:
             raise ValueError("table must be [n_seq, pages] and free [max_free]")
+        if not (-2 ** 31 <= page_size < 2 ** 31 and -2 ** 31 <= n_pages < 2 ** 31):
+            raise ValueError("page_size and n_pages must fit int32")      # (ctypes would wrap them)
         d = SeqPagesDesc()
         d.n_seq, d.ld_table = table.shape
         d.page_size, d.n_pages, d.max_free = page_size, n_pages, free.shape[0]
@@ -527,6 +529,8 @@ class AttnPlan:
         n = n_kv.shape[0]
         if pages.dim() != 2 or pages.shape[0] != n:
             raise ValueError("pages must be [n_seq, n]")
+        if not -2 ** 31 <= max_new < 2 ** 31:
+            raise ValueError("max_new must fit int32")
         if self._captured_rows is not None and self.max_tok > self._captured_rows:
             raise ValueError(f"a captured run's q or out has only {self._captured_rows} rows, and a step that is set on the "
                              f"device may have {self.max_tok} tokens")
