@@ -273,3 +273,49 @@ def test_serving_steps_in_one_graph(L, cdt, max_new):
                 after[j] = 0
         kv = after
         assert lists.n_kv.tolist() == kv and lists.free.tolist()[:len(stack)] == stack
+
+
+def replayed_plan(L, act, cdt, n_new, n_kv, max_tok, max_new, run_inside=False, seed=21):
+    """A plan, and a graph that sets it on the device to this step (and runs it, where asked)."""
+    rng = np.random.default_rng(seed)
+    tables, n_pages = tables_of(n_kv, 16, rng)
+    pages, kval, vval = caches(L, cdt, n_pages, 16, 2, 64, seed + 1)
+    q = torch.from_numpy(rng.normal(size=(max_tok, 8, 64))).to(act).cuda()
+    out = torch.full_like(q, 77.0)
+    plan = L.AttnPlan(pages, n_head=8, dtype=act, max_tok=max_tok, max_seq=len(n_new) + 1, max_table=tables.size)
+    args = ints(np.concatenate([[0], np.cumsum(n_new)])), ints(n_kv), ints(tables), max_new
+    plan.set_device(*args)                                      # (the first launches, not captured)
+    plan.run(q, pages, out)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        plan.set_device(*args)
+        if run_inside:
+            plan.run(q, pages, out)
+    out.fill_(77.0)
+
+    def right():
+        assert plan.error() == 0
+        got = out.double().cpu().numpy()
+        assert (got[sum(n_new):] == 77.0).all()
+        verify(got, q, kval, vval, tables, n_new, n_kv, 16, 0, 0, act)
+    return plan, g, pages, q, out, tables, right, args
+
+
+@pytest.mark.parametrize("act,cdt", [PAIRS[0], PAIRS[4]])
+def test_runs_after_a_replayed_set_need_the_rows_of_its_step(L, act, cdt):
+    """set_device captured, a smaller step set by the host, the graph replayed: the plan holds the graph's step again, and a run
+    whose q and out would do for the host's is refused."""
+    plan, g, pages, q, out, tables, right, _ = replayed_plan(L, act, cdt, [1] * 7, [40, 3, 90, 17, 1, 64, 33], 8, 1)
+    plan.set([1], [40], tables[:1])
+    g.replay()
+    for n in (1, 7):
+        with pytest.raises(ValueError, match="fewer rows"):
+            plan.run(q[:n], pages, out[:n])
+    assert (out == 77.0).all()
+    plan.run(q, pages, out)
+    right()
+    plan.set([1], [40], tables[:1])                             # and the host's step where no replay came after it
+    out.fill_(77.0)
+    plan.run(q, pages, out)
+    assert plan.error() == 0 and (out[1:] == 77.0).all() and not (out[:1] == 77.0).any()

@@ -142,3 +142,54 @@ def test_python_checks_of_the_page_lists(B):
                 dict(n_free=i(2)), dict(n_free=i(1).float())):
         with pytest.raises(ValueError):
             B.SeqPages(**{**ok, **bad})
+
+
+@pytest.fixture
+def plan_without_a_device(B, monkeypatch):
+    """A plan of 8 tokens over a library that accepts everything: what the binding itself keeps count of."""
+    class Lib:
+        llm_attn_plan_set = llm_attn_plan_set_device = staticmethod(lambda *a: 0)
+    monkeypatch.setattr(B, "lib", lambda: Lib)
+    plan = B.AttnPlan.__new__(B.AttnPlan)
+    plan.ptr, plan.device, plan.dtype, plan.n_head, plan.head_dim = None, None, torch.float16, 2, 64
+    plan.n_tok, plan.max_tok, plan._captured_rows, plan._run = 0, 8, None, lambda *a: 0
+    plan.capturing = False
+    plan._capturing = lambda: plan.capturing
+    k = torch.zeros(4, 16, 2, 64, dtype=torch.float16)
+    pages, rows = B.KvPages(k, k), lambda n: torch.zeros(n, 2, 64, dtype=torch.float16)
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)
+    return plan, lambda n, m=None: plan.run(rows(n), pages, rows(n if m is None else m)), lambda: plan.set_device(i(3), i(2), i(2, 4), 1)
+
+
+def test_a_captured_set_device_asks_every_later_run_for_max_tok_rows(plan_without_a_device):
+    """Its replay may come after any other set, and leaves a step of up to max_tok tokens on the device."""
+    plan, run, set_device = plan_without_a_device
+    plan.capturing = True
+    set_device()
+    plan.capturing = False
+    for _ in range(2):
+        plan.set([1], [5], [[0]], stream=0)
+        for n, m in ((1, 1), (7, 8), (8, 7)):
+            with pytest.raises(ValueError, match="fewer rows"):
+                run(n, m)
+        run(8)
+        plan.capturing = True                              # (a graph that is replayed behind the other)
+        with pytest.raises(ValueError, match="fewer rows"):
+            run(1)
+        run(8)
+        plan.capturing = False
+        set_device()                                       # an eager one changes nothing about it
+
+
+def test_an_eager_set_device_asks_the_runs_of_its_step_for_max_tok_rows(plan_without_a_device):
+    plan, run, set_device = plan_without_a_device
+    set_device()
+    with pytest.raises(ValueError, match="fewer rows"):
+        run(7)
+    plan.set([1], [5], [[0]], stream=0)
+    run(1)
+    plan.capturing = True
+    run(1)
+    plan.capturing = False
+    with pytest.raises(ValueError, match="captured run"):  # a graph holds a run whose rows would not do
+        set_device()

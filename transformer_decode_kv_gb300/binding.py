@@ -476,6 +476,8 @@ class AttnPlan:
     """Attention of new tokens over a paged cache like `pages` (its type and shape, not its memory):
     made once, set once per step, run once per layer. dtype is the type of q and out."""
 
+    _replayed_tok = 0                       # tokens that a step may have which a graph's replay sets: none, or max_tok
+
     def __init__(self, pages: KvPages, n_head: int, dtype, max_tok: int, max_seq: int, max_table: int,
                  window: int = 0, n_sink: int = 0, scale: float = 0.0):
         import torch
@@ -520,12 +522,13 @@ class AttnPlan:
             stream = torch.cuda.current_stream(self.device).cuda_stream
         _op(lib().llm_attn_plan_set(self.ptr, len(n_new), _ptr(n_new, C.c_int32),
                                     _ptr(n_kv, C.c_int32), _ptr(t, C.c_int32), t.shape[1], stream))
-        self.n_tok = int(n_new.sum())
+        self.n_tok = max(int(n_new.sum()), self._replayed_tok)
 
     def set_device(self, start, n_kv, pages, max_new: int, stream: Optional[int] = None) -> None:
         """The same from device tensors (int32), as pages_extend leaves them, without a wait: start [n_seq + 1], the
         first new token of each sequence and their number; n_kv [n_seq], cached rows with the new ones; page table
-        [n_seq, ld]. max_new bounds a sequence's new tokens. Runs then need q and out of max_tok rows."""
+        [n_seq, ld]. max_new bounds a sequence's new tokens. Runs then need q and out of max_tok rows. Captured, the call
+        is made again by every replay, whatever the plan was set to before: from then on every run needs max_tok rows."""
         n = n_kv.shape[0]
         if pages.dim() != 2 or pages.shape[0] != n:
             raise ValueError("pages must be [n_seq, n]")
@@ -539,6 +542,8 @@ class AttnPlan:
                                            _need(n_kv, "n_kv", "int32", (n,)), _need(pages, "pages", "int32", (n, ld)), ld,
                                            max_new, _stream_of(start, stream)))
         self.n_tok = self.max_tok
+        if self._captures(stream):
+            self._replayed_tok = self.max_tok
 
     def _captures(self, stream: Optional[int]) -> bool:
         """Whether a run on this stream (None: torch's current one) is recorded into a graph."""
@@ -551,13 +556,14 @@ class AttnPlan:
     def run(self, q, pages: KvPages, out, stream: Optional[int] = None) -> None:
         """out[i] = attention of token i of the step; q and out [at least the step's tokens, n_head,
         head_dim], rows past the tokens are not touched. After a captured run the plan takes no step of
-        more tokens than that run's q and out have rows."""
+        more tokens than that run's q and out have rows; after a captured set_device every run needs max_tok rows."""
         sq = _rows(q, "q", self.n_head, self.head_dim)
         so = _rows(out, "out", self.n_head, self.head_dim)
         if q.dtype is not self.dtype or out.dtype is not self.dtype:
             raise TypeError(f"q and out must be {self.dtype}")
         if q.shape[0] < self.n_tok or out.shape[0] < self.n_tok:
-            raise ValueError(f"q or out has fewer rows than the step has tokens ({self.n_tok})")
+            raise ValueError(f"q or out has fewer rows than the step has tokens ({self.n_tok})" + (
+                ": a graph holds a set_device, whose replay may set as many" if self._replayed_tok else ""))
         if self._captures(stream):
             rows = min(q.shape[0], out.shape[0])
             self._captured_rows = rows if self._captured_rows is None else min(rows, self._captured_rows)
