@@ -446,7 +446,9 @@ int llm_attn_plan_set(llm_attn_plan *plan, int32_t n_seq, const int32_t *n_new, 
  * with the new ones), and pages [n_seq][ld_pages] are device arrays. The work is enqueued on `stream`; the arrays are free
  * again when it has run. The call may be captured, and a graph of it, the stores and the runs follows the lengths.
  * max_new, at most max_tok, bounds the new tokens of one sequence: 1 for a decode step. It decides which kernels
- * the runs after this call launch (llm_attn_plan_form): give what the steps need. A step that is out of range
+ * the runs after this call launch (llm_attn_plan_form): give what the steps need. Every replay of a captured call sets the plan again,
+ * whatever it was set to before. So once a call was captured, all runs of the plan need q and out of max_tok rows and launch
+ * what the captured steps need beside their own (the runs captured behind it in the same capture: only what its step needs). A step that is out of range
  * (llm_attn_plan_set's -1, or more than max_new tokens of a sequence) sets bit 32 of the plan's error word, and the
  * runs leave the output alone. A run of such a plan may be captured whatever the step, an empty one too; its q and out
  * need rows for max_tok tokens. Pages outside the cache are found by the runs (bit 1; their keys are not seen). */
@@ -457,8 +459,9 @@ int llm_attn_plan_set_device(llm_attn_plan *plan, int32_t n_seq, const int32_t *
 int llm_attn_run(llm_attn_plan *plan, const void *q, int64_t q_stride_tok, int64_t q_stride_head,
                  const llm_kv_pages *kv, void *out, int64_t o_stride_tok, int64_t o_stride_head,
                  void *stream);
-/* The kernels the plan needs: 0 nothing to run, else the sum of 1 (8-row tiles: a token or two per
- * sequence), 2 (16-row tiles: a few) and 4 (256-row tensor-core tiles: chunks). -1: NULL. */
+/* The kernels that runs of the plan launch, for the step set last and those of captured llm_attn_plan_set_device calls: 0 nothing
+ * to run, else the sum of 1 (8-row tiles: a token or two per sequence), 2 (16-row tiles: a few) and 4 (256-row tensor-core
+ * tiles: chunks). -1: NULL. */
 int llm_attn_plan_form(const llm_attn_plan *plan);
 /* The plan's error word (0 = none, ~0 = the device could not be read) after waiting for its device; cleared by
  * the call. Besides the bits above: 8, a wait inside a kernel gave up (rows that this cost are NaN); 16 and 32 as said at

@@ -319,3 +319,78 @@ def test_runs_after_a_replayed_set_need_the_rows_of_its_step(L, act, cdt):
     out.fill_(77.0)
     plan.run(q, pages, out)
     assert plan.error() == 0 and (out[1:] == 77.0).all() and not (out[:1] == 77.0).any()
+
+
+CHUNKS = [1, 40, 0, 1], [30, 90, 5, 17]
+SINGLES = [1] * 7, [40, 3, 90, 17, 1, 64, 33]
+
+
+@pytest.mark.parametrize("n_new,n_kv,max_new,first", [(*SINGLES, 1, []), (*SINGLES, 1, [40]), (*CHUNKS, 40, [1]), (*CHUNKS, 40, [])])
+@pytest.mark.parametrize("act,cdt", [PAIRS[0], PAIRS[4]])
+def test_runs_after_a_replayed_set_launch_what_its_step_needs(L, act, cdt, n_new, n_kv, max_new, first):
+    """The host's step in between is empty, or needs other kernels than the graph's."""
+    plan, g, pages, q, out, tables, right, _ = replayed_plan(L, act, cdt, n_new, n_kv, 64, max_new)
+    plan.set(first, [n + 3 for n in first], tables[:len(first)])
+    g.replay()
+    plan.run(q, pages, out)
+    right()
+    # the same run captured, in a graph without the set, also where the step at hand is empty
+    plan.set([], [], tables[:0])
+    runs = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(runs):
+        plan.run(q, pages, out)
+    out.fill_(77.0)
+    g.replay()
+    runs.replay()
+    torch.cuda.synchronize()
+    right()
+    # an empty step, which has not to be taken for the graph's
+    plan.set([], [], tables[:0])
+    out.fill_(77.0)
+    plan.run(q, pages, out)
+    assert plan.error() == 0 and (out == 77.0).all()
+
+
+@pytest.mark.parametrize("act,cdt", [PAIRS[0], PAIRS[4]])
+def test_a_captured_set_that_is_not_replayed_changes_no_step(L, act, cdt):
+    """Between the capture and its replays the device holds what was set before, from the host or on the device."""
+    plan, g, pages, q, out, tables, right, args = replayed_plan(L, act, cdt, *CHUNKS, 64, 40)
+    for way in ("host", "device"):
+        if way == "host":
+            plan.set(*CHUNKS, tables)
+        else:
+            plan.set_device(*args)
+        other = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(other):
+            plan.set_device(*args[:3], 1)
+        out.fill_(77.0)
+        plan.run(q, pages, out)
+        right()
+    other.replay()                                              # more new tokens than its max_new
+    out.fill_(77.0)
+    plan.run(q, pages, out)
+    assert plan.error() == 32 and (out == 77.0).all()
+
+
+def test_two_graphs_with_other_steps_of_one_plan(L):
+    """Decode steps and chunks, each with its own set and run, in turn."""
+    act, cdt = PAIRS[5]
+    plan, decode, pages, q, out, tables, right, args = replayed_plan(L, act, cdt, *SINGLES, 64, 1, run_inside=True)
+    start, kv = ints([0, 0, 0, 40, 40, 40, 40, 40]), ints([40, 3, 90, 17, 1, 64, 33])
+    chunks = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(chunks):
+        plan.set_device(start, kv, args[2], 40)
+        plan.run(q, pages, out)
+    for _ in range(3):
+        out.fill_(77.0)
+        decode.replay()
+        right()
+        out.fill_(77.0)
+        chunks.replay()
+        assert plan.error() == 0 and (out[40:] == 77.0).all() and not (out[:40] == 77.0).any()
+        first = out.clone() if _ == 0 else first
+        assert torch.equal(out, first)
+    plan.set([0, 0, 40, 0, 0, 0, 0], [40, 3, 90, 17, 1, 64, 33], tables)
+    out.fill_(77.0)
+    plan.run(q, pages, out)                                     # the same step from the host: sums in another order
+    assert plan.error() == 0 and (out[:40].float() - first[:40].float()).abs().max() <= 2 ** -7 * first[:40].float().abs().max()

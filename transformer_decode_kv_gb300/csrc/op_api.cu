@@ -296,7 +296,6 @@ struct llm_attn_plan {
     PagedPlanCaps caps{};
     int device = 0;
     float scale_log2 = 0.f;
-    PagedPlan plan;
     // device buffer: header, both forms' CTA starts, their units, page table; the pinned copy it is uploaded from
     size_t off_first[2] = {0, 0}, off_cuts = 0, off_units[2] = {0, 0}, off_table = 0, bytes = 0;
     uint8_t *d_buf = nullptr, *h_buf = nullptr;
@@ -304,11 +303,16 @@ struct llm_attn_plan {
     float2* part_ml = nullptr;
     int32_t *tickets = nullptr, *redo = nullptr;
     uint32_t* err = nullptr;
-    // set from the device: the forms that the plan may then have (0: set from the host), and the scratch of making it
-    int32_t device_form = 0;
+    // The forms of the set that was made last outside a capture (from the device: those that its step may have), and those
+    // of every set that was captured: from then on a replay may leave such a step on the device at any time, and runs
+    // launch what either needs. Only a run that is captured behind such a set, in the same capture, has that set's step for certain.
+    int32_t set_form = 0, captured_form = 0, capture_form = 0;
+    unsigned long long capture_id = 0;           // of the capture that the last of these belongs to; capture_form: its forms
+    bool on_device = false;                      // the last set outside a capture was made on the device
+    int32_t form() const { return set_form | captured_form; }
+    // scratch of plans made on the device
     int32_t* lists = nullptr;
     int64_t* tile_pre = nullptr;
-    int32_t form() const { return device_form ? device_form : plan.form(); }
     cudaEvent_t uploaded = nullptr;
     bool pending = false;
 };
@@ -504,8 +508,8 @@ int llm_attn_plan_set(llm_attn_plan* p, int32_t n_seq, const int32_t* n_new, con
     if (e == cudaSuccess) e = cudaEventRecord(p->uploaded, st);
     if (e != cudaSuccess) { cudaGetLastError(); return failed("plan upload", e); }
     p->pending = true;
-    p->plan = std::move(plan);
-    p->device_form = 0;
+    p->set_form = plan.form();
+    p->on_device = false;
     return 0;
 }
 
@@ -525,6 +529,10 @@ int llm_attn_plan_set_device(llm_attn_plan* p, int32_t n_seq, const int32_t* sta
     if (r) return r;
     OnDevice on(dev);
     if (!on.ok()) return failed("cudaSetDevice", cudaGetLastError());
+    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+    unsigned long long id = 0;
+    const cudaError_t e = cudaStreamGetCaptureInfo(static_cast<cudaStream_t>(stream), &cs, &id);
+    if (e != cudaSuccess) { cudaGetLastError(); return failed("stream", e); }
     PlanDeviceArgs a;
     const int32_t form = plan_numbers(p->ps, max_new, a);
     a.n_seq = n_seq; a.ld_table = ld_pages;
@@ -543,7 +551,14 @@ int llm_attn_plan_set_device(llm_attn_plan* p, int32_t n_seq, const int32_t* sta
     a.table_off = p->lists + 2 * ((size_t)p->shape.max_seq + 1);
     a.err = p->err;
     if (!launch_attn_plan_device(a, static_cast<cudaStream_t>(stream))) return failed("plan launch", cudaGetLastError());
-    p->device_form = form;
+    if (cs == cudaStreamCaptureStatusNone) {
+        p->set_form = form;
+        p->on_device = true;
+    } else {
+        p->captured_form |= form;
+        p->capture_form = form;
+        p->capture_id = id;
+    }
     return 0;
 }
 
@@ -554,7 +569,8 @@ int llm_attn_run(llm_attn_plan* p, const void* q, int64_t q_stride_tok, int64_t 
     if (kv->type != p->kv.type || kv->n_head_kv != p->kv.n_head_kv || kv->head_dim != p->kv.head_dim ||
         kv->page_size != p->kv.page_size || kv->n_pages != p->kv.n_pages)
         return refuse("the cache is not of the plan's type and shape");
-    if (p->form() == 0) {
+    int32_t form = p->form();
+    if (form == 0) {
         // (a graph without the kernels would replay later steps as nothing, and nobody would learn of it)
         cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
         OnDevice on(p->device);
@@ -576,6 +592,13 @@ int llm_attn_run(llm_attn_plan* p, const void* q, int64_t q_stride_tok, int64_t 
     if (r) return r;
     OnDevice on(dev);
     if (!on.ok()) return failed("cudaSetDevice", cudaGetLastError());
+    if (p->captured_form) {
+        cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+        unsigned long long id = 0;
+        const cudaError_t e = cudaStreamGetCaptureInfo(static_cast<cudaStream_t>(stream), &cs, &id);
+        if (e != cudaSuccess) { cudaGetLastError(); return failed("stream", e); }
+        if (cs != cudaStreamCaptureStatusNone && id == p->capture_id) form = p->capture_form;
+    }
     AttnPagedArgs a;
     a.kv = paged_kv(kv);
     a.q_type = p->shape.type;
@@ -599,8 +622,8 @@ int llm_attn_run(llm_attn_plan* p, const void* q, int64_t q_stride_tok, int64_t 
     a.part_o2 = p->part_o + plan_part_rows(p->caps, false) * kv->head_dim;
     a.part_ml2 = p->part_ml + plan_part_rows(p->caps, false);
     a.tickets = p->tickets; a.redo2 = p->redo; a.err = p->err;
-    a.form = p->form();
-    a.early = p->device_form != 0 || kv->type == LLM_TYPE_F4_E2M1;
+    a.form = form;
+    a.early = p->on_device || p->captured_form != 0 || kv->type == LLM_TYPE_F4_E2M1;
     a.n_sm = p->ps.n_sm;
     if (!launch_attn_paged(a, static_cast<cudaStream_t>(stream))) return failed("attention launch", cudaGetLastError());
     return 0;
