@@ -394,3 +394,38 @@ def test_two_graphs_with_other_steps_of_one_plan(L):
     out.fill_(77.0)
     plan.run(q, pages, out)                                     # the same step from the host: sums in another order
     assert plan.error() == 0 and (out[:40].float() - first[:40].float()).abs().max() <= 2 ** -7 * first[:40].float().abs().max()
+
+
+@pytest.mark.parametrize("act,cdt", [PAIRS[0], PAIRS[1], PAIRS[4]])
+def test_plans_made_behind_replays_that_lack_their_kernels(L, act, cdt):
+    """A captured run of both tile forms leaves a step of another form alone; the planner behind it, launched early, must not
+    begin before both of its kernels have read the plan. Nothing is waited for in between."""
+    rng = np.random.default_rng(31)
+    mixed, few, one = ([1, 40, 1], [300, 700, 90]), ([3, 0, 2], [300, 9, 90]), ([1, 1, 1], [300, 700, 90])
+    tables, n_pages = tables_of(mixed[1], 16, rng)
+    pages, kval, vval = caches(L, cdt, n_pages, 16, 2, 64, 32)
+    q = torch.from_numpy(rng.normal(size=(42, 8, 64))).to(act).cuda()
+    lost = torch.full_like(q, 77.0)
+    plan = L.AttnPlan(pages, n_head=8, dtype=act, max_tok=42, max_seq=3, max_table=tables.size)
+    plan.set(*mixed, tables)
+    assert plan.form == 5
+    plan.run(q, pages, lost)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        plan.run(q, pages, lost)
+    lost.fill_(77.0)
+    table = ints(tables)
+    on = [(ints(np.concatenate([[0], np.cumsum(n)])), ints(kv), m) for (n, kv), m in ((few, 3), (one, 1))]
+    outs = [[torch.full_like(q, 55.0) for _ in range(20)] for _ in on]
+    torch.cuda.synchronize()
+    for i in range(20):
+        plan.set_device(on[0][0], on[0][1], table, on[0][2])     # 16-row tiles, which the graph has not
+        g.replay()
+        for (start, kv, m), o in zip(on, outs):
+            plan.set_device(start, kv, table, m)
+            plan.run(q, pages, o[i])
+    assert plan.error() == 16 and (lost == 77.0).all()
+    for (n, kv), o in zip((few, one), outs):
+        assert all(torch.equal(x, o[0]) for x in o) and (o[0][sum(n):] == 55.0).all()
+        verify(o[0].double().cpu().numpy(), q, kval, vval, tables, n, kv, 16, 0, 0, act)

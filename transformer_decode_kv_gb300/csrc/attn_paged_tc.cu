@@ -362,9 +362,15 @@ __global__ void __launch_bounds__(threads_of(CT), 1) attn_tc_rows_kernel(AttnPag
     // starts where they leave SMs free, and waits for them at its end. Otherwise, launched early, it waits for the kernel in front
     asm volatile("griddepcontrol.launch_dependents;");
     if (!beside) asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (form_missing(a)) return;
+    // (Every way out waits so: what is launched early behind this kernel waits for this one only, and may write the plan that the small
+    // tiles still have to read.)
+    if (form_missing(a)) {
+        if (beside) asm volatile("griddepcontrol.wait;" ::: "memory");
+        return;
+    }
     if (sa(sm) & 1023u) {                                   // the swizzle patterns repeat every 1024 bytes
         if (tid == 0 && a.err) atomicOr(a.err, ERR_TIMEOUT);
+        if (beside) asm volatile("griddepcontrol.wait;" ::: "memory");
         return;
     }
     const int ui0 = a.first2[blockIdx.x], ui1 = a.first2[blockIdx.x + 1];
