@@ -451,7 +451,8 @@ int llm_attn_plan_set(llm_attn_plan *plan, int32_t n_seq, const int32_t *n_new, 
  * what the captured steps need beside their own (the runs captured behind it in the same capture: only what its step needs). A step that is out of range
  * (llm_attn_plan_set's -1, or more than max_new tokens of a sequence) sets bit 32 of the plan's error word, and the
  * runs leave the output alone. A run of such a plan may be captured whatever the step, an empty one too; its q and out
- * need rows for max_tok tokens. Pages outside the cache are found by the runs (bit 1; their keys are not seen). */
+ * need rows for max_tok tokens. Pages outside the cache are found by the runs (bit 1; their keys are not seen, and a row that
+ * is left without any is NaN). */
 int llm_attn_plan_set_device(llm_attn_plan *plan, int32_t n_seq, const int32_t *start, const int32_t *n_kv,
                              const int32_t *pages, int32_t ld_pages, int32_t max_new, void *stream);
 /* q row (i, h) at i * q_stride_tok + h * q_stride_head elements, out likewise; 16-byte aligned rows.

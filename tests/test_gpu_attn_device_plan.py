@@ -429,3 +429,85 @@ def test_plans_made_behind_replays_that_lack_their_kernels(L, act, cdt):
     for (n, kv), o in zip((few, one), outs):
         assert all(torch.equal(x, o[0]) for x in o) and (o[0][sum(n):] == 55.0).all()
         verify(o[0].double().cpu().numpy(), q, kval, vval, tables, n, kv, 16, 0, 0, act)
+
+
+def attention_without(q, kval, vval, table, bad, n_new, n_kv, page, window, n_sink):
+    """The formula over the keys whose pages are in the cache, for one sequence: (out, mag, smag, rows without a key)."""
+    H, hd = q.shape[1:]
+    G = H // kval.shape[1]
+    j = np.arange(n_kv)
+    good = ~np.isin(j // page, bad)
+    cells = np.where(good, table[j // page].astype(np.int64), 0) * page + j % page
+    out, mag, smag, none = np.zeros(q.shape), np.zeros(q.shape), np.zeros(q.shape[:2]), np.zeros(n_new, bool)
+    for t in range(n_new):
+        p = n_kv - n_new + t
+        vis = good & (j <= p)
+        if window:
+            vis &= (j > p - window) | (j < n_sink)
+        none[t] = not vis.any()
+        if none[t]:
+            continue
+        for h in range(H):
+            K, V = kval[cells[vis], h // G], vval[cells[vis], h // G]
+            z = K @ q[t, h] * hd ** -0.5
+            smag[t, h] = (np.abs(K) @ np.abs(q[t, h])).max() * hd ** -0.5
+            w = np.exp(z - z.max())
+            w /= w.sum()
+            out[t, h], mag[t, h] = w @ V, w @ np.abs(V)
+    return out, mag, smag, none
+
+
+@pytest.mark.parametrize("act,cdt", [(torch.float16, torch.float16), (torch.bfloat16, torch.bfloat16), (torch.bfloat16, torch.uint8),
+                                     (torch.float16, "f4"), (torch.bfloat16, "f4"), (torch.float32, torch.uint8)])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("page,window,n_sink", [(16, 0, 0), (64, 0, 0), (17, 0, 0), (16, 200, 40), (64, 300, 70), (1, 0, 0)])
+@pytest.mark.parametrize("n_new", [50, 3])
+def test_chunks_over_pages_outside_the_cache(L, act, cdt, hd, page, window, n_sink, n_new):
+    """Entries past the cache and negative ones among whole runs of good pages, where blocks of keys are brought in bulk: their keys
+    have no part, whatever the entry, and the others their full part."""
+    rng = np.random.default_rng(41)
+    n_kv = 700
+    tables, n_pages = tables_of([n_kv], page, rng)
+    need = -(-n_kv // page)
+    pages, kval, vval = caches(L, cdt, n_pages, page, 2, hd, 42)
+    bad = sorted({0, need // 3, need // 2, need // 2 + 2, need - 1})
+    shown = tables.copy()
+    shown[0, bad] = [-1, n_pages, 2 ** 31 - 1, -2 ** 31, n_pages + 5][:len(bad)]
+    q = torch.from_numpy(rng.normal(size=(n_new + 1, 8, hd))).to(act).cuda()
+    plan = L.AttnPlan(pages, n_head=8, dtype=act, max_tok=n_new + 1, max_seq=1, max_table=need, window=window, n_sink=n_sink)
+    out = torch.full_like(q, 77.0)
+    plan.set_device(ints([0, n_new]), ints([n_kv]), ints(shown), n_new)
+    plan.run(q, pages, out)
+    assert plan.form == (2 | (4 if n_new == 50 and act != torch.float32 else 0)) and plan.error() == 1
+    got = out.double().cpu().numpy()
+    assert (got[n_new:] == 77.0).all()
+    ref, mag, smag, none = attention_without(q.double().cpu().numpy()[:n_new], kval, vval, tables[0], bad, n_new, n_kv, page, window,
+                                             n_sink)
+    tol = O.attention_tol(ref, mag, smag, act, n_kv, hd, np.abs(vval).max())
+    assert not none.any()
+    wrong = ~(np.abs(got[:n_new] - ref) <= tol)
+    assert not wrong.any(), (np.argwhere(wrong)[:5], got[:n_new][wrong][:5], ref[wrong][:5], tol[wrong][:5])
+
+
+@pytest.mark.parametrize("act,cdt", [(torch.float16, torch.float16), (torch.bfloat16, torch.uint8), (torch.float16, "f4")])
+@pytest.mark.parametrize("n_new", [1, 9, 60])
+def test_rows_whose_keys_are_all_on_pages_outside_the_cache(L, act, cdt, n_new):
+    """Such a row is NaN, as one of scores without weight is; a row with one key left has that key's value."""
+    rng = np.random.default_rng(43)
+    pages, kval, vval = caches(L, cdt, 6, 64, 2, 64, 44)
+    q = torch.from_numpy(rng.normal(size=(n_new, 8, 64))).to(act).cuda()
+    out = torch.full_like(q, 77.0)
+    plan = L.AttnPlan(pages, n_head=8, dtype=act, max_tok=n_new, max_seq=1, max_table=2)
+    n_kv = 64 + (n_new + 1) // 2                                # the first rows see the bad page only
+    if n_new == 1:
+        n_kv = 64
+    plan.set_device(ints([0, n_new]), ints([n_kv]), ints([[6, 3]]), n_new)
+    plan.run(q, pages, out)
+    assert plan.error() == 1
+    got = out.double().cpu().numpy()
+    p = np.arange(n_kv - n_new, n_kv)
+    assert np.isnan(got[p < 64]).all() and (p < 64).any()
+    if n_new > 1:
+        one = got[p == 64][0]
+        val = np.repeat(vval[3 * 64], 4, axis=0)
+        assert (np.abs(one - val) <= 4 * O.HALF_EPS[act] * np.abs(val) + 1e-30).all()
