@@ -376,8 +376,10 @@ typedef struct llm_seq_pages {
  * n_free_out receive the new lengths and the stack's new size; they may be n_kv and n_free. max_tok is at most 2^24.
  * All or nothing: where a length is negative, a sequence would pass ld_table pages or 2^31 - 1 rows, the tokens max_tok,
  * or the pages *n_free (or that is not in 0 .. max_free), bit 32 of err is set and the step has no tokens: start is zeros, cell and
- * pos are -1, lengths, stack and table stay. A page outside 0 .. n_pages - 1 (in the stack, or the last one of a
- * sequence) gives its tokens cell -1 and err bit 1. */
+ * pos are -1, lengths, stack and table stay. Page numbers are not among what is checked first: a page outside 0 .. n_pages - 1
+ * (in the stack, or the last one of a sequence) sets err bit 1 and gives its tokens cell -1, so that a store skips them, but the
+ * step is made: a page from the stack is entered in the table as it is, lengths and stack advance, and attention finds the page
+ * as one outside the cache. */
 int llm_pages_extend(const llm_seq_pages *p, const int32_t *n_new, int32_t *n_kv_out, int32_t *n_free_out,
                      int32_t max_tok, int32_t *cell, int32_t *pos, int32_t *start, uint32_t *err, void *stream);
 

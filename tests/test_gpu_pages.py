@@ -225,3 +225,35 @@ def test_bad_arguments_are_refused(L):
     with pytest.raises(L.LlmError, match="cells"):
         L.pages_extend(L.SeqPages(ls.d_table, ls.d_kv, ls.d_free, ls.d_n, 1 << 16, 1 << 15), **ok)
     assert ls.unchanged()
+
+
+def test_bad_pages_stay_in_the_lists(L):
+    """A step over a bad page of the stack is made all the same: the page is entered, lengths and stack advance, and a trim puts
+    it back as it is."""
+    ls = Lists(L, [10, 8], 8, 4, 3)
+    ls.d_free[2] = -4                                           # taken by the first sequence
+    ls.d_free[1] = ls.n_pages                                   # by the second
+    cell, pos, start, err, _ = extend(L, ls, [8, 2], 12)
+    assert err == 1 and start == [0, 8, 10] and cell[6:] == [-1] * 6 and min(cell[:6]) >= 0 and pos[:10] == [*range(10, 18), 8, 9]
+    assert ls.d_table[0].tolist() == [*ls.table[0, :2], -4, -9] and ls.d_table[1].tolist() == [ls.table[1, 0], ls.n_pages, -9, -9]
+    assert ls.d_kv.tolist() == [18, 10] and ls.d_n.tolist() == [1]
+    e = ints([0])
+    L.pages_trim(ls.lists, ints([10, 8]), err=e)
+    assert int(e) == 1 and ls.d_kv.tolist() == [10, 8] and ls.d_n.tolist() == [3]
+    assert ls.d_free.tolist()[:3] == [ls.stack[0], -4, ls.n_pages]
+
+
+@pytest.mark.parametrize("n_seq,page", [(5000, 1), (300, 4)])
+def test_trim_of_many_pages(L, n_seq, page):
+    """A stack of more places than one cluster of four takes at a time, in few sequences and in many."""
+    rng = np.random.default_rng(n_seq)
+    n_kv = rng.integers(0, 80 * page if n_seq < 1000 else 6, n_seq).tolist()
+    keep = [int(k) for k in rng.integers(-1, np.array(n_kv) + 1)]
+    gone = [(i, j) for i, (a, k) in enumerate(zip(n_kv, keep)) if k >= 0 for j in range(-(-k // page), -(-a // page))]
+    ls = Lists(L, n_kv, page, 80, 9000, room=len(gone) + 7)
+    assert ls.max_free > 8192 and len(gone) > 4096
+    err = ints([0])
+    L.pages_trim(ls.lists, ints(keep), err=err)
+    stack = ls.stack + [int(ls.table[i, j]) for i, j in gone]
+    assert int(err) == 0 and ls.d_free.tolist() == stack + [-5] * 7 and np.array_equal(ls.d_table.cpu(), ls.table)
+    assert ls.d_kv.tolist() == [a if k < 0 else k for a, k in zip(n_kv, keep)] and ls.d_n.tolist() == [len(stack)]
