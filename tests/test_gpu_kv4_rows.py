@@ -193,3 +193,25 @@ def test_capture_and_other_streams(L):
         L.kv_load(pages, cell, *o)
     st.synchronize()
     assert torch.equal(o[0].cpu(), want)
+
+
+@pytest.mark.parametrize("rdt", ROWS)
+def test_rows_below_the_normal_range_are_read_back_rounded_once(L, rdt):
+    """Every code times every block number times the least scales: float32 holds the product, whatever its size, and the row's type
+    rounds it once."""
+    n_pages, page, hd = 4, 32, 128
+    k, v = empty(n_pages, page, 1, hd)
+    pages = F.kv_pages(L, k, v)
+    code = np.broadcast_to(np.arange(hd) % 16, (n_pages, page, 1, hd)).astype(np.uint8)
+    blk = np.arange(n_pages * page * 8).reshape(n_pages, page, 1, 8) % 127      # (every number from 0 to 448)
+    s = 2.0 ** (-126 + 5 * np.arange(n_pages))[:, None, None] * np.ones((n_pages, page, 1))
+    for x in (k, v):
+        for t, a in zip(x, (F.pack(code), s.astype(np.float32), blk.astype(np.uint8))):
+            t.copy_(torch.from_numpy(a.copy()))
+    cell = torch.arange(n_pages * page, dtype=torch.int32, device="cuda")
+    o = [torch.full((n_pages * page, 1, hd), 5.0, dtype=rdt, device="cuda") for _ in range(2)]
+    L.kv_load(pages, cell, *o)
+    want = F.values(code, blk, s).reshape(-1, 1, hd)
+    assert np.array_equal(want.astype(np.float32), want) and (np.abs(want[want != 0]) < 2.0 ** -126).any()
+    for x in o:
+        assert torch.equal(x.cpu(), torch.from_numpy(want).float().to(rdt))

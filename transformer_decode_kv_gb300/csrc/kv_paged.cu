@@ -381,7 +381,9 @@ __global__ void __launch_bounds__(kThr) kv_load4_kernel(KvRowsArgs a) {
     }
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
-        // (the product of code and block scale is exact; with s it rounds where a value is below float32's normal range)
+        // (Both products are exact: code and block scale make a multiple of 2^-10 of six significant bits at most, and s, a power of two of
+        // 2^-126 or more, leaves a multiple of 2^-136, which float32 holds below its normal range too. The one rounding is that to
+        // the rows' type.)
         float x[kVals];
         const float bs = from_e4m3x2(b[v]).x;
         from_e2m1x8(u[v].x, bs, x);
