@@ -511,3 +511,61 @@ def test_rows_whose_keys_are_all_on_pages_outside_the_cache(L, act, cdt, n_new):
         one = got[p == 64][0]
         val = np.repeat(vval[3 * 64], 4, axis=0)
         assert (np.abs(one - val) <= 4 * O.HALF_EPS[act] * np.abs(val) + 1e-30).all()
+
+
+@pytest.mark.parametrize("act,cdt", [PAIRS[0], PAIRS[5]])
+def test_captured_steps_behind_copies_and_other_streams(L, act, cdt):
+    """What is launched early has something else than a kernel in front in these graphs: a memset, a copy, two streams that meet; and
+    two sets with their runs follow each other in one capture."""
+    rng = np.random.default_rng(51)
+    page, n_seq, tok = 16, 3, 45
+    tables, n_pages = tables_of([700, 90, 33], page, rng)
+    pages, kval, vval = caches(L, cdt, n_pages, page, 2, 64, 52)
+    before, add = [659, 89, 30], [41, 1, 3]
+    stack = [tables[2, 2], tables[0, 43], tables[0, 42]]          # (handed out last first)
+    lists = L.SeqPages(ints(tables), ints(before), ints(stack), ints([3]), page, n_pages)
+    n_new, cell, pos, start, after, left = ints([0] * 3), ints([0] * tok), ints([0] * tok), ints([0] * 4), ints([0] * 3), ints([0])
+    src, err = ints(add), ints([0])
+    x = [torch.from_numpy(rng.normal(size=(tok, 2, 64))).to(act).cuda() for _ in range(2)]
+    k, v = (torch.zeros_like(t) for t in x)
+    q = torch.from_numpy(rng.normal(size=(tok, 8, 64))).to(act).cuda()
+    out, small = torch.full_like(q, 77.0), torch.full_like(q, 77.0)
+    plan = L.AttnPlan(pages, n_head=8, dtype=act, max_tok=tok, max_seq=n_seq, max_table=tables.size)
+    two = ints([0, 0, 1, 4])                                    # the last two sequences' new tokens alone
+    side = torch.cuda.Stream()
+
+    def step():
+        here = torch.cuda.current_stream()
+        n_new.copy_(src)
+        L.pages_extend(lists, n_new, cell, pos, start, n_kv_out=after, n_free_out=left, err=err)
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            k.copy_(x[0])
+        v.copy_(x[1])
+        here.wait_stream(side)
+        L.kv_store(pages, k, v, cell, err=err)
+        out.zero_()
+        plan.set_device(start, after, lists.table, 41)
+        plan.run(q, pages, out)
+        small.copy_(out)
+        plan.set_device(two, after, lists.table, 3)
+        plan.run(q, pages, small)
+
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    T = sum(add)
+    for seed in range(3):
+        for t in (*x, q):
+            t.copy_(torch.from_numpy(np.random.default_rng(seed).normal(size=tuple(t.shape))))
+        n_new.zero_()
+        g.replay()
+        assert plan.error() == 0 and int(err) == 0 and start.tolist() == [0, 41, 42, 45] and after.tolist() == [700, 90, 33]
+        for t, val in zip(x, (kval, vval)):
+            t = t.double().cpu().numpy()[:T]
+            val[np.array(cell.tolist()[:T])] = F.values(*F.quantise(t)) if cdt == "f4" else t
+        verify(out.double().cpu().numpy(), q, kval, vval, tables, add, [700, 90, 33], page, 0, 0, act)
+        verify(small.double().cpu().numpy()[:4], q[:4], kval, vval, tables, [0, 1, 3], [700, 90, 33], page, 0, 0, act)
+        assert torch.equal(small[4:], out[4:])
