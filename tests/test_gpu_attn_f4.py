@@ -222,3 +222,23 @@ def test_a_page_outside_the_cache_is_refused(L):
     plan = L.AttnPlan(pages, n_head=4, dtype=torch.float16, max_tok=4, max_seq=2, max_table=8)
     with pytest.raises(L.LlmError, match="page"):
         plan.set([1], [20], [[0, 4]])
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("page", [16, 17, 64])
+@pytest.mark.parametrize("n_sink", [0, 5, 70])
+def test_what_the_window_has_left_behind_may_hold_anything(L, act, page, n_sink):
+    """NaN scales, block numbers and codes in cells that no row of the step sees any more, in the same pages and blocks of keys as
+    cells that rows see."""
+    n_new, n_kv, window = [150, 1, 9], [500, 300, 200], 100
+
+    def mutate(k, v, kval, vval, tables):
+        for t, m, n in zip(tables, n_new, n_kv):
+            j = np.arange(n_sink, max(n_sink, n - m - window + 1))
+            p, a = torch.from_numpy(t[j // page].astype(np.int64)), torch.from_numpy(j % page)
+            for c in (k, v):
+                c[0][p, a] = 0x77
+                c[1][p, a] = float("nan")
+                c[2][p, a] = 0x7f
+    check(L, act, 64, 2, 4, page, n_new, n_kv, window, n_sink, seed=51, mutate=mutate)
+    check(L, act, 128, 1, 4, page, n_new, n_kv, window, n_sink, seed=52, mutate=mutate)
