@@ -14,13 +14,18 @@ int64_t block_keys(const PlanShape& s, int f, int rows) { return f ? 128 : 32 * 
 // What a unit costs beyond its keys, in blocks: Q in, the warps' (halves') results out and merged. (32 / 8 heads of
 // 128. Small tiles: 32 single tokens over 1 .. 2304 keys took 47, 39 and 39 us at 0, 1 and 2, one over 513 11.3, 12.3
 // and 14 us. 256 rows: chunks of 20 .. 1000 tokens of five sequences 99, 89 and 87 us at 2, 3 and 4, 16 tokens over
-// 8192 keys 40 us at 3 and 46 us at 4.)
+// 8192 keys 40 us at 3 and 46 us at 4. E2M1 caches. Small tiles: the same single tokens 23.8 and 24.8 us at 1 and 2, one over 513
+// 9.2 and 8.4. 256 rows at 2, 3, 4 and 6, bf16: five chunks of 20 .. 1000 tokens 155, 131, 128 and 133 us, under a window of
+// 1024 72, 69, 68 and 60; 512 tokens over 8192 keys 87, 84, 83 and 91; 16 over 8192 40, 39, 46 and 46: 3 fits them as well, and
+// a windowed step of short chunks would gain a seventh at 6.)
 constexpr int64_t kUnitCost[2] = {1, 3};
 // Sequences with at least this many rows per KV head take 256-row tiles. 32 / 8 heads of 128, small tiles against large
 // ones, us: f16, one sequence over 8192 keys: 32 rows 30 : 40, 64 rows 37 : 40, 96 rows 45 : 41, 128 rows 52 : 42;
 // sixteen over 2048: 32 rows 58 : 39, 64 rows 96 : 39. E4M3 (whose large tiles convert their rows first): one, 64 rows
-// 29 : 46, 128 rows 44 : 47; sixteen, 32 rows 37 : 60, 64 rows 73 : 60. One number for both types is a compromise: it fits
-// many sequences of E4M3 rows and costs a single one 17 us at 64 rows, and f16 steps of many sequences would gain at 32.
+// 29 : 46, 128 rows 44 : 47; sixteen, 32 rows 37 : 60, 64 rows 73 : 60. E2M1: one, 32 rows 24 : 39, 64 rows 29 : 40, 96 rows
+// 39 : 41, 128 rows 44 : 42; sixteen, 32 rows 37 : 39, 64 rows 75 : 40. One number for all types is a compromise: it fits
+// many sequences of E4M3 and E2M1 rows and costs a single one 17 and 11 us at 64 rows, and f16 steps of many sequences would
+// gain at 32.
 constexpr int64_t kTcRows = 64;
 
 int64_t ctas(const PlanShape& s, int f) { return (int64_t)s.n_sm * (f ? 1 : kAttnRowsCtas); }

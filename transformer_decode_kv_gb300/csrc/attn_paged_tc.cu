@@ -36,7 +36,7 @@
 // back into TMEM): at the end of 8192 keys the tensor pipe is active for 56% of the time, issue slots are used for 38%, the
 // exponential unit for 29%. 512 f16 tokens at the end of 8192 take 80 us, where cut tiles weigh; over E4M3 1203 and 113
 // us, where the rows' conversion shares issue slots and shared memory with the softmax (tensor pipe 30%, issue slots 37%);
-// over E2M1 812 and 84 us (tensor pipe 41%, issue slots 47%): a third fewer raw bytes, converters that wait for nothing but
+// over E2M1 815 and 85 us (tensor pipe 41%, issue slots 47%): a third fewer raw bytes, converters that wait for nothing but
 // landed bytes, and code that the instruction cache holds beside the softmax. A unit costs about 20 000 cycles beside its blocks
 // (Q in, hidden keys, epilogue), which is what small units of windowed chunks consist of.
 //

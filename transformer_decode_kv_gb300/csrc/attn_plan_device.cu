@@ -11,7 +11,9 @@
 // One CTA makes the units, the others copy the page table. It is latency: lengths, four running sums, and two rounds of
 // independent items, the CTAs' ends (a thread finds the tile that its end falls into, and makes the unit that begins there)
 // and the tiles (each its first unit). 32 single tokens with 8 KV heads take 7.8 us (18.5 with the lists in global memory and
-// eight lanes a tile, 9.5 with all places in 64 bits), six chunks of 1228 tokens together 9.8.
+// eight lanes a tile, 9.5 with all places in 64 bits), six chunks of 1228 tokens together 9.8. Planned again and again: 512 single
+// tokens 16.6 us, 2048 93, a prompt of 8192 f32 tokens (16-row tiles) 42, of f16 ones 7.3. A layer's attention of these steps takes
+// 85 us (of 32 .. 256 keys each; 457 of 512 .. 4096), 615, 5866 and 479, and one plan serves all layers: one CTA is enough.
 #include "paged.h"
 
 #include <algorithm>

@@ -15,9 +15,9 @@
 // q = q0 + (y - q0 b) r (P. Markstein's theorem, IBM J. Res. Dev. 34, 1990).
 //
 // F4_E2M1 has kernels of its own, whose threads hold a block of K and one of V: 8192 rows of K and V as below, stored and read
-// back, take 16.3 us for 87 MB (5.3 TB/s; 12.8 us at the card's copy rate; 20.8 where launches do not overlap; store 13.7 and load
-// 9.4 under the profiler). The store issues instructions 56% of the time: seven per value, of which the quotient takes four.
-// One row a thread, K and V apart, took 27.2 us.
+// back, take 19.5 us for 87 MB (4.4 TB/s; 12.8 us at the card's copy rate). Where the same rows come again and again, L2 holds
+// them: 16.2 us, of which launches that do not overlap would make 20.8, and one row a thread, K and V apart, 27.2. Store 13.7 and
+// load 9.4 under the profiler; the store issues instructions 56% of the time: seven per value, of which the quotient takes four.
 //
 // Both kernels of the other types move every byte once. 8192 rows of K and V (8 heads of 128, bf16 values, E4M3 cache), stored and read back,
 // take 23.8 us for 101 MB (4.3 TB/s; 15.0 us at the card's copy rate): a step's few rows are bound by the launch,

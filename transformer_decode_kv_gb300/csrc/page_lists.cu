@@ -11,7 +11,9 @@
 // thousand lengths are a few microseconds' worth of nothing) and share out the tokens; its barrier keeps lengths and
 // the stack's size in place until every CTA has read them, so that both may be updated where they are. 64 sequences take
 // 5.4 us on the GPU (a launch of nothing: about 2), 512 with 17 thousand new tokens 9.5 with eight CTAs, 11.4 with four,
-// 16 with two.
+// 16 with two. Trims, one after the other: 64 sequences of which eight end and give back 1632 pages 3.6 us, 512 of which 32 end,
+// 37 thousand pages, 7.1; all 512 at once, 546 thousand pages, 53 (a bisection per page: a server that ends that many in one
+// step has no tokens to wait for).
 #include "paged.h"
 
 namespace llm {
